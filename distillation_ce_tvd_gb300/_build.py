@@ -20,7 +20,8 @@ LIB_NAME = "libfused_ce_tvd.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["fct_api.cu", "fct_forward.cu", "fct_backward.cu", "fct_loss.cu", "fct_linear.cu",
-           "fct_noalloc.cu", "fct_host.cu", "fct_vocab.cu", "fct_gemm.cu"]
+           "fct_noalloc.cu", "fct_host.cu", "fct_vocab.cu", "fct_gemm.cu", "fct_spec_api.cu",
+           "fct_kv.cu", "fct_tree_attention.cu", "fct_verify.cu"]
 HEADERS = ["fct_common.cuh", "fct_internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -15,8 +15,10 @@ import torch
 
 from . import _build
 
-FCT_F32, FCT_BF16 = 0, 1
+FCT_F32, FCT_BF16, FCT_E4M3 = 0, 1, 2
 FCT_DEV_TARGET_OUT_OF_RANGE = 0x1
+FCT_DEV_INDEX_OUT_OF_RANGE = 0x4
+FCT_DEV_NO_DISTRIBUTION = 0x8
 IGNORE_INDEX = -100
 
 _lock = threading.Lock()
@@ -34,6 +36,8 @@ EXPORTS = ("fused_ce_tvd_forward", "fused_ce_tvd_forward_ex", "fused_ce_tvd_back
            "fct_gemm_bf16_workspace_size",
            "fused_ce_tvd_vp_lse", "fused_ce_tvd_vp_merge_lse", "fused_ce_tvd_vp_tvd",
            "fused_ce_tvd_vp_merge_tvd", "fused_ce_tvd_vp_backward",
+           "fct_kv_cache_write", "fct_kv_cache_move", "fct_tree_attention",
+           "fct_tree_attention_workspace_size", "fct_spec_verify",
            "fct_status_string", "fct_version")
 
 
@@ -45,6 +49,17 @@ class Options(ctypes.Structure):
 
 
 RING_AUTO, RING_CP_ASYNC, RING_TMA = 0, 1, 2
+
+
+class _KvCacheStruct(ctypes.Structure):
+    """fct_kv_cache: a paged key/value cache (see include/fused_ce_tvd.h)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("num_pages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("scale_page_stride", ctypes.c_int64),
+                ("scale_slot_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64)]
 
 
 def options(ctas_per_row: int = 0, l2_keep: int = 0, stagger: float = 0.0,
@@ -144,6 +159,19 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                                  vp, vp, vp, vp, vp, i64, vp, i64, vp, vp]
         for f in ("fused_ce_tvd_vp_lse", "fused_ce_tvd_vp_merge_lse", "fused_ce_tvd_vp_tvd",
                   "fused_ce_tvd_vp_merge_tvd", "fused_ce_tvd_vp_backward"):
+            getattr(lib, f).restype = i32
+        kc, sz = ctypes.POINTER(_KvCacheStruct), ctypes.c_size_t
+        lib.fct_kv_cache_write.argtypes = [vp, vp, i64, i64, i32, i64, vp, kc, vp, vp]
+        lib.fct_kv_cache_move.argtypes = [kc, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, vp]
+        lib.fct_tree_attention.argtypes = [vp, i64, i64, i64, i32, kc, vp, i64, i64, vp, vp, i64,
+                                           vp, i64, ctypes.c_float, vp, i64, i64, vp, vp, sz, vp,
+                                           vp]
+        lib.fct_tree_attention_workspace_size.argtypes = [i64, i32, i32, i32]
+        lib.fct_tree_attention_workspace_size.restype = sz
+        lib.fct_spec_verify.argtypes = [vp, i64, vp, i64, i32, i64, i64, vp, vp, vp, i64, vp, vp,
+                                        i64, vp, i64, vp, vp, vp, vp, vp]
+        for f in ("fct_kv_cache_write", "fct_kv_cache_move", "fct_tree_attention",
+                  "fct_spec_verify"):
             getattr(lib, f).restype = i32
         lib.fct_status_string.argtypes = [i32]
         lib.fct_status_string.restype = ctypes.c_char_p
@@ -888,3 +916,225 @@ def fused_linear_ce_tvd_forward_backward_noalloc(h_student, w_student, h_teacher
         _ptr(dev_status), _stream(stream))
     _check(rc, "fused_linear_ce_tvd_forward_backward_noalloc")
     return (*outs, grad_h, grad_w)
+
+
+# ------------------------------------------------------------------ speculative decoding step
+
+class KVCache:
+    """A paged key/value cache: ``k`` and ``v`` are (num_pages, page_size, n_kv_heads, head_dim)
+    CUDA tensors of the same strides with unit stride along head_dim (any order of the other
+    dimensions: permuted views are fine), bfloat16, or float8_e4m3fn with the uint8 exponent bytes
+    ``k_scale`` and ``v_scale`` (num_pages, page_size, n_kv_heads).  The value held is
+    payload * 2**(byte - 127).
+
+    The object keeps the tensors and the library's description of them; make it once per layer.
+    """
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "struct", "ref", "device")
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        code = {torch.bfloat16: FCT_BF16, torch.float8_e4m3fn: FCT_E4M3}.get(k.dtype)
+        if code is None:
+            raise TypeError(f"k: dtype {k.dtype} is not bfloat16 or float8_e4m3fn")
+        if not (k.is_cuda and v.is_cuda) or k.device != v.device:
+            raise ValueError("k and v must be CUDA tensors of one device")
+        if k.dim() != 4 or v.dtype != k.dtype or v.shape != k.shape or v.stride() != k.stride() \
+                or (k.shape[3] > 1 and k.stride(3) != 1):
+            raise ValueError("k and v must be (num_pages, page_size, n_kv_heads, head_dim) of one "
+                             "dtype and one set of strides, with unit stride along head_dim")
+        scales = (0, 0, 0)
+        if code == FCT_E4M3:
+            for x, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                if x is None or x.device != k.device or x.dtype != torch.uint8 \
+                        or x.shape != k.shape[:3]:
+                    raise ValueError(f"{name} must be a uint8 tensor of shape (num_pages, "
+                                     "page_size, n_kv_heads) on the cache's device")
+            if k_scale.stride() != v_scale.stride():
+                raise ValueError("k_scale and v_scale must have the same strides")
+            scales = k_scale.stride()
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("a bfloat16 cache has no scales")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device = k.device
+        self.struct = _KvCacheStruct(
+            k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if k_scale is not None else None,
+            v_scale.data_ptr() if v_scale is not None else None, code, k.shape[1], k.shape[2],
+            k.shape[3], k.shape[0], *k.stride()[:3], *scales)
+        self.ref = ctypes.byref(self.struct)
+
+
+def _vec(x, dtype, n, device, name):
+    """The address of a contiguous vector of ``n`` values."""
+    if x.dtype != dtype or x.dim() != 1 or x.shape[0] != n or x.device != device \
+            or (n > 1 and x.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous {dtype} vector of {n} values on {device}")
+    return x.data_ptr()
+
+
+def _table(x, dtype, rows, device, name):
+    """(address, row stride, columns) of a 2-D tensor of ``rows`` rows with unit column stride."""
+    if x.dtype != dtype or x.dim() != 2 or x.shape[0] != rows or x.device != device \
+            or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError(f"{name} must be a 2-D {dtype} tensor of {rows} rows on {device} with "
+                         "unit stride along columns")
+    cols = x.shape[1]
+    return x.data_ptr(), (x.stride(0) if rows > 1 else cols), cols
+
+
+def _status_ptr(x):
+    return x.data_ptr() if x is not None else None
+
+
+def fct_kv_cache_write(cache, k, v, slots, *, dev_status=None, stream=None):
+    """Write ``n`` new tokens' keys and values (n, n_kv_heads, head_dim; float32 or bfloat16, views
+    with unit stride along head_dim) to the slots (page * page_size + offset; int64 (n,), negative
+    skips) of the cache, in place.  An e4m3 cache is quantised as it is written: per token and head
+    the smallest power of two that keeps every value within 448, then round to nearest even."""
+    s = cache.struct
+    code = {torch.float32: FCT_F32, torch.bfloat16: FCT_BF16}.get(k.dtype)
+    if code is None:
+        raise TypeError(f"k: dtype {k.dtype} is not float32 or bfloat16")
+    if k.dim() != 3 or k.shape[1] != s.n_heads or k.shape[2] != s.head_dim \
+            or v.shape != k.shape or v.dtype != k.dtype or v.stride() != k.stride() \
+            or k.device != cache.device or v.device != cache.device \
+            or (s.head_dim > 1 and k.stride(2) != 1):
+        raise ValueError("k and v must be (n, n_kv_heads, head_dim) on the cache's device, of one "
+                         "dtype and one set of strides, with unit stride along head_dim")
+    n = k.shape[0]
+    rc = load().fct_kv_cache_write(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), code, n,
+                                   _vec(slots, torch.int64, n, cache.device, "slots"), cache.ref,
+                                   _status_ptr(dev_status), _stream(stream))
+    _check(rc, "fct_kv_cache_write")
+
+
+def fct_kv_cache_move(cache, block_table, context_len, path, count, *, dev_status=None,
+                      stream=None):
+    """Move the accepted nodes' keys and values (``path`` and ``count`` as fct_spec_verify returns
+    them) to the positions after each request's context, in place."""
+    B = context_len.shape[0]
+    tab, ld_t, pages = _table(block_table, torch.int32, B, cache.device, "block_table")
+    pth, ld_p, depth = _table(path, torch.int32, B, cache.device, "path")
+    rc = load().fct_kv_cache_move(cache.ref, tab, ld_t, pages,
+                                  _vec(context_len, torch.int32, B, cache.device, "context_len"),
+                                  B, pth, ld_p, depth,
+                                  _vec(count, torch.int32, B, cache.device, "count"),
+                                  _status_ptr(dev_status), _stream(stream))
+    _check(rc, "fct_kv_cache_move")
+
+
+def fct_tree_attention_workspace_size(n_nodes: int, n_q_heads: int, n_kv_heads: int,
+                                      head_dim: int) -> int:
+    """Bytes of device workspace fct_tree_attention needs."""
+    return int(load().fct_tree_attention_workspace_size(int(n_nodes), int(n_q_heads),
+                                                        int(n_kv_heads), int(head_dim)))
+
+
+def _heads(x, device, name):
+    if x.dim() != 3 or x.dtype != torch.bfloat16 or x.device != device \
+            or (x.shape[2] > 1 and x.stride(2) != 1):
+        raise ValueError(f"{name} must be a (n_nodes, n_q_heads, head_dim) bfloat16 tensor on the "
+                         "cache's device with unit stride along head_dim")
+
+
+def fct_tree_attention(q, cache, block_table, context_len, node_start, tree_mask=None, *,
+                       scale=None, out=None, lse=None, workspace=None, dev_status=None,
+                       stream=None):
+    """Attention of every request's drafted nodes over its pages of the cache: (out, lse).
+
+    ``q`` (n_nodes, n_q_heads, head_dim) bfloat16 holds the requests' nodes one after the other,
+    request b's from node_start[b] to node_start[b + 1].  A node sees its request's first
+    context_len[b] tokens and the nodes whose bits its row of ``tree_mask`` (n_nodes, words) int64
+    has (None: a chain, each node sees the ones before it and itself); node i of a request lies in
+    the cache at position context_len[b] + i.  ``out`` is bfloat16 like q, ``lse`` (n_nodes,
+    n_q_heads) float32.  ``scale`` defaults to head_dim ** -0.5.  ``workspace``: a uint8 tensor of
+    fct_tree_attention_workspace_size bytes to keep between calls (allocated here if None).
+    """
+    s, dev = cache.struct, cache.device
+    _heads(q, dev, "q")
+    N, H, D = q.shape
+    if D != s.head_dim or H % s.n_heads != 0:
+        raise ValueError("q's heads must be a multiple of the cache's and share its head_dim")
+    B = context_len.shape[0]
+    tab, ld_t, pages = _table(block_table, torch.int32, B, dev, "block_table")
+    mask, words = None, 0
+    if tree_mask is not None:
+        mask, ld_m, words = _table(tree_mask, torch.int64, N, dev, "tree_mask")
+        if ld_m != words:
+            raise ValueError("tree_mask must be contiguous")
+    if out is None:
+        out = torch.empty((N, H, D), device=dev, dtype=torch.bfloat16)
+    else:
+        _heads(out, dev, "out")
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    if lse is None:
+        lse = torch.empty((N, H), device=dev, dtype=torch.float32)
+    elif lse.dtype != torch.float32 or lse.shape != (N, H) or not lse.is_contiguous() \
+            or lse.device != dev:
+        raise ValueError("lse must be a contiguous (n_nodes, n_q_heads) float32 tensor")
+    if workspace is None:
+        workspace = torch.empty(fct_tree_attention_workspace_size(N, H, s.n_heads, D) if N else 0,
+                                device=dev, dtype=torch.uint8)
+    rc = load().fct_tree_attention(
+        q.data_ptr(), q.stride(0), q.stride(1), N, H, cache.ref, tab, ld_t, pages,
+        _vec(context_len, torch.int32, B, dev, "context_len"),
+        _vec(node_start, torch.int32, B + 1, dev, "node_start"), B, mask, words,
+        D ** -0.5 if scale is None else scale, out.data_ptr(), out.stride(0), out.stride(1),
+        lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _status_ptr(dev_status), _stream(stream))
+    _check(rc, "fct_tree_attention")
+    return out, lse
+
+
+def fct_spec_verify(target_logits, tokens, parent, node_start, uniform, noise, draft_logits=None,
+                    temperature=None, *, max_depth, out_tokens=None, path=None, count=None,
+                    dev_status=None, stream=None):
+    """Verify each request's drafted tree against the target's logits: (out_tokens, path, count).
+
+    ``target_logits`` (n_nodes, V) float32 or bfloat16: row n is the target's distribution after
+    node n (a request's node 0 is its last committed token).  ``draft_logits``: the distributions
+    the children were drawn from, or None where the draft proposes them for certain (the best
+    tokens of each node).  ``tokens`` int64, ``parent`` int32 (index within the request, -1 for node
+    0) and ``uniform`` float32 in [0, 1): one per node; ``noise`` (batch, V) float32, exponentially
+    distributed (``torch.empty(...).exponential_()``); ``temperature`` (batch,) float32 or None.
+
+    ``out_tokens`` (batch, max_depth + 1) int64: the accepted tokens, the next token, then -1;
+    ``path`` (batch, max_depth) int32: the accepted nodes; ``count`` (batch,) int32: how many.
+    """
+    code, ld_t = _logits(target_logits, "target_logits")
+    N, V = target_logits.shape
+    dev = target_logits.device
+    dft, ld_d = None, 0
+    if draft_logits is not None:
+        code_d, ld_d = _logits(draft_logits, "draft_logits")
+        if code_d != code or draft_logits.shape != (N, V) or draft_logits.device != dev:
+            raise ValueError("draft_logits must match target_logits' shape, dtype and device")
+        dft = draft_logits.data_ptr()
+    B = node_start.shape[0] - 1
+    if B < 0:
+        raise ValueError("node_start must have batch + 1 values")
+    nse, ld_n, cols = _table(noise, torch.float32, B, dev, "noise")
+    if cols != V:
+        raise ValueError("noise must be (batch, V)")
+    P = int(max_depth)
+    if out_tokens is None:
+        out_tokens = torch.empty((B, P + 1), device=dev, dtype=torch.int64)
+    if path is None:
+        path = torch.empty((B, P), device=dev, dtype=torch.int32)
+    if count is None:
+        count = torch.empty((B,), device=dev, dtype=torch.int32)
+    for x, shape, dtype, name in ((out_tokens, (B, P + 1), torch.int64, "out_tokens"),
+                                  (path, (B, P), torch.int32, "path"),
+                                  (count, (B,), torch.int32, "count")):
+        if x.shape != shape or x.dtype != dtype or x.device != dev or not x.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+    rc = load().fct_spec_verify(
+        target_logits.data_ptr(), ld_t, dft, ld_d, code, N, V,
+        _vec(tokens, torch.int64, N, dev, "tokens"), _vec(parent, torch.int32, N, dev, "parent"),
+        _vec(node_start, torch.int32, B + 1, dev, "node_start"), B,
+        _vec(uniform, torch.float32, N, dev, "uniform"), nse, ld_n,
+        _vec(temperature, torch.float32, B, dev, "temperature") if temperature is not None else None,
+        P, out_tokens.data_ptr(), path.data_ptr(), count.data_ptr(), _status_ptr(dev_status),
+        _stream(stream))
+    _check(rc, "fct_spec_verify")
+    return out_tokens, path, count

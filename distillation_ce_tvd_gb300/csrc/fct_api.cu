@@ -614,6 +614,18 @@ int vp_merge_impl(const float* parts, int64_t n_shards, const int64_t* target, i
 
 namespace fct {
 
+int current_device_sms(int* sms, int* device) {
+  DeviceInfo d;
+  const int rc = current_device(&d);
+  if (rc != FCT_OK) return rc;
+  if (cudaGetDevice(device) != cudaSuccess) {
+    cudaGetLastError();
+    return FCT_ERR_CUDA;
+  }
+  *sms = d.sms;
+  return FCT_OK;
+}
+
 int plan_linear_forward(int64_t V, int logits_dtype, FwdPlan* plan, int* device, int* sms) {
   DeviceInfo d;
   const int rc = current_device(&d);
@@ -923,6 +935,6 @@ size_t fct_gemm_bf16_workspace_size(int64_t M, int64_t N) {
   return fct::gemm_split_workspace_bytes(M, N);
 }
 
-int fct_version(void) { return 500; }  // 0.5.0: tensor-core GEMM entry point, lse partials in the fused-linear workspace
+int fct_version(void) { return 600; }  // 0.6.0: the speculative decoding step
 
 }  // extern "C"

@@ -195,6 +195,85 @@ cudaError_t launch_gemm(const GemmOperand& A, const GemmOperand& B, void* C, int
                         float2* lse_part = nullptr, int64_t lse_ld = 0);
 size_t gemm_split_workspace_bytes(int64_t M, int64_t N);
 
+// The calling thread's current device, if it is one the kernels are built
+// for: its SM count and index.  Returns an fct_status.
+int current_device_sms(int* sms, int* device);
+
+// Speculative decoding step (fct_kv.cu, fct_tree_attention.cu, fct_verify.cu;
+// entry points in fct_spec_api.cu).
+
+// Where each request's tokens are in a paged cache.
+struct PageTable {
+  const int32_t* table;  // (batch, max_pages), row stride ld
+  int64_t ld, max_pages;
+  const int32_t* context_len;  // (batch,)
+  int64_t batch;
+};
+
+struct KvWriteArgs {
+  const void* k;
+  const void* v;
+  int64_t ld_token, ld_head;
+  int src_dtype;  // FCT_F32 or FCT_BF16
+  int64_t n_tokens;
+  const int64_t* slots;
+  fct_kv_cache cache;
+  int32_t* dev_status;
+};
+cudaError_t launch_kv_write(const KvWriteArgs& a, cudaStream_t st);
+
+struct KvMoveArgs {
+  fct_kv_cache cache;
+  PageTable pages;
+  const int32_t* path;  // (batch, path_len), row stride ld_path
+  int64_t ld_path, path_len;
+  const int32_t* count;
+  int32_t* dev_status;
+};
+cudaError_t launch_kv_move(const KvMoveArgs& a, cudaStream_t st);
+
+struct AttnArgs {
+  const void* q;
+  int64_t ld_qn, ld_qh;
+  int64_t n_nodes;
+  int n_q_heads;
+  fct_kv_cache cache;
+  PageTable pages;
+  const int32_t* node_start;
+  const int64_t* mask;  // nullptr: chains
+  int64_t mask_words;
+  float scale;
+  void* out;
+  int64_t ld_on, ld_oh;
+  float* lse;  // optional
+  void* workspace;
+  int32_t* dev_status;
+};
+size_t attn_workspace_bytes(int64_t n_nodes, int n_q_heads, int n_heads, int head_dim, int sms);
+cudaError_t launch_attention(const AttnArgs& a, int sms, int device, cudaStream_t st);
+
+struct VerifyArgs {
+  const void* target;
+  const void* draft;  // nullptr: the drafted tokens are proposed for certain
+  int64_t ld_t, ld_d;
+  int dtype;
+  int64_t n_nodes, V;
+  const int64_t* tokens;
+  const int32_t* parent;
+  const int32_t* node_start;
+  int64_t batch;
+  const float* uniform;
+  const float* noise;
+  int64_t ld_noise;
+  const float* temperature;  // nullptr: 1
+  int64_t max_depth;
+  int64_t* out_tokens;
+  int32_t* path;
+  int32_t* count;
+  int32_t* dev_status;
+};
+cudaError_t launch_verify(const VerifyArgs& a, int sms, int device, cudaStream_t st);
+
 cudaError_t launch_forward(const FwdArgs& a, const FwdPlan& plan, cudaStream_t st);
 cudaError_t launch_mean(const LossArgs& a, cudaStream_t st);
 cudaError_t launch_backward(const BwdArgs& a, bool vec, int sms, cudaStream_t st);

@@ -56,7 +56,8 @@
 extern "C" {
 #endif
 
-typedef enum { FCT_F32 = 0, FCT_BF16 = 1 } fct_dtype;
+/* FCT_E4M3 (8-bit floats) is an element type of the key/value cache only. */
+typedef enum { FCT_F32 = 0, FCT_BF16 = 1, FCT_E4M3 = 2 } fct_dtype;
 
 typedef enum {
   FCT_OK = 0,
@@ -69,6 +70,8 @@ typedef enum {
 /* Bits OR-ed into *dev_status by the kernels. */
 #define FCT_DEV_TARGET_OUT_OF_RANGE 0x1
 #define FCT_DEV_WAIT_TIMEOUT 0x2 /* a bounded wait in a kernel gave up; outputs invalid */
+#define FCT_DEV_INDEX_OUT_OF_RANGE 0x4 /* a slot, page, path or length is outside its array */
+#define FCT_DEV_NO_DISTRIBUTION 0x8    /* a row of logits that is visited has no softmax */
 
 /*
  * Launch options of the multi-pass forward kernels (a tuning and measurement
@@ -627,6 +630,191 @@ int fused_ce_tvd_vp_backward(const void* student, int64_t ld_student,
                              int64_t ld_grad, int32_t* dev_status,
                              void* stream);
 
+/*
+ * One step of speculative decoding with a distilled draft model.  The loss
+ * above trains a draft whose distribution q stays near the target's p in
+ * total variation, because a drafted token survives verification with
+ * probability 1 - tvd(p, q); these four operations are what uses the draft
+ * (no counterpart in the PR #1384 analysis):
+ *
+ *   fct_kv_cache_write  the new tokens' keys and values into a paged cache,
+ *                       in bf16 or quantised to 8 bits as they are written;
+ *   fct_tree_attention  attention of every node of each request's drafted
+ *                       tree (or of one token) over the cache;
+ *   fct_spec_verify     which drafted tokens the target accepts, and the next
+ *                       token, from given random numbers;
+ *   fct_kv_cache_move   the accepted path's keys and values to the front.
+ *
+ * A request has nodes 0 .. T - 1: node 0 is its last committed token, the
+ * others are drafted, and every node's parent has a lower index.  The nodes
+ * of a batch are packed: request b owns rows node_start[b] ..
+ * node_start[b + 1] - 1 (node_start has batch + 1 int32 values, ascending
+ * from 0 to n_nodes).  Before the step the cache holds context_len[b] tokens
+ * of the request, and node i is written at position context_len[b] + i.
+ *
+ * Position i of request b lies in page block_table[b * ld_table + i /
+ * page_size] at offset i % page_size; entries past a request's last position
+ * are not read.  A page index outside the pool, a position past max_pages
+ * pages or a negative length sets FCT_DEV_INDEX_OUT_OF_RANGE; nothing outside
+ * the arrays is read or written, and that request's outputs are not valid.
+ */
+
+/*
+ * A paged cache: element d of head h of the token at offset s of page p is at
+ * p * page_stride + s * slot_stride + h * head_stride + d (elements) of k and
+ * of v, so any order of pages, tokens and heads is one of strides.
+ *
+ *   dtype    : FCT_BF16, or FCT_E4M3 with one exponent byte per token and
+ *              head in k_scale and v_scale, at p * scale_page_stride + s *
+ *              scale_slot_stride + h * scale_head_stride: the value held is
+ *              payload * 2^(byte - 127), and byte 255 makes the vector NaN.
+ *   head_dim : a multiple of 8, at most 256, else FCT_ERR_UNSUPPORTED.
+ *   k, v     : aligned to 8 elements, strides multiples of 8 elements, else
+ *              FCT_ERR_ALIGNMENT.  Distinct (p, s, h) must not overlap.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  uint8_t* k_scale; /* NULL for FCT_BF16 */
+  uint8_t* v_scale;
+  int32_t dtype;
+  int32_t page_size;
+  int32_t n_heads;
+  int32_t head_dim;
+  int64_t num_pages;
+  int64_t page_stride, slot_stride, head_stride;
+  int64_t scale_page_stride, scale_slot_stride, scale_head_stride;
+} fct_kv_cache;
+
+/*
+ * Writes n_tokens new keys and values into the cache.
+ *
+ *   k, v   : (n_tokens, n_heads, head_dim), FCT_F32 or FCT_BF16, unit stride
+ *            along head_dim; strides ld_token and ld_head (elements) for both.
+ *   slots  : (n_tokens,) int64: page * page_size + offset; a negative slot
+ *            skips its token, one past the pool also sets
+ *            FCT_DEV_INDEX_OUT_OF_RANGE.  If two tokens have the same slot,
+ *            which of them stays is not defined.
+ * FCT_BF16: values rounded once, to nearest even.  FCT_E4M3: per token and
+ * head, the exponent is the smallest e >= -126 with max |x| <= 448 * 2^e, and
+ * the payload is x * 2^-e rounded to nearest even, so nothing saturates and
+ * the scaling itself is exact.  A vector with a NaN or an infinity is stored
+ * as byte 255 with payload 0: it reads back as NaN as a whole.
+ */
+int fct_kv_cache_write(const void* k, const void* v, int64_t ld_token,
+                       int64_t ld_head, fct_dtype dtype, int64_t n_tokens,
+                       const int64_t* slots, const fct_kv_cache* cache,
+                       int32_t* dev_status, void* stream);
+
+/*
+ * After verification: for j < count[b], the key, value and scales of the
+ * token at position context_len[b] + path[b * ld_path + j] move to position
+ * context_len[b] + 1 + j, in place, so that the accepted path follows the
+ * context without gaps (node 0 stays).  path[b] lists the accepted nodes as
+ * fct_spec_verify writes them: ascending, path[j] >= j + 1; a request's move
+ * stops at the first entry that is not (FCT_DEV_INDEX_OUT_OF_RANGE), and
+ * count[b] is clipped to [0, path_len].  Requests must not share the pages
+ * they move in.
+ */
+int fct_kv_cache_move(const fct_kv_cache* cache, const int32_t* block_table,
+                      int64_t ld_table, int64_t max_pages,
+                      const int32_t* context_len, int64_t batch,
+                      const int32_t* path, int64_t ld_path, int64_t path_len,
+                      const int32_t* count, int32_t* dev_status, void* stream);
+
+/*
+ * Attention of the drafted trees over the cache.  For node i of request b
+ * and query head h, with kv head h / (n_q_heads / n_heads) and the
+ * context_len[b] + T_b keys of the request's positions:
+ *
+ *   s_j = scale * q . k_j for the visible j: all j < context_len[b], and the
+ *         nodes j - context_len[b] whose bit in the node's mask is set;
+ *   out = sum_j softmax(s)_j v_j,   lse = log sum_j exp(s_j).
+ *
+ * What is not visible has no influence, whatever it holds.  A node that sees
+ * nothing gets out = 0 and lse = -inf.
+ *
+ *   q, out      : (n_nodes, n_q_heads, head_dim) bf16, unit stride along
+ *                 head_dim, strides ld_*_node and ld_*_head; n_q_heads a
+ *                 multiple of the cache's n_heads.  out must not overlap q.
+ *   tree_mask   : (n_nodes, mask_words) int64: bit j % 64 of word j / 64 says
+ *                 that the node sees node j of its request (itself included;
+ *                 nodes past 64 * mask_words are not seen).  NULL with
+ *                 mask_words = 0: a chain, node i sees nodes 0 .. i.
+ *   lse         : (n_nodes, n_q_heads) fp32, or NULL.
+ *   workspace   : device memory, 16-byte aligned, of at least
+ *                 fct_tree_attention_workspace_size bytes, clobbered: partial
+ *                 results of requests whose keys are split over several CTAs.
+ * Products take bf16 operands (softmax weights are rounded to bf16 for the
+ * second one, 2^-9 each; e4m3 values are exact in bf16) with fp32 sums; the
+ * softmax statistics are fp32.  The order of all sums is fixed by the
+ * arguments and the device: repeated calls give the same bits.
+ */
+size_t fct_tree_attention_workspace_size(int64_t n_nodes, int32_t n_q_heads,
+                                         int32_t n_heads, int32_t head_dim);
+
+int fct_tree_attention(const void* q, int64_t ld_q_node, int64_t ld_q_head,
+                       int64_t n_nodes, int32_t n_q_heads,
+                       const fct_kv_cache* cache, const int32_t* block_table,
+                       int64_t ld_table, int64_t max_pages,
+                       const int32_t* context_len, const int32_t* node_start,
+                       int64_t batch, const int64_t* tree_mask,
+                       int64_t mask_words, float scale, void* out,
+                       int64_t ld_out_node, int64_t ld_out_head, float* lse,
+                       void* workspace, size_t workspace_bytes,
+                       int32_t* dev_status, void* stream);
+
+/*
+ * Verification of drafted tokens.  From each request's node 0 down, at node
+ * n with p = softmax(target[n] / T) and, with draft logits, q =
+ * softmax(draft[n] / T), the children are tried in index order, starting
+ * from the residual r = p with mass Z = 1.  Child c, token x:
+ *
+ *   with draft logits   accepted if uniform[c] * Z * q(x) < r(x); if not,
+ *                       r = max(p - S q, 0) with S the sum of the Z so far,
+ *                       and Z = sum_v r(v);
+ *   without             (the draft proposes x for certain) accepted if
+ *                       uniform[c] * Z < r(x); if not, r(x) = 0, Z = sum r.
+ *
+ * An accepted child becomes the next node.  Where none is (or max_depth
+ * tokens have been), the next token is the v with the largest r(v) /
+ * noise(v), the lowest v among equals, and the walk ends (if r is 0
+ * everywhere, p takes its place).  With children drawn from q independently,
+ * uniform in [0, 1) and noise exponentially distributed, the tokens follow
+ * the target's distribution exactly.  T = 0 is greedy: p is 1 at the largest
+ * logit (the lowest index among equals) and 0 elsewhere.
+ *
+ *   target      : (n_nodes, V) logits, FCT_F32 or FCT_BF16, row stride ld_*;
+ *                 row n is the target's distribution after node n.  -inf
+ *                 means probability 0.
+ *   draft       : the same for the draft, or NULL; rows of nodes without
+ *                 children are not read.
+ *   tokens      : (n_nodes,) int64; node 0's is not read.  A drafted token
+ *                 outside [0, V) is rejected (p = q = 0) and sets
+ *                 FCT_DEV_TARGET_OUT_OF_RANGE.
+ *   parent      : (n_nodes,) int32: the parent's index within the request,
+ *                 -1 for node 0.  A node whose parent is not a lower index is
+ *                 no one's child.
+ *   uniform     : (n_nodes,) fp32, read for drafted nodes.
+ *   noise       : (batch, V) fp32, row stride ld_noise, positive.
+ *   temperature : (batch,) fp32, >= 0, or NULL (1).
+ *   out_tokens  : (batch, max_depth + 1) int64: the accepted tokens, the next
+ *                 token, then -1.
+ *   path        : (batch, max_depth) int32: the accepted nodes, then -1.
+ *   count       : (batch,) int32: accepted tokens.
+ * A visited row without a distribution (a NaN, +inf, or nothing above -inf)
+ * accepts nothing, gives the next token -1 and sets FCT_DEV_NO_DISTRIBUTION.
+ * A request without nodes gets count 0 and tokens -1.
+ */
+int fct_spec_verify(const void* target, int64_t ld_target, const void* draft,
+                    int64_t ld_draft, fct_dtype dtype, int64_t n_nodes,
+                    int64_t V, const int64_t* tokens, const int32_t* parent,
+                    const int32_t* node_start, int64_t batch,
+                    const float* uniform, const float* noise, int64_t ld_noise,
+                    const float* temperature, int64_t max_depth,
+                    int64_t* out_tokens, int32_t* path, int32_t* count,
+                    int32_t* dev_status, void* stream);
+
 /* Human-readable name of a fct_status value (static storage). */
 const char* fct_status_string(int status);
 
@@ -635,7 +823,8 @@ const char* fct_status_string(int status);
  * and later: tuning goes through fct_options on the _ex entry points (no
  * process-wide knob).  500 and later: fct_gemm_bf16 and its workspace query;
  * the fused-linear workspace also holds the log-sum-exp partials of the
- * logits GEMMs (query its size again). */
+ * logits GEMMs (query its size again).  600 and later: the speculative
+ * decoding step (fct_kv_cache_*, fct_tree_attention, fct_spec_verify). */
 int fct_version(void);
 
 #ifdef __cplusplus
