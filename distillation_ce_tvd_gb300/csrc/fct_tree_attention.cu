@@ -1,6 +1,10 @@
 // Attention of drafted trees (and of single tokens) over a paged cache; the
 // operation is described in include/fused_ce_tvd.h, fct_tree_attention.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_fp16.h>
+
+#include <mutex>
 
 #include "fct_common.cuh"
 #include "fct_internal.h"
@@ -165,12 +169,1185 @@ cudaError_t launch_general(const AttnArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+// ---------------------------------------------------------------- tensor cores
+//
+// head_dim 64 and 128 over pages of whole 8-token rows.  The rows of a kv
+// head's query tile are the (node, query head of the group) pairs: every key
+// is read once for all of them.
+//
+//   S = Q K^T  (128 rows x 128 keys, fp32 in tensor memory, tcgen05.mma)
+//   P = 2^(S * scale * log2 e - m), rounded to bf16 over S's own columns
+//   O += P V   (P from tensor memory, V as it lies in the cache: MN-major)
+//
+// A unit of work is a request, a kv head and up to 256 rows; its keys come in
+// tiles of 128.  A unit of at most 128 rows gives its even key tiles to
+// softmax group A and its odd ones to group B, each with an S and an O of its
+// own (merged at the end), so that one group's softmax runs beside the other's
+// products; a larger unit gives each group 128 of its rows and every tile.
+// All key tiles of all units, in order, are dealt to the CTAs (one per SM) in
+// equal runs, whatever the requests' lengths; a unit cut between CTAs leaves
+// partial sums in the workspace, which combine_kernel adds in order.
+//
+// Per CTA: warp 0 loads tiles by TMA (one box per page piece), warp 1 issues
+// the products, warps 4-7 and 8-11 are the softmax groups, warps 12-15
+// prepare tiles: they turn e4m3 tiles into bf16 (exact: payload times a power
+// of two), and clear what must not reach a product from the tiles past the
+// context (slots past the end, and non-finite values of drafted nodes, which
+// are added back to the rows that see them).
+
+constexpr int kTile = 128;      // keys per tile, rows per query tile
+constexpr int kAThreads = 512;
+constexpr int kSoftThreads = 256;
+constexpr int kPrepThreads = 128;
+constexpr int kUnitRows = 2 * kTile;
+constexpr int kBadRing = 16;
+constexpr uint32_t kAtTmemCols = 512;
+// Requests of at most this many keys take the weights' rounding remainders
+// (p minus its bf16 value) through a second product: a weight's 2^-8 averages
+// out over many keys, not over few.  Longer ones are bound by their keys'
+// bytes or by the products, and save the second one.
+constexpr int64_t kFineKeys = 2048;
+constexpr float kLazyLog2 = 8.f;  // O is rescaled when the maximum grows by more than 2^8
+
+template <int kD, bool kFp8>
+struct AttnShape {
+  static constexpr int kHalves = kD / 64;  // 128-byte column blocks of a bf16 row
+  static constexpr uint32_t kTileBytes = kTile * kD * 2;
+  static constexpr uint32_t kRawBytes = kTile * kD;
+  static constexpr int kSlots = kD == 128 ? (kFp8 ? 3 : 5) : (kFp8 ? 4 : 8);
+  static constexpr int kRaw = kFp8 ? (kD == 128 ? 4 : 8) : 0;
+  static constexpr size_t kTilesBytes =
+      2 * kTileBytes + size_t(kSlots) * kTileBytes + size_t(kRaw) * kRawBytes;
+  // After the tiles (two of Q, the ring of K and V, the ring of e4m3 tiles).
+  struct Control {
+    uint64_t full_bar[kSlots], empty_bar[kSlots];
+    // bf16: a V tile past the context lands on tail_full and is handed on by
+    // the preparing warps on prep_bar, instead of full_bar
+    uint64_t tail_full[kSlots], prep_bar[kSlots];
+    uint64_t raw_full[kRaw + 1], raw_scaled[kRaw + 1], raw_empty[kRaw + 1];
+    uint64_t s_full[2], p_full[2], q_full, o_full, ml_full, done_bar;
+    int64_t sched[2];
+    union {
+      int64_t scan[kAThreads / 32];  // while the schedule is made
+      float2 ml[2][kTile];           // the groups' maxima and sums, row by row
+    };
+    uint32_t tmem_base;
+    int abort_flag;
+    int bad_seg[kBadRing];
+    uint8_t raw_scale[kRaw ? kRaw : 1][kRaw ? kTile : 1];
+  };
+  static constexpr size_t kSmem = kTilesBytes + sizeof(Control);
+  static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
+};
+
+// What one CTA does with one unit: key tiles [tile0, tile0 + tiles) of it.
+struct Segment {
+  int64_t b;
+  int h;            // kv head
+  int node0;        // first row of q of the request
+  int nodes;        // its nodes
+  int64_t ctx, len; // tokens before the nodes, and with them
+  int row0, rows;   // this unit's rows of the request's nodes * group
+  int64_t tile0;
+  int tiles;
+  bool whole;       // the unit's only segment
+  int part;         // else: workspace slot of this CTA (0 its first, 1 its last)
+};
+
+struct AttnDims {
+  int group;
+  int64_t room;  // positions a block table row holds
+};
+
+struct RequestShape {
+  int node0, nodes;
+  int64_t ctx, len, tiles;
+  int row_units;
+  bool bad;
+  __device__ __forceinline__ int64_t work(int heads) const { return tiles * row_units * heads; }
+};
+
+__device__ __forceinline__ RequestShape request_shape(const AttnArgs& a, const AttnDims& d, int64_t b) {
+  RequestShape r;
+  int64_t n0 = a.node_start[b], n1 = a.node_start[b + 1];
+  r.bad = n0 < 0 || n1 > a.n_nodes || n1 < n0;
+  if (r.bad) n0 = n1 = 0;
+  r.node0 = static_cast<int>(n0);
+  r.nodes = static_cast<int>(n1 - n0);
+  r.ctx = a.pages.context_len[b];
+  if (r.ctx < 0) {
+    r.bad = true;
+    r.ctx = 0;
+  }
+  r.len = r.ctx + r.nodes;
+  if (r.len > d.room) {
+    r.bad = r.bad || r.nodes > 0;
+    r.len = d.room;
+  }
+  r.tiles = (r.len + kTile - 1) / kTile;
+  r.row_units = static_cast<int>((int64_t(r.nodes) * d.group + kUnitRows - 1) / kUnitRows);
+  return r;
+}
+
+// How many CTAs share `total` tiles (each gets one at least), the first tile
+// of CTA c's run, and whose run a tile is in.
+__device__ __forceinline__ int64_t run_count(int64_t total, int64_t ctas) {
+  return total < ctas ? total : ctas;
+}
+__device__ __forceinline__ int64_t run_start(int64_t total, int64_t runs, int64_t c) {
+  return c >= runs ? total : total * c / runs;
+}
+__device__ __forceinline__ int64_t run_of(int64_t total, int64_t runs, int64_t tile) {
+  return ((tile + 1) * runs - 1) / total;
+}
+
+// Walks the segments of a CTA's run; every role of the CTA walks the same.
+struct SegmentWalk {
+  const AttnArgs& a;
+  const AttnDims& d;
+  int64_t b, off, left;
+  __device__ __forceinline__ bool next(Segment& s) {
+    if (left <= 0) return false;
+    RequestShape r = request_shape(a, d, b);
+    int64_t w = r.work(a.cache.n_heads);
+    while (off >= w) {
+      off = 0;
+      if (++b >= a.pages.batch) return false;
+      r = request_shape(a, d, b);
+      w = r.work(a.cache.n_heads);
+    }
+    const int64_t unit = off / r.tiles;
+    s.b = b;
+    s.node0 = r.node0;
+    s.nodes = r.nodes;
+    s.ctx = r.ctx;
+    s.len = r.len;
+    s.h = static_cast<int>(unit / r.row_units);
+    s.row0 = static_cast<int>(unit % r.row_units) * kUnitRows;
+    const int all_rows = r.nodes * d.group;
+    s.rows = all_rows - s.row0 < kUnitRows ? all_rows - s.row0 : kUnitRows;
+    s.tile0 = off % r.tiles;
+    const int64_t n = r.tiles - s.tile0 < left ? r.tiles - s.tile0 : left;
+    s.tiles = static_cast<int>(n);
+    s.whole = n == r.tiles;
+    s.part = s.tile0 > 0 ? 0 : 1;
+    off += n;
+    left -= n;
+    return true;
+  }
+};
+
+__device__ __forceinline__ void tc_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void async_fence() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+// The barrier's phase completes when every product issued before has.
+__device__ __forceinline__ void umma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   smem_addr(bar))
+               : "memory");
+}
+// D = A B^T (+ D): A and B from shared memory, or A from tensor memory.
+template <uint32_t kIdesc>
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(kIdesc), "r"(acc)
+      : "memory");
+}
+template <uint32_t kIdesc>
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "l"(b), "r"(kIdesc), "r"(acc)
+      : "memory");
+}
+// Instruction descriptor: fp32 accumulator, bf16 operands, M = 128, N; bit 16
+// marks an MN-major B.
+__host__ __device__ constexpr uint32_t attn_idesc(int n, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(b_mn) << 16) | (uint32_t(n >> 3) << 17) |
+         (uint32_t(kTile >> 4) << 24);
+}
+// Shared-memory descriptor of a tile in 128-byte swizzle: 8-row atoms 1024
+// bytes apart; MN-major (V: rows are keys): the next 64 columns start one
+// kTile x 128-byte block later.
+__device__ __forceinline__ uint64_t attn_desc(uint32_t saddr, bool mn) {
+  uint64_t d = uint64_t((saddr & 0x3FFFFu) >> 4);
+  d |= uint64_t(mn ? (kTile * 128) >> 4 : 1u) << 16;
+  d |= uint64_t(1024 >> 4) << 32;
+  d |= uint64_t(1) << 46;
+  d |= uint64_t(2) << 61;
+  return d;
+}
+
+#define FCT_R32(r)                                                                              \
+  "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),            \
+      "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),    \
+      "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), \
+      "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), \
+      "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+#define FCT_U32(r)                                                                              \
+  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),        \
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),          \
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),        \
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),        \
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+
+// 32 columns of tensor memory, one lane per thread of the warp.
+__device__ __forceinline__ void tm_ld(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : FCT_R32(r)
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+      "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tm_st(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::FCT_U32(r),
+      "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tm_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// A box of a 4-D tensor map (head_dim, slot, head, page).
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int slot, int head,
+                                        int page, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(slot), "r"(head), "r"(page),
+      "r"(smem_addr(bar))
+      : "memory");
+}
+
+// 32 bits of a node's mask from bit s on (s >= 0).
+__device__ __forceinline__ uint32_t mask_bits(const int64_t* words, int64_t n_words, int64_t s) {
+  const int64_t i = s >> 6;
+  const int sh = static_cast<int>(s & 63);
+  const uint64_t lo = i < n_words ? static_cast<uint64_t>(words[i]) : 0;
+  const uint64_t hi = sh && i + 1 < n_words ? static_cast<uint64_t>(words[i + 1]) << (64 - sh) : 0;
+  return static_cast<uint32_t>((lo >> sh) | hi);
+}
+
+// Which of the 32 keys from position p0 on node i of the segment sees.
+__device__ __forceinline__ uint32_t visible32(const AttnArgs& a, const Segment& s, int node, int64_t p0) {
+  const int64_t first = p0 - s.ctx;  // node index of the first key, or < 0
+  uint32_t m;
+  if (first + 32 <= 0) {
+    m = 0xffffffffu;
+  } else {
+    const int64_t from = first < 0 ? 0 : first;
+    if (a.mask == nullptr) {
+      const int64_t n = node - from + 1;
+      m = n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+    } else {
+      m = mask_bits(a.mask + int64_t(s.node0 + node) * a.mask_words, a.mask_words, from);
+    }
+    if (first < 0) m = (m << -first) | ((1u << -first) - 1u);
+  }
+  const int64_t held = s.len - p0;
+  if (held < 32) m &= held <= 0 ? 0u : (1u << held) - 1u;
+  return m;
+}
+
+// The pool's page and slot of a position; the page may be outside the pool
+// (the table is the caller's).
+__device__ __forceinline__ int page_of(const AttnArgs& a, const Segment& s, int64_t pos, int* slot) {
+  const int64_t p = pos / a.cache.page_size;
+  *slot = static_cast<int>(pos - p * a.cache.page_size);
+  return a.pages.table[s.b * a.pages.ld + p];
+}
+
+// Order in which a segment's K and V tiles are used (and loaded): K runs
+// `lead` tiles ahead of V.  f(is_v, tile) for each.
+template <typename F>
+__device__ __forceinline__ void for_items(int tiles, int lead, F f) {
+  for (int j = 0; j < lead && j < tiles; ++j)
+    if (!f(false, j)) return;
+  for (int j = 0; j < tiles; ++j) {
+    if (!f(true, j)) return;
+    if (j + lead < tiles && !f(false, j + lead)) return;
+  }
+}
+
+// Two e4m3 (bytes 1 and 3 of w, the others 0) to bf16, times 2^-120.
+__device__ __forceinline__ uint32_t e4m3_bits(uint32_t w) {
+  return ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
+template <int kD, bool kFp8>
+__global__ void __launch_bounds__(kAThreads, 1)
+    attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                     const __grid_constant__ AttnArgs a, const __grid_constant__ AttnDims d,
+                     int box_rows, int part_rows) {
+  using Sh = AttnShape<kD, kFp8>;
+  extern __shared__ __align__(1024) uint8_t attn_smem[];
+  auto& ctl = *reinterpret_cast<typename Sh::Control*>(attn_smem + Sh::kTilesBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t smem0 = smem_addr(attn_smem);
+  // The tiles' swizzle needs 1024-byte alignment, which a kernel without
+  // static shared memory has; were it not so, nothing could be computed.
+  if (smem0 % 1024 != 0) {
+    if (threadIdx.x == 0 && a.dev_status) atomicOr(a.dev_status, FCT_DEV_WAIT_TIMEOUT);
+    return;
+  }
+  const uint32_t slot0 = smem0 + 2 * Sh::kTileBytes;
+  const uint32_t raw0 = slot0 + Sh::kSlots * Sh::kTileBytes;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Sh::kSlots; ++i) {
+      mbar_init(&ctl.full_bar[i], kFp8 ? kPrepThreads : 1);
+      mbar_init(&ctl.empty_bar[i], 1);
+      mbar_init(&ctl.tail_full[i], 1);
+      mbar_init(&ctl.prep_bar[i], kPrepThreads);
+    }
+    for (int i = 0; i < Sh::kRaw; ++i) {
+      mbar_init(&ctl.raw_full[i], 1);
+      mbar_init(&ctl.raw_scaled[i], 32);
+      mbar_init(&ctl.raw_empty[i], kPrepThreads);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&ctl.s_full[w], 1);
+      mbar_init(&ctl.p_full[w], kTile);
+    }
+    mbar_init(&ctl.q_full, kSoftThreads);
+    mbar_init(&ctl.o_full, 1);
+    mbar_init(&ctl.ml_full, kSoftThreads);
+    mbar_init(&ctl.done_bar, 1);
+    ctl.abort_flag = 0;
+    for (int i = 0; i < kBadRing; ++i) ctl.bad_seg[i] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(&ctl.tmem_base)),
+                 "r"(kAtTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+
+  // The schedule: the sum of all requests' tiles, then the request and the
+  // offset in it where this CTA's run starts.
+  bool bad_request = false;
+  int64_t total = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t before = 0;
+    const int64_t start = pass ? run_start(total, run_count(total, gridDim.x), blockIdx.x) : -1;
+    for (int64_t b0 = 0; b0 < a.pages.batch; b0 += kAThreads) {
+      const int64_t b = b0 + threadIdx.x;
+      int64_t w = 0;
+      if (b < a.pages.batch) {
+        const RequestShape r = request_shape(a, d, b);
+        w = r.work(a.cache.n_heads);
+        bad_request |= r.bad;
+      }
+      int64_t incl = w;
+#pragma unroll
+      for (int k = 1; k < 32; k <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, incl, k);
+        if (lane >= k) incl += o;
+      }
+      __syncthreads();
+      if (lane == 31) ctl.scan[warp] = incl;
+      __syncthreads();
+      int64_t base = before, all = 0;
+      for (int i = 0; i < kAThreads / 32; ++i) {
+        if (i < warp) base += ctl.scan[i];
+        all += ctl.scan[i];
+      }
+      if (pass && w > 0 && base + incl - w <= start && start < base + incl) {
+        ctl.sched[0] = b;
+        ctl.sched[1] = start - (base + incl - w);
+      }
+      before += all;
+    }
+    total = before;
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = ctl.tmem_base;
+  const int64_t runs = run_count(total, gridDim.x);
+  const int64_t run0 = run_start(total, runs, blockIdx.x);
+  const int64_t run1 = run_start(total, runs, blockIdx.x + 1);
+  SegmentWalk walk{a, d, run1 > run0 ? ctl.sched[0] : 0, run1 > run0 ? ctl.sched[1] : 0, run1 - run0};
+  Segment seg;
+  int32_t status = 0;
+  if (bad_request && blockIdx.x == 0) status |= FCT_DEV_INDEX_OUT_OF_RANGE;
+  auto lead_of = [](const Segment& s) { return s.rows > kTile ? 1 : 2; };
+  // whether a key tile (index in the unit) reaches past the context
+  auto is_tail = [](const Segment& s, int64_t tile) { return (tile + 1) * kTile > s.ctx; };
+
+  if (warp == 0) {
+    // ---- loads: the warp's lanes take a tile's boxes
+    constexpr int kBoxCols = kFp8 ? 1 : Sh::kHalves;
+    constexpr int kRing = kFp8 ? Sh::kRaw : Sh::kSlots;
+    uint64_t* full = kFp8 ? ctl.raw_full : ctl.full_bar;
+    uint64_t* empty = kFp8 ? ctl.raw_empty : ctl.empty_bar;
+    const uint32_t ring0 = kFp8 ? raw0 : slot0;
+    constexpr uint32_t kItemBytes = kFp8 ? Sh::kRawBytes : Sh::kTileBytes;
+    const int boxes = kTile / box_rows * kBoxCols;
+    const uint32_t box_bytes = uint32_t(box_rows) * (kFp8 ? kD : 128);
+    uint32_t item = 0;
+    // per slot: the barrier of its last fill (1: tail_full), and each
+    // barrier's next parity
+    uint32_t last_tail = 0, full_phase = 0, tail_phase = 0;
+    bool ok = true;
+    while (ok && walk.next(seg)) {
+      for_items(seg.tiles, lead_of(seg), [&](bool is_v, int j) {
+        const uint32_t slot = item % kRing, phase = (item / kRing) & 1u;
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], phase ^ 1u, &ctl.abort_flag))) {
+          ok = false;
+          return false;
+        }
+        const bool prep = !kFp8 && is_v && is_tail(seg, seg.tile0 + j);
+        uint64_t* bar = prep ? &ctl.tail_full[slot] : &full[slot];
+        last_tail = (last_tail & ~(1u << slot)) | (uint32_t(prep) << slot);
+        (prep ? tail_phase : full_phase) ^= 1u << slot;
+        const int64_t p0 = (seg.tile0 + j) * kTile;
+        const int64_t held = seg.len - p0;
+        const int rows = held < kTile ? static_cast<int>(held) : kTile;
+        if (lane == 0)
+          mbar_arrive_expect_tx(bar,
+                                uint32_t((rows + box_rows - 1) / box_rows) * kBoxCols * box_bytes);
+        __syncwarp();
+        const int piece = lane / kBoxCols, half = lane % kBoxCols;
+        if (lane < boxes && piece * box_rows < rows) {
+          int at;
+          const int page = page_of(a, seg, p0 + piece * box_rows, &at);
+          if (page < 0 || page >= a.cache.num_pages) status |= FCT_DEV_INDEX_OUT_OF_RANGE;
+          const uint32_t dst = ring0 + slot * kItemBytes +
+                               (kFp8 ? uint32_t(piece) * box_bytes
+                                     : uint32_t(half) * (kTile * 128) + uint32_t(piece) * box_bytes);
+          tma_box(dst, is_v ? &map_v : &map_k, half * 64, at, seg.h, page, bar);
+        }
+        ++item;
+        return true;
+      });
+    }
+    // the last fills have landed before the CTA ends (bounded, even after an
+    // abort)
+    for (uint32_t slot = 0; slot < uint32_t(kRing) && slot < item; ++slot) {
+      const bool tail = (last_tail >> slot) & 1u;
+      mbar_wait(tail ? &ctl.tail_full[slot] : &full[slot],
+                (((tail ? tail_phase : full_phase) >> slot) & 1u) ^ 1u, &ctl.abort_flag, false);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---- products
+      constexpr uint32_t kIdS = attn_idesc(kTile, false), kIdO = attn_idesc(kD, true);
+      const uint32_t tm_s[2] = {tmem, tmem + kTile};
+      const uint32_t tm_o[2] = {tmem + 2 * kTile, tmem + 2 * kTile + kD};
+      uint32_t item = 0, seg_n = 0, full_phase = 0, prep_phase = 0;
+      uint32_t p_n[2] = {0, 0};
+      bool ok = true;
+      auto wait_item = [&](uint32_t it) {
+        const uint32_t slot = it % Sh::kSlots;
+        const bool got = mbar_wait(&ctl.full_bar[slot], (full_phase >> slot) & 1u, &ctl.abort_flag);
+        full_phase ^= 1u << slot;
+        return got;
+      };
+      auto scores = [&](int w, int q_tile, uint32_t it) {
+        const uint64_t qd = attn_desc(smem0 + uint32_t(q_tile) * Sh::kTileBytes, false);
+        const uint64_t kd = attn_desc(slot0 + (it % Sh::kSlots) * Sh::kTileBytes, false);
+#pragma unroll
+        for (int k = 0; k < kD / 16; ++k) {
+          const uint64_t step = uint64_t((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4;
+          umma_ss<kIdS>(tm_s[w], qd + step, kd + step, k > 0);
+        }
+        umma_commit(&ctl.s_full[w]);
+      };
+      auto values = [&](int w, uint32_t it, bool first) {
+        const uint64_t vd = attn_desc(slot0 + (it % Sh::kSlots) * Sh::kTileBytes, true);
+        for (int part = 0; part < (seg.len <= kFineKeys ? 2 : 1); ++part) {
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            umma_ts<kIdO>(tm_o[w], tm_s[w] + part * (kTile / 2) + k * 8,
+                          vd + uint64_t(k * 16 * 128 >> 4), !first || part + k > 0);
+        }
+      };
+      auto wait_p = [&](int w) {
+        const bool got = mbar_wait(&ctl.p_full[w], p_n[w] & 1u, &ctl.abort_flag);
+        ++p_n[w];
+        tc_after();
+        return got;
+      };
+      auto wait_v = [&](uint32_t it, int64_t tile) {
+        if (kFp8 || !is_tail(seg, tile)) return wait_item(it);
+        const uint32_t slot = it % Sh::kSlots;
+        const bool got = mbar_wait(&ctl.prep_bar[slot], (prep_phase >> slot) & 1u, &ctl.abort_flag);
+        prep_phase ^= 1u << slot;
+        return got;
+      };
+      while (ok && walk.next(seg)) {
+        const bool two = seg.rows > kTile;
+        if (!mbar_wait(&ctl.q_full, seg_n & 1u, &ctl.abort_flag)) break;
+        ++seg_n;
+        tc_after();
+        if (two) {
+          uint32_t k_item = item++;
+          ok = wait_item(k_item);
+          if (!ok) break;
+          tc_after();
+          scores(0, 0, k_item);
+          scores(1, 1, k_item);
+          umma_commit(&ctl.empty_bar[k_item % Sh::kSlots]);
+          for (int j = 0; ok && j < seg.tiles; ++j) {
+            const uint32_t v_item = item++;
+            const bool more = j + 1 < seg.tiles;
+            if (more) k_item = item++;
+            ok = wait_v(v_item, seg.tile0 + j) && wait_p(0);
+            if (!ok) break;
+            values(0, v_item, j == 0);
+            if (more) {
+              ok = wait_item(k_item);
+              if (!ok) break;
+              tc_after();
+              scores(0, 0, k_item);
+            }
+            ok = wait_p(1);
+            if (!ok) break;
+            values(1, v_item, j == 0);
+            umma_commit(&ctl.empty_bar[v_item % Sh::kSlots]);
+            if (more) {
+              scores(1, 1, k_item);
+              umma_commit(&ctl.empty_bar[k_item % Sh::kSlots]);
+            }
+          }
+        } else {
+          for (int j = 0; ok && j < 2 && j < seg.tiles; ++j) {
+            const uint32_t k_item = item++;
+            ok = wait_item(k_item);
+            if (!ok) break;
+            tc_after();
+            scores(j, 0, k_item);
+            umma_commit(&ctl.empty_bar[k_item % Sh::kSlots]);
+          }
+          for (int j = 0; ok && j < seg.tiles; ++j) {
+            const uint32_t v_item = item++;
+            ok = wait_v(v_item, seg.tile0 + j) && wait_p(j & 1);
+            if (!ok) break;
+            values(j & 1, v_item, j < 2);
+            umma_commit(&ctl.empty_bar[v_item % Sh::kSlots]);
+            if (j + 2 < seg.tiles) {
+              const uint32_t k_item = item++;
+              ok = wait_item(k_item);
+              if (!ok) break;
+              tc_after();
+              scores(j & 1, 0, k_item);
+              umma_commit(&ctl.empty_bar[k_item % Sh::kSlots]);
+            }
+          }
+        }
+        if (ok) umma_commit(&ctl.o_full);
+      }
+      umma_commit(&ctl.done_bar);  // every product issued has completed
+    }
+  } else if (warp == 2) {
+    if constexpr (kFp8) {
+      // ---- scale bytes of the raw tiles, four keys per lane
+      uint32_t item = 0;
+      bool ok = true;
+      while (ok && walk.next(seg)) {
+        for_items(seg.tiles, lead_of(seg), [&](bool is_v, int j) {
+          const uint32_t r = item % Sh::kRaw, phase = (item / Sh::kRaw) & 1u;
+          if (!__all_sync(0xffffffffu, mbar_wait(&ctl.raw_empty[r], phase ^ 1u, &ctl.abort_flag))) {
+            ok = false;
+            return false;
+          }
+          const int64_t p0 = (seg.tile0 + j) * kTile;
+#pragma unroll
+          for (int i = 0; i < kTile / 32; ++i) {
+            const int64_t pos = p0 + i * 32 + lane;
+            uint8_t byte = 0;
+            if (pos < seg.len) {
+              int at;
+              const int64_t page = page_of(a, seg, pos, &at);
+              if (page >= 0 && page < a.cache.num_pages)
+                byte = (is_v ? a.cache.v_scale : a.cache.k_scale)[page * a.cache.scale_page_stride +
+                                                                  at * a.cache.scale_slot_stride +
+                                                                  seg.h * a.cache.scale_head_stride];
+            }
+            ctl.raw_scale[r][i * 32 + lane] = byte;
+          }
+          mbar_arrive(&ctl.raw_scaled[r]);
+          ++item;
+          return true;
+        });
+      }
+    }
+  } else if (warp >= 12) {
+    // ---- tiles prepared
+    const int t = threadIdx.x - 12 * 32;
+    uint32_t item = 0, tail_phase = 0;
+    int seg_n = 0;
+    bool ok = true;
+    while (ok && walk.next(seg)) {
+      ++seg_n;
+      for_items(seg.tiles, lead_of(seg), [&](bool is_v, int j) {
+        const uint32_t it = item++;
+        const uint32_t slot = it % Sh::kSlots;
+        const int64_t tile = seg.tile0 + j, p0 = tile * kTile;
+        const uint32_t dst = slot0 + slot * Sh::kTileBytes;
+        if constexpr (kFp8) {
+          const uint32_t r = it % Sh::kRaw;
+          if (!mbar_wait(&ctl.raw_full[r], (it / Sh::kRaw) & 1u, &ctl.abort_flag) ||
+              !mbar_wait(&ctl.raw_scaled[r], (it / Sh::kRaw) & 1u, &ctl.abort_flag) ||
+              !mbar_wait(&ctl.empty_bar[slot], ((it / Sh::kSlots) & 1u) ^ 1u, &ctl.abort_flag)) {
+            ok = false;
+            return false;
+          }
+          constexpr int kChunks = kD / 16;  // 16 payload bytes each
+          const uint32_t src = raw0 + r * Sh::kRawBytes;
+          const int c = t % kChunks;
+          bool found = false;
+#pragma unroll 2
+          for (int i = 0; i < kTile * kChunks / kPrepThreads; ++i) {
+            const int row = i * (kPrepThreads / kChunks) + t / kChunks;
+            uint32_t byte = ctl.raw_scale[r][row];
+            uint4 w;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                         : "r"(src + uint32_t(row) * kD + uint32_t(c) * 16));
+            const int64_t pos = p0 + row;
+            if (is_v && pos >= seg.ctx && (pos >= seg.len || byte == 255)) {
+              found |= pos < seg.len;
+              w = make_uint4(0, 0, 0, 0);
+              byte = 127;
+            }
+            // 2^120 * 2^(byte - 127) as one bf16 factor, or as two
+            const bool one = byte <= 134;
+            const uint32_t m1 = (one ? byte + 120 : 247u) << 7;
+            const uint32_t m2 = byte == 255 ? 0x7fc0u : byte << 7;
+            const uint32_t f1 = m1 | (m1 << 16), f2 = m2 | (m2 << 16);
+            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              o[2 * k] = mul_bf16x2(e4m3_bits(__byte_perm(in[k], 0, 0x1404)), f1);
+              o[2 * k + 1] = mul_bf16x2(e4m3_bits(__byte_perm(in[k], 0, 0x3424)), f1);
+            }
+            if (!one) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], f2);
+            }
+            const uint32_t line = dst + uint32_t(c / 4) * (kTile * 128) + uint32_t(row) * 128;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               line + uint32_t((((c % 4) * 2 + k) ^ (row & 7)) * 16)),
+                           "r"(o[4 * k]), "r"(o[4 * k + 1]), "r"(o[4 * k + 2]), "r"(o[4 * k + 3])
+                           : "memory");
+          }
+          if (found) ctl.bad_seg[seg_n % kBadRing] = seg_n;
+          mbar_arrive(&ctl.raw_empty[r]);
+          async_fence();
+          mbar_arrive(&ctl.full_bar[slot]);
+        } else {
+          if (!is_v || !is_tail(seg, tile)) return true;
+          if (!mbar_wait(&ctl.tail_full[slot], (tail_phase >> slot) & 1u, &ctl.abort_flag)) {
+            ok = false;
+            return false;
+          }
+          tail_phase ^= 1u << slot;
+          const int64_t pos = p0 + t;
+          if (pos >= seg.ctx) {
+            const bool past = pos >= seg.len;
+            bool found = false;
+            for (int c = 0; c < kD / 8; ++c) {
+              const uint32_t at = dst + uint32_t(c / 8) * (kTile * 128) + uint32_t(t) * 128 +
+                                  uint32_t(((c % 8) ^ (t & 7)) * 16);
+              uint32_t w[4];
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                           : "r"(at));
+              bool change = past;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const bool lo = (w[k] & 0x7f80u) == 0x7f80u, hi = (w[k] & 0x7f800000u) == 0x7f800000u;
+                change |= lo || hi;
+                if (past || lo) w[k] &= 0xffff0000u;
+                if (past || hi) w[k] &= 0x0000ffffu;
+              }
+              if (change) {
+                found |= !past;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]),
+                             "r"(w[2]), "r"(w[3])
+                             : "memory");
+              }
+            }
+            if (found) ctl.bad_seg[seg_n % kBadRing] = seg_n;
+          }
+          async_fence();
+          mbar_arrive(&ctl.prep_bar[slot]);
+        }
+        return true;
+      });
+    }
+  } else if (warp >= 4) {
+    // ---- softmax groups A (warps 4-7) and B (8-11): one row per thread
+    const int w = warp >= 8 ? 1 : 0;
+    const int r = threadIdx.x & (kTile - 1);       // row of the query tile, lane of tensor memory
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t tm_s = tmem + uint32_t(w) * kTile + lanes;
+    const uint32_t tm_o = tmem + 2 * kTile + lanes;
+    const float sl2 = fabsf(a.scale) * kLog2e;
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+    const bool vec_q = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && a.ld_qn % 8 == 0 && a.ld_qh % 8 == 0;
+    const bool vec_o = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.ld_on % 8 == 0 && a.ld_oh % 8 == 0;
+    uint32_t s_n = 0, ml_n = 0;
+    int seg_n = 0;
+    bool ok = true;
+    while (ok && walk.next(seg)) {
+      ++seg_n;
+      const bool two = seg.rows > kTile;
+      const int row = (two ? w * kTile : 0) + r;   // of the unit
+      const bool live = row < seg.rows;
+      const bool warp_live = (row & ~31) < seg.rows;
+      const int node = live ? (seg.row0 + row) / d.group : 0;
+      const int head = seg.h * d.group + (live ? (seg.row0 + row) % d.group : 0);
+      // the query tile, in the products' swizzle; with one tile its columns
+      // are split over the groups
+      if (live) {
+        const uint16_t* src = static_cast<const uint16_t*>(a.q) + int64_t(seg.node0 + node) * a.ld_qn +
+                              int64_t(head) * a.ld_qh;
+        const uint32_t dst = smem0 + (two ? uint32_t(w) * Sh::kTileBytes : 0u) + uint32_t(r) * 128;
+        const int c0 = two ? 0 : w * (kD / 16), c1 = two ? kD / 8 : c0 + kD / 16;
+        for (int c = c0; c < c1; ++c) {
+          uint32_t x[4];
+          if (vec_q) {
+            const uint4 v = *reinterpret_cast<const uint4*>(src + c * 8);
+            x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              x[k] = uint32_t(src[c * 8 + 2 * k]) | (uint32_t(src[c * 8 + 2 * k + 1]) << 16);
+          }
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           dst + uint32_t(c / 8) * (kTile * 128) + uint32_t(((c % 8) ^ (r & 7)) * 16)),
+                       "r"(x[0] ^ flip), "r"(x[1] ^ flip), "r"(x[2] ^ flip), "r"(x[3] ^ flip)
+                       : "memory");
+        }
+      }
+      async_fence();
+      tc_before();
+      mbar_arrive(&ctl.q_full);
+
+      float m = -INFINITY, l = 0.f;   // the weights' exponent offset and their sum
+      bool first = true;
+      for (int j = two ? 0 : w; j < seg.tiles; j += two ? 1 : 2) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&ctl.s_full[w], s_n & 1u, &ctl.abort_flag))) {
+          ok = false;
+          break;
+        }
+        ++s_n;
+        tc_after();
+        if (warp_live) {
+          const int64_t p0 = (seg.tile0 + j) * kTile;
+          const bool tail = is_tail(seg, seg.tile0 + j);
+          uint32_t vis[4];
+          if (tail) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vis[i] = live ? visible32(a, seg, node, p0 + 32 * i) : 0u;
+          }
+          __syncwarp();
+          float top = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t x[32];
+            tm_ld(tm_s + 32 * i, x);
+            if (tail) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!((vis[i] >> k) & 1u)) x[k] = 0xff800000u;
+            }
+#pragma unroll
+            for (int k = 0; k < 32; k += 2)
+              top = max3(top, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+          }
+          top *= sl2;
+          const bool grow = top > m + kLazyLog2 || (m == -INFINITY && top > -INFINITY);
+          if (__any_sync(0xffffffffu, grow)) {
+            const float f = grow ? ex2(m - top) : 1.f;
+            if (grow) m = top;
+            l *= f;
+            if (!first) {
+#pragma unroll 1
+              for (int i = 0; i < kD / 32; ++i) {
+                uint32_t x[32];
+                tm_ld(tm_o + uint32_t(w * kD + 32 * i), x);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
+                tm_st(tm_o + uint32_t(w * kD + 32 * i), x);
+              }
+            }
+          }
+          const float off = m == -INFINITY ? 0.f : -m;
+          const float2 s2 = make_float2(sl2, sl2), o2 = make_float2(off, off);
+          float2 sum = make_float2(0.f, 0.f);
+          // P over S's first half, and its remainders over the second: what a
+          // chunk's remainders overwrite has been read two chunks later
+          const bool fine = seg.len <= kFineKeys;
+          uint32_t low[32];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t x[32], p[16];
+            tm_ld(tm_s + 32 * i, x);
+            if (tail) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!((vis[i] >> k) & 1u)) x[k] = 0xff800000u;
+            }
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              float2 e = __ffma2_rn(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), s2, o2);
+              e.x = ex2(e.x);
+              e.y = ex2(e.y);
+              sum = __fadd2_rn(sum, e);
+              p[k / 2] = pack_bf16x2(e.x, e.y);
+              x[k] = __float_as_uint(e.x);
+              x[k + 1] = __float_as_uint(e.y);
+            }
+            tm_st16(tm_s + 16 * i, p);
+            if (fine) {
+              if (i == 2) tm_st(tm_s + kTile / 2, low);
+#pragma unroll
+              for (int k = 0; k < 32; k += 2)
+                low[16 * (i & 1) + k / 2] =
+                    pack_bf16x2(__uint_as_float(x[k]) - __uint_as_float(p[k / 2] << 16),
+                                __uint_as_float(x[k + 1]) - __uint_as_float(p[k / 2] & 0xffff0000u));
+              if (i == 3) tm_st(tm_s + kTile / 2 + 32, low);
+            }
+          }
+          l += sum.x + sum.y;
+          tm_st_wait();
+        }
+        first = false;
+        tc_before();
+        mbar_arrive(&ctl.p_full[w]);
+      }
+      if (!ok || !__all_sync(0xffffffffu, mbar_wait(&ctl.o_full, (seg_n - 1) & 1u, &ctl.abort_flag))) break;
+      tc_after();
+      const bool fix = *reinterpret_cast<volatile int*>(&ctl.bad_seg[seg_n % kBadRing]) == seg_n;
+
+      // one tile of rows: both groups hold sums of the same row; each
+      // finishes half of the columns
+      float wa = 1.f, wb = 0.f, M = m, L = l;
+      if (!two) {
+        // (the next segment's write follows every thread's read of this one's:
+        // it waits for products that wait for all threads' query rows)
+        ctl.ml[w][r] = make_float2(m, l);
+        mbar_arrive(&ctl.ml_full);
+        if (!__all_sync(0xffffffffu, mbar_wait(&ctl.ml_full, ml_n & 1u, &ctl.abort_flag))) break;
+        ++ml_n;
+        const float2 A = ctl.ml[0][r], B = seg.tiles > 1 ? ctl.ml[1][r] : make_float2(-INFINITY, 0.f);
+        M = fmaxf(A.x, B.x);
+        const float base = M == -INFINITY ? 0.f : M;
+        wa = ex2(A.x - base);
+        wb = ex2(B.x - base);
+        L = A.y * wa + B.y * wb;
+      }
+      if (warp_live) {
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const int c0 = two ? 0 : w * (kD / 2), c1 = two ? kD : c0 + kD / 2;
+        float* part = nullptr;
+        if (!seg.whole) {
+          float* base = static_cast<float*>(a.workspace) +
+                        (int64_t(blockIdx.x) * 2 + seg.part) * part_rows * (kD + 2);
+          part = base + int64_t(row) * kD;
+          if (live && (two || w == 0))
+            reinterpret_cast<float2*>(base + int64_t(part_rows) * kD)[row] = make_float2(M, L);
+        } else if (live && (two || w == 0) && a.lse) {
+          a.lse[int64_t(seg.node0 + node) * a.n_q_heads + head] =
+              L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+        }
+#pragma unroll 1
+        for (int c = c0; c < c1; c += 32) {
+          uint32_t x[32];
+          float o[32];
+          __syncwarp();
+          if (two) {
+            tm_ld(tm_o + uint32_t(w * kD + c), x);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __uint_as_float(x[k]);
+          } else {
+            tm_ld(tm_o + uint32_t(c), x);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __uint_as_float(x[k]) * wa;
+            if (seg.tiles > 1) {
+              tm_ld(tm_o + uint32_t(kD + c), x);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = fmaf(__uint_as_float(x[k]), wb, o[k]);
+            }
+          }
+          if (live && fix) {
+            // non-finite values of drafted nodes that this row sees
+            const int64_t end = (seg.tile0 + seg.tiles) * kTile < seg.len ? (seg.tile0 + seg.tiles) * kTile : seg.len;
+            for (int64_t pos = seg.ctx > seg.tile0 * kTile ? seg.ctx : seg.tile0 * kTile; pos < end; ++pos) {
+              if (!(visible32(a, seg, node, pos) & 1u)) continue;
+              int at;
+              const int64_t page = page_of(a, seg, pos, &at);
+              if (page < 0 || page >= a.cache.num_pages) continue;
+              if constexpr (kFp8) {
+                if (a.cache.v_scale[page * a.cache.scale_page_stride + at * a.cache.scale_slot_stride +
+                                    seg.h * a.cache.scale_head_stride] == 255) {
+#pragma unroll
+                  for (int k = 0; k < 32; ++k) o[k] = __int_as_float(0x7fc00000);
+                }
+              } else {
+                const bf16_t* v = static_cast<const bf16_t*>(a.cache.v) + page * a.cache.page_stride +
+                                  at * a.cache.slot_stride + seg.h * a.cache.head_stride + c;
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                  const float y = Elem<bf16_t>::load1(v + k);
+                  if (!(fabsf(y) < INFINITY)) o[k] += y;
+                }
+              }
+            }
+          }
+          if (live && part) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<float4*>(part + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          } else if (live) {
+            uint16_t* dst = static_cast<uint16_t*>(a.out) + int64_t(seg.node0 + node) * a.ld_on +
+                            int64_t(head) * a.ld_oh + c;
+            if (L == 0.f) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = 0.f;
+            } else {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] *= inv;
+            }
+            if (vec_o) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 8)
+                *reinterpret_cast<uint4*>(dst + k) =
+                    make_uint4(pack_bf16x2(o[k], o[k + 1]), pack_bf16x2(o[k + 2], o[k + 3]),
+                               pack_bf16x2(o[k + 4], o[k + 5]), pack_bf16x2(o[k + 6], o[k + 7]));
+            } else {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) dst[k] = static_cast<uint16_t>(pack_bf16x2(o[k], 0.f));
+            }
+          }
+        }
+      }
+    }
+  }
+  tc_before();
+  __syncthreads();
+  if (warp == 1) {
+    if (lane == 0) mbar_wait(&ctl.done_bar, 0, &ctl.abort_flag, false);
+    __syncwarp();
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kAtTmemCols)
+                 : "memory");
+  }
+  if (threadIdx.x == 0 && ctl.abort_flag) status |= FCT_DEV_WAIT_TIMEOUT;
+  if (status && a.dev_status) atomicOr(a.dev_status, status);
+}
+
+// Adds the partial sums of units that were cut between CTAs: one warp per
+// node and query head, the pieces in the order of the keys.
+constexpr int kCombineWarps = 4;
+
+template <int kD>
+__global__ void __launch_bounds__(kCombineWarps * 32)
+    combine_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnDims d, int ctas,
+                   int part_rows) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t item = int64_t(blockIdx.x) * kCombineWarps + warp;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (item >= a.n_nodes * a.n_q_heads) return;
+  const int64_t node = item / a.n_q_heads;
+  const int head = static_cast<int>(item % a.n_q_heads);
+  // tiles before the node's request, and all
+  int64_t total = 0, before = 0, mine = -1;
+  RequestShape r{};
+  for (int64_t b0 = 0; b0 < a.pages.batch; b0 += 32) {
+    const int64_t b = b0 + lane;
+    RequestShape x{};
+    int64_t w = 0;
+    if (b < a.pages.batch) {
+      x = request_shape(a, d, b);
+      w = x.work(a.cache.n_heads);
+    }
+    const unsigned here = __ballot_sync(0xffffffffu, w > 0 && node >= x.node0 && node < x.node0 + x.nodes);
+    int64_t incl = w;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, incl, k);
+      if (lane >= k) incl += o;
+    }
+    if (here) {
+      const int src = __ffs(here) - 1;
+      mine = b0 + src;
+      before = total + __shfl_sync(0xffffffffu, incl - w, src);
+    }
+    total += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (mine < 0) return;
+  r = request_shape(a, d, mine);
+  const int row = static_cast<int>(node - r.node0) * d.group + head % d.group;
+  const int64_t unit = int64_t(head / d.group) * r.row_units + row / kUnitRows;
+  const int64_t t0 = before + unit * r.tiles, t1 = t0 + r.tiles;
+  const int64_t runs = run_count(total, ctas);
+  const int64_t c0 = run_of(total, runs, t0), c1 = run_of(total, runs, t1 - 1);
+  if (c0 == c1) return;
+  const int at = row % kUnitRows;
+  const float* ws = static_cast<const float*>(a.workspace);
+  const int64_t slot = int64_t(part_rows) * (kD + 2);
+  constexpr int kPer = kD / 32;
+  float M = -INFINITY, L = 0.f, o[kPer] = {};
+  for (int64_t c = c0; c <= c1; ++c) {
+    const float* p = ws + (c * 2 + (c == c0 ? 1 : 0)) * slot;
+    const float2 x = reinterpret_cast<const float2*>(p + int64_t(part_rows) * kD)[at];
+    const float mn = fmaxf(M, x.x);
+    const float base = mn == -INFINITY ? 0.f : mn;
+    const float f = ex2(M - base), g = ex2(x.x - base);
+    L = L * f + x.y * g;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      o[k] = o[k] * f + (g == 0.f ? 0.f : g * p[int64_t(at) * kD + lane * kPer + k]);
+    M = mn;
+  }
+  bf16_t* dst = static_cast<bf16_t*>(a.out) + node * a.ld_on + int64_t(head) * a.ld_oh + lane * kPer;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) Elem<bf16_t>::store1(dst + k, L == 0.f ? 0.f : o[k] / L);
+  if (a.lse && lane == 0) a.lse[item] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 attn_encode_fn() {
+  static std::once_flag once;
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    else
+      cudaGetLastError();
+  });
+  return fn;
+}
+
+// Tensor map of a pool: (head_dim, slot, head, page), boxes of box_rows slots
+// of one head and page; bf16 in 64-column blocks with 128-byte swizzle, e4m3
+// whole rows as they are.
+bool cache_map(CUtensorMap* map, const fct_kv_cache& c, void* base, int box_rows) {
+  auto encode = attn_encode_fn();
+  if (encode == nullptr) return false;
+  const bool fp8 = c.dtype == FCT_E4M3;
+  const cuuint64_t e = fp8 ? 1 : 2;
+  const cuuint64_t dims[4] = {cuuint64_t(c.head_dim), cuuint64_t(c.page_size), cuuint64_t(c.n_heads),
+                              cuuint64_t(c.num_pages)};
+  const cuuint64_t strides[3] = {cuuint64_t(c.slot_stride) * e, cuuint64_t(c.head_stride) * e,
+                                 cuuint64_t(c.page_stride) * e};
+  const cuuint32_t box[4] = {cuuint32_t(fp8 ? c.head_dim : 64), cuuint32_t(box_rows), 1, 1};
+  const cuuint32_t elem[4] = {1, 1, 1, 1};
+  return encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base,
+                dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Whether the tensor-core kernel takes this cache: a head_dim it is built
+// for, pages of whole 8-token rows (a TMA box fills whole swizzle atoms), and
+// what a tensor map needs (16-byte base and strides, 40-bit strides, 32-bit
+// sizes).
+bool tensor_core_layout(const fct_kv_cache& c) {
+  if (c.head_dim != 64 && c.head_dim != 128) return false;
+  if (c.page_size % 8 != 0 || c.num_pages > INT32_MAX) return false;
+  const int64_t e = c.dtype == FCT_E4M3 ? 1 : 2;
+  for (const void* p : {c.k, c.v})
+    if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return false;
+  for (int64_t s : {c.slot_stride, c.head_stride, c.page_stride})
+    if ((s * e) % 16 != 0 || s * e >= (int64_t(1) << 40) || s <= 0) return false;
+  return true;
+}
+
+// Rows of a workspace slot: the most a unit has, in fours (16-byte rows).
+int part_rows_of(int64_t n_nodes, int group) {
+  const int64_t rows = (n_nodes * group + 3) / 4 * 4;
+  return static_cast<int>(rows < kUnitRows ? rows : kUnitRows);
+}
+
+template <int kD, bool kFp8>
+cudaError_t launch_tensor(const AttnArgs& a, int sms, int device, cudaStream_t st) {
+  using Sh = AttnShape<kD, kFp8>;
+  static std::once_flag once[64];
+  static cudaError_t ready[64];
+  if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+  auto kernel = attention_kernel<kD, kFp8>;
+  std::call_once(once[device], [&] {
+    ready[device] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(Sh::kSmem));
+  });
+  if (ready[device] != cudaSuccess) return ready[device];
+  int box_rows = kTile;
+  while (a.cache.page_size % box_rows != 0) box_rows /= 2;
+  CUtensorMap mk, mv;
+  if (!cache_map(&mk, a.cache, a.cache.k, box_rows) || !cache_map(&mv, a.cache, a.cache.v, box_rows))
+    return cudaErrorInvalidValue;
+  const AttnDims d{a.n_q_heads / a.cache.n_heads, a.pages.max_pages * a.cache.page_size};
+  const int part_rows = part_rows_of(a.n_nodes, d.group);
+  kernel<<<static_cast<unsigned>(sms), kAThreads, Sh::kSmem, st>>>(mk, mv, a, d, box_rows, part_rows);
+  cudaError_t e = cudaGetLastError();
+  // units of one tile are never cut
+  if (e != cudaSuccess || d.room <= kTile) return e;
+  const int64_t items = a.n_nodes * a.n_q_heads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((items + kCombineWarps - 1) / kCombineWarps));
+  cfg.blockDim = dim3(kCombineWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, combine_kernel<kD>, a, d, sms, part_rows);
+}
+
 }  // namespace
 
-size_t attn_workspace_bytes(int64_t, int, int, int, int) { return 0; }
+size_t attn_workspace_bytes(int64_t n_nodes, int n_q_heads, int n_heads, int head_dim, int sms) {
+  if (head_dim != 64 && head_dim != 128) return 0;
+  return size_t(sms) * 2 * size_t(part_rows_of(n_nodes, n_q_heads / n_heads)) * (head_dim + 2) * 4;
+}
 
-cudaError_t launch_attention(const AttnArgs& a, int, int, cudaStream_t st) {
-  return launch_general(a, st);
+cudaError_t launch_attention(const AttnArgs& a, int sms, int device, cudaStream_t st) {
+  if (!tensor_core_layout(a.cache)) return launch_general(a, st);
+  const bool fp8 = a.cache.dtype == FCT_E4M3;
+  if (a.cache.head_dim == 128)
+    return fp8 ? launch_tensor<128, true>(a, sms, device, st) : launch_tensor<128, false>(a, sms, device, st);
+  return fp8 ? launch_tensor<64, true>(a, sms, device, st) : launch_tensor<64, false>(a, sms, device, st);
 }
 
 }  // namespace fct
