@@ -125,11 +125,14 @@ __device__ __forceinline__ void cluster_barrier() {
                "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Reduction slots: per warp of this CTA, and per CTA of the cluster; two of
-// each, used in turn, so that one barrier per reduction is enough.
+// Reduction slots: per warp of this CTA, and per CTA of the cluster, filled
+// by the CTAs with stores that complete on `bar`.  Two of each, used in turn:
+// a CTA sends for the next reduction but one only after it has received for
+// the next one from every CTA, and those sent after they had read this one's.
 struct Slots {
   uint4 warp[2][kVWarps];
   uint4 cta[2][kMaxCtas];
+  uint64_t bar[2];
 };
 
 // The staged rows of a CTA: which pieces have landed.
@@ -149,7 +152,7 @@ struct Rows {
   int V, begin, end;
   int rank, ctas;
   Slots* slots;
-  int parity = 0;
+  uint32_t reductions = 0;
   // staged: pieces of the share and vectors per piece, and the current node's
   // rows from vector `begin` on with the barriers their pieces land on
   int pieces = 1, piece = 0;
@@ -166,29 +169,35 @@ struct Rows {
   __device__ __forceinline__ S all(S x, S none, F fold) {
     static_assert(sizeof(S) <= 16, "one slot");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    parity ^= 1;
+    const int turn = reductions & 1;
+    uint64_t* bar = &slots->bar[turn];
     x = fold(x, 32);
-    if (lane == 0) memcpy(&slots->warp[parity][warp], &x, sizeof(S));
+    if (lane == 0) memcpy(&slots->warp[turn][warp], &x, sizeof(S));
     __syncthreads();
     if (warp == 0) {
+      if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(ctas) * 16);
       x = none;
-      if (lane < kVWarps) memcpy(&x, &slots->warp[parity][lane], sizeof(S));
+      if (lane < kVWarps) memcpy(&x, &slots->warp[turn][lane], sizeof(S));
       x = broadcast(fold(x, kVWarps));  // lanes from kVWarps on have folded `none` only
       if (lane < ctas) {
-        uint32_t w[4] = {0, 0, 0, 0}, dst;
+        uint32_t w[4] = {0, 0, 0, 0};
         memcpy(w, &x, sizeof(S));
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                     : "=r"(dst)
-                     : "r"(smem_addr(&slots->cta[parity][rank])), "r"(lane));
-        asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]),
-                     "r"(w[1]), "r"(w[2]), "r"(w[3])
-                     : "memory");
+        asm volatile(
+            "{\n\t.reg .b32 dst, bar;\n\t"
+            "mapa.shared::cluster.u32 dst, %0, %2;\n\t"
+            "mapa.shared::cluster.u32 bar, %1, %2;\n\t"
+            "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [dst], {%3, %4, %5, %6}, "
+            "[bar];\n\t}" ::"r"(smem_addr(&slots->cta[turn][rank])),
+            "r"(smem_addr(bar)), "r"(lane), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+            : "memory");
       }
       __syncwarp();
     }
-    cluster_barrier();
+    if (lane == 0) mbar_wait(bar, (reductions >> 1) & 1u, abort, false);
+    __syncwarp();
+    ++reductions;
     x = none;
-    if (lane < ctas) memcpy(&x, &slots->cta[parity][lane], sizeof(S));
+    if (lane < ctas) memcpy(&x, &slots->cta[turn][lane], sizeof(S));
     return broadcast(fold(x, ctas));
   }
   template <typename S>
@@ -355,11 +364,12 @@ __global__ void __launch_bounds__(kVThreads, 1)
   const int nodes = static_cast<int>(n64);  // node indexes below are the request's
   if (threadIdx.x == 0) {
     stage.abort = 0;
-    if (kStaged) {
+    mbar_init(&slots.bar[0], 1);
+    mbar_init(&slots.bar[1], 1);
+    if (kStaged)
       for (int i = 0; i < bufs; ++i)
         for (int c = 0; c < kChunks; ++c) mbar_init(&stage.bar[i][c], 1);
-      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   for (int i = threadIdx.x; i < nodes && i < kNodeCap; i += kVThreads) {
     held.tokens[i] = a.tokens[first + i];
@@ -373,8 +383,8 @@ __global__ void __launch_bounds__(kVThreads, 1)
   int64_t* toks = a.out_tokens + b * (a.max_depth + 1);
   int32_t* path = a.path + b * a.max_depth;
   // `held` is filled, and every CTA of the cluster runs: its shared memory may
-  // be written from now on.  (The last reduction's barrier comes after all
-  // such writes, so a CTA may also leave when it is done.)
+  // be written from now on.
+  __syncwarp();
   cluster_barrier();
   auto token = [&](int i) { return i < kNodeCap ? held.tokens[i] : a.tokens[first + i]; };
   auto parent = [&](int i) { return i < kNodeCap ? held.parent[i] : a.parent[first + i]; };
@@ -649,11 +659,12 @@ __global__ void __launch_bounds__(kVThreads, 1)
       last = -1;
     }
   }
-  if constexpr (kStaged) {
-    // copies ahead of the walk's end have landed before the CTA leaves
-    drop();
-    if (threadIdx.x == 0 && stage.abort) status |= FCT_DEV_WAIT_TIMEOUT;
-  }
+  __syncwarp();
+  // no CTA leaves while another may still write to it (each has everything
+  // that was sent to it, unless a wait ran out)
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if constexpr (kStaged) drop();  // copies ahead of the walk's end have landed
+  if (threadIdx.x == 0 && stage.abort) status |= FCT_DEV_WAIT_TIMEOUT;
   if (writer) {
     toks[depth] = last;
     a.count[b] = static_cast<int32_t>(depth);
@@ -664,6 +675,8 @@ __global__ void __launch_bounds__(kVThreads, 1)
       toks[i + 1] = -1;
       path[i] = -1;
     }
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 template <typename T, int VE, bool kStaged>
