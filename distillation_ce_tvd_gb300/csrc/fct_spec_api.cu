@@ -143,6 +143,9 @@ int fct_tree_attention(const void* q, int64_t ld_q_node, int64_t ld_q_head, int6
   if (n_nodes == 0 || batch == 0) return FCT_OK;
   if (batch > kMaxBatch || n_nodes > INT32_MAX) return FCT_ERR_UNSUPPORTED;
   if ((rc = check_pages(block_table, ld_table, max_pages, context_len, batch)) != FCT_OK) return rc;
+  // positions are 32-bit in the kernels, with room for a tile past the last
+  if (max_pages > ((int64_t(1) << 31) - 1024) / cache->page_size) return FCT_ERR_UNSUPPORTED;
+  if (n_nodes * (n_q_heads / cache->n_heads) > INT32_MAX) return FCT_ERR_UNSUPPORTED;
   if (q == nullptr || out == nullptr || node_start == nullptr) return FCT_ERR_INVALID_ARG;
   if (mask_words < 0 || (tree_mask == nullptr) != (mask_words == 0)) return FCT_ERR_INVALID_ARG;
   if (mask_words > (int64_t(1) << 24)) return FCT_ERR_UNSUPPORTED;

@@ -197,8 +197,9 @@ cudaError_t launch_general(const AttnArgs& a, cudaStream_t st) {
 
 constexpr int kTile = 128;      // keys per tile, rows per query tile
 constexpr int kAThreads = 512;
-constexpr int kSoftThreads = 256;
+constexpr int kSoftWarps = 8;
 constexpr int kPrepThreads = 128;
+constexpr int kPrepWarps = kPrepThreads / 32;
 constexpr int kUnitRows = 2 * kTile;
 constexpr int kBadRing = 16;
 constexpr uint32_t kAtTmemCols = 512;
@@ -242,29 +243,27 @@ struct AttnShape {
 
 // What one CTA does with one unit: key tiles [tile0, tile0 + tiles) of it.
 struct Segment {
-  int64_t b;
-  int h;            // kv head
-  int node0;        // first row of q of the request
-  int nodes;        // its nodes
-  int64_t ctx, len; // tokens before the nodes, and with them
-  int row0, rows;   // this unit's rows of the request's nodes * group
-  int64_t tile0;
-  int tiles;
+  int b;
+  int h;           // kv head
+  int node0;       // first row of q of the request
+  int ctx, len;    // tokens before the nodes, and with them
+  int row0, rows;  // this unit's rows of the request's nodes * group
+  int tile0, tiles;
   bool whole;       // the unit's only segment
   int part;         // else: workspace slot of this CTA (0 its first, 1 its last)
 };
 
 struct AttnDims {
   int group;
-  int64_t room;  // positions a block table row holds
+  int room;  // positions a block table row holds
 };
 
 struct RequestShape {
   int node0, nodes;
-  int64_t ctx, len, tiles;
+  int ctx, len, tiles;
   int row_units;
   bool bad;
-  __device__ __forceinline__ int64_t work(int heads) const { return tiles * row_units * heads; }
+  __device__ __forceinline__ int64_t work(int heads) const { return int64_t(tiles) * row_units * heads; }
 };
 
 __device__ __forceinline__ RequestShape request_shape(const AttnArgs& a, const AttnDims& d, int64_t b) {
@@ -279,11 +278,9 @@ __device__ __forceinline__ RequestShape request_shape(const AttnArgs& a, const A
     r.bad = true;
     r.ctx = 0;
   }
-  r.len = r.ctx + r.nodes;
-  if (r.len > d.room) {
-    r.bad = r.bad || r.nodes > 0;
-    r.len = d.room;
-  }
+  const int64_t len = int64_t(r.ctx) + r.nodes;
+  r.bad = r.bad || (len > d.room && r.nodes > 0);
+  r.len = len > d.room ? d.room : static_cast<int>(len);
   r.tiles = (r.len + kTile - 1) / kTile;
   r.row_units = static_cast<int>((int64_t(r.nodes) * d.group + kUnitRows - 1) / kUnitRows);
   return r;
@@ -317,18 +314,16 @@ struct SegmentWalk {
       w = r.work(a.cache.n_heads);
     }
     const int64_t unit = off / r.tiles;
-    s.b = b;
+    s.b = static_cast<int>(b);
     s.node0 = r.node0;
-    s.nodes = r.nodes;
     s.ctx = r.ctx;
     s.len = r.len;
     s.h = static_cast<int>(unit / r.row_units);
     s.row0 = static_cast<int>(unit % r.row_units) * kUnitRows;
-    const int all_rows = r.nodes * d.group;
-    s.rows = all_rows - s.row0 < kUnitRows ? all_rows - s.row0 : kUnitRows;
-    s.tile0 = off % r.tiles;
-    const int64_t n = r.tiles - s.tile0 < left ? r.tiles - s.tile0 : left;
-    s.tiles = static_cast<int>(n);
+    s.rows = min(r.nodes * d.group - s.row0, kUnitRows);
+    s.tile0 = static_cast<int>(off - unit * r.tiles);
+    const int n = r.tiles - s.tile0 < left ? r.tiles - s.tile0 : static_cast<int>(left);
+    s.tiles = n;
     s.whole = n == r.tiles;
     s.part = s.tile0 > 0 ? 0 : 1;
     off += n;
@@ -428,6 +423,19 @@ __device__ __forceinline__ void tm_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// A warp waits for a phase (one lane asks: 32 would be served one by one) and
+// agrees on the outcome.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  int got = 0;
+  if ((threadIdx.x & 31) == 0) got = mbar_wait(bar, parity, abort);
+  return __shfl_sync(0xffffffffu, got, 0) != 0;
+}
+// A warp's arrival, after what all its lanes have done.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 // A box of a 4-D tensor map (head_dim, slot, head, page).
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int slot, int head,
                                         int page, uint64_t* bar) {
@@ -440,40 +448,39 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
 }
 
 // 32 bits of a node's mask from bit s on (s >= 0).
-__device__ __forceinline__ uint32_t mask_bits(const int64_t* words, int64_t n_words, int64_t s) {
-  const int64_t i = s >> 6;
-  const int sh = static_cast<int>(s & 63);
+__device__ __forceinline__ uint32_t mask_bits(const int64_t* words, int64_t n_words, int s) {
+  const int i = s >> 6, sh = s & 63;
   const uint64_t lo = i < n_words ? static_cast<uint64_t>(words[i]) : 0;
   const uint64_t hi = sh && i + 1 < n_words ? static_cast<uint64_t>(words[i + 1]) << (64 - sh) : 0;
   return static_cast<uint32_t>((lo >> sh) | hi);
 }
 
 // Which of the 32 keys from position p0 on node i of the segment sees.
-__device__ __forceinline__ uint32_t visible32(const AttnArgs& a, const Segment& s, int node, int64_t p0) {
-  const int64_t first = p0 - s.ctx;  // node index of the first key, or < 0
+__device__ __forceinline__ uint32_t visible32(const AttnArgs& a, const Segment& s, int node, int p0) {
+  const int first = p0 - s.ctx;  // node index of the first key, or < 0
   uint32_t m;
   if (first + 32 <= 0) {
     m = 0xffffffffu;
   } else {
-    const int64_t from = first < 0 ? 0 : first;
+    const int from = max(first, 0);
     if (a.mask == nullptr) {
-      const int64_t n = node - from + 1;
+      const int n = node - from + 1;
       m = n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
     } else {
       m = mask_bits(a.mask + int64_t(s.node0 + node) * a.mask_words, a.mask_words, from);
     }
     if (first < 0) m = (m << -first) | ((1u << -first) - 1u);
   }
-  const int64_t held = s.len - p0;
+  const int held = s.len - p0;
   if (held < 32) m &= held <= 0 ? 0u : (1u << held) - 1u;
   return m;
 }
 
 // The pool's page and slot of a position; the page may be outside the pool
 // (the table is the caller's).
-__device__ __forceinline__ int page_of(const AttnArgs& a, const Segment& s, int64_t pos, int* slot) {
-  const int64_t p = pos / a.cache.page_size;
-  *slot = static_cast<int>(pos - p * a.cache.page_size);
+__device__ __forceinline__ int page_of(const AttnArgs& a, const Segment& s, int pos, int* slot) {
+  const int p = pos / a.cache.page_size;
+  *slot = pos - p * a.cache.page_size;
   return a.pages.table[s.b * a.pages.ld + p];
 }
 
@@ -521,23 +528,23 @@ __global__ void __launch_bounds__(kAThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < Sh::kSlots; ++i) {
-      mbar_init(&ctl.full_bar[i], kFp8 ? kPrepThreads : 1);
+      mbar_init(&ctl.full_bar[i], kFp8 ? kPrepWarps : 1);
       mbar_init(&ctl.empty_bar[i], 1);
       mbar_init(&ctl.tail_full[i], 1);
-      mbar_init(&ctl.prep_bar[i], kPrepThreads);
+      mbar_init(&ctl.prep_bar[i], kPrepWarps);
     }
     for (int i = 0; i < Sh::kRaw; ++i) {
       mbar_init(&ctl.raw_full[i], 1);
-      mbar_init(&ctl.raw_scaled[i], 32);
-      mbar_init(&ctl.raw_empty[i], kPrepThreads);
+      mbar_init(&ctl.raw_scaled[i], 1);
+      mbar_init(&ctl.raw_empty[i], kPrepWarps);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&ctl.s_full[w], 1);
-      mbar_init(&ctl.p_full[w], kTile);
+      mbar_init(&ctl.p_full[w], kSoftWarps / 2);
     }
-    mbar_init(&ctl.q_full, kSoftThreads);
+    mbar_init(&ctl.q_full, kSoftWarps);
     mbar_init(&ctl.o_full, 1);
-    mbar_init(&ctl.ml_full, kSoftThreads);
+    mbar_init(&ctl.ml_full, kSoftWarps);
     mbar_init(&ctl.done_bar, 1);
     ctl.abort_flag = 0;
     for (int i = 0; i < kBadRing; ++i) ctl.bad_seg[i] = 0;
@@ -601,7 +608,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
   if (bad_request && blockIdx.x == 0) status |= FCT_DEV_INDEX_OUT_OF_RANGE;
   auto lead_of = [](const Segment& s) { return s.rows > kTile ? 1 : 2; };
   // whether a key tile (index in the unit) reaches past the context
-  auto is_tail = [](const Segment& s, int64_t tile) { return (tile + 1) * kTile > s.ctx; };
+  auto is_tail = [](const Segment& s, int tile) { return (tile + 1) * kTile > s.ctx; };
 
   if (warp == 0) {
     // ---- loads: the warp's lanes take a tile's boxes
@@ -621,7 +628,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
     while (ok && walk.next(seg)) {
       for_items(seg.tiles, lead_of(seg), [&](bool is_v, int j) {
         const uint32_t slot = item % kRing, phase = (item / kRing) & 1u;
-        if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], phase ^ 1u, &ctl.abort_flag))) {
+        if (!warp_wait(&empty[slot], phase ^ 1u, &ctl.abort_flag)) {
           ok = false;
           return false;
         }
@@ -629,9 +636,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
         uint64_t* bar = prep ? &ctl.tail_full[slot] : &full[slot];
         last_tail = (last_tail & ~(1u << slot)) | (uint32_t(prep) << slot);
         (prep ? tail_phase : full_phase) ^= 1u << slot;
-        const int64_t p0 = (seg.tile0 + j) * kTile;
-        const int64_t held = seg.len - p0;
-        const int rows = held < kTile ? static_cast<int>(held) : kTile;
+        const int p0 = (seg.tile0 + j) * kTile;
+        const int rows = min(seg.len - p0, kTile);
         if (lane == 0)
           mbar_arrive_expect_tx(bar,
                                 uint32_t((rows + box_rows - 1) / box_rows) * kBoxCols * box_bytes);
@@ -687,7 +693,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
         for (int part = 0; part < (seg.len <= kFineKeys ? 2 : 1); ++part) {
 #pragma unroll
           for (int k = 0; k < kTile / 16; ++k)
-            umma_ts<kIdO>(tm_o[w], tm_s[w] + part * (kTile / 2) + k * 8,
+            umma_ts<kIdO>(tm_o[w], tm_s[w] + (k / 2) * 32 + part * 16 + (k % 2) * 8,
                           vd + uint64_t(k * 16 * 128 >> 4), !first || part + k > 0);
         }
       };
@@ -697,7 +703,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
         tc_after();
         return got;
       };
-      auto wait_v = [&](uint32_t it, int64_t tile) {
+      auto wait_v = [&](uint32_t it, int tile) {
         if (kFp8 || !is_tail(seg, tile)) return wait_item(it);
         const uint32_t slot = it % Sh::kSlots;
         const bool got = mbar_wait(&ctl.prep_bar[slot], (prep_phase >> slot) & 1u, &ctl.abort_flag);
@@ -776,14 +782,14 @@ __global__ void __launch_bounds__(kAThreads, 1)
       while (ok && walk.next(seg)) {
         for_items(seg.tiles, lead_of(seg), [&](bool is_v, int j) {
           const uint32_t r = item % Sh::kRaw, phase = (item / Sh::kRaw) & 1u;
-          if (!__all_sync(0xffffffffu, mbar_wait(&ctl.raw_empty[r], phase ^ 1u, &ctl.abort_flag))) {
+          if (!warp_wait(&ctl.raw_empty[r], phase ^ 1u, &ctl.abort_flag)) {
             ok = false;
             return false;
           }
-          const int64_t p0 = (seg.tile0 + j) * kTile;
+          const int p0 = (seg.tile0 + j) * kTile;
 #pragma unroll
           for (int i = 0; i < kTile / 32; ++i) {
-            const int64_t pos = p0 + i * 32 + lane;
+            const int pos = p0 + i * 32 + lane;
             uint8_t byte = 0;
             if (pos < seg.len) {
               int at;
@@ -795,7 +801,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
             }
             ctl.raw_scale[r][i * 32 + lane] = byte;
           }
-          mbar_arrive(&ctl.raw_scaled[r]);
+          warp_arrive(&ctl.raw_scaled[r]);
           ++item;
           return true;
         });
@@ -812,13 +818,13 @@ __global__ void __launch_bounds__(kAThreads, 1)
       for_items(seg.tiles, lead_of(seg), [&](bool is_v, int j) {
         const uint32_t it = item++;
         const uint32_t slot = it % Sh::kSlots;
-        const int64_t tile = seg.tile0 + j, p0 = tile * kTile;
+        const int tile = seg.tile0 + j, p0 = tile * kTile;
         const uint32_t dst = slot0 + slot * Sh::kTileBytes;
         if constexpr (kFp8) {
           const uint32_t r = it % Sh::kRaw;
-          if (!mbar_wait(&ctl.raw_full[r], (it / Sh::kRaw) & 1u, &ctl.abort_flag) ||
-              !mbar_wait(&ctl.raw_scaled[r], (it / Sh::kRaw) & 1u, &ctl.abort_flag) ||
-              !mbar_wait(&ctl.empty_bar[slot], ((it / Sh::kSlots) & 1u) ^ 1u, &ctl.abort_flag)) {
+          if (!warp_wait(&ctl.raw_full[r], (it / Sh::kRaw) & 1u, &ctl.abort_flag) ||
+              !warp_wait(&ctl.raw_scaled[r], (it / Sh::kRaw) & 1u, &ctl.abort_flag) ||
+              !warp_wait(&ctl.empty_bar[slot], ((it / Sh::kSlots) & 1u) ^ 1u, &ctl.abort_flag)) {
             ok = false;
             return false;
           }
@@ -834,7 +840,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
                          : "r"(src + uint32_t(row) * kD + uint32_t(c) * 16));
-            const int64_t pos = p0 + row;
+            const int pos = p0 + row;
             if (is_v && pos >= seg.ctx && (pos >= seg.len || byte == 255)) {
               found |= pos < seg.len;
               w = make_uint4(0, 0, 0, 0);
@@ -865,17 +871,17 @@ __global__ void __launch_bounds__(kAThreads, 1)
                            : "memory");
           }
           if (found) ctl.bad_seg[seg_n % kBadRing] = seg_n;
-          mbar_arrive(&ctl.raw_empty[r]);
           async_fence();
-          mbar_arrive(&ctl.full_bar[slot]);
+          warp_arrive(&ctl.raw_empty[r]);
+          warp_arrive(&ctl.full_bar[slot]);
         } else {
           if (!is_v || !is_tail(seg, tile)) return true;
-          if (!mbar_wait(&ctl.tail_full[slot], (tail_phase >> slot) & 1u, &ctl.abort_flag)) {
+          if (!warp_wait(&ctl.tail_full[slot], (tail_phase >> slot) & 1u, &ctl.abort_flag)) {
             ok = false;
             return false;
           }
           tail_phase ^= 1u << slot;
-          const int64_t pos = p0 + t;
+          const int pos = p0 + t;
           if (pos >= seg.ctx) {
             const bool past = pos >= seg.len;
             bool found = false;
@@ -904,7 +910,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
             if (found) ctl.bad_seg[seg_n % kBadRing] = seg_n;
           }
           async_fence();
-          mbar_arrive(&ctl.prep_bar[slot]);
+          warp_arrive(&ctl.prep_bar[slot]);
         }
         return true;
       });
@@ -956,19 +962,19 @@ __global__ void __launch_bounds__(kAThreads, 1)
       }
       async_fence();
       tc_before();
-      mbar_arrive(&ctl.q_full);
+      warp_arrive(&ctl.q_full);
 
       float m = -INFINITY, l = 0.f;   // the weights' exponent offset and their sum
       bool first = true;
       for (int j = two ? 0 : w; j < seg.tiles; j += two ? 1 : 2) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&ctl.s_full[w], s_n & 1u, &ctl.abort_flag))) {
+        if (!warp_wait(&ctl.s_full[w], s_n & 1u, &ctl.abort_flag)) {
           ok = false;
           break;
         }
         ++s_n;
         tc_after();
         if (warp_live) {
-          const int64_t p0 = (seg.tile0 + j) * kTile;
+          const int p0 = (seg.tile0 + j) * kTile;
           const bool tail = is_tail(seg, seg.tile0 + j);
           uint32_t vis[4];
           if (tail) {
@@ -1010,10 +1016,9 @@ __global__ void __launch_bounds__(kAThreads, 1)
           const float off = m == -INFINITY ? 0.f : -m;
           const float2 s2 = make_float2(sl2, sl2), o2 = make_float2(off, off);
           float2 sum = make_float2(0.f, 0.f);
-          // P over S's first half, and its remainders over the second: what a
-          // chunk's remainders overwrite has been read two chunks later
+          // 32 columns of S at a time, their place taken by P's 16 and, where
+          // wanted, the remainders' 16
           const bool fine = seg.len <= kFineKeys;
-          uint32_t low[32];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t x[32], p[16];
@@ -1033,15 +1038,13 @@ __global__ void __launch_bounds__(kAThreads, 1)
               x[k] = __float_as_uint(e.x);
               x[k + 1] = __float_as_uint(e.y);
             }
-            tm_st16(tm_s + 16 * i, p);
+            tm_st16(tm_s + 32 * i, p);
             if (fine) {
-              if (i == 2) tm_st(tm_s + kTile / 2, low);
 #pragma unroll
               for (int k = 0; k < 32; k += 2)
-                low[16 * (i & 1) + k / 2] =
-                    pack_bf16x2(__uint_as_float(x[k]) - __uint_as_float(p[k / 2] << 16),
-                                __uint_as_float(x[k + 1]) - __uint_as_float(p[k / 2] & 0xffff0000u));
-              if (i == 3) tm_st(tm_s + kTile / 2 + 32, low);
+                p[k / 2] = pack_bf16x2(__uint_as_float(x[k]) - __uint_as_float(p[k / 2] << 16),
+                                       __uint_as_float(x[k + 1]) - __uint_as_float(p[k / 2] & 0xffff0000u));
+              tm_st16(tm_s + 32 * i + 16, p);
             }
           }
           l += sum.x + sum.y;
@@ -1049,9 +1052,9 @@ __global__ void __launch_bounds__(kAThreads, 1)
         }
         first = false;
         tc_before();
-        mbar_arrive(&ctl.p_full[w]);
+        warp_arrive(&ctl.p_full[w]);
       }
-      if (!ok || !__all_sync(0xffffffffu, mbar_wait(&ctl.o_full, (seg_n - 1) & 1u, &ctl.abort_flag))) break;
+      if (!ok || !warp_wait(&ctl.o_full, (seg_n - 1) & 1u, &ctl.abort_flag)) break;
       tc_after();
       const bool fix = *reinterpret_cast<volatile int*>(&ctl.bad_seg[seg_n % kBadRing]) == seg_n;
 
@@ -1062,8 +1065,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
         // (the next segment's write follows every thread's read of this one's:
         // it waits for products that wait for all threads' query rows)
         ctl.ml[w][r] = make_float2(m, l);
-        mbar_arrive(&ctl.ml_full);
-        if (!__all_sync(0xffffffffu, mbar_wait(&ctl.ml_full, ml_n & 1u, &ctl.abort_flag))) break;
+        warp_arrive(&ctl.ml_full);
+        if (!warp_wait(&ctl.ml_full, ml_n & 1u, &ctl.abort_flag)) break;
         ++ml_n;
         const float2 A = ctl.ml[0][r], B = seg.tiles > 1 ? ctl.ml[1][r] : make_float2(-INFINITY, 0.f);
         M = fmaxf(A.x, B.x);
@@ -1107,8 +1110,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
           }
           if (live && fix) {
             // non-finite values of drafted nodes that this row sees
-            const int64_t end = (seg.tile0 + seg.tiles) * kTile < seg.len ? (seg.tile0 + seg.tiles) * kTile : seg.len;
-            for (int64_t pos = seg.ctx > seg.tile0 * kTile ? seg.ctx : seg.tile0 * kTile; pos < end; ++pos) {
+            const int end = min((seg.tile0 + seg.tiles) * kTile, seg.len);
+            for (int pos = max(seg.ctx, seg.tile0 * kTile); pos < end; ++pos) {
               if (!(visible32(a, seg, node, pos) & 1u)) continue;
               int at;
               const int64_t page = page_of(a, seg, pos, &at);
@@ -1316,7 +1319,7 @@ cudaError_t launch_tensor(const AttnArgs& a, int sms, int device, cudaStream_t s
   CUtensorMap mk, mv;
   if (!cache_map(&mk, a.cache, a.cache.k, box_rows) || !cache_map(&mv, a.cache, a.cache.v, box_rows))
     return cudaErrorInvalidValue;
-  const AttnDims d{a.n_q_heads / a.cache.n_heads, a.pages.max_pages * a.cache.page_size};
+  const AttnDims d{a.n_q_heads / a.cache.n_heads, static_cast<int>(a.pages.max_pages * a.cache.page_size)};
   const int part_rows = part_rows_of(a.n_nodes, d.group);
   kernel<<<static_cast<unsigned>(sms), kAThreads, Sh::kSmem, st>>>(mk, mv, a, d, box_rows, part_rows);
   cudaError_t e = cudaGetLastError();

@@ -741,6 +741,8 @@ int fct_kv_cache_move(const fct_kv_cache* cache, const int32_t* block_table,
  *                 that the node sees node j of its request (itself included;
  *                 nodes past 64 * mask_words are not seen).  NULL with
  *                 mask_words = 0: a chain, node i sees nodes 0 .. i.
+ *   block_table : max_pages * page_size at most 2^31 - 1024, else
+ *                 FCT_ERR_UNSUPPORTED.
  *   lse         : (n_nodes, n_q_heads) fp32, or NULL.
  *   workspace   : device memory, 16-byte aligned, of at least
  *                 fct_tree_attention_workspace_size bytes, clobbered: partial
