@@ -347,39 +347,51 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
                    smem_addr(bar))
                : "memory");
 }
-// D = A B^T (+ D): A and B from shared memory, or A from tensor memory.
+// Upper half of a tile's shared-memory descriptor: 8-row atoms of 1024 bytes
+// (128-byte swizzle), version 1.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+// D = A B^T (+ D): A and B from shared memory, or A from tensor memory.  The
+// descriptors come as their lower halves.
 template <uint32_t kIdesc>
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(kIdesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(kIdesc), "r"(acc), "n"(kDescHi)
       : "memory");
 }
 template <uint32_t kIdesc>
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t acc) {
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a_tmem), "l"(b), "r"(kIdesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b), "r"(kIdesc), "r"(acc), "n"(kDescHi)
       : "memory");
 }
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+               : "=r"(is));
+  return is != 0;
+}
+// x, known to be the same in all lanes.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // Instruction descriptor: fp32 accumulator, bf16 operands, M = 128, N; bit 16
 // marks an MN-major B.
 __host__ __device__ constexpr uint32_t attn_idesc(int n, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(b_mn) << 16) | (uint32_t(n >> 3) << 17) |
          (uint32_t(kTile >> 4) << 24);
 }
-// Shared-memory descriptor of a tile in 128-byte swizzle: 8-row atoms 1024
-// bytes apart; MN-major (V: rows are keys): the next 64 columns start one
-// kTile x 128-byte block later.
-__device__ __forceinline__ uint64_t attn_desc(uint32_t saddr, bool mn) {
-  uint64_t d = uint64_t((saddr & 0x3FFFFu) >> 4);
-  d |= uint64_t(mn ? (kTile * 128) >> 4 : 1u) << 16;
-  d |= uint64_t(1024 >> 4) << 32;
-  d |= uint64_t(1) << 46;
-  d |= uint64_t(2) << 61;
-  return d;
+// Lower half of a tile's descriptor: its address and, for an MN-major tile (V:
+// rows are keys), the distance to the next 64 columns, one kTile x 128-byte
+// block.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, bool mn) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((mn ? uint32_t(kTile * 128) >> 4 : 1u) << 16);
 }
 
 #define FCT_R32(r)                                                                              \
@@ -664,116 +676,117 @@ __global__ void __launch_bounds__(kAThreads, 1)
                 (((tail ? tail_phase : full_phase) >> slot) & 1u) ^ 1u, &ctl.abort_flag, false);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---- products
-      constexpr uint32_t kIdS = attn_idesc(kTile, false), kIdO = attn_idesc(kD, true);
-      const uint32_t tm_s[2] = {tmem, tmem + kTile};
-      const uint32_t tm_o[2] = {tmem + 2 * kTile, tmem + 2 * kTile + kD};
-      uint32_t item = 0, seg_n = 0, full_phase = 0, prep_phase = 0;
-      uint32_t p_n[2] = {0, 0};
-      bool ok = true;
-      auto wait_item = [&](uint32_t it) {
-        const uint32_t slot = it % Sh::kSlots;
-        const bool got = mbar_wait(&ctl.full_bar[slot], (full_phase >> slot) & 1u, &ctl.abort_flag);
-        full_phase ^= 1u << slot;
-        return got;
-      };
-      auto scores = [&](int w, int q_tile, uint32_t it) {
-        const uint64_t qd = attn_desc(smem0 + uint32_t(q_tile) * Sh::kTileBytes, false);
-        const uint64_t kd = attn_desc(slot0 + (it % Sh::kSlots) * Sh::kTileBytes, false);
+    // ---- products: the warp goes through the tiles converged, one lane
+    // issues (what the issue needs is then the same in all lanes, which keeps
+    // it in uniform registers)
+    constexpr uint32_t kIdS = attn_idesc(kTile, false), kIdO = attn_idesc(kD, true);
+    uint32_t item = 0, seg_n = 0, full_phase = 0, prep_phase = 0;
+    uint32_t p_n[2] = {0, 0};
+    bool ok = true;
+    const bool issue = elect_one();
+    auto slot_addr = [&](uint32_t it) { return uniform(slot0 + (it % Sh::kSlots) * Sh::kTileBytes); };
+    auto wait_item = [&](uint32_t it) {
+      const uint32_t slot = it % Sh::kSlots;
+      const bool got = warp_wait(&ctl.full_bar[slot], (full_phase >> slot) & 1u, &ctl.abort_flag);
+      full_phase ^= 1u << slot;
+      return got;
+    };
+    auto scores = [&](int w, int q_tile, uint32_t it, bool last) {
+      const uint32_t tm_s = uniform(tmem + uint32_t(w) * kTile);
+      const uint32_t qd = uniform(desc_lo(smem0 + uint32_t(q_tile) * Sh::kTileBytes, false));
+      const uint32_t kd = desc_lo(slot_addr(it), false);
+      tc_after();
+      if (issue) {
 #pragma unroll
         for (int k = 0; k < kD / 16; ++k) {
-          const uint64_t step = uint64_t((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4;
-          umma_ss<kIdS>(tm_s[w], qd + step, kd + step, k > 0);
+          const uint32_t step = uint32_t((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4;
+          umma_ss<kIdS>(tm_s, qd + step, kd + step, k > 0);
         }
         umma_commit(&ctl.s_full[w]);
-      };
-      auto values = [&](int w, uint32_t it, bool first) {
-        const uint64_t vd = attn_desc(slot0 + (it % Sh::kSlots) * Sh::kTileBytes, true);
-        for (int part = 0; part < (seg.len <= kFineKeys ? 2 : 1); ++part) {
+        if (last) umma_commit(&ctl.empty_bar[it % Sh::kSlots]);
+      }
+      __syncwarp();
+    };
+    auto values = [&](int w, uint32_t it, bool first, bool last) {
+      const uint32_t tm_s = uniform(tmem + uint32_t(w) * kTile);
+      const uint32_t tm_o = uniform(tmem + 2 * kTile + uint32_t(w) * kD);
+      const uint32_t vd = desc_lo(slot_addr(it), true);
+      tc_after();
+      if (issue) {
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          umma_ts<kIdO>(tm_o, tm_s + (k / 2) * 32 + (k % 2) * 8, vd + (k * 16 * 128 >> 4), !first || k > 0);
+        if (seg.len <= kFineKeys) {
 #pragma unroll
           for (int k = 0; k < kTile / 16; ++k)
-            umma_ts<kIdO>(tm_o[w], tm_s[w] + (k / 2) * 32 + part * 16 + (k % 2) * 8,
-                          vd + uint64_t(k * 16 * 128 >> 4), !first || part + k > 0);
+            umma_ts<kIdO>(tm_o, tm_s + (k / 2) * 32 + 16 + (k % 2) * 8, vd + (k * 16 * 128 >> 4), 1);
         }
-      };
-      auto wait_p = [&](int w) {
-        const bool got = mbar_wait(&ctl.p_full[w], p_n[w] & 1u, &ctl.abort_flag);
-        ++p_n[w];
-        tc_after();
-        return got;
-      };
-      auto wait_v = [&](uint32_t it, int tile) {
-        if (kFp8 || !is_tail(seg, tile)) return wait_item(it);
-        const uint32_t slot = it % Sh::kSlots;
-        const bool got = mbar_wait(&ctl.prep_bar[slot], (prep_phase >> slot) & 1u, &ctl.abort_flag);
-        prep_phase ^= 1u << slot;
-        return got;
-      };
-      while (ok && walk.next(seg)) {
-        const bool two = seg.rows > kTile;
-        if (!mbar_wait(&ctl.q_full, seg_n & 1u, &ctl.abort_flag)) break;
-        ++seg_n;
-        tc_after();
-        if (two) {
-          uint32_t k_item = item++;
-          ok = wait_item(k_item);
+        if (last) umma_commit(&ctl.empty_bar[it % Sh::kSlots]);
+      }
+      __syncwarp();
+    };
+    auto wait_p = [&](int w) {
+      const bool got = warp_wait(&ctl.p_full[w], p_n[w] & 1u, &ctl.abort_flag);
+      ++p_n[w];
+      return got;
+    };
+    auto wait_v = [&](uint32_t it, int tile) {
+      if (kFp8 || !is_tail(seg, tile)) return wait_item(it);
+      const uint32_t slot = it % Sh::kSlots;
+      const bool got = warp_wait(&ctl.prep_bar[slot], (prep_phase >> slot) & 1u, &ctl.abort_flag);
+      prep_phase ^= 1u << slot;
+      return got;
+    };
+    while (ok && walk.next(seg)) {
+      const bool two = seg.rows > kTile;
+      if (!warp_wait(&ctl.q_full, seg_n & 1u, &ctl.abort_flag)) break;
+      ++seg_n;
+      if (two) {
+        uint32_t k_item = item++;
+        ok = wait_item(k_item);
+        if (!ok) break;
+        scores(0, 0, k_item, false);
+        scores(1, 1, k_item, true);
+        for (int j = 0; ok && j < seg.tiles; ++j) {
+          const uint32_t v_item = item++;
+          const bool more = j + 1 < seg.tiles;
+          if (more) k_item = item++;
+          ok = wait_v(v_item, seg.tile0 + j) && wait_p(0);
           if (!ok) break;
-          tc_after();
-          scores(0, 0, k_item);
-          scores(1, 1, k_item);
-          umma_commit(&ctl.empty_bar[k_item % Sh::kSlots]);
-          for (int j = 0; ok && j < seg.tiles; ++j) {
-            const uint32_t v_item = item++;
-            const bool more = j + 1 < seg.tiles;
-            if (more) k_item = item++;
-            ok = wait_v(v_item, seg.tile0 + j) && wait_p(0);
-            if (!ok) break;
-            values(0, v_item, j == 0);
-            if (more) {
-              ok = wait_item(k_item);
-              if (!ok) break;
-              tc_after();
-              scores(0, 0, k_item);
-            }
-            ok = wait_p(1);
-            if (!ok) break;
-            values(1, v_item, j == 0);
-            umma_commit(&ctl.empty_bar[v_item % Sh::kSlots]);
-            if (more) {
-              scores(1, 1, k_item);
-              umma_commit(&ctl.empty_bar[k_item % Sh::kSlots]);
-            }
-          }
-        } else {
-          for (int j = 0; ok && j < 2 && j < seg.tiles; ++j) {
-            const uint32_t k_item = item++;
+          values(0, v_item, j == 0, false);
+          if (more) {
             ok = wait_item(k_item);
             if (!ok) break;
-            tc_after();
-            scores(j, 0, k_item);
-            umma_commit(&ctl.empty_bar[k_item % Sh::kSlots]);
+            scores(0, 0, k_item, false);
           }
-          for (int j = 0; ok && j < seg.tiles; ++j) {
-            const uint32_t v_item = item++;
-            ok = wait_v(v_item, seg.tile0 + j) && wait_p(j & 1);
-            if (!ok) break;
-            values(j & 1, v_item, j < 2);
-            umma_commit(&ctl.empty_bar[v_item % Sh::kSlots]);
-            if (j + 2 < seg.tiles) {
-              const uint32_t k_item = item++;
-              ok = wait_item(k_item);
-              if (!ok) break;
-              tc_after();
-              scores(j & 1, 0, k_item);
-              umma_commit(&ctl.empty_bar[k_item % Sh::kSlots]);
-            }
+          ok = wait_p(1);
+          if (!ok) break;
+          values(1, v_item, j == 0, true);
+          if (more) scores(1, 1, k_item, true);
+        }
+      } else {
+        for (int j = 0; ok && j < 2 && j < seg.tiles; ++j) {
+          const uint32_t k_item = item++;
+          ok = wait_item(k_item);
+          if (ok) scores(j, 0, k_item, true);
+        }
+        for (int j = 0; ok && j < seg.tiles; ++j) {
+          const uint32_t v_item = item++;
+          ok = wait_v(v_item, seg.tile0 + j) && wait_p(j & 1);
+          if (!ok) break;
+          values(j & 1, v_item, j < 2, true);
+          if (j + 2 < seg.tiles) {
+            const uint32_t k_item = item++;
+            ok = wait_item(k_item);
+            if (ok) scores(j & 1, 0, k_item, true);
           }
         }
-        if (ok) umma_commit(&ctl.o_full);
       }
-      umma_commit(&ctl.done_bar);  // every product issued has completed
+      if (ok && issue) umma_commit(&ctl.o_full);
+      __syncwarp();
     }
+    if (issue) umma_commit(&ctl.done_bar);  // every product issued has completed
+    __syncwarp();
   } else if (warp == 2) {
     if constexpr (kFp8) {
       // ---- scale bytes of the raw tiles, four keys per lane
