@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "fct_common.cuh"
 #include "fct_internal.h"
@@ -196,10 +197,7 @@ cudaError_t launch_general(const AttnArgs& a, cudaStream_t st) {
 // are added back to the rows that see them).
 
 constexpr int kTile = 128;      // keys per tile, rows per query tile
-constexpr int kAThreads = 512;
 constexpr int kSoftWarps = 8;
-constexpr int kPrepThreads = 128;
-constexpr int kPrepWarps = kPrepThreads / 32;
 constexpr int kUnitRows = 2 * kTile;
 constexpr int kBadRing = 16;
 constexpr uint32_t kAtTmemCols = 512;
@@ -212,10 +210,21 @@ constexpr float kLazyLog2 = 8.f;  // O is rescaled when the maximum grows by mor
 
 template <int kD, bool kFp8>
 struct AttnShape {
+  // Warps: 0 loads, 1 products, 4-11 softmax; e4m3: 2 and 3 fetch scale bytes,
+  // 12-15 prepare; bf16: 2 and 3 prepare.
+  static constexpr int kThreads = kFp8 ? 512 : 384;
+  static constexpr int kPrepWarp0 = kFp8 ? 12 : 2, kPrepWarps = kFp8 ? 4 : 2;
+  // Registers per thread of warps 0-3, the softmax groups and warps 12-15,
+  // moved between the warp groups: together what the kernel is launched with,
+  // 65536 / kThreads each (in eights).
+  static constexpr int kLaunchRegs = kFp8 ? 128 : 168;
+  static constexpr int kLowRegs = kFp8 ? 104 : 120, kSoftRegs = kFp8 ? 152 : 192;
+  static_assert((kFp8 ? 2 : 1) * kLowRegs + 2 * kSoftRegs <= kThreads / 128 * kLaunchRegs, "registers");
   static constexpr int kHalves = kD / 64;  // 128-byte column blocks of a bf16 row
   static constexpr uint32_t kTileBytes = kTile * kD * 2;
   static constexpr uint32_t kRawBytes = kTile * kD;
   static constexpr int kSlots = kD == 128 ? (kFp8 ? 3 : 5) : (kFp8 ? 4 : 8);
+  static constexpr int kRing = kFp8 ? (kD == 128 ? 4 : 8) : 1;
   static constexpr int kRaw = kFp8 ? (kD == 128 ? 4 : 8) : 0;
   static constexpr size_t kTilesBytes =
       2 * kTileBytes + size_t(kSlots) * kTileBytes + size_t(kRaw) * kRawBytes;
@@ -229,8 +238,8 @@ struct AttnShape {
     uint64_t s_full[2], p_full[2], q_full, o_full, ml_full, done_bar;
     int64_t sched[2];
     union {
-      int64_t scan[kAThreads / 32];  // while the schedule is made
-      float2 ml[2][kTile];           // the groups' maxima and sums, row by row
+      int64_t scan[kThreads / 32];  // while the schedule is made
+      float2 ml[2][kTile];          // the groups' maxima and sums, lane by lane
     };
     uint32_t tmem_base;
     int abort_flag;
@@ -400,6 +409,12 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, bool mn) {
       "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), \
       "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), \
       "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+#define FCT_RW32(r)                                                                             \
+  "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),            \
+      "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),    \
+      "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]),              \
+      "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),              \
+      "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
 #define FCT_U32(r)                                                                              \
   "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),        \
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),          \
@@ -415,6 +430,17 @@ __device__ __forceinline__ void tm_ld(uint32_t taddr, uint32_t (&r)[32]) {
       : FCT_R32(r)
       : "r"(taddr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// The same in two steps: the registers hold their values after tm_ld_done.
+__device__ __forceinline__ void tm_ld_start(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : FCT_R32(r)
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tm_ld_done(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : FCT_RW32(r)::"memory");
 }
 __device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -435,12 +461,22 @@ __device__ __forceinline__ void tm_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// A warp waits for a phase (one lane asks: 32 would be served one by one) and
-// agrees on the outcome.
+// mbar_wait without a function call: a kernel that moves registers between its
+// warps has none.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                           bool heed_abort = true) {
+  if (mbar_try(bar, parity)) return true;
+  const long long t0 = clock64();
+  do {
+    if (heed_abort && *abort) return false;
+    if (mbar_try(bar, parity)) return true;
+  } while (clock64() - t0 <= kWaitLimitCycles);
+  *abort = 1;
+  return false;
+}
+// A warp waits for a phase and agrees on the outcome.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  int got = 0;
-  if ((threadIdx.x & 31) == 0) got = mbar_wait(bar, parity, abort);
-  return __shfl_sync(0xffffffffu, got, 0) != 0;
+  return __all_sync(0xffffffffu, wait_phase(bar, parity, abort));
 }
 // A warp's arrival, after what all its lanes have done.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
@@ -518,8 +554,116 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
   return r;
 }
 
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// One key tile of a softmax warp: the chunks [chunk0, chunk0 + kN) of 32 keys
+// are its share, of the rows of its 32 lanes.  S's columns become P's (16 per
+// chunk, and 16 of the weights' rounding remainders where `fine`); the chunks
+// of other warps, which hold the same rows, become zero.
+template <int kD, int kN>
+__device__ __forceinline__ void soft_tile(uint32_t tm_s, uint32_t tm_o, int chunk0, bool tail,
+                                          const uint32_t (&vis)[kN], bool fine, bool first, float sl2,
+                                          float& m, float& l) {
+  constexpr int kHold = kN < 2 ? kN : 2;  // chunks in registers; with more, S is read twice
+  uint32_t x[kHold][32];
+  float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) tm_ld_start(tm_s + 32 * (chunk0 + i0 + i), x[i]);
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) tm_ld_done(x[i]);
+    if (tail) {
+#pragma unroll
+      for (int i = 0; i < kHold; ++i)
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          if (!((vis[i0 + i] >> k) & 1u)) x[i][k] = 0xff800000u;
+    }
+  };
+#pragma unroll
+  for (int i0 = 0; i0 < kN; i0 += kHold) {
+    load(i0);
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)
+#pragma unroll
+      for (int k = 0; k < 32; k += 2)
+        tops[(k / 2) % 4] = max3(tops[(k / 2) % 4], __uint_as_float(x[i][k]), __uint_as_float(x[i][k + 1]));
+  }
+  const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * sl2;
+  const bool grow = top > m + kLazyLog2 || (m == -INFINITY && top > -INFINITY);
+  if (__any_sync(0xffffffffu, grow)) {
+    const float f = grow ? ex2(m - top) : 1.f;
+    if (grow) m = top;
+    l *= f;
+    if (!first) {
+#pragma unroll 1
+      for (int c = 0; c < kD; c += 32) {
+        uint32_t o[32];
+        tm_ld(tm_o + uint32_t(c), o);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+        tm_st(tm_o + uint32_t(c), o);
+      }
+    }
+  }
+  const float off = m == -INFINITY ? 0.f : -m;
+  const float2 s2 = make_float2(sl2, sl2), o2 = make_float2(off, off);
+  float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i0 = 0; i0 < kN; i0 += kHold) {
+    if (kN > kHold) load(i0);
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+      uint32_t p[16];
+#pragma unroll
+      for (int k = 0; k < 32; k += 2) {
+        float2 e = __ffma2_rn(make_float2(__uint_as_float(x[i][k]), __uint_as_float(x[i][k + 1])), s2, o2);
+        e.x = ex2(e.x);
+        e.y = ex2(e.y);
+        if (k % 4 == 0)
+          sum0 = __fadd2_rn(sum0, e);
+        else
+          sum1 = __fadd2_rn(sum1, e);
+        p[k / 2] = pack_bf16x2(e.x, e.y);
+        x[i][k] = __float_as_uint(e.x);
+        x[i][k + 1] = __float_as_uint(e.y);
+      }
+      tm_st16(tm_s + 32 * (chunk0 + i0 + i), p);
+      if (fine) {
+#pragma unroll
+        for (int k = 0; k < 32; k += 2)
+          p[k / 2] = pack_bf16x2(__uint_as_float(x[i][k]) - __uint_as_float(p[k / 2] << 16),
+                                 __uint_as_float(x[i][k + 1]) - __uint_as_float(p[k / 2] & 0xffff0000u));
+        tm_st16(tm_s + 32 * (chunk0 + i0 + i) + 16, p);
+      }
+    }
+  }
+  if constexpr (kN < 4) {
+    const uint32_t zero[16] = {};
+#pragma unroll
+    for (int c = 0; c < 4; c += kN) {
+      if (c != chunk0) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          tm_st16(tm_s + 32 * (c + i), zero);
+          if (fine) tm_st16(tm_s + 32 * (c + i) + 16, zero);
+        }
+      }
+    }
+  }
+  l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+  tm_st_wait();
+}
+
 template <int kD, bool kFp8>
-__global__ void __launch_bounds__(kAThreads, 1)
+__global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                      const __grid_constant__ AttnArgs a, const __grid_constant__ AttnDims d,
                      int box_rows, int part_rows) {
@@ -540,15 +684,15 @@ __global__ void __launch_bounds__(kAThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < Sh::kSlots; ++i) {
-      mbar_init(&ctl.full_bar[i], kFp8 ? kPrepWarps : 1);
+      mbar_init(&ctl.full_bar[i], kFp8 ? Sh::kPrepWarps : 1);
       mbar_init(&ctl.empty_bar[i], 1);
       mbar_init(&ctl.tail_full[i], 1);
-      mbar_init(&ctl.prep_bar[i], kPrepWarps);
+      mbar_init(&ctl.prep_bar[i], Sh::kPrepWarps);
     }
     for (int i = 0; i < Sh::kRaw; ++i) {
       mbar_init(&ctl.raw_full[i], 1);
       mbar_init(&ctl.raw_scaled[i], 1);
-      mbar_init(&ctl.raw_empty[i], kPrepWarps);
+      mbar_init(&ctl.raw_empty[i], Sh::kPrepWarps);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&ctl.s_full[w], 1);
@@ -577,7 +721,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
   for (int pass = 0; pass < 2; ++pass) {
     int64_t before = 0;
     const int64_t start = pass ? run_start(total, run_count(total, gridDim.x), blockIdx.x) : -1;
-    for (int64_t b0 = 0; b0 < a.pages.batch; b0 += kAThreads) {
+    for (int64_t b0 = 0; b0 < a.pages.batch; b0 += Sh::kThreads) {
       const int64_t b = b0 + threadIdx.x;
       int64_t w = 0;
       if (b < a.pages.batch) {
@@ -595,7 +739,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
       if (lane == 31) ctl.scan[warp] = incl;
       __syncthreads();
       int64_t base = before, all = 0;
-      for (int i = 0; i < kAThreads / 32; ++i) {
+      for (int i = 0; i < Sh::kThreads / 32; ++i) {
         if (i < warp) base += ctl.scan[i];
         all += ctl.scan[i];
       }
@@ -622,7 +766,131 @@ __global__ void __launch_bounds__(kAThreads, 1)
   // whether a key tile (index in the unit) reaches past the context
   auto is_tail = [](const Segment& s, int tile) { return (tile + 1) * kTile > s.ctx; };
 
-  if (warp == 0) {
+  auto prepare = [&]() {
+    // ---- tiles prepared
+    const int t = threadIdx.x - Sh::kPrepWarp0 * 32;
+    constexpr int kPrepThreads = Sh::kPrepWarps * 32;
+    uint32_t item = 0, tail_phase = 0;
+    int seg_n = 0;
+    bool ok = true;
+    while (ok && walk.next(seg)) {
+      ++seg_n;
+      for_items(seg.tiles, lead_of(seg), [&](bool is_v, int j) {
+        const uint32_t it = item++;
+        const uint32_t slot = it % Sh::kSlots;
+        const int tile = seg.tile0 + j, p0 = tile * kTile;
+        const uint32_t dst = slot0 + slot * Sh::kTileBytes;
+        if constexpr (kFp8) {
+          const uint32_t r = it % Sh::kRaw;
+          if (!warp_wait(&ctl.raw_full[r], (it / Sh::kRaw) & 1u, &ctl.abort_flag) ||
+              !warp_wait(&ctl.raw_scaled[r], (it / Sh::kRaw) & 1u, &ctl.abort_flag) ||
+              !warp_wait(&ctl.empty_bar[slot], ((it / Sh::kSlots) & 1u) ^ 1u, &ctl.abort_flag)) {
+            ok = false;
+            return false;
+          }
+          constexpr int kChunks = kD / 16;  // 16 payload bytes each
+          const uint8_t* raw_tiles = attn_smem + (2 + Sh::kSlots) * Sh::kTileBytes;
+          const int c = t % kChunks;
+          bool found = false;
+          constexpr int kRows = kPrepThreads / kChunks;  // rows of one pass
+          constexpr int kBatch = 4;                      // passes whose loads are under way at once
+#pragma unroll 1
+          for (int i0 = 0; i0 < kTile / kRows; i0 += kBatch) {
+            uint4 in4[kBatch];
+            uint32_t byte[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const int row = (i0 + i) * kRows + t / kChunks;
+              in4[i] = *reinterpret_cast<const uint4*>(raw_tiles + r * Sh::kRawBytes + row * kD + c * 16);
+              byte[i] = ctl.raw_scale[r][row];
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const int row = (i0 + i) * kRows + t / kChunks;
+              const int pos = p0 + row;
+              if (is_v && pos >= seg.ctx && (pos >= seg.len || byte[i] == 255)) {
+                found |= pos < seg.len;
+                in4[i] = make_uint4(0, 0, 0, 0);
+                byte[i] = 127;
+              }
+              // 2^120 * 2^(byte - 127) as one bf16 factor, or as two
+              const bool one = byte[i] <= 134;
+              const uint32_t m1 = (one ? byte[i] + 120 : 247u) << 7;
+              const uint32_t f1 = m1 | (m1 << 16);
+              const uint32_t in[4] = {in4[i].x, in4[i].y, in4[i].z, in4[i].w};
+              uint32_t o[8];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                o[2 * k] = mul_bf16x2(e4m3_bits(__byte_perm(in[k], 0, 0x1404)), f1);
+                o[2 * k + 1] = mul_bf16x2(e4m3_bits(__byte_perm(in[k], 0, 0x3424)), f1);
+              }
+              if (!one) {
+                const uint32_t m2 = byte[i] == 255 ? 0x7fc0u : byte[i] << 7;
+                const uint32_t f2 = m2 | (m2 << 16);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], f2);
+              }
+              uint8_t* line = attn_smem + 2 * Sh::kTileBytes + slot * Sh::kTileBytes +
+                              (c / 4) * (kTile * 128) + row * 128;
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                *reinterpret_cast<uint4*>(line + (((c % 4) * 2 + k) ^ (row & 7)) * 16) =
+                    make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            }
+          }
+          if (found) ctl.bad_seg[seg_n % kBadRing] = seg_n;
+          async_fence();
+          warp_arrive(&ctl.raw_empty[r]);
+          warp_arrive(&ctl.full_bar[slot]);
+        } else {
+          if (!is_v || !is_tail(seg, tile)) return true;
+          if (!warp_wait(&ctl.tail_full[slot], (tail_phase >> slot) & 1u, &ctl.abort_flag)) {
+            ok = false;
+            return false;
+          }
+          tail_phase ^= 1u << slot;
+          for (int row = t; row < kTile; row += kPrepThreads) {
+            const int pos = p0 + row;
+            if (pos < seg.ctx) continue;
+            const bool past = pos >= seg.len;
+            bool found = false;
+            for (int c = 0; c < kD / 8; ++c) {
+              const uint32_t at = dst + uint32_t(c / 8) * (kTile * 128) + uint32_t(row) * 128 +
+                                  uint32_t(((c % 8) ^ (row & 7)) * 16);
+              uint32_t w[4];
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                           : "r"(at));
+              bool change = past;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const bool lo = (w[k] & 0x7f80u) == 0x7f80u, hi = (w[k] & 0x7f800000u) == 0x7f800000u;
+                change |= lo || hi;
+                if (past || lo) w[k] &= 0xffff0000u;
+                if (past || hi) w[k] &= 0x0000ffffu;
+              }
+              if (change) {
+                found |= !past;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]),
+                             "r"(w[2]), "r"(w[3])
+                             : "memory");
+              }
+            }
+            if (found) ctl.bad_seg[seg_n % kBadRing] = seg_n;
+          }
+          async_fence();
+          warp_arrive(&ctl.prep_bar[slot]);
+        }
+        return true;
+      });
+    }
+  };
+
+  // (registers are moved before the warps of a group go different ways: all of
+  // them execute the same instruction)
+  if (warp < 4) {
+    fewer_registers<Sh::kLowRegs>();
+    if (warp == 0) {
     // ---- loads: the warp's lanes take a tile's boxes
     constexpr int kBoxCols = kFp8 ? 1 : Sh::kHalves;
     constexpr int kRing = kFp8 ? Sh::kRaw : Sh::kSlots;
@@ -672,10 +940,10 @@ __global__ void __launch_bounds__(kAThreads, 1)
     // abort)
     for (uint32_t slot = 0; slot < uint32_t(kRing) && slot < item; ++slot) {
       const bool tail = (last_tail >> slot) & 1u;
-      mbar_wait(tail ? &ctl.tail_full[slot] : &full[slot],
+      wait_phase(tail ? &ctl.tail_full[slot] : &full[slot],
                 (((tail ? tail_phase : full_phase) >> slot) & 1u) ^ 1u, &ctl.abort_flag, false);
     }
-  } else if (warp == 1) {
+    } else if (warp == 1) {
     // ---- products: the warp goes through the tiles converged, one lane
     // issues (what the issue needs is then the same in all lanes, which keeps
     // it in uniform registers)
@@ -787,151 +1055,57 @@ __global__ void __launch_bounds__(kAThreads, 1)
     }
     if (issue) umma_commit(&ctl.done_bar);  // every product issued has completed
     __syncwarp();
-  } else if (warp == 2) {
-    if constexpr (kFp8) {
-      // ---- scale bytes of the raw tiles, four keys per lane
-      uint32_t item = 0;
-      bool ok = true;
-      while (ok && walk.next(seg)) {
-        for_items(seg.tiles, lead_of(seg), [&](bool is_v, int j) {
-          const uint32_t r = item % Sh::kRaw, phase = (item / Sh::kRaw) & 1u;
-          if (!warp_wait(&ctl.raw_empty[r], phase ^ 1u, &ctl.abort_flag)) {
-            ok = false;
-            return false;
-          }
-          const int p0 = (seg.tile0 + j) * kTile;
-#pragma unroll
-          for (int i = 0; i < kTile / 32; ++i) {
-            const int pos = p0 + i * 32 + lane;
-            uint8_t byte = 0;
-            if (pos < seg.len) {
-              int at;
-              const int64_t page = page_of(a, seg, pos, &at);
-              if (page >= 0 && page < a.cache.num_pages)
-                byte = (is_v ? a.cache.v_scale : a.cache.k_scale)[page * a.cache.scale_page_stride +
-                                                                  at * a.cache.scale_slot_stride +
-                                                                  seg.h * a.cache.scale_head_stride];
-            }
-            ctl.raw_scale[r][i * 32 + lane] = byte;
-          }
-          warp_arrive(&ctl.raw_scaled[r]);
-          ++item;
-          return true;
-        });
-      }
-    }
-  } else if (warp >= 12) {
-    // ---- tiles prepared
-    const int t = threadIdx.x - 12 * 32;
-    uint32_t item = 0, tail_phase = 0;
-    int seg_n = 0;
-    bool ok = true;
+    } else if constexpr (kFp8) {
+    // ---- scale bytes of the raw tiles, four keys per lane; warps 2 and 3 take
+    // the items in turn and fetch the next one's bytes before they hand on
+    // this one's
+    uint32_t item = 0, held_item = 0;
+    uint32_t held = 0;  // four bytes
+    bool ok = true, holds = false;
+    auto hand_on = [&]() {
+      const uint32_t r = held_item % Sh::kRing, phase = (held_item / Sh::kRing) & 1u;
+      ok = warp_wait(&ctl.raw_empty[r], phase ^ 1u, &ctl.abort_flag);
+      if (!ok) return;
+      *reinterpret_cast<uint32_t*>(&ctl.raw_scale[r][4 * lane]) = held;
+      warp_arrive(&ctl.raw_scaled[r]);
+    };
     while (ok && walk.next(seg)) {
-      ++seg_n;
       for_items(seg.tiles, lead_of(seg), [&](bool is_v, int j) {
         const uint32_t it = item++;
-        const uint32_t slot = it % Sh::kSlots;
-        const int tile = seg.tile0 + j, p0 = tile * kTile;
-        const uint32_t dst = slot0 + slot * Sh::kTileBytes;
-        if constexpr (kFp8) {
-          const uint32_t r = it % Sh::kRaw;
-          if (!warp_wait(&ctl.raw_full[r], (it / Sh::kRaw) & 1u, &ctl.abort_flag) ||
-              !warp_wait(&ctl.raw_scaled[r], (it / Sh::kRaw) & 1u, &ctl.abort_flag) ||
-              !warp_wait(&ctl.empty_bar[slot], ((it / Sh::kSlots) & 1u) ^ 1u, &ctl.abort_flag)) {
-            ok = false;
-            return false;
-          }
-          constexpr int kChunks = kD / 16;  // 16 payload bytes each
-          const uint32_t src = raw0 + r * Sh::kRawBytes;
-          const int c = t % kChunks;
-          bool found = false;
-#pragma unroll 2
-          for (int i = 0; i < kTile * kChunks / kPrepThreads; ++i) {
-            const int row = i * (kPrepThreads / kChunks) + t / kChunks;
-            uint32_t byte = ctl.raw_scale[r][row];
-            uint4 w;
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                         : "r"(src + uint32_t(row) * kD + uint32_t(c) * 16));
-            const int pos = p0 + row;
-            if (is_v && pos >= seg.ctx && (pos >= seg.len || byte == 255)) {
-              found |= pos < seg.len;
-              w = make_uint4(0, 0, 0, 0);
-              byte = 127;
-            }
-            // 2^120 * 2^(byte - 127) as one bf16 factor, or as two
-            const bool one = byte <= 134;
-            const uint32_t m1 = (one ? byte + 120 : 247u) << 7;
-            const uint32_t m2 = byte == 255 ? 0x7fc0u : byte << 7;
-            const uint32_t f1 = m1 | (m1 << 16), f2 = m2 | (m2 << 16);
-            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-            uint32_t o[8];
+        if ((it & 1u) != uint32_t(warp & 1)) return true;
+        const int p0 = (seg.tile0 + j) * kTile + 4 * lane;
+        const uint8_t* scales = is_v ? a.cache.v_scale : a.cache.k_scale;
+        uint32_t bytes = 0;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              o[2 * k] = mul_bf16x2(e4m3_bits(__byte_perm(in[k], 0, 0x1404)), f1);
-              o[2 * k + 1] = mul_bf16x2(e4m3_bits(__byte_perm(in[k], 0, 0x3424)), f1);
-            }
-            if (!one) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], f2);
-            }
-            const uint32_t line = dst + uint32_t(c / 4) * (kTile * 128) + uint32_t(row) * 128;
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                               line + uint32_t((((c % 4) * 2 + k) ^ (row & 7)) * 16)),
-                           "r"(o[4 * k]), "r"(o[4 * k + 1]), "r"(o[4 * k + 2]), "r"(o[4 * k + 3])
-                           : "memory");
+        for (int i = 0; i < 4; ++i) {
+          if (p0 + i < seg.len) {
+            int at;
+            const int64_t page = page_of(a, seg, p0 + i, &at);
+            if (page >= 0 && page < a.cache.num_pages)
+              bytes |= uint32_t(scales[page * a.cache.scale_page_stride + at * a.cache.scale_slot_stride +
+                                       seg.h * a.cache.scale_head_stride])
+                       << (8 * i);
           }
-          if (found) ctl.bad_seg[seg_n % kBadRing] = seg_n;
-          async_fence();
-          warp_arrive(&ctl.raw_empty[r]);
-          warp_arrive(&ctl.full_bar[slot]);
-        } else {
-          if (!is_v || !is_tail(seg, tile)) return true;
-          if (!warp_wait(&ctl.tail_full[slot], (tail_phase >> slot) & 1u, &ctl.abort_flag)) {
-            ok = false;
-            return false;
-          }
-          tail_phase ^= 1u << slot;
-          const int pos = p0 + t;
-          if (pos >= seg.ctx) {
-            const bool past = pos >= seg.len;
-            bool found = false;
-            for (int c = 0; c < kD / 8; ++c) {
-              const uint32_t at = dst + uint32_t(c / 8) * (kTile * 128) + uint32_t(t) * 128 +
-                                  uint32_t(((c % 8) ^ (t & 7)) * 16);
-              uint32_t w[4];
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                           : "r"(at));
-              bool change = past;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const bool lo = (w[k] & 0x7f80u) == 0x7f80u, hi = (w[k] & 0x7f800000u) == 0x7f800000u;
-                change |= lo || hi;
-                if (past || lo) w[k] &= 0xffff0000u;
-                if (past || hi) w[k] &= 0x0000ffffu;
-              }
-              if (change) {
-                found |= !past;
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]),
-                             "r"(w[2]), "r"(w[3])
-                             : "memory");
-              }
-            }
-            if (found) ctl.bad_seg[seg_n % kBadRing] = seg_n;
-          }
-          async_fence();
-          warp_arrive(&ctl.prep_bar[slot]);
         }
-        return true;
+        if (holds) hand_on();
+        held = bytes;
+        held_item = it;
+        holds = true;
+        return ok;
       });
     }
-  } else if (warp >= 4) {
-    // ---- softmax groups A (warps 4-7) and B (8-11): one row per thread
+    if (ok && holds) hand_on();
+    } else {
+      prepare();
+    }
+  } else if (warp < 12) {
+    more_registers<Sh::kSoftRegs>();
+    // ---- softmax groups A (warps 4-7) and B (8-11).  A lane of tensor memory
+    // is a row; with at most 64 (32) rows the query tile holds them twice (four
+    // times), and the warps of each copy take a half (quarter) of a tile's
+    // keys, with maxima, sums and outputs of their own.
     const int w = warp >= 8 ? 1 : 0;
-    const int r = threadIdx.x & (kTile - 1);       // row of the query tile, lane of tensor memory
+    const int r = threadIdx.x & (kTile - 1);       // lane of tensor memory
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const uint32_t tm_s = tmem + uint32_t(w) * kTile + lanes;
     const uint32_t tm_o = tmem + 2 * kTile + lanes;
@@ -942,10 +1116,17 @@ __global__ void __launch_bounds__(kAThreads, 1)
     uint32_t s_n = 0, ml_n = 0;
     int seg_n = 0;
     bool ok = true;
+    // all softmax warps meet (false: a wait ran out)
+    auto meet = [&]() {
+      warp_arrive(&ctl.ml_full);
+      return warp_wait(&ctl.ml_full, ml_n++ & 1u, &ctl.abort_flag);
+    };
     while (ok && walk.next(seg)) {
       ++seg_n;
       const bool two = seg.rows > kTile;
-      const int row = (two ? w * kTile : 0) + r;   // of the unit
+      // rows per copy: 32, 64, or all 128 lanes
+      const int span = two || seg.rows > 64 ? kTile : seg.rows > 32 ? 64 : 32;
+      const int row = (two ? w * kTile : 0) + (r & (span - 1));   // of the unit
       const bool live = row < seg.rows;
       const bool warp_live = (row & ~31) < seg.rows;
       const int node = live ? (seg.row0 + row) / d.group : 0;
@@ -979,6 +1160,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
 
       float m = -INFINITY, l = 0.f;   // the weights' exponent offset and their sum
       bool first = true;
+      const bool fine = seg.len <= kFineKeys;
+      const int chunk0 = span == kTile ? 0 : span == 64 ? (warp & 2) : (warp & 3);
       for (int j = two ? 0 : w; j < seg.tiles; j += two ? 1 : 2) {
         if (!warp_wait(&ctl.s_full[w], s_n & 1u, &ctl.abort_flag)) {
           ok = false;
@@ -987,81 +1170,24 @@ __global__ void __launch_bounds__(kAThreads, 1)
         ++s_n;
         tc_after();
         if (warp_live) {
-          const int p0 = (seg.tile0 + j) * kTile;
+          const int p0 = (seg.tile0 + j) * kTile + 32 * chunk0;
           const bool tail = is_tail(seg, seg.tile0 + j);
-          uint32_t vis[4];
-          if (tail) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) vis[i] = live ? visible32(a, seg, node, p0 + 32 * i) : 0u;
-          }
-          __syncwarp();
-          float top = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t x[32];
-            tm_ld(tm_s + 32 * i, x);
+          auto take = [&](auto count) {
+            constexpr int kN = decltype(count)::value;
+            uint32_t vis[kN];
             if (tail) {
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!((vis[i] >> k) & 1u)) x[k] = 0xff800000u;
+              for (int i = 0; i < kN; ++i) vis[i] = live ? visible32(a, seg, node, p0 + 32 * i) : 0u;
+              __syncwarp();
             }
-#pragma unroll
-            for (int k = 0; k < 32; k += 2)
-              top = max3(top, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-          }
-          top *= sl2;
-          const bool grow = top > m + kLazyLog2 || (m == -INFINITY && top > -INFINITY);
-          if (__any_sync(0xffffffffu, grow)) {
-            const float f = grow ? ex2(m - top) : 1.f;
-            if (grow) m = top;
-            l *= f;
-            if (!first) {
-#pragma unroll 1
-              for (int i = 0; i < kD / 32; ++i) {
-                uint32_t x[32];
-                tm_ld(tm_o + uint32_t(w * kD + 32 * i), x);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
-                tm_st(tm_o + uint32_t(w * kD + 32 * i), x);
-              }
-            }
-          }
-          const float off = m == -INFINITY ? 0.f : -m;
-          const float2 s2 = make_float2(sl2, sl2), o2 = make_float2(off, off);
-          float2 sum = make_float2(0.f, 0.f);
-          // 32 columns of S at a time, their place taken by P's 16 and, where
-          // wanted, the remainders' 16
-          const bool fine = seg.len <= kFineKeys;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t x[32], p[16];
-            tm_ld(tm_s + 32 * i, x);
-            if (tail) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!((vis[i] >> k) & 1u)) x[k] = 0xff800000u;
-            }
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              float2 e = __ffma2_rn(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), s2, o2);
-              e.x = ex2(e.x);
-              e.y = ex2(e.y);
-              sum = __fadd2_rn(sum, e);
-              p[k / 2] = pack_bf16x2(e.x, e.y);
-              x[k] = __float_as_uint(e.x);
-              x[k + 1] = __float_as_uint(e.y);
-            }
-            tm_st16(tm_s + 32 * i, p);
-            if (fine) {
-#pragma unroll
-              for (int k = 0; k < 32; k += 2)
-                p[k / 2] = pack_bf16x2(__uint_as_float(x[k]) - __uint_as_float(p[k / 2] << 16),
-                                       __uint_as_float(x[k + 1]) - __uint_as_float(p[k / 2] & 0xffff0000u));
-              tm_st16(tm_s + 32 * i + 16, p);
-            }
-          }
-          l += sum.x + sum.y;
-          tm_st_wait();
+            soft_tile<kD, kN>(tm_s, tm_o + uint32_t(w) * kD, chunk0, tail, vis, fine, first, sl2, m, l);
+          };
+          if (span == 32)
+            take(std::integral_constant<int, 1>());
+          else if (span == 64)
+            take(std::integral_constant<int, 2>());
+          else
+            take(std::integral_constant<int, 4>());
         }
         first = false;
         tc_before();
@@ -1070,115 +1196,170 @@ __global__ void __launch_bounds__(kAThreads, 1)
       if (!ok || !warp_wait(&ctl.o_full, (seg_n - 1) & 1u, &ctl.abort_flag)) break;
       tc_after();
       const bool fix = *reinterpret_cast<volatile int*>(&ctl.bad_seg[seg_n % kBadRing]) == seg_n;
-
-      // one tile of rows: both groups hold sums of the same row; each
-      // finishes half of the columns
-      float wa = 1.f, wb = 0.f, M = m, L = l;
-      if (!two) {
-        // (the next segment's write follows every thread's read of this one's:
-        // it waits for products that wait for all threads' query rows)
-        ctl.ml[w][r] = make_float2(m, l);
-        warp_arrive(&ctl.ml_full);
-        if (!warp_wait(&ctl.ml_full, ml_n & 1u, &ctl.abort_flag)) break;
-        ++ml_n;
-        const float2 A = ctl.ml[0][r], B = seg.tiles > 1 ? ctl.ml[1][r] : make_float2(-INFINITY, 0.f);
-        M = fmaxf(A.x, B.x);
-        const float base = M == -INFINITY ? 0.f : M;
-        wa = ex2(A.x - base);
-        wb = ex2(B.x - base);
-        L = A.y * wa + B.y * wb;
-      }
-      if (warp_live) {
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        const int c0 = two ? 0 : w * (kD / 2), c1 = two ? kD : c0 + kD / 2;
-        float* part = nullptr;
-        if (!seg.whole) {
-          float* base = static_cast<float*>(a.workspace) +
-                        (int64_t(blockIdx.x) * 2 + seg.part) * part_rows * (kD + 2);
-          part = base + int64_t(row) * kD;
-          if (live && (two || w == 0))
-            reinterpret_cast<float2*>(base + int64_t(part_rows) * kD)[row] = make_float2(M, L);
-        } else if (live && (two || w == 0) && a.lse) {
-          a.lse[int64_t(seg.node0 + node) * a.n_q_heads + head] =
+      float* const slot = seg.whole ? nullptr
+                                    : static_cast<float*>(a.workspace) +
+                                          (int64_t(blockIdx.x) * 2 + seg.part) * part_rows * (kD + 2);
+      // a row's maximum and sum, and n of its columns from c on, to where they go
+      auto put_stats = [&](int row_, float M, float L) {
+        const int i = seg.row0 + row_;
+        if (slot)
+          reinterpret_cast<float2*>(slot + int64_t(part_rows) * kD)[row_] = make_float2(M, L);
+        else if (a.lse)
+          a.lse[int64_t(seg.node0 + i / d.group) * a.n_q_heads + seg.h * d.group + i % d.group] =
               L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
-        }
-#pragma unroll 1
-        for (int c = c0; c < c1; c += 32) {
-          uint32_t x[32];
-          float o[32];
-          __syncwarp();
-          if (two) {
-            tm_ld(tm_o + uint32_t(w * kD + c), x);
+      };
+      auto put = [&](int row_, int c, auto& o, float L) {
+        constexpr int kN = int(sizeof(o) / sizeof(float));
+        const int i = seg.row0 + row_, node_ = i / d.group, head_ = seg.h * d.group + i % d.group;
+        if (fix) {
+          // non-finite values of drafted nodes that this row sees
+          const int end = min((seg.tile0 + seg.tiles) * kTile, seg.len);
+          for (int pos = max(seg.ctx, seg.tile0 * kTile); pos < end; ++pos) {
+            if (!(visible32(a, seg, node_, pos) & 1u)) continue;
+            int at;
+            const int64_t page = page_of(a, seg, pos, &at);
+            if (page < 0 || page >= a.cache.num_pages) continue;
+            if constexpr (kFp8) {
+              if (a.cache.v_scale[page * a.cache.scale_page_stride + at * a.cache.scale_slot_stride +
+                                  seg.h * a.cache.scale_head_stride] == 255) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __uint_as_float(x[k]);
-          } else {
-            tm_ld(tm_o + uint32_t(c), x);
+                for (int k = 0; k < kN; ++k) o[k] = __int_as_float(0x7fc00000);
+              }
+            } else {
+              const bf16_t* v = static_cast<const bf16_t*>(a.cache.v) + page * a.cache.page_stride +
+                                at * a.cache.slot_stride + seg.h * a.cache.head_stride + c;
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __uint_as_float(x[k]) * wa;
-            if (seg.tiles > 1) {
-              tm_ld(tm_o + uint32_t(kD + c), x);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = fmaf(__uint_as_float(x[k]), wb, o[k]);
-            }
-          }
-          if (live && fix) {
-            // non-finite values of drafted nodes that this row sees
-            const int end = min((seg.tile0 + seg.tiles) * kTile, seg.len);
-            for (int pos = max(seg.ctx, seg.tile0 * kTile); pos < end; ++pos) {
-              if (!(visible32(a, seg, node, pos) & 1u)) continue;
-              int at;
-              const int64_t page = page_of(a, seg, pos, &at);
-              if (page < 0 || page >= a.cache.num_pages) continue;
-              if constexpr (kFp8) {
-                if (a.cache.v_scale[page * a.cache.scale_page_stride + at * a.cache.scale_slot_stride +
-                                    seg.h * a.cache.scale_head_stride] == 255) {
-#pragma unroll
-                  for (int k = 0; k < 32; ++k) o[k] = __int_as_float(0x7fc00000);
-                }
-              } else {
-                const bf16_t* v = static_cast<const bf16_t*>(a.cache.v) + page * a.cache.page_stride +
-                                  at * a.cache.slot_stride + seg.h * a.cache.head_stride + c;
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                  const float y = Elem<bf16_t>::load1(v + k);
-                  if (!(fabsf(y) < INFINITY)) o[k] += y;
-                }
+              for (int k = 0; k < kN; ++k) {
+                const float y = Elem<bf16_t>::load1(v + k);
+                if (!(fabsf(y) < INFINITY)) o[k] += y;
               }
             }
           }
-          if (live && part) {
+        }
+        if (slot) {
+#pragma unroll
+          for (int k = 0; k < kN; k += 4)
+            *reinterpret_cast<float4*>(slot + int64_t(row_) * kD + c + k) =
+                make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          return;
+        }
+        const float inv = 1.f / L;
+#pragma unroll
+        for (int k = 0; k < kN; ++k) o[k] = L == 0.f ? 0.f : o[k] * inv;
+        uint16_t* dst = static_cast<uint16_t*>(a.out) + int64_t(seg.node0 + node_) * a.ld_on +
+                        int64_t(head_) * a.ld_oh + c;
+        if (vec_o) {
+          if constexpr (kN % 8 == 0) {
+#pragma unroll
+            for (int k = 0; k < kN; k += 8)
+              *reinterpret_cast<uint4*>(dst + k) =
+                  make_uint4(pack_bf16x2(o[k], o[k + 1]), pack_bf16x2(o[k + 2], o[k + 3]),
+                             pack_bf16x2(o[k + 4], o[k + 5]), pack_bf16x2(o[k + 6], o[k + 7]));
+          } else {
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < kN; ++k) dst[k] = static_cast<uint16_t>(pack_bf16x2(o[k], 0.f));
+        }
+      };
+      if (two) {
+        if (live) put_stats(row, m, l);
+        if (warp_live) {
+#pragma unroll 1
+          for (int c = 0; c < kD; c += 32) {
+            uint32_t x[32];
+            float o[32];
+            __syncwarp();
+            tm_ld(tm_o + uint32_t(w * kD + c), x);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __uint_as_float(x[k]);
+            if (live) put(row, c, o, l);
+          }
+        }
+        continue;
+      }
+      // One query tile: a row's sums are spread over both groups and its copies.
+      // (The next segment's write of ml follows every thread's read of this
+      // one's: it waits for products that wait for all threads' query rows.)
+      ctl.ml[w][r] = make_float2(m, l);
+      if (!meet()) break;
+      const bool both = seg.tiles > 1;
+      auto row_sums = [&](int first_lane, float& M, float& L) {
+        M = -INFINITY;
+        for (int c = first_lane; c < kTile; c += span)
+          M = max3(M, ctl.ml[0][c].x, both ? ctl.ml[1][c].x : -INFINITY);
+        const float base = M == -INFINITY ? 0.f : M;
+        L = 0.f;
+        for (int c = first_lane; c < kTile; c += span) {
+          L += ctl.ml[0][c].y * ex2(ctl.ml[0][c].x - base);
+          if (both) L += ctl.ml[1][c].y * ex2(ctl.ml[1][c].x - base);
+        }
+      };
+      float M, L;
+      row_sums(r & (span - 1), M, L);
+      const float base = M == -INFINITY ? 0.f : M;
+      const float wa = ex2(ctl.ml[0][r].x - base), wb = both ? ex2(ctl.ml[1][r].x - base) : 0.f;
+      if (live && w == 0 && r == row) put_stats(row, M, L);
+      // each group merges half of the columns of both; copies meet in the query
+      // tiles' place (all products of this segment are done), 16-byte pieces
+      // of a row at their place exclusive-or the row
+      const uint32_t xch = smem0 + uint32_t(r) * (kD * 4);
+      if (warp_live) {
+#pragma unroll 1
+        for (int c = w * (kD / 2); c < (w + 1) * (kD / 2); c += 32) {
+          uint32_t x[32];
+          float o[32];
+          __syncwarp();
+          tm_ld(tm_o + uint32_t(c), x);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __uint_as_float(x[k]) * wa;
+          if (both) {
+            tm_ld(tm_o + uint32_t(kD + c), x);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = fmaf(__uint_as_float(x[k]), wb, o[k]);
+          }
+          if (span == kTile) {
+            if (live) put(row, c, o, L);
+          } else {
 #pragma unroll
             for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<float4*>(part + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-          } else if (live) {
-            uint16_t* dst = static_cast<uint16_t*>(a.out) + int64_t(seg.node0 + node) * a.ld_on +
-                            int64_t(head) * a.ld_oh + c;
-            if (L == 0.f) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = 0.f;
-            } else {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] *= inv;
-            }
-            if (vec_o) {
-#pragma unroll
-              for (int k = 0; k < 32; k += 8)
-                *reinterpret_cast<uint4*>(dst + k) =
-                    make_uint4(pack_bf16x2(o[k], o[k + 1]), pack_bf16x2(o[k + 2], o[k + 3]),
-                               pack_bf16x2(o[k + 4], o[k + 5]), pack_bf16x2(o[k + 6], o[k + 7]));
-            } else {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) dst[k] = static_cast<uint16_t>(pack_bf16x2(o[k], 0.f));
-            }
+              asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               xch + uint32_t((((c + k) / 4) ^ (r & (kD / 4 - 1))) * 16)),
+                           "f"(o[k]), "f"(o[k + 1]), "f"(o[k + 2]), "f"(o[k + 3])
+                           : "memory");
           }
         }
       }
+      if (span < kTile) {
+        if (!meet()) break;
+        constexpr int kPieces = kD / 4;  // of a row; a warp takes 32 at a time
+        for (int i = (warp - 4) * 32 + lane; i < seg.rows * kPieces; i += kSoftWarps * 32) {
+          const int row_ = i / kPieces, piece = i % kPieces;
+          float o[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int c = row_; c < kTile; c += span) {
+            float x[4];
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+                         : "r"(smem0 + uint32_t(c) * (kD * 4) +
+                               uint32_t((piece ^ (c & (kPieces - 1))) * 16)));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] += x[k];
+          }
+          row_sums(row_, M, L);
+          put(row_, piece * 4, o, L);
+        }
+        if (!meet()) break;  // before the next query rows take the place
+      }
     }
+  } else {
+    fewer_registers<Sh::kLowRegs>();
+    if constexpr (kFp8) prepare();
   }
   tc_before();
   __syncthreads();
   if (warp == 1) {
-    if (lane == 0) mbar_wait(&ctl.done_bar, 0, &ctl.abort_flag, false);
+    if (lane == 0) wait_phase(&ctl.done_bar, 0, &ctl.abort_flag, false);
     __syncwarp();
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kAtTmemCols)
@@ -1325,6 +1506,12 @@ cudaError_t launch_tensor(const AttnArgs& a, int sms, int device, cudaStream_t s
   std::call_once(once[device], [&] {
     ready[device] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(Sh::kSmem));
+    // the warp groups share out exactly what the CTA is launched with; with
+    // less, the ones that ask for more would wait for it
+    cudaFuncAttributes f;
+    if (ready[device] == cudaSuccess) ready[device] = cudaFuncGetAttributes(&f, kernel);
+    if (ready[device] == cudaSuccess && f.numRegs < Sh::kLaunchRegs)
+      ready[device] = cudaErrorInvalidDeviceFunction;
   });
   if (ready[device] != cudaSuccess) return ready[device];
   int box_rows = kTile;
@@ -1334,7 +1521,7 @@ cudaError_t launch_tensor(const AttnArgs& a, int sms, int device, cudaStream_t s
     return cudaErrorInvalidValue;
   const AttnDims d{a.n_q_heads / a.cache.n_heads, static_cast<int>(a.pages.max_pages * a.cache.page_size)};
   const int part_rows = part_rows_of(a.n_nodes, d.group);
-  kernel<<<static_cast<unsigned>(sms), kAThreads, Sh::kSmem, st>>>(mk, mv, a, d, box_rows, part_rows);
+  kernel<<<static_cast<unsigned>(sms), Sh::kThreads, Sh::kSmem, st>>>(mk, mv, a, d, box_rows, part_rows);
   cudaError_t e = cudaGetLastError();
   // units of one tile are never cut
   if (e != cudaSuccess || d.room <= kTile) return e;
