@@ -5,7 +5,6 @@
 #include <cuda_fp16.h>
 
 #include <mutex>
-#include <type_traits>
 
 #include "fct_common.cuh"
 #include "fct_internal.h"
@@ -534,13 +533,17 @@ __device__ __forceinline__ int page_of(const AttnArgs& a, const Segment& s, int 
 
 // Order in which a segment's K and V tiles are used (and loaded): K runs
 // `lead` tiles ahead of V.  f(is_v, tile) for each.
+// (One loop with one call: the roles' bodies are long, and all of them share
+// the instruction cache.)
 template <typename F>
 __device__ __forceinline__ void for_items(int tiles, int lead, F f) {
-  for (int j = 0; j < lead && j < tiles; ++j)
-    if (!f(false, j)) return;
-  for (int j = 0; j < tiles; ++j) {
-    if (!f(true, j)) return;
-    if (j + lead < tiles && !f(false, j + lead)) return;
+  const int ahead = min(lead, tiles), paired = 2 * (tiles - ahead);
+#pragma unroll 1
+  for (int n = 0; n < 2 * tiles; ++n) {
+    const int m = n - ahead;
+    const bool is_v = m >= 0 && (m >= paired || !(m & 1));
+    const int j = m < 0 ? n : m >= paired ? m - paired / 2 : (m >> 1) + (is_v ? 0 : ahead);
+    if (!f(is_v, j)) return;
   }
 }
 
@@ -563,38 +566,51 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-// One key tile of a softmax warp: the chunks [chunk0, chunk0 + kN) of 32 keys
-// are its share, of the rows of its 32 lanes.  S's columns become P's (16 per
-// chunk, and 16 of the weights' rounding remainders where `fine`); the chunks
-// of other warps, which hold the same rows, become zero.
-template <int kD, int kN>
-__device__ __forceinline__ void soft_tile(uint32_t tm_s, uint32_t tm_o, int chunk0, bool tail,
-                                          const uint32_t (&vis)[kN], bool fine, bool first, float sl2,
-                                          float& m, float& l) {
-  constexpr int kHold = kN < 2 ? kN : 2;  // chunks in registers; with more, S is read twice
-  uint32_t x[kHold][32];
-  float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+// One key tile of a softmax warp: `chunks` (1, 2 or 4) chunks of 32 keys from
+// chunk0 on are its share, of the rows of its 32 lanes.  S's columns become
+// P's (16 per chunk, and 16 of the weights' rounding remainders where `fine`);
+// the chunks of other warps, which hold the same rows, become zero.  Two
+// chunks are held at a time (with four, S is read twice), in loops that stay
+// small: the roles of a CTA share one instruction cache.
+template <int kD>
+__device__ __forceinline__ void soft_tile(const AttnArgs& a, const Segment& seg, uint32_t tm_s,
+                                          uint32_t tm_o, int chunk0, int chunks, int node, bool live,
+                                          int p0, bool tail, bool fine, bool first, float sl2, float& m,
+                                          float& l) {
+  uint32_t x[2][32];
   auto load = [&](int i0) {
-#pragma unroll
-    for (int i = 0; i < kHold; ++i) tm_ld_start(tm_s + 32 * (chunk0 + i0 + i), x[i]);
-#pragma unroll
-    for (int i = 0; i < kHold; ++i) tm_ld_done(x[i]);
+    const uint32_t at = tm_s + 32 * (chunk0 + i0);
+    tm_ld_start(at, x[0]);
+    if (chunks > 1) tm_ld_start(at + 32, x[1]);
+    tm_ld_done(x[0]);
+    tm_ld_done(x[1]);
     if (tail) {
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t vis = live ? visible32(a, seg, node, p0 + 32 * (i0 + i)) : 0u;
+        __syncwarp();
 #pragma unroll
-      for (int i = 0; i < kHold; ++i)
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-          if (!((vis[i0 + i] >> k) & 1u)) x[i][k] = 0xff800000u;
+        for (int k = 0; k < 32; ++k) {
+          if (i == 0)
+            x[0][k] = (vis >> k) & 1u ? x[0][k] : 0xff800000u;
+          else
+            x[1][k] = (vis >> k) & 1u ? x[1][k] : 0xff800000u;
+        }
+      }
     }
   };
-#pragma unroll
-  for (int i0 = 0; i0 < kN; i0 += kHold) {
+  float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+  for (int i0 = 0; i0 < chunks; i0 += 2) {
     load(i0);
 #pragma unroll
-    for (int i = 0; i < kHold; ++i)
+    for (int k = 0; k < 32; k += 2)
+      tops[(k / 2) % 4] = max3(tops[(k / 2) % 4], __uint_as_float(x[0][k]), __uint_as_float(x[0][k + 1]));
+    if (chunks > 1) {
 #pragma unroll
       for (int k = 0; k < 32; k += 2)
-        tops[(k / 2) % 4] = max3(tops[(k / 2) % 4], __uint_as_float(x[i][k]), __uint_as_float(x[i][k + 1]));
+        tops[(k / 2) % 4] = max3(tops[(k / 2) % 4], __uint_as_float(x[1][k]), __uint_as_float(x[1][k + 1]));
+    }
   }
   const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * sl2;
   const bool grow = top > m + kLazyLog2 || (m == -INFINITY && top > -INFINITY);
@@ -616,45 +632,44 @@ __device__ __forceinline__ void soft_tile(uint32_t tm_s, uint32_t tm_o, int chun
   const float off = m == -INFINITY ? 0.f : -m;
   const float2 s2 = make_float2(sl2, sl2), o2 = make_float2(off, off);
   float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+  auto weights = [&](uint32_t (&y)[32], uint32_t at) {
+    uint32_t p[16];
 #pragma unroll
-  for (int i0 = 0; i0 < kN; i0 += kHold) {
-    if (kN > kHold) load(i0);
-#pragma unroll
-    for (int i = 0; i < kHold; ++i) {
-      uint32_t p[16];
-#pragma unroll
-      for (int k = 0; k < 32; k += 2) {
-        float2 e = __ffma2_rn(make_float2(__uint_as_float(x[i][k]), __uint_as_float(x[i][k + 1])), s2, o2);
-        e.x = ex2(e.x);
-        e.y = ex2(e.y);
-        if (k % 4 == 0)
-          sum0 = __fadd2_rn(sum0, e);
-        else
-          sum1 = __fadd2_rn(sum1, e);
-        p[k / 2] = pack_bf16x2(e.x, e.y);
-        x[i][k] = __float_as_uint(e.x);
-        x[i][k + 1] = __float_as_uint(e.y);
-      }
-      tm_st16(tm_s + 32 * (chunk0 + i0 + i), p);
-      if (fine) {
-#pragma unroll
-        for (int k = 0; k < 32; k += 2)
-          p[k / 2] = pack_bf16x2(__uint_as_float(x[i][k]) - __uint_as_float(p[k / 2] << 16),
-                                 __uint_as_float(x[i][k + 1]) - __uint_as_float(p[k / 2] & 0xffff0000u));
-        tm_st16(tm_s + 32 * (chunk0 + i0 + i) + 16, p);
-      }
+    for (int k = 0; k < 32; k += 2) {
+      float2 e = __ffma2_rn(make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), s2, o2);
+      e.x = ex2(e.x);
+      e.y = ex2(e.y);
+      if (k % 4 == 0)
+        sum0 = __fadd2_rn(sum0, e);
+      else
+        sum1 = __fadd2_rn(sum1, e);
+      p[k / 2] = pack_bf16x2(e.x, e.y);
+      y[k] = __float_as_uint(e.x);
+      y[k + 1] = __float_as_uint(e.y);
     }
+    tm_st16(at, p);
+    if (fine) {
+#pragma unroll
+      for (int k = 0; k < 32; k += 2)
+        p[k / 2] = pack_bf16x2(__uint_as_float(y[k]) - __uint_as_float(p[k / 2] << 16),
+                               __uint_as_float(y[k + 1]) - __uint_as_float(p[k / 2] & 0xffff0000u));
+      tm_st16(at + 16, p);
+    }
+  };
+#pragma unroll 1
+  for (int i0 = 0; i0 < chunks; i0 += 2) {
+    if (chunks > 2) load(i0);
+    const uint32_t at = tm_s + 32 * (chunk0 + i0);
+    weights(x[0], at);
+    if (chunks > 1) weights(x[1], at + 32);
   }
-  if constexpr (kN < 4) {
+  if (chunks < 4) {
     const uint32_t zero[16] = {};
 #pragma unroll
-    for (int c = 0; c < 4; c += kN) {
-      if (c != chunk0) {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          tm_st16(tm_s + 32 * (c + i), zero);
-          if (fine) tm_st16(tm_s + 32 * (c + i) + 16, zero);
-        }
+    for (int c = 0; c < 4; ++c) {
+      if ((c & -chunks) != chunk0) {
+        tm_st16(tm_s + 32 * c, zero);
+        if (fine) tm_st16(tm_s + 32 * c + 16, zero);
       }
     }
   }
@@ -790,23 +805,26 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
           }
           constexpr int kChunks = kD / 16;  // 16 payload bytes each
           const uint8_t* raw_tiles = attn_smem + (2 + Sh::kSlots) * Sh::kTileBytes;
-          const int c = t % kChunks;
+          // eight lanes take four 16-byte pieces of two rows: their stores fall
+          // on different banks
           bool found = false;
-          constexpr int kRows = kPrepThreads / kChunks;  // rows of one pass
+          constexpr int kRows = kPrepThreads / 4;        // rows of one pass
           constexpr int kBatch = 4;                      // passes whose loads are under way at once
 #pragma unroll 1
-          for (int i0 = 0; i0 < kTile / kRows; i0 += kBatch) {
+          for (int i0 = 0; i0 < kTile * kChunks / kPrepThreads; i0 += kBatch) {
             uint4 in4[kBatch];
             uint32_t byte[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-              const int row = (i0 + i) * kRows + t / kChunks;
+              const int n = i0 + i, row = n / (kChunks / 4) * kRows + t / 4;
+              const int c = n % (kChunks / 4) * 4 + t % 4;
               in4[i] = *reinterpret_cast<const uint4*>(raw_tiles + r * Sh::kRawBytes + row * kD + c * 16);
               byte[i] = ctl.raw_scale[r][row];
             }
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-              const int row = (i0 + i) * kRows + t / kChunks;
+              const int n = i0 + i, row = n / (kChunks / 4) * kRows + t / 4;
+              const int c = n % (kChunks / 4) * 4 + t % 4;
               const int pos = p0 + row;
               if (is_v && pos >= seg.ctx && (pos >= seg.len || byte[i] == 255)) {
                 found |= pos < seg.len;
@@ -905,7 +923,24 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
     // barrier's next parity
     uint32_t last_tail = 0, full_phase = 0, tail_phase = 0;
     bool ok = true;
+    const int piece = lane / kBoxCols, half = lane % kBoxCols;
     while (ok && walk.next(seg)) {
+      // A lane's page and slot of a tile's piece, looked up a tile ahead (K of
+      // tile j + 1 before that of tile j is sent) and kept for V, which is at
+      // most two tiles behind.
+      int pages[4], slots[4];
+      auto look_up = [&](int j) {
+        const int pos = (seg.tile0 + j) * kTile + piece * box_rows;
+        int page = 0, at = 0;
+        if (j < seg.tiles && lane < boxes && pos < seg.len) page = page_of(a, seg, pos, &at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((j & 3) == i) {
+            pages[i] = page;
+            slots[i] = at;
+          }
+      };
+      look_up(0);
       for_items(seg.tiles, lead_of(seg), [&](bool is_v, int j) {
         const uint32_t slot = item % kRing, phase = (item / kRing) & 1u;
         if (!warp_wait(&empty[slot], phase ^ 1u, &ctl.abort_flag)) {
@@ -922,10 +957,15 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
           mbar_arrive_expect_tx(bar,
                                 uint32_t((rows + box_rows - 1) / box_rows) * kBoxCols * box_bytes);
         __syncwarp();
-        const int piece = lane / kBoxCols, half = lane % kBoxCols;
+        int page = 0, at = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((j & 3) == i) {
+            page = pages[i];
+            at = slots[i];
+          }
+        if (!is_v) look_up(j + 1);
         if (lane < boxes && piece * box_rows < rows) {
-          int at;
-          const int page = page_of(a, seg, p0 + piece * box_rows, &at);
           if (page < 0 || page >= a.cache.num_pages) status |= FCT_DEV_INDEX_OUT_OF_RANGE;
           const uint32_t dst = ring0 + slot * kItemBytes +
                                (kFp8 ? uint32_t(piece) * box_bytes
@@ -949,7 +989,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
     // it in uniform registers)
     constexpr uint32_t kIdS = attn_idesc(kTile, false), kIdO = attn_idesc(kD, true);
     uint32_t item = 0, seg_n = 0, full_phase = 0, prep_phase = 0;
-    uint32_t p_n[2] = {0, 0};
+    uint32_t p_phase = 0;
     bool ok = true;
     const bool issue = elect_one();
     auto slot_addr = [&](uint32_t it) { return uniform(slot0 + (it % Sh::kSlots) * Sh::kTileBytes); };
@@ -994,8 +1034,8 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
       __syncwarp();
     };
     auto wait_p = [&](int w) {
-      const bool got = warp_wait(&ctl.p_full[w], p_n[w] & 1u, &ctl.abort_flag);
-      ++p_n[w];
+      const bool got = warp_wait(&ctl.p_full[w], (p_phase >> w) & 1u, &ctl.abort_flag);
+      p_phase ^= 1u << w;
       return got;
     };
     auto wait_v = [&](uint32_t it, int tile) {
@@ -1009,44 +1049,31 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
       const bool two = seg.rows > kTile;
       if (!warp_wait(&ctl.q_full, seg_n & 1u, &ctl.abort_flag)) break;
       ++seg_n;
-      if (two) {
-        uint32_t k_item = item++;
-        ok = wait_item(k_item);
-        if (!ok) break;
-        scores(0, 0, k_item, false);
-        scores(1, 1, k_item, true);
-        for (int j = 0; ok && j < seg.tiles; ++j) {
-          const uint32_t v_item = item++;
-          const bool more = j + 1 < seg.tiles;
-          if (more) k_item = item++;
-          ok = wait_v(v_item, seg.tile0 + j) && wait_p(0);
-          if (!ok) break;
-          values(0, v_item, j == 0, false);
-          if (more) {
-            ok = wait_item(k_item);
-            if (!ok) break;
-            scores(0, 0, k_item, false);
-          }
-          ok = wait_p(1);
-          if (!ok) break;
-          values(1, v_item, j == 0, true);
-          if (more) scores(1, 1, k_item, true);
-        }
-      } else {
-        for (int j = 0; ok && j < 2 && j < seg.tiles; ++j) {
-          const uint32_t k_item = item++;
+      uint32_t k_item = 0;
+#pragma unroll 1
+      for (int w = 0; ok && w < (two ? 2 : min(2, seg.tiles)); ++w) {
+        if (!two || w == 0) {
+          k_item = item++;
           ok = wait_item(k_item);
-          if (ok) scores(j, 0, k_item, true);
         }
-        for (int j = 0; ok && j < seg.tiles; ++j) {
-          const uint32_t v_item = item++;
-          ok = wait_v(v_item, seg.tile0 + j) && wait_p(j & 1);
+        if (ok) scores(w, two ? w : 0, k_item, !two || w == 1);
+      }
+      const int lead = lead_of(seg), last = two ? 1 : 0;
+#pragma unroll 1
+      for (int j = 0; ok && j < seg.tiles; ++j) {
+        const uint32_t v_item = item++;
+        const bool more = j + lead < seg.tiles;
+        if (more) k_item = item++;
+        ok = wait_v(v_item, seg.tile0 + j);
+#pragma unroll 1
+        for (int u = 0; ok && u <= last; ++u) {
+          const int w = two ? u : j & 1;
+          ok = wait_p(w);
           if (!ok) break;
-          values(j & 1, v_item, j < 2, true);
-          if (j + 2 < seg.tiles) {
-            const uint32_t k_item = item++;
-            ok = wait_item(k_item);
-            if (ok) scores(j & 1, 0, k_item, true);
+          values(w, v_item, j < lead, u == last);
+          if (more) {
+            if (u == 0) ok = wait_item(k_item);
+            if (ok) scores(w, two ? u : 0, k_item, u == last);
           }
         }
       }
@@ -1172,22 +1199,8 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
         if (warp_live) {
           const int p0 = (seg.tile0 + j) * kTile + 32 * chunk0;
           const bool tail = is_tail(seg, seg.tile0 + j);
-          auto take = [&](auto count) {
-            constexpr int kN = decltype(count)::value;
-            uint32_t vis[kN];
-            if (tail) {
-#pragma unroll
-              for (int i = 0; i < kN; ++i) vis[i] = live ? visible32(a, seg, node, p0 + 32 * i) : 0u;
-              __syncwarp();
-            }
-            soft_tile<kD, kN>(tm_s, tm_o + uint32_t(w) * kD, chunk0, tail, vis, fine, first, sl2, m, l);
-          };
-          if (span == 32)
-            take(std::integral_constant<int, 1>());
-          else if (span == 64)
-            take(std::integral_constant<int, 2>());
-          else
-            take(std::integral_constant<int, 4>());
+          soft_tile<kD>(a, seg, tm_s, tm_o + uint32_t(w) * kD, chunk0, span / 32, node, live, p0, tail,
+                        fine, first, sl2, m, l);
         }
         first = false;
         tc_before();
