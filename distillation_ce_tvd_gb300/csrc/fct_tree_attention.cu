@@ -210,20 +210,20 @@ constexpr float kLazyLog2 = 8.f;  // O is rescaled when the maximum grows by mor
 template <int kD, bool kFp8>
 struct AttnShape {
   // Warps: 0 loads, 1 products, 4-11 softmax; e4m3: 2 and 3 fetch scale bytes,
-  // 12-15 prepare; bf16: 2 and 3 prepare.
+  // 12-15 prepare; bf16: 2 prepares, 3 loads V (0 loads K).
   static constexpr int kThreads = kFp8 ? 512 : 384;
-  static constexpr int kPrepWarp0 = kFp8 ? 12 : 2, kPrepWarps = kFp8 ? 4 : 2;
+  static constexpr int kPrepWarp0 = kFp8 ? 12 : 2, kPrepWarps = kFp8 ? 4 : 1;
   // Registers per thread of warps 0-3, the softmax groups and warps 12-15,
   // moved between the warp groups: together what the kernel is launched with,
   // 65536 / kThreads each (in eights).
   static constexpr int kLaunchRegs = kFp8 ? 128 : 168;
-  static constexpr int kLowRegs = kFp8 ? 104 : 120, kSoftRegs = kFp8 ? 152 : 192;
+  static constexpr int kLowRegs = kFp8 ? 80 : 120, kSoftRegs = kFp8 ? 176 : 192;
   static_assert((kFp8 ? 2 : 1) * kLowRegs + 2 * kSoftRegs <= kThreads / 128 * kLaunchRegs, "registers");
   static constexpr int kHalves = kD / 64;  // 128-byte column blocks of a bf16 row
   static constexpr uint32_t kTileBytes = kTile * kD * 2;
   static constexpr uint32_t kRawBytes = kTile * kD;
   static constexpr int kSlots = kD == 128 ? (kFp8 ? 3 : 5) : (kFp8 ? 4 : 8);
-  static constexpr int kRing = kFp8 ? (kD == 128 ? 4 : 8) : 1;
+  static constexpr int kRing = kFp8 ? (kD == 128 ? 4 : 8) : 1;  // raw slots (1 where unused)
   static constexpr int kRaw = kFp8 ? (kD == 128 ? 4 : 8) : 0;
   static constexpr size_t kTilesBytes =
       2 * kTileBytes + size_t(kSlots) * kTileBytes + size_t(kRaw) * kRawBytes;
@@ -657,8 +657,8 @@ __device__ __forceinline__ void soft_tile(const AttnArgs& a, const Segment& seg,
     }
   };
 #pragma unroll 1
-  for (int i0 = 0; i0 < chunks; i0 += 2) {
-    if (chunks > 2) load(i0);
+  for (int i0 = chunks > 2 ? 2 : 0; i0 >= 0; i0 -= 2) {  // the last two are still held
+    if (chunks > 2 && i0 == 0) load(i0);
     const uint32_t at = tm_s + 32 * (chunk0 + i0);
     weights(x[0], at);
     if (chunks > 1) weights(x[1], at + 32);
@@ -780,6 +780,97 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
   auto lead_of = [](const Segment& s) { return s.rows > kTile ? 1 : 2; };
   // whether a key tile (index in the unit) reaches past the context
   auto is_tail = [](const Segment& s, int tile) { return (tile + 1) * kTile > s.ctx; };
+
+  // ---- loads: a warp sends K tiles, V tiles or both, its lanes a tile's boxes
+  auto load_tiles = [&](bool do_k, bool do_v) {
+    constexpr int kBoxCols = kFp8 ? 1 : Sh::kHalves;
+    constexpr int kRing = kFp8 ? Sh::kRaw : Sh::kSlots;
+    uint64_t* full = kFp8 ? ctl.raw_full : ctl.full_bar;
+    uint64_t* empty = kFp8 ? ctl.raw_empty : ctl.empty_bar;
+    const uint32_t ring0 = kFp8 ? raw0 : slot0;
+    constexpr uint32_t kItemBytes = kFp8 ? Sh::kRawBytes : Sh::kTileBytes;
+    const int boxes = kTile / box_rows * kBoxCols;
+    const uint32_t box_bytes = uint32_t(box_rows) * (kFp8 ? kD : 128);
+    const int page_size = a.cache.page_size;
+    uint32_t item = 0;
+    // per slot: the barrier of its last fill (1: tail_full), and each
+    // barrier's next parity, both warps' fills counted
+    uint32_t last_tail = 0, full_phase = 0, tail_phase = 0;
+    bool ok = true;
+    const int piece = lane / kBoxCols, half = lane % kBoxCols;
+    while (ok && walk.next(seg)) {
+      // The lane's piece of tile `next`: its place in the block table, and its
+      // page, asked for a tile ahead of its use.  A tile's page is kept for V,
+      // which is sent at most two tiles after K.
+      const int32_t* table = a.pages.table + seg.b * a.pages.ld;
+      int pos = seg.tile0 * kTile + piece * box_rows;
+      int in_table = pos / page_size, in_page = pos - in_table * page_size;
+      int next = 0, asked_page = 0, asked_at = 0;
+      int pages[4] = {0, 0, 0, 0}, slots[4] = {0, 0, 0, 0};
+      auto ask = [&]() {
+        asked_at = in_page;
+        asked_page = 0;
+        if (next < seg.tiles && lane < boxes && pos < seg.len) asked_page = table[in_table];
+        ++next;
+        pos += kTile;
+        in_page += kTile % page_size;
+        in_table += kTile / page_size;
+        if (in_page >= page_size) {
+          in_page -= page_size;
+          ++in_table;
+        }
+      };
+      ask();
+      for_items(seg.tiles, lead_of(seg), [&](bool is_v, int j) {
+        const uint32_t slot = item % kRing, phase = (item / kRing) & 1u;
+        ++item;
+        const bool prep = !kFp8 && is_v && is_tail(seg, seg.tile0 + j);
+        last_tail = (last_tail & ~(1u << slot)) | (uint32_t(prep) << slot);
+        (prep ? tail_phase : full_phase) ^= 1u << slot;
+        if (!is_v) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((j & 3) == i) {
+              pages[i] = asked_page;
+              slots[i] = asked_at;
+            }
+          ask();
+        }
+        if (!(is_v ? do_v : do_k)) return true;
+        if (!warp_wait(&empty[slot], phase ^ 1u, &ctl.abort_flag)) {
+          ok = false;
+          return false;
+        }
+        uint64_t* bar = prep ? &ctl.tail_full[slot] : &full[slot];
+        const int rows = min(seg.len - (seg.tile0 + j) * kTile, kTile);
+        if (lane == 0)
+          mbar_arrive_expect_tx(bar, uint32_t((rows + box_rows - 1) / box_rows) * kBoxCols * box_bytes);
+        __syncwarp();
+        if (lane < boxes && piece * box_rows < rows) {
+          int page = 0, at = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((j & 3) == i) {
+              page = pages[i];
+              at = slots[i];
+            }
+          if (page < 0 || page >= a.cache.num_pages) status |= FCT_DEV_INDEX_OUT_OF_RANGE;
+          const uint32_t dst = ring0 + slot * kItemBytes +
+                               (kFp8 ? uint32_t(piece) * box_bytes
+                                     : uint32_t(half) * (kTile * 128) + uint32_t(piece) * box_bytes);
+          tma_box(dst, is_v ? &map_v : &map_k, half * 64, at, seg.h, page, bar);
+        }
+        return true;
+      });
+    }
+    // the last fills have landed before the CTA ends (bounded, even after an
+    // abort)
+    for (uint32_t slot = 0; slot < uint32_t(kRing) && slot < item; ++slot) {
+      const bool tail = (last_tail >> slot) & 1u;
+      wait_phase(tail ? &ctl.tail_full[slot] : &full[slot],
+                 (((tail ? tail_phase : full_phase) >> slot) & 1u) ^ 1u, &ctl.abort_flag, false);
+    }
+  };
 
   auto prepare = [&]() {
     // ---- tiles prepared
@@ -909,80 +1000,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
   if (warp < 4) {
     fewer_registers<Sh::kLowRegs>();
     if (warp == 0) {
-    // ---- loads: the warp's lanes take a tile's boxes
-    constexpr int kBoxCols = kFp8 ? 1 : Sh::kHalves;
-    constexpr int kRing = kFp8 ? Sh::kRaw : Sh::kSlots;
-    uint64_t* full = kFp8 ? ctl.raw_full : ctl.full_bar;
-    uint64_t* empty = kFp8 ? ctl.raw_empty : ctl.empty_bar;
-    const uint32_t ring0 = kFp8 ? raw0 : slot0;
-    constexpr uint32_t kItemBytes = kFp8 ? Sh::kRawBytes : Sh::kTileBytes;
-    const int boxes = kTile / box_rows * kBoxCols;
-    const uint32_t box_bytes = uint32_t(box_rows) * (kFp8 ? kD : 128);
-    uint32_t item = 0;
-    // per slot: the barrier of its last fill (1: tail_full), and each
-    // barrier's next parity
-    uint32_t last_tail = 0, full_phase = 0, tail_phase = 0;
-    bool ok = true;
-    const int piece = lane / kBoxCols, half = lane % kBoxCols;
-    while (ok && walk.next(seg)) {
-      // A lane's page and slot of a tile's piece, looked up a tile ahead (K of
-      // tile j + 1 before that of tile j is sent) and kept for V, which is at
-      // most two tiles behind.
-      int pages[4], slots[4];
-      auto look_up = [&](int j) {
-        const int pos = (seg.tile0 + j) * kTile + piece * box_rows;
-        int page = 0, at = 0;
-        if (j < seg.tiles && lane < boxes && pos < seg.len) page = page_of(a, seg, pos, &at);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if ((j & 3) == i) {
-            pages[i] = page;
-            slots[i] = at;
-          }
-      };
-      look_up(0);
-      for_items(seg.tiles, lead_of(seg), [&](bool is_v, int j) {
-        const uint32_t slot = item % kRing, phase = (item / kRing) & 1u;
-        if (!warp_wait(&empty[slot], phase ^ 1u, &ctl.abort_flag)) {
-          ok = false;
-          return false;
-        }
-        const bool prep = !kFp8 && is_v && is_tail(seg, seg.tile0 + j);
-        uint64_t* bar = prep ? &ctl.tail_full[slot] : &full[slot];
-        last_tail = (last_tail & ~(1u << slot)) | (uint32_t(prep) << slot);
-        (prep ? tail_phase : full_phase) ^= 1u << slot;
-        const int p0 = (seg.tile0 + j) * kTile;
-        const int rows = min(seg.len - p0, kTile);
-        if (lane == 0)
-          mbar_arrive_expect_tx(bar,
-                                uint32_t((rows + box_rows - 1) / box_rows) * kBoxCols * box_bytes);
-        __syncwarp();
-        int page = 0, at = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if ((j & 3) == i) {
-            page = pages[i];
-            at = slots[i];
-          }
-        if (!is_v) look_up(j + 1);
-        if (lane < boxes && piece * box_rows < rows) {
-          if (page < 0 || page >= a.cache.num_pages) status |= FCT_DEV_INDEX_OUT_OF_RANGE;
-          const uint32_t dst = ring0 + slot * kItemBytes +
-                               (kFp8 ? uint32_t(piece) * box_bytes
-                                     : uint32_t(half) * (kTile * 128) + uint32_t(piece) * box_bytes);
-          tma_box(dst, is_v ? &map_v : &map_k, half * 64, at, seg.h, page, bar);
-        }
-        ++item;
-        return true;
-      });
-    }
-    // the last fills have landed before the CTA ends (bounded, even after an
-    // abort)
-    for (uint32_t slot = 0; slot < uint32_t(kRing) && slot < item; ++slot) {
-      const bool tail = (last_tail >> slot) & 1u;
-      wait_phase(tail ? &ctl.tail_full[slot] : &full[slot],
-                (((tail ? tail_phase : full_phase) >> slot) & 1u) ^ 1u, &ctl.abort_flag, false);
-    }
+      load_tiles(true, kFp8);
     } else if (warp == 1) {
     // ---- products: the warp goes through the tiles converged, one lane
     // issues (what the issue needs is then the same in all lanes, which keeps
@@ -1122,8 +1140,10 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
       });
     }
     if (ok && holds) hand_on();
-    } else {
+    } else if (warp == 2) {
       prepare();
+    } else {
+      load_tiles(false, true);
     }
   } else if (warp < 12) {
     more_registers<Sh::kSoftRegs>();
