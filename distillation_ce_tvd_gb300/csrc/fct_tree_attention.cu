@@ -235,11 +235,8 @@ struct AttnShape {
     uint64_t tail_full[kSlots], prep_bar[kSlots];
     uint64_t raw_full[kRaw + 1], raw_scaled[kRaw + 1], raw_empty[kRaw + 1];
     uint64_t s_full[2], p_full[2], q_full, o_full, ml_full, done_bar;
-    int64_t sched[2];
-    union {
-      int64_t scan[kThreads / 32];  // while the schedule is made
-      float2 ml[2][kTile];          // the groups' maxima and sums, lane by lane
-    };
+    int64_t sched[4];     // the run: request, offset in it, length; whether units are whole
+    float2 ml[2][kTile];  // the groups' maxima and sums, lane by lane
     uint32_t tmem_base;
     int abort_flag;
     int bad_seg[kBadRing];
@@ -270,8 +267,8 @@ struct RequestShape {
   int node0, nodes;
   int ctx, len, tiles;
   int row_units;
+  int last_rows;  // of its last row unit; the others have kUnitRows
   bool bad;
-  __device__ __forceinline__ int64_t work(int heads) const { return int64_t(tiles) * row_units * heads; }
 };
 
 __device__ __forceinline__ RequestShape request_shape(const AttnArgs& a, const AttnDims& d, int64_t b) {
@@ -290,53 +287,153 @@ __device__ __forceinline__ RequestShape request_shape(const AttnArgs& a, const A
   r.bad = r.bad || (len > d.room && r.nodes > 0);
   r.len = len > d.room ? d.room : static_cast<int>(len);
   r.tiles = (r.len + kTile - 1) / kTile;
-  r.row_units = static_cast<int>((int64_t(r.nodes) * d.group + kUnitRows - 1) / kUnitRows);
+  const int rows = r.nodes * d.group;
+  r.row_units = (rows + kUnitRows - 1) / kUnitRows;
+  r.last_rows = rows - (r.row_units - 1) * kUnitRows;
   return r;
 }
 
-// How many CTAs share `total` tiles (each gets one at least), the first tile
-// of CTA c's run, and whose run a tile is in.
-__device__ __forceinline__ int64_t run_count(int64_t total, int64_t ctas) {
-  return total < ctas ? total : ctas;
+// What the deal counts.  A unit costs kUnitCost for its start and end (as
+// measured, in key tiles of 128 rows) and each of its key tiles 1, or 2 with
+// both query tiles; the sum over all units is dealt in equal runs.  Where no
+// request has more than kWholeTiles tiles, a unit counts 1 and is never cut: a
+// second CTA would save less than combining costs.
+constexpr int kUnitCost = 3, kWholeTiles = 4, kMinRun = kUnitCost + 1;
+
+struct Deal {
+  bool whole;
+  // of a unit with `rows` rows of a request with `tiles` tiles
+  __device__ __forceinline__ int per_tile(int rows) const { return rows > kTile ? 2 : 1; }
+  __device__ __forceinline__ int64_t unit(int tiles, int rows) const {
+    return whole ? 1 : kUnitCost + int64_t(tiles) * per_tile(rows);
+  }
+  __device__ __forceinline__ int64_t head(const RequestShape& r) const {
+    return r.row_units == 0 ? 0
+                            : (r.row_units - 1) * unit(r.tiles, kUnitRows) + unit(r.tiles, r.last_rows);
+  }
+  __device__ __forceinline__ int64_t request(const RequestShape& r, int heads) const {
+    return r.tiles == 0 ? 0 : head(r) * heads;
+  }
+  // The first tile that starts at cost x of the unit or later.
+  __device__ __forceinline__ int tile_at(int64_t x, int tiles, int rows) const {
+    if (x <= 0 || (!whole && x <= kUnitCost)) return 0;
+    if (whole) return tiles;
+    const int per = per_tile(rows);
+    const int64_t n = (x - kUnitCost + per - 1) / per;
+    return n < tiles ? static_cast<int>(n) : tiles;
+  }
+  // How many CTAs share `total`, and where CTA c's run starts.
+  __device__ __forceinline__ int64_t runs(int64_t total, int64_t ctas) const {
+    const int64_t most = whole ? total : (total + kMinRun - 1) / kMinRun;
+    return most < ctas ? most : ctas;
+  }
+  __device__ __forceinline__ static int64_t run_start(int64_t total, int64_t runs, int64_t c) {
+    return c >= runs ? total : total * c / runs;
+  }
+  // Whose run cost x is in.
+  __device__ __forceinline__ static int64_t run_of(int64_t total, int64_t runs, int64_t x) {
+    return ((x + 1) * runs - 1) / total;
+  }
+};
+
+// A warp's view of the whole batch: the deal, its total, and for one cost
+// `find` the request it falls in and the offset there.
+struct Batch {
+  Deal deal;
+  int64_t total;
+  bool bad;
+};
+__device__ __forceinline__ Batch batch_of(const AttnArgs& a, const AttnDims& d) {
+  const int lane = threadIdx.x & 31;
+  int most = 0;
+  int64_t cost[2] = {0, 0};
+  bool bad = false;
+#pragma unroll 2
+  for (int64_t b = lane; b < a.pages.batch; b += 32) {
+    const RequestShape r = request_shape(a, d, b);
+    bad |= r.bad;
+    if (r.nodes > 0) most = max(most, r.tiles);
+    cost[0] += Deal{false}.request(r, a.cache.n_heads);
+    cost[1] += Deal{true}.request(r, a.cache.n_heads);
+  }
+#pragma unroll
+  for (int k = 16; k >= 1; k >>= 1) {
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, k));
+    cost[0] += __shfl_xor_sync(0xffffffffu, cost[0], k);
+    cost[1] += __shfl_xor_sync(0xffffffffu, cost[1], k);
+  }
+  const bool whole = most <= kWholeTiles;
+  return Batch{Deal{whole}, cost[whole ? 1 : 0], __any_sync(0xffffffffu, bad) != 0};
 }
-__device__ __forceinline__ int64_t run_start(int64_t total, int64_t runs, int64_t c) {
-  return c >= runs ? total : total * c / runs;
-}
-__device__ __forceinline__ int64_t run_of(int64_t total, int64_t runs, int64_t tile) {
-  return ((tile + 1) * runs - 1) / total;
+// f(before, cost, b, shape) for the request of every lane, 32 at a time,
+// until f says (to the whole warp) that it has what it looked for.
+template <typename F>
+__device__ __forceinline__ void scan_requests(const AttnArgs& a, const AttnDims& d, const Deal& deal, F f) {
+  const int lane = threadIdx.x & 31;
+  int64_t before = 0;
+  for (int64_t b0 = 0; b0 < a.pages.batch; b0 += 32) {
+    const int64_t b = b0 + lane;
+    RequestShape r{};
+    int64_t w = 0;
+    if (b < a.pages.batch) {
+      r = request_shape(a, d, b);
+      w = deal.request(r, a.cache.n_heads);
+    }
+    int64_t incl = w;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, incl, k);
+      if (lane >= k) incl += o;
+    }
+    if (f(before + incl - w, w, b, r)) return;
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
 }
 
 // Walks the segments of a CTA's run; every role of the CTA walks the same.
 struct SegmentWalk {
   const AttnArgs& a;
   const AttnDims& d;
-  int64_t b, off, left;
+  Deal deal;
+  int b;
+  int64_t off, left;  // cost into request b, and of the run's rest
+  RequestShape r;     // of request b
+  __device__ __forceinline__ SegmentWalk(const AttnArgs& a_, const AttnDims& d_, Deal deal_, int64_t b_,
+                                         int64_t off_, int64_t left_)
+      : a(a_), d(d_), deal(deal_), b(static_cast<int>(b_)), off(off_), left(left_) {
+    if (left > 0) r = request_shape(a, d, b);
+  }
   __device__ __forceinline__ bool next(Segment& s) {
-    if (left <= 0) return false;
-    RequestShape r = request_shape(a, d, b);
-    int64_t w = r.work(a.cache.n_heads);
-    while (off >= w) {
-      off = 0;
-      if (++b >= a.pages.batch) return false;
-      r = request_shape(a, d, b);
-      w = r.work(a.cache.n_heads);
+    while (left > 0) {
+      const int64_t w = deal.request(r, a.cache.n_heads);
+      if (off >= w) {
+        off = 0;
+        if (++b >= a.pages.batch) return false;
+        r = request_shape(a, d, b);
+        continue;
+      }
+      const int64_t head = deal.head(r), full = deal.unit(r.tiles, kUnitRows);
+      s.h = static_cast<int>(off / head);
+      const int64_t in_head = off - s.h * head;
+      const int u = static_cast<int>(min(in_head / full, int64_t(r.row_units - 1)));
+      const int64_t x0 = in_head - u * full;
+      s.rows = u == r.row_units - 1 ? r.last_rows : kUnitRows;
+      const int64_t cost = deal.unit(r.tiles, s.rows);
+      const int64_t x1 = min(cost, x0 + left);
+      off += x1 - x0;
+      left -= x1 - x0;
+      s.b = b;
+      s.node0 = r.node0;
+      s.ctx = r.ctx;
+      s.len = r.len;
+      s.row0 = u * kUnitRows;
+      s.tile0 = deal.tile_at(x0, r.tiles, s.rows);
+      s.tiles = (x1 == cost ? r.tiles : deal.tile_at(x1, r.tiles, s.rows)) - s.tile0;
+      s.whole = s.tiles == r.tiles;
+      s.part = s.tile0 > 0 ? 0 : 1;
+      if (s.tiles > 0) return true;
     }
-    const int64_t unit = off / r.tiles;
-    s.b = static_cast<int>(b);
-    s.node0 = r.node0;
-    s.ctx = r.ctx;
-    s.len = r.len;
-    s.h = static_cast<int>(unit / r.row_units);
-    s.row0 = static_cast<int>(unit % r.row_units) * kUnitRows;
-    s.rows = min(r.nodes * d.group - s.row0, kUnitRows);
-    s.tile0 = static_cast<int>(off - unit * r.tiles);
-    const int n = r.tiles - s.tile0 < left ? r.tiles - s.tile0 : static_cast<int>(left);
-    s.tiles = n;
-    s.whole = n == r.tiles;
-    s.part = s.tile0 > 0 ? 0 : 1;
-    off += n;
-    left -= n;
-    return true;
+    return false;
   }
 };
 
@@ -729,54 +826,34 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
 
-  // The schedule: the sum of all requests' tiles, then the request and the
-  // offset in it where this CTA's run starts.
-  bool bad_request = false;
-  int64_t total = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    int64_t before = 0;
-    const int64_t start = pass ? run_start(total, run_count(total, gridDim.x), blockIdx.x) : -1;
-    for (int64_t b0 = 0; b0 < a.pages.batch; b0 += Sh::kThreads) {
-      const int64_t b = b0 + threadIdx.x;
-      int64_t w = 0;
-      if (b < a.pages.batch) {
-        const RequestShape r = request_shape(a, d, b);
-        w = r.work(a.cache.n_heads);
-        bad_request |= r.bad;
-      }
-      int64_t incl = w;
-#pragma unroll
-      for (int k = 1; k < 32; k <<= 1) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, incl, k);
-        if (lane >= k) incl += o;
-      }
-      __syncthreads();
-      if (lane == 31) ctl.scan[warp] = incl;
-      __syncthreads();
-      int64_t base = before, all = 0;
-      for (int i = 0; i < Sh::kThreads / 32; ++i) {
-        if (i < warp) base += ctl.scan[i];
-        all += ctl.scan[i];
-      }
-      if (pass && w > 0 && base + incl - w <= start && start < base + incl) {
-        ctl.sched[0] = b;
-        ctl.sched[1] = start - (base + incl - w);
-      }
-      before += all;
+  int32_t status = 0;
+  if (warp == 2) {
+    // the deal: this CTA's run, as the request and the offset in it where it starts
+    const Batch batch = batch_of(a, d);
+    if (batch.bad && blockIdx.x == 0 && lane == 0) status |= FCT_DEV_INDEX_OUT_OF_RANGE;
+    const int64_t runs = batch.deal.runs(batch.total, gridDim.x);
+    const int64_t run0 = Deal::run_start(batch.total, runs, blockIdx.x);
+    const int64_t run1 = Deal::run_start(batch.total, runs, blockIdx.x + 1);
+    if (lane == 0) {
+      ctl.sched[2] = run1 - run0;
+      ctl.sched[3] = batch.deal.whole;
     }
-    total = before;
+    if (run1 > run0)
+      scan_requests(a, d, batch.deal, [&](int64_t before, int64_t cost, int64_t b, const RequestShape&) {
+        const bool here = cost > 0 && before <= run0 && run0 < before + cost;
+        if (here) {
+          ctl.sched[0] = b;
+          ctl.sched[1] = run0 - before;
+        }
+        return __any_sync(0xffffffffu, here) != 0;
+      });
   }
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tmem = ctl.tmem_base;
-  const int64_t runs = run_count(total, gridDim.x);
-  const int64_t run0 = run_start(total, runs, blockIdx.x);
-  const int64_t run1 = run_start(total, runs, blockIdx.x + 1);
-  SegmentWalk walk{a, d, run1 > run0 ? ctl.sched[0] : 0, run1 > run0 ? ctl.sched[1] : 0, run1 - run0};
+  SegmentWalk walk(a, d, Deal{ctl.sched[3] != 0}, ctl.sched[0], ctl.sched[1], ctl.sched[2]);
   Segment seg;
-  int32_t status = 0;
-  if (bad_request && blockIdx.x == 0) status |= FCT_DEV_INDEX_OUT_OF_RANGE;
   auto lead_of = [](const Segment& s) { return s.rows > kTile ? 1 : 2; };
   // whether a key tile (index in the unit) reaches past the context
   auto is_tail = [](const Segment& s, int tile) { return (tile + 1) * kTile > s.ctx; };
@@ -958,35 +1035,43 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
             return false;
           }
           tail_phase ^= 1u << slot;
-          for (int row = t; row < kTile; row += kPrepThreads) {
-            const int pos = p0 + row;
-            if (pos < seg.ctx) continue;
-            const bool past = pos >= seg.len;
-            bool found = false;
-            for (int c = 0; c < kD / 8; ++c) {
-              const uint32_t at = dst + uint32_t(c / 8) * (kTile * 128) + uint32_t(row) * 128 +
-                                  uint32_t(((c % 8) ^ (row & 7)) * 16);
-              uint32_t w[4];
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                           : "r"(at));
-              bool change = past;
+          // 16-byte pieces of the rows past the context, several under way at once
+          constexpr int kPieces = kD / 8, kBatch = 8;
+          const int from = max(seg.ctx - p0, 0);
+          const int held = min(seg.len - p0, kTile);  // rows from here on are cleared
+          uint8_t* tile_at = attn_smem + (2 + slot) * Sh::kTileBytes;
+          auto place = [&](int n) {
+            const int row = n / kPieces, c = n % kPieces;
+            return reinterpret_cast<uint4*>(tile_at + (c / 8) * (kTile * 128) + row * 128 + ((c % 8) ^ (row & 7)) * 16);
+          };
+          bool found = false;
+          for (int n0 = from * kPieces + t; n0 < held * kPieces; n0 += kPrepThreads * kBatch) {
+            uint4 v[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+              if (n0 + i * kPrepThreads < held * kPieces) v[i] = *place(n0 + i * kPrepThreads);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              if (n0 + i * kPrepThreads >= held * kPieces) continue;
+              uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+              bool change = false;
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const bool lo = (w[k] & 0x7f80u) == 0x7f80u, hi = (w[k] & 0x7f800000u) == 0x7f800000u;
                 change |= lo || hi;
-                if (past || lo) w[k] &= 0xffff0000u;
-                if (past || hi) w[k] &= 0x0000ffffu;
+                if (lo) w[k] &= 0xffff0000u;
+                if (hi) w[k] &= 0x0000ffffu;
               }
               if (change) {
-                found |= !past;
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]),
-                             "r"(w[2]), "r"(w[3])
-                             : "memory");
+                found = true;
+                *place(n0 + i * kPrepThreads) = make_uint4(w[0], w[1], w[2], w[3]);
               }
             }
-            if (found) ctl.bad_seg[seg_n % kBadRing] = seg_n;
           }
+#pragma unroll 4
+          for (int n = max(from, held) * kPieces + t; n < kTile * kPieces; n += kPrepThreads)
+            *place(n) = make_uint4(0, 0, 0, 0);
+          if (found) ctl.bad_seg[seg_n % kBadRing] = seg_n;
           async_fence();
           warp_arrive(&ctl.prep_bar[slot]);
         }
@@ -1184,21 +1269,31 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
         const uint16_t* src = static_cast<const uint16_t*>(a.q) + int64_t(seg.node0 + node) * a.ld_qn +
                               int64_t(head) * a.ld_qh;
         const uint32_t dst = smem0 + (two ? uint32_t(w) * Sh::kTileBytes : 0u) + uint32_t(r) * 128;
-        const int c0 = two ? 0 : w * (kD / 16), c1 = two ? kD / 8 : c0 + kD / 16;
-        for (int c = c0; c < c1; ++c) {
-          uint32_t x[4];
+        // half of a row at a time, all its loads under way at once
+        constexpr int kHalf = kD / 16;
+#pragma unroll 1
+        for (int c0 = two ? 0 : w * kHalf; c0 < (two ? kD / 8 : (w + 1) * kHalf); c0 += kHalf) {
+          uint4 x[kHalf];
           if (vec_q) {
-            const uint4 v = *reinterpret_cast<const uint4*>(src + c * 8);
-            x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+#pragma unroll
+            for (int c = 0; c < kHalf; ++c) x[c] = *reinterpret_cast<const uint4*>(src + (c0 + c) * 8);
           } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              x[k] = uint32_t(src[c * 8 + 2 * k]) | (uint32_t(src[c * 8 + 2 * k + 1]) << 16);
+            for (int c = 0; c < kHalf; ++c) {
+              uint32_t y[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                y[k] = uint32_t(src[(c0 + c) * 8 + 2 * k]) | (uint32_t(src[(c0 + c) * 8 + 2 * k + 1]) << 16);
+              x[c] = make_uint4(y[0], y[1], y[2], y[3]);
+            }
           }
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           dst + uint32_t(c / 8) * (kTile * 128) + uint32_t(((c % 8) ^ (r & 7)) * 16)),
-                       "r"(x[0] ^ flip), "r"(x[1] ^ flip), "r"(x[2] ^ flip), "r"(x[3] ^ flip)
-                       : "memory");
+#pragma unroll
+          for (int c = 0; c < kHalf; ++c)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             dst + uint32_t((c0 + c) / 8) * (kTile * 128) +
+                             uint32_t((((c0 + c) % 8) ^ (r & 7)) * 16)),
+                         "r"(x[c].x ^ flip), "r"(x[c].y ^ flip), "r"(x[c].z ^ flip), "r"(x[c].w ^ flip)
+                         : "memory");
         }
       }
       async_fence();
@@ -1379,7 +1474,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k) o[k] += x[k];
           }
-          row_sums(row_, M, L);
+          if (!slot) row_sums(row_, M, L);
           put(row_, piece * 4, o, L);
         }
         if (!meet()) break;  // before the next query rows take the place
@@ -1410,61 +1505,80 @@ template <int kD>
 __global__ void __launch_bounds__(kCombineWarps * 32)
     combine_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnDims d, int ctas,
                    int part_rows) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t item = int64_t(blockIdx.x) * kCombineWarps + warp;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (item >= a.n_nodes * a.n_q_heads) return;
+  const int lane = threadIdx.x & 31;
+  const int64_t item = int64_t(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5);
+  // Where the pieces are depends on the arguments only and is worked out while
+  // the attention kernel still runs; every thread waits for that kernel before
+  // it reads a piece or leaves.
+  const bool valid = item < a.n_nodes * a.n_q_heads;
   const int64_t node = item / a.n_q_heads;
   const int head = static_cast<int>(item % a.n_q_heads);
-  // tiles before the node's request, and all
-  int64_t total = 0, before = 0, mine = -1;
+  const Batch batch = batch_of(a, d);
+  int64_t before = 0;
   RequestShape r{};
-  for (int64_t b0 = 0; b0 < a.pages.batch; b0 += 32) {
-    const int64_t b = b0 + lane;
-    RequestShape x{};
-    int64_t w = 0;
-    if (b < a.pages.batch) {
-      x = request_shape(a, d, b);
-      w = x.work(a.cache.n_heads);
-    }
-    const unsigned here = __ballot_sync(0xffffffffu, w > 0 && node >= x.node0 && node < x.node0 + x.nodes);
-    int64_t incl = w;
-#pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-      const int64_t o = __shfl_up_sync(0xffffffffu, incl, k);
-      if (lane >= k) incl += o;
-    }
-    if (here) {
-      const int src = __ffs(here) - 1;
-      mine = b0 + src;
-      before = total + __shfl_sync(0xffffffffu, incl - w, src);
-    }
-    total += __shfl_sync(0xffffffffu, incl, 31);
-  }
-  if (mine < 0) return;
-  r = request_shape(a, d, mine);
+  bool found = false;
+  if (valid && !batch.deal.whole) scan_requests(a, d, batch.deal, [&](int64_t before_, int64_t, int64_t, const RequestShape& x) {
+    const unsigned here = __ballot_sync(0xffffffffu, node >= x.node0 && node < x.node0 + x.nodes);
+    if (!here) return false;
+    const int src = __ffs(here) - 1;
+    before = __shfl_sync(0xffffffffu, before_, src);
+    r.node0 = __shfl_sync(0xffffffffu, x.node0, src);
+    r.tiles = __shfl_sync(0xffffffffu, x.tiles, src);
+    r.row_units = __shfl_sync(0xffffffffu, x.row_units, src);
+    r.last_rows = __shfl_sync(0xffffffffu, x.last_rows, src);
+    found = true;
+    return true;
+  });
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!found || r.tiles == 0) return;
+  const Deal& deal = batch.deal;
   const int row = static_cast<int>(node - r.node0) * d.group + head % d.group;
-  const int64_t unit = int64_t(head / d.group) * r.row_units + row / kUnitRows;
-  const int64_t t0 = before + unit * r.tiles, t1 = t0 + r.tiles;
-  const int64_t runs = run_count(total, ctas);
-  const int64_t c0 = run_of(total, runs, t0), c1 = run_of(total, runs, t1 - 1);
-  if (c0 == c1) return;
-  const int at = row % kUnitRows;
+  const int u = row / kUnitRows, at = row % kUnitRows;
+  const int rows = u == r.row_units - 1 ? r.last_rows : kUnitRows;
+  const int64_t s = before + (head / d.group) * deal.head(r) + u * deal.unit(r.tiles, kUnitRows);
+  const int64_t cost = deal.unit(r.tiles, rows);
+  const int64_t runs = deal.runs(batch.total, ctas);
+  const int64_t c0 = Deal::run_of(batch.total, runs, s), c1 = Deal::run_of(batch.total, runs, s + cost - 1);
   const float* ws = static_cast<const float*>(a.workspace);
   const int64_t slot = int64_t(part_rows) * (kD + 2);
   constexpr int kPer = kD / 32;
   float M = -INFINITY, L = 0.f, o[kPer] = {};
-  for (int64_t c = c0; c <= c1; ++c) {
-    const float* p = ws + (c * 2 + (c == c0 ? 1 : 0)) * slot;
-    const float2 x = reinterpret_cast<const float2*>(p + int64_t(part_rows) * kD)[at];
-    const float mn = fmaxf(M, x.x);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float f = ex2(M - base), g = ex2(x.x - base);
-    L = L * f + x.y * g;
+  for (int64_t base = c0; base <= c1; base += 32) {
+    // a lane's piece: its place (-1: none), maximum and sum
+    const int64_t c = base + lane;
+    int64_t p = -1;
+    float2 x = make_float2(-INFINITY, 0.f);
+    if (c <= c1) {
+      const int64_t x0 = Deal::run_start(batch.total, runs, c) - s;
+      const int64_t x1 = Deal::run_start(batch.total, runs, c + 1) - s;
+      const int t0 = deal.tile_at(x0, r.tiles, rows);
+      const int t1 = x1 >= cost ? r.tiles : deal.tile_at(x1, r.tiles, rows);
+      if (t0 == 0 && t1 == r.tiles) p = -2;  // one CTA has it all
+      else if (t0 < t1) p = (c * 2 + (t0 > 0 ? 0 : 1)) * slot;
+      if (p >= 0) x = reinterpret_cast<const float2*>(ws + p + int64_t(part_rows) * kD)[at];
+    }
+    if (__any_sync(0xffffffffu, p == -2)) return;
+    float top = x.x;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k)
-      o[k] = o[k] * f + (g == 0.f ? 0.f : g * p[int64_t(at) * kD + lane * kPer + k]);
+    for (int k = 16; k >= 1; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+    const float mn = fmaxf(M, top), off = mn == -INFINITY ? 0.f : mn;
+    const float f = ex2(M - off), g = ex2(x.x - off);
+    L = L * f + warp_sum(x.y * g);
     M = mn;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) o[k] *= f;
+    const int n = c1 - base < 31 ? static_cast<int>(c1 - base) + 1 : 32;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const int64_t pi = __shfl_sync(0xffffffffu, p, i);
+      const float gi = __shfl_sync(0xffffffffu, g, i);
+      // (a NaN or infinity in a piece that counts for nothing stays out)
+      if (pi >= 0 && gi != 0.f) {
+        const float* src = ws + pi + int64_t(at) * kD + lane * kPer;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) o[k] = fmaf(gi, src[k], o[k]);
+      }
+    }
   }
   bf16_t* dst = static_cast<bf16_t*>(a.out) + node * a.ld_on + int64_t(head) * a.ld_oh + lane * kPer;
 #pragma unroll
@@ -1556,8 +1670,8 @@ cudaError_t launch_tensor(const AttnArgs& a, int sms, int device, cudaStream_t s
   const int part_rows = part_rows_of(a.n_nodes, d.group);
   kernel<<<static_cast<unsigned>(sms), Sh::kThreads, Sh::kSmem, st>>>(mk, mv, a, d, box_rows, part_rows);
   cudaError_t e = cudaGetLastError();
-  // units of one tile are never cut
-  if (e != cudaSuccess || d.room <= kTile) return e;
+  // units of so few tiles are never cut
+  if (e != cudaSuccess || d.room <= kWholeTiles * kTile) return e;
   const int64_t items = a.n_nodes * a.n_q_heads;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((items + kCombineWarps - 1) / kCombineWarps));
