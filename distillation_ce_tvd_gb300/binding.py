@@ -930,7 +930,8 @@ class KVCache:
     The object keeps the tensors and the library's description of them; make it once per layer.
     """
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "struct", "ref", "device")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "struct", "ref", "device", "index", "n_heads",
+                 "head_dim")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         code = {torch.bfloat16: FCT_BF16, torch.float8_e4m3fn: FCT_E4M3}.get(k.dtype)
@@ -955,7 +956,8 @@ class KVCache:
         elif k_scale is not None or v_scale is not None:
             raise ValueError("a bfloat16 cache has no scales")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
+        self.n_heads, self.head_dim = int(k.shape[2]), int(k.shape[3])
         self.struct = _KvCacheStruct(
             k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if k_scale is not None else None,
             v_scale.data_ptr() if v_scale is not None else None, code, k.shape[1], k.shape[2],
@@ -963,22 +965,40 @@ class KVCache:
         self.ref = ctypes.byref(self.struct)
 
 
-def _vec(x, dtype, n, device, name):
-    """The address of a contiguous vector of ``n`` values."""
-    if x.dtype != dtype or x.dim() != 1 or x.shape[0] != n or x.device != device \
-            or (n > 1 and x.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous {dtype} vector of {n} values on {device}")
+# The step's calls take a few microseconds on the GPU at small sizes, so their
+# checks ask each tensor as little as possible.
+
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream, index):
+    """The address of ``stream``, or of the current stream of CUDA device ``index``."""
+    if stream is None:
+        if _current_raw_stream is not None:
+            return _current_raw_stream(index)
+        return torch.cuda.current_stream(index).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _library():
+    return _lib if _lib is not None else load()
+
+
+def _vec(x, dtype, n, index, name):
+    """The address of a contiguous vector of ``n`` values on CUDA device ``index``."""
+    if x.dtype is not dtype or x.shape != (n,) or x.get_device() != index or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} vector of {n} values on cuda:{index}")
     return x.data_ptr()
 
 
-def _table(x, dtype, rows, device, name):
+def _table(x, dtype, rows, index, name):
     """(address, row stride, columns) of a 2-D tensor of ``rows`` rows with unit column stride."""
-    if x.dtype != dtype or x.dim() != 2 or x.shape[0] != rows or x.device != device \
-            or (x.shape[1] > 1 and x.stride(1) != 1):
-        raise ValueError(f"{name} must be a 2-D {dtype} tensor of {rows} rows on {device} with "
+    shape = x.shape
+    if x.dtype is not dtype or len(shape) != 2 or shape[0] != rows or x.get_device() != index \
+            or (shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError(f"{name} must be a 2-D {dtype} tensor of {rows} rows on cuda:{index} with "
                          "unit stride along columns")
-    cols = x.shape[1]
-    return x.data_ptr(), (x.stride(0) if rows > 1 else cols), cols
+    return x.data_ptr(), (x.stride(0) if rows > 1 else shape[1]), shape[1]
 
 
 def _status_ptr(x):
@@ -990,20 +1010,19 @@ def fct_kv_cache_write(cache, k, v, slots, *, dev_status=None, stream=None):
     with unit stride along head_dim) to the slots (page * page_size + offset; int64 (n,), negative
     skips) of the cache, in place.  An e4m3 cache is quantised as it is written: per token and head
     the smallest power of two that keeps every value within 448, then round to nearest even."""
-    s = cache.struct
-    code = {torch.float32: FCT_F32, torch.bfloat16: FCT_BF16}.get(k.dtype)
-    if code is None:
+    code = FCT_BF16 if k.dtype is torch.bfloat16 else FCT_F32
+    if code == FCT_F32 and k.dtype is not torch.float32:
         raise TypeError(f"k: dtype {k.dtype} is not float32 or bfloat16")
-    if k.dim() != 3 or k.shape[1] != s.n_heads or k.shape[2] != s.head_dim \
-            or v.shape != k.shape or v.dtype != k.dtype or v.stride() != k.stride() \
-            or k.device != cache.device or v.device != cache.device \
-            or (s.head_dim > 1 and k.stride(2) != 1):
+    shape, strides, index = k.shape, k.stride(), cache.index
+    if len(shape) != 3 or shape[1] != cache.n_heads or shape[2] != cache.head_dim \
+            or v.shape != shape or v.dtype is not k.dtype or v.stride() != strides \
+            or k.get_device() != index or v.get_device() != index or strides[2] != 1:
         raise ValueError("k and v must be (n, n_kv_heads, head_dim) on the cache's device, of one "
                          "dtype and one set of strides, with unit stride along head_dim")
-    n = k.shape[0]
-    rc = load().fct_kv_cache_write(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), code, n,
-                                   _vec(slots, torch.int64, n, cache.device, "slots"), cache.ref,
-                                   _status_ptr(dev_status), _stream(stream))
+    n = shape[0]
+    rc = _library().fct_kv_cache_write(k.data_ptr(), v.data_ptr(), strides[0], strides[1], code, n,
+                                       _vec(slots, torch.int64, n, index, "slots"), cache.ref,
+                                       _status_ptr(dev_status), _raw_stream(stream, index))
     _check(rc, "fct_kv_cache_write")
 
 
@@ -1011,14 +1030,13 @@ def fct_kv_cache_move(cache, block_table, context_len, path, count, *, dev_statu
                       stream=None):
     """Move the accepted nodes' keys and values (``path`` and ``count`` as fct_spec_verify returns
     them) to the positions after each request's context, in place."""
-    B = context_len.shape[0]
-    tab, ld_t, pages = _table(block_table, torch.int32, B, cache.device, "block_table")
-    pth, ld_p, depth = _table(path, torch.int32, B, cache.device, "path")
-    rc = load().fct_kv_cache_move(cache.ref, tab, ld_t, pages,
-                                  _vec(context_len, torch.int32, B, cache.device, "context_len"),
-                                  B, pth, ld_p, depth,
-                                  _vec(count, torch.int32, B, cache.device, "count"),
-                                  _status_ptr(dev_status), _stream(stream))
+    B, index = context_len.shape[0], cache.index
+    tab, ld_t, pages = _table(block_table, torch.int32, B, index, "block_table")
+    pth, ld_p, depth = _table(path, torch.int32, B, index, "path")
+    rc = _library().fct_kv_cache_move(cache.ref, tab, ld_t, pages,
+                                      _vec(context_len, torch.int32, B, index, "context_len"), B,
+                                      pth, ld_p, depth, _vec(count, torch.int32, B, index, "count"),
+                                      _status_ptr(dev_status), _raw_stream(stream, index))
     _check(rc, "fct_kv_cache_move")
 
 
@@ -1029,11 +1047,14 @@ def fct_tree_attention_workspace_size(n_nodes: int, n_q_heads: int, n_kv_heads: 
                                                         int(n_kv_heads), int(head_dim)))
 
 
-def _heads(x, device, name):
-    if x.dim() != 3 or x.dtype != torch.bfloat16 or x.device != device \
-            or (x.shape[2] > 1 and x.stride(2) != 1):
-        raise ValueError(f"{name} must be a (n_nodes, n_q_heads, head_dim) bfloat16 tensor on the "
-                         "cache's device with unit stride along head_dim")
+def _heads(x, shape, index, name):
+    """(address, strides) of a bfloat16 tensor of (n_nodes, n_q_heads, head_dim)."""
+    strides = x.stride()
+    if x.shape != shape or x.dtype is not torch.bfloat16 or x.get_device() != index \
+            or strides[2] != 1:
+        raise ValueError(f"{name} must be a {tuple(shape)} bfloat16 tensor on the cache's device "
+                         "with unit stride along head_dim")
+    return x.data_ptr(), strides[0], strides[1]
 
 
 def fct_tree_attention(q, cache, block_table, context_len, node_start, tree_mask=None, *,
@@ -1049,39 +1070,41 @@ def fct_tree_attention(q, cache, block_table, context_len, node_start, tree_mask
     n_q_heads) float32.  ``scale`` defaults to head_dim ** -0.5.  ``workspace``: a uint8 tensor of
     fct_tree_attention_workspace_size bytes to keep between calls (allocated here if None).
     """
-    s, dev = cache.struct, cache.device
-    _heads(q, dev, "q")
-    N, H, D = q.shape
-    if D != s.head_dim or H % s.n_heads != 0:
-        raise ValueError("q's heads must be a multiple of the cache's and share its head_dim")
+    index = cache.index
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim or shape[1] % cache.n_heads != 0:
+        raise ValueError("q must be (n_nodes, n_q_heads, head_dim) with the cache's head_dim and a "
+                         "multiple of its heads")
+    N, H, D = shape
+    q_ptr, q_node, q_head = _heads(q, shape, index, "q")
     B = context_len.shape[0]
-    tab, ld_t, pages = _table(block_table, torch.int32, B, dev, "block_table")
+    tab, ld_t, pages = _table(block_table, torch.int32, B, index, "block_table")
     mask, words = None, 0
     if tree_mask is not None:
-        mask, ld_m, words = _table(tree_mask, torch.int64, N, dev, "tree_mask")
+        mask, ld_m, words = _table(tree_mask, torch.int64, N, index, "tree_mask")
         if ld_m != words:
             raise ValueError("tree_mask must be contiguous")
     if out is None:
-        out = torch.empty((N, H, D), device=dev, dtype=torch.bfloat16)
+        out = torch.empty(shape, device=cache.device, dtype=torch.bfloat16)
+        o_ptr, o_node, o_head = out.data_ptr(), H * D, D
     else:
-        _heads(out, dev, "out")
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
+        o_ptr, o_node, o_head = _heads(out, shape, index, "out")
     if lse is None:
-        lse = torch.empty((N, H), device=dev, dtype=torch.float32)
-    elif lse.dtype != torch.float32 or lse.shape != (N, H) or not lse.is_contiguous() \
-            or lse.device != dev:
+        lse = torch.empty((N, H), device=cache.device, dtype=torch.float32)
+    elif lse.dtype is not torch.float32 or lse.shape != (N, H) or not lse.is_contiguous() \
+            or lse.get_device() != index:
         raise ValueError("lse must be a contiguous (n_nodes, n_q_heads) float32 tensor")
     if workspace is None:
-        workspace = torch.empty(fct_tree_attention_workspace_size(N, H, s.n_heads, D) if N else 0,
-                                device=dev, dtype=torch.uint8)
-    rc = load().fct_tree_attention(
-        q.data_ptr(), q.stride(0), q.stride(1), N, H, cache.ref, tab, ld_t, pages,
-        _vec(context_len, torch.int32, B, dev, "context_len"),
-        _vec(node_start, torch.int32, B + 1, dev, "node_start"), B, mask, words,
-        D ** -0.5 if scale is None else scale, out.data_ptr(), out.stride(0), out.stride(1),
-        lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _status_ptr(dev_status), _stream(stream))
+        workspace = torch.empty(
+            fct_tree_attention_workspace_size(N, H, cache.n_heads, D) if N else 0,
+            device=cache.device, dtype=torch.uint8)
+    rc = _library().fct_tree_attention(
+        q_ptr, q_node, q_head, N, H, cache.ref, tab, ld_t, pages,
+        _vec(context_len, torch.int32, B, index, "context_len"),
+        _vec(node_start, torch.int32, B + 1, index, "node_start"), B, mask, words,
+        D ** -0.5 if scale is None else scale, o_ptr, o_node, o_head, lse.data_ptr(),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _status_ptr(dev_status), _raw_stream(stream, index))
     _check(rc, "fct_tree_attention")
     return out, lse
 
@@ -1101,40 +1124,46 @@ def fct_spec_verify(target_logits, tokens, parent, node_start, uniform, noise, d
     ``out_tokens`` (batch, max_depth + 1) int64: the accepted tokens, the next token, then -1;
     ``path`` (batch, max_depth) int32: the accepted nodes; ``count`` (batch,) int32: how many.
     """
-    code, ld_t = _logits(target_logits, "target_logits")
+    dtype = target_logits.dtype
+    code = FCT_BF16 if dtype is torch.bfloat16 else FCT_F32
+    if code == FCT_F32 and dtype is not torch.float32:
+        raise TypeError(f"target_logits: dtype {dtype} is not float32 or bfloat16")
+    index = target_logits.get_device()
+    if index < 0 or target_logits.dim() != 2:
+        raise ValueError("target_logits must be a (n_nodes, V) CUDA tensor")
     N, V = target_logits.shape
-    dev = target_logits.device
+    tgt, ld_t, _ = _table(target_logits, dtype, N, index, "target_logits")
     dft, ld_d = None, 0
     if draft_logits is not None:
-        code_d, ld_d = _logits(draft_logits, "draft_logits")
-        if code_d != code or draft_logits.shape != (N, V) or draft_logits.device != dev:
+        dft, ld_d, cols = _table(draft_logits, dtype, N, index, "draft_logits")
+        if cols != V:
             raise ValueError("draft_logits must match target_logits' shape, dtype and device")
-        dft = draft_logits.data_ptr()
     B = node_start.shape[0] - 1
     if B < 0:
         raise ValueError("node_start must have batch + 1 values")
-    nse, ld_n, cols = _table(noise, torch.float32, B, dev, "noise")
+    nse, ld_n, cols = _table(noise, torch.float32, B, index, "noise")
     if cols != V:
         raise ValueError("noise must be (batch, V)")
     P = int(max_depth)
-    if out_tokens is None:
-        out_tokens = torch.empty((B, P + 1), device=dev, dtype=torch.int64)
-    if path is None:
-        path = torch.empty((B, P), device=dev, dtype=torch.int32)
-    if count is None:
-        count = torch.empty((B,), device=dev, dtype=torch.int32)
-    for x, shape, dtype, name in ((out_tokens, (B, P + 1), torch.int64, "out_tokens"),
-                                  (path, (B, P), torch.int32, "path"),
-                                  (count, (B,), torch.int32, "count")):
-        if x.shape != shape or x.dtype != dtype or x.device != dev or not x.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
-    rc = load().fct_spec_verify(
-        target_logits.data_ptr(), ld_t, dft, ld_d, code, N, V,
-        _vec(tokens, torch.int64, N, dev, "tokens"), _vec(parent, torch.int32, N, dev, "parent"),
-        _vec(node_start, torch.int32, B + 1, dev, "node_start"), B,
-        _vec(uniform, torch.float32, N, dev, "uniform"), nse, ld_n,
-        _vec(temperature, torch.float32, B, dev, "temperature") if temperature is not None else None,
-        P, out_tokens.data_ptr(), path.data_ptr(), count.data_ptr(), _status_ptr(dev_status),
-        _stream(stream))
+    dev = target_logits.device
+    def output(x, shape, want, name):
+        if x is None:
+            return torch.empty(shape, device=dev, dtype=want)
+        if x.shape != shape or x.dtype is not want or x.get_device() != index \
+                or not x.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {want} tensor of shape {shape}")
+        return x
+
+    out_tokens = output(out_tokens, (B, P + 1), torch.int64, "out_tokens")
+    path = output(path, (B, P), torch.int32, "path")
+    count = output(count, (B,), torch.int32, "count")
+    rc = _library().fct_spec_verify(
+        tgt, ld_t, dft, ld_d, code, N, V, _vec(tokens, torch.int64, N, index, "tokens"),
+        _vec(parent, torch.int32, N, index, "parent"),
+        _vec(node_start, torch.int32, B + 1, index, "node_start"), B,
+        _vec(uniform, torch.float32, N, index, "uniform"), nse, ld_n,
+        _vec(temperature, torch.float32, B, index, "temperature") if temperature is not None
+        else None, P, out_tokens.data_ptr(), path.data_ptr(), count.data_ptr(),
+        _status_ptr(dev_status), _raw_stream(stream, index))
     _check(rc, "fct_spec_verify")
     return out_tokens, path, count
