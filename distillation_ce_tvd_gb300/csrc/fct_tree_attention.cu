@@ -971,57 +971,67 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
             ok = false;
             return false;
           }
-          constexpr int kChunks = kD / 16;  // 16 payload bytes each
-          const uint8_t* raw_tiles = attn_smem + (2 + Sh::kSlots) * Sh::kTileBytes;
-          // eight lanes take four 16-byte pieces of two rows: their stores fall
-          // on different banks
+          // A thread takes 16-byte pieces t % 4 (+ 4) of row t / 4 of each 32 rows:
+          // eight lanes store to different banks, and every address but the
+          // first is a constant away.  The next row is loaded before the present
+          // one is turned.
+          constexpr int kHalves = Sh::kHalves;
+          const uint32_t src = raw0 + r * Sh::kRawBytes + uint32_t(t / 4) * kD + uint32_t(t % 4) * 16;
+          const uint32_t out0 = dst + uint32_t(t / 4) * 128 + uint32_t((((t % 4) * 2) ^ ((t / 4) & 7)) * 16);
+          const uint32_t out1 = out0 ^ 16u;
+          const uint32_t scale = smem_addr(&ctl.raw_scale[r][t / 4]);
+          const bool clear = is_v && is_tail(seg, tile);
           bool found = false;
-          constexpr int kRows = kPrepThreads / 4;        // rows of one pass
-          constexpr int kBatch = 4;                      // passes whose loads are under way at once
+          uint32_t in[kHalves][4], byte;
+          auto load = [&](int block) {
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(scale + 32u * block));
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(in[h][0]), "=r"(in[h][1]), "=r"(in[h][2]), "=r"(in[h][3])
+                           : "r"(src + 32u * kD * block + 64u * h));
+          };
+          load(0);
 #pragma unroll 1
-          for (int i0 = 0; i0 < kTile * kChunks / kPrepThreads; i0 += kBatch) {
-            uint4 in4[kBatch];
-            uint32_t byte[kBatch];
+          for (int block = 0; block < kTile / 32; ++block) {
+            uint32_t x[kHalves][4], e = byte;
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              const int n = i0 + i, row = n / (kChunks / 4) * kRows + t / 4;
-              const int c = n % (kChunks / 4) * 4 + t % 4;
-              in4[i] = *reinterpret_cast<const uint4*>(raw_tiles + r * Sh::kRawBytes + row * kD + c * 16);
-              byte[i] = ctl.raw_scale[r][row];
-            }
+            for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              const int n = i0 + i, row = n / (kChunks / 4) * kRows + t / 4;
-              const int c = n % (kChunks / 4) * 4 + t % 4;
-              const int pos = p0 + row;
-              if (is_v && pos >= seg.ctx && (pos >= seg.len || byte[i] == 255)) {
+              for (int k = 0; k < 4; ++k) x[h][k] = in[h][k];
+            if (block + 1 < kTile / 32) load(block + 1);
+            if (clear) {
+              const int pos = p0 + block * 32 + t / 4;
+              if (pos >= seg.ctx && (pos >= seg.len || e == 255)) {
                 found |= pos < seg.len;
-                in4[i] = make_uint4(0, 0, 0, 0);
-                byte[i] = 127;
+                e = 127;
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) x[h][0] = x[h][1] = x[h][2] = x[h][3] = 0;
               }
-              // 2^120 * 2^(byte - 127) as one bf16 factor, or as two
-              const bool one = byte[i] <= 134;
-              const uint32_t m1 = (one ? byte[i] + 120 : 247u) << 7;
-              const uint32_t f1 = m1 | (m1 << 16);
-              const uint32_t in[4] = {in4[i].x, in4[i].y, in4[i].z, in4[i].w};
+            }
+            // 2^120 * 2^(e - 127) as one bf16 factor, or as two
+            const bool one = e <= 134;
+            const uint32_t f1 = (one ? e + 120 : 247u) * 0x00800080u;
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {
               uint32_t o[8];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                o[2 * k] = mul_bf16x2(e4m3_bits(__byte_perm(in[k], 0, 0x1404)), f1);
-                o[2 * k + 1] = mul_bf16x2(e4m3_bits(__byte_perm(in[k], 0, 0x3424)), f1);
+                o[2 * k] = mul_bf16x2(e4m3_bits(__byte_perm(x[h][k], 0, 0x1404)), f1);
+                o[2 * k + 1] = mul_bf16x2(e4m3_bits(__byte_perm(x[h][k], 0, 0x3424)), f1);
               }
               if (!one) {
-                const uint32_t m2 = byte[i] == 255 ? 0x7fc0u : byte[i] << 7;
-                const uint32_t f2 = m2 | (m2 << 16);
+                const uint32_t f2 = e == 255 ? 0x7fc07fc0u : e * 0x00800080u;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], f2);
               }
-              uint8_t* line = attn_smem + 2 * Sh::kTileBytes + slot * Sh::kTileBytes +
-                              (c / 4) * (kTile * 128) + row * 128;
-#pragma unroll
-              for (int k = 0; k < 2; ++k)
-                *reinterpret_cast<uint4*>(line + (((c % 4) * 2 + k) ^ (row & 7)) * 16) =
-                    make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+              const uint32_t at = 32u * 128 * block + uint32_t(h) * (kTile * 128);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out0 + at), "r"(o[0]),
+                           "r"(o[1]), "r"(o[2]), "r"(o[3])
+                           : "memory");
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out1 + at), "r"(o[4]),
+                           "r"(o[5]), "r"(o[6]), "r"(o[7])
+                           : "memory");
             }
           }
           if (found) ctl.bad_seg[seg_n % kBadRing] = seg_n;
