@@ -210,15 +210,16 @@ constexpr float kLazyLog2 = 8.f;  // O is rescaled when the maximum grows by mor
 template <int kD, bool kFp8>
 struct AttnShape {
   // Warps: 0 loads, 1 products, 4-11 softmax; e4m3: 2 and 3 fetch scale bytes,
-  // 12-15 prepare; bf16: 2 prepares, 3 loads V (0 loads K).
-  static constexpr int kThreads = kFp8 ? 512 : 384;
-  static constexpr int kPrepWarp0 = kFp8 ? 12 : 2, kPrepWarps = kFp8 ? 4 : 1;
-  // Registers per thread of warps 0-3, the softmax groups and warps 12-15,
-  // moved between the warp groups: together what the kernel is launched with,
-  // 65536 / kThreads each (in eights).
-  static constexpr int kLaunchRegs = kFp8 ? 128 : 168;
-  static constexpr int kLowRegs = kFp8 ? 80 : 120, kSoftRegs = kFp8 ? 176 : 192;
-  static_assert((kFp8 ? 2 : 1) * kLowRegs + 2 * kSoftRegs <= kThreads / 128 * kLaunchRegs, "registers");
+  // 12-19 prepare; bf16: 2 prepares, 3 loads V (0 loads K).
+  static constexpr int kThreads = kFp8 ? 640 : 384;
+  static constexpr int kPrepWarp0 = kFp8 ? 12 : 2, kPrepWarps = kFp8 ? 4 : 1;  // per tile
+  static constexpr int kPrepGroups = kFp8 ? 2 : 1;  // taking tiles in turn
+  // Registers per thread of the softmax groups and of all other warps, moved
+  // between the warp groups: together what the kernel is launched with, 65536
+  // / kThreads each (in eights).
+  static constexpr int kLaunchRegs = kFp8 ? 96 : 168;
+  static constexpr int kLowRegs = kFp8 ? 64 : 120, kSoftRegs = kFp8 ? 144 : 192;
+  static_assert((kThreads / 128 - 2) * kLowRegs + 2 * kSoftRegs <= kThreads / 128 * kLaunchRegs, "registers");
   static constexpr int kHalves = kD / 64;  // 128-byte column blocks of a bf16 row
   static constexpr uint32_t kTileBytes = kTile * kD * 2;
   static constexpr uint32_t kRawBytes = kTile * kD;
@@ -951,8 +952,9 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
 
   auto prepare = [&]() {
     // ---- tiles prepared
-    const int t = threadIdx.x - Sh::kPrepWarp0 * 32;
     constexpr int kPrepThreads = Sh::kPrepWarps * 32;
+    const int t = (threadIdx.x - Sh::kPrepWarp0 * 32) % kPrepThreads;
+    const uint32_t group = (warp - Sh::kPrepWarp0) / Sh::kPrepWarps;
     uint32_t item = 0, tail_phase = 0;
     int seg_n = 0;
     bool ok = true;
@@ -965,17 +967,21 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
         const uint32_t dst = slot0 + slot * Sh::kTileBytes;
         if constexpr (kFp8) {
           const uint32_t r = it % Sh::kRaw;
+          // (a group waits for the slots of the other's tiles too, so that it is
+          // never a phase behind when it waits for its own)
+          ok = warp_wait(&ctl.empty_bar[slot], ((it / Sh::kSlots) & 1u) ^ 1u, &ctl.abort_flag);
+          if (!ok || it % Sh::kPrepGroups != group) return ok;
+          static_assert(Sh::kRaw % Sh::kPrepGroups == 0, "a raw slot belongs to one group");
           if (!warp_wait(&ctl.raw_full[r], (it / Sh::kRaw) & 1u, &ctl.abort_flag) ||
-              !warp_wait(&ctl.raw_scaled[r], (it / Sh::kRaw) & 1u, &ctl.abort_flag) ||
-              !warp_wait(&ctl.empty_bar[slot], ((it / Sh::kSlots) & 1u) ^ 1u, &ctl.abort_flag)) {
+              !warp_wait(&ctl.raw_scaled[r], (it / Sh::kRaw) & 1u, &ctl.abort_flag)) {
             ok = false;
             return false;
           }
-          // A thread takes 16-byte pieces t % 4 (+ 4) of row t / 4 of each 32 rows:
+          // A thread takes 16-byte pieces t % 4 (+ 4) of row t / 4 of each kRows rows:
           // eight lanes store to different banks, and every address but the
           // first is a constant away.  The next row is loaded before the present
           // one is turned.
-          constexpr int kHalves = Sh::kHalves;
+          constexpr int kHalves = Sh::kHalves, kRows = kPrepThreads / 4;
           const uint32_t src = raw0 + r * Sh::kRawBytes + uint32_t(t / 4) * kD + uint32_t(t % 4) * 16;
           const uint32_t out0 = dst + uint32_t(t / 4) * 128 + uint32_t((((t % 4) * 2) ^ ((t / 4) & 7)) * 16);
           const uint32_t out1 = out0 ^ 16u;
@@ -984,24 +990,24 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
           bool found = false;
           uint32_t in[kHalves][4], byte;
           auto load = [&](int block) {
-            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(scale + 32u * block));
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(scale + uint32_t(kRows) * block));
 #pragma unroll
             for (int h = 0; h < kHalves; ++h)
               asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                            : "=r"(in[h][0]), "=r"(in[h][1]), "=r"(in[h][2]), "=r"(in[h][3])
-                           : "r"(src + 32u * kD * block + 64u * h));
+                           : "r"(src + uint32_t(kRows * kD) * block + 64u * h));
           };
           load(0);
 #pragma unroll 1
-          for (int block = 0; block < kTile / 32; ++block) {
+          for (int block = 0; block < kTile / kRows; ++block) {
             uint32_t x[kHalves][4], e = byte;
 #pragma unroll
             for (int h = 0; h < kHalves; ++h)
 #pragma unroll
               for (int k = 0; k < 4; ++k) x[h][k] = in[h][k];
-            if (block + 1 < kTile / 32) load(block + 1);
+            if (block + 1 < kTile / kRows) load(block + 1);
             if (clear) {
-              const int pos = p0 + block * 32 + t / 4;
+              const int pos = p0 + block * kRows + t / 4;
               if (pos >= seg.ctx && (pos >= seg.len || e == 255)) {
                 found |= pos < seg.len;
                 e = 127;
@@ -1025,7 +1031,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], f2);
               }
-              const uint32_t at = 32u * 128 * block + uint32_t(h) * (kTile * 128);
+              const uint32_t at = uint32_t(kRows * 128) * block + uint32_t(h) * (kTile * 128);
               asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out0 + at), "r"(o[0]),
                            "r"(o[1]), "r"(o[2]), "r"(o[3])
                            : "memory");
