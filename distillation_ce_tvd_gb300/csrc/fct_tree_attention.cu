@@ -211,20 +211,17 @@ template <int kD, bool kFp8>
 struct AttnShape {
   // Warps: 0 loads, 1 products, 4-11 softmax; e4m3: 2 and 3 fetch scale bytes,
   // 12-19 prepare; bf16: 2 prepares, 3 loads V (0 loads K).
-  static constexpr int kThreads = kFp8 ? 640 : 384;
+  static constexpr int kThreads = kFp8 ? 512 : 384;
   static constexpr int kPrepWarp0 = kFp8 ? 12 : 2, kPrepWarps = kFp8 ? 4 : 1;  // per tile
-  static constexpr int kPrepGroups = kFp8 ? 2 : 1;  // taking tiles in turn
-  // Registers per thread of the softmax groups and of all other warps, moved
-  // between the warp groups: together what the kernel is launched with, 65536
-  // / kThreads each (in eights).
-  static constexpr int kLaunchRegs = kFp8 ? 96 : 168;
-  static constexpr int kLowRegs = kFp8 ? 64 : 120, kSoftRegs = kFp8 ? 144 : 192;
-  static_assert((kThreads / 128 - 2) * kLowRegs + 2 * kSoftRegs <= kThreads / 128 * kLaunchRegs, "registers");
+  [[maybe_unused]] static constexpr int kPrepGroups = 1;  // taking tiles in turn
+  // Score chunks of 32 keys that a softmax thread holds: what the registers of
+  // 65536 / kThreads allow without spilling.
+  static constexpr int kHold = kFp8 ? 1 : 2;
   static constexpr int kHalves = kD / 64;  // 128-byte column blocks of a bf16 row
   static constexpr uint32_t kTileBytes = kTile * kD * 2;
   static constexpr uint32_t kRawBytes = kTile * kD;
   static constexpr int kSlots = kD == 128 ? (kFp8 ? 3 : 5) : (kFp8 ? 4 : 8);
-  static constexpr int kRing = kFp8 ? (kD == 128 ? 4 : 8) : 1;  // raw slots (1 where unused)
+  [[maybe_unused]] static constexpr int kRing = kFp8 ? (kD == 128 ? 4 : 8) : 1;  // raw slots (1 where unused)
   static constexpr int kRaw = kFp8 ? (kD == 128 ? 4 : 8) : 0;
   static constexpr size_t kTilesBytes =
       2 * kTileBytes + size_t(kSlots) * kTileBytes + size_t(kRaw) * kRawBytes;
@@ -558,15 +555,29 @@ __device__ __forceinline__ void tm_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// mbar_wait without a function call: a kernel that moves registers between its
-// warps has none.
+// Whether a phase has completed; the thread may be suspended for some
+// microseconds before the answer is no, so that waiting warps leave the issue
+// slots to the others.
+__device__ __forceinline__ bool mbar_try_long(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity), "r"(20000u)
+      : "memory");
+  return done != 0;
+}
+// mbar_wait without a function call.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort,
                                            bool heed_abort = true) {
-  if (mbar_try(bar, parity)) return true;
+  const uint32_t at = smem_addr(bar);
+  if (mbar_try_long(at, parity)) return true;
   const long long t0 = clock64();
   do {
     if (heed_abort && *abort) return false;
-    if (mbar_try(bar, parity)) return true;
+    if (mbar_try_long(at, parity)) return true;
   } while (clock64() - t0 <= kWaitLimitCycles);
   *abort = 1;
   return false;
@@ -655,59 +666,46 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
   return r;
 }
 
-template <int kRegs>
-__device__ __forceinline__ void more_registers() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void fewer_registers() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-
 // One key tile of a softmax warp: `chunks` (1, 2 or 4) chunks of 32 keys from
 // chunk0 on are its share, of the rows of its 32 lanes.  S's columns become
 // P's (16 per chunk, and 16 of the weights' rounding remainders where `fine`);
-// the chunks of other warps, which hold the same rows, become zero.  Two
-// chunks are held at a time (with four, S is read twice), in loops that stay
-// small: the roles of a CTA share one instruction cache.
-template <int kD>
+// the chunks of other warps, which hold the same rows, become zero.  kHold
+// chunks are held at a time (S is read twice where there are more), in loops
+// that stay small: the roles of a CTA share one instruction cache.
+template <int kD, int kHold>
 __device__ __forceinline__ void soft_tile(const AttnArgs& a, const Segment& seg, uint32_t tm_s,
                                           uint32_t tm_o, int chunk0, int chunks, int node, bool live,
                                           int p0, bool tail, bool fine, bool first, float sl2, float& m,
                                           float& l) {
-  uint32_t x[2][32];
+  uint32_t x[kHold][32];
   auto load = [&](int i0) {
     const uint32_t at = tm_s + 32 * (chunk0 + i0);
     tm_ld_start(at, x[0]);
-    if (chunks > 1) tm_ld_start(at + 32, x[1]);
-    tm_ld_done(x[0]);
-    tm_ld_done(x[1]);
+    if (kHold > 1 && chunks > 1) tm_ld_start(at + 32, x[kHold - 1]);
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) tm_ld_done(x[i]);
     if (tail) {
-#pragma unroll 1
-      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int i = 0; i < kHold; ++i) {
         const uint32_t vis = live ? visible32(a, seg, node, p0 + 32 * (i0 + i)) : 0u;
         __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          if (i == 0)
-            x[0][k] = (vis >> k) & 1u ? x[0][k] : 0xff800000u;
-          else
-            x[1][k] = (vis >> k) & 1u ? x[1][k] : 0xff800000u;
-        }
+        for (int k = 0; k < 32; ++k) x[i][k] = (vis >> k) & 1u ? x[i][k] : 0xff800000u;
       }
     }
   };
   float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-  for (int i0 = 0; i0 < chunks; i0 += 2) {
+  for (int i0 = 0; i0 < chunks; i0 += kHold) {
     load(i0);
 #pragma unroll
-    for (int k = 0; k < 32; k += 2)
-      tops[(k / 2) % 4] = max3(tops[(k / 2) % 4], __uint_as_float(x[0][k]), __uint_as_float(x[0][k + 1]));
-    if (chunks > 1) {
+    for (int i = 0; i < kHold; ++i) {
+      if (i < chunks) {
 #pragma unroll
-      for (int k = 0; k < 32; k += 2)
-        tops[(k / 2) % 4] = max3(tops[(k / 2) % 4], __uint_as_float(x[1][k]), __uint_as_float(x[1][k + 1]));
+        for (int k = 0; k < 32; k += 2)
+          tops[(k / 2) % 4] =
+              max3(tops[(k / 2) % 4], __uint_as_float(x[i][k]), __uint_as_float(x[i][k + 1]));
+      }
     }
   }
   const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * sl2;
@@ -754,12 +752,14 @@ __device__ __forceinline__ void soft_tile(const AttnArgs& a, const Segment& seg,
       tm_st16(at + 16, p);
     }
   };
+  const int last = chunks > kHold ? chunks - kHold : 0;  // its chunks are still held
 #pragma unroll 1
-  for (int i0 = chunks > 2 ? 2 : 0; i0 >= 0; i0 -= 2) {  // the last two are still held
-    if (chunks > 2 && i0 == 0) load(i0);
+  for (int i0 = last; i0 >= 0; i0 -= kHold) {
+    if (i0 != last) load(i0);
     const uint32_t at = tm_s + 32 * (chunk0 + i0);
-    weights(x[0], at);
-    if (chunks > 1) weights(x[1], at + 32);
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)
+      if (i < chunks) weights(x[i], at + 32 * i);
   }
   if (chunks < 4) {
     const uint32_t zero[16] = {};
@@ -1096,10 +1096,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
     }
   };
 
-  // (registers are moved before the warps of a group go different ways: all of
-  // them execute the same instruction)
   if (warp < 4) {
-    fewer_registers<Sh::kLowRegs>();
     if (warp == 0) {
       load_tiles(true, kFp8);
     } else if (warp == 1) {
@@ -1247,7 +1244,6 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
       load_tiles(false, true);
     }
   } else if (warp < 12) {
-    more_registers<Sh::kSoftRegs>();
     // ---- softmax groups A (warps 4-7) and B (8-11).  A lane of tensor memory
     // is a row; with at most 64 (32) rows the query tile holds them twice (four
     // times), and the warps of each copy take a half (quarter) of a tile's
@@ -1330,7 +1326,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
         if (warp_live) {
           const int p0 = (seg.tile0 + j) * kTile + 32 * chunk0;
           const bool tail = is_tail(seg, seg.tile0 + j);
-          soft_tile<kD>(a, seg, tm_s, tm_o + uint32_t(w) * kD, chunk0, span / 32, node, live, p0, tail,
+          soft_tile<kD, Sh::kHold>(a, seg, tm_s, tm_o + uint32_t(w) * kD, chunk0, span / 32, node, live, p0, tail,
                         fine, first, sl2, m, l);
         }
         first = false;
@@ -1497,7 +1493,6 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
       }
     }
   } else {
-    fewer_registers<Sh::kLowRegs>();
     if constexpr (kFp8) prepare();
   }
   tc_before();
@@ -1635,7 +1630,9 @@ bool cache_map(CUtensorMap* map, const fct_kv_cache& c, void* base, int box_rows
   return encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base,
                 dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                c.head_dim * int(e) >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                           : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Whether the tensor-core kernel takes this cache: a head_dim it is built
@@ -1669,12 +1666,6 @@ cudaError_t launch_tensor(const AttnArgs& a, int sms, int device, cudaStream_t s
   std::call_once(once[device], [&] {
     ready[device] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(Sh::kSmem));
-    // the warp groups share out exactly what the CTA is launched with; with
-    // less, the ones that ask for more would wait for it
-    cudaFuncAttributes f;
-    if (ready[device] == cudaSuccess) ready[device] = cudaFuncGetAttributes(&f, kernel);
-    if (ready[device] == cudaSuccess && f.numRegs < Sh::kLaunchRegs)
-      ready[device] = cudaErrorInvalidDeviceFunction;
   });
   if (ready[device] != cudaSuccess) return ready[device];
   int box_rows = kTile;
