@@ -216,7 +216,7 @@ struct AttnShape {
   [[maybe_unused]] static constexpr int kPrepGroups = 1;  // taking tiles in turn
   // Score chunks of 32 keys that a softmax thread holds: what the registers of
   // 65536 / kThreads allow without spilling.
-  static constexpr int kHold = kFp8 ? 1 : 2;
+  static constexpr int kHold = 1;
   static constexpr int kHalves = kD / 64;  // 128-byte column blocks of a bf16 row
   static constexpr uint32_t kTileBytes = kTile * kD * 2;
   static constexpr uint32_t kRawBytes = kTile * kD;
@@ -1508,93 +1508,97 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
   if (status && a.dev_status) atomicOr(a.dev_status, status);
 }
 
-// Adds the partial sums of units that were cut between CTAs: one warp per
-// node and query head, the pieces in the order of the keys.
-constexpr int kCombineWarps = 4;
+// Adds the partial sums of units that were cut between CTAs, the pieces in the
+// order of the keys, one row to a warp.  A unit is cut where runs meet, so
+// blockIdx.x stands for the start of run blockIdx.x + 1: the meeting points
+// inside one unit share its rows, and the kCombineBlocks blocks of each share
+// that share.
+constexpr int kCombineWarps = 8, kCombineBlocks = 8;
 
 template <int kD>
 __global__ void __launch_bounds__(kCombineWarps * 32)
     combine_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnDims d, int ctas,
                    int part_rows) {
-  const int lane = threadIdx.x & 31;
-  const int64_t item = int64_t(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5);
-  // Where the pieces are depends on the arguments only and is worked out while
-  // the attention kernel still runs; every thread waits for that kernel before
-  // it reads a piece or leaves.
-  const bool valid = item < a.n_nodes * a.n_q_heads;
-  const int64_t node = item / a.n_q_heads;
-  const int head = static_cast<int>(item % a.n_q_heads);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // Which unit is cut here depends on the arguments only and is worked out
+  // while the attention kernel still runs; every thread waits for that kernel
+  // before it reads a piece or leaves.
   const Batch batch = batch_of(a, d);
-  int64_t before = 0;
-  RequestShape r{};
-  bool found = false;
-  if (valid && !batch.deal.whole) scan_requests(a, d, batch.deal, [&](int64_t before_, int64_t, int64_t, const RequestShape& x) {
-    const unsigned here = __ballot_sync(0xffffffffu, node >= x.node0 && node < x.node0 + x.nodes);
-    if (!here) return false;
-    const int src = __ffs(here) - 1;
-    before = __shfl_sync(0xffffffffu, before_, src);
-    r.node0 = __shfl_sync(0xffffffffu, x.node0, src);
-    r.tiles = __shfl_sync(0xffffffffu, x.tiles, src);
-    r.row_units = __shfl_sync(0xffffffffu, x.row_units, src);
-    r.last_rows = __shfl_sync(0xffffffffu, x.last_rows, src);
-    found = true;
-    return true;
-  });
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!found || r.tiles == 0) return;
   const Deal& deal = batch.deal;
-  const int row = static_cast<int>(node - r.node0) * d.group + head % d.group;
-  const int u = row / kUnitRows, at = row % kUnitRows;
+  const int64_t runs = deal.runs(batch.total, ctas), c = int64_t(blockIdx.x) + 1;
+  const int64_t cut = Deal::run_start(batch.total, runs, c);
+  int64_t before = 0, b = -1;
+  if (!deal.whole && c < runs)
+    scan_requests(a, d, deal, [&](int64_t before_, int64_t cost, int64_t b_, const RequestShape&) {
+      const unsigned here = __ballot_sync(0xffffffffu, cost > 0 && before_ <= cut && cut < before_ + cost);
+      if (!here) return false;
+      const int src = __ffs(here) - 1;
+      before = __shfl_sync(0xffffffffu, before_, src);
+      b = __shfl_sync(0xffffffffu, b_, src);
+      return true;
+    });
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (b < 0) return;
+  const RequestShape r = request_shape(a, d, b);
+  const int64_t head_cost = deal.head(r), full = deal.unit(r.tiles, kUnitRows);
+  const int64_t h = (cut - before) / head_cost, in_head = (cut - before) - h * head_cost;
+  const int u = static_cast<int>(min(in_head / full, int64_t(r.row_units - 1)));
   const int rows = u == r.row_units - 1 ? r.last_rows : kUnitRows;
-  const int64_t s = before + (head / d.group) * deal.head(r) + u * deal.unit(r.tiles, kUnitRows);
-  const int64_t cost = deal.unit(r.tiles, rows);
-  const int64_t runs = deal.runs(batch.total, ctas);
+  const int64_t s = before + h * head_cost + u * full, cost = deal.unit(r.tiles, rows);
+  if (cut == s) return;  // the runs meet between units
   const int64_t c0 = Deal::run_of(batch.total, runs, s), c1 = Deal::run_of(batch.total, runs, s + cost - 1);
   const float* ws = static_cast<const float*>(a.workspace);
   const int64_t slot = int64_t(part_rows) * (kD + 2);
   constexpr int kPer = kD / 32;
-  float M = -INFINITY, L = 0.f, o[kPer] = {};
-  for (int64_t base = c0; base <= c1; base += 32) {
-    // a lane's piece: its place (-1: none), maximum and sum
-    const int64_t c = base + lane;
-    int64_t p = -1;
-    float2 x = make_float2(-INFINITY, 0.f);
-    if (c <= c1) {
-      const int64_t x0 = Deal::run_start(batch.total, runs, c) - s;
-      const int64_t x1 = Deal::run_start(batch.total, runs, c + 1) - s;
-      const int t0 = deal.tile_at(x0, r.tiles, rows);
-      const int t1 = x1 >= cost ? r.tiles : deal.tile_at(x1, r.tiles, rows);
-      if (t0 == 0 && t1 == r.tiles) p = -2;  // one CTA has it all
-      else if (t0 < t1) p = (c * 2 + (t0 > 0 ? 0 : 1)) * slot;
-      if (p >= 0) x = reinterpret_cast<const float2*>(ws + p + int64_t(part_rows) * kD)[at];
-    }
-    if (__any_sync(0xffffffffu, p == -2)) return;
-    float top = x.x;
+  // the meeting points inside the unit are the starts of runs c0 + 1 .. c1
+  const int64_t step = (c1 - c0) * kCombineBlocks * kCombineWarps;
+  for (int64_t at = ((c - c0 - 1) * kCombineBlocks + blockIdx.y) * kCombineWarps + warp; at < rows;
+       at += step) {
+    float M = -INFINITY, L = 0.f, o[kPer] = {};
+    for (int64_t base = c0; base <= c1; base += 32) {
+      // a lane's piece: its place (-1: none), maximum and sum
+      const int64_t ci = base + lane;
+      int64_t p = -1;
+      float2 x = make_float2(-INFINITY, 0.f);
+      if (ci <= c1) {
+        const int64_t x1 = Deal::run_start(batch.total, runs, ci + 1) - s;
+        const int t0 = deal.tile_at(Deal::run_start(batch.total, runs, ci) - s, r.tiles, rows);
+        const int t1 = x1 >= cost ? r.tiles : deal.tile_at(x1, r.tiles, rows);
+        if (t0 == 0 && t1 == r.tiles) p = -2;  // one CTA has all the tiles
+        else if (t0 < t1) p = (ci * 2 + (t0 > 0 ? 0 : 1)) * slot;
+        if (p >= 0) x = reinterpret_cast<const float2*>(ws + p + int64_t(part_rows) * kD)[at];
+      }
+      if (__any_sync(0xffffffffu, p == -2)) return;
+      float top = x.x;
 #pragma unroll
-    for (int k = 16; k >= 1; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-    const float mn = fmaxf(M, top), off = mn == -INFINITY ? 0.f : mn;
-    const float f = ex2(M - off), g = ex2(x.x - off);
-    L = L * f + warp_sum(x.y * g);
-    M = mn;
+      for (int k = 16; k >= 1; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+      const float mn = fmaxf(M, top), off = mn == -INFINITY ? 0.f : mn;
+      const float f = ex2(M - off), g = ex2(x.x - off);
+      L = L * f + warp_sum(x.y * g);
+      M = mn;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) o[k] *= f;
-    const int n = c1 - base < 31 ? static_cast<int>(c1 - base) + 1 : 32;
+      for (int k = 0; k < kPer; ++k) o[k] *= f;
+      const int n = c1 - base < 31 ? static_cast<int>(c1 - base) + 1 : 32;
 #pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-      const int64_t pi = __shfl_sync(0xffffffffu, p, i);
-      const float gi = __shfl_sync(0xffffffffu, g, i);
-      // (a NaN or infinity in a piece that counts for nothing stays out)
-      if (pi >= 0 && gi != 0.f) {
-        const float* src = ws + pi + int64_t(at) * kD + lane * kPer;
+      for (int i = 0; i < n; ++i) {
+        const int64_t pi = __shfl_sync(0xffffffffu, p, i);
+        const float gi = __shfl_sync(0xffffffffu, g, i);
+        // (a NaN or infinity in a piece that counts for nothing stays out)
+        if (pi >= 0 && gi != 0.f) {
+          const float* src = ws + pi + at * kD + lane * kPer;
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) o[k] = fmaf(gi, src[k], o[k]);
+          for (int k = 0; k < kPer; ++k) o[k] = fmaf(gi, src[k], o[k]);
+        }
       }
     }
-  }
-  bf16_t* dst = static_cast<bf16_t*>(a.out) + node * a.ld_on + int64_t(head) * a.ld_oh + lane * kPer;
+    const int i = u * kUnitRows + static_cast<int>(at);
+    const int64_t node = r.node0 + i / d.group, head = h * d.group + i % d.group;
+    bf16_t* dst = static_cast<bf16_t*>(a.out) + node * a.ld_on + head * a.ld_oh + lane * kPer;
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) Elem<bf16_t>::store1(dst + k, L == 0.f ? 0.f : o[k] / L);
-  if (a.lse && lane == 0) a.lse[item] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    for (int k = 0; k < kPer; ++k) Elem<bf16_t>::store1(dst + k, L == 0.f ? 0.f : o[k] / L);
+    if (a.lse && lane == 0)
+      a.lse[node * a.n_q_heads + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+  }
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 attn_encode_fn() {
@@ -1679,9 +1683,9 @@ cudaError_t launch_tensor(const AttnArgs& a, int sms, int device, cudaStream_t s
   cudaError_t e = cudaGetLastError();
   // units of so few tiles are never cut
   if (e != cudaSuccess || d.room <= kWholeTiles * kTile) return e;
-  const int64_t items = a.n_nodes * a.n_q_heads;
+  if (sms < 2) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((items + kCombineWarps - 1) / kCombineWarps));
+  cfg.gridDim = dim3(static_cast<unsigned>(sms - 1), kCombineBlocks);
   cfg.blockDim = dim3(kCombineWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
