@@ -220,7 +220,7 @@ struct KvWriteArgs {
   fct_kv_cache cache;
   int32_t* dev_status;
 };
-cudaError_t launch_kv_write(const KvWriteArgs& a, cudaStream_t st);
+cudaError_t launch_kv_write(const KvWriteArgs& a, int sms, cudaStream_t st);
 
 struct KvMoveArgs {
   fct_kv_cache cache;

@@ -93,7 +93,7 @@ int fct_kv_cache_write(const void* k, const void* v, int64_t ld_token, int64_t l
   if ((rc = fct::current_device_sms(&sms, &device)) != FCT_OK) return rc;
   return launched(fct::launch_kv_write(
       fct::KvWriteArgs{k, v, ld_token, ld_head, dtype, n_tokens, slots, *cache, dev_status},
-      static_cast<cudaStream_t>(stream)));
+      sms, static_cast<cudaStream_t>(stream)));
 }
 
 int fct_kv_cache_move(const fct_kv_cache* cache, const int32_t* block_table, int64_t ld_table,
