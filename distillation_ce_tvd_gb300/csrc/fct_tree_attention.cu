@@ -291,19 +291,24 @@ __device__ __forceinline__ RequestShape request_shape(const AttnArgs& a, const A
   return r;
 }
 
-// What the deal counts.  A unit costs kUnitCost for its start and end (as
-// measured, in key tiles of 128 rows) and each of its key tiles 1, or 2 with
-// both query tiles; the sum over all units is dealt in equal runs.  Where no
-// request has more than kWholeTiles tiles, a unit counts 1 and is never cut: a
-// second CTA would save less than combining costs.
-constexpr int kUnitCost = 3, kWholeTiles = 4, kMinRun = kUnitCost + 1;
+// What the deal counts.  A unit costs start_cost for its start and end (as
+// measured: 9 us, or 8 bf16 key tiles of 128 rows, or 3 of the slower e4m3
+// ones) and each of its key tiles 1, or 2 with both query tiles; the sum over
+// all units is dealt in equal runs.  48 requests of 450 to 8190 keys in bf16
+// took 190 us with a start cost of 3, 173 with 5, 167 with 7, 168 with 9; the
+// e4m3 trees 208 with 3, 211 with 5, 215 with 7.  Where no request has more
+// than kWholeTiles tiles, a unit counts 1 and is never cut: a second CTA would
+// save less than combining costs.
+constexpr int kWholeTiles = 4;
+__host__ __device__ constexpr int start_cost_of(bool fp8) { return fp8 ? 3 : 8; }
 
 struct Deal {
   bool whole;
+  int start_cost;
   // of a unit with `rows` rows of a request with `tiles` tiles
   __device__ __forceinline__ int per_tile(int rows) const { return rows > kTile ? 2 : 1; }
   __device__ __forceinline__ int64_t unit(int tiles, int rows) const {
-    return whole ? 1 : kUnitCost + int64_t(tiles) * per_tile(rows);
+    return whole ? 1 : start_cost + int64_t(tiles) * per_tile(rows);
   }
   __device__ __forceinline__ int64_t head(const RequestShape& r) const {
     return r.row_units == 0 ? 0
@@ -314,15 +319,15 @@ struct Deal {
   }
   // The first tile that starts at cost x of the unit or later.
   __device__ __forceinline__ int tile_at(int64_t x, int tiles, int rows) const {
-    if (x <= 0 || (!whole && x <= kUnitCost)) return 0;
+    if (x <= 0 || (!whole && x <= start_cost)) return 0;
     if (whole) return tiles;
     const int per = per_tile(rows);
-    const int64_t n = (x - kUnitCost + per - 1) / per;
+    const int64_t n = (x - start_cost + per - 1) / per;
     return n < tiles ? static_cast<int>(n) : tiles;
   }
   // How many CTAs share `total`, and where CTA c's run starts.
   __device__ __forceinline__ int64_t runs(int64_t total, int64_t ctas) const {
-    const int64_t most = whole ? total : (total + kMinRun - 1) / kMinRun;
+    const int64_t most = whole ? total : (total + start_cost) / (start_cost + 1);
     return most < ctas ? most : ctas;
   }
   __device__ __forceinline__ static int64_t run_start(int64_t total, int64_t runs, int64_t c) {
@@ -343,6 +348,7 @@ struct Batch {
 };
 __device__ __forceinline__ Batch batch_of(const AttnArgs& a, const AttnDims& d) {
   const int lane = threadIdx.x & 31;
+  const int start_cost = start_cost_of(a.cache.dtype == FCT_E4M3);
   int most = 0;
   int64_t cost[2] = {0, 0};
   bool bad = false;
@@ -351,8 +357,8 @@ __device__ __forceinline__ Batch batch_of(const AttnArgs& a, const AttnDims& d) 
     const RequestShape r = request_shape(a, d, b);
     bad |= r.bad;
     if (r.nodes > 0) most = max(most, r.tiles);
-    cost[0] += Deal{false}.request(r, a.cache.n_heads);
-    cost[1] += Deal{true}.request(r, a.cache.n_heads);
+    cost[0] += Deal{false, start_cost}.request(r, a.cache.n_heads);
+    cost[1] += Deal{true, start_cost}.request(r, a.cache.n_heads);
   }
 #pragma unroll
   for (int k = 16; k >= 1; k >>= 1) {
@@ -361,7 +367,7 @@ __device__ __forceinline__ Batch batch_of(const AttnArgs& a, const AttnDims& d) 
     cost[1] += __shfl_xor_sync(0xffffffffu, cost[1], k);
   }
   const bool whole = most <= kWholeTiles;
-  return Batch{Deal{whole}, cost[whole ? 1 : 0], __any_sync(0xffffffffu, bad) != 0};
+  return Batch{Deal{whole, start_cost}, cost[whole ? 1 : 0], __any_sync(0xffffffffu, bad) != 0};
 }
 // f(before, cost, b, shape) for the request of every lane, 32 at a time,
 // until f says (to the whole warp) that it has what it looked for.
@@ -853,7 +859,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
   __syncthreads();
   tc_after();
   const uint32_t tmem = ctl.tmem_base;
-  SegmentWalk walk(a, d, Deal{ctl.sched[3] != 0}, ctl.sched[0], ctl.sched[1], ctl.sched[2]);
+  SegmentWalk walk(a, d, Deal{ctl.sched[3] != 0, start_cost_of(kFp8)}, ctl.sched[0], ctl.sched[1], ctl.sched[2]);
   Segment seg;
   auto lead_of = [](const Segment& s) { return s.rows > kTile ? 1 : 2; };
   // whether a key tile (index in the unit) reaches past the context

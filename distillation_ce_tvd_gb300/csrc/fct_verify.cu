@@ -318,6 +318,8 @@ struct Nodes {
   int64_t tokens[kNodeCap];
   int32_t parent[kNodeCap];
   float uniform[kNodeCap];
+  int32_t child[kNodeCap];    // the first one, INT_MAX if none
+  int32_t sibling[kNodeCap];  // the next one, -1 if none
 };
 
 __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -375,7 +377,18 @@ __global__ void __launch_bounds__(kVThreads, 1)
     held.tokens[i] = a.tokens[first + i];
     held.parent[i] = a.parent[first + i];
     held.uniform[i] = a.uniform[first + i];
+    held.child[i] = INT_MAX;
   }
+  __syncthreads();
+  const bool small = nodes <= kNodeCap;  // children are looked up in the tables
+  if (small)
+    for (int i = threadIdx.x; i < nodes; i += kVThreads) {
+      const int p = held.parent[i];
+      if (p >= 0 && p < i) atomicMin(&held.child[p], i);
+      int next = i + 1;
+      while (next < nodes && held.parent[next] != p) ++next;
+      held.sibling[i] = p >= 0 && next < nodes ? next : -1;
+    }
   const float temp = a.temperature ? a.temperature[b] : 1.f;
   const bool greedy = !(temp > 0.f);
   const float k = greedy ? kLog2e : kLog2e / temp;
@@ -393,6 +406,10 @@ __global__ void __launch_bounds__(kVThreads, 1)
   // The first child of `at` after node c, or -1.  Every warp looks for itself
   // and gets the same answer.
   auto next_child = [&](int at, int c) {
+    if (small) {
+      const int next = c == at ? held.child[at] : held.sibling[c];
+      return next == INT_MAX ? -1 : next;
+    }
     for (int c0 = c + 1; c0 < nodes; c0 += 32) {
       const int i = c0 + lane;
       const unsigned hit = __ballot_sync(0xffffffffu, i < nodes && parent(i) == at);
