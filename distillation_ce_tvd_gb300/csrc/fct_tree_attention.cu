@@ -211,9 +211,9 @@ template <int kD, bool kFp8>
 struct AttnShape {
   // Warps: 0 loads, 1 products, 4-11 softmax; e4m3: 2 and 3 fetch scale bytes,
   // 12-19 prepare; bf16: 2 prepares, 3 loads V (0 loads K).
-  static constexpr int kThreads = kFp8 ? 512 : 384;
+  static constexpr int kThreads = kFp8 ? 640 : 384;
   static constexpr int kPrepWarp0 = kFp8 ? 12 : 2, kPrepWarps = kFp8 ? 4 : 1;  // per tile
-  [[maybe_unused]] static constexpr int kPrepGroups = 1;  // taking tiles in turn
+  [[maybe_unused]] static constexpr int kPrepGroups = kFp8 ? 2 : 1;  // taking tiles in turn
   // Score chunks of 32 keys that a softmax thread holds: what the registers of
   // 65536 / kThreads allow without spilling.
   static constexpr int kHold = 1;
