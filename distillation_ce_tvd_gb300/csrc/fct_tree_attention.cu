@@ -213,7 +213,7 @@ struct AttnShape {
   // 12-19 prepare; bf16: 2 prepares, 3 loads V (0 loads K).
   static constexpr int kThreads = kFp8 ? 640 : 384;
   static constexpr int kPrepWarp0 = kFp8 ? 12 : 2, kPrepWarps = kFp8 ? 4 : 1;  // per tile
-  [[maybe_unused]] static constexpr int kPrepGroups = kFp8 ? 2 : 1;  // taking tiles in turn
+  static constexpr int kPrepGroups = kFp8 ? 2 : 1;  // taking tiles in turn
   // Score chunks of 32 keys that a softmax thread holds: what the registers of
   // 65536 / kThreads allow without spilling.
   static constexpr int kHold = 1;
@@ -221,7 +221,7 @@ struct AttnShape {
   static constexpr uint32_t kTileBytes = kTile * kD * 2;
   static constexpr uint32_t kRawBytes = kTile * kD;
   static constexpr int kSlots = kD == 128 ? (kFp8 ? 3 : 5) : (kFp8 ? 4 : 8);
-  [[maybe_unused]] static constexpr int kRing = kFp8 ? (kD == 128 ? 4 : 8) : 1;  // raw slots (1 where unused)
+  static constexpr int kRing = kFp8 ? (kD == 128 ? 4 : 8) : 1;  // raw slots (1 where unused)
   static constexpr int kRaw = kFp8 ? (kD == 128 ? 4 : 8) : 0;
   static constexpr size_t kTilesBytes =
       2 * kTileBytes + size_t(kSlots) * kTileBytes + size_t(kRaw) * kRawBytes;
@@ -241,6 +241,7 @@ struct AttnShape {
     uint8_t raw_scale[kRaw ? kRaw : 1][kRaw ? kTile : 1];
   };
   static constexpr size_t kSmem = kTilesBytes + sizeof(Control);
+  static_assert(kRing >= 1 && kPrepGroups >= 1, "a ring and a group at least");
   static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
 
@@ -322,7 +323,7 @@ struct Deal {
     if (x <= 0 || (!whole && x <= start_cost)) return 0;
     if (whole) return tiles;
     const int per = per_tile(rows);
-    const int64_t n = (x - start_cost + per - 1) / per;
+    const int64_t n = (x - start_cost + per - 1) >> (per - 1);  // per is 1 or 2
     return n < tiles ? static_cast<int>(n) : tiles;
   }
   // How many CTAs share `total`, and where CTA c's run starts.
