@@ -19,6 +19,9 @@ namespace {
 // keys.  In a warp, `lanes` threads (a power of two, head_dim / 8 rounded up)
 // hold a key's vector, 8 elements each, so a warp looks at 32 / lanes keys at
 // a time.  Any page size, head_dim and stride that fct_kv_cache takes.
+// Every query head of every node reads its keys for itself, so what bounds it
+// is loads and CUDA-core arithmetic: 48 requests x 5 nodes, 32 query and 8 kv
+// heads of 128, 450 to 8190 keys in bf16 took it 4.7 ms.
 
 constexpr int kGWarps = 4;
 
@@ -188,12 +191,23 @@ cudaError_t launch_general(const AttnArgs& a, cudaStream_t st) {
 // equal runs, whatever the requests' lengths; a unit cut between CTAs leaves
 // partial sums in the workspace, which combine_kernel adds in order.
 //
-// Per CTA: warp 0 loads tiles by TMA (one box per page piece), warp 1 issues
-// the products, warps 4-7 and 8-11 are the softmax groups, warps 12-15
-// prepare tiles: they turn e4m3 tiles into bf16 (exact: payload times a power
-// of two), and clear what must not reach a product from the tiles past the
-// context (slots past the end, and non-finite values of drafted nodes, which
-// are added back to the rows that see them).
+// What bounds it: with few rows the bytes of the keys (1 x 8 nodes, 32 query
+// and 8 kv heads of 128, 131071 keys in bf16: 537 MB in 99 us, 5.4 TB/s; 48
+// requests x 5 nodes, 870 MB: 166 us); with 256 rows per unit neither (12 x 64
+// nodes, 64 query heads: 118 GFLOP in 164 us, 0.72 PFLOP/s; without softmax
+// and most products a copy still took 156 of then 184 us); in e4m3 the
+// conversion and the hand-over of tiles between the roles (20 x 27 nodes,
+// 400 MB: 191 us, 2.1 TB/s; 208 with one converting group instead of two, 159
+// without the conversion).
+//
+// Per CTA: warp 1 issues the products, warps 4-7 and 8-11 are the softmax
+// groups.  bf16: warps 0 and 3 load K and V tiles by TMA (one box per page
+// piece), warp 2 prepares the tiles past the context.  e4m3: warp 0 loads,
+// warps 2 and 3 fetch the scale bytes, warps 12-15 and 16-19 prepare tiles in
+// turn: they make them bf16 (exact: payload times a power of two).  Preparing
+// clears what must not reach a product from the tiles past the context (slots
+// past the end, and non-finite values of drafted nodes, which are added back
+// to the rows that see them).
 
 constexpr int kTile = 128;      // keys per tile, rows per query tile
 constexpr int kSoftWarps = 8;
@@ -1519,7 +1533,9 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
 // order of the keys, one row to a warp.  A unit is cut where runs meet, so
 // blockIdx.x stands for the start of run blockIdx.x + 1: the meeting points
 // inside one unit share its rows, and the kCombineBlocks blocks of each share
-// that share.
+// that share.  A chain of dependent loads and few bytes: latency bounds it.  12
+// x 64 nodes of 64 query heads took 171 us in all this way, 182 with one grid
+// over all rows, most of which no unit's cut touches.
 constexpr int kCombineWarps = 8, kCombineBlocks = 8;
 
 template <int kD>

@@ -669,6 +669,7 @@ int fused_ce_tvd_vp_backward(const void* student, int64_t ld_student,
  *              scale_slot_stride + h * scale_head_stride: the value held is
  *              payload * 2^(byte - 127), and byte 255 makes the vector NaN.
  *   head_dim : a multiple of 8, at most 256, else FCT_ERR_UNSUPPORTED.
+ *   n_heads  : at most 65536, num_pages at most 2^40, else FCT_ERR_UNSUPPORTED.
  *   k, v     : aligned to 8 elements, strides multiples of 8 elements, else
  *              FCT_ERR_ALIGNMENT.  Distinct (p, s, h) must not overlap.
  */
@@ -805,6 +806,8 @@ int fct_tree_attention(const void* q, int64_t ld_q_node, int64_t ld_q_head,
  *                 token, then -1.
  *   path        : (batch, max_depth) int32: the accepted nodes, then -1.
  *   count       : (batch,) int32: accepted tokens.
+ * V is at most 2^30, and batch at most 2^24 here, in fct_tree_attention and in
+ * fct_kv_cache_move, else FCT_ERR_UNSUPPORTED.
  * A visited row without a distribution (a NaN, +inf, or nothing above -inf)
  * accepts nothing, gives the next token -1 and sets FCT_DEV_NO_DISTRIBUTION.
  * A request without nodes gets count 0 and tokens -1.
