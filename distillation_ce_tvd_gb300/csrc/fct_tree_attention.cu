@@ -203,8 +203,10 @@ cudaError_t launch_general(const AttnArgs& a, cudaStream_t st) {
 // Per CTA: warp 1 issues the products, warps 4-7 and 8-11 are the softmax
 // groups.  bf16: warps 0 and 3 load K and V tiles by TMA (one box per page
 // piece), warp 2 prepares the tiles past the context.  e4m3: warp 0 loads,
-// warps 2 and 3 fetch the scale bytes, warps 12-15 and 16-19 prepare tiles in
-// turn: they make them bf16 (exact: payload times a power of two).  Preparing
+// warps 2 and 3 fetch the scale bytes, warps 12-19 prepare every tile: they make
+// it bf16 (exact: payload times a power of two) in its slot, since a row of 128
+// payload bytes lands where that row's second half of bf16 goes, and one warp
+// reads and writes the row; a row of 64 lands behind the slot's tile.  Preparing
 // clears what must not reach a product from the tiles past the context (slots
 // past the end, and non-finite values of drafted nodes, which are added back
 // to the rows that see them).
@@ -226,36 +228,38 @@ struct AttnShape {
   // Warps: 0 loads, 1 products, 4-11 softmax; e4m3: 2 and 3 fetch scale bytes,
   // 12-19 prepare; bf16: 2 prepares, 3 loads V (0 loads K).
   static constexpr int kThreads = kFp8 ? 640 : 384;
-  static constexpr int kPrepWarp0 = kFp8 ? 12 : 2, kPrepWarps = kFp8 ? 4 : 1;  // per tile
-  static constexpr int kPrepGroups = kFp8 ? 2 : 1;  // taking tiles in turn
+  static constexpr int kPrepWarp0 = kFp8 ? 12 : 2, kPrepWarps = kFp8 ? 8 : 1;
   // Score chunks of 32 keys that a softmax thread holds: what the registers of
   // 65536 / kThreads allow without spilling.
   static constexpr int kHold = 1;
   static constexpr int kHalves = kD / 64;  // 128-byte column blocks of a bf16 row
   static constexpr uint32_t kTileBytes = kTile * kD * 2;
-  static constexpr uint32_t kRawBytes = kTile * kD;
-  static constexpr int kSlots = kD == 128 ? (kFp8 ? 3 : 5) : (kFp8 ? 4 : 8);
-  static constexpr int kRing = kFp8 ? (kD == 128 ? 4 : 8) : 1;  // raw slots (1 where unused)
-  static constexpr int kRaw = kFp8 ? (kD == 128 ? 4 : 8) : 0;
-  static constexpr size_t kTilesBytes =
-      2 * kTileBytes + size_t(kSlots) * kTileBytes + size_t(kRaw) * kRawBytes;
-  // After the tiles (two of Q, the ring of K and V, the ring of e4m3 tiles).
+  // An e4m3 tile lands kRawAt bytes into its slot, in rows of kD bytes.
+  static constexpr uint32_t kRawAt = kFp8 ? kTile * 128 : 0;
+  static constexpr uint32_t kSlotBytes = kFp8 ? kRawAt + (kD == 128 ? kTile * 128 : kTile * kD) : kTileBytes;
+  static_assert(kSlotBytes >= kTileBytes && kSlotBytes % 1024 == 0, "a slot holds a tile");
+  static constexpr int kSlots = kD == 128 ? 5 : (kFp8 ? 7 : 8);
+  static constexpr int kRaw = kFp8 ? kSlots : 1;    // (1 where unused)
+  static constexpr int kTail = kFp8 ? 1 : kSlots;
+  static constexpr size_t kTilesBytes = 2 * kTileBytes + size_t(kSlots) * kSlotBytes;
+  // After the tiles (two of Q, the ring of K and V).
   struct Control {
     uint64_t full_bar[kSlots], empty_bar[kSlots];
     // bf16: a V tile past the context lands on tail_full and is handed on by
-    // the preparing warps on prep_bar, instead of full_bar
-    uint64_t tail_full[kSlots], prep_bar[kSlots];
-    uint64_t raw_full[kRaw + 1], raw_scaled[kRaw + 1], raw_empty[kRaw + 1];
+    // the preparing warp on prep_bar, instead of full_bar
+    uint64_t tail_full[kTail], prep_bar[kTail];
+    // e4m3: a tile and its scale bytes land on these, and full_bar says that it
+    // is bf16
+    uint64_t raw_full[kRaw], raw_scaled[kRaw];
     uint64_t s_full[2], p_full[2], q_full, o_full, ml_full, done_bar;
     int64_t sched[4];     // the run: request, offset in it, length; whether units are whole
     float2 ml[2][kTile];  // the groups' maxima and sums, lane by lane
     uint32_t tmem_base;
     int abort_flag;
     int bad_seg[kBadRing];
-    uint8_t raw_scale[kRaw ? kRaw : 1][kRaw ? kTile : 1];
+    uint8_t raw_scale[kRaw][kFp8 ? kTile : 4];
   };
   static constexpr size_t kSmem = kTilesBytes + sizeof(Control);
-  static_assert(kRing >= 1 && kPrepGroups >= 1, "a ring and a group at least");
   static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
 
@@ -813,20 +817,20 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
     return;
   }
   const uint32_t slot0 = smem0 + 2 * Sh::kTileBytes;
-  const uint32_t raw0 = slot0 + Sh::kSlots * Sh::kTileBytes;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < Sh::kSlots; ++i) {
       mbar_init(&ctl.full_bar[i], kFp8 ? Sh::kPrepWarps : 1);
       mbar_init(&ctl.empty_bar[i], 1);
+    }
+    for (int i = 0; i < Sh::kTail; ++i) {
       mbar_init(&ctl.tail_full[i], 1);
       mbar_init(&ctl.prep_bar[i], Sh::kPrepWarps);
     }
     for (int i = 0; i < Sh::kRaw; ++i) {
       mbar_init(&ctl.raw_full[i], 1);
       mbar_init(&ctl.raw_scaled[i], 1);
-      mbar_init(&ctl.raw_empty[i], Sh::kPrepWarps);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&ctl.s_full[w], 1);
@@ -883,11 +887,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
   // ---- loads: a warp sends K tiles, V tiles or both, its lanes a tile's boxes
   auto load_tiles = [&](bool do_k, bool do_v) {
     constexpr int kBoxCols = kFp8 ? 1 : Sh::kHalves;
-    constexpr int kRing = kFp8 ? Sh::kRaw : Sh::kSlots;
     uint64_t* full = kFp8 ? ctl.raw_full : ctl.full_bar;
-    uint64_t* empty = kFp8 ? ctl.raw_empty : ctl.empty_bar;
-    const uint32_t ring0 = kFp8 ? raw0 : slot0;
-    constexpr uint32_t kItemBytes = kFp8 ? Sh::kRawBytes : Sh::kTileBytes;
     const int boxes = kTile / box_rows * kBoxCols;
     const uint32_t box_bytes = uint32_t(box_rows) * (kFp8 ? kD : 128);
     const int page_size = a.cache.page_size;
@@ -921,7 +921,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
       };
       ask();
       for_items(seg.tiles, lead_of(seg), [&](bool is_v, int j) {
-        const uint32_t slot = item % kRing, phase = (item / kRing) & 1u;
+        const uint32_t slot = item % Sh::kSlots, phase = (item / Sh::kSlots) & 1u;
         ++item;
         const bool prep = !kFp8 && is_v && is_tail(seg, seg.tile0 + j);
         last_tail = (last_tail & ~(1u << slot)) | (uint32_t(prep) << slot);
@@ -936,7 +936,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
           ask();
         }
         if (!(is_v ? do_v : do_k)) return true;
-        if (!warp_wait(&empty[slot], phase ^ 1u, &ctl.abort_flag)) {
+        if (!warp_wait(&ctl.empty_bar[slot], phase ^ 1u, &ctl.abort_flag)) {
           ok = false;
           return false;
         }
@@ -954,7 +954,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
               at = slots[i];
             }
           if (page < 0 || page >= a.cache.num_pages) status |= FCT_DEV_INDEX_OUT_OF_RANGE;
-          const uint32_t dst = ring0 + slot * kItemBytes +
+          const uint32_t dst = slot0 + slot * Sh::kSlotBytes + Sh::kRawAt +
                                (kFp8 ? uint32_t(piece) * box_bytes
                                      : uint32_t(half) * (kTile * 128) + uint32_t(piece) * box_bytes);
           tma_box(dst, is_v ? &map_v : &map_k, half * 64, at, seg.h, page, bar);
@@ -964,7 +964,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
     }
     // the last fills have landed before the CTA ends (bounded, even after an
     // abort)
-    for (uint32_t slot = 0; slot < uint32_t(kRing) && slot < item; ++slot) {
+    for (uint32_t slot = 0; slot < uint32_t(Sh::kSlots) && slot < item; ++slot) {
       const bool tail = (last_tail >> slot) & 1u;
       wait_phase(tail ? &ctl.tail_full[slot] : &full[slot],
                  (((tail ? tail_phase : full_phase) >> slot) & 1u) ^ 1u, &ctl.abort_flag, false);
@@ -975,7 +975,6 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
     // ---- tiles prepared
     constexpr int kPrepThreads = Sh::kPrepWarps * 32;
     const int t = (threadIdx.x - Sh::kPrepWarp0 * 32) % kPrepThreads;
-    const uint32_t group = (warp - Sh::kPrepWarp0) / Sh::kPrepWarps;
     uint32_t item = 0, tail_phase = 0;
     int seg_n = 0;
     bool ok = true;
@@ -985,28 +984,24 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
         const uint32_t it = item++;
         const uint32_t slot = it % Sh::kSlots;
         const int tile = seg.tile0 + j, p0 = tile * kTile;
-        const uint32_t dst = slot0 + slot * Sh::kTileBytes;
+        const uint32_t dst = slot0 + slot * Sh::kSlotBytes;
         if constexpr (kFp8) {
-          const uint32_t r = it % Sh::kRaw;
-          // (a group waits for the slots of the other's tiles too, so that it is
-          // never a phase behind when it waits for its own)
-          ok = warp_wait(&ctl.empty_bar[slot], ((it / Sh::kSlots) & 1u) ^ 1u, &ctl.abort_flag);
-          if (!ok || it % Sh::kPrepGroups != group) return ok;
-          static_assert(Sh::kRaw % Sh::kPrepGroups == 0, "a raw slot belongs to one group");
-          if (!warp_wait(&ctl.raw_full[r], (it / Sh::kRaw) & 1u, &ctl.abort_flag) ||
-              !warp_wait(&ctl.raw_scaled[r], (it / Sh::kRaw) & 1u, &ctl.abort_flag)) {
+          const uint32_t phase = (it / Sh::kSlots) & 1u;
+          if (!warp_wait(&ctl.raw_full[slot], phase, &ctl.abort_flag) ||
+              !warp_wait(&ctl.raw_scaled[slot], phase, &ctl.abort_flag)) {
             ok = false;
             return false;
           }
           // A thread takes 16-byte pieces t % 4 (+ 4) of row t / 4 of each kRows rows:
           // eight lanes store to different banks, and every address but the
           // first is a constant away.  The next row is loaded before the present
-          // one is turned.
+          // one is turned; a row's four lanes have all loaded it before any of
+          // them stores to it.
           constexpr int kHalves = Sh::kHalves, kRows = kPrepThreads / 4;
-          const uint32_t src = raw0 + r * Sh::kRawBytes + uint32_t(t / 4) * kD + uint32_t(t % 4) * 16;
+          const uint32_t src = dst + Sh::kRawAt + uint32_t(t / 4) * kD + uint32_t(t % 4) * 16;
           const uint32_t out0 = dst + uint32_t(t / 4) * 128 + uint32_t((((t % 4) * 2) ^ ((t / 4) & 7)) * 16);
           const uint32_t out1 = out0 ^ 16u;
-          const uint32_t scale = smem_addr(&ctl.raw_scale[r][t / 4]);
+          const uint32_t scale = smem_addr(&ctl.raw_scale[slot][t / 4]);
           const bool clear = is_v && is_tail(seg, tile);
           bool found = false;
           uint32_t in[kHalves][4], byte;
@@ -1027,6 +1022,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
 #pragma unroll
               for (int k = 0; k < 4; ++k) x[h][k] = in[h][k];
             if (block + 1 < kTile / kRows) load(block + 1);
+            __syncwarp();
             if (clear) {
               const int pos = p0 + block * kRows + t / 4;
               if (pos >= seg.ctx && (pos >= seg.len || e == 255)) {
@@ -1063,7 +1059,6 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
           }
           if (found) ctl.bad_seg[seg_n % kBadRing] = seg_n;
           async_fence();
-          warp_arrive(&ctl.raw_empty[r]);
           warp_arrive(&ctl.full_bar[slot]);
         } else {
           if (!is_v || !is_tail(seg, tile)) return true;
@@ -1076,7 +1071,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
           constexpr int kPieces = kD / 8, kBatch = 8;
           const int from = max(seg.ctx - p0, 0);
           const int held = min(seg.len - p0, kTile);  // rows from here on are cleared
-          uint8_t* tile_at = attn_smem + (2 + slot) * Sh::kTileBytes;
+          uint8_t* tile_at = attn_smem + 2 * Sh::kTileBytes + slot * Sh::kSlotBytes;
           auto place = [&](int n) {
             const int row = n / kPieces, c = n % kPieces;
             return reinterpret_cast<uint4*>(tile_at + (c / 8) * (kTile * 128) + row * 128 + ((c % 8) ^ (row & 7)) * 16);
@@ -1129,7 +1124,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
     uint32_t p_phase = 0;
     bool ok = true;
     const bool issue = elect_one();
-    auto slot_addr = [&](uint32_t it) { return uniform(slot0 + (it % Sh::kSlots) * Sh::kTileBytes); };
+    auto slot_addr = [&](uint32_t it) { return uniform(slot0 + (it % Sh::kSlots) * Sh::kSlotBytes); };
     auto wait_item = [&](uint32_t it) {
       const uint32_t slot = it % Sh::kSlots;
       const bool got = warp_wait(&ctl.full_bar[slot], (full_phase >> slot) & 1u, &ctl.abort_flag);
@@ -1227,11 +1222,11 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
     uint32_t held = 0;  // four bytes
     bool ok = true, holds = false;
     auto hand_on = [&]() {
-      const uint32_t r = held_item % Sh::kRing, phase = (held_item / Sh::kRing) & 1u;
-      ok = warp_wait(&ctl.raw_empty[r], phase ^ 1u, &ctl.abort_flag);
+      const uint32_t slot = held_item % Sh::kSlots, phase = (held_item / Sh::kSlots) & 1u;
+      ok = warp_wait(&ctl.empty_bar[slot], phase ^ 1u, &ctl.abort_flag);
       if (!ok) return;
-      *reinterpret_cast<uint32_t*>(&ctl.raw_scale[r][4 * lane]) = held;
-      warp_arrive(&ctl.raw_scaled[r]);
+      *reinterpret_cast<uint32_t*>(&ctl.raw_scale[slot][4 * lane]) = held;
+      warp_arrive(&ctl.raw_scaled[slot]);
     };
     while (ok && walk.next(seg)) {
       for_items(seg.tiles, lead_of(seg), [&](bool is_v, int j) {
