@@ -1528,64 +1528,107 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
 // order of the keys, one row to a warp.  A unit is cut where runs meet, so
 // blockIdx.x stands for the start of run blockIdx.x + 1: the meeting points
 // inside one unit share its rows, and the kCombineBlocks blocks of each share
-// that share.  A chain of dependent loads and few bytes: latency bounds it.  12
-// x 64 nodes of 64 query heads took 171 us in all this way, 182 with one grid
-// over all rows, most of which no unit's cut touches.
-constexpr int kCombineWarps = 8, kCombineBlocks = 8;
+// that share.  Few bytes: what bounds it is the latency of a block's start, of
+// working out its unit and of the loads of a piece.  8, 16 and 32 blocks of 8
+// warps per meeting point, each warp working its unit out, took 1 x 8 nodes
+// over 131071 keys 101, 108 and 126 us in all; 2 blocks of 16 warps and one
+// warp to work it out 97 (12 x 64 nodes of 64 query heads: 164 -> 156).
+constexpr int kCombineWarps = 16, kCombineBlocks = 2;
 
 template <int kD>
 __global__ void __launch_bounds__(kCombineWarps * 32)
     combine_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnDims d, int ctas,
                    int part_rows) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // Which unit is cut here depends on the arguments only and is worked out
-  // while the attention kernel still runs; every thread waits for that kernel
-  // before it reads a piece or leaves.
-  const Batch batch = batch_of(a, d);
-  const Deal& deal = batch.deal;
-  const int64_t runs = deal.runs(batch.total, ctas), c = int64_t(blockIdx.x) + 1;
-  const int64_t cut = Deal::run_start(batch.total, runs, c);
-  int64_t before = 0, b = -1;
-  if (!deal.whole && c < runs)
-    scan_requests(a, d, deal, [&](int64_t before_, int64_t cost, int64_t b_, const RequestShape&) {
-      const unsigned here = __ballot_sync(0xffffffffu, cost > 0 && before_ <= cut && cut < before_ + cost);
-      if (!here) return false;
-      const int src = __ffs(here) - 1;
-      before = __shfl_sync(0xffffffffu, before_, src);
-      b = __shfl_sync(0xffffffffu, b_, src);
-      return true;
-    });
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (b < 0) return;
-  const RequestShape r = request_shape(a, d, b);
-  const int64_t head_cost = deal.head(r), full = deal.unit(r.tiles, kUnitRows);
-  const int64_t h = (cut - before) / head_cost, in_head = (cut - before) - h * head_cost;
-  const int u = static_cast<int>(min(in_head / full, int64_t(r.row_units - 1)));
-  const int rows = u == r.row_units - 1 ? r.last_rows : kUnitRows;
-  const int64_t s = before + h * head_cost + u * full, cost = deal.unit(r.tiles, rows);
-  if (cut == s) return;  // the runs meet between units
-  const int64_t c0 = Deal::run_of(batch.total, runs, s), c1 = Deal::run_of(batch.total, runs, s + cost - 1);
+  // Which unit is cut here depends on the arguments only.  One warp works it out
+  // for the block: it is 64-bit divisions mostly, and those of 16 warps took
+  // longer than the rows.  Every thread waits for the attention kernel before
+  // it reads a piece or leaves.
+  __shared__ struct {
+    int64_t total, runs, c0, c1, s, cost, h, node0, first[32];
+    int rows, u, tiles;
+  } cut;
+  constexpr int kPer = kD / 32;
+  const int64_t c = int64_t(blockIdx.x) + 1;
   const float* ws = static_cast<const float*>(a.workspace);
   const int64_t slot = int64_t(part_rows) * (kD + 2);
-  constexpr int kPer = kD / 32;
+  // Where a run's piece of the unit lies: -1 if it has none, -2 if it has all of
+  // the tiles.  The same for every row.
+  // (units are only cut where they are not dealt whole)
+  const Deal cut_deal{false, start_cost_of(a.cache.dtype == FCT_E4M3)};
+  auto piece_at = [&](int64_t ci) -> int64_t {
+    if (ci > cut.c1) return -1;
+    const int64_t x1 = Deal::run_start(cut.total, cut.runs, ci + 1) - cut.s;
+    const int t0 = cut_deal.tile_at(Deal::run_start(cut.total, cut.runs, ci) - cut.s, cut.tiles, cut.rows);
+    const int t1 = x1 >= cut.cost ? cut.tiles : cut_deal.tile_at(x1, cut.tiles, cut.rows);
+    if (t0 == 0 && t1 == cut.tiles) return -2;
+    return t0 < t1 ? (ci * 2 + (t0 > 0 ? 0 : 1)) * slot : -1;
+  };
+  if (warp == 0) {
+    const Batch batch = batch_of(a, d);
+    const Deal& deal = batch.deal;
+    const int64_t runs = deal.runs(batch.total, ctas);
+    const int64_t at = Deal::run_start(batch.total, runs, c);
+    int64_t before = 0, b = -1;
+    if (!deal.whole && c < runs)
+      scan_requests(a, d, deal, [&](int64_t before_, int64_t cost, int64_t b_, const RequestShape&) {
+        const unsigned here = __ballot_sync(0xffffffffu, cost > 0 && before_ <= at && at < before_ + cost);
+        if (!here) return false;
+        const int src = __ffs(here) - 1;
+        before = __shfl_sync(0xffffffffu, before_, src);
+        b = __shfl_sync(0xffffffffu, b_, src);
+        return true;
+      });
+    int rows = 0;  // 0: the runs meet between units, or there is no run
+    if (b >= 0) {
+      const RequestShape r = request_shape(a, d, b);
+      const int64_t head_cost = deal.head(r), full = deal.unit(r.tiles, kUnitRows);
+      const int64_t h = (at - before) / head_cost, in_head = (at - before) - h * head_cost;
+      const int u = static_cast<int>(min(in_head / full, int64_t(r.row_units - 1)));
+      const int64_t s = before + h * head_cost + u * full;
+      if (at != s) {
+        rows = u == r.row_units - 1 ? r.last_rows : kUnitRows;
+        const int64_t cost = deal.unit(r.tiles, rows);
+        if (lane == 0) {
+          cut.total = batch.total;
+          cut.runs = runs;
+          cut.c0 = Deal::run_of(batch.total, runs, s);
+          cut.c1 = Deal::run_of(batch.total, runs, s + cost - 1);
+          cut.s = s;
+          cut.cost = cost;
+          cut.h = h;
+          cut.node0 = r.node0;
+          cut.u = u;
+          cut.tiles = r.tiles;
+        }
+      }
+    }
+    if (lane == 0) cut.rows = rows;
+    __syncwarp();
+    if (rows > 0) cut.first[lane] = piece_at(cut.c0 + lane);
+  }
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int rows = cut.rows, u = cut.u;
+  if (rows == 0) return;
+  const int64_t c0 = cut.c0, c1 = cut.c1, h = cut.h;
+  // a piece's maximum and sum of row `at`
+  auto stats = [&](int64_t p, int64_t at) {
+    return p >= 0 && at < rows ? reinterpret_cast<const float2*>(ws + p + int64_t(part_rows) * kD)[at]
+                               : make_float2(-INFINITY, 0.f);
+  };
+  const int64_t first = cut.first[lane];
   // the meeting points inside the unit are the starts of runs c0 + 1 .. c1
   const int64_t step = (c1 - c0) * kCombineBlocks * kCombineWarps;
-  for (int64_t at = ((c - c0 - 1) * kCombineBlocks + blockIdx.y) * kCombineWarps + warp; at < rows;
-       at += step) {
+  const int64_t at0 = ((c - c0 - 1) * kCombineBlocks + blockIdx.y) * kCombineWarps + warp;
+  float2 ahead = stats(first, at0);
+  for (int64_t at = at0; at < rows; at += step) {
     float M = -INFINITY, L = 0.f, o[kPer] = {};
+    const float2 present = ahead;
+    ahead = stats(first, at + step);
     for (int64_t base = c0; base <= c1; base += 32) {
-      // a lane's piece: its place (-1: none), maximum and sum
-      const int64_t ci = base + lane;
-      int64_t p = -1;
-      float2 x = make_float2(-INFINITY, 0.f);
-      if (ci <= c1) {
-        const int64_t x1 = Deal::run_start(batch.total, runs, ci + 1) - s;
-        const int t0 = deal.tile_at(Deal::run_start(batch.total, runs, ci) - s, r.tiles, rows);
-        const int t1 = x1 >= cost ? r.tiles : deal.tile_at(x1, r.tiles, rows);
-        if (t0 == 0 && t1 == r.tiles) p = -2;  // one CTA has all the tiles
-        else if (t0 < t1) p = (ci * 2 + (t0 > 0 ? 0 : 1)) * slot;
-        if (p >= 0) x = reinterpret_cast<const float2*>(ws + p + int64_t(part_rows) * kD)[at];
-      }
+      const int64_t p = base == c0 ? first : piece_at(base + lane);
+      const float2 x = base == c0 ? present : stats(p, at);
       if (__any_sync(0xffffffffu, p == -2)) return;
       float top = x.x;
 #pragma unroll
@@ -1610,7 +1653,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
       }
     }
     const int i = u * kUnitRows + static_cast<int>(at);
-    const int64_t node = r.node0 + i / d.group, head = h * d.group + i % d.group;
+    const int64_t node = cut.node0 + i / d.group, head = h * d.group + i % d.group;
     bf16_t* dst = static_cast<bf16_t*>(a.out) + node * a.ld_on + head * a.ld_oh + lane * kPer;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) Elem<bf16_t>::store1(dst + k, L == 0.f ? 0.f : o[k] / L);
