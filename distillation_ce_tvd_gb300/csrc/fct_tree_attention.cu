@@ -192,13 +192,12 @@ cudaError_t launch_general(const AttnArgs& a, cudaStream_t st) {
 // partial sums in the workspace, which combine_kernel adds in order.
 //
 // What bounds it: with few rows the bytes of the keys (1 x 8 nodes, 32 query
-// and 8 kv heads of 128, 131071 keys in bf16: 537 MB in 99 us, 5.4 TB/s; 48
-// requests x 5 nodes, 870 MB: 166 us); with 256 rows per unit neither (12 x 64
-// nodes, 64 query heads: 118 GFLOP in 164 us, 0.72 PFLOP/s; without softmax
-// and most products a copy still took 156 of then 184 us); in e4m3 the
-// conversion and the hand-over of tiles between the roles (20 x 27 nodes,
-// 400 MB: 191 us, 2.1 TB/s; 208 with one converting group instead of two, 159
-// without the conversion).
+// and 8 kv heads of 128, 131071 keys in bf16: 537 MB in 98 us, 5.5 TB/s; 48
+// requests x 5 nodes, 870 MB: 161 us); with 256 rows per unit a call's fixed
+// cost of some 50 us and 1.7 us per tile (12 x 64 nodes, 64 query heads: 118
+// GFLOP in 157 us, 0.75 PFLOP/s); in e4m3 the conversion, the scale bytes and
+// the hand-over of tiles between the roles, 1.8 us per tile (20 x 27 nodes, 400
+// MB: 190 us, 2.1 TB/s; a copy without conversion took 171 of then 194).
 //
 // Per CTA: warp 1 issues the products, warps 4-7 and 8-11 are the softmax
 // groups.  bf16: warps 0 and 3 load K and V tiles by TMA (one box per page
