@@ -63,11 +63,6 @@ def _log(rng, lo, hi):
     return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
 
 
-def _held(depth):
-    """Nodes that a tree of four children each and this depth has room for."""
-    return (4 ** (depth + 1) - 1) // 3
-
-
 def draw(rng):
     op = rng.choice(["write", "move", "attend", "attend", "attend", "verify", "verify"])
     cache = rng.choice(["bf16", "e4m3"])
@@ -78,8 +73,7 @@ def draw(rng):
         return dict(op=op, tokens=_log(rng, 1, 16389), heads=heads, dim=dim, page=page, cache=cache,
                     source=rng.choice(["bf16", "f32"]))
     if op == "move":
-        batch, nodes, depth = _log(rng, 1, 256), _log(rng, 9, 64), rng.randint(2, 8)
-        return dict(op=op, batch=batch, nodes=min(nodes, _held(depth)), depth=depth,
+        return dict(op=op, batch=_log(rng, 1, 256), nodes=_log(rng, 9, 64), depth=rng.randint(2, 8),
                     heads=heads, dim=dim, page=page, cache=cache, context=_log(rng, 1, 900))
     if op == "attend":
         nodes = _log(rng, 1, 64)
@@ -95,7 +89,7 @@ def draw(rng):
                     tree=rng.choice(["chain", "tree"]))
     chain = rng.random() < 0.5
     depth = rng.randint(1, 8)
-    nodes = depth + 1 if chain else min(_log(rng, depth + 1, 40), _held(depth))
+    nodes = depth + 1 if chain else _log(rng, depth + 1, 40)
     vocab = _log(rng, 1000, 256000)
     batch = _log(rng, 1, max(1, min(64, 64 * 16 * 151936 // (2 * nodes * vocab))))
     return dict(op=op, batch=batch, nodes=nodes, depth=depth, vocab=vocab,
