@@ -179,8 +179,12 @@ cudaError_t launch_general(const AttnArgs& a, cudaStream_t st) {
 // is read once for all of them.
 //
 //   S = Q K^T  (128 rows x 128 keys, fp32 in tensor memory, tcgen05.mma)
-//   P = 2^(S * scale * log2 e - m), rounded to bf16 over S's own columns
+//   P = 2^(S * scale * log2 e - m) as two bf16, over S's own columns
 //   O += P V   (P from tensor memory, V as it lies in the cache: MN-major)
+//
+// A weight goes through the second product as its bf16 value and the bf16 of
+// what that rounding left, 16 bits together: with the first alone an output is
+// off by up to 2^-8 of the largest weight's value, at any number of keys.
 //
 // A unit of work is a request, a kv head and up to 256 rows; its keys come in
 // tiles of 128.  A unit of at most 128 rows gives its even key tiles to
@@ -215,11 +219,6 @@ constexpr int kSoftWarps = 8;
 constexpr int kUnitRows = 2 * kTile;
 constexpr int kBadRing = 16;
 constexpr uint32_t kAtTmemCols = 512;
-// Requests of at most this many keys take the weights' rounding remainders
-// (p minus its bf16 value) through a second product: a weight's 2^-8 averages
-// out over many keys, not over few.  Longer ones are bound by their keys'
-// bytes or by the products, and save the second one.
-constexpr int64_t kFineKeys = 2048;
 constexpr float kLazyLog2 = 8.f;  // O is rescaled when the maximum grows by more than 2^8
 
 template <int kD, bool kFp8>
@@ -560,6 +559,12 @@ __device__ __forceinline__ void tm_ld_start(uint32_t taddr, uint32_t (&r)[32]) {
 __device__ __forceinline__ void tm_ld_done(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : FCT_RW32(r)::"memory");
 }
+__device__ __forceinline__ void tm_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]),
+      "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
@@ -692,15 +697,14 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
 
 // One key tile of a softmax warp: `chunks` (1, 2 or 4) chunks of 32 keys from
 // chunk0 on are its share, of the rows of its 32 lanes.  S's columns become
-// P's (16 per chunk, and 16 of the weights' rounding remainders where `fine`);
+// P's (per chunk 16 of the weights in bf16 and 16 of what the rounding left);
 // the chunks of other warps, which hold the same rows, become zero.  kHold
 // chunks are held at a time (S is read twice where there are more), in loops
 // that stay small: the roles of a CTA share one instruction cache.
 template <int kD, int kHold>
 __device__ __forceinline__ void soft_tile(const AttnArgs& a, const Segment& seg, uint32_t tm_s,
                                           uint32_t tm_o, int chunk0, int chunks, int node, bool live,
-                                          int p0, bool tail, bool fine, bool first, float sl2, float& m,
-                                          float& l) {
+                                          int p0, bool tail, bool first, float sl2, float& m, float& l) {
   uint32_t x[kHold][32];
   auto load = [&](int i0) {
     const uint32_t at = tm_s + 32 * (chunk0 + i0);
@@ -753,27 +757,26 @@ __device__ __forceinline__ void soft_tile(const AttnArgs& a, const Segment& seg,
   const float2 s2 = make_float2(sl2, sl2), o2 = make_float2(off, off);
   float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
   auto weights = [&](uint32_t (&y)[32], uint32_t at) {
-    uint32_t p[16];
+    // 16 keys at a time, so that few registers are held
 #pragma unroll
-    for (int k = 0; k < 32; k += 2) {
-      float2 e = __ffma2_rn(make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), s2, o2);
-      e.x = ex2(e.x);
-      e.y = ex2(e.y);
-      if (k % 4 == 0)
-        sum0 = __fadd2_rn(sum0, e);
-      else
-        sum1 = __fadd2_rn(sum1, e);
-      p[k / 2] = pack_bf16x2(e.x, e.y);
-      y[k] = __float_as_uint(e.x);
-      y[k + 1] = __float_as_uint(e.y);
-    }
-    tm_st16(at, p);
-    if (fine) {
+    for (int h = 0; h < 2; ++h) {
+      uint32_t p[8], rest[8];
 #pragma unroll
-      for (int k = 0; k < 32; k += 2)
-        p[k / 2] = pack_bf16x2(__uint_as_float(y[k]) - __uint_as_float(p[k / 2] << 16),
-                               __uint_as_float(y[k + 1]) - __uint_as_float(p[k / 2] & 0xffff0000u));
-      tm_st16(at + 16, p);
+      for (int k = 0; k < 16; k += 2) {
+        float2 e = __ffma2_rn(make_float2(__uint_as_float(y[16 * h + k]), __uint_as_float(y[16 * h + k + 1])),
+                              s2, o2);
+        e.x = ex2(e.x);
+        e.y = ex2(e.y);
+        if (k % 4 == 0)
+          sum0 = __fadd2_rn(sum0, e);
+        else
+          sum1 = __fadd2_rn(sum1, e);
+        p[k / 2] = pack_bf16x2(e.x, e.y);
+        rest[k / 2] = pack_bf16x2(e.x - __uint_as_float(p[k / 2] << 16),
+                                  e.y - __uint_as_float(p[k / 2] & 0xffff0000u));
+      }
+      tm_st8(at + 8 * h, p);
+      tm_st8(at + 16 + 8 * h, rest);
     }
   };
   const int last = chunks > kHold ? chunks - kHold : 0;  // its chunks are still held
@@ -791,7 +794,7 @@ __device__ __forceinline__ void soft_tile(const AttnArgs& a, const Segment& seg,
     for (int c = 0; c < 4; ++c) {
       if ((c & -chunks) != chunk0) {
         tm_st16(tm_s + 32 * c, zero);
-        if (fine) tm_st16(tm_s + 32 * c + 16, zero);
+        tm_st16(tm_s + 32 * c + 16, zero);
       }
     }
   }
@@ -1152,14 +1155,10 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
       const uint32_t vd = desc_lo(slot_addr(it), true);
       tc_after();
       if (issue) {
+        // a chunk of 32 keys: two steps of weights, two of remainders
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          umma_ts<kIdO>(tm_o, tm_s + (k / 2) * 32 + (k % 2) * 8, vd + (k * 16 * 128 >> 4), !first || k > 0);
-        if (seg.len <= kFineKeys) {
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            umma_ts<kIdO>(tm_o, tm_s + (k / 2) * 32 + 16 + (k % 2) * 8, vd + (k * 16 * 128 >> 4), 1);
-        }
+        for (int k = 0; k < 2 * kTile / 16; ++k)
+          umma_ts<kIdO>(tm_o, tm_s + k * 8, vd + (((k / 4) * 2 + k % 2) * 16 * 128 >> 4), !first || k > 0);
         if (last) umma_commit(&ctl.empty_bar[it % Sh::kSlots]);
       }
       __syncwarp();
@@ -1329,7 +1328,6 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
 
       float m = -INFINITY, l = 0.f;   // the weights' exponent offset and their sum
       bool first = true;
-      const bool fine = seg.len <= kFineKeys;
       const int chunk0 = span == kTile ? 0 : span == 64 ? (warp & 2) : (warp & 3);
       for (int j = two ? 0 : w; j < seg.tiles; j += two ? 1 : 2) {
         if (!warp_wait(&ctl.s_full[w], s_n & 1u, &ctl.abort_flag)) {
@@ -1341,8 +1339,8 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
         if (warp_live) {
           const int p0 = (seg.tile0 + j) * kTile + 32 * chunk0;
           const bool tail = is_tail(seg, seg.tile0 + j);
-          soft_tile<kD, Sh::kHold>(a, seg, tm_s, tm_o + uint32_t(w) * kD, chunk0, span / 32, node, live, p0, tail,
-                        fine, first, sl2, m, l);
+          soft_tile<kD, Sh::kHold>(a, seg, tm_s, tm_o + uint32_t(w) * kD, chunk0, span / 32, node, live,
+                                   p0, tail, first, sl2, m, l);
         }
         first = false;
         tc_before();

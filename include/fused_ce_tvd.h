@@ -749,10 +749,9 @@ int fct_kv_cache_move(const fct_kv_cache* cache, const int32_t* block_table,
  *                 fct_tree_attention_workspace_size bytes, clobbered: partial
  *                 results of requests whose keys are split over several CTAs.
  * Products take bf16 operands (e4m3 values are exact in bf16) with fp32 sums;
- * the softmax statistics are fp32.  Softmax weights are rounded to bf16 for
- * the second product (2^-8 each, which averages out over the keys); where a
- * request has at most 2048 keys their remainders go through it as well.  The order of all sums is fixed by the
- * arguments and the device: repeated calls give the same bits.
+ * the softmax statistics are fp32.  A softmax weight enters the second product
+ * as two bf16, 16 bits together (2^-17 of itself).  The order of all sums is
+ * fixed by the arguments and the device: repeated calls give the same bits.
  */
 size_t fct_tree_attention_workspace_size(int64_t n_nodes, int32_t n_q_heads,
                                          int32_t n_heads, int32_t head_dim);

@@ -1,0 +1,44 @@
+"""Tree attention on the GPU against attention in 64 bits: weights that a few of many keys carry.
+
+Tolerances.  Scores: exact products summed in fp32, in fewer than 32 roundings of at most
+sum |q||k| * scale, which is under 60 here, so 32 * 60 * 2^-24 = 1.2e-4 in a score and as much in its
+weight's relative error, twice for numerator and sum; weights to 16 bits (2^-17).  Under
+4e-4 * sum w|v| together.  The output is rounded to bf16 once: 2^-8 of itself.
+"""
+import pytest
+import torch
+
+import spec_util as su
+from distillation_ce_tvd_gb300 import binding
+from test_gpu_tree_attention import case, run
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF16 = torch.bfloat16
+
+
+def close(c, scale=None):
+    out, lse, st = run(c, scale=scale)
+    assert st == 0
+    ref, ref_lse, bound = su.attention_ref(
+        c["q"], su.values_of(c["k"], c["ks"]), su.values_of(c["v"], c["vs"]), c["table"], c["page"],
+        c["contexts"], c["starts"], c["mask"], c["q"].shape[2] ** -0.5 if scale is None else scale)
+    worst = ((out.cpu().double() - ref).abs() - 2.0 ** -8 * ref.abs() - 4e-4 * bound).max().item()
+    assert worst <= 0, worst
+    assert float((lse.cpu().double() - ref_lse).abs().max()) <= 4e-4
+    return out, lse
+
+
+@pytest.mark.parametrize("dtype", [BF16, su.E4M3])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("nodes", [[5, 5, 3, 2], [12, 9, 16, 14], [70, 3, 33, 40]])
+def test_peaked_weights_at_any_number_of_keys(dtype, dim, nodes):
+    # a few keys carry the weight, so that roundings do not average out; from one tile of rows held
+    # four times to two tiles, below and above 2048 keys
+    close(case([1900, 2060, 4500, 9000], nodes, 8, 2, dim, 16, dtype, seed=dim + nodes[0],
+               spread=4.0 if dtype == BF16 else 2.0))
+
+
+@pytest.mark.parametrize("scale", [-0.125, 0.07])
+def test_negative_scales(scale):
+    close(case([0, 61, 700], [3, 9, 40], 8, 2, 64, 16, seed=2), scale)
