@@ -1267,8 +1267,15 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const uint32_t tm_s = tmem + uint32_t(w) * kTile + lanes;
     const uint32_t tm_o = tmem + 2 * kTile + lanes;
-    const float sl2 = fabsf(a.scale) * kLog2e;
+    // The factor of the scores is positive, so that -inf (masked) stays -inf: a
+    // negative scale negates the query rows, a scale of 0 makes them 0.
+    const bool no_scale = a.scale == 0.f;
+    const float sl2 = no_scale ? kLog2e : fabsf(a.scale) * kLog2e;
     const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+    // bf16 pairs times 0: NaN where they are not finite
+    auto times_zero = [](uint32_t x) {
+      return ((x & 0x7f80u) == 0x7f80u ? 0x7fc0u : 0u) | ((x & 0x7f800000u) == 0x7f800000u ? 0x7fc00000u : 0u);
+    };
     const bool vec_q = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && a.ld_qn % 8 == 0 && a.ld_qh % 8 == 0;
     const bool vec_o = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.ld_on % 8 == 0 && a.ld_oh % 8 == 0;
     uint32_t s_n = 0, ml_n = 0;
@@ -1312,6 +1319,11 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
                 y[k] = uint32_t(src[(c0 + c) * 8 + 2 * k]) | (uint32_t(src[(c0 + c) * 8 + 2 * k + 1]) << 16);
               x[c] = make_uint4(y[0], y[1], y[2], y[3]);
             }
+          }
+          if (no_scale) {
+#pragma unroll
+            for (int c = 0; c < kHalf; ++c)
+              x[c] = make_uint4(times_zero(x[c].x), times_zero(x[c].y), times_zero(x[c].z), times_zero(x[c].w));
           }
 #pragma unroll
           for (int c = 0; c < kHalf; ++c)

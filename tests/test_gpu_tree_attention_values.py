@@ -1,10 +1,13 @@
-"""Tree attention on the GPU against attention in 64 bits: weights that a few of many keys carry.
+"""Tree attention on the GPU against attention in 64 bits: weights that a few of many keys carry,
+and a scale of zero.
 
 Tolerances.  Scores: exact products summed in fp32, in fewer than 32 roundings of at most
 sum |q||k| * scale, which is under 60 here, so 32 * 60 * 2^-24 = 1.2e-4 in a score and as much in its
 weight's relative error, twice for numerator and sum; weights to 16 bits (2^-17).  Under
 4e-4 * sum w|v| together.  The output is rounded to bf16 once: 2^-8 of itself.
 """
+import math
+
 import pytest
 import torch
 
@@ -37,6 +40,24 @@ def test_peaked_weights_at_any_number_of_keys(dtype, dim, nodes):
     # four times to two tiles, below and above 2048 keys
     close(case([1900, 2060, 4500, 9000], nodes, 8, 2, dim, 16, dtype, seed=dim + nodes[0],
                spread=4.0 if dtype == BF16 else 2.0))
+
+
+@pytest.mark.parametrize("dtype", [BF16, su.E4M3])
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 32), (72, 16), (128, 5)])
+def test_a_scale_of_zero_gives_the_mean(dtype, dim, page):
+    c = case([0, 61, 700], [3, 9, 40], 8, 2, dim, page, dtype, seed=1)
+    for scale in (0.0, -0.0):
+        out, lse = close(c, scale)
+    seen = torch.tensor([sum(bin(w & (2 ** 64 - 1)).count("1") for w in row) for row in c["mask"].tolist()])
+    ctx = torch.tensor([0] * 3 + [61] * 9 + [700] * 40)
+    assert torch.allclose(lse.cpu().double(), (seen + ctx).double().log()[:, None], atol=1e-5)
+    # 0 times what is not finite is not a number
+    c["q"][5, 3, 7] = math.nan
+    c["q"][6, 2, 0] = math.inf
+    got, got_lse, st = run(c, scale=0.0)
+    bad = torch.isnan(got_lse)
+    assert st == 0 and bad.nonzero().tolist() == [[5, 3], [6, 2]]
+    assert bool(torch.isnan(got[bad]).all()) and torch.equal(got[~bad], out[~bad])
 
 
 @pytest.mark.parametrize("scale", [-0.125, 0.07])
