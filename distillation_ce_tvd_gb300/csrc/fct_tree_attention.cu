@@ -219,7 +219,10 @@ constexpr int kSoftWarps = 8;
 constexpr int kUnitRows = 2 * kTile;
 constexpr int kBadRing = 16;
 constexpr uint32_t kAtTmemCols = 512;
-constexpr float kLazyLog2 = 8.f;  // O is rescaled when the maximum grows by more than 2^8
+// O is rescaled when the scores' maximum passes the weights' offset, which is
+// then put 2^8 above it: a weight is never more than 1, so that O overflows no
+// earlier than the values do.
+constexpr float kLazyLog2 = 8.f;
 
 template <int kD, bool kFp8>
 struct AttnShape {
@@ -737,10 +740,10 @@ __device__ __forceinline__ void soft_tile(const AttnArgs& a, const Segment& seg,
     }
   }
   const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * sl2;
-  const bool grow = top > m + kLazyLog2 || (m == -INFINITY && top > -INFINITY);
+  const bool grow = top > m;
   if (__any_sync(0xffffffffu, grow)) {
-    const float f = grow ? ex2(m - top) : 1.f;
-    if (grow) m = top;
+    const float f = grow ? ex2(m - (top + kLazyLog2)) : 1.f;
+    if (grow) m = top + kLazyLog2;
     l *= f;
     if (!first) {
 #pragma unroll 1

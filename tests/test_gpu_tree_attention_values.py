@@ -1,5 +1,5 @@
 """Tree attention on the GPU against attention in 64 bits: weights that a few of many keys carry,
-and a scale of zero.
+a scale of zero, values near the largest.
 
 Tolerances.  Scores: exact products summed in fp32, in fewer than 32 roundings of at most
 sum |q||k| * scale, which is under 60 here, so 32 * 60 * 2^-24 = 1.2e-4 in a score and as much in its
@@ -63,3 +63,29 @@ def test_a_scale_of_zero_gives_the_mean(dtype, dim, page):
 @pytest.mark.parametrize("scale", [-0.125, 0.07])
 def test_negative_scales(scale):
     close(case([0, 61, 700], [3, 9, 40], 8, 2, 64, 16, seed=2), scale)
+
+
+@pytest.mark.parametrize("dtype", [BF16, su.E4M3])
+@pytest.mark.parametrize("nodes", [3, 40])
+def test_values_near_the_largest_do_not_overflow(dtype, nodes):
+    # the key that holds 2^127 comes in the third tile, with a score 5 above all others': its value
+    # has to be weighted with less than 1 before anything is summed
+    c = case([300], [nodes], 4, 1, 64, 16, dtype, tree=False, seed=5)
+    raw = [c[x].view(torch.uint8 if dtype == su.E4M3 else torch.int16) for x in "kv"]
+    for x in raw:
+        x.zero_()
+    c["q"].zero_()
+    c["q"][..., 0] = 1.0
+    at = (int(c["table"][0, 299 // 16]), 299 % 16, 0)
+    if dtype == su.E4M3:
+        c["ks"][:], c["vs"][:] = 127, 127
+        raw[0][at + (0,)], raw[1][at] = 0x4A, 0x38     # 5, and 1 with a scale of 2^127
+        c["vs"][at] = 254
+    else:
+        c["k"][at + (0,)], c["v"][at] = 5.0, 2.0 ** 127
+    out, lse, st = run(c, scale=1.0)
+    assert st == 0
+    others = 300 + torch.arange(nodes, dtype=torch.float64)
+    want = 2.0 ** 127 * math.exp(5) / (math.exp(5) + others)
+    got = out.cpu().double()
+    assert float((got / want[:, None, None] - 1).abs().max()) <= 2.0 ** -8 + 1e-5
