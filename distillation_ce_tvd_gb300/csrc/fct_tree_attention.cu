@@ -25,6 +25,16 @@ namespace {
 
 constexpr int kGWarps = 4;
 
+// Four e4m3 payloads.
+__device__ __forceinline__ float4 e4m3_floats(uint32_t w) {
+  uint32_t lo, hi;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"(static_cast<uint16_t>(w)));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"(static_cast<uint16_t>(w >> 16)));
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
 // 8 elements of a cached vector, payload only.
 __device__ __forceinline__ void load_cached(const void* pool, int dtype, int64_t at, float (&x)[8]) {
   if (dtype == FCT_BF16) {
@@ -32,13 +42,12 @@ __device__ __forceinline__ void load_cached(const void* pool, int dtype, int64_t
   } else {
     const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pool) + at);
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      const uint16_t two = static_cast<uint16_t>((j < 4 ? w.x : w.y) >> (8 * (j % 4)));
-      uint32_t h;
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    for (int j = 0; j < 8; j += 4) {
+      const float4 f = e4m3_floats(j < 4 ? w.x : w.y);
       x[j] = f.x;
       x[j + 1] = f.y;
+      x[j + 2] = f.z;
+      x[j + 3] = f.w;
     }
   }
 }
@@ -48,6 +57,9 @@ __device__ __forceinline__ float scale_of(uint8_t byte) {
   return byte == 255 ? __int_as_float(0x7fc00000)
                      : byte == 0 ? __int_as_float(0x00400000) : __uint_as_float(uint32_t(byte) << 23);
 }
+// From this byte on a payload times its scale can be 2^128 or more, which reads
+// as an infinity.
+constexpr int kLargeScale = 247;
 
 __global__ void __launch_bounds__(kGWarps * 32) attention_general_kernel(AttnArgs a, int lanes) {
   __shared__ float sm_m[kGWarps], sm_l[kGWarps];
@@ -110,15 +122,23 @@ __global__ void __launch_bounds__(kGWarps * 32) attention_general_kernel(AttnArg
       load_cached(c.k, c.dtype, at, k);
       load_cached(c.v, c.dtype, at, v);
     }
-    float s = 0.f;
+    float s = 0.f, ks = 1.f, vs = 1.f;
+    if (e && sees) {
+      ks = scale_of(c.k_scale[sc]);
+      vs = scale_of(c.v_scale[sc]);
+      if (max(c.k_scale[sc], c.v_scale[sc]) >= kLargeScale) {
+#pragma unroll
+        for (int d = 0; d < 8; ++d) {
+          k[d] *= ks;
+          v[d] *= vs;
+        }
+        ks = vs = 1.f;
+      }
+    }
 #pragma unroll
     for (int d = 0; d < 8; ++d) s = fmaf(q[d], k[d], s);
     for (int x = lanes / 2; x >= 1; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    float vs = 1.f;
-    if (e && sees) {
-      s *= scale_of(c.k_scale[sc]);
-      vs = scale_of(c.v_scale[sc]);
-    }
+    s *= ks;
     if (sees) {
       const float mn = fmaxf(m, s);
       const float base = mn == -INFINITY ? 0.f : mn;
@@ -664,6 +684,14 @@ __device__ __forceinline__ uint32_t visible32(const AttnArgs& a, const Segment& 
   return m;
 }
 
+// A bf16 pair without its infinities and NaNs; whether it had any.
+__device__ __forceinline__ bool drop_non_finite(uint32_t& x) {
+  const bool lo = (x & 0x7f80u) == 0x7f80u, hi = (x & 0x7f800000u) == 0x7f800000u;
+  if (lo) x &= 0xffff0000u;
+  if (hi) x &= 0x0000ffffu;
+  return lo || hi;
+}
+
 // The pool's page and slot of a position; the page may be outside the pool
 // (the table is the caller's).
 __device__ __forceinline__ int page_of(const AttnArgs& a, const Segment& s, int pos, int* slot) {
@@ -1028,14 +1056,12 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
               for (int k = 0; k < 4; ++k) x[h][k] = in[h][k];
             if (block + 1 < kTile / kRows) load(block + 1);
             __syncwarp();
-            if (clear) {
-              const int pos = p0 + block * kRows + t / 4;
-              if (pos >= seg.ctx && (pos >= seg.len || e == 255)) {
-                found |= pos < seg.len;
-                e = 127;
+            const int pos = p0 + block * kRows + t / 4;
+            const bool drafted = clear && pos >= seg.ctx;
+            if (drafted && pos >= seg.len) {
+              e = 127;
 #pragma unroll
-                for (int h = 0; h < kHalves; ++h) x[h][0] = x[h][1] = x[h][2] = x[h][3] = 0;
-              }
+              for (int h = 0; h < kHalves; ++h) x[h][0] = x[h][1] = x[h][2] = x[h][3] = 0;
             }
             // 2^120 * 2^(e - 127) as one bf16 factor, or as two
             const bool one = e <= 134;
@@ -1052,6 +1078,10 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
                 const uint32_t f2 = e == 255 ? 0x7fc07fc0u : e * 0x00800080u;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], f2);
+              }
+              if (drafted) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) found |= drop_non_finite(o[k]);
               }
               const uint32_t at = uint32_t(kRows * 128) * block + uint32_t(h) * (kTile * 128);
               asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out0 + at), "r"(o[0]),
@@ -1093,12 +1123,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
               uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
               bool change = false;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const bool lo = (w[k] & 0x7f80u) == 0x7f80u, hi = (w[k] & 0x7f800000u) == 0x7f800000u;
-                change |= lo || hi;
-                if (lo) w[k] &= 0xffff0000u;
-                if (hi) w[k] &= 0x0000ffffu;
-              }
+              for (int k = 0; k < 4; ++k) change |= drop_non_finite(w[k]);
               if (change) {
                 found = true;
                 *place(n0 + i * kPrepThreads) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -1387,20 +1412,28 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
             int at;
             const int64_t page = page_of(a, seg, pos, &at);
             if (page < 0 || page >= a.cache.num_pages) continue;
+            const int64_t v_at = page * a.cache.page_stride + at * a.cache.slot_stride +
+                                 seg.h * a.cache.head_stride + c;
+            auto add = [&](int k, float y) {
+              if (!(fabsf(y) < INFINITY)) o[k] += y;
+            };
             if constexpr (kFp8) {
-              if (a.cache.v_scale[page * a.cache.scale_page_stride + at * a.cache.scale_slot_stride +
-                                  seg.h * a.cache.scale_head_stride] == 255) {
+              const float scale =
+                  scale_of(a.cache.v_scale[page * a.cache.scale_page_stride + at * a.cache.scale_slot_stride +
+                                           seg.h * a.cache.scale_head_stride]);
+              const uint8_t* v = static_cast<const uint8_t*>(a.cache.v) + v_at;
 #pragma unroll
-                for (int k = 0; k < kN; ++k) o[k] = __int_as_float(0x7fc00000);
+              for (int k = 0; k < kN; k += 4) {
+                const float4 y = e4m3_floats(*reinterpret_cast<const uint32_t*>(v + k));
+                add(k, y.x * scale);
+                add(k + 1, y.y * scale);
+                add(k + 2, y.z * scale);
+                add(k + 3, y.w * scale);
               }
             } else {
-              const bf16_t* v = static_cast<const bf16_t*>(a.cache.v) + page * a.cache.page_stride +
-                                at * a.cache.slot_stride + seg.h * a.cache.head_stride + c;
+              const bf16_t* v = static_cast<const bf16_t*>(a.cache.v) + v_at;
 #pragma unroll
-              for (int k = 0; k < kN; ++k) {
-                const float y = Elem<bf16_t>::load1(v + k);
-                if (!(fabsf(y) < INFINITY)) o[k] += y;
-              }
+              for (int k = 0; k < kN; ++k) add(k, Elem<bf16_t>::load1(v + k));
             }
           }
         }

@@ -1,5 +1,5 @@
-"""Tree attention on the GPU against attention in 64 bits: weights that a few of many keys carry,
-a scale of zero, values near the largest.
+"""Tree attention on the GPU against attention in 64 bits: weights that a few of many keys carry, a
+scale of zero, values near the largest and values that are not finite.
 
 Tolerances.  Scores: exact products summed in fp32, in fewer than 32 roundings of at most
 sum |q||k| * scale, which is under 60 here, so 32 * 60 * 2^-24 = 1.2e-4 in a score and as much in its
@@ -63,6 +63,48 @@ def test_a_scale_of_zero_gives_the_mean(dtype, dim, page):
 @pytest.mark.parametrize("scale", [-0.125, 0.07])
 def test_negative_scales(scale):
     close(case([0, 61, 700], [3, 9, 40], 8, 2, 64, 16, seed=2), scale)
+
+
+def put(c, which, b, pos, head, d, payload, byte=None):
+    """One element (or all, d = slice(None)) of a cached vector by its 8-bit payload."""
+    at = (int(c["table"][b, pos // c["page"]]), pos % c["page"], head)
+    c[which].view(torch.uint8)[at + (d,)] = payload
+    if byte is not None:
+        c[which + "s"][at] = byte
+
+
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 64), (72, 16), (128, 5)])
+@pytest.mark.parametrize("byte", [247, 248, 250, 254, 255])
+@pytest.mark.parametrize("nodes", [9, 80])
+def test_large_scales_of_drafted_nodes_stay_with_who_sees_them(dim, page, byte, nodes):
+    c = case([61], [nodes], 4, 2, dim, page, su.E4M3, seed=4)
+    last = 61 + nodes - 1
+    word, bit = (nodes - 1) // 64, (nodes - 1) % 64
+    one = (1 << bit) - (1 << 64 if bit == 63 else 0)
+    c["mask"][:-1, word] &= ~one                    # a leaf: only its own row sees it, and the context
+    c["mask"][-1] = 0
+    c["mask"][-1, word] = one
+    put(c, "v", 0, last, 0, slice(None), 0x38)      # 1, and below 448, -448 and NaN
+    clean, clean_lse, _ = run(c)
+    for d, payload in ((2, 0x7E), (9, 0xFE)):
+        put(c, "v", 0, last, 0, d, payload, byte)
+    out, lse, st = run(c)
+    assert st == 0
+    assert torch.equal(out[:-1], clean[:-1]) and torch.equal(out[-1, 2:], clean[-1, 2:])
+    assert torch.equal(lse, clean_lse)
+    own = out[-1, :2].float().cpu()
+    if byte == 255:
+        assert bool(torch.isnan(own).all())
+    else:                                           # 2^128 and more reads as an infinity
+        assert bool((own[:, 2] == math.inf).all()) and bool((own[:, 9] == -math.inf).all())
+        rest = torch.ones(dim, dtype=torch.bool)
+        rest[[2, 9]] = False
+        # 1 * 2^(byte - 127) counts with its weight
+        assert bool((torch.isfinite(own[:, rest]) == (byte < 255)).all())
+        assert bool((own[:, rest] > 1e20).all())
+    put(c, "k", 0, last, 1, slice(None), 0x7E, 254)  # a key that only its own row sees
+    got, got_lse, st = run(c)
+    assert st == 0 and torch.equal(got[:-1], clean[:-1]) and torch.equal(got_lse[:-1], clean_lse[:-1])
 
 
 @pytest.mark.parametrize("dtype", [BF16, su.E4M3])
