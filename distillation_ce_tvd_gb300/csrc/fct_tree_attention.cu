@@ -1004,6 +1004,33 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
     }
   };
 
+  // Puts NaN where the payloads of the key tile at p0 (slot dst) are e4m3's NaN:
+  // rows row0, row0 + step, ..., 16-byte pieces `piece` (+ 4).  Of drafted values
+  // (`clear`) it puts 0, and says whether there were any.
+  auto place_nans = [&](bool is_v, int p0, int row0, int step, int piece, uint32_t dst, bool clear) {
+    bool dropped = false;
+#pragma unroll 1
+    for (int row = row0; row < kTile && p0 + row < seg.len; row += step) {
+      int at;
+      const int64_t page = page_of(a, seg, p0 + row, &at);
+      if (page < 0 || page >= a.cache.num_pages) continue;
+      const uint8_t* src = static_cast<const uint8_t*>(is_v ? a.cache.v : a.cache.k) +
+                           page * a.cache.page_stride + at * a.cache.slot_stride + seg.h * a.cache.head_stride;
+      const bool drop = clear && p0 + row >= seg.ctx;
+#pragma unroll 1
+      for (int i = 0; i < Sh::kHalves * 16; ++i) {
+        const int c = piece * 16 + i % 16;  // of a 64-column block
+        if ((src[(i / 16) * 64 + c] & 0x7f) != 0x7f) continue;
+        dropped |= drop;
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + uint32_t(i / 16) * (kTile * 128) + uint32_t(row) * 128 +
+                                                     uint32_t(((c / 8) ^ (row & 7)) * 16 + (c % 8) * 2)),
+                     "h"(static_cast<uint16_t>(drop ? 0 : 0x7fc0))
+                     : "memory");
+      }
+    }
+    return dropped;
+  };
+
   auto prepare = [&]() {
     // ---- tiles prepared
     constexpr int kPrepThreads = Sh::kPrepWarps * 32;
@@ -1037,6 +1064,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
           const uint32_t scale = smem_addr(&ctl.raw_scale[slot][t / 4]);
           const bool clear = is_v && is_tail(seg, tile);
           bool found = false;
+          uint32_t nans = 0;
           uint32_t in[kHalves][4], byte;
           auto load = [&](int block) {
             asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(scale + uint32_t(kRows) * block));
@@ -1063,6 +1091,12 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
 #pragma unroll
               for (int h = 0; h < kHalves; ++h) x[h][0] = x[h][1] = x[h][2] = x[h][3] = 0;
             }
+            // bit 7 of a byte where adding 1 changes it: 7 bits of ones, e4m3's NaN
+            // (a carry into the next byte comes from such a byte only)
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) nans |= (x[h][k] + 0x01010101u) ^ x[h][k];
             // 2^120 * 2^(e - 127) as one bf16 factor, or as two
             const bool one = e <= 134;
             const uint32_t f1 = (one ? e + 120 : 247u) * 0x00800080u;
@@ -1092,6 +1126,9 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
                            : "memory");
             }
           }
+          // e4m3's NaN came out as 480 times the scale: rare, so that this thread's
+          // places are looked through once more, in the cache
+          if (nans & 0x80808080u) found |= place_nans(is_v, p0, t / 4, kRows, t % 4, dst, clear);
           if (found) ctl.bad_seg[seg_n % kBadRing] = seg_n;
           async_fence();
           warp_arrive(&ctl.full_bar[slot]);

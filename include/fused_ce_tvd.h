@@ -667,8 +667,8 @@ int fused_ce_tvd_vp_backward(const void* student, int64_t ld_student,
  *   dtype    : FCT_BF16, or FCT_E4M3 with one exponent byte per token and
  *              head in k_scale and v_scale, at p * scale_page_stride + s *
  *              scale_slot_stride + h * scale_head_stride: the value held is
- *              payload * 2^(byte - 127), an infinity from 2^128 on, and byte 255
- *              makes the vector NaN.
+ *              payload * 2^(byte - 127), an infinity from 2^128 on; a NaN
+ *              payload is NaN, and byte 255 makes the vector NaN.
  *   head_dim : a multiple of 8, at most 256, else FCT_ERR_UNSUPPORTED.
  *   n_heads  : at most 65536, num_pages at most 2^40, else FCT_ERR_UNSUPPORTED.
  *   k, v     : aligned to 8 elements, strides multiples of 8 elements, else

@@ -73,6 +73,30 @@ def put(c, which, b, pos, head, d, payload, byte=None):
         c[which + "s"][at] = byte
 
 
+@pytest.mark.parametrize("payload", [0x7F, 0xFF])
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 64), (72, 16), (128, 5)])
+def test_not_a_number_payloads_of_an_e4m3_cache(dim, page, payload):
+    # the scale's byte is an ordinary one
+    c = case([61, 140, 30], [9, 12, 50], 4, 2, dim, page, su.E4M3, seed=3)
+    clean, clean_lse, _ = run(c)
+    put(c, "v", 0, 17, 1, 5, payload)               # a value of the context: its column, its head
+    put(c, "k", 1, 130, 0, 63, payload)             # a key: its head's rows
+    put(c, "v", 2, 30 + 4, 0, 8, payload)           # a value of a drafted node: who sees it
+    out, lse, st = run(c)
+    assert st == 0
+    want = torch.zeros(out.shape, dtype=torch.bool)
+    want[:9, 2:, 5] = True
+    want[9:21, :2] = True
+    sees = [i for i in range(50) if (int(c["mask"][21 + i, 0]) >> 4) & 1]
+    want[torch.tensor(sees) + 21, :2, 8] = True
+    assert 1 <= len(sees) < 50
+    assert torch.equal(torch.isnan(out).cpu(), want)
+    assert torch.equal(out[~want.to(DEV)], clean[~want.to(DEV)])
+    rows = torch.isnan(lse).cpu()
+    assert rows[9:21, :2].all() and int(rows.sum()) == 24
+    assert torch.equal(lse[~rows.to(DEV)], clean_lse[~rows.to(DEV)])
+
+
 @pytest.mark.parametrize("dim,page", [(64, 16), (128, 64), (72, 16), (128, 5)])
 @pytest.mark.parametrize("byte", [247, 248, 250, 254, 255])
 @pytest.mark.parametrize("nodes", [9, 80])
