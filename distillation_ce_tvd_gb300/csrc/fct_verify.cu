@@ -39,9 +39,13 @@ constexpr int kMaxBufs = 4;
 constexpr int kChunks = 4;
 constexpr int kStageBytes = 216 * 1024;
 
-// log2-domain state of a row: p(v) = 2^(x_v * k - lse2).
+// A row's softmax: p(v) = 2^(x_v * k - m2) * inv, with m2 the largest x_v * k and
+// inv = 1 / sum_v 2^(x_v * k - m2).  Kept apart: the exponent's rounding is then
+// that of the distance from the maximum.  In one number, m2 + log2(sum), it is
+// that of the logits themselves, and a constant added to a row, or a low
+// temperature, costs bits of every probability (1024 at T = 1: 4e-5).
 struct RowNorm {
-  float lse2;
+  float m2, inv;
   bool ok;  // a softmax exists
 };
 
@@ -221,8 +225,8 @@ struct Rows {
   __device__ __forceinline__ float all_sum(float x) { return all(x, 0.f, FoldSum()); }
   __device__ __forceinline__ Best all_best(Best x) { return all(x, best_none(), FoldBest()); }
   __device__ __forceinline__ static RowNorm norm(Lse2 st) {
-    const float lse2 = st.m2 + log2f(st.s);
-    return RowNorm{lse2, lse2 > -INFINITY && lse2 < INFINITY};
+    const bool ok = st.m2 > -INFINITY && st.m2 < INFINITY && st.s > 0.f && st.s < INFINITY;
+    return RowNorm{st.m2, 1.f / st.s, ok};
   }
 
   // The thread of the cluster whose sweep sees element v.
@@ -574,12 +578,12 @@ __global__ void __launch_bounds__(kVThreads, 1)
                                           [&](auto& x, auto&, auto&, int) { fold(sp, x, k); });
       NormPair st{lse2x_fold(sp), lse2x_fold(sq)};
       st = rows.all(st, NormPair{lse2_empty(), lse2_empty()}, FoldNorms());
-      const RowNorm p = rows.norm(st.p), q = dr ? rows.norm(st.q) : RowNorm{0.f, true};
+      const RowNorm p = rows.norm(st.p), q = dr ? rows.norm(st.q) : RowNorm{0.f, 1.f, true};
       if (!p.ok || !q.ok) {
         status |= FCT_DEV_NO_DISTRIBUTION;
         break;
       }
-      auto prob = [&](float x, RowNorm n) { return ex2(fmaf(x, k, -n.lse2)); };
+      auto prob = [&](float x, RowNorm n) { return ex2(fmaf(x, k, -n.m2)) * n.inv; };
       float S = 0.f, Z = 1.f, left = 1.f;
       Rejected rej;
       rej.n = 0;
@@ -631,8 +635,10 @@ __global__ void __launch_bounds__(kVThreads, 1)
         c = next_child(at, c);
         if (c < 0) break;
         // another sibling: the mass that is left.  Without draft logits it is 1
-        // less the rejected ones' probabilities; each is within a few 2^-24, so
-        // the difference is good while an eighth or more is left.
+        // less the rejected ones' probabilities; each is within some 2^-19 of
+        // itself (the distance from the maximum times 3 * 2^-24, the exponential
+        // and the sum), so the difference is good to 2^-16 while an eighth or
+        // more is left.
         if (!dr && left >= 0.125f) {
           Z = left;
         } else {
