@@ -59,6 +59,22 @@ __device__ __forceinline__ Best best_of(Best a, Best b) {
 }
 __device__ __forceinline__ Best best_none() { return Best{-INFINITY, INT_MAX}; }
 
+// Best in a race whose keys are log2 of p(v) / noise(v), p up to a factor: x_v is
+// taken relative to `top`, the largest x seen (by the thread, then by all), so
+// that a key's rounding is that of a distance from it, not of the logit.
+struct Race {
+  float key;
+  int v;
+  float top;
+};
+__device__ __forceinline__ Race race_none() { return Race{-INFINITY, INT_MAX, -INFINITY}; }
+// `top` raised to the larger t: the key, if there is one, goes down by what
+// that is.
+__device__ __forceinline__ void raise(Race& r, float t, float k) {
+  if (r.v >= 0 && r.v < INT_MAX) r.key = fmaf(r.top - t, k, r.key);
+  r.top = t;
+}
+
 // Folds a vector into a base-2 log-sum-exp state.  Unlike the loss's update
 // it takes rows with -inf entries (masked logits): while the state's maximum
 // is -inf the exponent offset is 0, so -inf contributes 0 and not NaN.  NaN
@@ -119,6 +135,17 @@ struct FoldBest {
     for (int m = width / 2; m >= 1; m >>= 1)
       x = best_of(x, Best{__shfl_xor_sync(0xffffffffu, x.key, m), __shfl_xor_sync(0xffffffffu, x.v, m)});
     return x;
+  }
+};
+
+struct FoldRace {
+  float k;
+  __device__ __forceinline__ Race operator()(Race x, int width) const {
+    float top = x.top;
+    for (int m = width / 2; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+    if (x.top < top) raise(x, top, k);
+    const Best best = FoldBest()(Best{x.key, x.v}, width);
+    return Race{best.key, best.v, top};
   }
 };
 
@@ -544,18 +571,21 @@ __global__ void __launch_bounds__(kVThreads, 1)
       last = best.v;
     } else if (c < 0) {
       // no child to test: r = p, and the race needs p up to a factor only, so
-      // one pass does, on log2 of p(v) / noise(v)
-      Best best = best_none();
+      // one pass does, on log2 of p(v) / noise(v) (the logarithm's 2^-20 is the
+      // largest error)
+      Race best = race_none();
       bool bad = false;
       rows.template sweep<false, true, kNoiseUnroll>(tr, nullptr, noise, true, [&](auto& x, auto&, auto& e, int v) {
+        const float top = vec_max(x);
+        if (top > best.top) raise(best, top, k);
 #pragma unroll
         for (int j = 0; j < int(sizeof(x) / sizeof(float)); ++j) {
           bad |= !(x[j] < INFINITY);
-          const float key = fmaf(x[j], k, -__log2f(e[j]));
-          if (key > best.key) best = Best{key, v + j};
+          const float key = fmaf(x[j] - best.top, k, -__log2f(e[j]));
+          if (key > best.key) best = Race{key, v + j, best.top};
         }
       });
-      best = rows.all_best(bad ? Best{INFINITY, -1} : best);
+      best = rows.all(bad ? Race{INFINITY, -1, -INFINITY} : best, race_none(), FoldRace{k});
       if (best.v < 0 || best.v >= V)
         status |= FCT_DEV_NO_DISTRIBUTION;
       else

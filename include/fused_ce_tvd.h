@@ -806,6 +806,10 @@ int fct_tree_attention(const void* q, int64_t ld_q_node, int64_t ld_q_head,
  *                 token, then -1.
  *   path        : (batch, max_depth) int32: the accepted nodes, then -1.
  *   count       : (batch,) int32: accepted tokens.
+ * Arithmetic is fp32: a probability is 2^d / sum with d the distance from the
+ * row's largest logit, so it is as good for a row with a constant added; some
+ * 2^-19 of itself where it matters.  At a node without children to test the
+ * race is on log2 of r(v) / noise(v), within 2^-18 of itself.
  * V is at most 2^30, and batch at most 2^24 here, in fct_tree_attention and in
  * fct_kv_cache_move, else FCT_ERR_UNSUPPORTED.
  * A visited row without a distribution (a NaN, +inf, or nothing above -inf)

@@ -6,6 +6,8 @@ exact in fp32; d is within 3 * 2^-24 of itself (the factor's two roundings and t
 for |d| <= 24, times ln 2; the exponential and the sum add under 2e-6.  A ratio of two such
 probabilities is within 1e-5.  Decisions use tokens with |d| <= 12, which halves the first part.
 """
+import math
+
 import pytest
 import torch
 
@@ -60,6 +62,36 @@ def test_acceptance_against_a_drafts_probability(at, dt, T, V):
     noise = torch.empty((B, V)).exponential_(generator=gen)
     _, count = verify(target, tokens, uniform, noise, draft, torch.full((B,), T), 2)
     assert torch.equal(count[usable] == 1, yes[usable])
+
+
+@pytest.mark.parametrize("V", [999, 4096, 32768])
+@pytest.mark.parametrize("at,T", [(0.0, 1.0), (1024.0, 1.0), (-1024.0, 1.0), (30.0, 0.0625)])
+@pytest.mark.parametrize("drafted", [False, True])
+def test_the_race_for_the_next_token(at, T, V, drafted):
+    # two tokens whose p / noise are 1e-5 apart, the others far behind; from a node without children,
+    # and after a rejected child (which the target gives no probability)
+    B, gen = 64, torch.Generator().manual_seed(int(at) + V + 1)
+    n = 2 if drafted else 1
+    target = logits(gen, n * B, V, at)
+    target[:, 7] = -math.inf
+    p = torch.softmax(target[::n].double() / T, 1)
+    two = torch.topk(p, 2).indices
+    two = two[:, torch.randperm(2, generator=gen)]
+    rows = torch.arange(B)
+    noise = torch.full((B, V), 1e6)
+    first = torch.arange(B) % 2 == 0
+    a, b = p[rows, two[:, 0]], p[rows, two[:, 1]]
+    usable = torch.minimum(a, b) > 2.0 ** -12 * torch.maximum(a, b)
+    assert int(usable.sum()) > B // 2
+    noise[rows, two[:, 0]] = a.float()
+    # the fp32 noise decides: the other's share is set from what it became
+    ratio = noise[rows, two[:, 0]].double() / a
+    noise[rows, two[:, 1]] = (b * ratio * torch.where(first, 1 + GAP, 1 - GAP)).float()
+    tokens, uniform = torch.full((n * B,), 7), torch.full((n * B,), 0.5)
+    out, count = verify(target, tokens, uniform, noise, None, torch.full((B,), T), n)
+    assert int(count.sum()) == 0
+    want = torch.where(first, two[:, 0], two[:, 1])
+    assert torch.equal(out[:, 0][usable], want[usable])
 
 
 def test_a_constant_on_a_row_changes_nothing():
