@@ -971,13 +971,31 @@ class KVCache:
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _raw_stream(stream, index):
-    """The address of ``stream``, or of the current stream of CUDA device ``index``."""
-    if stream is None:
-        if _current_raw_stream is not None:
-            return _current_raw_stream(index)
-        return torch.cuda.current_stream(index).cuda_stream
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+def _raw_stream(index):
+    """The address of the current stream of CUDA device ``index``."""
+    if _current_raw_stream is not None:
+        return _current_raw_stream(index)
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+def on_stream(f, stream, index, /, *args, **kw):
+    """``f(*args, **kw)`` with ``stream`` (a torch stream, or a raw handle) as the current stream of
+    CUDA device ``index``, so that what f allocates or computes in torch is ordered with what it
+    launches there.  The tensors it returns may be used on the caller's stream too, once that has
+    waited for ``stream``."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(getattr(stream, "cuda_stream", stream))
+        if handle == 2:
+            raise ValueError("the per-thread default stream cannot be made current in torch")
+        stream = torch.cuda.default_stream(index) if handle < 2 else torch.cuda.ExternalStream(handle, device=index)
+    caller = torch.cuda.current_stream(index)
+    with torch.cuda.stream(stream):
+        out = f(*args, **kw)
+    if caller != stream:
+        for x in out if isinstance(out, tuple) else (out,):
+            if isinstance(x, torch.Tensor) and x.is_cuda:
+                x.record_stream(caller)
+    return out
 
 
 def _library():
@@ -1010,6 +1028,9 @@ def fct_kv_cache_write(cache, k, v, slots, *, dev_status=None, stream=None):
     with unit stride along head_dim) to the slots (page * page_size + offset; int64 (n,), negative
     skips) of the cache, in place.  An e4m3 cache is quantised as it is written: per token and head
     the smallest power of two that keeps every value within 448, then round to nearest even."""
+    if stream is not None:
+        return on_stream(fct_kv_cache_write, stream, cache.index, cache, k, v, slots,
+                         dev_status=dev_status)
     code = FCT_BF16 if k.dtype is torch.bfloat16 else FCT_F32
     if code == FCT_F32 and k.dtype is not torch.float32:
         raise TypeError(f"k: dtype {k.dtype} is not float32 or bfloat16")
@@ -1022,7 +1043,7 @@ def fct_kv_cache_write(cache, k, v, slots, *, dev_status=None, stream=None):
     n = shape[0]
     rc = _library().fct_kv_cache_write(k.data_ptr(), v.data_ptr(), strides[0], strides[1], code, n,
                                        _vec(slots, torch.int64, n, index, "slots"), cache.ref,
-                                       _status_ptr(dev_status), _raw_stream(stream, index))
+                                       _status_ptr(dev_status), _raw_stream(index))
     _check(rc, "fct_kv_cache_write")
 
 
@@ -1030,13 +1051,16 @@ def fct_kv_cache_move(cache, block_table, context_len, path, count, *, dev_statu
                       stream=None):
     """Move the accepted nodes' keys and values (``path`` and ``count`` as fct_spec_verify returns
     them) to the positions after each request's context, in place."""
+    if stream is not None:
+        return on_stream(fct_kv_cache_move, stream, cache.index, cache, block_table, context_len,
+                         path, count, dev_status=dev_status)
     B, index = context_len.shape[0], cache.index
     tab, ld_t, pages = _table(block_table, torch.int32, B, index, "block_table")
     pth, ld_p, depth = _table(path, torch.int32, B, index, "path")
     rc = _library().fct_kv_cache_move(cache.ref, tab, ld_t, pages,
                                       _vec(context_len, torch.int32, B, index, "context_len"), B,
                                       pth, ld_p, depth, _vec(count, torch.int32, B, index, "count"),
-                                      _status_ptr(dev_status), _raw_stream(stream, index))
+                                      _status_ptr(dev_status), _raw_stream(index))
     _check(rc, "fct_kv_cache_move")
 
 
@@ -1070,6 +1094,10 @@ def fct_tree_attention(q, cache, block_table, context_len, node_start, tree_mask
     n_q_heads) float32.  ``scale`` defaults to head_dim ** -0.5.  ``workspace``: a uint8 tensor of
     fct_tree_attention_workspace_size bytes to keep between calls (allocated here if None).
     """
+    if stream is not None:
+        return on_stream(fct_tree_attention, stream, cache.index, q, cache, block_table, context_len,
+                         node_start, tree_mask, scale=scale, out=out, lse=lse, workspace=workspace,
+                         dev_status=dev_status)
     index = cache.index
     shape = q.shape
     if len(shape) != 3 or shape[2] != cache.head_dim or shape[1] % cache.n_heads != 0:
@@ -1104,7 +1132,7 @@ def fct_tree_attention(q, cache, block_table, context_len, node_start, tree_mask
         _vec(node_start, torch.int32, B + 1, index, "node_start"), B, mask, words,
         D ** -0.5 if scale is None else scale, o_ptr, o_node, o_head, lse.data_ptr(),
         workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _status_ptr(dev_status), _raw_stream(stream, index))
+        _status_ptr(dev_status), _raw_stream(index))
     _check(rc, "fct_tree_attention")
     return out, lse
 
@@ -1124,6 +1152,11 @@ def fct_spec_verify(target_logits, tokens, parent, node_start, uniform, noise, d
     ``out_tokens`` (batch, max_depth + 1) int64: the accepted tokens, the next token, then -1;
     ``path`` (batch, max_depth) int32: the accepted nodes; ``count`` (batch,) int32: how many.
     """
+    if stream is not None:
+        return on_stream(fct_spec_verify, stream, target_logits.get_device(), target_logits, tokens,
+                         parent, node_start, uniform, noise, draft_logits, temperature,
+                         max_depth=max_depth, out_tokens=out_tokens, path=path, count=count,
+                         dev_status=dev_status)
     dtype = target_logits.dtype
     code = FCT_BF16 if dtype is torch.bfloat16 else FCT_F32
     if code == FCT_F32 and dtype is not torch.float32:
@@ -1164,6 +1197,6 @@ def fct_spec_verify(target_logits, tokens, parent, node_start, uniform, noise, d
         _vec(uniform, torch.float32, N, index, "uniform"), nse, ld_n,
         _vec(temperature, torch.float32, B, index, "temperature") if temperature is not None
         else None, P, out_tokens.data_ptr(), path.data_ptr(), count.data_ptr(),
-        _status_ptr(dev_status), _raw_stream(stream, index))
+        _status_ptr(dev_status), _raw_stream(index))
     _check(rc, "fct_spec_verify")
     return out_tokens, path, count
