@@ -53,11 +53,16 @@ def commit(caches, block_table, context_len, target_logits, tokens, parent, node
     """Verify the drafted trees and keep what was accepted: (out_tokens, path, count, new
     context_len).  The accepted nodes' keys and values move behind the context in every cache of
     ``caches``; the last value of a request's out_tokens is its next node 0."""
+    if stream is not None:
+        return binding.on_stream(
+            commit, stream, target_logits.get_device(), caches, block_table, context_len,
+            target_logits, tokens, parent, node_start, uniform, noise, draft_logits, temperature,
+            max_depth=max_depth, dev_status=dev_status)
     out, path, count = binding.fct_spec_verify(
         target_logits, tokens, parent, node_start, uniform, noise, draft_logits, temperature,
-        max_depth=max_depth, dev_status=dev_status, stream=stream)
+        max_depth=max_depth, dev_status=dev_status)
     for cache in caches:
         binding.fct_kv_cache_move(cache, block_table, context_len, path, count,
-                                  dev_status=dev_status, stream=stream)
+                                  dev_status=dev_status)
     has_nodes = (node_start[1:] > node_start[:-1]).to(torch.int32)
     return out, path, count, context_len + has_nodes + count

@@ -5,7 +5,7 @@ import torch
 
 import test_gpu_tree_attention as attention
 import test_gpu_verify as verification
-from distillation_ce_tvd_gb300 import binding
+from distillation_ce_tvd_gb300 import binding, speculative
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -45,10 +45,15 @@ def test_attention_without_a_workspace(raw):
 def test_verification_outputs():
     c = verification.case([6] * 8, 3000, torch.float32, True, seed=1)
     want, _ = verification.run(c, 5)
-    side = torch.cuda.Stream()
-    got, st = verification.run(c, 5, stream=side)
-    torch.cuda.synchronize()
-    assert st == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
+    args = [c[x].to(DEV) for x in ("target", "tokens", "parent")] \
+        + [torch.tensor(c["starts"], dtype=torch.int32, device=DEV)] \
+        + [c[x].to(DEV) for x in ("uniform", "noise", "draft")]
+    side = busy_side_stream()
+    got = binding.fct_spec_verify(*args, max_depth=5, stream=side)
+    junk = fill([x.numel() * x.element_size() for x in got])
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a.cpu(), b) for a, b in zip(got, want))
+    del junk
 
 
 def test_the_default_streams_handles():
@@ -57,3 +62,24 @@ def test_the_default_streams_handles():
     for handle in (0, 1):
         torch.cuda.synchronize()
         assert torch.equal(attention.run(c, stream=handle)[0], want)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_commit(raw):
+    # the new context lengths wait for verification
+    c = verification.case([6] * 8, 3000, torch.float32, True, seed=1)
+    want, _ = verification.run(c, 5)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    pool = torch.zeros((16, 16, 2, 64), dtype=torch.bfloat16, device=DEV)
+    table, context = torch.arange(16, **i32).view(8, 2), torch.arange(8, **i32)
+    args = [c[x].to(DEV) for x in ("target", "tokens", "parent")] \
+        + [torch.tensor(c["starts"], dtype=torch.int32, device=DEV)] \
+        + [c[x].to(DEV) for x in ("uniform", "noise", "draft")]
+    side = busy_side_stream()
+    out, path, count, lengths = speculative.commit(
+        [binding.KVCache(pool, pool.clone())], table, context, *args, max_depth=5,
+        stream=side.cuda_stream if raw else side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a.cpu(), b) for a, b in zip((out, path, count), want))
+    assert torch.equal(lengths.cpu(), torch.arange(8, dtype=torch.int32) + 1 + want[2])
+    assert 0 < int(want[2].sum())

@@ -5,7 +5,7 @@ import contextlib
 import pytest
 import torch
 
-from distillation_ce_tvd_gb300 import binding
+from distillation_ce_tvd_gb300 import binding, speculative
 
 BF16 = torch.bfloat16
 HERE, SIDE = object(), object()
@@ -98,3 +98,25 @@ def test_what_a_call_allocates_belongs_to_its_stream(lib, call):
     call(cache(), stream=SIDE)
     assert [c[1] for c in lib.calls] == [HERE, SIDE] and lib.now is HERE
     assert len(lib.made) == 2 * made and all(now is SIDE for now, _, _ in lib.made[made:])
+
+
+def test_the_new_context_lengths_are_computed_on_the_calls_stream(lib):
+    # they depend on what verification writes there
+    class Watch(torch.overrides.TorchFunctionMode):
+        sums = []
+
+        def __torch_function__(self, f, types, args=(), kwargs=None):
+            if getattr(f, "__name__", "") in ("add", "__add__", "gt", "__gt__"):
+                self.sums.append(lib.now)
+            return f(*args, **(kwargs or {}))
+    z = torch.zeros((5, 10))
+    args = ([cache(), cache()], *PAGES, z, torch.zeros(5, dtype=torch.int64), torch.zeros(5, **I32),
+            STARTS, torch.zeros(5), torch.ones((2, 10)))
+    for stream in (None, SIDE):
+        lib.calls.clear()
+        Watch.sums.clear()
+        with Watch():
+            speculative.commit(*args, max_depth=2, stream=stream)
+        want = HERE if stream is None else SIDE
+        assert [c[:2] for c in lib.calls] == [("fct_spec_verify", want)] + [("fct_kv_cache_move", want)] * 2
+        assert len(Watch.sums) >= 3 and all(x is want for x in Watch.sums)
