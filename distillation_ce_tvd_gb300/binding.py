@@ -9,6 +9,7 @@ the library cannot be built or loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import threading
 
 import torch
@@ -239,6 +240,40 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def on_stream(f, stream, index, /, *args, **kw):
+    """``f(*args, **kw)`` with ``stream`` (a torch stream, or a raw handle) as the current stream of
+    CUDA device ``index``, so that what f allocates or computes in torch is ordered with what it
+    launches there.  The tensors it returns may be used on the caller's stream too, once that has
+    waited for ``stream``."""
+    handle = int(getattr(stream, "cuda_stream", stream))
+    caller = torch.cuda.current_stream(index)
+    if handle == caller.cuda_stream and torch.cuda.current_device() == index:
+        return f(*args, **kw)
+    if not isinstance(stream, torch.cuda.Stream):
+        if handle == 2:
+            raise ValueError("the per-thread default stream cannot be made current in torch")
+        stream = torch.cuda.default_stream(index) if handle < 2 else torch.cuda.ExternalStream(handle, device=index)
+    with torch.cuda.stream(stream):
+        out = f(*args, **kw)
+    if caller != stream:
+        for x in out if isinstance(out, tuple) else (out,):
+            if isinstance(x, torch.Tensor) and x.is_cuda:
+                x.record_stream(caller)
+    return out
+
+
+def _streamed(f):
+    """A call whose ``stream=`` is the current stream while it runs (see on_stream)."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is not None:
+            index = next((x.get_device() for x in (*args, *kw.values()) if torch.is_tensor(x)), -1)
+            if index >= 0:
+                return on_stream(f, stream, index, *args, **kw)
+        return f(*args, **kw)
+    return call
+
+
 def _check(rc: int, what: str):
     if rc != 0:
         raise FctError(rc, what)
@@ -252,6 +287,7 @@ def _out(x, n, device, name):
 
 # ------------------------------------------------------------------ entry points
 
+@_streamed
 def fused_ce_tvd_forward(student, teacher, target, ignore_index=IGNORE_INDEX, *, ce=None,
                          tvd=None, student_lse=None, teacher_lse=None, sigma=None,
                          dev_status=None, stream=None, options=None):
@@ -273,6 +309,7 @@ def fused_ce_tvd_forward(student, teacher, target, ignore_index=IGNORE_INDEX, *,
     return tuple(outs)
 
 
+@_streamed
 def fused_ce_tvd_backward(student, teacher, target, student_lse, teacher_lse, sigma,
                           grad_ce, grad_tvd, ignore_index=IGNORE_INDEX, *, grad_student=None,
                           inplace=False, dev_status=None, stream=None):
@@ -310,6 +347,7 @@ def fused_ce_tvd_backward(student, teacher, target, student_lse, teacher_lse, si
     return grad_student
 
 
+@_streamed
 def fused_ce_tvd_forward_backward(student, teacher, target, grad_ce, grad_tvd,
                                   ignore_index=IGNORE_INDEX, *, ce=None, tvd=None,
                                   student_lse=None, teacher_lse=None, sigma=None,
@@ -367,6 +405,7 @@ def _signs(x, BT, V, dtype, device):
     return x
 
 
+@_streamed
 def fused_ce_tvd_forward_signs(student, teacher, target, ignore_index=IGNORE_INDEX, *, ce=None,
                                tvd=None, student_lse=None, teacher_lse=None, sigma=None,
                                signs=None, dev_status=None, stream=None, options=None):
@@ -392,6 +431,7 @@ def fused_ce_tvd_forward_signs(student, teacher, target, ignore_index=IGNORE_IND
     return (*outs, signs)
 
 
+@_streamed
 def fused_ce_tvd_backward_signs(student, teacher, target, student_lse, teacher_lse, sigma, signs,
                                 grad_ce, grad_tvd, ignore_index=IGNORE_INDEX, *,
                                 grad_student=None, inplace=False, dev_status=None, stream=None):
@@ -428,6 +468,7 @@ def fused_ce_tvd_backward_signs(student, teacher, target, student_lse, teacher_l
     return grad_student
 
 
+@_streamed
 def ce_forward(logits, target, ignore_index=IGNORE_INDEX, *, ce=None, lse=None,
                dev_status=None, stream=None, options=None):
     """Per-row (ce, lse) of plain cross-entropy, fp32 (BT,)."""
@@ -444,6 +485,7 @@ def ce_forward(logits, target, ignore_index=IGNORE_INDEX, *, ce=None, lse=None,
     return ce, lse
 
 
+@_streamed
 def ce_backward(logits, target, lse, grad_ce, ignore_index=IGNORE_INDEX, *, grad_logits=None,
                 inplace=False, dev_status=None, stream=None):
     """Gradient of sum_r grad_ce[r]*ce[r] w.r.t. the logits."""
@@ -466,6 +508,7 @@ def ce_backward(logits, target, lse, grad_ce, ignore_index=IGNORE_INDEX, *, grad
     return grad_logits
 
 
+@_streamed
 def ce_forward_backward(logits, target, grad_ce, ignore_index=IGNORE_INDEX, *, ce=None, lse=None,
                         grad_logits=None, inplace=False, dev_status=None, stream=None,
                         options=None):
@@ -493,6 +536,7 @@ def ce_forward_backward(logits, target, grad_ce, ignore_index=IGNORE_INDEX, *, c
     return ce, lse, grad_logits
 
 
+@_streamed
 def fused_ce_tvd_mean_upstream(target, ignore_index=IGNORE_INDEX, alpha=1.0, beta=1.0, *,
                                grad_ce=None, grad_tvd=None, count=None, stream=None):
     """Upstream gradients (alpha/n, beta/n) of the mean over the n kept rows,
@@ -510,6 +554,7 @@ def fused_ce_tvd_mean_upstream(target, ignore_index=IGNORE_INDEX, alpha=1.0, bet
     return gce, gtvd, cnt
 
 
+@_streamed
 def fused_ce_tvd_mean_loss(ce, tvd, target, ignore_index=IGNORE_INDEX, alpha=1.0, beta=1.0, *,
                            loss=None, stream=None):
     """(alpha * sum ce + beta * sum tvd) / n over the kept rows, as a 1-element tensor."""
@@ -609,7 +654,12 @@ def fused_ce_tvd_forward_backward_host(student, teacher, target, grad_ce, grad_t
     rows = max(1, min(int(block_rows), max(BT, 1)))
     need = fused_ce_tvd_host_workspace_size(V, student.dtype, rows)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), device=dev, dtype=torch.uint8)
+        spec = dict(device=dev, dtype=torch.uint8)
+        if stream is None:
+            workspace = torch.empty(max(need, 1), **spec)
+        else:
+            index = torch.cuda.current_device() if dev.index is None else dev.index
+            workspace = on_stream(torch.empty, stream, index, max(need, 1), **spec)
     if not workspace.is_cuda:
         raise ValueError("workspace must be device memory")
     if status is not None:
@@ -641,6 +691,7 @@ def _parts(x, k, name):
     return x
 
 
+@_streamed
 def fused_ce_tvd_vp_lse(student, teacher, target, v_begin, ignore_index=IGNORE_INDEX, *,
                         part=None, stream=None):
     """Pass 1 on one vocabulary shard: (BT, 3) float32 of the shard's student
@@ -659,6 +710,7 @@ def fused_ce_tvd_vp_lse(student, teacher, target, v_begin, ignore_index=IGNORE_I
     return part
 
 
+@_streamed
 def fused_ce_tvd_vp_merge_lse(parts, target, V, ignore_index=IGNORE_INDEX, *, ce=None,
                               student_lse=None, teacher_lse=None, dev_status=None, stream=None):
     """Merge of pass 1 over the shards (``parts``: (n_shards, BT, 3), shard
@@ -676,6 +728,7 @@ def fused_ce_tvd_vp_merge_lse(parts, target, V, ignore_index=IGNORE_INDEX, *, ce
     return tuple(outs)
 
 
+@_streamed
 def fused_ce_tvd_vp_tvd(student, teacher, target, student_lse, teacher_lse,
                         ignore_index=IGNORE_INDEX, *, part=None, stream=None):
     """Pass 2 on one shard: (BT, 2) float32 of the shard's sum of p*sign(p - q)
@@ -694,6 +747,7 @@ def fused_ce_tvd_vp_tvd(student, teacher, target, student_lse, teacher_lse,
     return part
 
 
+@_streamed
 def fused_ce_tvd_vp_merge_tvd(parts, target, ignore_index=IGNORE_INDEX, *, tvd=None, sigma=None,
                               stream=None):
     """Merge of pass 2 over the shards (``parts``: (n_shards, BT, 2)): (tvd, sigma)."""
@@ -708,6 +762,7 @@ def fused_ce_tvd_vp_merge_tvd(parts, target, ignore_index=IGNORE_INDEX, *, tvd=N
     return tuple(outs)
 
 
+@_streamed
 def fused_ce_tvd_vp_backward(student, teacher, target, v_begin, V, student_lse, teacher_lse, sigma,
                              grad_ce, grad_tvd, ignore_index=IGNORE_INDEX, *, grad_student=None,
                              inplace=False, dev_status=None, stream=None):
@@ -759,6 +814,7 @@ def _mat(x, name):
     return max(int(x.stride(0)) if x.shape[0] > 1 else int(x.shape[1]), int(x.shape[1]))
 
 
+@_streamed
 def fused_linear_ce_tvd_forward_backward(h_student, w_student, h_teacher, w_teacher, target,
                                          grad_ce, grad_tvd, ignore_index=IGNORE_INDEX, *,
                                          chunk_rows=2048, logits_dtype=torch.float32,
@@ -834,6 +890,7 @@ def fct_gemm_bf16_workspace_size(M: int, N: int) -> int:
     return int(load().fct_gemm_bf16_workspace_size(int(M), int(N)))
 
 
+@_streamed
 def fct_gemm_bf16(a, b, c=None, *, accumulate=False, out_dtype=torch.float32, workspace=None,
                   dev_status=None, stream=None):
     """C = a @ b.T (or C += a @ b.T into an fp32 c) on the library's tcgen05 GEMM.
@@ -976,26 +1033,6 @@ def _raw_stream(index):
     if _current_raw_stream is not None:
         return _current_raw_stream(index)
     return torch.cuda.current_stream(index).cuda_stream
-
-
-def on_stream(f, stream, index, /, *args, **kw):
-    """``f(*args, **kw)`` with ``stream`` (a torch stream, or a raw handle) as the current stream of
-    CUDA device ``index``, so that what f allocates or computes in torch is ordered with what it
-    launches there.  The tensors it returns may be used on the caller's stream too, once that has
-    waited for ``stream``."""
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = int(getattr(stream, "cuda_stream", stream))
-        if handle == 2:
-            raise ValueError("the per-thread default stream cannot be made current in torch")
-        stream = torch.cuda.default_stream(index) if handle < 2 else torch.cuda.ExternalStream(handle, device=index)
-    caller = torch.cuda.current_stream(index)
-    with torch.cuda.stream(stream):
-        out = f(*args, **kw)
-    if caller != stream:
-        for x in out if isinstance(out, tuple) else (out,):
-            if isinstance(x, torch.Tensor) and x.is_cuda:
-                x.record_stream(caller)
-    return out
 
 
 def _library():

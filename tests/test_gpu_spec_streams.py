@@ -83,3 +83,20 @@ def test_commit(raw):
     assert all(torch.equal(a.cpu(), b) for a, b in zip((out, path, count), want))
     assert torch.equal(lengths.cpu(), torch.arange(8, dtype=torch.int32) + 1 + want[2])
     assert 0 < int(want[2].sum())
+
+
+def test_the_loss_from_hidden_states():
+    # its workspace and the zero-filled weight gradient
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    h, w, ht, wt = (torch.randn(s, generator=gen, device=DEV).to(torch.bfloat16) * 0.1
+                    for s in ((256, 64), (2048, 64), (256, 128), (2048, 128)))
+    target = torch.randint(0, 2048, (256,), generator=gen, device=DEV)
+    args = (h, w, ht, wt, target, 1 / 256, 1 / 256)
+    want = binding.fused_linear_ce_tvd_forward_backward(*args, chunk_rows=64)
+    need = binding.fused_linear_ce_tvd_workspace_size(2048, 64)
+    side = busy_side_stream()
+    got = binding.fused_linear_ce_tvd_forward_backward(*args, chunk_rows=64, stream=side)
+    junk = fill([need] + [x.numel() * x.element_size() for x in got])
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    del junk

@@ -8,12 +8,19 @@ import torch
 from distillation_ce_tvd_gb300 import binding, speculative
 
 BF16 = torch.bfloat16
-HERE, SIDE = object(), object()
+
+
+class Stream:
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+HERE, SIDE = Stream(0), Stream(64)
 
 
 class Recorder:
     def __init__(self):
-        self.calls, self.made, self.now, self.device = [], [], HERE, 0
+        self.calls, self.made, self.marked, self.now, self.device = [], [], [], HERE, 0
 
     def __getattr__(self, name):
         if name.endswith("workspace_size"):
@@ -46,10 +53,13 @@ def lib(monkeypatch):
     monkeypatch.setattr(binding, "_library", lambda: r)
     monkeypatch.setattr(binding, "_raw_stream", lambda *a: 0)
     monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda self, s: r.marked.append((s, self)))
     monkeypatch.setattr(torch.cuda, "stream", under)
     monkeypatch.setattr(torch.cuda, "device", on)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: r.now)
-    monkeypatch.setattr(torch.cuda, "Stream", object)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: r.device)
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
     monkeypatch.setattr(torch, "empty", noted)
     return r
 
@@ -98,6 +108,8 @@ def test_what_a_call_allocates_belongs_to_its_stream(lib, call):
     call(cache(), stream=SIDE)
     assert [c[1] for c in lib.calls] == [HERE, SIDE] and lib.now is HERE
     assert len(lib.made) == 2 * made and all(now is SIDE for now, _, _ in lib.made[made:])
+    # the results are marked as used by the caller's stream
+    assert [s for s, _ in lib.marked] == [HERE] * {write: 0, move: 0, attend: 2, verify: 3}[call]
 
 
 def test_the_new_context_lengths_are_computed_on_the_calls_stream(lib):
@@ -120,3 +132,44 @@ def test_the_new_context_lengths_are_computed_on_the_calls_stream(lib):
         want = HERE if stream is None else SIDE
         assert [c[:2] for c in lib.calls] == [("fct_spec_verify", want)] + [("fct_kv_cache_move", want)] * 2
         assert len(Watch.sums) >= 3 and all(x is want for x in Watch.sums)
+
+
+def loss_calls():
+    z, t = torch.zeros((4, 8)), torch.zeros(4, dtype=torch.int64)
+    row, one = torch.zeros(4), torch.ones(1)
+    signs = torch.zeros((4, 16), dtype=torch.uint8)
+    h, w = torch.zeros((4, 8), dtype=BF16), torch.zeros((16, 8), dtype=BF16)
+    b = binding
+    return {
+        "forward": lambda **k: b.fused_ce_tvd_forward(z, z, t, **k),
+        "backward": lambda **k: b.fused_ce_tvd_backward(z, z, t, row, row, row, one, row, **k),
+        "forward_backward": lambda **k: b.fused_ce_tvd_forward_backward(z, z, t, one, row, **k),
+        "ce_forward": lambda **k: b.ce_forward(z, t, **k),
+        "ce_backward": lambda **k: b.ce_backward(z, t, row, row, **k),
+        "ce_forward_backward": lambda **k: b.ce_forward_backward(z, t, row, **k),
+        "mean_upstream": lambda **k: b.fused_ce_tvd_mean_upstream(t, **k),
+        "mean_loss": lambda **k: b.fused_ce_tvd_mean_loss(row, row, t, **k),
+        "vp_lse": lambda **k: b.fused_ce_tvd_vp_lse(z, z, t, 0, **k),
+        "vp_backward": lambda **k: b.fused_ce_tvd_vp_backward(z, z, t, 0, 8, row, row, row, one, one, **k),
+        "linear": lambda **k: b.fused_linear_ce_tvd_forward_backward(h, w, h, w, t, one, row, **k),
+        "gemm": lambda **k: b.fct_gemm_bf16(h, w, **k),
+    }
+
+
+@pytest.mark.parametrize("name", sorted(loss_calls()))
+def test_so_it_does_in_the_loss_calls(lib, name):
+    # zero-filled gradients and broadcast upstream values too
+    class Watch(torch.overrides.TorchFunctionMode):
+        made = []
+
+        def __torch_function__(self, f, types, args=(), kwargs=None):
+            if getattr(f, "__name__", "") in ("empty_like", "zeros", "contiguous", "expand", "to"):
+                self.made.append(lib.now)
+            return f(*args, **(kwargs or {}))
+    call = loss_calls()[name]
+    Watch.made.clear()
+    with Watch():
+        call(stream=SIDE)
+    assert len(lib.calls) == 1 and lib.calls[0][1] is SIDE
+    assert all(now is SIDE for now, _, _ in lib.made) and all(now is SIDE for now in Watch.made)
+    assert len(lib.made) + len(Watch.made) > 0
