@@ -40,16 +40,17 @@ def step(student, teacher, target, v_begin, V, grad_ce, grad_tvd, exchange,
     Returns (ce, tvd, student_lse, teacher_lse, sigma, grad) with grad the
     gradient of this shard's columns.
     """
-    part1 = ops.fused_ce_tvd_vp_lse(student, teacher, target, v_begin, ignore_index, stream=stream)
+    if stream is not None:  # the exchange too is ordered with the passes
+        return binding.on_stream(step, stream, student.get_device(), student, teacher, target,
+                                 v_begin, V, grad_ce, grad_tvd, exchange, ignore_index, ops=ops,
+                                 dev_status=dev_status)
+    part1 = ops.fused_ce_tvd_vp_lse(student, teacher, target, v_begin, ignore_index)
     ce, lse_s, lse_t = ops.fused_ce_tvd_vp_merge_lse(exchange(part1), target, V, ignore_index,
-                                                     dev_status=dev_status, stream=stream)
-    part2 = ops.fused_ce_tvd_vp_tvd(student, teacher, target, lse_s, lse_t, ignore_index,
-                                    stream=stream)
-    tvd, sigma = ops.fused_ce_tvd_vp_merge_tvd(exchange(part2), target, ignore_index,
-                                               stream=stream)
+                                                     dev_status=dev_status)
+    part2 = ops.fused_ce_tvd_vp_tvd(student, teacher, target, lse_s, lse_t, ignore_index)
+    tvd, sigma = ops.fused_ce_tvd_vp_merge_tvd(exchange(part2), target, ignore_index)
     grad = ops.fused_ce_tvd_vp_backward(student, teacher, target, v_begin, V, lse_s, lse_t, sigma,
-                                        grad_ce, grad_tvd, ignore_index, dev_status=dev_status,
-                                        stream=stream)
+                                        grad_ce, grad_tvd, ignore_index, dev_status=dev_status)
     return ce, tvd, lse_s, lse_t, sigma, grad
 
 
@@ -71,20 +72,24 @@ def forward_backward_local(student, teacher, target, n_shards, grad_ce, grad_tvd
     views of the full (BT, V) logits: pass 1 on every shard, the merge, pass 2
     on every shard, the merge, the backward on every shard.  Returns the
     per-row outputs and the full (BT, V) gradient."""
+    if stream is not None:  # the stacking too is ordered with the passes
+        return binding.on_stream(forward_backward_local, stream, student.get_device(), student,
+                                 teacher, target, n_shards, grad_ce, grad_tvd, ignore_index,
+                                 dev_status=dev_status)
     BT, V = student.shape
     bounds = [shard_bounds(V, n_shards, k, student.element_size()) for k in range(n_shards)]
     bounds = [(b, e) for b, e in bounds if e > b]
     views = [(student[:, b:e], teacher[:, b:e], b) for b, e in bounds]
-    parts1 = torch.stack([binding.fused_ce_tvd_vp_lse(s, t, target, b, ignore_index, stream=stream)
+    parts1 = torch.stack([binding.fused_ce_tvd_vp_lse(s, t, target, b, ignore_index)
                           for s, t, b in views])
     ce, lse_s, lse_t = binding.fused_ce_tvd_vp_merge_lse(parts1, target, V, ignore_index,
-                                                         dev_status=dev_status, stream=stream)
-    parts2 = torch.stack([binding.fused_ce_tvd_vp_tvd(s, t, target, lse_s, lse_t, ignore_index,
-                                                      stream=stream) for s, t, _ in views])
-    tvd, sigma = binding.fused_ce_tvd_vp_merge_tvd(parts2, target, ignore_index, stream=stream)
+                                                         dev_status=dev_status)
+    parts2 = torch.stack([binding.fused_ce_tvd_vp_tvd(s, t, target, lse_s, lse_t, ignore_index)
+                          for s, t, _ in views])
+    tvd, sigma = binding.fused_ce_tvd_vp_merge_tvd(parts2, target, ignore_index)
     grad = torch.empty_like(student)
     for (s, t, b), (_, e) in zip(views, bounds):
         binding.fused_ce_tvd_vp_backward(s, t, target, b, V, lse_s, lse_t, sigma, grad_ce,
                                          grad_tvd, ignore_index, grad_student=grad[:, b:e],
-                                         dev_status=dev_status, stream=stream)
+                                         dev_status=dev_status)
     return ce, tvd, lse_s, lse_t, sigma, grad

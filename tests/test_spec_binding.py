@@ -5,7 +5,7 @@ import contextlib
 import pytest
 import torch
 
-from distillation_ce_tvd_gb300 import binding, speculative
+from distillation_ce_tvd_gb300 import binding, speculative, vocab_parallel
 
 BF16 = torch.bfloat16
 
@@ -173,3 +173,23 @@ def test_so_it_does_in_the_loss_calls(lib, name):
     assert len(lib.calls) == 1 and lib.calls[0][1] is SIDE
     assert all(now is SIDE for now, _, _ in lib.made) and all(now is SIDE for now in Watch.made)
     assert len(lib.made) + len(Watch.made) > 0
+
+
+def test_the_vocabulary_shards_partials_are_exchanged_on_the_steps_stream(lib):
+    z, t, one = torch.zeros((4, 16)), torch.zeros(4, dtype=torch.int64), torch.ones(1)
+    seen = []
+
+    def exchange(part):
+        seen.append(lib.now)
+        return torch.stack([part, part])
+
+    class Watch(torch.overrides.TorchFunctionMode):
+        def __torch_function__(self, f, types, args=(), kwargs=None):
+            if getattr(f, "__name__", "") == "stack":
+                seen.append(lib.now)
+            return f(*args, **(kwargs or {}))
+    vocab_parallel.step(z[:, :8], z[:, :8], t, 0, 16, one, one, exchange, stream=SIDE)
+    assert seen == [SIDE] * 2 and all(c[1] is SIDE for c in lib.calls) and len(lib.calls) == 5
+    with Watch():
+        vocab_parallel.forward_backward_local(z, z, t, 2, one, one, stream=SIDE)
+    assert seen == [SIDE] * 4 and all(c[1] is SIDE for c in lib.calls) and len(lib.calls) == 13
