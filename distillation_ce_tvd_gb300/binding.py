@@ -253,6 +253,8 @@ def on_stream(f, stream, index, /, *args, **kw):
         if handle == 2:
             raise ValueError("the per-thread default stream cannot be made current in torch")
         stream = torch.cuda.default_stream(index) if handle < 2 else torch.cuda.ExternalStream(handle, device=index)
+    elif stream.device_index != index:
+        raise ValueError(f"stream is of cuda:{stream.device_index}, the tensors are on cuda:{index}")
     with torch.cuda.stream(stream):
         out = f(*args, **kw)
     if caller != stream:
@@ -260,6 +262,13 @@ def on_stream(f, stream, index, /, *args, **kw):
             if isinstance(x, torch.Tensor) and x.is_cuda:
                 x.record_stream(caller)
     return out
+
+
+def on_device(f, index, /, *args, **kw):
+    """``f(*args, **kw)`` with CUDA device ``index`` current: the library launches on the calling
+    thread's device."""
+    with torch.cuda.device(index):
+        return f(*args, **kw)
 
 
 def _streamed(f):
@@ -1068,6 +1077,8 @@ def fct_kv_cache_write(cache, k, v, slots, *, dev_status=None, stream=None):
     if stream is not None:
         return on_stream(fct_kv_cache_write, stream, cache.index, cache, k, v, slots,
                          dev_status=dev_status)
+    if torch.cuda.current_device() != cache.index:
+        return on_device(fct_kv_cache_write, cache.index, cache, k, v, slots, dev_status=dev_status)
     code = FCT_BF16 if k.dtype is torch.bfloat16 else FCT_F32
     if code == FCT_F32 and k.dtype is not torch.float32:
         raise TypeError(f"k: dtype {k.dtype} is not float32 or bfloat16")
@@ -1091,6 +1102,9 @@ def fct_kv_cache_move(cache, block_table, context_len, path, count, *, dev_statu
     if stream is not None:
         return on_stream(fct_kv_cache_move, stream, cache.index, cache, block_table, context_len,
                          path, count, dev_status=dev_status)
+    if torch.cuda.current_device() != cache.index:
+        return on_device(fct_kv_cache_move, cache.index, cache, block_table, context_len, path,
+                         count, dev_status=dev_status)
     B, index = context_len.shape[0], cache.index
     tab, ld_t, pages = _table(block_table, torch.int32, B, index, "block_table")
     pth, ld_p, depth = _table(path, torch.int32, B, index, "path")
@@ -1103,7 +1117,7 @@ def fct_kv_cache_move(cache, block_table, context_len, path, count, *, dev_statu
 
 def fct_tree_attention_workspace_size(n_nodes: int, n_q_heads: int, n_kv_heads: int,
                                       head_dim: int) -> int:
-    """Bytes of device workspace fct_tree_attention needs."""
+    """Bytes of device workspace fct_tree_attention needs on the current device."""
     return int(load().fct_tree_attention_workspace_size(int(n_nodes), int(n_q_heads),
                                                         int(n_kv_heads), int(head_dim)))
 
@@ -1136,6 +1150,10 @@ def fct_tree_attention(q, cache, block_table, context_len, node_start, tree_mask
                          node_start, tree_mask, scale=scale, out=out, lse=lse, workspace=workspace,
                          dev_status=dev_status)
     index = cache.index
+    if torch.cuda.current_device() != index:
+        return on_device(fct_tree_attention, index, q, cache, block_table, context_len, node_start,
+                         tree_mask, scale=scale, out=out, lse=lse, workspace=workspace,
+                         dev_status=dev_status)
     shape = q.shape
     if len(shape) != 3 or shape[2] != cache.head_dim or shape[1] % cache.n_heads != 0:
         raise ValueError("q must be (n_nodes, n_q_heads, head_dim) with the cache's head_dim and a "
@@ -1201,6 +1219,10 @@ def fct_spec_verify(target_logits, tokens, parent, node_start, uniform, noise, d
     index = target_logits.get_device()
     if index < 0 or target_logits.dim() != 2:
         raise ValueError("target_logits must be a (n_nodes, V) CUDA tensor")
+    if torch.cuda.current_device() != index:
+        return on_device(fct_spec_verify, index, target_logits, tokens, parent, node_start, uniform,
+                         noise, draft_logits, temperature, max_depth=max_depth,
+                         out_tokens=out_tokens, path=path, count=count, dev_status=dev_status)
     N, V = target_logits.shape
     tgt, ld_t, _ = _table(target_logits, dtype, N, index, "target_logits")
     dft, ld_d = None, 0

@@ -12,7 +12,7 @@ BF16 = torch.bfloat16
 
 class Stream:
     def __init__(self, handle):
-        self.cuda_stream = handle
+        self.cuda_stream, self.device_index = handle, 0
 
 
 HERE, SIDE = Stream(0), Stream(64)
@@ -20,11 +20,12 @@ HERE, SIDE = Stream(0), Stream(64)
 
 class Recorder:
     def __init__(self):
-        self.calls, self.made, self.marked, self.now, self.device = [], [], [], HERE, 0
+        self.calls, self.made, self.marked, self.asked = [], [], [], []
+        self.now, self.device = HERE, 0
 
     def __getattr__(self, name):
         if name.endswith("workspace_size"):
-            return lambda *a: 4096
+            return lambda *a: self.asked.append(self.device) or 4096
         return lambda *a: self.calls.append((name, self.now, self.device, a)) or 0
 
 
@@ -132,6 +133,18 @@ def test_the_new_context_lengths_are_computed_on_the_calls_stream(lib):
         want = HERE if stream is None else SIDE
         assert [c[:2] for c in lib.calls] == [("fct_spec_verify", want)] + [("fct_kv_cache_move", want)] * 2
         assert len(Watch.sums) >= 3 and all(x is want for x in Watch.sums)
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_a_call_runs_on_its_tensors_device(lib, call):
+    lib.device = 1                      # the tensors say 0
+    call(cache())
+    assert [c[2] for c in lib.calls] == [0] and all(d == 0 for _, d, _ in lib.made)
+    assert lib.asked == [0] * (call is attend) and lib.device == 1
+    other = Stream(128)
+    other.device_index = 1
+    with pytest.raises(ValueError):
+        call(cache(), stream=other)
 
 
 def loss_calls():
