@@ -1065,8 +1065,13 @@ def _table(x, dtype, rows, index, name):
     return x.data_ptr(), (x.stride(0) if rows > 1 else shape[1]), shape[1]
 
 
-def _status_ptr(x):
-    return x.data_ptr() if x is not None else None
+def _status_ptr(x, index):
+    """The address of the status word on CUDA device ``index``, or None."""
+    if x is None:
+        return None
+    if x.dtype is not torch.int32 or x.numel() < 1 or x.get_device() != index:
+        raise ValueError(f"dev_status must be an int32 tensor on cuda:{index}")
+    return x.data_ptr()
 
 
 def fct_kv_cache_write(cache, k, v, slots, *, dev_status=None, stream=None):
@@ -1091,7 +1096,7 @@ def fct_kv_cache_write(cache, k, v, slots, *, dev_status=None, stream=None):
     n = shape[0]
     rc = _library().fct_kv_cache_write(k.data_ptr(), v.data_ptr(), strides[0], strides[1], code, n,
                                        _vec(slots, torch.int64, n, index, "slots"), cache.ref,
-                                       _status_ptr(dev_status), _raw_stream(index))
+                                       _status_ptr(dev_status, index), _raw_stream(index))
     _check(rc, "fct_kv_cache_write")
 
 
@@ -1111,7 +1116,7 @@ def fct_kv_cache_move(cache, block_table, context_len, path, count, *, dev_statu
     rc = _library().fct_kv_cache_move(cache.ref, tab, ld_t, pages,
                                       _vec(context_len, torch.int32, B, index, "context_len"), B,
                                       pth, ld_p, depth, _vec(count, torch.int32, B, index, "count"),
-                                      _status_ptr(dev_status), _raw_stream(index))
+                                      _status_ptr(dev_status, index), _raw_stream(index))
     _check(rc, "fct_kv_cache_move")
 
 
@@ -1181,13 +1186,15 @@ def fct_tree_attention(q, cache, block_table, context_len, node_start, tree_mask
         workspace = torch.empty(
             fct_tree_attention_workspace_size(N, H, cache.n_heads, D) if N else 0,
             device=cache.device, dtype=torch.uint8)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
     rc = _library().fct_tree_attention(
         q_ptr, q_node, q_head, N, H, cache.ref, tab, ld_t, pages,
         _vec(context_len, torch.int32, B, index, "context_len"),
         _vec(node_start, torch.int32, B + 1, index, "node_start"), B, mask, words,
         D ** -0.5 if scale is None else scale, o_ptr, o_node, o_head, lse.data_ptr(),
         workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _status_ptr(dev_status), _raw_stream(index))
+        _status_ptr(dev_status, index), _raw_stream(index))
     _check(rc, "fct_tree_attention")
     return out, lse
 
@@ -1256,6 +1263,6 @@ def fct_spec_verify(target_logits, tokens, parent, node_start, uniform, noise, d
         _vec(uniform, torch.float32, N, index, "uniform"), nse, ld_n,
         _vec(temperature, torch.float32, B, index, "temperature") if temperature is not None
         else None, P, out_tokens.data_ptr(), path.data_ptr(), count.data_ptr(),
-        _status_ptr(dev_status), _raw_stream(index))
+        _status_ptr(dev_status, index), _raw_stream(index))
     _check(rc, "fct_spec_verify")
     return out_tokens, path, count

@@ -206,3 +206,26 @@ def test_the_vocabulary_shards_partials_are_exchanged_on_the_steps_stream(lib):
     with Watch():
         vocab_parallel.forward_backward_local(z, z, t, 2, one, one, stream=SIDE)
     assert seen == [SIDE] * 4 and all(c[1] is SIDE for c in lib.calls) and len(lib.calls) == 13
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_the_status_word_and_the_workspace_are_checked(lib, monkeypatch, call):
+    good = torch.zeros(1, **I32)
+    call(cache(), dev_status=good)
+    for bad in (good.long(), good.float(), good[:0]):
+        with pytest.raises(ValueError):
+            call(cache(), dev_status=bad)
+    far = torch.zeros(4096, dtype=torch.uint8)
+    if call is attend:
+        call(cache(), workspace=far)
+        with pytest.raises(ValueError):
+            call(cache(), workspace=torch.zeros((64, 128), dtype=torch.uint8)[:, ::2])
+    # on another device
+    where = {id(good): -1, id(far): 1}
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: where.get(id(self), 0))
+    with pytest.raises(ValueError):
+        call(cache(), dev_status=good)
+    if call is attend:
+        with pytest.raises(ValueError):
+            call(cache(), workspace=far)
+    assert len(lib.calls) == 1 + (call is attend)
