@@ -38,14 +38,28 @@ def ancestor_mask(parents, device, words: int | None = None) -> torch.Tensor:
     return torch.tensor(rows, dtype=torch.int64, device=device).reshape(len(rows), words)
 
 
+#: The slot of a node that has no place in the block table: past any pool, so that
+#: fct_kv_cache_write skips the node and sets FCT_DEV_INDEX_OUT_OF_RANGE.
+NO_SLOT = 2 ** 62
+
+
 def node_slots(block_table: torch.Tensor, context_len: torch.Tensor, node_start: torch.Tensor,
                n_nodes: int, page_size: int) -> torch.Tensor:
     """The cache slots (page * page_size + offset) of all nodes: node i of request b is at position
-    context_len[b] + i."""
+    context_len[b] + i.  Nodes of no request, positions outside the table and entries without a page
+    get NO_SLOT."""
     node = torch.arange(n_nodes, device=block_table.device)
-    b = torch.searchsorted(node_start.long(), node, right=True) - 1
-    pos = context_len.long()[b] + node - node_start.long()[b]
-    return block_table.long()[b, pos // page_size] * page_size + pos % page_size
+    batch, width = block_table.shape
+    if batch == 0 or width == 0:
+        return torch.full_like(node, NO_SLOT)
+    start = node_start.long()
+    b = torch.searchsorted(start, node, right=True) - 1
+    held = (b >= 0) & (b < batch)
+    b = b.clamp(0, batch - 1)
+    pos = context_len.long()[b] + node - start[b]
+    held &= (pos >= 0) & (pos < width * page_size)
+    page = block_table.long()[b, (pos // page_size).clamp(0, width - 1)]
+    return torch.where(held & (page >= 0), page * page_size + pos % page_size, NO_SLOT)
 
 
 def commit(caches, block_table, context_len, target_logits, tokens, parent, node_start, uniform,
