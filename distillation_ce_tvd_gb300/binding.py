@@ -1172,6 +1172,8 @@ def fct_tree_attention(q, cache, block_table, context_len, node_start, tree_mask
         mask, ld_m, words = _table(tree_mask, torch.int64, N, index, "tree_mask")
         if ld_m != words:
             raise ValueError("tree_mask must be contiguous")
+        if words == 0 and N > 0:
+            raise ValueError("tree_mask must have at least one word per node")
     if out is None:
         out = torch.empty(shape, device=cache.device, dtype=torch.bfloat16)
         o_ptr, o_node, o_head = out.data_ptr(), H * D, D

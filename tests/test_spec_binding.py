@@ -229,3 +229,12 @@ def test_the_status_word_and_the_workspace_are_checked(lib, monkeypatch, call):
         with pytest.raises(ValueError):
             call(cache(), workspace=far)
     assert len(lib.calls) == 1 + (call is attend)
+
+
+def test_a_mask_without_words_is_not_a_chain(lib):
+    # its address is null, which the library takes for no mask
+    mask = torch.zeros((5, 1), dtype=torch.int64)
+    attend(cache(), tree_mask=mask)
+    with pytest.raises(ValueError):
+        attend(cache(), tree_mask=mask[:, :0])
+    assert len(lib.calls) == 1
