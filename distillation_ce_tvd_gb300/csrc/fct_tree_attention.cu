@@ -61,6 +61,14 @@ __device__ __forceinline__ float scale_of(uint8_t byte) {
 // as an infinity.
 constexpr int kLargeScale = 247;
 
+// Whether node_start[b] .. node_start[b + 1] is not a range of the nodes, or is
+// the first (last) and does not start at 0 (end at n_nodes).
+__device__ __forceinline__ bool bad_nodes(const AttnArgs& a, int64_t b) {
+  const int64_t n0 = a.node_start[b], n1 = a.node_start[b + 1];
+  return n0 < 0 || n1 > a.n_nodes || n1 < n0 || (b == 0 && n0 != 0) ||
+         (b == a.pages.batch - 1 && n1 != a.n_nodes);
+}
+
 __global__ void __launch_bounds__(kGWarps * 32) attention_general_kernel(AttnArgs a, int lanes) {
   __shared__ float sm_m[kGWarps], sm_l[kGWarps];
   __shared__ float sm_o[kGWarps][256];
@@ -75,6 +83,11 @@ __global__ void __launch_bounds__(kGWarps * 32) attention_general_kernel(AttnArg
     if (a.node_start[mid] <= node) lo = mid; else hi = mid;
   }
   const int64_t b = lo, first = a.node_start[b], end = a.node_start[b + 1];
+  if (blockIdx.x == 0) {
+    bool bad = false;
+    for (int64_t r = threadIdx.x; r < a.pages.batch; r += kGWarps * 32) bad |= bad_nodes(a, r);
+    if (bad && a.dev_status) atomicOr(a.dev_status, FCT_DEV_INDEX_OUT_OF_RANGE);
+  }
   if (node < first || node >= end) return;
   const int64_t i = node - first, nodes = end - first;
   int64_t ctx = a.pages.context_len[b], len = ctx + nodes;
@@ -312,8 +325,8 @@ struct RequestShape {
 __device__ __forceinline__ RequestShape request_shape(const AttnArgs& a, const AttnDims& d, int64_t b) {
   RequestShape r;
   int64_t n0 = a.node_start[b], n1 = a.node_start[b + 1];
-  r.bad = n0 < 0 || n1 > a.n_nodes || n1 < n0;
-  if (r.bad) n0 = n1 = 0;
+  r.bad = bad_nodes(a, b);
+  if (n0 < 0 || n1 > a.n_nodes || n1 < n0) n0 = n1 = 0;
   r.node0 = static_cast<int>(n0);
   r.nodes = static_cast<int>(n1 - n0);
   r.ctx = a.pages.context_len[b];

@@ -655,8 +655,9 @@ int fused_ce_tvd_vp_backward(const void* student, int64_t ld_student,
  * Position i of request b lies in page block_table[b * ld_table + i /
  * page_size] at offset i % page_size; entries past a request's last position
  * are not read.  A page index outside the pool, a position past max_pages
- * pages or a negative length sets FCT_DEV_INDEX_OUT_OF_RANGE; nothing outside
- * the arrays is read or written, and that request's outputs are not valid.
+ * pages, a negative length or (in fct_tree_attention) a node_start that is not
+ * as above sets FCT_DEV_INDEX_OUT_OF_RANGE; nothing outside the arrays is read
+ * or written, and that request's outputs are not valid.
  */
 
 /*
