@@ -233,8 +233,11 @@ def test_the_status_word_and_the_workspace_are_checked(lib, monkeypatch, call):
 
 def test_a_mask_without_words_is_not_a_chain(lib):
     # its address is null, which the library takes for no mask
-    mask = torch.zeros((5, 1), dtype=torch.int64)
-    attend(cache(), tree_mask=mask)
-    with pytest.raises(ValueError):
-        attend(cache(), tree_mask=mask[:, :0])
-    assert len(lib.calls) == 1
+    for n in (1, 5):
+        q, mask = torch.zeros((n, 4, 64), dtype=BF16), torch.zeros((n, 1), dtype=torch.int64)
+        args = (cache(), PAGES[0][:1], PAGES[1][:1], torch.tensor([0, n], **I32))
+        lib.calls.clear()
+        binding.fct_tree_attention(q, *args, mask)
+        with pytest.raises(ValueError):
+            binding.fct_tree_attention(q, *args, mask[:, :0])
+        assert len(lib.calls) == 1
