@@ -429,7 +429,8 @@ __global__ void __launch_bounds__(kVThreads, 1)
       held.sibling[i] = p >= 0 && next < nodes ? next : -1;
     }
   const float temp = a.temperature ? a.temperature[b] : 1.f;
-  const bool greedy = !(temp > 0.f);
+  const bool no_temp = !(temp >= 0.f), greedy = !(temp > 0.f);
+  if (no_temp && nodes > 0) status |= FCT_DEV_NO_DISTRIBUTION;
   const float k = greedy ? kLog2e : kLog2e / temp;
   const float* noise = a.noise + b * a.ld_noise;
   int64_t* toks = a.out_tokens + b * (a.max_depth + 1);
@@ -522,7 +523,7 @@ __global__ void __launch_bounds__(kVThreads, 1)
 
   int at = 0, staged = -1;  // staged: the node whose copies are next in turn
   int64_t depth = 0, last = -1;
-  for (bool walking = nodes > 0; walking;) {
+  for (bool walking = nodes > 0 && !no_temp; walking;) {
     const T* tr = target_row(at);
     int c = depth < a.max_depth ? next_child(at, at) : -1;
     if constexpr (kStaged) {

@@ -813,8 +813,9 @@ int fct_tree_attention(const void* q, int64_t ld_q_node, int64_t ld_q_head,
  * race is on log2 of r(v) / noise(v), within 2^-18 of itself.
  * V is at most 2^30, and batch at most 2^24 here, in fct_tree_attention and in
  * fct_kv_cache_move, else FCT_ERR_UNSUPPORTED.
- * A visited row without a distribution (a NaN, +inf, or nothing above -inf)
- * accepts nothing, gives the next token -1 and sets FCT_DEV_NO_DISTRIBUTION.
+ * A visited row without a distribution (a NaN, +inf, or nothing above -inf; any
+ * row at a temperature that is not >= 0) accepts nothing, gives the next token
+ * -1 and sets FCT_DEV_NO_DISTRIBUTION.
  * A request without nodes gets count 0 and tokens -1.
  */
 int fct_spec_verify(const void* target, int64_t ld_target, const void* draft,

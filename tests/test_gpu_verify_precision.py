@@ -108,3 +108,20 @@ def test_a_constant_on_a_row_changes_nothing():
     for a, b in ((1024.0, 0.0), (0.0, 1024.0), (-1024.0, 512.0)):
         got = verify(target + a, *args, draft + b, None, nodes)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_a_temperature_that_is_none_has_no_distribution():
+    # not a number, and below 0: it was taken for greedy
+    V, gen = 500, torch.Generator().manual_seed(5)
+    target, temperature = logits(gen, 8, V, 0.0), torch.tensor([1.0, math.nan, -1.0, 0.0])
+    tokens = torch.zeros(8, dtype=torch.int64)
+    tokens[1::2] = target[::2].argmax(1)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out, path, count = binding.fct_spec_verify(
+        target.to(DEV), tokens.to(DEV), torch.tensor([-1, 0] * 4, dtype=torch.int32, device=DEV),
+        torch.arange(0, 9, 2, dtype=torch.int32, device=DEV), torch.zeros(8, device=DEV),
+        torch.ones((4, V), device=DEV), None, temperature.to(DEV), max_depth=1, dev_status=st)
+    assert st.item() == binding.FCT_DEV_NO_DISTRIBUTION
+    assert count.tolist() == [1, 0, 0, 1] and path[:, 0].tolist() == [1, -1, -1, 1]
+    assert out[1:3].tolist() == [[-1, -1]] * 2
+    assert out[0, 0] == tokens[1] and out[3].tolist() == [int(tokens[7]), int(target[7].argmax())]
