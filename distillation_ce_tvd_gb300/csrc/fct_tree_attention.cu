@@ -263,9 +263,6 @@ struct AttnShape {
   // 12-19 prepare; bf16: 2 prepares, 3 loads V (0 loads K).
   static constexpr int kThreads = kFp8 ? 640 : 384;
   static constexpr int kPrepWarp0 = kFp8 ? 12 : 2, kPrepWarps = kFp8 ? 8 : 1;
-  // Score chunks of 32 keys that a softmax thread holds: what the registers of
-  // 65536 / kThreads allow without spilling.
-  static constexpr int kHold = 1;
   static constexpr int kHalves = kD / 64;  // 128-byte column blocks of a bf16 row
   static constexpr uint32_t kTileBytes = kTile * kD * 2;
   // An e4m3 tile lands kRawAt bytes into its slot, in rows of kD bytes.
@@ -575,24 +572,14 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, bool mn) {
       "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),        \
       "r"(r[29]), "r"(r[30]), "r"(r[31])
 
-// 32 columns of tensor memory, one lane per thread of the warp.
+// 32 columns of tensor memory, one lane per thread of the warp.  The wait has
+// the registers as operands, so that no use of them comes before it.
 __device__ __forceinline__ void tm_ld(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
       "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : FCT_R32(r)
       : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-// The same in two steps: the registers hold their values after tm_ld_done.
-__device__ __forceinline__ void tm_ld_start(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : FCT_R32(r)
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tm_ld_done(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : FCT_RW32(r)::"memory");
 }
 __device__ __forceinline__ void tm_st8(uint32_t taddr, const uint32_t (&r)[8]) {
@@ -742,43 +729,30 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
 // One key tile of a softmax warp: `chunks` (1, 2 or 4) chunks of 32 keys from
 // chunk0 on are its share, of the rows of its 32 lanes.  S's columns become
 // P's (per chunk 16 of the weights in bf16 and 16 of what the rounding left);
-// the chunks of other warps, which hold the same rows, become zero.  kHold
-// chunks are held at a time (S is read twice where there are more), in loops
-// that stay small: the roles of a CTA share one instruction cache.
-template <int kD, int kHold>
+// the chunks of other warps, which hold the same rows, become zero.  One chunk
+// is held at a time (S is read twice where there are more), in loops that stay
+// small: the roles of a CTA share one instruction cache.
+template <int kD>
 __device__ __forceinline__ void soft_tile(const AttnArgs& a, const Segment& seg, uint32_t tm_s,
                                           uint32_t tm_o, int chunk0, int chunks, int node, bool live,
                                           int p0, bool tail, bool first, float sl2, float& m, float& l) {
-  uint32_t x[kHold][32];
-  auto load = [&](int i0) {
-    const uint32_t at = tm_s + 32 * (chunk0 + i0);
-    tm_ld_start(at, x[0]);
-    if (kHold > 1 && chunks > 1) tm_ld_start(at + 32, x[kHold - 1]);
-#pragma unroll
-    for (int i = 0; i < kHold; ++i) tm_ld_done(x[i]);
+  uint32_t x[32];
+  auto load = [&](int i) {
+    tm_ld(tm_s + 32 * (chunk0 + i), x);
     if (tail) {
+      const uint32_t vis = live ? visible32(a, seg, node, p0 + 32 * i) : 0u;
+      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < kHold; ++i) {
-        const uint32_t vis = live ? visible32(a, seg, node, p0 + 32 * (i0 + i)) : 0u;
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 32; ++k) x[i][k] = (vis >> k) & 1u ? x[i][k] : 0xff800000u;
-      }
+      for (int k = 0; k < 32; ++k) x[k] = (vis >> k) & 1u ? x[k] : 0xff800000u;
     }
   };
   float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-  for (int i0 = 0; i0 < chunks; i0 += kHold) {
-    load(i0);
+  for (int i = 0; i < chunks; ++i) {
+    load(i);
 #pragma unroll
-    for (int i = 0; i < kHold; ++i) {
-      if (i < chunks) {
-#pragma unroll
-        for (int k = 0; k < 32; k += 2)
-          tops[(k / 2) % 4] =
-              max3(tops[(k / 2) % 4], __uint_as_float(x[i][k]), __uint_as_float(x[i][k + 1]));
-      }
-    }
+    for (int k = 0; k < 32; k += 2)
+      tops[(k / 2) % 4] = max3(tops[(k / 2) % 4], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
   }
   const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * sl2;
   const bool grow = top > m;
@@ -800,14 +774,14 @@ __device__ __forceinline__ void soft_tile(const AttnArgs& a, const Segment& seg,
   const float off = m == -INFINITY ? 0.f : -m;
   const float2 s2 = make_float2(sl2, sl2), o2 = make_float2(off, off);
   float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
-  auto weights = [&](uint32_t (&y)[32], uint32_t at) {
+  auto weights = [&](uint32_t at) {
     // 16 keys at a time, so that few registers are held
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t p[8], rest[8];
 #pragma unroll
       for (int k = 0; k < 16; k += 2) {
-        float2 e = __ffma2_rn(make_float2(__uint_as_float(y[16 * h + k]), __uint_as_float(y[16 * h + k + 1])),
+        float2 e = __ffma2_rn(make_float2(__uint_as_float(x[16 * h + k]), __uint_as_float(x[16 * h + k + 1])),
                               s2, o2);
         e.x = ex2(e.x);
         e.y = ex2(e.y);
@@ -823,14 +797,10 @@ __device__ __forceinline__ void soft_tile(const AttnArgs& a, const Segment& seg,
       tm_st8(at + 16 + 8 * h, rest);
     }
   };
-  const int last = chunks > kHold ? chunks - kHold : 0;  // its chunks are still held
 #pragma unroll 1
-  for (int i0 = last; i0 >= 0; i0 -= kHold) {
-    if (i0 != last) load(i0);
-    const uint32_t at = tm_s + 32 * (chunk0 + i0);
-#pragma unroll
-    for (int i = 0; i < kHold; ++i)
-      if (i < chunks) weights(x[i], at + 32 * i);
+  for (int i = chunks - 1; i >= 0; --i) {
+    if (i != chunks - 1) load(i);  // (the last is still held)
+    weights(tm_s + 32 * (chunk0 + i));
   }
   if (chunks < 4) {
     const uint32_t zero[16] = {};
@@ -1429,8 +1399,8 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
         if (warp_live) {
           const int p0 = (seg.tile0 + j) * kTile + 32 * chunk0;
           const bool tail = is_tail(seg, seg.tile0 + j);
-          soft_tile<kD, Sh::kHold>(a, seg, tm_s, tm_o + uint32_t(w) * kD, chunk0, span / 32, node, live,
-                                   p0, tail, first, sl2, m, l);
+          soft_tile<kD>(a, seg, tm_s, tm_o + uint32_t(w) * kD, chunk0, span / 32, node, live, p0, tail,
+                        first, sl2, m, l);
         }
         first = false;
         tc_before();
