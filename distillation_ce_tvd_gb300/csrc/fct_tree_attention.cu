@@ -790,8 +790,10 @@ __device__ __forceinline__ void soft_tile(const AttnArgs& a, const Segment& seg,
         else
           sum1 = __fadd2_rn(sum1, e);
         p[k / 2] = pack_bf16x2(e.x, e.y);
-        rest[k / 2] = pack_bf16x2(e.x - __uint_as_float(p[k / 2] << 16),
-                                  e.y - __uint_as_float(p[k / 2] & 0xffff0000u));
+        const float2 r = __ffma2_rn(make_float2(__uint_as_float(p[k / 2] << 16),
+                                                __uint_as_float(p[k / 2] & 0xffff0000u)),
+                                    make_float2(-1.f, -1.f), e);
+        rest[k / 2] = pack_bf16x2(r.x, r.y);
       }
       tm_st8(at + 8 * h, p);
       tm_st8(at + 16 + 8 * h, rest);
@@ -987,10 +989,11 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
     }
   };
 
-  // Puts NaN where the payloads of the key tile at p0 (slot dst) are e4m3's NaN:
-  // rows row0, row0 + step, ..., 16-byte pieces `piece` (+ 4).  Of drafted values
-  // (`clear`) it puts 0, and says whether there were any.
-  auto place_nans = [&](bool is_v, int p0, int row0, int step, int piece, uint32_t dst, bool clear) {
+  // Goes through converted places once more, rows row0, row0 + step, ... of the
+  // key tile at p0 in slot dst, 16-byte pieces `piece` (+ 4): puts NaN where the
+  // payload is e4m3's, and 0 for what is not finite of drafted values (`clear`).
+  // Whether there were any of the latter.
+  auto mend_tile = [&](bool is_v, int p0, int row0, int step, int piece, uint32_t dst, bool clear) {
     bool dropped = false;
 #pragma unroll 1
     for (int row = row0; row < kTile && p0 + row < seg.len; row += step) {
@@ -1003,11 +1006,14 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
 #pragma unroll 1
       for (int i = 0; i < Sh::kHalves * 16; ++i) {
         const int c = piece * 16 + i % 16;  // of a 64-column block
-        if ((src[(i / 16) * 64 + c] & 0x7f) != 0x7f) continue;
+        const uint32_t place = dst + uint32_t(i / 16) * (kTile * 128) + uint32_t(row) * 128 +
+                               uint32_t(((c / 8) ^ (row & 7)) * 16 + (c % 8) * 2);
+        const bool nan = (src[(i / 16) * 64 + c] & 0x7f) == 0x7f;
+        uint16_t x;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(place));
+        if (!nan && !(drop && (x & 0x7f80) == 0x7f80)) continue;
         dropped |= drop;
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + uint32_t(i / 16) * (kTile * 128) + uint32_t(row) * 128 +
-                                                     uint32_t(((c / 8) ^ (row & 7)) * 16 + (c % 8) * 2)),
-                     "h"(static_cast<uint16_t>(drop ? 0 : 0x7fc0))
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(place), "h"(static_cast<uint16_t>(drop ? 0 : 0x7fc0))
                      : "memory");
       }
     }
@@ -1046,8 +1052,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
           const uint32_t out1 = out0 ^ 16u;
           const uint32_t scale = smem_addr(&ctl.raw_scale[slot][t / 4]);
           const bool clear = is_v && is_tail(seg, tile);
-          bool found = false;
-          uint32_t nans = 0;
+          uint32_t odd = 0;  // bit 7 of some byte: this thread's places are looked through once more
           uint32_t in[kHalves][4], byte;
           auto load = [&](int block) {
             asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(scale + uint32_t(kRows) * block));
@@ -1067,19 +1072,22 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
               for (int k = 0; k < 4; ++k) x[h][k] = in[h][k];
             if (block + 1 < kTile / kRows) load(block + 1);
             __syncwarp();
-            const int pos = p0 + block * kRows + t / 4;
-            const bool drafted = clear && pos >= seg.ctx;
-            if (drafted && pos >= seg.len) {
-              e = 127;
+            if (clear) {
+              const int pos = p0 + block * kRows + t / 4;
+              if (pos >= seg.len) {
+                e = 127;
 #pragma unroll
-              for (int h = 0; h < kHalves; ++h) x[h][0] = x[h][1] = x[h][2] = x[h][3] = 0;
+                for (int h = 0; h < kHalves; ++h) x[h][0] = x[h][1] = x[h][2] = x[h][3] = 0;
+              } else if (pos >= seg.ctx && e >= kLargeScale) {
+                odd = ~0u;
+              }
             }
             // bit 7 of a byte where adding 1 changes it: 7 bits of ones, e4m3's NaN
             // (a carry into the next byte comes from such a byte only)
 #pragma unroll
             for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) nans |= (x[h][k] + 0x01010101u) ^ x[h][k];
+              for (int k = 0; k < 4; ++k) odd |= (x[h][k] + 0x01010101u) ^ x[h][k];
             // 2^120 * 2^(e - 127) as one bf16 factor, or as two
             const bool one = e <= 134;
             const uint32_t f1 = (one ? e + 120 : 247u) * 0x00800080u;
@@ -1096,10 +1104,6 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], f2);
               }
-              if (drafted) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) found |= drop_non_finite(o[k]);
-              }
               const uint32_t at = uint32_t(kRows * 128) * block + uint32_t(h) * (kTile * 128);
               asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out0 + at), "r"(o[0]),
                            "r"(o[1]), "r"(o[2]), "r"(o[3])
@@ -1109,10 +1113,10 @@ __global__ void __launch_bounds__(AttnShape<kD, kFp8>::kThreads, 1)
                            : "memory");
             }
           }
-          // e4m3's NaN came out as 480 times the scale: rare, so that this thread's
-          // places are looked through once more, in the cache
-          if (nans & 0x80808080u) found |= place_nans(is_v, p0, t / 4, kRows, t % 4, dst, clear);
-          if (found) ctl.bad_seg[seg_n % kBadRing] = seg_n;
+          // (e4m3's NaN came out as 480 times the scale, a large scale's values may
+          // be infinite; both are rare)
+          if ((odd & 0x80808080u) && mend_tile(is_v, p0, t / 4, kRows, t % 4, dst, clear))
+            ctl.bad_seg[seg_n % kBadRing] = seg_n;
           async_fence();
           warp_arrive(&ctl.full_bar[slot]);
         } else {
