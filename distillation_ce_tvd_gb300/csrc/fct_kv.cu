@@ -13,7 +13,7 @@ namespace fct {
 namespace {
 
 constexpr int kKvThreads = 256;
-constexpr int kBlocksPerSm = 8;  // of the write kernel's persistent grid
+constexpr int kBlocksPerSm = 8;  // of the write kernel's grid, at most
 
 __device__ __forceinline__ void set_status(int32_t* status, int32_t bit) {
   if (status) atomicOr(status, bit);
@@ -102,10 +102,12 @@ __device__ __forceinline__ Slot slot_of(int64_t slot, int page_size) {
 }
 
 // kTokens tokens per thread at a time; the next ones' loads are under way while
-// these are written, in a grid of kBlocksPerSm blocks per SM.  At 16389 tokens
-// of 8 heads of 128 in bf16: into a bf16 cache 25 us (134 MB, 5.5 TB/s), into
-// e4m3 31 us (101 MB, 3.3 TB/s); one block per token took 33 and 40 us, four
-// tokens at a time into e4m3 33.
+// these are written, in a grid of at most kBlocksPerSm blocks per SM (four of the
+// two-token kernels, with 56 registers, are resident at a time, so that a large
+// call runs in two waves).  At 16389 tokens of 8 heads of 128 in bf16: into a
+// bf16 cache 25 us (134 MB, 5.5 TB/s), into e4m3 31 us (101 MB, 3.3 TB/s); in
+// fp32 34 us into either (201 and 168 MB, 5.9 and 4.9 TB/s); one block per token
+// took 33 and 40 us from bf16, four tokens at a time into e4m3 33.
 template <typename T, bool kVecSrc, bool kE4m3, int kTokens>
 __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const __grid_constant__ KvWriteArgs a,
                                                               WriteShape w) {

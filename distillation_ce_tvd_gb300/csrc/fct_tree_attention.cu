@@ -229,12 +229,13 @@ cudaError_t launch_general(const AttnArgs& a, cudaStream_t st) {
 // partial sums in the workspace, which combine_kernel adds in order.
 //
 // What bounds it: with few rows the bytes of the keys (1 x 8 nodes, 32 query
-// and 8 kv heads of 128, 131071 keys in bf16: 537 MB in 98 us, 5.5 TB/s; 48
-// requests x 5 nodes, 870 MB: 161 us); with 256 rows per unit a call's fixed
-// cost of some 50 us and 1.7 us per tile (12 x 64 nodes, 64 query heads: 118
-// GFLOP in 157 us, 0.75 PFLOP/s); in e4m3 the conversion, the scale bytes and
-// the hand-over of tiles between the roles, 1.8 us per tile (20 x 27 nodes, 400
-// MB: 190 us, 2.1 TB/s; a copy without conversion took 171 of then 194).
+// and 8 kv heads of 128, 131071 keys in bf16: 537 MB in 99 us, 5.4 TB/s; 48
+// requests x 5 nodes, 870 MB: 155-168 us); with 256 rows per unit a call's fixed
+// cost of some 50 us and 2.4 us per tile (12 x 64 nodes, 64 query heads: 118
+// GFLOP, 177 with the remainders, in 181 us); in e4m3 the conversion, the scale
+// bytes and the hand-over of tiles between the roles, 2.2 us per tile (20 x 27
+// nodes, 400 MB: 218 us, 1.8 TB/s).  One bf16 per weight took 148, 203 and 161
+// us where two took 159, 207 and 187 (48 x 5, 20 x 27, 12 x 64).
 //
 // Per CTA: warp 1 issues the products, warps 4-7 and 8-11 are the softmax
 // groups.  bf16: warps 0 and 3 load K and V tiles by TMA (one box per page
@@ -342,8 +343,8 @@ __device__ __forceinline__ RequestShape request_shape(const AttnArgs& a, const A
 }
 
 // What the deal counts.  A unit costs start_cost for its start and end (as
-// measured: 9 us, or 8 bf16 key tiles of 128 rows, or 3 of the slower e4m3
-// ones) and each of its key tiles 1, or 2 with both query tiles; the sum over
+// measured with head_dim 128 and one bf16 per weight: 9 us, or 8 bf16 key tiles
+// of 128 rows, or 3 of the slower e4m3 ones; not measured for 64) and each of its key tiles 1, or 2 with both query tiles; the sum over
 // all units is dealt in equal runs.  48 requests of 450 to 8190 keys in bf16
 // took 190 us with a start cost of 3, 173 with 5, 167 with 7, 168 with 9; the
 // e4m3 trees 208 with 3, 211 with 5, 215 with 7.  Where no request has more

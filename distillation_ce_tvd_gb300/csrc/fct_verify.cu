@@ -12,7 +12,7 @@
 // walk does not reach are not read.
 //
 // The nodes follow one another, so what a request costs is mostly latency: at
-// 64 requests of 7 drafted tokens and V = 151936 bf16 (92 us, 197 MB expected)
+// 64 requests of 7 drafted tokens and V = 151936 bf16 (93 us, 197 MB expected)
 // a node takes 6 us on its four CTAs, 3 of them the sweep of the rows, 1.1 the
 // reduction over the cluster, the rest the decision and the next row's copies.
 // One request of 4 drafted tokens at V = 32000 fp32 takes 16 us, 24 trees of 32

@@ -701,8 +701,9 @@ typedef struct {
  * FCT_BF16: values rounded once, to nearest even.  FCT_E4M3: per token and
  * head, the exponent is the smallest e >= -126 with max |x| <= 448 * 2^e, and
  * the payload is x * 2^-e rounded to nearest even, so nothing saturates and
- * the scaling itself is exact.  A vector with a NaN or an infinity is stored
- * as byte 255 with payload 0: it reads back as NaN as a whole.
+ * the scaling itself is exact (a value within 2^-5 of the largest fp32 rounds
+ * to 2^128, which reads as an infinity).  A vector with a NaN or an infinity is
+ * stored as byte 255 with payload 0: it reads back as NaN as a whole.
  */
 int fct_kv_cache_write(const void* k, const void* v, int64_t ld_token,
                        int64_t ld_head, fct_dtype dtype, int64_t n_tokens,
@@ -752,7 +753,7 @@ int fct_kv_cache_move(const fct_kv_cache* cache, const int32_t* block_table,
  *                 results of requests whose keys are split over several CTAs.
  * Products take bf16 operands (e4m3 values are exact in bf16) with fp32 sums;
  * the softmax statistics are fp32.  A softmax weight enters the second product
- * as two bf16, 16 bits together (2^-17 of itself).  The order of all sums is
+ * as two bf16, 16 bits together (within 2^-16 of itself).  The order of all sums is
  * fixed by the arguments and the device: repeated calls give the same bits.
  */
 size_t fct_tree_attention_workspace_size(int64_t n_nodes, int32_t n_q_heads,
@@ -809,7 +810,8 @@ int fct_tree_attention(const void* q, int64_t ld_q_node, int64_t ld_q_head,
  *   count       : (batch,) int32: accepted tokens.
  * Arithmetic is fp32: a probability is 2^d / sum with d the distance from the
  * row's largest logit, so it is as good for a row with a constant added; some
- * 2^-19 of itself where it matters.  At a node without children to test the
+ * 2^-19 of itself where it matters.  Without draft logits Z is 1 less the
+ * rejected probabilities while an eighth or more is left.  At a node without children to test the
  * race is on log2 of r(v) / noise(v), within 2^-18 of itself.
  * V is at most 2^30, and batch at most 2^24 here, in fct_tree_attention and in
  * fct_kv_cache_move, else FCT_ERR_UNSUPPORTED.

@@ -3,7 +3,7 @@ scale of zero, values near the largest and values that are not finite.
 
 Tolerances.  Scores: exact products summed in fp32, in fewer than 32 roundings of at most
 sum |q||k| * scale, which is under 60 here, so 32 * 60 * 2^-24 = 1.2e-4 in a score and as much in its
-weight's relative error, twice for numerator and sum; weights to 16 bits (2^-17).  Under
+weight's relative error, twice for numerator and sum; weights to 16 bits (2^-16).  Under
 4e-4 * sum w|v| together.  The output is rounded to bf16 once: 2^-8 of itself.
 """
 import math
