@@ -20,6 +20,8 @@ FCT_F32, FCT_BF16, FCT_E4M3 = 0, 1, 2
 FCT_DEV_TARGET_OUT_OF_RANGE = 0x1
 FCT_DEV_INDEX_OUT_OF_RANGE = 0x4
 FCT_DEV_NO_DISTRIBUTION = 0x8
+FCT_DEV_BAD_LIST = 0x10
+FCT_TOP_MAX = 1024
 IGNORE_INDEX = -100
 
 _lock = threading.Lock()
@@ -39,6 +41,8 @@ EXPORTS = ("fused_ce_tvd_forward", "fused_ce_tvd_forward_ex", "fused_ce_tvd_back
            "fused_ce_tvd_vp_merge_tvd", "fused_ce_tvd_vp_backward",
            "fct_kv_cache_write", "fct_kv_cache_move", "fct_tree_attention",
            "fct_tree_attention_workspace_size", "fct_spec_verify",
+           "fct_top_logits", "fused_ce_tvd_top_forward", "fused_ce_tvd_top_backward",
+           "fused_ce_tvd_top_forward_backward",
            "fct_status_string", "fct_version")
 
 
@@ -61,6 +65,14 @@ class _KvCacheStruct(ctypes.Structure):
                 ("page_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64), ("scale_page_stride", ctypes.c_int64),
                 ("scale_slot_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64)]
+
+
+class _TopList(ctypes.Structure):
+    """fct_top_list: a teacher's top logits (see include/fused_ce_tvd.h)."""
+    _fields_ = [("values", ctypes.c_void_p), ("ld_values", ctypes.c_int64),
+                ("index", ctypes.c_void_p), ("ld_index", ctypes.c_int64),
+                ("rest_lse", ctypes.c_void_p), ("K", ctypes.c_int64),
+                ("reserved", ctypes.c_int64 * 2)]
 
 
 def options(ctas_per_row: int = 0, l2_keep: int = 0, stagger: float = 0.0,
@@ -173,6 +185,18 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                         i64, vp, i64, vp, vp, vp, vp, vp]
         for f in ("fct_kv_cache_write", "fct_kv_cache_move", "fct_tree_attention",
                   "fct_spec_verify"):
+            getattr(lib, f).restype = i32
+        tl = ctypes.POINTER(_TopList)
+        lib.fct_top_logits.argtypes = [vp, i64, i32, i64, i64, i64, vp, i64, vp, i64, vp, vp, vp]
+        lib.fused_ce_tvd_top_forward.argtypes = [vp, i64, i32, vp, tl, i64, i64, i64, vp, vp, vp,
+                                                 vp, vp, vp, vp, vp]
+        lib.fused_ce_tvd_top_backward.argtypes = [vp, i64, i32, vp, tl, i64, i64, i64, vp, vp, vp,
+                                                  vp, vp, vp, i64, vp, i64, vp, vp]
+        lib.fused_ce_tvd_top_forward_backward.argtypes = [vp, i64, i32, vp, tl, i64, i64, i64, vp,
+                                                          vp, i64, vp, vp, vp, vp, vp, vp, vp, i64,
+                                                          vp, vp]
+        for f in ("fct_top_logits", "fused_ce_tvd_top_forward", "fused_ce_tvd_top_backward",
+                  "fused_ce_tvd_top_forward_backward"):
             getattr(lib, f).restype = i32
         lib.fct_status_string.argtypes = [i32]
         lib.fct_status_string.restype = ctypes.c_char_p
@@ -1268,3 +1292,187 @@ def fct_spec_verify(target_logits, tokens, parent, node_start, uniform, noise, d
         _status_ptr(dev_status, index), _raw_stream(index))
     _check(rc, "fct_spec_verify")
     return out_tokens, path, count
+
+
+# ------------------------------------------------------------------ a teacher's top logits
+
+def _placed(f):
+    """A call that runs on its first tensor's device, with ``stream=`` as the current stream while it
+    does (see on_stream, on_device)."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        first = args[0] if args else next((x for x in kw.values() if torch.is_tensor(x)), None)
+        if not torch.is_tensor(first) or not first.is_cuda:
+            raise ValueError(f"{f.__name__}: the tensors must be CUDA tensors")
+        index = first.get_device()
+        if stream is not None:
+            return on_stream(f, stream, index, *args, **kw)
+        if torch.cuda.current_device() != index:
+            return on_device(f, index, *args, **kw)
+        return f(*args, **kw)
+    return call
+
+
+def _logits2(x, name, index=None):
+    """(address, row stride, dtype code) of a (BT, V) float32 or bfloat16 tensor."""
+    code = FCT_BF16 if x.dtype is torch.bfloat16 else FCT_F32
+    if code == FCT_F32 and x.dtype is not torch.float32:
+        raise TypeError(f"{name}: dtype {x.dtype} is not float32 or bfloat16")
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1) or \
+            (index is not None and x.get_device() != index):
+        raise ValueError(f"{name} must be (BT, V) with unit stride along V, on the call's device")
+    rows, cols = x.shape
+    return x.data_ptr(), x.stride(0) if rows > 1 else cols, code
+
+
+def _rows_out(x, n, index, device, name):
+    if x is None:
+        return torch.empty(n, device=device, dtype=torch.float32)
+    if x.dtype is not torch.float32 or x.shape != (n,) or not x.is_contiguous() \
+            or x.get_device() != index:
+        raise ValueError(f"{name} must be a contiguous float32 vector of {n} values on the call's "
+                         "device")
+    return x
+
+
+def _top_list(values, index_of_words, rest_lse, BT, index):
+    """The fct_top_list of a teacher's (BT, K) logits and int32 indices, and rest_lse (BT,) or None."""
+    v, ld_v, K = _table(values, torch.float32, BT, index, "top_values")
+    i, ld_i, cols = _table(index_of_words, torch.int32, BT, index, "top_index")
+    if cols != K:
+        raise ValueError("top_values and top_index must have the same shape")
+    rest = None if rest_lse is None else _vec(rest_lse, torch.float32, BT, index, "rest_lse")
+    return ctypes.byref(_TopList(v, ld_v, i, ld_i, rest, K))
+
+
+def _upstream2(g, BT, device, index, name):
+    """(tensor, stride): a float32 vector of BT values, or one value for all rows."""
+    if not torch.is_tensor(g):
+        return torch.full((1,), float(g), device=device, dtype=torch.float32), 0
+    if g.numel() == 1:
+        return g.reshape(1).to(device=device, dtype=torch.float32), 0
+    _vec(g, torch.float32, BT, index, name)
+    return g, 1
+
+
+def _upstream_pair(grad_ce, grad_tvd, BT, device, index):
+    gce, a = _upstream2(grad_ce, BT, device, index, "grad_ce")
+    gtvd, b = _upstream2(grad_tvd, BT, device, index, "grad_tvd")
+    if a != b:
+        gce, gtvd = gce.expand(BT).contiguous(), gtvd.expand(BT).contiguous()
+    return gce, gtvd, max(a, b)
+
+
+def _gradient_out(student, grad_student, inplace, index):
+    if inplace:
+        if grad_student is not None and grad_student is not student:
+            raise ValueError("inplace=True and grad_student= exclude each other")
+        grad_student = student
+    elif grad_student is None:
+        grad_student = torch.empty(student.shape, device=student.device, dtype=student.dtype)
+    ptr, ld, _ = _logits2(grad_student, "grad_student", index)
+    if grad_student.dtype is not student.dtype or grad_student.shape != student.shape:
+        raise ValueError("grad_student must match the student's shape and dtype")
+    return grad_student, ptr, ld
+
+
+_TOP_STATS = ("ce", "tvd", "student_lse", "student_rest", "teacher_lse", "sigma")
+
+
+@_placed
+def fct_top_logits(logits, k, *, values=None, index=None, rest_lse=None, dev_status=None):
+    """The k largest logits of each row: (values float32 (BT, k), index int32 (BT, k), rest_lse (BT,)).
+
+    In falling order, equal ones by rising index; ``rest_lse`` is the log-sum-exp of the row's other
+    logits.  Logits of -inf are not listed: a row with fewer than k others has index -1 and value
+    -inf in the places left.  ``logits`` (BT, V) float32 or bfloat16; k up to FCT_TOP_MAX.
+    """
+    x, ld, code = _logits2(logits, "logits")
+    BT, V = logits.shape
+    K, at, dev = int(k), logits.get_device(), logits.device
+    if values is None:
+        values = torch.empty((BT, max(K, 0)), device=dev, dtype=torch.float32)
+    if index is None:
+        index = torch.empty((BT, max(K, 0)), device=dev, dtype=torch.int32)
+    rest_lse = _rows_out(rest_lse, BT, at, dev, "rest_lse")
+    v, ld_v, cols_v = _table(values, torch.float32, BT, at, "values")
+    i, ld_i, cols_i = _table(index, torch.int32, BT, at, "index")
+    if cols_v != K or cols_i != K:
+        raise ValueError(f"values and index must be (BT, {K})")
+    rc = _library().fct_top_logits(x, ld, code, BT, V, K, v, ld_v, i, ld_i,
+                                   rest_lse.data_ptr(), _status_ptr(dev_status, at),
+                                   _raw_stream(at))
+    _check(rc, "fct_top_logits")
+    return values, index, rest_lse
+
+
+@_placed
+def fused_ce_tvd_top_forward(student, target, top_values, top_index, rest_lse=None,
+                             ignore_index=IGNORE_INDEX, *, ce=None, tvd=None, student_lse=None,
+                             student_rest=None, teacher_lse=None, sigma=None, dev_status=None):
+    """The loss against a teacher's top logits: per-row (ce, tvd, student_lse, student_rest,
+    teacher_lse, sigma), float32 (BT,).
+
+    ``top_values`` float32 and ``top_index`` int32 (BT, K): the teacher's logits and their words (-1:
+    not used), in any order; ``rest_lse`` (BT,): the log-sum-exp of its other logits, or None for a
+    teacher that has none.  The backward takes the last four outputs.
+    """
+    x, ld, code = _logits2(student, "student")
+    BT, V = student.shape
+    at, dev = student.get_device(), student.device
+    given = (ce, tvd, student_lse, student_rest, teacher_lse, sigma)
+    outs = tuple(_rows_out(o, BT, at, dev, n) for o, n in zip(given, _TOP_STATS))
+    rc = _library().fused_ce_tvd_top_forward(
+        x, ld, code, _vec(target, torch.int64, BT, at, "target"),
+        _top_list(top_values, top_index, rest_lse, BT, at), BT, V, int(ignore_index),
+        *(o.data_ptr() for o in outs), _status_ptr(dev_status, at), _raw_stream(at))
+    _check(rc, "fused_ce_tvd_top_forward")
+    return outs
+
+
+@_placed
+def fused_ce_tvd_top_backward(student, target, top_values, top_index, rest_lse, student_lse,
+                              student_rest, teacher_lse, sigma, grad_ce, grad_tvd,
+                              ignore_index=IGNORE_INDEX, *, grad_student=None, inplace=False,
+                              dev_status=None):
+    """Gradient of sum_r grad_ce[r]*ce[r] + grad_tvd[r]*tvd[r] w.r.t. the student, from the forward's
+    statistics.  ``inplace=True`` writes it over ``student`` and returns ``student``."""
+    x, ld, code = _logits2(student, "student")
+    BT, V = student.shape
+    at, dev = student.get_device(), student.device
+    gce, gtvd, stride = _upstream_pair(grad_ce, grad_tvd, BT, dev, at)
+    grad, g, ld_g = _gradient_out(student, grad_student, inplace, at)
+    saved = (student_lse, student_rest, teacher_lse, sigma)
+    rc = _library().fused_ce_tvd_top_backward(
+        x, ld, code, _vec(target, torch.int64, BT, at, "target"),
+        _top_list(top_values, top_index, rest_lse, BT, at), BT, V, int(ignore_index),
+        *(_vec(o, torch.float32, BT, at, n) for o, n in zip(saved, _TOP_STATS[2:])),
+        gce.data_ptr(), gtvd.data_ptr(), stride, g, ld_g, _status_ptr(dev_status, at),
+        _raw_stream(at))
+    _check(rc, "fused_ce_tvd_top_backward")
+    return grad
+
+
+@_placed
+def fused_ce_tvd_top_forward_backward(student, target, top_values, top_index, rest_lse, grad_ce,
+                                      grad_tvd, ignore_index=IGNORE_INDEX, *, ce=None, tvd=None,
+                                      student_lse=None, student_rest=None, teacher_lse=None,
+                                      sigma=None, grad_student=None, inplace=False,
+                                      dev_status=None):
+    """Forward and backward against a teacher's top logits in one launch, given the upstream
+    gradients: (ce, tvd, student_lse, student_rest, teacher_lse, sigma, grad_student), equal to
+    fused_ce_tvd_top_forward followed by fused_ce_tvd_top_backward."""
+    x, ld, code = _logits2(student, "student")
+    BT, V = student.shape
+    at, dev = student.get_device(), student.device
+    gce, gtvd, stride = _upstream_pair(grad_ce, grad_tvd, BT, dev, at)
+    given = (ce, tvd, student_lse, student_rest, teacher_lse, sigma)
+    outs = tuple(_rows_out(o, BT, at, dev, n) for o, n in zip(given, _TOP_STATS))
+    grad, g, ld_g = _gradient_out(student, grad_student, inplace, at)
+    rc = _library().fused_ce_tvd_top_forward_backward(
+        x, ld, code, _vec(target, torch.int64, BT, at, "target"),
+        _top_list(top_values, top_index, rest_lse, BT, at), BT, V, int(ignore_index),
+        gce.data_ptr(), gtvd.data_ptr(), stride, *(o.data_ptr() for o in outs), g, ld_g,
+        _status_ptr(dev_status, at), _raw_stream(at))
+    _check(rc, "fused_ce_tvd_top_forward_backward")
+    return (*outs, grad)

@@ -614,7 +614,7 @@ int vp_merge_impl(const float* parts, int64_t n_shards, const int64_t* target, i
 
 namespace fct {
 
-int current_device_sms(int* sms, int* device) {
+int current_device_sms(int* sms, int* device, int* l2_bytes) {
   DeviceInfo d;
   const int rc = current_device(&d);
   if (rc != FCT_OK) return rc;
@@ -623,6 +623,7 @@ int current_device_sms(int* sms, int* device) {
     return FCT_ERR_CUDA;
   }
   *sms = d.sms;
+  if (l2_bytes != nullptr) *l2_bytes = d.l2_bytes;
   return FCT_OK;
 }
 

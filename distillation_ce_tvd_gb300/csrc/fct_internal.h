@@ -196,8 +196,8 @@ cudaError_t launch_gemm(const GemmOperand& A, const GemmOperand& B, void* C, int
 size_t gemm_split_workspace_bytes(int64_t M, int64_t N);
 
 // The calling thread's current device, if it is one the kernels are built
-// for: its SM count and index.  Returns an fct_status.
-int current_device_sms(int* sms, int* device);
+// for: its SM count, index and (if asked for) L2 size.  Returns an fct_status.
+int current_device_sms(int* sms, int* device, int* l2_bytes = nullptr);
 
 // Speculative decoding step (fct_kv.cu, fct_tree_attention.cu, fct_verify.cu;
 // entry points in fct_spec_api.cu).
@@ -273,6 +273,55 @@ struct VerifyArgs {
   int32_t* dev_status;
 };
 cudaError_t launch_verify(const VerifyArgs& a, int sms, int device, cudaStream_t st);
+
+// Distillation from a teacher's top logits (fct_top_select.cu, fct_top_loss.cu,
+// fct_top_linear.cu; entry points in fct_top_api.cu).
+constexpr int kTopMax = FCT_TOP_MAX;              // longest list
+constexpr int64_t kTopMaxV = int64_t(1) << 23;    // largest vocabulary of the loss
+constexpr int kTopSmemMax = 200 * 1024;           // dynamic shared memory of its kernels
+
+struct TopSelectArgs {
+  const void* logits;
+  int64_t ld;
+  int dtype;
+  int64_t BT, V, K;
+  float* values;
+  int64_t ld_v;
+  int32_t* index;
+  int64_t ld_i;
+  float* rest;
+  int32_t* dev_status;
+};
+cudaError_t launch_top_select(const TopSelectArgs& a, int sms, int device, cudaStream_t st);
+
+struct TopArgs {
+  const void* student;
+  int64_t ld_s;
+  int dtype;
+  const int64_t* target;
+  const float* values;  // (BT, K) teacher logits
+  int64_t ld_v;
+  const int32_t* index;  // (BT, K)
+  int64_t ld_i;
+  const float* rest;  // (BT,), or nullptr: nothing outside the list
+  int64_t BT, V, K, ignore_index;
+  // written by the forward, read by the backward
+  float* ce;
+  float* tvd;
+  float* lse;
+  float* rest_lse;
+  float* t_lse;
+  float* sigma;
+  int32_t* dev_status;
+  // backward, and the single launch (nullptr grad: forward alone)
+  const float* grad_ce = nullptr;
+  const float* grad_tvd = nullptr;
+  int64_t grad_stride = 0;
+  void* grad = nullptr;
+  int64_t ld_g = 0;
+};
+cudaError_t launch_top_forward(const TopArgs& a, int sms, int device, int l2, cudaStream_t st);
+cudaError_t launch_top_backward(const TopArgs& a, cudaStream_t st);
 
 cudaError_t launch_forward(const FwdArgs& a, const FwdPlan& plan, cudaStream_t st);
 cudaError_t launch_mean(const LossArgs& a, cudaStream_t st);

@@ -72,6 +72,7 @@ typedef enum {
 #define FCT_DEV_WAIT_TIMEOUT 0x2 /* a bounded wait in a kernel gave up; outputs invalid */
 #define FCT_DEV_INDEX_OUT_OF_RANGE 0x4 /* a slot, page, path or length is outside its array */
 #define FCT_DEV_NO_DISTRIBUTION 0x8    /* a row of logits that is visited has no softmax */
+#define FCT_DEV_BAD_LIST 0x10          /* a top-logits list names no word, or one word twice */
 
 /*
  * Launch options of the multi-pass forward kernels (a tuning and measurement
@@ -629,6 +630,128 @@ int fused_ce_tvd_vp_backward(const void* student, int64_t ld_student,
                              int64_t grad_stride, void* grad_student,
                              int64_t ld_grad, int32_t* dev_status,
                              void* stream);
+
+/*
+ * Distillation from a teacher's top logits.  The loss above reads the
+ * teacher's whole row.  Where the teacher ran beforehand, or elsewhere, a row
+ * of it is kept as its K largest logits, their indices, and the log-sum-exp
+ * of all its other logits: 8 K + 4 bytes instead of V elements (no
+ * counterpart in the PR #1384 analysis).  fct_top_logits makes such lists;
+ * the fused_ce_tvd_top_* calls are the loss against them.
+ *
+ * With U the words that a row's list names, t_v their logits, and p =
+ * softmax(student) summed to p_rest outside U:
+ *
+ *   q      = softmax over (t_v for v in U, rest_lse); its last entry is q_rest
+ *   ce     = lse(student) - student[target]
+ *   tvd    = 0.5 * (sum_{v in U} |p_v - q_v| + |p_rest - q_rest|)
+ *   sign_v = sign(p_v - q_v) in U, sign(p_rest - q_rest) outside (sign(0) = 0)
+ *   sigma  = sum_{v in U} p_v*sign_v + p_rest*sign(p_rest - q_rest)
+ *   d(grad_ce*ce + grad_tvd*tvd)/ds_v
+ *          = grad_ce*(p_v - 1[v==target]) + grad_tvd*0.5*p_v*(sign_v - sigma)
+ *
+ * tvd is the total variation distance of the two distributions with the words
+ * outside U taken together: at most that of the whole rows, and equal to it
+ * where U holds all words, or where the teacher gives none outside U any
+ * probability (rest_lse NULL).
+ */
+
+/*
+ * The K largest logits of each row: values[r][0..K) in falling order (equal
+ * ones by rising index; -0 equals +0), their indices, and rest_lse[r], the
+ * natural log-sum-exp of the row's other logits (-inf if there are none, or
+ * none above -inf).
+ *
+ *   logits  : (BT, V), element type `dtype`, row stride ld >= V, aligned to
+ *             the element.
+ *   K       : 1 to FCT_TOP_MAX; V at most 2^31 - 2^16.  Else
+ *             FCT_ERR_UNSUPPORTED (K <= 0: FCT_ERR_INVALID_ARG).
+ *   values  : (BT, K) fp32, row stride ld_values >= K.
+ *   index   : (BT, K) int32, row stride ld_index >= K.
+ *   rest_lse: (BT,) fp32.
+ * Logits of -inf are never listed: a row with fewer than K others has index
+ * -1 and value -inf in the places left (so has a row with V < K).  A row with
+ * a NaN or +inf has no softmax: its list holds its largest numbers, its
+ * rest_lse is NaN, and FCT_DEV_NO_DISTRIBUTION is set; so it is, with
+ * rest_lse -inf, for a row of -inf alone.  Outputs must not overlap the
+ * logits or each other.  Repeated calls give the same bits.
+ */
+#define FCT_TOP_MAX 1024
+
+int fct_top_logits(const void* logits, int64_t ld, fct_dtype dtype, int64_t BT,
+                   int64_t V, int64_t K, float* values, int64_t ld_values,
+                   int32_t* index, int64_t ld_index, float* rest_lse,
+                   int32_t* dev_status, void* stream);
+
+/*
+ * A teacher's lists (device pointers), as fct_top_logits writes them or from
+ * elsewhere: any order of the entries, any number of them unused.
+ *
+ *   index    : (BT, K) int32, row stride ld_index >= K.  -1: the place is not
+ *              used, whatever its value.  A row with an index below -1 or at
+ *              or above V, or with one index twice, sets FCT_DEV_BAD_LIST,
+ *              and all its outputs are NaN.
+ *   values   : (BT, K) fp32, row stride ld_values >= K: the teacher's logits.
+ *   rest_lse : (BT,) fp32, the log-sum-exp of the teacher's other logits, or
+ *              NULL: it has no others (the list is renormalised).
+ *   K        : 1 to FCT_TOP_MAX.
+ *   reserved : must be 0.
+ * A row whose list holds no probability (no used place above -inf, and no
+ * rest) has no teacher: tvd and sigma are 0, teacher_lse is -inf, and its
+ * gradient is cross-entropy's.
+ */
+typedef struct {
+  const float* values;
+  int64_t ld_values;
+  const int32_t* index;
+  int64_t ld_index;
+  const float* rest_lse;
+  int64_t K;
+  int64_t reserved[2];
+} fct_top_list;
+
+/*
+ * The loss of (BT, V) student logits against top lists: forward, backward,
+ * and both in one launch where the upstream gradients are known before.
+ *
+ *   student, target, ignore_index, grad_ce, grad_tvd, grad_stride,
+ *   grad_student : as for fused_ce_tvd_forward, _backward and
+ *                  _forward_backward (the gradient may be in place).  Rows
+ *                  need no alignment beyond the element's.
+ *   ce, tvd, student_lse, student_rest, teacher_lse, sigma : (BT,) fp32,
+ *                  written by the forward; student_rest is the log-sum-exp of
+ *                  the student's logits outside U (-inf if U holds all
+ *                  words).  The backward reads the last four.  Rows with
+ *                  target == ignore_index: zeros, and the list is not read.
+ *   V            : at most 2^23, else FCT_ERR_UNSUPPORTED.
+ * The forward reads the row once, the backward reads and writes it once, the
+ * single launch reads and writes it once in memory (its second pass reads
+ * from L2) and gives the bits of the two calls.  All decide sign(p - q) from
+ * p = exp(s - student_lse) and q = exp(t - teacher_lse) in fp32.
+ */
+int fused_ce_tvd_top_forward(const void* student, int64_t ld_student,
+                             fct_dtype dtype, const int64_t* target,
+                             const fct_top_list* teacher, int64_t BT,
+                             int64_t V, int64_t ignore_index, float* ce,
+                             float* tvd, float* student_lse,
+                             float* student_rest, float* teacher_lse,
+                             float* sigma, int32_t* dev_status, void* stream);
+
+int fused_ce_tvd_top_backward(
+    const void* student, int64_t ld_student, fct_dtype dtype,
+    const int64_t* target, const fct_top_list* teacher, int64_t BT, int64_t V,
+    int64_t ignore_index, const float* student_lse, const float* student_rest,
+    const float* teacher_lse, const float* sigma, const float* grad_ce,
+    const float* grad_tvd, int64_t grad_stride, void* grad_student,
+    int64_t ld_grad, int32_t* dev_status, void* stream);
+
+int fused_ce_tvd_top_forward_backward(
+    const void* student, int64_t ld_student, fct_dtype dtype,
+    const int64_t* target, const fct_top_list* teacher, int64_t BT, int64_t V,
+    int64_t ignore_index, const float* grad_ce, const float* grad_tvd,
+    int64_t grad_stride, float* ce, float* tvd, float* student_lse,
+    float* student_rest, float* teacher_lse, float* sigma, void* grad_student,
+    int64_t ld_grad, int32_t* dev_status, void* stream);
 
 /*
  * One step of speculative decoding with a distilled draft model.  The loss
