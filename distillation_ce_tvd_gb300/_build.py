@@ -22,8 +22,8 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["fct_api.cu", "fct_forward.cu", "fct_backward.cu", "fct_loss.cu", "fct_linear.cu",
            "fct_noalloc.cu", "fct_host.cu", "fct_vocab.cu", "fct_gemm.cu", "fct_spec_api.cu",
            "fct_kv.cu", "fct_tree_attention.cu", "fct_verify.cu", "fct_top_api.cu",
-           "fct_top_select.cu", "fct_top_loss.cu"]
-HEADERS = ["fct_common.cuh", "fct_internal.h", "fct_top.cuh"]
+           "fct_top_select.cu", "fct_top_loss.cu", "fct_top_linear.cu"]
+HEADERS = ["fct_common.cuh", "fct_internal.h", "fct_top.cuh", "fct_pair.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -43,6 +43,10 @@ EXPORTS = ("fused_ce_tvd_forward", "fused_ce_tvd_forward_ex", "fused_ce_tvd_back
            "fct_tree_attention_workspace_size", "fct_spec_verify",
            "fct_top_logits", "fused_ce_tvd_top_forward", "fused_ce_tvd_top_backward",
            "fused_ce_tvd_top_forward_backward",
+           "fused_linear_ce_tvd_top_forward_workspace_size",
+           "fused_linear_ce_tvd_top_backward_workspace_size", "fused_linear_ce_tvd_top_forward",
+           "fused_linear_ce_tvd_top_backward", "fused_linear_ce_forward",
+           "fused_linear_ce_backward",
            "fct_status_string", "fct_version")
 
 
@@ -195,8 +199,23 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.fused_ce_tvd_top_forward_backward.argtypes = [vp, i64, i32, vp, tl, i64, i64, i64, vp,
                                                           vp, i64, vp, vp, vp, vp, vp, vp, vp, i64,
                                                           vp, vp]
+        lib.fused_linear_ce_tvd_top_forward_workspace_size.argtypes = [i64, i64, i64]
+        lib.fused_linear_ce_tvd_top_forward_workspace_size.restype = sz
+        lib.fused_linear_ce_tvd_top_backward_workspace_size.argtypes = [i64, i64, i64, i64, i64]
+        lib.fused_linear_ce_tvd_top_backward_workspace_size.restype = sz
+        lib.fused_linear_ce_tvd_top_forward.argtypes = [vp, i64, vp, i64, i64, vp, tl, i64, i64,
+                                                        i64, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]
+        lib.fused_linear_ce_tvd_top_backward.argtypes = [vp, i64, vp, i64, i64, vp, tl, i64, i64,
+                                                         i64, vp, vp, vp, vp, vp, vp, i64, vp, i64,
+                                                         vp, i64, i32, vp, sz, i64, vp, vp]
+        lib.fused_linear_ce_forward.argtypes = [vp, i64, vp, i64, i64, vp, i64, i64, i64, vp, vp,
+                                                vp, sz, vp, vp]
+        lib.fused_linear_ce_backward.argtypes = [vp, i64, vp, i64, i64, vp, i64, i64, i64, vp, vp,
+                                                 i64, vp, i64, vp, i64, i32, vp, sz, i64, vp, vp]
         for f in ("fct_top_logits", "fused_ce_tvd_top_forward", "fused_ce_tvd_top_backward",
-                  "fused_ce_tvd_top_forward_backward"):
+                  "fused_ce_tvd_top_forward_backward", "fused_linear_ce_tvd_top_forward",
+                  "fused_linear_ce_tvd_top_backward", "fused_linear_ce_forward",
+                  "fused_linear_ce_backward"):
             getattr(lib, f).restype = i32
         lib.fct_status_string.argtypes = [i32]
         lib.fct_status_string.restype = ctypes.c_char_p
@@ -1476,3 +1495,159 @@ def fused_ce_tvd_top_forward_backward(student, target, top_values, top_index, re
         _status_ptr(dev_status, at), _raw_stream(at))
     _check(rc, "fused_ce_tvd_top_forward_backward")
     return (*outs, grad)
+
+
+def _hidden(h, w):
+    """(h, ld_h, w, ld_w, BT, V, d, device index) of bfloat16 hidden states and weights."""
+    index = h.get_device()
+    if h.dim() != 2 or w.dim() != 2 or h.shape[1] != w.shape[1]:
+        raise ValueError("h must be (BT, d) and w (V, d)")
+    (BT, d), V = h.shape, w.shape[0]
+    hp, ld_h, _ = _table(h, torch.bfloat16, BT, index, "h")
+    wp, ld_w, _ = _table(w, torch.bfloat16, V, index, "w")
+    # one row: any stride that the tile loads take
+    return hp, ld_h if BT > 1 else -(-d // 8) * 8, wp, ld_w if V > 1 else -(-d // 8) * 8, BT, V, d, index
+
+
+def _space(workspace, need, device, index):
+    if workspace is None:
+        return torch.empty(need, device=device, dtype=torch.uint8)
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+    return workspace
+
+
+_GRAD_W_KINDS = {torch.bfloat16: 1, torch.float32: 0}
+
+
+def _linear_gradients(h, w, grad_h, grad_w, want_grad_h, want_grad_w, grad_w_dtype, accumulate, BT,
+                      V, d, index):
+    """(grad_h, its address and stride, grad_w, its address, stride and kind)."""
+    if want_grad_h and grad_h is None:
+        grad_h = torch.empty((BT, d), device=h.device, dtype=torch.bfloat16)
+    if want_grad_w and grad_w is None:
+        if accumulate:
+            raise ValueError("accumulate=True needs grad_w")
+        if grad_w_dtype not in _GRAD_W_KINDS:
+            raise ValueError("grad_w_dtype must be torch.bfloat16 or torch.float32")
+        grad_w = torch.empty((V, d), device=h.device, dtype=grad_w_dtype)
+    hp, ld_h, wp, ld_w, kind = None, 0, None, 0, 0
+    if grad_h is not None:
+        hp, ld_h, cols = _table(grad_h, torch.bfloat16, BT, index, "grad_h")
+        if cols != d:
+            raise ValueError("grad_h must match h's shape")
+    if grad_w is not None:
+        if grad_w.dtype not in _GRAD_W_KINDS or (accumulate and grad_w.dtype is not torch.float32):
+            raise ValueError("grad_w must be bfloat16 or float32, float32 to accumulate")
+        wp, ld_w, cols = _table(grad_w, grad_w.dtype, V, index, "grad_w")
+        if cols != d:
+            raise ValueError("grad_w must match w's shape")
+        kind = 2 if accumulate else _GRAD_W_KINDS[grad_w.dtype]
+    return grad_h, (hp, ld_h), grad_w, (wp, ld_w, kind)
+
+
+def fused_linear_ce_tvd_top_forward_workspace_size(BT: int, V: int, K: int = 0) -> int:
+    """Bytes of device workspace of the linear forward calls (K 0: cross-entropy alone)."""
+    return int(_library().fused_linear_ce_tvd_top_forward_workspace_size(int(BT), int(V), int(K)))
+
+
+def fused_linear_ce_tvd_top_backward_workspace_size(BT: int, V: int, d: int, K: int = 0,
+                                                    piece_cols: int = 0) -> int:
+    """Bytes of device workspace of the linear backward calls (K 0: cross-entropy alone)."""
+    return int(_library().fused_linear_ce_tvd_top_backward_workspace_size(
+        int(BT), int(V), int(d), int(K), int(piece_cols)))
+
+
+@_placed
+def fused_linear_ce_tvd_top_forward(h, w, target, top_values, top_index, rest_lse=None,
+                                    ignore_index=IGNORE_INDEX, *, ce=None, tvd=None,
+                                    student_lse=None, student_rest=None, teacher_lse=None,
+                                    sigma=None, workspace=None, dev_status=None):
+    """The loss of logits h @ w.T against a teacher's top logits, without the logits: per-row (ce,
+    tvd, student_lse, student_rest, teacher_lse, sigma), as fused_ce_tvd_top_forward.
+
+    ``h`` (BT, d) and ``w`` (V, d) bfloat16 with 16-byte rows.  ``workspace``: a uint8 tensor of
+    fused_linear_ce_tvd_top_forward_workspace_size bytes to keep between calls (allocated if None).
+    """
+    hp, ld_h, wp, ld_w, BT, V, d, at = _hidden(h, w)
+    dev = h.device
+    lists = _top_list(top_values, top_index, rest_lse, BT, at)
+    given = (ce, tvd, student_lse, student_rest, teacher_lse, sigma)
+    outs = tuple(_rows_out(o, BT, at, dev, n) for o, n in zip(given, _TOP_STATS))
+    space = _space(workspace, fused_linear_ce_tvd_top_forward_workspace_size(
+        BT, V, top_index.shape[1]), dev, at)
+    rc = _library().fused_linear_ce_tvd_top_forward(
+        hp, ld_h, wp, ld_w, d, _vec(target, torch.int64, BT, at, "target"), lists, BT, V,
+        int(ignore_index), *(o.data_ptr() for o in outs), space.data_ptr(),
+        space.numel() * space.element_size(), _status_ptr(dev_status, at), _raw_stream(at))
+    _check(rc, "fused_linear_ce_tvd_top_forward")
+    return outs
+
+
+@_placed
+def fused_linear_ce_tvd_top_backward(h, w, target, top_values, top_index, rest_lse, student_lse,
+                                     student_rest, teacher_lse, sigma, grad_ce, grad_tvd,
+                                     ignore_index=IGNORE_INDEX, *, grad_h=None, grad_w=None,
+                                     want_grad_h=True, want_grad_w=True,
+                                     grad_w_dtype=torch.bfloat16, accumulate=False, piece_cols=0,
+                                     workspace=None, dev_status=None):
+    """(grad_h, grad_w) of sum_r grad_ce[r]*ce[r] + grad_tvd[r]*tvd[r] from the forward's statistics.
+
+    ``grad_h`` bfloat16; ``grad_w`` bfloat16 or float32 (``grad_w_dtype`` where it is allocated
+    here), and with ``accumulate`` added to the float32 tensor given.  The vocabulary goes in pieces
+    of ``piece_cols`` words (0: 2**28 / BT), which the workspace grows with
+    (fused_linear_ce_tvd_top_backward_workspace_size).
+    """
+    hp, ld_h, wp, ld_w, BT, V, d, at = _hidden(h, w)
+    dev = h.device
+    lists = _top_list(top_values, top_index, rest_lse, BT, at)
+    gce, gtvd, stride = _upstream_pair(grad_ce, grad_tvd, BT, dev, at)
+    grad_h, gh, grad_w, gw = _linear_gradients(h, w, grad_h, grad_w, want_grad_h, want_grad_w,
+                                               grad_w_dtype, accumulate, BT, V, d, at)
+    space = _space(workspace, fused_linear_ce_tvd_top_backward_workspace_size(
+        BT, V, d, top_index.shape[1], piece_cols), dev, at)
+    saved = (student_lse, student_rest, teacher_lse, sigma)
+    rc = _library().fused_linear_ce_tvd_top_backward(
+        hp, ld_h, wp, ld_w, d, _vec(target, torch.int64, BT, at, "target"), lists, BT, V,
+        int(ignore_index), *(_vec(o, torch.float32, BT, at, n) for o, n in zip(saved, _TOP_STATS[2:])),
+        gce.data_ptr(), gtvd.data_ptr(), stride, *gh, *gw, space.data_ptr(),
+        space.numel() * space.element_size(), int(piece_cols), _status_ptr(dev_status, at),
+        _raw_stream(at))
+    _check(rc, "fused_linear_ce_tvd_top_backward")
+    return grad_h, grad_w
+
+
+@_placed
+def fused_linear_ce_forward(h, w, target, ignore_index=IGNORE_INDEX, *, ce=None, lse=None,
+                            workspace=None, dev_status=None):
+    """Cross-entropy of logits h @ w.T, without the logits: per-row (ce, lse), float32 (BT,)."""
+    hp, ld_h, wp, ld_w, BT, V, d, at = _hidden(h, w)
+    outs = tuple(_rows_out(o, BT, at, h.device, n) for o, n in ((ce, "ce"), (lse, "lse")))
+    space = _space(workspace, fused_linear_ce_tvd_top_forward_workspace_size(BT, V), h.device, at)
+    rc = _library().fused_linear_ce_forward(
+        hp, ld_h, wp, ld_w, d, _vec(target, torch.int64, BT, at, "target"), BT, V,
+        int(ignore_index), *(o.data_ptr() for o in outs), space.data_ptr(),
+        space.numel() * space.element_size(), _status_ptr(dev_status, at), _raw_stream(at))
+    _check(rc, "fused_linear_ce_forward")
+    return outs
+
+
+@_placed
+def fused_linear_ce_backward(h, w, target, lse, grad_ce, ignore_index=IGNORE_INDEX, *, grad_h=None,
+                             grad_w=None, want_grad_h=True, want_grad_w=True,
+                             grad_w_dtype=torch.bfloat16, accumulate=False, piece_cols=0,
+                             workspace=None, dev_status=None):
+    """(grad_h, grad_w) of sum_r grad_ce[r]*ce[r], as fused_linear_ce_tvd_top_backward."""
+    hp, ld_h, wp, ld_w, BT, V, d, at = _hidden(h, w)
+    gce, stride = _upstream2(grad_ce, BT, h.device, at, "grad_ce")
+    grad_h, gh, grad_w, gw = _linear_gradients(h, w, grad_h, grad_w, want_grad_h, want_grad_w,
+                                               grad_w_dtype, accumulate, BT, V, d, at)
+    space = _space(workspace, fused_linear_ce_tvd_top_backward_workspace_size(
+        BT, V, d, 0, piece_cols), h.device, at)
+    rc = _library().fused_linear_ce_backward(
+        hp, ld_h, wp, ld_w, d, _vec(target, torch.int64, BT, at, "target"), BT, V,
+        int(ignore_index), _vec(lse, torch.float32, BT, at, "lse"), gce.data_ptr(), stride, *gh, *gw,
+        space.data_ptr(), space.numel() * space.element_size(), int(piece_cols),
+        _status_ptr(dev_status, at), _raw_stream(at))
+    _check(rc, "fused_linear_ce_backward")
+    return grad_h, grad_w

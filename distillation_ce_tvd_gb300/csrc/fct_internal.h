@@ -323,6 +323,46 @@ struct TopArgs {
 cudaError_t launch_top_forward(const TopArgs& a, int sms, int device, int l2, cudaStream_t st);
 cudaError_t launch_top_backward(const TopArgs& a, cudaStream_t st);
 
+// The same loss, or cross-entropy alone (K 0, tvd nullptr), from bf16 hidden
+// states and weights.
+struct TopLinearArgs {
+  const void* h;  // (BT, d)
+  int64_t ld_h;
+  const void* w;  // (V, d)
+  int64_t ld_w, d;
+  const int64_t* target;
+  const float* values;
+  int64_t ld_v;
+  const int32_t* index;
+  int64_t ld_i;
+  const float* rest;
+  int64_t BT, V, K, ignore_index;
+  float* ce;
+  float* tvd;
+  float* lse;
+  float* rest_lse;
+  float* t_lse;
+  float* sigma;
+  void* workspace;
+  int32_t* dev_status;
+  // backward
+  const float* grad_ce = nullptr;
+  const float* grad_tvd = nullptr;
+  int64_t grad_stride = 0;
+  void* grad_h = nullptr;  // (BT, d) bf16
+  int64_t ld_gh = 0;
+  void* grad_w = nullptr;  // (V, d), bf16 or fp32 by grad_w_kind (FCT_GEMM_*)
+  int64_t ld_gw = 0;
+  int grad_w_kind = 0;
+  int64_t piece_cols = 0;  // 0: automatic
+};
+size_t top_linear_forward_bytes(int64_t BT, int64_t V, int64_t K);
+size_t top_linear_backward_bytes(int64_t BT, int64_t V, int64_t d, int64_t K, int64_t piece_cols);
+cudaError_t launch_top_linear_forward(const TopLinearArgs& a, int sms, int device,
+                                      cudaStream_t st);
+cudaError_t launch_top_linear_backward(const TopLinearArgs& a, int sms, int device,
+                                       cudaStream_t st);
+
 cudaError_t launch_forward(const FwdArgs& a, const FwdPlan& plan, cudaStream_t st);
 cudaError_t launch_mean(const LossArgs& a, cudaStream_t st);
 cudaError_t launch_backward(const BwdArgs& a, bool vec, int sms, cudaStream_t st);

@@ -61,5 +61,113 @@ __device__ __forceinline__ float finish(float m2, float s) {
   return static_cast<float>((double(m2) + double(e) + double(log2f(f))) * 0.6931471805599453);
 }
 
+// exp(x - l), the probability of a logit x under a log-sum-exp l held in fp32.
+__device__ __forceinline__ float prob(float x, float l) { return ex2((x - l) * kLog2e); }
+
+// The sign of p - q for logits x and y under log-sum-exps l and m held in
+// fp32, with a row's sigma.  Where p and q are both near 1 (a student and a
+// teacher that are sure of one word) l and m lose what tells them apart: their
+// roundings, up to `doubt`, exceed 1 - p and 1 - q, and a sign that differs
+// from the one in sigma leaves p (sign - sigma) near 1 or 2 where it should be
+// 0.  A word or a rest with p > 3/4 is the only one, and its sign is that of
+// sigma: |sigma| > 1/2 with a sign, < 1/4 with none.
+__device__ __forceinline__ float sign_of(float x, float l, float y, float m, float doubt,
+                                         float sigma) {
+  const float p = prob(x, l);
+  if (p > 0.75f && fabsf((x - l) - (y - m)) <= doubt)
+    return sigma > 0.375f ? 1.f : sigma < -0.375f ? -1.f : 0.f;
+  return sgn_pq(p, prob(y, m));
+}
+
+// What a row's gradient is made of.
+struct Coefs {
+  float gce, h;  // grad_ce, grad_tvd / 2
+  float lse, t_lse, sigma;
+  float doubt;   // most that (s - lse) - (t - t_lse) is off by the roundings of the two
+  float outside; // coefficient of p_v outside U
+  bool teacher;  // the list holds some probability
+};
+__device__ __forceinline__ Coefs make_coefs(float gce, float gtvd, float lse, float rest,
+                                            float t_lse, float t_rest, float sigma) {
+  const float doubt = (fabsf(lse) + fabsf(t_lse)) * 1.1920929e-07f;  // twice the half steps
+  Coefs c{gce, 0.5f * gtvd, lse, t_lse, sigma, doubt, gce, !(t_lse == -INFINITY)};
+  if (c.teacher)
+    c.outside = fmaf(c.h, sign_of(rest, lse, t_rest, t_lse, doubt + fabsf(rest) * 1.1920929e-07f,
+                                  sigma) - sigma, gce);
+  return c;
+}
+// The gradient at a listed word with student logit s and teacher logit t.
+__device__ __forceinline__ float listed_grad(const Coefs& c, float s, float t, bool target) {
+  const float p = prob(s, c.lse);
+  const float k =
+      c.teacher ? fmaf(c.h, sign_of(s, c.lse, t, c.t_lse, c.doubt, c.sigma) - c.sigma, c.gce) : c.gce;
+  return target ? fmaf(p, k, -c.gce) : p * k;
+}
+
+struct Sums {  // of one row's list, held by every lane of a warp
+  float lse, rest, t_lse, tvd, sigma;
+};
+
+// The list's part of the loss, by one warp: the student's and the teacher's
+// logits of K places (-inf where unused), and the student's state outside U.
+// The signs are those of p and q from their sums, before any log-sum-exp is
+// rounded.
+static __device__ Sums list_sums(const float* s, const float* t, int K, float rest_m2, float rest_s,
+                                 float t_rest) {
+  const int lane = threadIdx.x & 31;
+  float ms = -INFINITY, mt = t_rest;
+  for (int k = lane; k < K; k += 32) {
+    ms = fmaxf(ms, s[k]);
+    mt = fmaxf(mt, t[k]);
+  }
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) {
+    ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, m));
+    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, m));
+  }
+  const float ms2 = fmaxf(ms * kLog2e, rest_m2), mt2 = mt * kLog2e;
+  const float ns = ms2 == -INFINITY ? 0.f : -ms2, nt = mt2 == -INFINITY ? 0.f : -mt2;
+  float us = 0.f, ut = 0.f;
+  for (int k = lane; k < K; k += 32) {
+    us += ex2(fmaf(s[k], kLog2e, ns));
+    ut += ex2(fmaf(t[k], kLog2e, nt));
+  }
+  us = warp_sum(us);
+  ut = warp_sum(ut);
+  const float rs = rest_s == 0.f ? 0.f : rest_s * ex2(rest_m2 + ns);
+  const float rt = ex2(fmaf(t_rest, kLog2e, nt));
+  const float zs = us + rs, zt = ut + rt;
+  Sums o;
+  o.lse = finish(ms2, zs);
+  o.rest = finish(rest_m2, rest_s);
+  o.t_lse = finish(mt2, zt);
+  if (o.t_lse == -INFINITY) {  // no teacher: cross-entropy alone
+    o.tvd = 0.f;
+    o.sigma = 0.f;
+    return o;
+  }
+  const float is = 1.f / zs, it = 1.f / zt;
+  float d = 0.f, g = 0.f;
+  for (int k = lane; k < K; k += 32) {
+    // (products rounded by themselves: equal p and q differ by 0)
+    const float p = __fmul_rn(ex2(fmaf(s[k], kLog2e, ns)), is);
+    const float q = __fmul_rn(ex2(fmaf(t[k], kLog2e, nt)), it);
+    d += fabsf(p - q);
+    g += p * sgn_pq(p, q);
+  }
+  d = warp_sum(d);
+  g = warp_sum(g);
+  // where both sides have most of their mass outside U, the difference of the
+  // two large numbers is that of the small ones inside
+  const float p = __fmul_rn(rs, is), q = __fmul_rn(rt, it);
+  const float gap = p > 0.5f && q > 0.5f ? __fmul_rn(ut, it) - __fmul_rn(us, is) : p - q;
+  o.tvd = 0.5f * (d + fabsf(gap));
+  const float side = sgn_pq(gap, 0.f);
+  o.sigma = fmaf(p, side, g);
+  // (a comparison with NaN gives the sign 0: a teacher's NaN is carried on here)
+  if (o.t_lse != o.t_lse) o.sigma = o.t_lse;
+  return o;
+}
+
 }  // namespace top
 }  // namespace fct

@@ -120,6 +120,107 @@ int loss_impl(const void* student, int64_t ld, int dtype, const int64_t* target,
                           : fct::launch_top_backward(a, st));
 }
 
+// From hidden states: forward (grad false) or backward; t nullptr is
+// cross-entropy alone, whose tvd, rest, t_lse, sigma and grad_tvd are nullptr.
+int linear_impl(const void* h, int64_t ld_h, const void* w, int64_t ld_w, int64_t d,
+                const int64_t* target, const fct_top_list* t, bool list, int64_t BT, int64_t V,
+                int64_t ignore_index, float* ce, float* tvd, float* lse, float* rest,
+                float* t_lse, float* sigma, bool grad, const float* grad_ce,
+                const float* grad_tvd, int64_t grad_stride, void* grad_h, int64_t ld_gh,
+                void* grad_w, int64_t ld_gw, int grad_w_kind, void* workspace,
+                size_t workspace_bytes, int64_t piece_cols, int32_t* dev_status, void* stream) {
+  if (BT < 0 || V <= 0 || d <= 0 || piece_cols < 0) return FCT_ERR_INVALID_ARG;
+  int rc;
+  if (list && (rc = check_list(t)) != FCT_OK) return rc;
+  const int64_t K = list ? t->K : 0, most = fct::kGemmMaxDim;
+  if (grad) {
+    if (grad_stride != 0 && grad_stride != 1) return FCT_ERR_INVALID_ARG;
+    if (grad_w_kind != FCT_GEMM_F32 && grad_w_kind != FCT_GEMM_BF16 &&
+        grad_w_kind != FCT_GEMM_ADD_F32)
+      return FCT_ERR_UNSUPPORTED;
+  }
+  if (BT == 0 && !(grad && grad_w)) return FCT_OK;
+  if (BT > most || V > most || d > most || ld_h > most || ld_w > most || piece_cols > most ||
+      (grad_h && ld_gh > most) || (grad_w && ld_gw > most))
+    return FCT_ERR_UNSUPPORTED;
+  auto row = [&](const void* p, int64_t n = -1, int64_t size = 4) {
+    return Array{p, 1, n < 0 ? BT : n, n < 0 ? BT : n, size};
+  };
+  Array in[14], out[8];
+  int n_in = 0, n_out = 0;
+  const int64_t ew = grad_w_kind == FCT_GEMM_BF16 ? 2 : 4;
+  if (BT > 0) {
+    in[n_in++] = Array{h, BT, d, ld_h, 2};
+    in[n_in++] = Array{w, V, d, ld_w, 2};
+    in[n_in++] = row(target, -1, 8);
+    if (list) {
+      in[n_in++] = Array{t->index, BT, K, t->ld_index, 4};
+      in[n_in++] = Array{t->values, BT, K, t->ld_values, 4};
+      if (t->rest_lse) in[n_in++] = row(t->rest_lse);
+    }
+    Array* stats = grad ? in : out;
+    int& n = grad ? n_in : n_out;
+    if (!grad) stats[n++] = row(ce);
+    stats[n++] = row(lse);
+    if (list) {
+      if (!grad) stats[n++] = row(tvd);
+      for (float* p : {rest, t_lse, sigma}) stats[n++] = row(p);
+    }
+    if (grad) {
+      in[n_in++] = row(grad_ce, grad_stride ? BT : 1);
+      if (list) in[n_in++] = row(grad_tvd, grad_stride ? BT : 1);
+      if (grad_h) out[n_out++] = Array{grad_h, BT, d, ld_gh, 2};
+    }
+  }
+  if (grad && grad_w) out[n_out++] = Array{grad_w, V, d, ld_gw, ew};
+  const size_t need = BT == 0 ? 0
+                      : grad  ? fct::top_linear_backward_bytes(BT, V, d, K, piece_cols)
+                              : fct::top_linear_forward_bytes(BT, V, K);
+  if (need == SIZE_MAX) return FCT_ERR_UNSUPPORTED;
+  if (BT > 0) {
+    if (workspace == nullptr || workspace_bytes < need) return FCT_ERR_INVALID_ARG;
+    const int64_t n = static_cast<int64_t>(need);
+    out[n_out++] = Array{workspace, 1, n, n, 1};
+  }
+  if ((rc = check_arrays(in, n_in, out, n_out)) != FCT_OK) return rc;
+  if (BT > 0 && (!fct::gemm_operand_ok(h, ld_h) || !fct::gemm_operand_ok(w, ld_w) ||
+                 !aligned(workspace, 256)))
+    return FCT_ERR_ALIGNMENT;
+  if ((rc = check_status(dev_status)) != FCT_OK) return rc;
+  int sms = 0, device = 0;
+  if ((rc = fct::current_device_sms(&sms, &device)) != FCT_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (BT == 0) {  // a weight gradient of no rows
+    if (grad_w_kind != FCT_GEMM_ADD_F32 &&
+        cudaMemset2DAsync(grad_w, size_t(ld_gw) * ew, 0, size_t(d) * ew, size_t(V), st) !=
+            cudaSuccess)
+      return FCT_ERR_CUDA;
+    return FCT_OK;
+  }
+  fct::TopLinearArgs a{h, ld_h, w, ld_w, d, target, list ? t->values : nullptr,
+                       list ? t->ld_values : 0, list ? t->index : nullptr, list ? t->ld_index : 0,
+                       list ? t->rest_lse : nullptr, BT, V, K, ignore_index, ce, tvd, lse, rest,
+                       t_lse, sigma, workspace, dev_status};
+  if (!grad) return launched(fct::launch_top_linear_forward(a, sms, device, st));
+  a.grad_ce = grad_ce;
+  a.grad_tvd = grad_tvd;
+  a.grad_stride = grad_stride;
+  a.grad_h = grad_h;
+  a.ld_gh = ld_gh;
+  a.grad_w = grad_w;
+  a.ld_gw = ld_gw;
+  a.grad_w_kind = grad_w_kind;
+  a.piece_cols = piece_cols;
+  if (grad_h == nullptr && grad_w == nullptr) return FCT_OK;
+  return launched(fct::launch_top_linear_backward(a, sms, device, st));
+}
+
+bool sizes_ok(int64_t BT, int64_t V, int64_t d, int64_t K, int64_t piece) {
+  const int64_t most = fct::kGemmMaxDim;
+  return BT > 0 && V > 0 && d > 0 && K >= 0 && piece >= 0 && BT <= most && V <= most &&
+         d <= most && K <= FCT_TOP_MAX && piece <= most;
+}
+
 }  // namespace
 
 extern "C" {
@@ -180,6 +281,68 @@ int fused_ce_tvd_top_forward_backward(const void* student, int64_t ld_student, f
   return loss_impl(student, ld_student, dtype, target, teacher, BT, V, ignore_index, ce, tvd,
                    student_lse, student_rest, teacher_lse, sigma, true, true, grad_ce, grad_tvd,
                    grad_stride, grad_student, ld_grad, dev_status, stream);
+}
+
+size_t fused_linear_ce_tvd_top_forward_workspace_size(int64_t BT, int64_t V, int64_t K) {
+  if (!sizes_ok(BT, V, 1, K, 0)) return 0;
+  const size_t b = fct::top_linear_forward_bytes(BT, V, K);
+  return b == SIZE_MAX ? 0 : b;
+}
+
+size_t fused_linear_ce_tvd_top_backward_workspace_size(int64_t BT, int64_t V, int64_t d, int64_t K,
+                                                       int64_t piece_cols) {
+  if (!sizes_ok(BT, V, d, K, piece_cols)) return 0;
+  const size_t b = fct::top_linear_backward_bytes(BT, V, d, K, piece_cols);
+  return b == SIZE_MAX ? 0 : b;
+}
+
+int fused_linear_ce_tvd_top_forward(const void* h, int64_t ld_h, const void* w, int64_t ld_w,
+                                    int64_t d, const int64_t* target, const fct_top_list* teacher,
+                                    int64_t BT, int64_t V, int64_t ignore_index, float* ce,
+                                    float* tvd, float* student_lse, float* student_rest,
+                                    float* teacher_lse, float* sigma, void* workspace,
+                                    size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  return linear_impl(h, ld_h, w, ld_w, d, target, teacher, true, BT, V, ignore_index, ce, tvd,
+                     student_lse, student_rest, teacher_lse, sigma, false, nullptr, nullptr, 0,
+                     nullptr, 0, nullptr, 0, 0, workspace, workspace_bytes, 0, dev_status, stream);
+}
+
+int fused_linear_ce_tvd_top_backward(const void* h, int64_t ld_h, const void* w, int64_t ld_w,
+                                     int64_t d, const int64_t* target, const fct_top_list* teacher,
+                                     int64_t BT, int64_t V, int64_t ignore_index,
+                                     const float* student_lse, const float* student_rest,
+                                     const float* teacher_lse, const float* sigma,
+                                     const float* grad_ce, const float* grad_tvd,
+                                     int64_t grad_stride, void* grad_h, int64_t ld_grad_h,
+                                     void* grad_w, int64_t ld_grad_w, int32_t grad_w_kind,
+                                     void* workspace, size_t workspace_bytes, int64_t piece_cols,
+                                     int32_t* dev_status, void* stream) {
+  return linear_impl(h, ld_h, w, ld_w, d, target, teacher, true, BT, V, ignore_index, nullptr,
+                     nullptr, const_cast<float*>(student_lse), const_cast<float*>(student_rest),
+                     const_cast<float*>(teacher_lse), const_cast<float*>(sigma), true, grad_ce,
+                     grad_tvd, grad_stride, grad_h, ld_grad_h, grad_w, ld_grad_w, grad_w_kind,
+                     workspace, workspace_bytes, piece_cols, dev_status, stream);
+}
+
+int fused_linear_ce_forward(const void* h, int64_t ld_h, const void* w, int64_t ld_w, int64_t d,
+                            const int64_t* target, int64_t BT, int64_t V, int64_t ignore_index,
+                            float* ce, float* lse, void* workspace, size_t workspace_bytes,
+                            int32_t* dev_status, void* stream) {
+  return linear_impl(h, ld_h, w, ld_w, d, target, nullptr, false, BT, V, ignore_index, ce, nullptr,
+                     lse, nullptr, nullptr, nullptr, false, nullptr, nullptr, 0, nullptr, 0,
+                     nullptr, 0, 0, workspace, workspace_bytes, 0, dev_status, stream);
+}
+
+int fused_linear_ce_backward(const void* h, int64_t ld_h, const void* w, int64_t ld_w, int64_t d,
+                             const int64_t* target, int64_t BT, int64_t V, int64_t ignore_index,
+                             const float* lse, const float* grad_ce, int64_t grad_stride,
+                             void* grad_h, int64_t ld_grad_h, void* grad_w, int64_t ld_grad_w,
+                             int32_t grad_w_kind, void* workspace, size_t workspace_bytes,
+                             int64_t piece_cols, int32_t* dev_status, void* stream) {
+  return linear_impl(h, ld_h, w, ld_w, d, target, nullptr, false, BT, V, ignore_index, nullptr,
+                     nullptr, const_cast<float*>(lse), nullptr, nullptr, nullptr, true, grad_ce,
+                     nullptr, grad_stride, grad_h, ld_grad_h, grad_w, ld_grad_w, grad_w_kind,
+                     workspace, workspace_bytes, piece_cols, dev_status, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,808 @@
+// The loss against a teacher's top logits, or cross-entropy alone, from hidden
+// states and lm_head weights: the (BT, V) logits never exist.
+//
+// Forward: one pass of logit tiles (h w^T on the tensor cores) whose epilogue
+// keeps of each tile row a log-sum-exp state over the words outside the list,
+// and the logits of the listed words and the target; a small kernel merges
+// those into the loss.  Backward, in pieces of the vocabulary: the same tiles
+// again, now leaving the epilogue as bf16 gradients of the logits; a product
+// of those with the piece's weights adds to d hidden, and one with the hidden
+// states is the piece's d weight, complete.  So the forward is 2 BT V d
+// operations and the backward 6 BT V d (a third of them the logits again),
+// bound by the tensor cores; few rows are bound by reading the weights.
+//
+// Precision: the tensor cores' fp32 accumulators drop what lies below them
+// (4096 products: 1.5e-5 off, always towards 0, at logits near 3.5; products
+// and sums in fp32 registers: 2e-6).  A loss of nearly equal masses shows
+// that.  So a tile's sum runs in the accumulator over 512 products at a time,
+// and these partial sums are added in fp32 registers: eight epilogue warps
+// hold 128 columns of a row per thread.
+//
+// Roles per CTA of a pair, as in the plain GEMM: warp 0 issues the copies,
+// warp 1 (of CTA 0) the products, warps 4 to 11 are the epilogue, two per 32
+// rows with 128 columns each.  Two accumulators alternate between partial
+// sums, so that products go on while the last partial sum is added.
+#include <climits>
+#include <mutex>
+
+#include "fct_internal.h"
+#include "fct_pair.cuh"
+#include "fct_top.cuh"
+
+namespace fct {
+
+namespace {
+
+using namespace pair;
+
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+// Registers move from the first warpgroup to the two of the epilogue: of the
+// launch's 384 x 168, 128 x 40 and 256 x 232.
+constexpr int kLeanRegs = 40, kEpiRegs = 232;
+static_assert(128 * kLeanRegs + 256 * kEpiRegs <= kThreads * 168, "the launch's registers");
+constexpr int kCols = 128;   // columns of a tile row that an epilogue thread holds
+constexpr int kChunk = 8;    // K blocks of 64 summed in the accumulator
+constexpr size_t kSmem = size_t(kGStages) * kGStageBytes + kEpiWarps * kOutBufBytes + 1024;
+constexpr int kSortThreads = 128;
+
+// What the backward's epilogue needs of a row.
+struct RowCoefs {
+  top::Coefs c;
+  int target;
+  int live;  // 0: an ignored row, whose gradient is 0
+};
+
+struct TileArgs {
+  int64_t M, N, K;      // rows, columns of this piece, hidden size
+  int64_t v0;           // the piece's first word
+  const int32_t* words; // (M, L) each row's listed words, rising; INT_MAX behind them
+  const float* teacher; // (M, L) their teacher logits
+  int64_t L;
+  // forward
+  const int64_t* target;
+  float2* part;  // (M, part_ld): states per 128 columns
+  int64_t part_ld;
+  float* listed;    // (M, L) student logits of `words` (the backward's own use too)
+  float* tg_logit;  // (M)
+  // backward
+  const RowCoefs* rows;
+  int32_t* status;
+};
+
+// mbar_wait without a call: a call would have the epilogue's registers, most
+// of which hold a tile row, saved around it.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                     bool heed_abort = true) {
+  if (mbar_try(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (uint32_t it = 0; it < (1u << 30); ++it) {
+    if (heed_abort && *abort) return false;
+    if (mbar_try(bar, parity)) return true;
+    if (clock64() - t0 > kWaitLimitCycles) break;
+  }
+  *abort = 1;
+  return false;
+}
+
+// The first place of a row's words at or above v.
+__device__ __forceinline__ int first_at(const int32_t* words, int L, int v) {
+  int lo = 0, hi = L;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (words[mid] < v)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+template <bool kGrad>
+__global__ void __launch_bounds__(kThreads, 1)
+    tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                const __grid_constant__ CUtensorMap tmG, const TileArgs a) {
+  extern __shared__ uint8_t tile_smem[];
+  __shared__ __align__(8) uint64_t full_bar[kGStages], empty_bar[kGStages];
+  __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], done_bar;
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int64_t pair_id = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+  const uint32_t smem0 = (smem_addr(tile_smem) + 1023u) & ~1023u;
+  const int64_t m_tiles = (a.M + kBM - 1) / kBM, n_tiles = (a.N + kBN - 1) / kBN;
+  const int64_t units = m_tiles * n_tiles;
+  const int k_iters = static_cast<int>((a.K + kBK - 1) / kBK);
+  const int chunks = (k_iters + kChunk - 1) / kChunk;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kGStages; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 2 * kEpiWarps);
+    }
+    mbar_init(&done_bar, 1);
+    abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(&tmem_base)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before any copy or arrive
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  const uint32_t full0 = map_to_rank(smem_addr(&full_bar[0]), 0);
+  const uint32_t acc_empty0 = map_to_rank(smem_addr(&acc_empty[0]), 0);
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLeanRegs));
+    if (warp == 0) {
+      if (lane == 0) {  // ---- copies (both CTAs)
+        int stage = 0;
+        uint32_t phase = 0, issued = 0;
+        bool ok = true;
+        for (int64_t u = pair_id; ok && u < units; u += n_pairs) {
+          const int m0 = static_cast<int>((u % m_tiles) * kBM) + int(rank) * kCtaRows;
+          const int n0 = static_cast<int>((u / m_tiles) * kBN) + int(rank) * kCtaRows;
+          for (int kb = 0; kb < k_iters; ++kb) {
+            if (!wait(&empty_bar[stage], phase ^ 1u, &abort_flag)) {
+              ok = false;
+              break;
+            }
+            if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * kGStageBytes);
+            const uint32_t sa = smem0 + stage * kGStageBytes;
+            load_rows<false>(sa, &tmA, m0, kb, full0 + 8u * stage);
+            load_rows<false>(sa + kHalfBytes, &tmB, n0, kb, full0 + 8u * stage);
+            ++issued;
+            if (++stage == kGStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+        }
+        // the last fills of both CTAs have landed before the leader's producer leaves
+        if (leader)
+          for (uint32_t i = (issued > uint32_t(kGStages) ? issued - kGStages : 0); i < issued; ++i)
+            wait(&full_bar[i % kGStages], (i / kGStages) & 1u, &abort_flag, false);
+      }
+    } else if (warp == 1) {
+      if (lane == 0 && leader) {  // ---- products for the pair
+        constexpr uint32_t kId = idesc<false, false>();
+        int stage = 0;
+        uint32_t phase = 0, sums = 0;
+        bool ok = true;
+        for (int64_t u = pair_id; ok && u < units; u += n_pairs) {
+          for (int kb0 = 0; ok && kb0 < k_iters; kb0 += kChunk, ++sums) {
+            const int acc = static_cast<int>(sums & 1u);
+            if (!wait(&acc_empty[acc], ((sums >> 1) & 1u) ^ 1u, &abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem + uint32_t(acc * kBN);
+            const int kb1 = min(k_iters, kb0 + kChunk);
+            for (int kb = kb0; kb < kb1; ++kb) {
+              if (!wait(&full_bar[stage], phase, &abort_flag)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t sa = smem0 + stage * kGStageBytes;
+              const uint64_t adesc = smem_desc<false>(sa), bdesc = smem_desc<false>(sa + kHalfBytes);
+  #pragma unroll
+              for (int kk = 0; kk < kBK / 16; ++kk)
+                umma_bf16<kId>(d, adesc + kk * desc_k_step<false>(), bdesc + kk * desc_k_step<false>(),
+                               (kb > kb0 || kk > 0) ? 1u : 0u);
+              umma_commit_pair(&empty_bar[stage]);
+              if (++stage == kGStages) {
+                stage = 0;
+                phase ^= 1u;
+              }
+            }
+            if (ok) umma_commit_pair(&acc_full[acc]);
+          }
+        }
+        umma_commit_pair(&done_bar);  // every product issued has completed
+      }
+    }
+  } else {  // ---- epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t tq = tmem + (uint32_t(q * 32) << 16) + uint32_t(half * kCols);
+    const uint32_t buf = smem0 + kGStages * kGStageBytes + uint32_t(warp - 4) * kOutBufBytes;
+    const int L = static_cast<int>(a.L);
+    uint32_t sums = 0;
+    bool ok = true;
+    for (int64_t u = pair_id; ok && u < units; u += n_pairs) {
+      const int64_t row = (u % m_tiles) * kBM + int64_t(rank) * kCtaRows + q * 32 + lane;
+      const int64_t n0 = (u / m_tiles) * kBN + half * kCols;  // first column in the piece
+      const int col0 = static_cast<int>(a.v0 + n0);           // its word
+      // the list's part of this row and these columns, found while the products run
+      int at = L, next = INT_MAX, tg = -1;
+      const int32_t* words = a.words + row * a.L;
+      RowCoefs rc;
+      if (row < a.M) {
+        at = first_at(words, L, col0);
+        if (at < L) next = words[at];
+        if constexpr (kGrad) {
+          rc = a.rows[row];
+          tg = rc.target;
+        } else {
+          const int64_t t = a.target[row];
+          if (t >= col0 && t < col0 + kCols) tg = static_cast<int>(t);
+        }
+      }
+      float x[kCols];
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c, ++sums) {
+        const int acc = static_cast<int>(sums & 1u);
+        ok = __all_sync(0xffffffffu, wait(&acc_full[acc], (sums >> 1) & 1u, &abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int g = 0; g < kCols / 32; ++g) {
+          uint32_t r[32];
+          tmem_ld32(tq + uint32_t(acc * kBN + g * 32), r);
+          if (c == 0) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[g * 32 + j] = __uint_as_float(r[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const float2 s = __fadd2_rn(make_float2(x[g * 32 + j], x[g * 32 + j + 1]),
+                                          make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])));
+              x[g * 32 + j] = s.x;
+              x[g * 32 + j + 1] = s.y;
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acc_empty0 + 8u * acc);
+      }
+      if (!ok) break;
+      const int64_t left = a.N - n0;  // columns inside the piece
+      if constexpr (!kGrad) {
+        // ---- forward: words of the list and the target go out and, the list's,
+        // out of the sum
+#pragma unroll
+        for (int g = 0; g < kCols / 32; ++g) {
+          const int c0 = col0 + g * 32, first = at;
+          uint32_t mask = 0;
+          while (next < c0 + 32) {
+            mask |= 1u << (next - c0);
+            next = ++at < L ? words[at] : INT_MAX;
+          }
+          const bool here = static_cast<uint32_t>(tg - c0) < 32u;
+          if (__any_sync(0xffffffffu, mask != 0 || here)) {
+            float* out = a.listed + row * a.L + first;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              if (here && tg - c0 == j) a.tg_logit[row] = x[g * 32 + j];
+              if ((mask >> j) & 1u) {
+                *out++ = x[g * 32 + j];
+                x[g * 32 + j] = -INFINITY;
+              }
+            }
+          }
+          if (left < (g + 1) * 32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (g * 32 + j >= left) x[g * 32 + j] = -INFINITY;
+          }
+        }
+        float vm = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < kCols; j += 2) vm = max3(vm, x[j], x[j + 1]);
+        const float m2 = vm * kLog2e, nm = m2 == -INFINITY ? 0.f : -m2;
+        float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+        const float2 L2 = make_float2(kLog2e, kLog2e), n2 = make_float2(nm, nm);
+#pragma unroll
+        for (int j = 0; j < kCols; j += 4) {
+          const float2 e0 = __ffma2_rn(make_float2(x[j], x[j + 1]), L2, n2);
+          const float2 e1 = __ffma2_rn(make_float2(x[j + 2], x[j + 3]), L2, n2);
+          s0 = __fadd2_rn(s0, make_float2(ex2(e0.x), ex2(e0.y)));
+          s1 = __fadd2_rn(s1, make_float2(ex2(e1.x), ex2(e1.y)));
+        }
+        if (row < a.M)
+          a.part[row * a.part_ld + n0 / kCols] = make_float2(m2, (s0.x + s0.y) + (s1.x + s1.y));
+      } else {
+        // ---- backward: the logits' gradient, 64 columns at a time through shared memory
+        const int y = static_cast<int>(row) - lane;
+#pragma unroll
+        for (int b = 0; b < kCols / 64; ++b) {
+          uint32_t w[32], masks[2];
+          int mid = 0, mid_next = 0, end = 0, end_next = 0;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const int o = b * 64 + g * 32;
+            // the logits of listed words and of the target go through memory, so that
+            // the code that turns one into a gradient is there once
+            const int c0 = col0 + o;
+            int place = g == 0 ? at : mid, word = g == 0 ? next : mid_next;
+            float* out = a.listed + row * a.L + place;
+            uint32_t mask = 0;
+            while (word < c0 + 32) {
+              mask |= 1u << (word - c0);
+              word = ++place < L ? words[place] : INT_MAX;
+            }
+            if (g == 0) mid = place, mid_next = word;
+            else end = place, end_next = word;
+            masks[g] = mask;
+            const bool here = static_cast<uint32_t>(tg - c0) < 32u;
+            if (__any_sync(0xffffffffu, mask != 0 || here)) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                if (here && tg - c0 == j) a.tg_logit[row] = x[o + j];
+                if ((mask >> j) & 1u) *out++ = x[o + j];
+              }
+            }
+            const float2 nl = make_float2(-rc.c.lse, -rc.c.lse), L2 = make_float2(kLog2e, kLog2e);
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const float2 e = __fmul2_rn(__fadd2_rn(make_float2(x[o + j], x[o + j + 1]), nl), L2);
+              w[g * 16 + j / 2] = pack_bf16x2(ex2(e.x) * rc.c.outside, ex2(e.y) * rc.c.outside);
+            }
+            if (left < o + 32) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                if (o + 2 * j >= left) w[g * 16 + j] = 0u;
+                if (o + 2 * j + 1 == left) w[g * 16 + j] &= 0xffffu;
+              }
+            }
+          }
+          if (row >= a.M || !rc.live) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) w[j] = 0u;
+          }
+          if (lane == 0) bulk_wait_read_0();  // the last store has read the buffer
+          __syncwarp();
+          stage_row(buf, lane, w);
+          // the listed words and the target, over what was staged there (an
+          // ignored row has neither)
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const int c0 = col0 + b * 64 + g * 32;
+            const bool here = static_cast<uint32_t>(tg - c0) < 32u;
+            const uint32_t here_bit = here ? 1u << (tg - c0) : 0u;
+            for (uint32_t todo = masks[g] | here_bit; todo != 0; todo &= todo - 1) {
+              const uint32_t bit = todo & (0u - todo);
+              float grad;
+              if (masks[g] & bit) {
+                grad = top::listed_grad(rc.c, a.listed[row * a.L + at], a.teacher[row * a.L + at],
+                                        bit == here_bit);
+                ++at;
+              } else {
+                grad = fmaf(top::prob(a.tg_logit[row], rc.c.lse), rc.c.outside, -rc.c.gce);
+              }
+              const int in = g * 64 + (__ffs(static_cast<int>(todo)) - 1) * 2;  // byte in the row
+              const uint32_t addr = buf + uint32_t(lane) * 128u +
+                                    uint32_t((((in >> 4) ^ (lane & 7)) << 4) + (in & 15));
+              asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr),
+                           "h"(static_cast<unsigned short>(pack_bf16x2(grad, 0.f)))
+                           : "memory");
+            }
+          }
+          at = end;
+          next = end_next;
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0 && b * 64 < left && y < a.M)
+            tma_store_2d<false>(&tmG, static_cast<int>(n0) + b * 64, y, buf);
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all();  // the gradients are written before the kernel ends
+  }
+  tc_fence_before();
+  __syncthreads();
+  // the pair's products have all completed before either CTA frees its tensor
+  // memory or leaves
+  if (warp == 1 && lane == 0) wait(&done_bar, 0, &abort_flag, false);
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(kTmemCols)
+                 : "memory");
+  if (threadIdx.x == 0 && abort_flag && a.status) atomicOr(a.status, FCT_DEV_WAIT_TIMEOUT);
+}
+
+// ---------------------------------------------------------------- rows
+
+struct ListArgs {
+  int64_t V, K;  // K 0: no list
+  const float* values;
+  int64_t ld_v;
+  const int32_t* index;
+  int64_t ld_i;
+  const float* rest;
+  const int64_t* target;
+  int64_t ignore_index;
+  int32_t* words;  // (BT, K)
+  float* teacher;
+  int32_t* bad;  // forward: (BT)
+  // backward
+  RowCoefs* rows;
+  const float* lse;
+  const float* rest_lse;
+  const float* t_lse;
+  const float* sigma;
+  const float* grad_ce;
+  const float* grad_tvd;
+  int64_t grad_stride;
+  int32_t* dev_status;
+};
+
+// One CTA per row: the list sorted by word, so that a tile finds its part, and
+// the row's coefficients.
+template <bool kGrad>
+__global__ void __launch_bounds__(kSortThreads) list_kernel(ListArgs a) {
+  __shared__ unsigned long long key[kTopMax];
+  const int64_t row = blockIdx.x;
+  const int K = static_cast<int>(a.K), tid = threadIdx.x;
+  const int64_t tg = a.target[row];
+  const bool ignored = tg == a.ignore_index;
+  bool bad = false;
+  if (K > 0) {
+    int P = 2;
+    while (P < K) P *= 2;
+    for (int k = tid; k < P; k += kSortThreads) {
+      int v = INT_MAX;
+      if (k < K && !ignored) {
+        v = a.index[row * a.ld_i + k];
+        if (v < 0 || v >= a.V) {
+          if (v != -1) bad = true;
+          v = INT_MAX;
+        }
+      }
+      key[k] = (static_cast<unsigned long long>(static_cast<uint32_t>(v)) << 32) | uint32_t(k);
+    }
+    __syncthreads();
+    for (int size = 2; size <= P; size *= 2)
+      for (int step = size / 2; step > 0; step /= 2) {
+        for (int i = tid; i < P / 2; i += kSortThreads) {
+          const int lo = (i / step) * 2 * step + (i % step), hi = lo + step;
+          const bool up = (lo & size) == 0;
+          const unsigned long long x = key[lo], y = key[hi];
+          if ((x > y) == up) {
+            key[lo] = y;
+            key[hi] = x;
+          }
+        }
+        __syncthreads();
+      }
+    for (int k = tid; k < K; k += kSortThreads) {
+      const int v = static_cast<int>(key[k] >> 32);
+      const bool used = v != INT_MAX;
+      a.words[row * a.K + k] = v;
+      a.teacher[row * a.K + k] =
+          used ? a.values[row * a.ld_v + static_cast<int64_t>(key[k] & 0xffffffffu)] : -INFINITY;
+      if (used && k > 0 && static_cast<int>(key[k - 1] >> 32) == v) bad = true;
+    }
+  }
+  const int wrong = __syncthreads_or(bad);
+  if (tid != 0) return;
+  const bool outside = !ignored && (tg < 0 || tg >= a.V);
+  const int status = (outside ? FCT_DEV_TARGET_OUT_OF_RANGE : 0) | (wrong ? FCT_DEV_BAD_LIST : 0);
+  if (status && a.dev_status) atomicOr(a.dev_status, status);
+  if constexpr (kGrad) {
+    RowCoefs r;
+    const float nan = __uint_as_float(0x7fc00000u);
+    const bool ok = !outside && !wrong;
+    const float gce = a.grad_ce[row * a.grad_stride];
+    r.c = K > 0 ? top::make_coefs(gce, a.grad_tvd[row * a.grad_stride], ok ? a.lse[row] : nan,
+                                  a.rest_lse[row], a.t_lse[row], a.rest ? a.rest[row] : -INFINITY,
+                                  a.sigma[row])
+                : top::make_coefs(gce, 0.f, ok ? a.lse[row] : nan, 0.f, -INFINITY, -INFINITY, 0.f);
+    r.target = ok && !ignored ? static_cast<int>(tg) : -1;
+    r.live = !ignored;
+    a.rows[row] = r;
+  } else {
+    a.bad[row] = wrong;
+  }
+}
+
+struct MergeArgs {
+  const float2* part;
+  int64_t parts, K;
+  const float* listed;
+  const int32_t* words;
+  const float* teacher;
+  const float* tg_logit;
+  const int32_t* bad;
+  const float* rest;
+  const int64_t* target;
+  int64_t V, ignore_index;
+  float* ce;
+  float* tvd;  // nullptr with the following: cross-entropy alone
+  float* lse;
+  float* rest_lse;
+  float* t_lse;
+  float* sigma;
+};
+
+// One CTA per row: the tiles' states and the list's logits merged into the loss.
+__global__ void __launch_bounds__(kSortThreads) merge_kernel(MergeArgs a) {
+  __shared__ float s[kTopMax], t[kTopMax];
+  __shared__ float2 state[kSortThreads / 32];
+  const int64_t row = blockIdx.x;
+  const int K = static_cast<int>(a.K), tid = threadIdx.x;
+  const int64_t tg = a.target[row];
+  if (tg == a.ignore_index) {
+    if (tid == 0) {
+      a.ce[row] = 0.f;
+      a.lse[row] = 0.f;
+      if (a.tvd != nullptr) {
+        a.tvd[row] = 0.f;
+        a.rest_lse[row] = 0.f;
+        a.t_lse[row] = 0.f;
+        a.sigma[row] = 0.f;
+      }
+    }
+    return;
+  }
+  Lse2 st{-INFINITY, 0.f};
+  for (int64_t i = tid; i < a.parts; i += kSortThreads) {
+    const float2 p = a.part[row * a.parts + i];
+    st = top::merge(st, Lse2{p.x, p.y});
+  }
+  st = top::warp_merge(st);
+  if ((tid & 31) == 0) state[tid >> 5] = make_float2(st.m2, st.s);
+  for (int k = tid; k < K; k += kSortThreads) {
+    const bool used = a.words[row * a.K + k] != INT_MAX;
+    s[k] = used ? a.listed[row * a.K + k] : -INFINITY;
+    t[k] = a.teacher[row * a.K + k];
+  }
+  __syncthreads();
+  if (tid >= 32) return;
+  const float2 w = tid < kSortThreads / 32 ? state[tid] : make_float2(-INFINITY, 0.f);
+  const Lse2 r = top::warp_merge(Lse2{w.x, w.y});
+  const float t_rest = a.rest ? a.rest[row] : -INFINITY;
+  top::Sums o = top::list_sums(s, t, K, r.m2, r.s, t_rest);
+  const float nan = __uint_as_float(0x7fc00000u);
+  if (a.bad[row]) o = top::Sums{nan, nan, nan, nan, nan};
+  if (tid != 0) return;
+  a.ce[row] = tg >= 0 && tg < a.V ? o.lse - a.tg_logit[row] : nan;
+  a.lse[row] = o.lse;
+  if (a.tvd != nullptr) {
+    a.tvd[row] = o.tvd;
+    a.rest_lse[row] = o.rest;
+    a.t_lse[row] = o.t_lse;
+    a.sigma[row] = o.sigma;
+  }
+}
+
+// bf16 rows from the fp32 sum over the pieces.
+__global__ void __launch_bounds__(256) round_kernel(const float* src, int64_t ld_src, uint16_t* dst,
+                                                    int64_t ld, int64_t rows, int64_t cols) {
+  const int64_t per = (cols + 1) / 2, total = rows * per;
+  for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
+    const int64_t r = i / per, c = (i - r * per) * 2;
+    const float2 v = *reinterpret_cast<const float2*>(src + r * ld_src + c);  // rows padded to 4
+    const uint32_t p = pack_bf16x2(v.x, v.y);
+    uint16_t* d = dst + r * ld + c;
+    d[0] = static_cast<uint16_t>(p);
+    if (c + 1 < cols) d[1] = static_cast<uint16_t>(p >> 16);
+  }
+}
+
+// ---------------------------------------------------------------- launch
+
+struct PairLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  PairLaunch() {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+};
+
+template <bool kGrad>
+cudaError_t run_tiles(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mg,
+                      const TileArgs& a, int sms, int device, cudaStream_t st) {
+  auto kernel = tile_kernel<kGrad>;
+  static std::once_flag once[64];
+  static int pairs[64];
+  std::call_once(once[device], [&] {
+    pairs[device] = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmem)) != cudaSuccess)
+      return;
+    PairLaunch l;
+    l.cfg.gridDim = dim3(2 * 64);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &l.cfg) == cudaSuccess) pairs[device] = n;
+  });
+  if (pairs[device] <= 0) return cudaErrorInvalidConfiguration;
+  int64_t n = ((a.M + kBM - 1) / kBM) * ((a.N + kBN - 1) / kBN);
+  if (n > pairs[device]) n = pairs[device];
+  if (n > sms / 2) n = sms / 2;
+  PairLaunch l;
+  l.cfg.gridDim = dim3(static_cast<unsigned>(2 * n));
+  l.cfg.stream = st;
+  return cudaLaunchKernelEx(&l.cfg, kernel, ma, mb, mg, a);
+}
+
+constexpr size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
+
+// Regions of a workspace, one behind the other, each on 256 bytes.
+struct Carve {
+  char* base;
+  size_t used = 0;
+  bool fits = true;
+  template <typename T>
+  T* take(int64_t rows, int64_t cols) {
+    if (rows > 0 && cols > 0 && uint64_t(cols) > (SIZE_MAX / 4 - used) / sizeof(T) / uint64_t(rows))
+      fits = false;
+    char* p = base ? base + used : nullptr;
+    if (fits) used += round_up(size_t(rows) * size_t(cols) * sizeof(T));
+    return reinterpret_cast<T*>(p);
+  }
+};
+
+struct ForwardSpace {
+  float2* part;
+  int32_t* words;
+  float* teacher;
+  float* listed;
+  float* tg_logit;
+  int32_t* bad;
+  int64_t parts;
+  size_t bytes;
+  ForwardSpace(void* base, int64_t BT, int64_t V, int64_t K) {
+    Carve c{static_cast<char*>(base)};
+    parts = (V + kBN - 1) / kBN * (kBN / kCols);
+    part = c.take<float2>(BT, parts);
+    words = c.take<int32_t>(BT, K);
+    teacher = c.take<float>(BT, K);
+    listed = c.take<float>(BT, K);
+    tg_logit = c.take<float>(BT, 1);
+    bad = c.take<int32_t>(BT, 1);
+    bytes = c.fits ? c.used : SIZE_MAX;
+  }
+};
+
+// Columns of a piece: as given, rounded to whole tiles, or 2^28 logits.
+int64_t piece_of(int64_t BT, int64_t V, int64_t asked) {
+  int64_t cols = asked > 0 ? asked : (int64_t(1) << 28) / (BT > 0 ? BT : 1);
+  cols = (cols + kBN - 1) / kBN * kBN;
+  if (cols < kBN) cols = kBN;
+  return cols < V ? cols : V;
+}
+
+struct BackwardSpace {
+  int32_t* words;
+  float* teacher;
+  float* listed;
+  float* tg_logit;
+  RowCoefs* rows;
+  uint16_t* G;
+  float* sum;   // d hidden summed over pieces, or the partial sums of its one product
+  size_t sum_bytes;
+  int64_t piece, ld_g, ld_sum;
+  size_t bytes;
+  BackwardSpace(void* base, int64_t BT, int64_t V, int64_t d, int64_t K, int64_t asked) {
+    Carve c{static_cast<char*>(base)};
+    piece = piece_of(BT, V, asked);
+    ld_g = (piece + 7) / 8 * 8;
+    ld_sum = (d + 3) / 4 * 4;
+    words = c.take<int32_t>(BT, K);
+    teacher = c.take<float>(BT, K);
+    listed = c.take<float>(BT, K);
+    tg_logit = c.take<float>(BT, 1);
+    rows = c.take<RowCoefs>(BT, 1);
+    G = c.take<uint16_t>(BT, ld_g);
+    // one piece: room to split its K where d hidden has few tiles
+    sum_bytes = 0;
+    if (piece < V)
+      sum_bytes = size_t(BT) * size_t(ld_sum) * 4;
+    else if (((BT + kBM - 1) / kBM) * ((d + kBN - 1) / kBN) <= 152)
+      sum_bytes = gemm_split_workspace_bytes(BT, d);
+    sum = c.take<float>(1, static_cast<int64_t>((sum_bytes + 3) / 4));
+    bytes = c.fits ? c.used : SIZE_MAX;
+  }
+};
+
+}  // namespace
+
+size_t top_linear_forward_bytes(int64_t BT, int64_t V, int64_t K) {
+  return ForwardSpace(nullptr, BT, V, K).bytes;
+}
+size_t top_linear_backward_bytes(int64_t BT, int64_t V, int64_t d, int64_t K, int64_t piece) {
+  return BackwardSpace(nullptr, BT, V, d, K, piece).bytes;
+}
+
+cudaError_t launch_top_linear_forward(const TopLinearArgs& a, int sms, int device,
+                                      cudaStream_t st) {
+  const ForwardSpace w(a.workspace, a.BT, a.V, a.K);
+  CUtensorMap ma, mb;
+  if (!operand_map(&ma, GemmOperand{a.h, a.ld_h, false}, a.BT, a.d, kCtaRows) ||
+      !operand_map(&mb, GemmOperand{a.w, a.ld_w, false}, a.V, a.d, kCtaRows))
+    return cudaErrorInvalidValue;
+  ListArgs l{a.V, a.K, a.values, a.ld_v, a.index, a.ld_i, a.rest, a.target, a.ignore_index,
+             w.words, w.teacher, w.bad};
+  l.dev_status = a.dev_status;
+  list_kernel<false><<<static_cast<unsigned>(a.BT), kSortThreads, 0, st>>>(l);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  TileArgs t{a.BT, a.V, a.d, 0, w.words, w.teacher, a.K, a.target, w.part, w.parts,
+             w.listed, w.tg_logit, nullptr, a.dev_status};
+  if ((e = run_tiles<false>(ma, mb, ma, t, sms, device, st)) != cudaSuccess) return e;
+  merge_kernel<<<static_cast<unsigned>(a.BT), kSortThreads, 0, st>>>(
+      MergeArgs{w.part, w.parts, a.K, w.listed, w.words, w.teacher, w.tg_logit, w.bad, a.rest,
+                a.target, a.V, a.ignore_index, a.ce, a.tvd, a.lse, a.rest_lse, a.t_lse, a.sigma});
+  return cudaGetLastError();
+}
+
+cudaError_t launch_top_linear_backward(const TopLinearArgs& a, int sms, int device,
+                                       cudaStream_t st) {
+  const BackwardSpace w(a.workspace, a.BT, a.V, a.d, a.K, a.piece_cols);
+  CUtensorMap ma;
+  if (!operand_map(&ma, GemmOperand{a.h, a.ld_h, false}, a.BT, a.d, kCtaRows))
+    return cudaErrorInvalidValue;
+  ListArgs l{a.V, a.K, a.values, a.ld_v, a.index, a.ld_i, a.rest, a.target, a.ignore_index,
+             w.words, w.teacher, nullptr, w.rows, a.lse, a.rest_lse, a.t_lse, a.sigma, a.grad_ce,
+             a.grad_tvd, a.grad_stride, a.dev_status};
+  list_kernel<true><<<static_cast<unsigned>(a.BT), kSortThreads, 0, st>>>(l);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const size_t ew = a.grad_w_kind == FCT_GEMM_BF16 ? 2 : 4;
+  for (int64_t v0 = 0; v0 < a.V; v0 += w.piece) {
+    const int64_t n = a.V - v0 < w.piece ? a.V - v0 : w.piece;
+    const uint16_t* wp = static_cast<const uint16_t*>(a.w) + v0 * a.ld_w;
+    CUtensorMap mb, mg;
+    // the gradient's rows are whole 16-byte units: columns n .. are written as 0
+    if (!operand_map(&mb, GemmOperand{wp, a.ld_w, false}, n, a.d, kCtaRows) ||
+        !make_c_map(&mg, w.G, a.BT, (n + 7) / 8 * 8, w.ld_g, true))
+      return cudaErrorInvalidValue;
+    TileArgs t{a.BT, n, a.d, v0, w.words, w.teacher, a.K, nullptr, nullptr, 0, w.listed,
+               w.tg_logit, w.rows, a.dev_status};
+    if ((e = run_tiles<true>(ma, mb, mg, t, sms, device, st)) != cudaSuccess) return e;
+    // d hidden (BT x d) += G (BT x n) W_piece (n x d)
+    if (a.grad_h != nullptr) {
+      const GemmOperand G{w.G, w.ld_g, false}, W{wp, a.ld_w, true};
+      if (n == a.V)
+        e = launch_gemm(G, W, a.grad_h, a.ld_gh, FCT_GEMM_BF16, a.BT, a.d, n, a.dev_status, sms,
+                        st, w.sum_bytes ? w.sum : nullptr, w.sum_bytes);
+      else
+        e = launch_gemm(G, W, w.sum, w.ld_sum, v0 == 0 ? FCT_GEMM_F32 : FCT_GEMM_ADD_F32, a.BT, a.d,
+                        n, a.dev_status, sms, st);
+      if (e != cudaSuccess) return e;
+    }
+    // d weight of the piece (n x d) = G^T (n x BT) h (BT x d)
+    if (a.grad_w != nullptr &&
+        (e = launch_gemm(GemmOperand{w.G, w.ld_g, true}, GemmOperand{a.h, a.ld_h, true},
+                         static_cast<char*>(a.grad_w) + size_t(v0) * size_t(a.ld_gw) * ew, a.ld_gw,
+                         a.grad_w_kind, n, a.d, a.BT, a.dev_status, sms, st)) != cudaSuccess)
+      return e;
+  }
+  if (a.grad_h != nullptr && w.piece < a.V) {
+    const int64_t blocks = (a.BT * ((a.d + 1) / 2) + 255) / 256;
+    const int64_t most = int64_t(sms) * 8;
+    round_kernel<<<static_cast<unsigned>(blocks < most ? blocks : most), 256, 0, st>>>(
+        w.sum, w.ld_sum, static_cast<uint16_t*>(a.grad_h), a.ld_gh, a.BT, a.d);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace fct

@@ -23,16 +23,16 @@ namespace fct {
 
 namespace {
 
+using top::Coefs;
+using top::list_sums;
+using top::listed_grad;
+using top::make_coefs;
+using top::prob;
+using top::Sums;
+
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;  // vectors of a row in flight per thread
-
-// ---------------------------------------------------------------- values
-
-// exp(x - l), the probability of a logit x under a log-sum-exp l held in fp32.
-// Every sign in both directions compares values of this function, so the
-// forward's sigma and the backward's signs agree whatever else is rounded.
-__device__ __forceinline__ float prob(float x, float l) { return ex2((x - l) * kLog2e); }
 
 // ---------------------------------------------------------------- rows
 
@@ -81,26 +81,6 @@ __device__ __forceinline__ float2 peer_state(const float2* mine, uint32_t rank) 
       : "r"(smem_addr(mine)), "r"(rank)
       : "memory");
   return v;
-}
-
-// What a row's gradient is made of.
-struct Coefs {
-  float gce, h;    // grad_ce, grad_tvd / 2
-  float lse, t_lse, sigma;
-  float outside;   // coefficient of p_v outside U
-  bool teacher;    // the list holds some probability
-};
-__device__ __forceinline__ Coefs make_coefs(float gce, float gtvd, float lse, float rest,
-                                            float t_lse, float t_rest, float sigma) {
-  Coefs c{gce, 0.5f * gtvd, lse, t_lse, sigma, gce, !(t_lse == -INFINITY)};
-  if (c.teacher) c.outside = fmaf(c.h, sgn_pq(prob(rest, lse), prob(t_rest, t_lse)) - sigma, gce);
-  return c;
-}
-// The gradient at a listed word with student logit s and teacher logit t.
-__device__ __forceinline__ float listed_grad(const Coefs& c, float s, float t, bool target) {
-  const float p = prob(s, c.lse);
-  const float k = c.teacher ? fmaf(c.h, sgn_pq(p, prob(t, c.t_lse)) - c.sigma, c.gce) : c.gce;
-  return target ? fmaf(p, k, -c.gce) : p * k;
 }
 
 template <int N>
@@ -182,67 +162,6 @@ __host__ __device__ constexpr int64_t bit_words(int64_t vecs, int vec) {
 // share's bits start on a byte.
 __host__ __device__ constexpr int64_t share(int64_t nvec, int C) {
   return ((nvec + C - 1) / C + 7) / 8 * 8;
-}
-
-struct Sums {  // of one row's list, held by every lane of a warp
-  float lse, rest, t_lse, tvd, sigma;
-};
-
-// The list's part of the loss, by one warp: (rest_m2, rest_s) is the student's
-// state outside U.
-__device__ Sums list_sums(const Shared& sh, int K, float rest_m2, float rest_s, float t_rest) {
-  const int lane = threadIdx.x & 31;
-  float ms = -INFINITY, mt = t_rest;
-  for (int k = lane; k < K; k += 32) {
-    ms = fmaxf(ms, sh.s[k]);
-    mt = fmaxf(mt, sh.t[k]);
-  }
-#pragma unroll
-  for (int m = 16; m >= 1; m >>= 1) {
-    ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, m));
-    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, m));
-  }
-  const float ms2 = fmaxf(ms * kLog2e, rest_m2), mt2 = mt * kLog2e;
-  const float ns = ms2 == -INFINITY ? 0.f : -ms2, nt = mt2 == -INFINITY ? 0.f : -mt2;
-  float us = 0.f, ut = 0.f;
-  for (int k = lane; k < K; k += 32) {
-    us += ex2(fmaf(sh.s[k], kLog2e, ns));
-    ut += ex2(fmaf(sh.t[k], kLog2e, nt));
-  }
-  us = warp_sum(us);
-  ut = warp_sum(ut);
-  const float rs = rest_s == 0.f ? 0.f : rest_s * ex2(rest_m2 + ns);
-  const float rt = ex2(fmaf(t_rest, kLog2e, nt));
-  const float zs = us + rs, zt = ut + rt;
-  Sums o;
-  o.lse = top::finish(ms2, zs);
-  o.rest = top::finish(rest_m2, rest_s);
-  o.t_lse = top::finish(mt2, zt);
-  if (o.t_lse == -INFINITY) {  // no teacher: cross-entropy alone
-    o.tvd = 0.f;
-    o.sigma = 0.f;
-    return o;
-  }
-  const float is = 1.f / zs, it = 1.f / zt;
-  float d = 0.f, g = 0.f;
-  for (int k = lane; k < K; k += 32) {
-    // (products rounded by themselves: equal p and q differ by 0)
-    const float p = __fmul_rn(ex2(fmaf(sh.s[k], kLog2e, ns)), is);
-    const float q = __fmul_rn(ex2(fmaf(sh.t[k], kLog2e, nt)), it);
-    d += fabsf(p - q);
-    g += p * sgn_pq(prob(sh.s[k], o.lse), prob(sh.t[k], o.t_lse));
-  }
-  d = warp_sum(d);
-  g = warp_sum(g);
-  // where both sides have most of their mass outside U, the difference of the
-  // two large numbers is that of the small ones inside
-  const float p = __fmul_rn(rs, is), q = __fmul_rn(rt, it);
-  const float gap = p > 0.5f && q > 0.5f ? __fmul_rn(us, is) - __fmul_rn(ut, it) : p - q;
-  o.tvd = 0.5f * (d + fabsf(gap));
-  o.sigma = fmaf(p, sgn_pq(prob(o.rest, o.lse), prob(t_rest, o.t_lse)), g);
-  // (a comparison with NaN gives the sign 0: a teacher's NaN is carried on here)
-  if (o.t_lse != o.t_lse) o.sigma = o.t_lse;
-  return o;
 }
 
 // One cluster of C CTAs per row, C fixed by V and the element type.  Each CTA
@@ -384,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, kGrad ? 2 : 3) top_forward_kernel(To
       const bool wrong = __any_sync(0xffffffffu, b != 0);
       const Lse2 rest = top::warp_merge(Lse2{s.x, s.y});
       const float t_rest = a.rest ? a.rest[row] : -INFINITY;
-      Sums o = list_sums(sh, K, rest.m2, rest.s, t_rest);
+      Sums o = list_sums(sh.s, sh.t, K, rest.m2, rest.s, t_rest);
       const float nan = __uint_as_float(0x7fc00000u);
       if (wrong) o = Sums{nan, nan, nan, nan, nan};
       if (tid == 0) {

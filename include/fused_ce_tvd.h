@@ -726,8 +726,11 @@ typedef struct {
  *   V            : at most 2^23, else FCT_ERR_UNSUPPORTED.
  * The forward reads the row once, the backward reads and writes it once, the
  * single launch reads and writes it once in memory (its second pass reads
- * from L2) and gives the bits of the two calls.  All decide sign(p - q) from
- * p = exp(s - student_lse) and q = exp(t - teacher_lse) in fp32.
+ * from L2) and gives the bits of the two calls.  The forward takes sign(p - q)
+ * from fp32 sums relative to the maxima, the backward from exp(s -
+ * student_lse) and exp(t - teacher_lse); where both are within their roundings
+ * of each other and p > 3/4, it takes the sign that sigma has (a student and a
+ * teacher sure of one word: the fp32 log-sum-exps do not hold 1 - p).
  */
 int fused_ce_tvd_top_forward(const void* student, int64_t ld_student,
                              fct_dtype dtype, const int64_t* target,
@@ -752,6 +755,88 @@ int fused_ce_tvd_top_forward_backward(
     int64_t grad_stride, float* ce, float* tvd, float* student_lse,
     float* student_rest, float* teacher_lse, float* sigma, void* grad_student,
     int64_t ld_grad, int32_t* dev_status, void* stream);
+
+/*
+ * The same loss, and cross-entropy alone, from hidden states and lm_head
+ * weights: logits = h w^T, which never exist as a whole.  The forward makes
+ * them a tile at a time and keeps each row's log-sum-exp states and the
+ * logits of its list and target.  The backward makes them again, a piece of
+ * the vocabulary at a time, as the bf16 gradient of that piece's logits; d
+ * hidden sums over the pieces, and d weight of a piece is complete with it.
+ * (The Liger-Kernel overview's fused linear cross-entropy goes through row
+ * blocks of logits; pieces of the vocabulary, the recomputation and the top
+ * lists are this library's.)  fused_linear_ce_tvd_forward_backward is the
+ * loss against a teacher model's own hidden states.
+ *
+ *   h (BT, d), w (V, d) : bf16, row strides ld_*; 16-byte aligned with ld_*
+ *                  multiples of 8 (TMA tile loads), else FCT_ERR_ALIGNMENT.
+ *   teacher      : a top list (its rules as above).
+ *   target, ignore_index, grad_ce, grad_tvd, grad_stride, ce ... sigma : as
+ *                  for fused_ce_tvd_top_forward and _backward;
+ *                  fused_linear_ce_* have ce, lse and grad_ce alone.
+ *   grad_h       : (BT, d) bf16 output, row stride ld_grad_h, or NULL.
+ *   grad_w       : (V, d) output, row stride ld_grad_w, or NULL; by
+ *                  grad_w_kind FCT_GEMM_BF16 (bf16, rounded once from fp32
+ *                  sums), FCT_GEMM_F32 (fp32) or FCT_GEMM_ADD_F32 (fp32,
+ *                  added to what it holds).  Anything else:
+ *                  FCT_ERR_UNSUPPORTED.
+ *   workspace    : device memory of the _workspace_size functions' bytes,
+ *                  256-byte aligned, clobbered; one per call in flight
+ *                  (captured graphs that may run at once need their own).
+ *   piece_cols   : words per piece of the backward, rounded up to a multiple
+ *                  of 256; 0: 2^28 / BT.  The workspace holds BT x piece_cols
+ *                  bf16 gradients and, if there are several pieces, (BT, d)
+ *                  fp32.  d weight does not depend on it; d hidden's sum
+ *                  over the vocabulary is grouped by it.
+ * BT, V, d and the row strides are at most 2^31 - 1024, else
+ * FCT_ERR_UNSUPPORTED.  K = 0 in the size functions: cross-entropy alone.
+ * Logits are sums in fp32 of partial sums of 512 products (which the tensor
+ * cores accumulate in fp32), the same in both directions.  The gradient of a
+ * logit is rounded to bf16 for the two products.  An ignored row gets a zero
+ * gradient; its hidden states enter d weight times zero, so they have to be
+ * finite.  A row that is NaN (a wrong target or list, not-finite logits)
+ * makes d weight NaN.  Repeated calls give the same bits.
+ */
+size_t fused_linear_ce_tvd_top_forward_workspace_size(int64_t BT, int64_t V,
+                                                      int64_t K);
+size_t fused_linear_ce_tvd_top_backward_workspace_size(int64_t BT, int64_t V,
+                                                       int64_t d, int64_t K,
+                                                       int64_t piece_cols);
+
+int fused_linear_ce_tvd_top_forward(
+    const void* h, int64_t ld_h, const void* w, int64_t ld_w, int64_t d,
+    const int64_t* target, const fct_top_list* teacher, int64_t BT, int64_t V,
+    int64_t ignore_index, float* ce, float* tvd, float* student_lse,
+    float* student_rest, float* teacher_lse, float* sigma, void* workspace,
+    size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+int fused_linear_ce_tvd_top_backward(
+    const void* h, int64_t ld_h, const void* w, int64_t ld_w, int64_t d,
+    const int64_t* target, const fct_top_list* teacher, int64_t BT, int64_t V,
+    int64_t ignore_index, const float* student_lse, const float* student_rest,
+    const float* teacher_lse, const float* sigma, const float* grad_ce,
+    const float* grad_tvd, int64_t grad_stride, void* grad_h,
+    int64_t ld_grad_h, void* grad_w, int64_t ld_grad_w, int32_t grad_w_kind,
+    void* workspace, size_t workspace_bytes, int64_t piece_cols,
+    int32_t* dev_status, void* stream);
+
+int fused_linear_ce_forward(const void* h, int64_t ld_h, const void* w,
+                            int64_t ld_w, int64_t d, const int64_t* target,
+                            int64_t BT, int64_t V, int64_t ignore_index,
+                            float* ce, float* lse, void* workspace,
+                            size_t workspace_bytes, int32_t* dev_status,
+                            void* stream);
+
+int fused_linear_ce_backward(const void* h, int64_t ld_h, const void* w,
+                             int64_t ld_w, int64_t d, const int64_t* target,
+                             int64_t BT, int64_t V, int64_t ignore_index,
+                             const float* lse, const float* grad_ce,
+                             int64_t grad_stride, void* grad_h,
+                             int64_t ld_grad_h, void* grad_w,
+                             int64_t ld_grad_w, int32_t grad_w_kind,
+                             void* workspace, size_t workspace_bytes,
+                             int64_t piece_cols, int32_t* dev_status,
+                             void* stream);
 
 /*
  * One step of speculative decoding with a distilled draft model.  The loss

@@ -188,6 +188,37 @@ def test_gradient_against_differences(dtype):
         assert abs((grad[r].double() * d).sum() - slope) <= tol
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_students_and_teachers_that_are_sure_of_one_word(dtype):
+    """1 - p below what fp32 log-sum-exps near 30 resolve: the gradient of tvd is still p (1 - p) and
+    the like, not p."""
+    rows, V, K = 40, 2000, 8
+    s, target, values, index, rest, gce, gtvd = tu.make(rows, V, K, dtype, 50)
+    for r in range(rows):
+        used = index[r] >= 0
+        word = int(index[r][used][0])
+        values[r][(index[r] == word)] = 35.0 + 0.37 * (r % 7)
+        s[r, word] = 32.0 + 0.5 * (r % 9)
+        if r % 3 == 0:      # the rest instead: the list is what hardly counts
+            s[r, word] = -3.0
+            values[r][used] = -12.0 - 0.5 * (r % 5)
+            s[r, index[r][used].long()] -= 14.0
+    gce = torch.zeros(rows)
+    stats, grad = all_ways(s, target, values, index, rest, gce, gtvd)
+    for r in range(rows):
+        if target[r] == tu.IGNORE:
+            continue
+        # |p (sign - sigma)| <= 2 (1 - p) for the word or the rest that p is near 1 of, 2 p elsewhere
+        p = torch.softmax(s[r].double(), 0)
+        used = index[r][index[r] >= 0].long()
+        p_rest = 1 - p[used].sum().item()
+        most = max(p.max().item(), p_rest)
+        left = p[used].sum().item() if p_rest == most else 1 - p.max().item()
+        assert most > 0.999
+        bound = 0.5 * abs(float(gtvd[r])) * 2 * (left + 2.0 ** -21)
+        assert grad[r].double().abs().max().item() <= bound, (r, most)
+
+
 def test_upstream_broadcast_split_and_repeated():
     s, target, values, index, rest, gce, gtvd = cuda(*tu.make(600, 5003, 40, torch.bfloat16, 6))
     one = binding.fused_ce_tvd_top_forward_backward(s, target, values, index, rest, 0.25, 0.5)

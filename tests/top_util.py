@@ -47,9 +47,9 @@ def _lse(x):
     return torch.logsumexp(x, 0).item() if x.numel() else -math.inf
 
 
-def row_ref(s, target, values, index, rest, gce=0.0, gtvd=0.0):
-    """The definition for one row of float64 logits.  Returns a dict with the statistics, the
-    gradient, and bounds of the error of each."""
+def row_ref(s, target, values, index, rest, gce=0.0, gtvd=0.0, err=0.0):
+    """The definition for one row of float64 logits, which the kernel may see up to ``err`` off.
+    Returns a dict with the statistics, the gradient, and bounds of the error of each."""
     V = s.numel()
     zero = torch.zeros(V, dtype=torch.float64)
     if target == IGNORE:
@@ -67,10 +67,11 @@ def row_ref(s, target, values, index, rest, gce=0.0, gtvd=0.0):
     p = torch.exp(s - lse)
     p_rest = math.exp(s_rest - lse)
     top_s, top_t = s.max().item(), t_all.max().item()
-    tol = dict(lse=lse_tol(lse, top_s, V), ce=lse_tol(lse, top_s, V) + U * abs(lse - s[target].item()),
-               rest=lse_tol(s_rest, s[~inside].max().item(), V) if s_rest > -math.inf else 0.0)
-    prob = 2.0 ** -21 + sum_error(V)                    # PROB
-    saved = prob + 2 * lse_tol(lse, top_s, V)           # exp(s - lse) with the rounded lse
+    tol = dict(lse=lse_tol(lse, top_s, V) + err,
+               ce=lse_tol(lse, top_s, V) + U * abs(lse - s[target].item()) + 2 * err,
+               rest=lse_tol(s_rest, s[~inside].max().item(), V) + err if s_rest > -math.inf else 0.0)
+    prob = 2.0 ** -21 + sum_error(V) + 2 * err          # PROB
+    saved = prob + 2 * lse_tol(lse, top_s, V) + 2 * err  # exp(s - lse) with the rounded lse
     if t_lse == -math.inf:
         side, sigma, tvd, flip, sigma_tol = zero, 0.0, 0.0, zero, 0.0
         tol |= dict(t_lse=0.0, tvd=0.0, sigma=0.0)
