@@ -278,7 +278,7 @@ cudaError_t launch_verify(const VerifyArgs& a, int sms, int device, cudaStream_t
 // fct_top_linear.cu; entry points in fct_top_api.cu).
 constexpr int kTopMax = FCT_TOP_MAX;              // longest list
 constexpr int64_t kTopMaxV = int64_t(1) << 23;    // largest vocabulary of the loss
-constexpr int kTopSmemMax = 200 * 1024;           // dynamic shared memory of its kernels
+constexpr int kStreamSmem = 222 * 1024;           // dynamic shared memory of an SM's CTAs
 
 struct TopSelectArgs {
   const void* logits;
@@ -292,7 +292,8 @@ struct TopSelectArgs {
   float* rest;
   int32_t* dev_status;
 };
-cudaError_t launch_top_select(const TopSelectArgs& a, int sms, int device, cudaStream_t st);
+cudaError_t launch_top_select(const TopSelectArgs& a, int sms, int device, int l2,
+                              cudaStream_t st);
 
 struct TopArgs {
   const void* student;

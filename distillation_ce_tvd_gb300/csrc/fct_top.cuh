@@ -1,4 +1,8 @@
-// Base-2 log-sum-exp states of the top-logits kernels.  Unlike the states of
+// What the top-logits kernels share.  Products that feed sums are rounded by
+// themselves (__fmul_rn) or fused by name (fmaf): a value is the same bits in
+// every kernel that computes it.
+//
+// Base-2 log-sum-exp states.  Unlike the states of
 // the dense loss they take rows with -inf entries anywhere (masked logits,
 // words that are left out): while a state has seen nothing finite its offset
 // is 0, so that -inf adds 0 and not NaN.  NaN and +inf stay visible as NaN.
@@ -9,19 +13,26 @@
 namespace fct {
 namespace top {
 
-// Folds a vector with maximum vm into a state.
+// A thread's running state: the largest logit, the exponents' offset -max log2 e
+// (0 while there is no finite one), and two partial sums.
+struct Run {
+  float mx, nm;
+  float2 s;
+};
+__device__ __forceinline__ Run run_empty() { return Run{-INFINITY, 0.f, make_float2(0.f, 0.f)}; }
+// Folds a vector with maximum vm.
 template <int N>
-__device__ __forceinline__ void fold(Lse2x& st, const float (&x)[N], float vm) {
+__device__ __forceinline__ void fold(Run& st, const float (&x)[N], float vm) {
   static_assert(N % 2 == 0, "pairs");
-  const float m2n = vm * kLog2e;
-  if (m2n > st.m2) {
-    const float sc = ex2(st.m2 - m2n);
+  if (vm > st.mx) {
+    const float nm = __fmul_rn(-vm, kLog2e);
+    const float sc = st.mx == -INFINITY ? 0.f : ex2(nm - st.nm);
     st.s.x *= sc;
     st.s.y *= sc;
-    st.m2 = m2n;
+    st.mx = vm;
+    st.nm = nm;
   }
-  const float nm = st.m2 == -INFINITY ? 0.f : -st.m2;
-  const float2 L2 = make_float2(kLog2e, kLog2e), n2 = make_float2(nm, nm);
+  const float2 L2 = make_float2(kLog2e, kLog2e), n2 = make_float2(st.nm, st.nm);
 #pragma unroll
   for (int j = 0; j < N; j += 2) {
     const float2 e = __ffma2_rn(make_float2(x[j], x[j + 1]), L2, n2);
@@ -29,24 +40,273 @@ __device__ __forceinline__ void fold(Lse2x& st, const float (&x)[N], float vm) {
   }
 }
 template <int N>
-__device__ __forceinline__ void fold(Lse2x& st, const float (&x)[N]) {
+__device__ __forceinline__ void fold(Run& st, const float (&x)[N]) {
   fold(st, x, vec_max(x));
+}
+__device__ __forceinline__ Lse2 folded(const Run& st) {
+  return Lse2{st.mx == -INFINITY ? -INFINITY : -st.nm, st.s.x + st.s.y};
 }
 
 // A state's sum relative to the maximum m (at least its own).  An empty state
 // has the sum 0; one of NaN alone has no maximum, and keeps its NaN.
 __device__ __forceinline__ float rescaled(Lse2 a, float m) {
-  return a.s == 0.f ? 0.f : a.m2 == -INFINITY ? a.s : a.s * ex2(a.m2 - m);
+  return a.s == 0.f ? 0.f : a.m2 == -INFINITY ? a.s : __fmul_rn(a.s, ex2(a.m2 - m));
 }
 __device__ __forceinline__ Lse2 merge(Lse2 a, Lse2 b) {
   const float m = fmaxf(a.m2, b.m2);
   return Lse2{m, rescaled(a, m) + rescaled(b, m)};
 }
-__device__ __forceinline__ Lse2 warp_merge(Lse2 a) {
+__device__ __forceinline__ Lse2 merge_warp(Lse2 a) {
   float m = a.m2;
 #pragma unroll
   for (int k = 16; k >= 1; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
   return Lse2{m, warp_sum(rescaled(a, m))};
+}
+
+// ---------------------------------------------------------------- clusters
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A 64-bit word of CTA `rank`'s shared memory, at the place that `mine` has here.
+__device__ __forceinline__ uint64_t peer_word(const uint64_t* mine, uint32_t rank) {
+  uint64_t v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
+      "ld.shared::cluster.u64 %0, [a];\n\t}"
+      : "=l"(v)
+      : "r"(smem_addr(mine)), "r"(rank)
+      : "memory");
+  return v;
+}
+// An arrival on CTA `rank`'s barrier at the place that `bar` has here.
+__device__ __forceinline__ void arrive_at(uint64_t* bar, uint32_t rank) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
+      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(rank)
+      : "memory");
+}
+
+// Waits (bounded, like mbar_wait) for a phase that arrivals of other CTAs
+// complete: what they wrote to their shared memory before is seen after.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const long long t0 = clock64();
+  for (uint32_t it = 0; it < (1u << 30); ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 q, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (*abort || clock64() - t0 > kWaitLimitCycles) break;
+  }
+  *abort = 1;
+  return false;
+}
+
+// ---------------------------------------------------------------- rows
+
+// A row of V elements as `head` elements before the first 16-byte boundary,
+// nvec vectors, and the rest from element tail0.  Element v has position
+// v - head + kVec: vector i starts at position (i + 1) kVec.
+template <typename T>
+struct Row {
+  const T* p;
+  int head, nvec, tail0, V;
+  __device__ __forceinline__ Row(const T* row, int V) : p(row), V(V) {
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));
+    constexpr int kVec = Elem<T>::kVec;
+    head = off ? min(kVec - off, V) : 0;
+    nvec = (V - head) / kVec;
+    tail0 = head + nvec * kVec;
+  }
+  __device__ __forceinline__ const uint4* vec(int i) const {
+    return reinterpret_cast<const uint4*>(p + head) + i;
+  }
+  // The j-th of the elements that are in no vector.
+  __device__ __forceinline__ int loose(int j) const { return j < head ? j : tail0 + (j - head); }
+  __device__ __forceinline__ int n_loose() const { return head + (V - tail0); }
+};
+
+// Vectors of a row that each of C CTAs takes: a multiple of eight.
+__host__ __device__ constexpr int64_t share(int64_t nvec, int C) {
+  return ((nvec + C - 1) / C + 7) / 8 * 8;
+}
+
+// ---------------------------------------------------------------- streaming rows
+
+// CTAs that stream rows have kRowThreads consumers and a warp that copies for
+// them (TMA bulk copies into a ring of shared memory).  That warp runs ahead,
+// into a row's second sweep and into the next row, so that copies are in
+// flight while the consumers look up lists, reduce and write results: with
+// loads of their own into registers, 64 KB in flight per SM only while
+// streaming, the single launch took 643 us at 1021 x 256000 fp32, half of the
+// memory's rate.  Barriers of the consumers are named (1): the copying warp
+// takes no part.
+constexpr int kRowThreads = 512;
+constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kStreamThreads = kRowThreads + 32;
+constexpr int kPerThread = 4;                              // vectors of a chunk per thread
+constexpr int kChunkVecs = kPerThread * kRowThreads;       // 32 KB
+constexpr int kMaxStages = 6;
+
+__device__ __forceinline__ void row_sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+__device__ __forceinline__ bool row_or(bool b) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, 512, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<int>(b))
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ int row_count(bool b) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "bar.red.popc.u32 %0, 1, 512, p;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<int>(b))
+      : "memory");
+  return r;
+}
+static_assert(kRowThreads == 512, "the barriers above");
+
+// The ring's barriers, in static shared memory.
+struct RingBars {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  int abort;
+};
+struct Ring {
+  RingBars* bars;
+  uint4* buf;  // stages x kChunkVecs, 16-byte aligned
+  int stages;
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ Ring(RingBars* b, uint4* p, int n) : bars(b), buf(p), stages(n) {}
+  // By one thread, before a __syncthreads.
+  __device__ __forceinline__ void init() {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], kRowWarps);
+    }
+    bars->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __device__ __forceinline__ void next() {
+    if (++slot == stages) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+  // Copying thread: vectors [v0, v1) of a row, a chunk at a time.  False if a
+  // wait ran out.
+  template <typename T>
+  __device__ __forceinline__ bool copy(const Row<T>& r, int v0, int v1, uint64_t pol) {
+    for (int c = v0; c < v1; c += kChunkVecs) {
+      if (!mbar_wait(&bars->empty[slot], phase ^ 1u, &bars->abort)) return false;
+      const uint32_t bytes = static_cast<uint32_t>(min(kChunkVecs, v1 - c)) * 16u;
+      mbar_arrive_expect_tx(&bars->full[slot], bytes);
+      asm volatile(
+          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+          " [%0], [%1], %2, [%3], %4;" ::"r"(smem_addr(buf + slot * kChunkVecs)),
+          "l"(__cvta_generic_to_global(r.vec(c))), "r"(bytes), "r"(smem_addr(&bars->full[slot])),
+          "l"(pol)
+          : "memory");
+      next();
+    }
+    return true;
+  }
+  // Copying thread, at the end: every copy has landed (bounded, even after an
+  // abort).  `copied` chunks in all.
+  __device__ __forceinline__ void drain(uint32_t copied) {
+    const uint32_t n = static_cast<uint32_t>(stages);
+    for (uint32_t i = copied > n ? copied - n : 0; i < copied; ++i)
+      mbar_wait(&bars->full[i % n], (i / n) & 1u, &bars->abort, false);
+  }
+  // Consumers: f(vector, its index, its place among a chunk's vectors of the
+  // thread) for vectors [v0, v1) of a row.
+  template <typename F>
+  __device__ __forceinline__ void each(int v0, int v1, F f) {
+    const int tid = threadIdx.x;
+    for (int c = v0; c < v1; c += kChunkVecs) {
+      mbar_wait(&bars->full[slot], phase, &bars->abort);
+      const uint4* p = buf + slot * kChunkVecs + tid;
+      if (c + kChunkVecs <= v1) {
+#pragma unroll
+        for (int u = 0; u < kPerThread; ++u) f(p[u * kRowThreads], c + u * kRowThreads + tid, u);
+      } else {
+#pragma unroll
+        for (int u = 0; u < kPerThread; ++u)
+          if (c + u * kRowThreads + tid < v1)
+            f(p[u * kRowThreads], c + u * kRowThreads + tid, u);
+      }
+      __syncwarp();
+      if ((tid & 31) == 0) mbar_arrive(&bars->empty[slot]);
+      next();
+    }
+  }
+};
+// Chunks of a share.
+__device__ __forceinline__ uint32_t chunks_of(int v0, int v1) {
+  return v1 > v0 ? static_cast<uint32_t>((v1 - v0 + kChunkVecs - 1) / kChunkVecs) : 0u;
+}
+
+// What CTAs of a cluster tell each other about a row: 16 bytes each, sent to
+// every CTA's slots, counted on its barrier.  Two turns alternate: a CTA sends
+// for row i + 2 after it has all of row i + 1, which the others sent after
+// they had taken theirs of row i.
+struct Exchange {
+  uint4 slot[2][8];
+  uint64_t bar[2];
+};
+__device__ __forceinline__ void exchange_init(Exchange& x) {
+  mbar_init(&x.bar[0], 1);
+  mbar_init(&x.bar[1], 1);
+}
+// By one warp of each CTA; `mine` counts from lane 0.
+__device__ __forceinline__ void exchange_send(Exchange& x, uint32_t turn, int C, int rank,
+                                              uint4 mine) {
+  const int lane = threadIdx.x & 31;
+  mine.x = __shfl_sync(0xffffffffu, mine.x, 0);
+  mine.y = __shfl_sync(0xffffffffu, mine.y, 0);
+  mine.z = __shfl_sync(0xffffffffu, mine.z, 0);
+  mine.w = __shfl_sync(0xffffffffu, mine.w, 0);
+  if (lane == 0) mbar_arrive_expect_tx(&x.bar[turn & 1u], static_cast<uint32_t>(C) * 16u);
+  __syncwarp();
+  if (lane < C) {
+    asm volatile(
+        "{\n\t.reg .b32 dst, bar;\n\t"
+        "mapa.shared::cluster.u32 dst, %0, %2;\n\t"
+        "mapa.shared::cluster.u32 bar, %1, %2;\n\t"
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [dst], {%3, %4, %5, %6}, "
+        "[bar];\n\t}" ::"r"(smem_addr(&x.slot[turn & 1u][rank])),
+        "r"(smem_addr(&x.bar[turn & 1u])), "r"(lane), "r"(mine.x), "r"(mine.y), "r"(mine.z),
+        "r"(mine.w)
+        : "memory");
+  }
+}
+// The other end: lane i < C has CTA i's.
+__device__ __forceinline__ uint4 exchange_take(Exchange& x, uint32_t turn, int C, int* abort) {
+  mbar_wait(&x.bar[turn & 1u], (turn >> 1) & 1u, abort);
+  const int lane = threadIdx.x & 31;
+  return lane < C ? x.slot[turn & 1u][lane] : make_uint4(0xff800000u, 0u, 0u, 0u);
 }
 
 // Natural log-sum-exp of a state, rounded once: the maximum and the
@@ -89,12 +349,16 @@ struct Coefs {
 };
 __device__ __forceinline__ Coefs make_coefs(float gce, float gtvd, float lse, float rest,
                                             float t_lse, float t_rest, float sigma) {
-  const float doubt = (fabsf(lse) + fabsf(t_lse)) * 1.1920929e-07f;  // twice the half steps
+  const float doubt = __fmul_rn(fabsf(lse) + fabsf(t_lse), 1.1920929e-07f);  // twice the half steps
   Coefs c{gce, 0.5f * gtvd, lse, t_lse, sigma, doubt, gce, !(t_lse == -INFINITY)};
   if (c.teacher)
-    c.outside = fmaf(c.h, sign_of(rest, lse, t_rest, t_lse, doubt + fabsf(rest) * 1.1920929e-07f,
+    c.outside = fmaf(c.h, sign_of(rest, lse, t_rest, t_lse, fmaf(fabsf(rest), 1.1920929e-07f, doubt),
                                   sigma) - sigma, gce);
   return c;
+}
+// The gradient at the target, with student logit s, where it is not listed.
+__device__ __forceinline__ float target_grad(const Coefs& c, float s) {
+  return fmaf(prob(s, c.lse), c.outside, -c.gce);
 }
 // The gradient at a listed word with student logit s and teacher logit t.
 __device__ __forceinline__ float listed_grad(const Coefs& c, float s, float t, bool target) {
@@ -125,7 +389,7 @@ static __device__ Sums list_sums(const float* s, const float* t, int K, float re
     ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, m));
     mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, m));
   }
-  const float ms2 = fmaxf(ms * kLog2e, rest_m2), mt2 = mt * kLog2e;
+  const float ms2 = fmaxf(__fmul_rn(ms, kLog2e), rest_m2), mt2 = __fmul_rn(mt, kLog2e);
   const float ns = ms2 == -INFINITY ? 0.f : -ms2, nt = mt2 == -INFINITY ? 0.f : -mt2;
   float us = 0.f, ut = 0.f;
   for (int k = lane; k < K; k += 32) {
@@ -134,7 +398,7 @@ static __device__ Sums list_sums(const float* s, const float* t, int K, float re
   }
   us = warp_sum(us);
   ut = warp_sum(ut);
-  const float rs = rest_s == 0.f ? 0.f : rest_s * ex2(rest_m2 + ns);
+  const float rs = rest_s == 0.f ? 0.f : __fmul_rn(rest_s, ex2(rest_m2 + ns));
   const float rt = ex2(fmaf(t_rest, kLog2e, nt));
   const float zs = us + rs, zt = ut + rt;
   Sums o;
@@ -153,7 +417,7 @@ static __device__ Sums list_sums(const float* s, const float* t, int K, float re
     const float p = __fmul_rn(ex2(fmaf(s[k], kLog2e, ns)), is);
     const float q = __fmul_rn(ex2(fmaf(t[k], kLog2e, nt)), it);
     d += fabsf(p - q);
-    g += p * sgn_pq(p, q);
+    g = fmaf(p, sgn_pq(p, q), g);
   }
   d = warp_sum(d);
   g = warp_sum(g);

@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         bit == here_bit);
                 ++at;
               } else {
-                grad = fmaf(top::prob(a.tg_logit[row], rc.c.lse), rc.c.outside, -rc.c.gce);
+                grad = top::target_grad(rc.c, a.tg_logit[row]);
               }
               const int in = g * 64 + (__ffs(static_cast<int>(todo)) - 1) * 2;  // byte in the row
               const uint32_t addr = buf + uint32_t(lane) * 128u +
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kSortThreads) merge_kernel(MergeArgs a) {
     const float2 p = a.part[row * a.parts + i];
     st = top::merge(st, Lse2{p.x, p.y});
   }
-  st = top::warp_merge(st);
+  st = top::merge_warp(st);
   if ((tid & 31) == 0) state[tid >> 5] = make_float2(st.m2, st.s);
   for (int k = tid; k < K; k += kSortThreads) {
     const bool used = a.words[row * a.K + k] != INT_MAX;
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kSortThreads) merge_kernel(MergeArgs a) {
   __syncthreads();
   if (tid >= 32) return;
   const float2 w = tid < kSortThreads / 32 ? state[tid] : make_float2(-INFINITY, 0.f);
-  const Lse2 r = top::warp_merge(Lse2{w.x, w.y});
+  const Lse2 r = top::merge_warp(Lse2{w.x, w.y});
   const float t_rest = a.rest ? a.rest[row] : -INFINITY;
   top::Sums o = top::list_sums(s, t, K, r.m2, r.s, t_rest);
   const float nan = __uint_as_float(0x7fc00000u);

@@ -23,123 +23,90 @@ namespace fct {
 
 namespace {
 
-using top::Coefs;
-using top::list_sums;
-using top::listed_grad;
-using top::make_coefs;
-using top::prob;
-using top::Sums;
-
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;  // vectors of a row in flight per thread
+using namespace top;
 
 // ---------------------------------------------------------------- rows
 
-// A row of V elements as `head` elements before the first 16-byte boundary,
-// nvec vectors, and the rest from element tail0.  Element v has position
-// v - head + kVec: vector i starts at position (i + 1) kVec.
-template <typename T>
-struct Row {
-  const T* p;
-  int head, nvec, tail0, V;
-  __device__ __forceinline__ Row(const T* row, int V) : p(row), V(V) {
-    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));
-    constexpr int kVec = Elem<T>::kVec;
-    head = off ? min(kVec - off, V) : 0;
-    nvec = (V - head) / kVec;
-    tail0 = head + nvec * kVec;
+// U vectors per thread of a row, NT apart, from vector i.
+template <int NT, int U, typename T>
+__device__ __forceinline__ void load(const Row<T>& r, int i, int v1, uint64_t pol, uint4 (&raw)[U]) {
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (i + u * NT < v1) raw[u] = ld16(r.vec(i + u * NT), pol);
+}
+template <int NT, int U, typename F>
+__device__ __forceinline__ void each(int i, int v1, const uint4 (&raw)[U], F f) {
+  if (i + (U - 1) * NT < v1) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) f(raw[u], i + u * NT);
+  } else {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i + u * NT < v1) f(raw[u], i + u * NT);
   }
-  __device__ __forceinline__ const uint4* vec(int i) const {
-    return reinterpret_cast<const uint4*>(p + head) + i;
+}
+
+// The gradient outside U as a function of the logit: 2^(x log2 e + offset)
+// factor.  offset is -lse log2 e rounded, and the factor has what that lost:
+// the exponent is one FMA, and the only rounding in it is that of its value.
+struct Outside {
+  float offset, factor;
+  __device__ __forceinline__ explicit Outside(const Coefs& c) {
+    offset = -__fmul_rn(c.lse, kLog2e);
+    factor = __fmul_rn(c.outside, ex2(-fmaf(c.lse, kLog2e, offset)));
   }
-  // The j-th of the elements that are in no vector.
-  __device__ __forceinline__ int loose(int j) const { return j < head ? j : tail0 + (j - head); }
-  __device__ __forceinline__ int n_loose() const { return head + (V - tail0); }
 };
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float2 peer_state(const float2* mine, uint32_t rank) {
-  float2 v;
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\t"
-      "ld.shared::cluster.v2.f32 {%0, %1}, [a];\n\t}"
-      : "=f"(v.x), "=f"(v.y)
-      : "r"(smem_addr(mine)), "r"(rank)
-      : "memory");
-  return v;
-}
-
 template <int N>
-__device__ __forceinline__ void outside_grad(const Coefs& c, const float (&x)[N], int off,
-                                             float (&g)[N]) {
-  const float2 nl = make_float2(-c.lse, -c.lse), L2 = make_float2(kLog2e, kLog2e);
+__device__ __forceinline__ void outside_grad(const Outside& o, const float (&x)[N], float (&g)[N]) {
+  const float2 L2 = make_float2(kLog2e, kLog2e), n2 = make_float2(o.offset, o.offset);
+  const float2 f2 = make_float2(o.factor, o.factor);
 #pragma unroll
   for (int j = 0; j < N; j += 2) {
-    const float2 e = __fmul2_rn(__fadd2_rn(make_float2(x[j], x[j + 1]), nl), L2);
-    g[j] = ex2(e.x) * c.outside;
-    g[j + 1] = ex2(e.y) * c.outside;
-  }
-  if (static_cast<uint32_t>(off) < uint32_t(N)) {  // the target is in this vector
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (j == off) g[j] = fmaf(prob(x[j], c.lse), c.outside, -c.gce);
+    const float2 e = __ffma2_rn(make_float2(x[j], x[j + 1]), L2, n2);
+    const float2 v = __fmul2_rn(make_float2(ex2(e.x), ex2(e.y)), f2);
+    g[j] = v.x;
+    g[j + 1] = v.y;
   }
 }
 
-// Vectors [v0, v1) of a row's gradient outside U, by all threads, and the
-// elements in no vector: the head's and the tail's where asked for.
+// A vector's gradient as if none of its words were listed or the target.
+// `same`: the gradient's rows have the alignment of the student's.
 template <typename T>
-__device__ __forceinline__ void stream_grad(const Row<T>& r, T* grow, const Coefs& c, int target,
-                                            int v0, int v1, bool head, bool tail, uint64_t pol) {
+__device__ __forceinline__ void vector_grad(const Outside& o, uint4 w, T* to, bool same,
+                                            uint64_t pol) {
   constexpr int VE = Elem<T>::kVec;
-  const int tid = threadIdx.x;
-  const bool same = (reinterpret_cast<uintptr_t>(r.p) % 16) == (reinterpret_cast<uintptr_t>(grow) % 16);
-  for (int i = v0 + tid; i < v1; i += kUnroll * kThreads) {
-    uint4 raw[kUnroll];
+  float x[VE], g[VE];
+  Elem<T>::unpack(w, x);
+  outside_grad(o, x, g);
+  if (same) {
+    st16(to, Elem<T>::pack(g), pol);
+  } else {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (i + u * kThreads < v1) raw[u] = ld16(r.vec(i + u * kThreads), pol);
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int iv = i + u * kThreads;
-      if (iv >= v1) break;
-      float x[VE], g[VE];
-      Elem<T>::unpack(raw[u], x);
-      const int e0 = r.head + iv * VE;
-      outside_grad(c, x, target - e0, g);
-      if (same) {
-        st16(grow + e0, Elem<T>::pack(g), pol);
-      } else {
-#pragma unroll
-        for (int j = 0; j < VE; ++j) Elem<T>::store1(grow + e0 + j, g[j]);
-      }
-    }
+    for (int j = 0; j < VE; ++j) Elem<T>::store1(to + j, g[j]);
   }
+}
+template <typename T>
+__device__ __forceinline__ bool same_alignment(const T* a, const T* b) {
+  return reinterpret_cast<uintptr_t>(a) % 16 == reinterpret_cast<uintptr_t>(b) % 16;
+}
+// The same for the elements in no vector, the head's and the tail's where asked for.
+template <typename T>
+__device__ __forceinline__ void loose_grad(const Row<T>& r, T* grow, const Outside& o, bool head,
+                                           bool tail) {
+  const int tid = threadIdx.x;
   if (tid < r.n_loose() && (tid < r.head ? head : tail)) {
     const int v = r.loose(tid);
-    const float p = prob(Elem<T>::load1(r.p + v), c.lse);
-    Elem<T>::store1(grow + v, v == target ? fmaf(p, c.outside, -c.gce) : p * c.outside);
+    const float x[2] = {Elem<T>::load1(r.p + v), 0.f};
+    float g[2];
+    outside_grad(o, x, g);
+    Elem<T>::store1(grow + v, g[0]);
   }
 }
 
 // A gradient row, or its part [v0, v1), set to one value.
-template <typename T>
+template <int NT, typename T>
 __device__ __forceinline__ void fill_grad(T* grow, int64_t v0, int64_t v1, float value) {
-  for (int64_t v = v0 + threadIdx.x; v < v1; v += kThreads) Elem<T>::store1(grow + v, value);
+  for (int64_t v = v0 + threadIdx.x; v < v1; v += NT) Elem<T>::store1(grow + v, value);
 }
 
 // ---------------------------------------------------------------- forward
@@ -158,97 +125,120 @@ __host__ __device__ constexpr int64_t bit_words(int64_t vecs, int vec) {
   return ((vecs + 2) * vec + 31) / 32 + 1;
 }
 
-// Vectors of a row that each of C CTAs takes: a multiple of eight, so that a
-// share's bits start on a byte.
-__host__ __device__ constexpr int64_t share(int64_t nvec, int C) {
-  return ((nvec + C - 1) / C + 7) / 8 * 8;
-}
-
 // One cluster of C CTAs per row, C fixed by V and the element type.  Each CTA
-// streams its share of the row; every CTA then has the row's sums (the
-// forward alone: CTA 0) from its peers' shared memory.
+// streams its share of the row; every CTA then has the row's sums (the forward
+// alone: CTA 0) from what its peers sent.
 //
 // kGrad: the same CTAs go over their share once more, which L2 still holds,
 // and write the gradient.
 template <typename T, bool kGrad>
-__global__ void __launch_bounds__(kThreads, kGrad ? 2 : 3) top_forward_kernel(TopArgs a, int words) {
-  constexpr int VE = Elem<T>::kVec;
-  extern __shared__ uint32_t top_smem[];
-  __shared__ float2 warp_state[kWarps];
-  __shared__ float2 cta_state[2];
-  __shared__ int bad_flag[2];
+__global__ void __launch_bounds__(kStreamThreads, 2)
+    top_forward_kernel(TopArgs a, int words, int stages) {
+  constexpr int VE = Elem<T>::kVec, NT = kRowThreads;
+  extern __shared__ uint4 top_smem[];
+  __shared__ __align__(8) RingBars bars;
+  __shared__ __align__(16) Exchange exchange;
+  __shared__ float2 warp_state[kRowWarps];
   __shared__ Sums sums;
   const int K = static_cast<int>(a.K), V = static_cast<int>(a.V), tid = threadIdx.x;
   const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
-  const Shared sh{top_smem, reinterpret_cast<float*>(top_smem + words),
-                  reinterpret_cast<float*>(top_smem + words) + K,
-                  reinterpret_cast<int*>(top_smem + words) + 2 * K};
+  uint32_t* lists = reinterpret_cast<uint32_t*>(top_smem + stages * kChunkVecs);
+  const Shared sh{lists, reinterpret_cast<float*>(lists + words),
+                  reinterpret_cast<float*>(lists + words) + K,
+                  reinterpret_cast<int*>(lists + words) + 2 * K};
   const uint8_t* bytes = reinterpret_cast<const uint8_t*>(sh.bits);
-  const uint64_t once = policy_evict_first(), again = policy_evict_last();
-  for (int i = tid; i < words; i += kThreads) sh.bits[i] = 0;
+  Ring ring(&bars, top_smem, stages);
+  if (tid == 0) {
+    exchange_init(exchange);
+    ring.init();
+  }
+  for (int i = tid; i < words; i += kStreamThreads) sh.bits[i] = 0;
   __syncthreads();
+  cluster_barrier();  // every CTA's barriers exist
   const int64_t n_clusters = gridDim.x / C;
-  int turn = 0;
-  for (int64_t row = blockIdx.x / C; row < a.BT; row += n_clusters) {
-    const T* srow = static_cast<const T*>(a.student) + row * a.ld_s;
-    const Row<T> r(srow, V);
+  auto share_of = [&](const Row<T>& r, int* v0, int* v1) {
     const int per = static_cast<int>(share(r.nvec, C));
-    const int v0 = min(rank * per, r.nvec), v1 = min(v0 + per, r.nvec);
-    const int64_t tg = a.target[row];
-    T* grow = kGrad ? static_cast<T*>(a.grad) + row * a.ld_g : nullptr;
-    if (tg == a.ignore_index) {
-      if (rank == 0 && tid == 0) {
-        a.ce[row] = 0.f;
-        a.tvd[row] = 0.f;
-        a.lse[row] = 0.f;
-        a.rest_lse[row] = 0.f;
-        a.t_lse[row] = 0.f;
-        a.sigma[row] = 0.f;
-      }
-      if constexpr (kGrad) {
-        const int64_t per_cta = (a.V + C - 1) / C;
-        fill_grad(grow, rank * per_cta, min(a.V, (rank + 1) * per_cta), 0.f);
-      }
-      continue;
-    }
-    const bool tg_ok = tg >= 0 && tg < V;
-    // ---- the list: its logits, and the bits of the words in this CTA's share
-    bool bad = false;
-    for (int k = tid; k < K; k += kThreads) {
-      const int v = a.index[row * a.ld_i + k];
-      float s = -INFINITY, t = -INFINITY;
-      int at = -1;
-      if (v != -1) {
-        if (v < 0 || v >= V) {
-          bad = true;
-        } else {
-          at = v;
-          s = Elem<T>::load1(srow + v);
-          t = a.values[row * a.ld_v + k];
-          const int pos = v - r.head + VE - v0 * VE;
-          const bool mine = (pos >= VE || rank == 0) && (pos < (v1 - v0 + 1) * VE || rank == C - 1);
-          if (mine && (atomicOr(&sh.bits[pos >> 5], 1u << (pos & 31)) >> (pos & 31) & 1u)) bad = true;
+    *v0 = min(rank * per, r.nvec);
+    *v1 = min(*v0 + per, r.nvec);
+  };
+
+  if (tid >= NT) {
+    if (tid == NT) {  // ---- copies
+      const uint64_t once = policy_evict_first(), first = kGrad ? policy_evict_last() : once;
+      uint32_t copied = 0;
+      for (int64_t row = blockIdx.x / C; row < a.BT; row += n_clusters) {
+        const int64_t tg = a.target[row];
+        if (tg == a.ignore_index) continue;
+        const Row<T> r(static_cast<const T*>(a.student) + row * a.ld_s, V);
+        int v0, v1;
+        share_of(r, &v0, &v1);
+        if (!ring.copy(r, v0, v1, first)) break;
+        copied += chunks_of(v0, v1);
+        if (kGrad && tg >= 0 && tg < V) {
+          if (!ring.copy(r, v0, v1, once)) break;
+          copied += chunks_of(v0, v1);
         }
       }
-      sh.s[k] = s;
-      sh.t[k] = t;
-      sh.idx[k] = at;
+      ring.drain(copied);
     }
-    const float tg_logit = tg_ok ? Elem<T>::load1(srow + tg) : 0.f;
-    const int any_bad = __syncthreads_or(bad);
-    // ---- the log-sum-exp of the words outside U
-    Lse2x st = lse2x_empty();
-    for (int i = v0 + tid; i < v1; i += kUnroll * kThreads) {
-      uint4 raw[kUnroll];
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-        if (i + u * kThreads < v1) raw[u] = ld16(r.vec(i + u * kThreads), kGrad ? again : once);
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int iv = i + u * kThreads;
-        if (iv >= v1) break;
+  } else {
+    const uint64_t once = policy_evict_first();
+    uint32_t turn = 0;
+    for (int64_t row = blockIdx.x / C; row < a.BT; row += n_clusters) {
+      const T* srow = static_cast<const T*>(a.student) + row * a.ld_s;
+      const int64_t tg = a.target[row];
+      T* grow = kGrad ? static_cast<T*>(a.grad) + row * a.ld_g : nullptr;
+      if (tg == a.ignore_index) {
+        if (rank == 0 && tid == 0) {
+          a.ce[row] = 0.f;
+          a.tvd[row] = 0.f;
+          a.lse[row] = 0.f;
+          a.rest_lse[row] = 0.f;
+          a.t_lse[row] = 0.f;
+          a.sigma[row] = 0.f;
+        }
+        if constexpr (kGrad) {
+          const int64_t per_cta = (a.V + C - 1) / C;
+          fill_grad<NT>(grow, rank * per_cta, min(a.V, (rank + 1) * per_cta), 0.f);
+        }
+        continue;
+      }
+      const Row<T> r(srow, V);
+      int v0, v1;
+      share_of(r, &v0, &v1);
+      const bool tg_ok = tg >= 0 && tg < V;
+      // ---- the list: its logits, and the bits of the words in this CTA's share
+      auto mine = [&](int pos) {
+        return (pos >= VE || rank == 0) && (pos < (v1 - v0 + 1) * VE || rank == C - 1);
+      };
+      bool bad = false;
+      for (int k = tid; k < K; k += NT) {
+        const int v = a.index[row * a.ld_i + k];
+        float s = -INFINITY, t = -INFINITY;
+        int at = -1;
+        if (v != -1) {
+          if (v < 0 || v >= V) {
+            bad = true;
+          } else {
+            at = v;
+            s = Elem<T>::load1(srow + v);
+            t = a.values[row * a.ld_v + k];
+            const int pos = v - r.head + VE - v0 * VE;
+            if (mine(pos) && (atomicOr(&sh.bits[pos >> 5], 1u << (pos & 31)) >> (pos & 31) & 1u))
+              bad = true;
+          }
+        }
+        sh.s[k] = s;
+        sh.t[k] = t;
+        sh.idx[k] = at;
+      }
+      const float tg_logit = tg_ok ? Elem<T>::load1(srow + tg) : 0.f;
+      bad = row_or(bad);
+      // ---- the log-sum-exp of the words outside U
+      Run st = run_empty();
+      ring.each(v0, v1, [&](uint4 w, int iv, int) {
         float x[VE];
-        Elem<T>::unpack(raw[u], x);
+        Elem<T>::unpack(w, x);
         const int pos = (iv - v0 + 1) * VE;
         const uint32_t m = VE == 8 ? bytes[pos >> 3] : (bytes[pos >> 3] >> (pos & 4)) & 15u;
         if (m) {
@@ -256,110 +246,108 @@ __global__ void __launch_bounds__(kThreads, kGrad ? 2 : 3) top_forward_kernel(To
           for (int j = 0; j < VE; ++j)
             if ((m >> j) & 1u) x[j] = -INFINITY;
         }
-        top::fold(st, x);
+        fold(st, x);
+      });
+      // the elements in no vector: the head with CTA 0, the tail with the last
+      if (tid < r.n_loose() && rank == (tid < r.head ? 0 : C - 1)) {
+        const int v = r.loose(tid), pos = v - r.head + VE - v0 * VE;
+        const float x = Elem<T>::load1(srow + v);
+        const float one[2] = {(sh.bits[pos >> 5] >> (pos & 31)) & 1u ? -INFINITY : x, -INFINITY};
+        fold(st, one);
       }
-    }
-    // the elements in no vector: the head with CTA 0, the tail with the last
-    if (tid < r.n_loose() && rank == (tid < r.head ? 0 : C - 1)) {
-      const int v = r.loose(tid), pos = v - r.head + VE - v0 * VE;
-      const float x = Elem<T>::load1(srow + v);
-      const float one[2] = {(sh.bits[pos >> 5] >> (pos & 31)) & 1u ? -INFINITY : x, -INFINITY};
-      top::fold(st, one);
-    }
-    const Lse2 w = top::warp_merge(lse2x_fold(st));
-    if ((tid & 31) == 0) warp_state[tid >> 5] = make_float2(w.m2, w.s);
-    __syncthreads();
-    // the bits go back to 0 for the next row
-    for (int k = tid; k < K; k += kThreads) {
-      const int pos = sh.idx[k] - r.head + VE - v0 * VE;
-      if (sh.idx[k] >= 0 && pos >= 0 && pos < words * 32) sh.bits[pos >> 5] = 0;
-    }
-    if (tid < 32) {
-      const float2 mine = tid < kWarps ? warp_state[tid] : make_float2(-INFINITY, 0.f);
-      const Lse2 b = top::warp_merge(Lse2{mine.x, mine.y});
-      if (tid == 0) {
-        cta_state[turn] = make_float2(b.m2, b.s);
-        bad_flag[turn] = any_bad;
+      const Lse2 w = merge_warp(folded(st));
+      if ((tid & 31) == 0) warp_state[tid >> 5] = make_float2(w.m2, w.s);
+      row_sync();
+      // the bits go back to 0 for the next row
+      for (int k = tid; k < K; k += NT) {
+        const int pos = sh.idx[k] - r.head + VE - v0 * VE;
+        if (sh.idx[k] >= 0 && pos >= 0 && pos < words * 32) sh.bits[pos >> 5] = 0;
       }
-    }
-    if (C > 1)
-      cluster_barrier();  // the states of this turn; those of the last one have been read
-    if (tid < 32 && (kGrad || rank == 0)) {
-      __syncwarp();
-      float2 s = make_float2(-INFINITY, 0.f);
-      int b = 0;
-      if (tid < C) {
-        s = C > 1 ? peer_state(&cta_state[turn], tid) : cta_state[turn];
-        if (C > 1)
-          asm volatile(
-              "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
-              "ld.shared::cluster.s32 %0, [a];\n\t}"
-              : "=r"(b)
-              : "r"(smem_addr(&bad_flag[turn])), "r"(tid)
-              : "memory");
-        else
-          b = bad_flag[turn];
-      }
-      const bool wrong = __any_sync(0xffffffffu, b != 0);
-      const Lse2 rest = top::warp_merge(Lse2{s.x, s.y});
-      const float t_rest = a.rest ? a.rest[row] : -INFINITY;
-      Sums o = list_sums(sh.s, sh.t, K, rest.m2, rest.s, t_rest);
-      const float nan = __uint_as_float(0x7fc00000u);
-      if (wrong) o = Sums{nan, nan, nan, nan, nan};
-      if (tid == 0) {
-        if (rank == 0) {
-          a.ce[row] = tg_ok ? o.lse - tg_logit : nan;
-          a.tvd[row] = o.tvd;
-          a.lse[row] = o.lse;
-          a.rest_lse[row] = o.rest;
-          a.t_lse[row] = o.t_lse;
-          a.sigma[row] = o.sigma;
-          const int status = (tg_ok ? 0 : FCT_DEV_TARGET_OUT_OF_RANGE) | (wrong ? FCT_DEV_BAD_LIST : 0);
-          if (status && a.dev_status) atomicOr(a.dev_status, status);
+      if (tid < 32) {
+        const float2 own = tid < kRowWarps ? warp_state[tid] : make_float2(-INFINITY, 0.f);
+        Lse2 rest = merge_warp(Lse2{own.x, own.y});
+        bool wrong = bad;
+        if (C > 1) {
+          exchange_send(exchange, turn, C, rank,
+                        make_uint4(__float_as_uint(rest.m2), __float_as_uint(rest.s), bad, 0u));
+          const uint4 got = exchange_take(exchange, turn, C, &bars.abort);
+          wrong = __any_sync(0xffffffffu, got.z != 0);
+          rest = merge_warp(Lse2{__uint_as_float(got.x), __uint_as_float(got.y)});
         }
-        if constexpr (kGrad) sums = o;
+        if (kGrad || rank == 0) {
+          const float t_rest = a.rest ? a.rest[row] : -INFINITY;
+          Sums o = list_sums(sh.s, sh.t, K, rest.m2, rest.s, t_rest);
+          const float nan = __uint_as_float(0x7fc00000u);
+          if (wrong) o = Sums{nan, nan, nan, nan, nan};
+          if (tid == 0) {
+            if (rank == 0) {
+              a.ce[row] = tg_ok ? o.lse - tg_logit : nan;
+              a.tvd[row] = o.tvd;
+              a.lse[row] = o.lse;
+              a.rest_lse[row] = o.rest;
+              a.t_lse[row] = o.t_lse;
+              a.sigma[row] = o.sigma;
+              const int status =
+                  (tg_ok ? 0 : FCT_DEV_TARGET_OUT_OF_RANGE) | (wrong ? FCT_DEV_BAD_LIST : 0);
+              if (status && a.dev_status) atomicOr(a.dev_status, status);
+            }
+            if constexpr (kGrad) sums = o;
+          }
+        }
       }
-    }
-    turn ^= 1;
-    __syncthreads();
-    if constexpr (kGrad) {
-      if (!tg_ok) {
-        const int64_t per_cta = (a.V + C - 1) / C;
-        fill_grad(grow, rank * per_cta, min(a.V, (rank + 1) * per_cta),
-                  __uint_as_float(0x7fc00000u));
-        __syncthreads();
-        continue;
+      ++turn;
+      row_sync();
+      if constexpr (kGrad) {
+        if (!tg_ok) {
+          const int64_t per_cta = (a.V + C - 1) / C;
+          fill_grad<NT>(grow, rank * per_cta, min(a.V, (rank + 1) * per_cta),
+                        __uint_as_float(0x7fc00000u));
+          row_sync();
+          continue;
+        }
+        const Coefs c = make_coefs(a.grad_ce[row * a.grad_stride], a.grad_tvd[row * a.grad_stride],
+                                   sums.lse, sums.rest, sums.t_lse,
+                                   a.rest ? a.rest[row] : -INFINITY, sums.sigma);
+        const Outside o(c);
+        const bool same = same_alignment(srow, grow);
+        ring.each(v0, v1, [&](uint4 w, int iv, int) {
+          vector_grad(o, w, grow + r.head + iv * VE, same, once);
+        });
+        loose_grad(r, grow, o, rank == 0, rank == C - 1);
+        // the words of U and the target over what was written there
+        bool listed = false;
+        for (int k = tid; k < K; k += NT) listed = listed || sh.idx[k] == tg;
+        listed = row_or(listed);
+        for (int k = tid; k < K; k += NT) {
+          const int v = sh.idx[k];
+          if (v >= 0 && mine(v - r.head + VE - v0 * VE))
+            Elem<T>::store1(grow + v, listed_grad(c, sh.s[k], sh.t[k], v == tg));
+        }
+        const int at = static_cast<int>(tg);
+        if (tid == 0 && !listed && mine(at - r.head + VE - v0 * VE))
+          Elem<T>::store1(grow + at, target_grad(c, tg_logit));
+        row_sync();  // the list and the sums are read: the next row may come
       }
-      const Coefs c = make_coefs(a.grad_ce[row * a.grad_stride], a.grad_tvd[row * a.grad_stride],
-                                 sums.lse, sums.rest, sums.t_lse,
-                                 a.rest ? a.rest[row] : -INFINITY, sums.sigma);
-      stream_grad(r, grow, c, static_cast<int>(tg), v0, v1, rank == 0, rank == C - 1, once);
-      __syncthreads();  // the words of U over what the stream wrote there
-      for (int k = tid; k < K; k += kThreads) {
-        const int v = sh.idx[k];
-        if (v < 0) continue;
-        const int pos = v - r.head + VE - v0 * VE;
-        const bool mine = (pos >= VE || rank == 0) && (pos < (v1 - v0 + 1) * VE || rank == C - 1);
-        if (mine) Elem<T>::store1(grow + v, listed_grad(c, sh.s[k], sh.t[k], v == tg));
-      }
-      __syncthreads();  // the list and the sums are read: the next row may come
     }
   }
-  if (C > 1) cluster_barrier();  // a peer may still read this CTA's shared memory
+  __syncthreads();
+  cluster_barrier();  // no CTA leaves while a peer may send to it
+  if (tid == 0 && bars.abort && a.dev_status) atomicOr(a.dev_status, FCT_DEV_WAIT_TIMEOUT);
 }
 
 // ---------------------------------------------------------------- backward
 
 // One CTA per kSeg vectors of a row (the elements in no vector go with the
-// last).  It reads the student's logits at the listed words of its segment
-// first, streams the segment as if no word were listed, and then writes those
-// words again: so the gradient may overwrite the student.
-constexpr int kSeg = kUnroll * kThreads;
-constexpr int kListRegs = (kTopMax + kThreads - 1) / kThreads;
+// first and the last).  It reads the student's logits at the listed words of
+// its segment first, streams the segment as if no word were listed, and then
+// writes those words again: so the gradient may overwrite the student.
+constexpr int kBwdThreads = 256, kBwdUnroll = 4;
+constexpr int kSeg = 4 * kBwdUnroll * kBwdThreads;
+constexpr int kListRegs = kTopMax / kBwdThreads;
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) top_backward_kernel(TopArgs a, int64_t segs) {
-  constexpr int VE = Elem<T>::kVec;
+__global__ void __launch_bounds__(kBwdThreads, 6) top_backward_kernel(TopArgs a, int64_t segs) {
+  constexpr int VE = Elem<T>::kVec, NT = kBwdThreads;
   const uint64_t once = policy_evict_first();
   const int tid = threadIdx.x, V = static_cast<int>(a.V), K = static_cast<int>(a.K);
   const int64_t row = blockIdx.x / segs;
@@ -376,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 3) top_backward_kernel(TopArgs a, in
     const bool ignored = tg == a.ignore_index;
     if (!ignored && first && tid == 0 && a.dev_status)
       atomicOr(a.dev_status, FCT_DEV_TARGET_OUT_OF_RANGE);
-    fill_grad(grow, e0, e1, ignored ? 0.f : __uint_as_float(0x7fc00000u));
+    fill_grad<NT>(grow, e0, e1, ignored ? 0.f : __uint_as_float(0x7fc00000u));
     return;
   }
   const Coefs c = make_coefs(a.grad_ce[row * a.grad_stride], a.grad_tvd[row * a.grad_stride],
@@ -384,9 +372,10 @@ __global__ void __launch_bounds__(kThreads, 3) top_backward_kernel(TopArgs a, in
                              a.rest ? a.rest[row] : -INFINITY, a.sigma[row]);
   int at[kListRegs];
   float g[kListRegs];
+  bool listed = false;  // the target is in the list
 #pragma unroll
   for (int j = 0; j < kListRegs; ++j) {
-    const int k = tid + j * kThreads;
+    const int k = tid + j * NT;
     at[j] = -1;
     g[j] = 0.f;
     if (k < K) {
@@ -394,15 +383,27 @@ __global__ void __launch_bounds__(kThreads, 3) top_backward_kernel(TopArgs a, in
       if (v >= e0 && v < e1) {
         at[j] = v;
         g[j] = listed_grad(c, Elem<T>::load1(srow + v), a.values[row * a.ld_v + k], v == tg);
+        listed = listed || v == tg;
       }
     }
   }
-  __syncthreads();
-  stream_grad(r, grow, c, static_cast<int>(tg), v0, v1, first, last, once);
-  __syncthreads();
+  float tg_grad = 0.f;
+  if (tid == 0 && tg >= e0 && tg < e1) tg_grad = target_grad(c, Elem<T>::load1(srow + tg));
+  if (a.grad == a.student) __syncthreads();  // read before any of it is overwritten
+  const Outside o(c);
+  const bool same = same_alignment(srow, grow);
+  for (int i = v0 + tid; i < v1; i += kBwdUnroll * NT) {
+    uint4 raw[kBwdUnroll];
+    load<NT>(r, i, v1, once, raw);
+    each<NT>(i, v1, raw,
+             [&](uint4 w, int iv) { vector_grad(o, w, grow + r.head + iv * VE, same, once); });
+  }
+  loose_grad(r, grow, o, first, last);
+  listed = __syncthreads_or(listed);
 #pragma unroll
   for (int j = 0; j < kListRegs; ++j)
     if (at[j] >= 0) Elem<T>::store1(grow + at[j], g[j]);
+  if (tid == 0 && !listed && tg >= e0 && tg < e1) Elem<T>::store1(grow + tg, tg_grad);
 }
 
 // ---------------------------------------------------------------- launch
@@ -423,13 +424,22 @@ template <typename T, bool kGrad>
 cudaError_t run_forward(const TopArgs& a, int sms, int device, int l2, cudaStream_t st) {
   constexpr int VE = Elem<T>::kVec;
   const int C = ctas_per_row(a.V, a.dtype, sms, l2);
-  const int64_t words = bit_words(share(a.V / VE, C), VE);
-  const size_t smem = size_t(words) * 4 + list_bytes(a.K);
+  const int64_t words = (bit_words(share(a.V / VE, C), VE) + 3) / 4 * 4;
+  const size_t lists = size_t(words) * 4 + list_bytes(a.K);
+  // two CTAs per SM share its shared memory; a long vocabulary's bits may leave room for one
+  int resident = 2;
+  int stages = static_cast<int>((kStreamSmem / 2 - int64_t(lists)) / (kChunkVecs * 16));
+  if (stages < 2) {
+    resident = 1;
+    stages = static_cast<int>((kStreamSmem - int64_t(lists)) / (kChunkVecs * 16));
+  }
+  if (stages > kMaxStages) stages = kMaxStages;
   auto kernel = top_forward_kernel<T, kGrad>;
   static std::once_flag once[64];
   static cudaError_t set[64];
   std::call_once(once[device], [&] {
-    set[device] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTopSmemMax);
+    set[device] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kStreamSmem);
   });
   if (set[device] != cudaSuccess) return set[device];
   cudaLaunchConfig_t cfg = {};
@@ -438,19 +448,16 @@ cudaError_t run_forward(const TopArgs& a, int sms, int device, int l2, cudaStrea
   attr[0].val.clusterDim.x = static_cast<unsigned>(C);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(kStreamThreads);
+  cfg.dynamicSmemBytes = size_t(stages) * kChunkVecs * 16 + lists;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = st;
-  int resident = kGrad ? 2 : 3;
-  const int by_smem = static_cast<int>((227 * 1024) / (smem + 1280));
-  if (by_smem < resident) resident = by_smem > 0 ? by_smem : 1;
   int64_t clusters = int64_t(sms) * resident / C;
   if (clusters < 1) clusters = 1;
   if (clusters > a.BT) clusters = a.BT;
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * C));
-  return cudaLaunchKernelEx(&cfg, kernel, a, static_cast<int>(words));
+  return cudaLaunchKernelEx(&cfg, kernel, a, static_cast<int>(words), stages);
 }
 
 template <typename T>
@@ -473,7 +480,7 @@ cudaError_t run_backward(const TopArgs& a, cudaStream_t st) {
     b.sigma += r0;
     b.grad_ce += a.grad_stride * r0;
     b.grad_tvd += a.grad_stride * r0;
-    top_backward_kernel<T><<<static_cast<unsigned>(b.BT * segs), kThreads, 0, st>>>(b, segs);
+    top_backward_kernel<T><<<static_cast<unsigned>(b.BT * segs), kBwdThreads, 0, st>>>(b, segs);
   }
   return cudaGetLastError();
 }
