@@ -292,8 +292,7 @@ struct TopSelectArgs {
   float* rest;
   int32_t* dev_status;
 };
-cudaError_t launch_top_select(const TopSelectArgs& a, int sms, int device, int l2,
-                              cudaStream_t st);
+cudaError_t launch_top_select(const TopSelectArgs& a, int sms, int device, cudaStream_t st);
 
 struct TopArgs {
   const void* student;

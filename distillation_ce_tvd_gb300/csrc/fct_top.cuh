@@ -13,25 +13,31 @@
 namespace fct {
 namespace top {
 
-// A thread's running state: the largest logit, the exponents' offset -max log2 e
-// (0 while there is no finite one), and two partial sums.
+// A thread's running state: a reference, the exponents' offset -reference
+// log2 e (0 while nothing finite was seen), and two partial sums of terms
+// relative to it.  The reference is a logit seen, not always the largest: it
+// is raised to a vector's maximum only where that passes it by kAhead, so that
+// terms stay below 2^29 and, after a row's first vector, a warp hardly ever
+// has a lane that raises.
+constexpr float kAhead = 20.f;
 struct Run {
-  float mx, nm;
+  float limit, nm;  // limit: reference + kAhead
   float2 s;
 };
 __device__ __forceinline__ Run run_empty() { return Run{-INFINITY, 0.f, make_float2(0.f, 0.f)}; }
-// Folds a vector with maximum vm.
-template <int N>
-__device__ __forceinline__ void fold(Run& st, const float (&x)[N], float vm) {
-  static_assert(N % 2 == 0, "pairs");
-  if (vm > st.mx) {
+__device__ __forceinline__ void raise(Run& st, float vm) {
+  if (vm > st.limit) {
     const float nm = __fmul_rn(-vm, kLog2e);
-    const float sc = st.mx == -INFINITY ? 0.f : ex2(nm - st.nm);
+    const float sc = st.limit == -INFINITY ? 0.f : ex2(nm - st.nm);
     st.s.x *= sc;
     st.s.y *= sc;
-    st.mx = vm;
+    st.limit = vm + kAhead;
     st.nm = nm;
   }
+}
+template <int N>
+__device__ __forceinline__ void add(Run& st, const float (&x)[N]) {
+  static_assert(N % 2 == 0, "pairs");
   const float2 L2 = make_float2(kLog2e, kLog2e), n2 = make_float2(st.nm, st.nm);
 #pragma unroll
   for (int j = 0; j < N; j += 2) {
@@ -39,12 +45,14 @@ __device__ __forceinline__ void fold(Run& st, const float (&x)[N], float vm) {
     st.s = __fadd2_rn(st.s, make_float2(ex2(e.x), ex2(e.y)));
   }
 }
+// Folds a vector.
 template <int N>
 __device__ __forceinline__ void fold(Run& st, const float (&x)[N]) {
-  fold(st, x, vec_max(x));
+  raise(st, vec_max(x));
+  add(st, x);
 }
 __device__ __forceinline__ Lse2 folded(const Run& st) {
-  return Lse2{st.mx == -INFINITY ? -INFINITY : -st.nm, st.s.x + st.s.y};
+  return Lse2{st.limit == -INFINITY ? -INFINITY : -st.nm, st.s.x + st.s.y};
 }
 
 // A state's sum relative to the maximum m (at least its own).  An empty state
@@ -188,6 +196,13 @@ __device__ __forceinline__ int row_count(bool b) {
 }
 static_assert(kRowThreads == 512, "the barriers above");
 
+// A vector of -inf.
+template <typename T>
+__device__ __forceinline__ uint4 nothing() {
+  const uint32_t w = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+  return make_uint4(w, w, w, w);
+}
+
 // The ring's barriers, in static shared memory.
 struct RingBars {
   uint64_t full[kMaxStages], empty[kMaxStages];
@@ -240,26 +255,51 @@ struct Ring {
     for (uint32_t i = copied > n ? copied - n : 0; i < copied; ++i)
       mbar_wait(&bars->full[i % n], (i / n) & 1u, &bars->abort, false);
   }
-  // Consumers: f(vector, its index, its place among a chunk's vectors of the
-  // thread) for vectors [v0, v1) of a row.
+  // Consumers: the next chunk, and its release.
+  __device__ __forceinline__ const uint4* wait() {
+    mbar_wait(&bars->full[slot], phase, &bars->abort);
+    return buf + slot * kChunkVecs;
+  }
+  __device__ __forceinline__ void release() {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->empty[slot]);
+    next();
+  }
+  // Consumers, all lanes of a warp together: f(vector, its index) for vectors
+  // [v0, v1) of a row, and a vector of -inf for a lane that has none.
+  template <typename T, typename F>
+  __device__ __forceinline__ void each_warp(int v0, int v1, F f) {
+    const int tid = threadIdx.x;
+    for (int c = v0; c < v1; c += kChunkVecs) {
+      const uint4* p = wait() + tid;
+      if (c + kChunkVecs <= v1) {
+#pragma unroll
+        for (int u = 0; u < kPerThread; ++u) f(p[u * kRowThreads], c + u * kRowThreads + tid);
+      } else {
+#pragma unroll
+        for (int u = 0; u < kPerThread; ++u) {
+          const int i = c + u * kRowThreads + tid;
+          f(i < v1 ? p[u * kRowThreads] : nothing<T>(), i);
+        }
+      }
+      release();
+    }
+  }
+  // Consumers: f(vector, its index) for vectors [v0, v1) of a row.
   template <typename F>
   __device__ __forceinline__ void each(int v0, int v1, F f) {
     const int tid = threadIdx.x;
     for (int c = v0; c < v1; c += kChunkVecs) {
-      mbar_wait(&bars->full[slot], phase, &bars->abort);
-      const uint4* p = buf + slot * kChunkVecs + tid;
+      const uint4* p = wait() + tid;
       if (c + kChunkVecs <= v1) {
 #pragma unroll
-        for (int u = 0; u < kPerThread; ++u) f(p[u * kRowThreads], c + u * kRowThreads + tid, u);
+        for (int u = 0; u < kPerThread; ++u) f(p[u * kRowThreads], c + u * kRowThreads + tid);
       } else {
 #pragma unroll
         for (int u = 0; u < kPerThread; ++u)
-          if (c + u * kRowThreads + tid < v1)
-            f(p[u * kRowThreads], c + u * kRowThreads + tid, u);
+          if (c + u * kRowThreads + tid < v1) f(p[u * kRowThreads], c + u * kRowThreads + tid);
       }
-      __syncwarp();
-      if ((tid & 31) == 0) mbar_arrive(&bars->empty[slot]);
-      next();
+      release();
     }
   }
 };

@@ -238,12 +238,12 @@ int fct_top_logits(const void* logits, int64_t ld, fct_dtype dtype, int64_t BT, 
                         {rest_lse, 1, BT, BT, 4}};
   if ((rc = check_arrays(in, 1, out, 3)) != FCT_OK) return rc;
   if ((rc = check_status(dev_status)) != FCT_OK) return rc;
-  int sms = 0, device = 0, l2 = 0;
-  if ((rc = fct::current_device_sms(&sms, &device, &l2)) != FCT_OK) return rc;
+  int sms = 0, device = 0;
+  if ((rc = fct::current_device_sms(&sms, &device)) != FCT_OK) return rc;
   return launched(fct::launch_top_select(
       fct::TopSelectArgs{logits, ld, dtype, BT, V, K, values, ld_values, index, ld_index, rest_lse,
                          dev_status},
-      sms, device, l2, static_cast<cudaStream_t>(stream)));
+      sms, device, static_cast<cudaStream_t>(stream)));
 }
 
 int fused_ce_tvd_top_forward(const void* student, int64_t ld_student, fct_dtype dtype,

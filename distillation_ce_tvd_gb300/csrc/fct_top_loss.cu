@@ -236,17 +236,23 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       bad = row_or(bad);
       // ---- the log-sum-exp of the words outside U
       Run st = run_empty();
-      ring.each(v0, v1, [&](uint4 w, int iv, int) {
+      const uint8_t* own_bytes = bytes - v0 * VE / 8;
+      ring.template each_warp<T>(v0, v1, [&](uint4 w, int iv) {
         float x[VE];
         Elem<T>::unpack(w, x);
-        const int pos = (iv - v0 + 1) * VE;
-        const uint32_t m = VE == 8 ? bytes[pos >> 3] : (bytes[pos >> 3] >> (pos & 4)) & 15u;
-        if (m) {
+        float vm = vec_max(x);
+        // (past the share's end: within the bits' room, or of no matter)
+        const int at = VE == 8 ? iv + 1 : (iv + 1) >> 1;
+        uint32_t m = iv < v1 ? own_bytes[at] : 0u;
+        if (VE == 4) m = (m >> (4 * ((iv + 1) & 1))) & 15u;
+        if (__any_sync(0xffffffffu, m != 0 || vm > st.limit)) {  // seldom
 #pragma unroll
           for (int j = 0; j < VE; ++j)
             if ((m >> j) & 1u) x[j] = -INFINITY;
+          vm = vec_max(x);
+          raise(st, vm);
         }
-        fold(st, x);
+        add(st, x);
       });
       // the elements in no vector: the head with CTA 0, the tail with the last
       if (tid < r.n_loose() && rank == (tid < r.head ? 0 : C - 1)) {
@@ -310,7 +316,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
                                    a.rest ? a.rest[row] : -INFINITY, sums.sigma);
         const Outside o(c);
         const bool same = same_alignment(srow, grow);
-        ring.each(v0, v1, [&](uint4 w, int iv, int) {
+        ring.each(v0, v1, [&](uint4 w, int iv) {
           vector_grad(o, w, grow + r.head + iv * VE, same, once);
         });
         loose_grad(r, grow, o, rank == 0, rank == C - 1);

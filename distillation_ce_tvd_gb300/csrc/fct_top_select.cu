@@ -1,27 +1,36 @@
 // The K largest logits of each row, and the log-sum-exp of the others.
 //
-// V e bytes from memory, which bound it, in two sweeps: the second reads from
-// L2.  The first finds the largest logit of each thread's part of the row.
-// These maxima are logits of their own, so what K of them reach, K logits of
-// the row reach: their K-th largest is a threshold that about K logits are
-// above (70 at K = 64 and 512 threads, 355 at K = 256).  The second sweep
-// keeps those few ("candidates") in shared memory and folds all others into
-// the log-sum-exp of the rest.  (One sweep with a threshold that rises as it
-// goes has 300 to 1200 candidates at K = 64, in nearly every warp's vectors:
-// 1218 us at 8192 x 151936 bf16, against ??.)
+// One pass over the row, V e bytes, which bound it.  Every thread keeps the
+// largest logit of each of its vectors' columns so far.  These maxima are
+// logits of their own, so what K of them reach, K logits of the row reach: that
+// is a threshold, found from the first chunk of a row (32 KB, 16384 bf16) and
+// again after 2, 4, 8, ... chunks.  A vector with nothing above it is folded
+// into the log-sum-exp of the rest at once; of 594 vectors of a warp at V =
+// 151936 and K = 64, about 34 are not.  Those wait in their warp's queue and
+// are taken 32 at a time, one per lane, so that a warp does not go through the
+// slow path for one lane: their elements above the threshold become candidates
+// in shared memory, the others are folded.  (Candidates taken at once, vector
+// by vector, cost 194 instructions per 32 vectors instead of ??, 1218 us at
+// 8192 x 151936 bf16, K = 64; a first sweep for the threshold and a second
+// over L2, 895.)
 //
 // So the rest is summed from its own terms, never as a difference: it keeps
-// its relative precision however little it holds.  Candidates beyond the K-th
-// are added as integers (2^40 = the largest of them), in any order the same;
-// the order of the other terms is fixed by the row's layout.  Repeated calls
-// give the same bits.
+// its relative precision however little it holds.  Candidates that a selection
+// drops are added as integers (2^31 = the largest of them), in any order the
+// same; the order of all other terms is fixed by the row's layout.  Repeated
+// calls give the same bits.
 //
-// Equal logits rank by index.  Where more candidates come than there is room
-// for (rows of few values), the second sweep is done again in rounds of rising
-// index with a selection in between: its threshold only ever meets later
-// rounds, where an equal logit has a larger index than K that rank before it.
+// Equal logits rank by index.  A threshold is below the maxima that it was
+// found from, so that everything equal to them is a candidate; where more
+// candidates come than there is room for (rows of few values), the row is
+// taken again in rounds of rising index with a selection in between, whose
+// threshold only ever meets later rounds: there, an equal logit has a larger
+// index than K that rank before it.
 #include <climits>
+#include <cstring>
 #include <mutex>
+
+#include <cuda_bf16.h>
 
 #include "fct_internal.h"
 #include "fct_top.cuh"
@@ -37,15 +46,18 @@ constexpr int kWarps = kRowWarps;
 constexpr int kBins = 1024;
 // Up to this K a thread's part has one maximum, above it one per vector of a
 // chunk: the maxima have to be several times K for the threshold to be near
-// the K-th logit.
-constexpr int kFewMaxima = 384;
+// the K-th logit.  A warp looks at 128 of them.
+constexpr int kFewMaxima = 96;
+constexpr int kPool = 128;
 
 // A selection may keep this many more than K: it need not split a bin.
-__host__ __device__ constexpr int slack(int K) { return K / 4 + 32; }
-// Room for candidates: what a selection keeps and one round of vectors.
+__host__ __device__ constexpr int slack(int K) { return K / 4 + 64; }
+// Room for candidates: what a selection keeps and a round of vectors.
+constexpr int kRound = 256;  // vectors of a round
 __host__ __device__ constexpr int capacity(int K, int vec) {
-  return K + slack(K) + kThreads * vec;
+  return K + slack(K) + kRound * vec;
 }
+constexpr int kQueue = 64;  // vectors that wait, per warp
 
 // Unsigned key that increases with the float (no NaN comes here; -0 is +0).
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -57,6 +69,11 @@ __device__ __forceinline__ float value_of(uint32_t k) {
 }
 constexpr uint32_t kKeyNegInf = 0x007fffffu;  // key_of(-inf)
 constexpr uint32_t kKeyZero = 0x80000000u;    // key_of(0)
+
+// The number before that of a key (before 0: not the other 0).
+__device__ __forceinline__ float before(uint32_t key) {
+  return key == kKeyZero ? -__uint_as_float(1u) : key > kKeyNegInf + 1 ? value_of(key - 1) : -INFINITY;
+}
 
 // Entries rank by value, then by lower index.
 __device__ __forceinline__ uint64_t rank_key(uint32_t key, int idx) {
@@ -83,8 +100,9 @@ struct Scratch {  // static shared memory of a CTA
   uint32_t drop_key;
   unsigned long long drop_sum;
   float2 warp_state[kWarps];
-  uint64_t state; // for CTA 0 of the cluster: the CTA's part of the rest
-  uint64_t n;     // and its candidates
+  uint16_t maxima[kPerThread * kThreads];  // the top halves of the maxima's keys
+  uint32_t pool_key[2][kWarps];
+  int queue[kWarps][kQueue];
 };
 
 // What has been dropped, as a base-2 state (all threads hold the same).
@@ -94,7 +112,7 @@ __device__ __forceinline__ void add_state(float2& a, float m2, float s) {
 }
 
 // Adds those of entries [from, n) that is_dropped says to `out`: integers in
-// units of 2^-40 of the largest, so that their order does not matter.
+// units of 2^-31 of the largest, so that their order does not matter.
 template <typename F>
 __device__ void drop(const Shared& sh, Scratch& sc, int from, int n, float2& out, F is_dropped) {
   const int tid = threadIdx.x;
@@ -115,25 +133,24 @@ __device__ void drop(const Shared& sh, Scratch& sc, int from, int n, float2& out
   unsigned long long sum = 0;
   for (int i = from + tid; i < n; i += kThreads)
     if (is_dropped(sh.entry[i]))
-      sum += static_cast<unsigned long long>(ex2(fmaf(entry_value(sh.entry[i]), kLog2e, -m2)) *
-                                             1099511627776.f);
+      sum += static_cast<uint32_t>(ex2(fmaf(entry_value(sh.entry[i]), kLog2e, -m2)) * 2147483648.f);
 #pragma unroll
   for (int k = 16; k >= 1; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
   if ((tid & 31) == 0 && sum) atomicAdd(&sc.drop_sum, sum);
   row_sync();
-  add_state(out, m2, static_cast<float>(sc.drop_sum) * (1.f / 1099511627776.f));
+  add_state(out, m2, static_cast<float>(sc.drop_sum) * (1.f / 2147483648.f));
 }
 
 // Keeps the K highest-ranking of n > K + slack entries, or up to `slack` more,
-// at the front; drops the others.  Returns how many are kept and the value
-// below or at which nothing of a later round can rank.
+// at the front; drops the others.  Returns how many are kept, and in `least` a
+// key that all of theirs reach.
 //
 // Levels of a histogram over a range of rank keys: the range first spans all
 // entries, then the bin that holds the K-th, until the bins up to that one
 // hold few enough.  The K-th bin narrows by 1024 a level; single keys are
 // unique, so that it ends.
 __device__ __noinline__ int select(const Shared& sh, Scratch& sc, int n, int K, float2& dropped,
-                                   float& thr) {
+                                   uint32_t& least) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     sc.lo = 0xffffffffu;
@@ -176,12 +193,12 @@ __device__ __noinline__ int select(const Shared& sh, Scratch& sc, int n, int K, 
     }
     if (lane == 31) sc.warp_count[warp] = run;
     row_sync();
-    int before = above + run - (c0 + c1);
-    for (int w = 0; w < warp; ++w) before += sc.warp_count[w];
-    if (before < K && before + c0 + c1 >= K) {
-      const bool second = before + c0 < K;
+    const int sum = lane < warp ? sc.warp_count[lane] : 0;  // (16 warps)
+    const int ahead = above + static_cast<int>(__reduce_add_sync(0xffffffffu, sum)) + run - (c0 + c1);
+    if (ahead < K && ahead + c0 + c1 >= K) {
+      const bool second = ahead + c0 < K;
       sc.bin = second ? b0 - 1 : b0;
-      sc.above = second ? before + c0 : before;
+      sc.above = second ? ahead + c0 : ahead;
       sc.inside = second ? c1 : c0;
     }
     row_sync();
@@ -202,20 +219,40 @@ __device__ __noinline__ int select(const Shared& sh, Scratch& sc, int n, int K, 
     if (i < n && e >= from) sh.entry[atomicAdd(&sc.kept, 1)] = e;
     row_sync();
   }
-  thr = value_of(static_cast<uint32_t>(from >> 32));
+  least = static_cast<uint32_t>(from >> 32);
   return sc.kept;
 }
 
-// Sorts n entries, highest rank first (bitonic; the room up to a power of two
-// is there).  Pairs of up to 64 entries stay within a warp's entries.
+// Up to this many entries are ordered by counting, more by sorting.
+constexpr int kCountMax = 192;
+
+// Orders n <= kCountMax entries: an entry's place is the number that rank
+// before it, counted by as many threads per entry as there are.
+__device__ __forceinline__ void count_entries(const Shared& sh, int n) {
+  const int tid = threadIdx.x;
+  const int parts = n <= 32 ? 16 : n <= 64 ? 8 : n <= 128 ? 4 : 2;
+  const int i = tid / parts, part = tid % parts;
+  const uint64_t own = i < n ? sh.entry[i] : ~0ull;
+  int place = 0;
+#pragma unroll 8
+  for (int j = part; j < n; j += parts) place += sh.entry[j] > own;
+  for (int d = 1; d < parts; d *= 2) place += __shfl_xor_sync(0xffffffffu, place, d);
+  row_sync();
+  if (i < n && part == 0) sh.entry[place] = own;
+  row_sync();
+}
+
+// Sorts n entries, highest rank first (bitonic, a power of two of them: the
+// room is there).  Steps within 32 entries are done in registers, by threads
+// that hold an entry each.
 __device__ __noinline__ void sort_entries(const Shared& sh, int n) {
   const int tid = threadIdx.x;
-  int P = 64;
+  int P = kThreads;
   while (P < n) P *= 2;
   for (int i = n + tid; i < P; i += kThreads) sh.entry[i] = 0;
   row_sync();
   for (int size = 2; size <= P; size *= 2) {
-    for (int step = size / 2; step > 0; step /= 2) {
+    for (int step = size / 2; step >= 32; step /= 2) {
       for (int i = tid; i < P / 2; i += kThreads) {
         const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
         const uint64_t x = sh.entry[lo], y = sh.entry[hi];
@@ -224,44 +261,43 @@ __device__ __noinline__ void sort_entries(const Shared& sh, int n) {
           sh.entry[hi] = x;
         }
       }
-      // the next step's pairs: 2 step entries apart at most
-      if (step > 32 || (step == 1 && size >= 64))
-        row_sync();
-      else
-        __syncwarp();
+      row_sync();
     }
+    // (sizes up to 32 need no other entries in between)
+    if (size < 32) continue;
+    for (int i = tid; i < P; i += kThreads) {
+      uint64_t x = sh.entry[i];
+      for (int z = size == 32 ? 2 : size; z <= size; z *= 2) {
+        const bool down = (i & z) == 0;  // highest first
+        for (int step = z / 2 < 32 ? z / 2 : 16; step > 0; step /= 2) {
+          const uint64_t y = __shfl_xor_sync(0xffffffffu, x, step);
+          const bool first = (i & step) == 0;
+          x = (x > y) == (first == down) ? x : y;
+        }
+      }
+      sh.entry[i] = x;
+    }
+    row_sync();
   }
-  row_sync();
 }
 
-// The largest t, with 16 bits, such that K of the block's values reach it (0:
-// fewer than K are above -inf): a bit a round.
+// The largest t such that `want` of the warp's values reach it (0: fewer than
+// that are above -inf): a bit a round.
 template <int N>
-__device__ __forceinline__ uint32_t block_threshold(const uint32_t (&key)[N], int K) {
+__device__ __forceinline__ uint32_t warp_threshold(const uint32_t (&key)[N], int want) {
   uint32_t t = 0;
-  for (int bit = 31; bit >= 16; --bit) {
+#pragma unroll 4
+  for (int bit = 15; bit >= 0; --bit) {
     const uint32_t trial = t | (1u << bit);
     int c = 0;
 #pragma unroll
-    for (int u = 0; u < N; ++u) c += row_count(key[u] >= trial);
-    if (c >= K) t = trial;
+    for (int u = 0; u < N; ++u) c += __popc(__ballot_sync(0xffffffffu, key[u] >= trial));
+    if (c >= want) t = trial;
   }
   return t;
 }
 
-__device__ __forceinline__ float raw_max(uint4 w, float) {
-  return fmaxf(max3(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z)),
-               __uint_as_float(w.w));
-}
-__device__ __forceinline__ float raw_max(uint4 w, bf16_t) {
-  float x[8];
-  Elem<bf16_t>::unpack(w, x);
-  return vec_max(x);
-}
-
-// One cluster of C CTAs per row at a time, C by V and the element type alone.
-// Each CTA finds the candidates of its share of the row; CTA 0 then takes over
-// the others' candidates and states.
+// One CTA per row at a time.
 template <typename T>
 __global__ void __launch_bounds__(kStreamThreads, 2)
     top_select_kernel(TopSelectArgs a, int cap, int stages) {
@@ -269,97 +305,51 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
   extern __shared__ uint4 select_smem[];
   __shared__ Scratch sc;
   __shared__ __align__(8) RingBars bars;
-  // CTA 0's: the others' candidates are ready; the others': CTA 0 has taken them over
-  __shared__ __align__(8) uint64_t ready_bar, taken_bar;
   const Shared sh{reinterpret_cast<uint64_t*>(select_smem + stages * kChunkVecs),
                   reinterpret_cast<int*>(select_smem + stages * kChunkVecs) + 2 * cap};
   const int K = static_cast<int>(a.K), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int V = static_cast<int>(a.V);
-  const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
-  const int64_t n_clusters = gridDim.x / C;
   Ring ring(&bars, select_smem, stages);
-  if (tid == 0) {
-    mbar_init(&ready_bar, C > 1 ? C - 1 : 1);
-    mbar_init(&taken_bar, 1);
-    ring.init();
-  }
+  if (tid == 0) ring.init();
   __syncthreads();
-  cluster_barrier();  // every CTA's barriers exist
-  auto share_of = [&](const Row<T>& r, int* v0, int* v1) {
-    const int per = static_cast<int>(share(r.nvec, C));
-    *v0 = min(rank * per, r.nvec);
-    *v1 = min(*v0 + per, r.nvec);
-  };
 
   if (tid >= kThreads) {
-    if (tid == kThreads) {  // ---- copies: every share twice
-      const uint64_t once = policy_evict_first(), again = policy_evict_last();
+    if (tid == kThreads) {  // ---- copies
+      const uint64_t once = policy_evict_first();
       uint32_t copied = 0;
-      for (int64_t row = blockIdx.x / C; row < a.BT; row += n_clusters) {
+      for (int64_t row = blockIdx.x; row < a.BT; row += gridDim.x) {
         const Row<T> r(static_cast<const T*>(a.logits) + row * a.ld, V);
-        int v0, v1;
-        share_of(r, &v0, &v1);
-        if (!ring.copy(r, v0, v1, again)) break;
-        copied += chunks_of(v0, v1);
-        if (!ring.copy(r, v0, v1, once)) break;
-        copied += chunks_of(v0, v1);
+        if (!ring.copy(r, 0, r.nvec, once)) break;
+        copied += chunks_of(0, r.nvec);
       }
       ring.drain(copied);
     }
   } else {
-    uint32_t turn = 0;
-    for (int64_t row = blockIdx.x / C; row < a.BT; row += n_clusters, ++turn) {
+    for (int64_t row = blockIdx.x; row < a.BT; row += gridDim.x) {
       const Row<T> r(static_cast<const T*>(a.logits) + row * a.ld, V);
-      int v0, v1;
-      share_of(r, &v0, &v1);
-
-      // ---- first sweep: the threshold
-      float mx[kPerThread];
-#pragma unroll
-      for (int u = 0; u < kPerThread; ++u) mx[u] = -INFINITY;
-      ring.each(v0, v1,
-                [&](uint4 w, int, int u) { mx[u] = fmaxf(mx[u], raw_max(w, T{})); });
-      uint32_t least;
-      if (K <= kFewMaxima) {
-        const uint32_t key[1] = {key_of(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]))};
-        least = block_threshold(key, K);
-      } else {
-        const uint32_t key[4] = {key_of(mx[0]), key_of(mx[1]), key_of(mx[2]), key_of(mx[3])};
-        least = block_threshold(key, K);
-      }
-      // logits at it are candidates too: the threshold is the number before it
-      // (before 0, not the other 0)
-      float thr = least == kKeyZero          ? -__uint_as_float(1u)
-                  : least > kKeyNegInf + 1 ? value_of(least - 1)
-                                           : -INFINITY;
-      if (tid == 0) sc.pushed = 0;
-      // CTA 0 has taken over the last row's candidates
-      if (rank != 0 && turn > 0) wait_cluster(&taken_bar, (turn - 1) & 1u, &bars.abort);
-      row_sync();
-
-      // ---- second sweep
       Run st = run_empty();
       float2 dropped = make_float2(-INFINITY, 0.f);
+      float thr = -INFINITY;
+      int waiting = 0;  // vectors in the warp's queue
+      if (tid == 0) sc.pushed = 0;
+      row_sync();
+
       auto push = [&](float x, int v) {
         const int at = atomicAdd(&sc.pushed, 1);
         if (at < cap) sh.entry[at] = rank_key(key_of(x), v);
       };
-      // one vector: candidates pushed, the others folded
+      // one vector: elements above the threshold pushed, the others folded
       auto take = [&](uint4 raw, int i) {
         float x[VE];
         Elem<T>::unpack(raw, x);
-        float vm = vec_max(x);
-        if (vm > thr) {
-          const int e0 = r.head + i * VE;
+        const int e0 = r.head + i * VE;
 #pragma unroll
-          for (int j = 0; j < VE; ++j)
-            if (x[j] > thr) {
-              push(x[j], e0 + j);
-              x[j] = -INFINITY;
-            }
-          vm = vec_max(x);
-        }
-        fold(st, x, vm);
+        for (int j = 0; j < VE; ++j)
+          if (x[j] > thr) {
+            push(x[j], e0 + j);
+            x[j] = -INFINITY;
+          }
+        fold(st, x);
       };
       auto take_loose = [&](int v) {
         const float x = Elem<T>::load1(r.p + v);
@@ -367,111 +357,176 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
           push(x, v);
         } else {
           const float one[2] = {x, -INFINITY};
-          fold(st, one, x);
+          fold(st, one);
         }
       };
-      const bool has_head = rank == 0 && tid < r.head;
-      const bool has_tail = rank == C - 1 && r.tail0 + tid < V;
-      if (has_head) take_loose(tid);
-      ring.each(v0, v1, [&](uint4 w, int i, int) { take(w, i); });
-      if (has_tail) take_loose(r.tail0 + tid);
-      row_sync();
-      int n = sc.pushed;
-      if (n > cap) {  // too many: again, a round of one vector per thread at a time
+      // the first n vectors of the warp's queue, one per lane
+      auto digest = [&](int n) {
+        __syncwarp();
+        if (lane < n) {
+          const int i = sc.queue[warp][lane];
+          take(*r.vec(i), i);
+        }
+        __syncwarp();
+        if (lane + n < waiting) {
+          const int i = sc.queue[warp][lane + n];
+          sc.queue[warp][lane] = i;
+        }
+        waiting -= n;
+        __syncwarp();
+      };
+      float mx[kPerThread];
+#pragma unroll
+      for (int u = 0; u < kPerThread; ++u) mx[u] = -INFINITY;
+      uint32_t found = 0;  // thresholds found so far
+      // Raises the threshold: each pool of maxima finds what its share of K
+      // reach; the least of those holds for all.
+      auto raise_threshold = [&]() {
+        const int pools = K <= kFewMaxima ? kThreads / kPool : kPerThread * kThreads / kPool;
+        if (K <= kFewMaxima) {
+          sc.maxima[tid] =
+              static_cast<uint16_t>(key_of(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3])) >> 16);
+        } else {
+#pragma unroll
+          for (int u = 0; u < kPerThread; ++u)
+            sc.maxima[u * kThreads + tid] = static_cast<uint16_t>(key_of(mx[u]) >> 16);
+        }
         row_sync();
+        uint32_t* keys = sc.pool_key[found++ & 1u];
+        if (warp < pools) {
+          const uint16_t* m = sc.maxima + warp * kPool + lane;
+          const uint32_t key[4] = {m[0], m[32], m[64], m[96]};
+          const uint32_t t = warp_threshold(key, (K + pools - 1) / pools);
+          if (lane == 0) keys[warp] = t << 16;
+        }
+        row_sync();
+        // (logits at it are candidates too)
+        thr = fmaxf(thr, before(__reduce_min_sync(0xffffffffu, keys[lane % pools])));
+      };
+      // The candidates so far, with room made for `more` unless there are too
+      // many already.  `rounds`: all that is still to come has a larger index
+      // than all so far, so that what equals the K-th cannot rank.
+      auto room = [&](int more, bool rounds) {
+        row_sync();
+        int n = sc.pushed;
+        row_sync();
+        if (n <= cap && n + more > cap) {
+          uint32_t least;
+          n = select(sh, sc, n, K, dropped, least);
+          thr = fmaxf(thr, rounds ? value_of(least) : before(least));
+          row_sync();
+          if (tid == 0) sc.pushed = n;
+          row_sync();
+        }
+        return n;
+      };
+
+      if (tid < r.head) take_loose(tid);
+      int chunks = 0;
+      bool full = false;  // more candidates came than there is room for
+      for (int c = 0; c < r.nvec; c += kChunkVecs) {
+        const uint4* p = ring.wait() + tid;
+        auto vec = [&](int u) {
+          return c + u * kThreads + tid < r.nvec ? p[u * kThreads] : nothing<T>();
+        };
+        if (c == 0) {
+#pragma unroll
+          for (int u = 0; u < kPerThread; ++u) {
+            float x[VE];
+            Elem<T>::unpack(vec(u), x);
+            mx[u] = vec_max(x);
+          }
+          raise_threshold();
+        }
+        float unusual = fminf(thr, st.limit);  // a vector with nothing above it is just added
+#pragma unroll
+        for (int u = 0; u < kPerThread; ++u) {
+          float x[VE];
+          Elem<T>::unpack(vec(u), x);
+          const float vm = vec_max(x);
+          mx[u] = fmaxf(mx[u], vm);
+          bool above = false;
+          if (__any_sync(0xffffffffu, vm > unusual)) {
+            above = vm > thr;
+            if (!above) raise(st, vm);
+            const uint32_t b = __ballot_sync(0xffffffffu, above);
+            if (above)
+              sc.queue[warp][waiting + __popc(b & ((1u << lane) - 1u))] = c + u * kThreads + tid;
+            waiting += __popc(b);
+            if (waiting >= 32) digest(32);
+            unusual = fminf(thr, st.limit);
+          }
+          if (!above) add(st, x);
+        }
+        ring.release();
+        ++chunks;
+        // (always the same decision in all warps)
+        const bool doubled = (chunks & (chunks - 1)) == 0;
+        if (doubled || K > kFewMaxima) {
+          if (doubled && chunks > 1 && c + kChunkVecs < r.nvec) raise_threshold();
+          if (!full) full = room(kRound * VE, false) > cap;
+        }
+      }
+      digest(waiting);
+      int n = room(VE, false);
+      full = full || n > cap;
+      if (!full) {
+        if (r.tail0 + tid < V) take_loose(r.tail0 + tid);
+      } else {  // again, in rounds of rising index with room made before each
         if (tid == 0) sc.pushed = 0;
         row_sync();
         st = run_empty();
-        auto room = [&](int more) {  // the candidates so far, with room for a round
-          row_sync();
-          n = sc.pushed;
-          row_sync();
-          if (n + more > cap) {
-            n = select(sh, sc, n, K, dropped, thr);
-            row_sync();
-            if (tid == 0) sc.pushed = n;
-            row_sync();
-          }
-        };
-        if (has_head) take_loose(tid);
-        for (int c = v0; c < v1; c += kThreads) {
-          room(kThreads * VE);
-          if (c + tid < v1) take(*r.vec(c + tid), c + tid);
+        dropped = make_float2(-INFINITY, 0.f);
+        thr = -INFINITY;
+        if (tid < r.head) take_loose(tid);
+        for (int c = 0; c < r.nvec; c += kRound) {
+          room(kRound * VE, true);
+          if (tid < kRound && c + tid < r.nvec) take(*r.vec(c + tid), c + tid);
         }
-        room(VE);
-        if (has_tail) take_loose(r.tail0 + tid);
-        row_sync();
-        n = sc.pushed;
+        room(VE, true);
+        if (r.tail0 + tid < V) take_loose(r.tail0 + tid);
       }
-      if (n > K + slack(K)) n = select(sh, sc, n, K, dropped, thr);
+      row_sync();
+      n = sc.pushed;
+      if (n > K + slack(K)) {
+        uint32_t least;
+        n = select(sh, sc, n, K, dropped, least);
+      }
       const Lse2 w = merge_warp(folded(st));
       if (lane == 0) sc.warp_state[warp] = make_float2(w.m2, w.s);
       row_sync();
-      Lse2 rest{-INFINITY, 0.f};  // warp 0 of CTA 0: the row's, but for what is dropped below
-      if (warp == 0) {
-        const float2 own = lane < kWarps ? sc.warp_state[lane] : make_float2(-INFINITY, 0.f);
-        rest = merge(merge_warp(Lse2{own.x, own.y}), Lse2{dropped.x, dropped.y});
-      }
-      dropped = make_float2(-INFINITY, 0.f);
-      if (rank != 0) {
-        if (tid == 0) {
-          sc.state = (uint64_t(__float_as_uint(rest.m2)) << 32) | __float_as_uint(rest.s);
-          sc.n = static_cast<uint64_t>(n);
-          arrive_at(&ready_bar, 0);  // and all entries, written before the last barrier
-        }
-        continue;
-      }
-      if (C > 1) {
-        wait_cluster(&ready_bar, turn & 1u, &bars.abort);
-        for (int p = 1; p < C; ++p) {
-          const uint64_t o = peer_word(&sc.state, static_cast<uint32_t>(p));
-          rest = merge(rest, Lse2{__uint_as_float(static_cast<uint32_t>(o >> 32)),
-                                  __uint_as_float(static_cast<uint32_t>(o))});
-          // (a CTA keeps no more than this; after a wait that ran out, anything is read)
-          const int more = static_cast<int>(
-              min(peer_word(&sc.n, static_cast<uint32_t>(p)), uint64_t(K + slack(K))));
-          if (n + more > cap) n = select(sh, sc, n, K, dropped, thr);
-          for (int i = tid; i < more; i += kThreads)
-            sh.entry[n + i] = peer_word(sh.entry + i, static_cast<uint32_t>(p));
-          n += more;
-          row_sync();
-        }
-        if (tid > 0 && tid < C) arrive_at(&taken_bar, static_cast<uint32_t>(tid));
-        if (n > K + slack(K)) n = select(sh, sc, n, K, dropped, thr);
-      }
-      sort_entries(sh, n);
+      if (n <= kCountMax)
+        count_entries(sh, n);
+      else
+        sort_entries(sh, n);
       for (int i = tid; i < K; i += kThreads) {
         const uint64_t e = i < n ? sh.entry[i] : 0;
         a.values[row * a.ld_v + i] = i < n ? entry_value(e) : -INFINITY;
         a.index[row * a.ld_i + i] = i < n ? entry_index(e) : -1;
       }
       if (n > K) drop(sh, sc, K, n, dropped, [](uint64_t) { return true; });
-      if (tid == 0) {
-        rest = merge(rest, Lse2{dropped.x, dropped.y});
-        const bool inf = n > 0 && entry_value(sh.entry[0]) == INFINITY;
-        const float out = inf ? __uint_as_float(0x7fc00000u) : finish(rest.m2, rest.s);
-        a.rest[row] = out;
-        if ((out != out || n == 0) && a.dev_status) atomicOr(a.dev_status, FCT_DEV_NO_DISTRIBUTION);
+      if (warp == 0) {
+        const float2 own = lane < kWarps ? sc.warp_state[lane] : make_float2(-INFINITY, 0.f);
+        const Lse2 rest = merge(merge_warp(Lse2{own.x, own.y}), Lse2{dropped.x, dropped.y});
+        if (lane == 0) {
+          const bool inf = n > 0 && entry_value(sh.entry[0]) == INFINITY;
+          const float out = inf ? __uint_as_float(0x7fc00000u) : finish(rest.m2, rest.s);
+          a.rest[row] = out;
+          if ((out != out || n == 0) && a.dev_status)
+            atomicOr(a.dev_status, FCT_DEV_NO_DISTRIBUTION);
+        }
       }
       row_sync();
     }
   }
   __syncthreads();
-  cluster_barrier();  // no CTA leaves while a peer may send to it or read from it
   if (tid == 0 && bars.abort && a.dev_status) atomicOr(a.dev_status, FCT_DEV_WAIT_TIMEOUT);
 }
 
-// CTAs per row: the rows in flight (two CTAs per SM) fit in 0.8 of L2, from
-// which the second sweep reads.
-int ctas_per_row(int64_t V, int dtype, int sms, int l2) {
-  const double row = double(V) * (dtype == FCT_BF16 ? 2 : 4);
-  int C = 1;
-  while (C < 8 && 2.0 * sms / C * row > 0.8 * l2) C *= 2;
-  return C;
-}
+constexpr int kSmem = kStreamSmem / 2 - 9 * 1024;  // dynamic, beside the static
 
 template <typename T>
-cudaError_t run(const TopSelectArgs& a, int sms, int device, int l2, cudaStream_t st) {
+cudaError_t run(const TopSelectArgs& a, int sms, int device, cudaStream_t st) {
   const int K = static_cast<int>(a.K);
   const int cap = capacity(K, Elem<T>::kVec);
   const size_t lists = size_t(cap) * 8 + kBins * 4;
@@ -479,36 +534,22 @@ cudaError_t run(const TopSelectArgs& a, int sms, int device, int l2, cudaStream_
   static std::once_flag once[64];
   static cudaError_t set[64];
   std::call_once(once[device], [&] {
-    set[device] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kStreamSmem);
+    set[device] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   });
   if (set[device] != cudaSuccess) return set[device];
-  const int C = ctas_per_row(a.V, a.dtype, sms, l2);
-  const int stages = static_cast<int>((kStreamSmem / 2 - lists) / (kChunkVecs * 16));
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(C);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(kStreamThreads);
-  cfg.dynamicSmemBytes = size_t(stages) * kChunkVecs * 16 + lists;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.stream = st;
-  int64_t clusters = int64_t(sms) * 2 / C;
-  if (clusters < 1) clusters = 1;
-  if (clusters > a.BT) clusters = a.BT;
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * C));
-  return cudaLaunchKernelEx(&cfg, kernel, a, cap, stages);
+  const int stages = static_cast<int>((kSmem - lists) / (kChunkVecs * 16));
+  int64_t grid = int64_t(sms) * 2;
+  if (grid > a.BT) grid = a.BT;
+  kernel<<<static_cast<unsigned>(grid), kStreamThreads, size_t(stages) * kChunkVecs * 16 + lists,
+           st>>>(a, cap, stages);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_top_select(const TopSelectArgs& a, int sms, int device, int l2,
-                              cudaStream_t st) {
-  return a.dtype == FCT_BF16 ? run<bf16_t>(a, sms, device, l2, st)
-                             : run<float>(a, sms, device, l2, st);
+cudaError_t launch_top_select(const TopSelectArgs& a, int sms, int device, cudaStream_t st) {
+  return a.dtype == FCT_BF16 ? run<bf16_t>(a, sms, device, st)
+                             : run<float>(a, sms, device, st);
 }
 
 }  // namespace fct
