@@ -111,48 +111,66 @@ __device__ __forceinline__ void fill_grad(T* grow, int64_t v0, int64_t v1, float
 
 // ---------------------------------------------------------------- forward
 
-// Shared memory of a CTA: the bits, then the list's student and teacher logits
-// and indices.
-struct Shared {
-  uint32_t* bits;
+// A row's list in shared memory.
+struct Lists {
   float* s;
   float* t;
   int* idx;
 };
-__host__ __device__ constexpr size_t list_bytes(int64_t K) { return size_t(K) * 12; }
+__host__ __device__ constexpr size_t list_bytes(int64_t K) { return size_t(K) * 24; }  // of two rows
 // Words of bits for `vecs` vectors of a row and the elements in none.
 __host__ __device__ constexpr int64_t bit_words(int64_t vecs, int vec) {
   return ((vecs + 2) * vec + 31) / 32 + 1;
 }
 
 // One cluster of C CTAs per row, C fixed by V and the element type.  Each CTA
-// streams its share of the row; every CTA then has the row's sums (the forward
-// alone: CTA 0) from what its peers sent.
+// streams its share of the row.  A warp of its own then works out the row's
+// loss from the warps' states, the list, and what the peers send, while the
+// consumers go on to the next row, whose list they fetched ahead.  (What a row
+// costs beside its bytes was 5.8 us of its CTA's time with one thing after the
+// other.)
 //
-// kGrad: the same CTAs go over their share once more, which L2 still holds,
-// and write the gradient.
+// kGrad: the consumers wait for the row's sums, go over their share once more,
+// which L2 still holds, and write the gradient.
+constexpr int kFwdThreads = kRowThreads + 64;  // consumers, copying warp, finishing warp
+
+struct Turn {  // a row on its way from the consumers to the finishing warp
+  float2 warp_state[kRowWarps];
+  float tg_logit;
+  int bad;
+  Sums sums;
+};
+
 template <typename T, bool kGrad>
-__global__ void __launch_bounds__(kStreamThreads, 2)
+__global__ void __launch_bounds__(kFwdThreads, 2)
     top_forward_kernel(TopArgs a, int words, int stages) {
   constexpr int VE = Elem<T>::kVec, NT = kRowThreads;
   extern __shared__ uint4 top_smem[];
   __shared__ __align__(8) RingBars bars;
   __shared__ __align__(16) Exchange exchange;
-  __shared__ float2 warp_state[kRowWarps];
-  __shared__ Sums sums;
+  // the consumers are done with a row of turn t; its sums are there and its
+  // buffers are free
+  __shared__ __align__(8) uint64_t ready_bar[2], done_bar[2];
+  __shared__ Turn turns[2];
   const int K = static_cast<int>(a.K), V = static_cast<int>(a.V), tid = threadIdx.x;
   const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
-  uint32_t* lists = reinterpret_cast<uint32_t*>(top_smem + stages * kChunkVecs);
-  const Shared sh{lists, reinterpret_cast<float*>(lists + words),
-                  reinterpret_cast<float*>(lists + words) + K,
-                  reinterpret_cast<int*>(lists + words) + 2 * K};
-  const uint8_t* bytes = reinterpret_cast<const uint8_t*>(sh.bits);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(top_smem + stages * kChunkVecs);
+  const uint8_t* bytes = reinterpret_cast<const uint8_t*>(bits);
+  // the lists of two rows: student's and teacher's logits, words
+  auto list = [&](uint32_t turn) {
+    float* p = reinterpret_cast<float*>(bits + words) + (turn & 1u) * 3 * K;
+    return Lists{p, p + K, reinterpret_cast<int*>(p + 2 * K)};
+  };
   Ring ring(&bars, top_smem, stages);
   if (tid == 0) {
     exchange_init(exchange);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ready_bar[i], kRowWarps);
+      mbar_init(&done_bar[i], 1);
+    }
     ring.init();
   }
-  for (int i = tid; i < words; i += kStreamThreads) sh.bits[i] = 0;
+  for (int i = tid; i < words; i += kFwdThreads) bits[i] = 0;
   __syncthreads();
   cluster_barrier();  // every CTA's barriers exist
   const int64_t n_clusters = gridDim.x / C;
@@ -162,7 +180,61 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     *v1 = min(*v0 + per, r.nvec);
   };
 
-  if (tid >= NT) {
+  if (tid >= NT + 32) {  // ---- the finishing warp
+    const int lane = tid & 31;
+    uint32_t turn = 0;
+    for (int64_t row = blockIdx.x / C; row < a.BT; row += n_clusters) {
+      const int64_t tg = a.target[row];
+      if (tg == a.ignore_index) {
+        if (rank == 0 && lane == 0) {
+          a.ce[row] = 0.f;
+          a.tvd[row] = 0.f;
+          a.lse[row] = 0.f;
+          a.rest_lse[row] = 0.f;
+          a.t_lse[row] = 0.f;
+          a.sigma[row] = 0.f;
+        }
+        continue;
+      }
+      const float t_rest = a.rest ? a.rest[row] : -INFINITY;
+      Turn& t = turns[turn & 1u];
+      mbar_wait(&ready_bar[turn & 1u], (turn >> 1) & 1u, &bars.abort);
+      const float2 own = lane < kRowWarps ? t.warp_state[lane] : make_float2(-INFINITY, 0.f);
+      Lse2 rest = merge_warp(Lse2{own.x, own.y});
+      bool wrong = t.bad != 0;
+      if (C > 1) {
+        exchange_send(exchange, turn, C, rank,
+                      make_uint4(__float_as_uint(rest.m2), __float_as_uint(rest.s), wrong, 0u));
+        const uint4 got = exchange_take(exchange, turn, C, &bars.abort);
+        wrong = __any_sync(0xffffffffu, got.z != 0);
+        rest = merge_warp(Lse2{__uint_as_float(got.x), __uint_as_float(got.y)});
+      }
+      if (kGrad || rank == 0) {
+        const Lists l = list(turn);
+        Sums o = list_sums(l.s, l.t, K, rest.m2, rest.s, t_rest);
+        const float nan = __uint_as_float(0x7fc00000u);
+        if (wrong) o = Sums{nan, nan, nan, nan, nan};
+        if (lane == 0) {
+          if constexpr (kGrad) t.sums = o;
+          if (rank == 0) {
+            const bool tg_ok = tg >= 0 && tg < V;
+            a.ce[row] = tg_ok ? o.lse - t.tg_logit : nan;
+            a.tvd[row] = o.tvd;
+            a.lse[row] = o.lse;
+            a.rest_lse[row] = o.rest;
+            a.t_lse[row] = o.t_lse;
+            a.sigma[row] = o.sigma;
+            const int status =
+                (tg_ok ? 0 : FCT_DEV_TARGET_OUT_OF_RANGE) | (wrong ? FCT_DEV_BAD_LIST : 0);
+            if (status && a.dev_status) atomicOr(a.dev_status, status);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&done_bar[turn & 1u]);
+      ++turn;
+    }
+  } else if (tid >= NT) {
     if (tid == NT) {  // ---- copies
       const uint64_t once = policy_evict_first(), first = kGrad ? policy_evict_last() : once;
       uint32_t copied = 0;
@@ -181,159 +253,167 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       }
       ring.drain(copied);
     }
-  } else {
+  } else {  // ---- consumers
     const uint64_t once = policy_evict_first();
     uint32_t turn = 0;
-    for (int64_t row = blockIdx.x / C; row < a.BT; row += n_clusters) {
-      const T* srow = static_cast<const T*>(a.student) + row * a.ld_s;
-      const int64_t tg = a.target[row];
+    // A list entry of a row: its word (-1: not used; -2: no word), and the
+    // logits of both sides.  Fetched a row ahead.
+    struct Entry {
+      int word;
+      float s, t;
+    };
+    auto fetch_word = [&](int64_t row, int k) {
+      if (k >= K) return -1;
+      const int v = a.index[row * a.ld_i + k];
+      return v >= 0 && v < V ? v : v == -1 ? -1 : -2;
+    };
+    auto fetch = [&](int64_t row, int k, int word) {
+      Entry e{word, -INFINITY, -INFINITY};
+      if (word >= 0) {
+        e.s = Elem<T>::load1(static_cast<const T*>(a.student) + row * a.ld_s + word);
+        e.t = a.values[row * a.ld_v + k];
+      }
+      return e;
+    };
+    auto fetch_target = [&](int64_t row) { return row < a.BT ? a.target[row] : a.ignore_index; };
+    auto logit_of = [&](int64_t row, int64_t tg) {
+      return tg >= 0 && tg < V
+                 ? Elem<T>::load1(static_cast<const T*>(a.student) + row * a.ld_s + tg)
+                 : 0.f;
+    };
+    int64_t row = blockIdx.x / C;
+    int64_t tg = fetch_target(row);
+    Entry e{-1, -INFINITY, -INFINITY};
+    float tg_logit = 0.f;
+    if (tg != a.ignore_index) {
+      e = fetch(row, tid, fetch_word(row, tid));
+      tg_logit = logit_of(row, tg);
+    }
+    for (; row < a.BT; row += n_clusters) {
       T* grow = kGrad ? static_cast<T*>(a.grad) + row * a.ld_g : nullptr;
+      const int64_t next_row = row + n_clusters;
+      const int64_t next_tg = fetch_target(next_row);
+      const bool next_live = next_tg != a.ignore_index;
+      int next_word = next_live ? fetch_word(next_row, tid) : -1;
       if (tg == a.ignore_index) {
-        if (rank == 0 && tid == 0) {
-          a.ce[row] = 0.f;
-          a.tvd[row] = 0.f;
-          a.lse[row] = 0.f;
-          a.rest_lse[row] = 0.f;
-          a.t_lse[row] = 0.f;
-          a.sigma[row] = 0.f;
-        }
         if constexpr (kGrad) {
           const int64_t per_cta = (a.V + C - 1) / C;
           fill_grad<NT>(grow, rank * per_cta, min(a.V, (rank + 1) * per_cta), 0.f);
         }
-        continue;
-      }
-      const Row<T> r(srow, V);
-      int v0, v1;
-      share_of(r, &v0, &v1);
-      const bool tg_ok = tg >= 0 && tg < V;
-      // ---- the list: its logits, and the bits of the words in this CTA's share
-      auto mine = [&](int pos) {
-        return (pos >= VE || rank == 0) && (pos < (v1 - v0 + 1) * VE || rank == C - 1);
-      };
-      bool bad = false;
-      for (int k = tid; k < K; k += NT) {
-        const int v = a.index[row * a.ld_i + k];
-        float s = -INFINITY, t = -INFINITY;
-        int at = -1;
-        if (v != -1) {
-          if (v < 0 || v >= V) {
-            bad = true;
-          } else {
-            at = v;
-            s = Elem<T>::load1(srow + v);
-            t = a.values[row * a.ld_v + k];
-            const int pos = v - r.head + VE - v0 * VE;
-            if (mine(pos) && (atomicOr(&sh.bits[pos >> 5], 1u << (pos & 31)) >> (pos & 31) & 1u))
+      } else {
+        const T* srow = static_cast<const T*>(a.student) + row * a.ld_s;
+        const Row<T> r(srow, V);
+        int v0, v1;
+        share_of(r, &v0, &v1);
+        const bool tg_ok = tg >= 0 && tg < V;
+        // ---- the list, and the bits of its words in this CTA's share
+        auto mine = [&](int pos) {
+          return (pos >= VE || rank == 0) && (pos < (v1 - v0 + 1) * VE || rank == C - 1);
+        };
+        Turn& t = turns[turn & 1u];
+        const Lists l = list(turn);
+        if (turn >= 2)  // the row of two turns ago has left these buffers
+          mbar_wait(&done_bar[turn & 1u], ((turn >> 1) - 1) & 1u, &bars.abort);
+        bool bad = false;
+        auto enter = [&](int k, const Entry& x) {
+          if (x.word == -2) bad = true;
+          if (x.word >= 0) {
+            const int pos = x.word - r.head + VE - v0 * VE;
+            if (mine(pos) && (atomicOr(&bits[pos >> 5], 1u << (pos & 31)) >> (pos & 31) & 1u))
               bad = true;
           }
-        }
-        sh.s[k] = s;
-        sh.t[k] = t;
-        sh.idx[k] = at;
-      }
-      const float tg_logit = tg_ok ? Elem<T>::load1(srow + tg) : 0.f;
-      bad = row_or(bad);
-      // ---- the log-sum-exp of the words outside U
-      Run st = run_empty();
-      const uint8_t* own_bytes = bytes - v0 * VE / 8;
-      ring.template each_warp<T>(v0, v1, [&](uint4 w, int iv) {
-        float x[VE];
-        Elem<T>::unpack(w, x);
-        float vm = vec_max(x);
-        // (past the share's end: within the bits' room, or of no matter)
-        const int at = VE == 8 ? iv + 1 : (iv + 1) >> 1;
-        uint32_t m = iv < v1 ? own_bytes[at] : 0u;
-        if (VE == 4) m = (m >> (4 * ((iv + 1) & 1))) & 15u;
-        if (__any_sync(0xffffffffu, m != 0 || vm > st.limit)) {  // seldom
+          l.s[k] = x.s;
+          l.t[k] = x.t;
+          l.idx[k] = x.word;
+        };
+        if (tid < K) enter(tid, e);
+        for (int k = tid + NT; k < K; k += NT) enter(k, fetch(row, k, fetch_word(row, k)));
+        bad = row_or(bad);
+        // ---- the log-sum-exp of the words outside U
+        Run st = run_empty();
+        const uint8_t* own_bytes = bytes - v0 * VE / 8;
+        ring.template each_warp<T>(v0, v1, [&](uint4 w, int iv) {
+          float x[VE];
+          Elem<T>::unpack(w, x);
+          float vm = vec_max(x);
+          // (past the share's end: within the bits' room, or of no matter)
+          const int at = VE == 8 ? iv + 1 : (iv + 1) >> 1;
+          uint32_t m = iv < v1 ? own_bytes[at] : 0u;
+          if (VE == 4) m = (m >> (4 * ((iv + 1) & 1))) & 15u;
+          if (__any_sync(0xffffffffu, m != 0 || vm > st.limit)) {  // seldom
 #pragma unroll
-          for (int j = 0; j < VE; ++j)
-            if ((m >> j) & 1u) x[j] = -INFINITY;
-          vm = vec_max(x);
-          raise(st, vm);
+            for (int j = 0; j < VE; ++j)
+              if ((m >> j) & 1u) x[j] = -INFINITY;
+            vm = vec_max(x);
+            raise(st, vm);
+          }
+          add(st, x);
+        });
+        // the elements in no vector: the head with CTA 0, the tail with the last
+        if (tid < r.n_loose() && rank == (tid < r.head ? 0 : C - 1)) {
+          const int v = r.loose(tid), pos = v - r.head + VE - v0 * VE;
+          const float x = Elem<T>::load1(srow + v);
+          const float one[2] = {(bits[pos >> 5] >> (pos & 31)) & 1u ? -INFINITY : x, -INFINITY};
+          fold(st, one);
         }
-        add(st, x);
-      });
-      // the elements in no vector: the head with CTA 0, the tail with the last
-      if (tid < r.n_loose() && rank == (tid < r.head ? 0 : C - 1)) {
-        const int v = r.loose(tid), pos = v - r.head + VE - v0 * VE;
-        const float x = Elem<T>::load1(srow + v);
-        const float one[2] = {(sh.bits[pos >> 5] >> (pos & 31)) & 1u ? -INFINITY : x, -INFINITY};
-        fold(st, one);
-      }
-      const Lse2 w = merge_warp(folded(st));
-      if ((tid & 31) == 0) warp_state[tid >> 5] = make_float2(w.m2, w.s);
-      row_sync();
-      // the bits go back to 0 for the next row
-      for (int k = tid; k < K; k += NT) {
-        const int pos = sh.idx[k] - r.head + VE - v0 * VE;
-        if (sh.idx[k] >= 0 && pos >= 0 && pos < words * 32) sh.bits[pos >> 5] = 0;
-      }
-      if (tid < 32) {
-        const float2 own = tid < kRowWarps ? warp_state[tid] : make_float2(-INFINITY, 0.f);
-        Lse2 rest = merge_warp(Lse2{own.x, own.y});
-        bool wrong = bad;
-        if (C > 1) {
-          exchange_send(exchange, turn, C, rank,
-                        make_uint4(__float_as_uint(rest.m2), __float_as_uint(rest.s), bad, 0u));
-          const uint4 got = exchange_take(exchange, turn, C, &bars.abort);
-          wrong = __any_sync(0xffffffffu, got.z != 0);
-          rest = merge_warp(Lse2{__uint_as_float(got.x), __uint_as_float(got.y)});
+        const Lse2 w = merge_warp(folded(st));
+        if ((tid & 31) == 0) t.warp_state[tid >> 5] = make_float2(w.m2, w.s);
+        if (tid == 0) {
+          t.bad = bad;
+          t.tg_logit = tg_logit;
         }
-        if (kGrad || rank == 0) {
-          const float t_rest = a.rest ? a.rest[row] : -INFINITY;
-          Sums o = list_sums(sh.s, sh.t, K, rest.m2, rest.s, t_rest);
-          const float nan = __uint_as_float(0x7fc00000u);
-          if (wrong) o = Sums{nan, nan, nan, nan, nan};
-          if (tid == 0) {
-            if (rank == 0) {
-              a.ce[row] = tg_ok ? o.lse - tg_logit : nan;
-              a.tvd[row] = o.tvd;
-              a.lse[row] = o.lse;
-              a.rest_lse[row] = o.rest;
-              a.t_lse[row] = o.t_lse;
-              a.sigma[row] = o.sigma;
-              const int status =
-                  (tg_ok ? 0 : FCT_DEV_TARGET_OUT_OF_RANGE) | (wrong ? FCT_DEV_BAD_LIST : 0);
-              if (status && a.dev_status) atomicOr(a.dev_status, status);
+        __syncwarp();
+        if ((tid & 31) == 0) mbar_arrive(&ready_bar[turn & 1u]);
+        const float this_logit = tg_logit;
+        // the next row's list is on its way while this one's sums are worked out
+        if (next_live) {
+          e = fetch(next_row, tid, next_word);
+          tg_logit = logit_of(next_row, next_tg);
+        }
+        row_sync();  // the bits are read: back to 0 for the next row
+        for (int k = tid; k < K; k += NT) {
+          const int pos = l.idx[k] - r.head + VE - v0 * VE;
+          if (l.idx[k] >= 0 && pos >= 0 && pos < words * 32) bits[pos >> 5] = 0;
+        }
+        if constexpr (kGrad) {
+          if (!tg_ok) {
+            const int64_t per_cta = (a.V + C - 1) / C;
+            fill_grad<NT>(grow, rank * per_cta, min(a.V, (rank + 1) * per_cta),
+                          __uint_as_float(0x7fc00000u));
+          } else {
+            mbar_wait(&done_bar[turn & 1u], (turn >> 1) & 1u, &bars.abort);
+            const Sums sums = t.sums;
+            const Coefs c = make_coefs(a.grad_ce[row * a.grad_stride],
+                                       a.grad_tvd[row * a.grad_stride], sums.lse, sums.rest,
+                                       sums.t_lse, a.rest ? a.rest[row] : -INFINITY, sums.sigma);
+            const Outside o(c);
+            const bool same = same_alignment(srow, grow);
+            ring.each(v0, v1, [&](uint4 w, int iv) {
+              vector_grad(o, w, grow + r.head + iv * VE, same, once);
+            });
+            loose_grad(r, grow, o, rank == 0, rank == C - 1);
+            // the words of U and the target over what was written there
+            bool listed = false;
+            for (int k = tid; k < K; k += NT) listed = listed || l.idx[k] == tg;
+            listed = row_or(listed);
+            for (int k = tid; k < K; k += NT) {
+              const int v = l.idx[k];
+              if (v >= 0 && mine(v - r.head + VE - v0 * VE))
+                Elem<T>::store1(grow + v, listed_grad(c, l.s[k], l.t[k], v == tg));
             }
-            if constexpr (kGrad) sums = o;
+            const int at = static_cast<int>(tg);
+            if (tid == 0 && !listed && mine(at - r.head + VE - v0 * VE))
+              Elem<T>::store1(grow + at, target_grad(c, this_logit));
           }
         }
+        row_sync();  // all bits are 0, and in the gradient's case the list is read
+        ++turn;
       }
-      ++turn;
-      row_sync();
-      if constexpr (kGrad) {
-        if (!tg_ok) {
-          const int64_t per_cta = (a.V + C - 1) / C;
-          fill_grad<NT>(grow, rank * per_cta, min(a.V, (rank + 1) * per_cta),
-                        __uint_as_float(0x7fc00000u));
-          row_sync();
-          continue;
-        }
-        const Coefs c = make_coefs(a.grad_ce[row * a.grad_stride], a.grad_tvd[row * a.grad_stride],
-                                   sums.lse, sums.rest, sums.t_lse,
-                                   a.rest ? a.rest[row] : -INFINITY, sums.sigma);
-        const Outside o(c);
-        const bool same = same_alignment(srow, grow);
-        ring.each(v0, v1, [&](uint4 w, int iv) {
-          vector_grad(o, w, grow + r.head + iv * VE, same, once);
-        });
-        loose_grad(r, grow, o, rank == 0, rank == C - 1);
-        // the words of U and the target over what was written there
-        bool listed = false;
-        for (int k = tid; k < K; k += NT) listed = listed || sh.idx[k] == tg;
-        listed = row_or(listed);
-        for (int k = tid; k < K; k += NT) {
-          const int v = sh.idx[k];
-          if (v >= 0 && mine(v - r.head + VE - v0 * VE))
-            Elem<T>::store1(grow + v, listed_grad(c, sh.s[k], sh.t[k], v == tg));
-        }
-        const int at = static_cast<int>(tg);
-        if (tid == 0 && !listed && mine(at - r.head + VE - v0 * VE))
-          Elem<T>::store1(grow + at, target_grad(c, tg_logit));
-        row_sync();  // the list and the sums are read: the next row may come
+      if (tg == a.ignore_index && next_live) {
+        e = fetch(next_row, tid, next_word);
+        tg_logit = logit_of(next_row, next_tg);
       }
+      tg = next_tg;
     }
   }
   __syncthreads();
@@ -454,7 +534,7 @@ cudaError_t run_forward(const TopArgs& a, int sms, int device, int l2, cudaStrea
   attr[0].val.clusterDim.x = static_cast<unsigned>(C);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(kStreamThreads);
+  cfg.blockDim = dim3(kFwdThreads);
   cfg.dynamicSmemBytes = size_t(stages) * kChunkVecs * 16 + lists;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
