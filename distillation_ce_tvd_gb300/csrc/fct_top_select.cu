@@ -46,9 +46,10 @@ constexpr int kWarps = kRowWarps;
 constexpr int kBins = 1024;
 // Up to this K a thread's part has one maximum, above it one per vector of a
 // chunk: the maxima have to be several times K for the threshold to be near
-// the K-th logit.  A warp looks at 128 of them.
+// the K-th logit.  A warp looks at 512 of them.
 constexpr int kFewMaxima = 96;
-constexpr int kPool = 128;
+constexpr int kPool = 512;
+constexpr int kPerLane = kPool / 32;
 
 // A selection may keep this many more than K: it need not split a bin.
 __host__ __device__ constexpr int slack(int K) { return K / 4 + 64; }
@@ -57,7 +58,7 @@ constexpr int kRound = 256;  // vectors of a round
 __host__ __device__ constexpr int capacity(int K, int vec) {
   return K + slack(K) + kRound * vec;
 }
-constexpr int kQueue = 64;  // vectors that wait, per warp
+constexpr int kQueue = 32 + 32 * kPerThread;  // vectors that wait, per warp
 
 // Unsigned key that increases with the float (no NaN comes here; -0 is +0).
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -80,9 +81,18 @@ __device__ __forceinline__ uint64_t rank_key(uint32_t key, int idx) {
   return (uint64_t(key) << 32) | uint32_t(~idx);
 }
 
+// Element j of a vector.
+__device__ __forceinline__ float element(uint4 w, int j, float) {
+  return __uint_as_float(j & 2 ? (j & 1 ? w.w : w.z) : (j & 1 ? w.y : w.x));
+}
+__device__ __forceinline__ float element(uint4 w, int j, bf16_t) {
+  const uint32_t two = j & 4 ? (j & 2 ? w.w : w.z) : (j & 2 ? w.y : w.x);
+  return __uint_as_float(j & 1 ? two & 0xffff0000u : two << 16);
+}
+
 struct Shared {
   uint64_t* entry;  // [cap] rank keys of the candidates
-  int* hist;        // [kBins]
+  int* hist;        // [kBins]; at a row's end, the few entries that are ordered by counting
 };
 __device__ __forceinline__ float entry_value(uint64_t e) {
   return value_of(static_cast<uint32_t>(e >> 32));
@@ -100,8 +110,11 @@ struct Scratch {  // static shared memory of a CTA
   uint32_t drop_key;
   unsigned long long drop_sum;
   float2 warp_state[kWarps];
-  uint16_t maxima[kPerThread * kThreads];  // the top halves of the maxima's keys
+  __align__(16) uint16_t maxima[kPerThread * kThreads];  // the top halves of the maxima's keys
   uint32_t pool_key[2][kWarps];
+  int left[kWarps];
+  uint64_t kth;   // the K-th entry, 0 if there are fewer
+  uint64_t highest;
   int queue[kWarps][kQueue];
 };
 
@@ -225,21 +238,22 @@ __device__ __noinline__ int select(const Shared& sh, Scratch& sc, int n, int K, 
 
 // Up to this many entries are ordered by counting, more by sorting.
 constexpr int kCountMax = 192;
+static_assert(kCountMax * 8 <= kBins * 4, "they are in the histogram's place");
 
-// Orders n <= kCountMax entries: an entry's place is the number that rank
-// before it, counted by as many threads per entry as there are.
-__device__ __forceinline__ void count_entries(const Shared& sh, int n) {
+// n <= kCountMax entries: f(place, entry) by one thread for each, its place the
+// number that rank before it, counted by as many threads per entry as there are.
+template <typename F>
+__device__ __forceinline__ void count_entries(const uint64_t* entry, int n, F f) {
   const int tid = threadIdx.x;
   const int parts = n <= 32 ? 16 : n <= 64 ? 8 : n <= 128 ? 4 : 2;
   const int i = tid / parts, part = tid % parts;
-  const uint64_t own = i < n ? sh.entry[i] : ~0ull;
+  if ((tid & ~31) / parts >= n) return;  // nothing for the whole warp
+  const uint64_t own = i < n ? entry[i] : ~0ull;
   int place = 0;
 #pragma unroll 8
-  for (int j = part; j < n; j += parts) place += sh.entry[j] > own;
+  for (int j = part; j < n; j += parts) place += entry[j] > own;
   for (int d = 1; d < parts; d *= 2) place += __shfl_xor_sync(0xffffffffu, place, d);
-  row_sync();
-  if (i < n && part == 0) sh.entry[place] = own;
-  row_sync();
+  if (i < n && part == 0) f(place, own);
 }
 
 // Sorts n entries, highest rank first (bitonic, a power of two of them: the
@@ -281,18 +295,25 @@ __device__ __noinline__ void sort_entries(const Shared& sh, int n) {
   }
 }
 
-// The largest t such that `want` of the warp's values reach it (0: fewer than
-// that are above -inf): a bit a round.
-template <int N>
-__device__ __forceinline__ uint32_t warp_threshold(const uint32_t (&key)[N], int want) {
-  uint32_t t = 0;
-#pragma unroll 4
-  for (int bit = 15; bit >= 0; --bit) {
-    const uint32_t trial = t | (1u << bit);
+// The largest t such that `want` of the warp's values reach it: a bit a round,
+// from the first that is not the same in all.
+__device__ __forceinline__ uint32_t warp_threshold(const uint32_t (&key)[kPerLane], int want) {
+  uint32_t lo = key[0], hi = key[0];
+#pragma unroll
+  for (int u = 1; u < kPerLane; ++u) {
+    lo = min(lo, key[u]);
+    hi = max(hi, key[u]);
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  uint32_t bit = lo == hi ? 0u : 1u << (31 - __clz(static_cast<int>(lo ^ hi)));
+  uint32_t t = bit == 0u ? lo : lo & ~(2u * bit - 1u);
+  for (; bit != 0u; bit >>= 1) {
+    const uint32_t trial = t | bit;
     int c = 0;
 #pragma unroll
-    for (int u = 0; u < N; ++u) c += __popc(__ballot_sync(0xffffffffu, key[u] >= trial));
-    if (c >= want) t = trial;
+    for (int u = 0; u < kPerLane; ++u) c += key[u] >= trial;
+    if (static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(c))) >= want) t = trial;
   }
   return t;
 }
@@ -342,13 +363,18 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       auto take = [&](uint4 raw, int i) {
         float x[VE];
         Elem<T>::unpack(raw, x);
-        const int e0 = r.head + i * VE;
+        uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < VE; ++j)
+        for (int j = 0; j < VE; ++j) {
           if (x[j] > thr) {
-            push(x[j], e0 + j);
+            m |= 1u << j;
             x[j] = -INFINITY;
           }
+        }
+        for (; m != 0; m &= m - 1) {
+          const int j = __ffs(static_cast<int>(m)) - 1;
+          push(element(raw, j, T{}), r.head + i * VE + j);
+        }
         fold(st, x);
       };
       auto take_loose = [&](int v) {
@@ -360,19 +386,16 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
           fold(st, one);
         }
       };
-      // the first n vectors of the warp's queue, one per lane
-      auto digest = [&](int n) {
+      // the first 32 vectors of the warp's queue, one per lane
+      auto digest = [&]() {
         __syncwarp();
-        if (lane < n) {
-          const int i = sc.queue[warp][lane];
-          take(*r.vec(i), i);
-        }
+        const int i = sc.queue[warp][lane];
+        take(*r.vec(i), i);
         __syncwarp();
-        if (lane + n < waiting) {
-          const int i = sc.queue[warp][lane + n];
-          sc.queue[warp][lane] = i;
+        waiting -= 32;
+        for (int q = lane; q < waiting; q += 32) {  // (a lane's own places, front to back)
+          sc.queue[warp][q] = sc.queue[warp][q + 32];
         }
-        waiting -= n;
         __syncwarp();
       };
       float mx[kPerThread];
@@ -394,8 +417,18 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         row_sync();
         uint32_t* keys = sc.pool_key[found++ & 1u];
         if (warp < pools) {
-          const uint16_t* m = sc.maxima + warp * kPool + lane;
-          const uint32_t key[4] = {m[0], m[32], m[64], m[96]};
+          const uint4* m = reinterpret_cast<const uint4*>(sc.maxima + warp * kPool) + lane;
+          uint32_t key[kPerLane];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint4 k8 = m[q * 32];
+            const uint32_t two[4] = {k8.x, k8.y, k8.z, k8.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              key[q * 8 + 2 * j] = two[j] & 0xffffu;
+              key[q * 8 + 2 * j + 1] = two[j] >> 16;
+            }
+          }
           const uint32_t t = warp_threshold(key, (K + pools - 1) / pools);
           if (lane == 0) keys[warp] = t << 16;
         }
@@ -426,6 +459,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       bool full = false;  // more candidates came than there is room for
       for (int c = 0; c < r.nvec; c += kChunkVecs) {
         const uint4* p = ring.wait() + tid;
+        const bool whole = c + kChunkVecs <= r.nvec;
         auto vec = [&](int u) {
           return c + u * kThreads + tid < r.nvec ? p[u * kThreads] : nothing<T>();
         };
@@ -439,10 +473,9 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
           raise_threshold();
         }
         float unusual = fminf(thr, st.limit);  // a vector with nothing above it is just added
-#pragma unroll
-        for (int u = 0; u < kPerThread; ++u) {
+        auto step = [&](uint4 w, int u) {
           float x[VE];
-          Elem<T>::unpack(vec(u), x);
+          Elem<T>::unpack(w, x);
           const float vm = vec_max(x);
           mx[u] = fmaxf(mx[u], vm);
           bool above = false;
@@ -453,21 +486,42 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
             if (above)
               sc.queue[warp][waiting + __popc(b & ((1u << lane) - 1u))] = c + u * kThreads + tid;
             waiting += __popc(b);
-            if (waiting >= 32) digest(32);
             unusual = fminf(thr, st.limit);
           }
           if (!above) add(st, x);
+        };
+        if (whole) {
+#pragma unroll
+          for (int u = 0; u < kPerThread; ++u) step(p[u * kThreads], u);
+        } else {
+#pragma unroll
+          for (int u = 0; u < kPerThread; ++u) step(vec(u), u);
         }
+        while (waiting >= 32) digest();
         ring.release();
         ++chunks;
         // (always the same decision in all warps)
         const bool doubled = (chunks & (chunks - 1)) == 0;
         if (doubled || K > kFewMaxima) {
-          if (doubled && chunks > 1 && c + kChunkVecs < r.nvec) raise_threshold();
+          // (not where little is left that a better one would spare)
+          if (doubled && chunks > 1 && r.nvec - c > (chunks / 2 + 1) * kChunkVecs) raise_threshold();
           if (!full) full = room(kRound * VE, false) > cap;
         }
       }
-      digest(waiting);
+      // what still waits, of all warps together, against the row's threshold
+      if (lane == 0) sc.left[warp] = waiting;
+      raise_threshold();
+      {
+        const int count = lane < kWarps ? sc.left[lane] : 0;
+        const int ahead = static_cast<int>(
+            __reduce_add_sync(0xffffffffu, lane < warp ? count : 0));
+        const int total = static_cast<int>(__reduce_add_sync(0xffffffffu, count));
+        int* flat = reinterpret_cast<int*>(sc.maxima);  // (has been read)
+        if (lane < waiting) flat[ahead + lane] = sc.queue[warp][lane];
+        row_sync();
+        if (tid < total) take(*r.vec(flat[tid]), flat[tid]);
+        __syncwarp();
+      }
       int n = room(VE, false);
       full = full || n > cap;
       if (!full) {
@@ -486,33 +540,68 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         room(VE, true);
         if (r.tail0 + tid < V) take_loose(r.tail0 + tid);
       }
-      row_sync();
-      n = sc.pushed;
-      if (n > K + slack(K)) {
-        uint32_t least;
-        n = select(sh, sc, n, K, dropped, least);
-      }
       const Lse2 w = merge_warp(folded(st));
       if (lane == 0) sc.warp_state[warp] = make_float2(w.m2, w.s);
-      row_sync();
-      if (n <= kCountMax)
-        count_entries(sh, n);
-      else
-        sort_entries(sh, n);
-      for (int i = tid; i < K; i += kThreads) {
-        const uint64_t e = i < n ? sh.entry[i] : 0;
-        a.values[row * a.ld_v + i] = i < n ? entry_value(e) : -INFINITY;
-        a.index[row * a.ld_i + i] = i < n ? entry_index(e) : -1;
+      if (tid == 0) {
+        sc.kept = 0;
+        sc.kth = 0;
       }
-      if (n > K) drop(sh, sc, K, n, dropped, [](uint64_t) { return true; });
+      row_sync();
+      n = sc.pushed;
+      // those above the threshold: K of them, or hardly more, or all there are
+      uint64_t* few = reinterpret_cast<uint64_t*>(sh.hist);
+      if (!full) {
+        for (int i = tid; i < n; i += kThreads) {
+          const uint64_t e = sh.entry[i];
+          if (entry_value(e) > thr) {
+            const int at = atomicAdd(&sc.kept, 1);
+            if (at < kCountMax) few[at] = e;
+          }
+        }
+        row_sync();
+      }
+      const int kept = sc.kept;
+      uint64_t highest = 0;
+      if (!full && kept <= kCountMax) {
+        count_entries(few, kept, [&](int place, uint64_t e) {
+          if (place < K) {
+            a.values[row * a.ld_v + place] = entry_value(e);
+            a.index[row * a.ld_i + place] = entry_index(e);
+          }
+          if (place == K - 1) sc.kth = e;
+          if (place == 0) sc.highest = e;
+        });
+        for (int i = kept + tid; i < K; i += kThreads) {
+          a.values[row * a.ld_v + i] = -INFINITY;
+          a.index[row * a.ld_i + i] = -1;
+        }
+        row_sync();
+        const uint64_t kth = sc.kth;
+        drop(sh, sc, 0, n, dropped, [&](uint64_t e) { return e < kth; });
+        highest = kept > 0 ? sc.highest : 0;
+      } else {
+        row_sync();  // sc.kept is read
+        if (n > K + slack(K)) {
+          uint32_t least;
+          n = select(sh, sc, n, K, dropped, least);
+        }
+        sort_entries(sh, n);
+        for (int i = tid; i < K; i += kThreads) {
+          const uint64_t e = i < n ? sh.entry[i] : 0;
+          a.values[row * a.ld_v + i] = i < n ? entry_value(e) : -INFINITY;
+          a.index[row * a.ld_i + i] = i < n ? entry_index(e) : -1;
+        }
+        if (n > K) drop(sh, sc, K, n, dropped, [](uint64_t) { return true; });
+        highest = n > 0 ? sh.entry[0] : 0;
+      }
       if (warp == 0) {
         const float2 own = lane < kWarps ? sc.warp_state[lane] : make_float2(-INFINITY, 0.f);
         const Lse2 rest = merge(merge_warp(Lse2{own.x, own.y}), Lse2{dropped.x, dropped.y});
         if (lane == 0) {
-          const bool inf = n > 0 && entry_value(sh.entry[0]) == INFINITY;
+          const bool inf = highest != 0 && entry_value(highest) == INFINITY;
           const float out = inf ? __uint_as_float(0x7fc00000u) : finish(rest.m2, rest.s);
           a.rest[row] = out;
-          if ((out != out || n == 0) && a.dev_status)
+          if ((out != out || highest == 0) && a.dev_status)
             atomicOr(a.dev_status, FCT_DEV_NO_DISTRIBUTION);
         }
       }
