@@ -158,43 +158,31 @@ __host__ __device__ constexpr int64_t share(int64_t nvec, int C) {
 
 // ---------------------------------------------------------------- streaming rows
 
-// CTAs that stream rows have kRowThreads consumers and a warp that copies for
-// them (TMA bulk copies into a ring of shared memory).  That warp runs ahead,
-// into a row's second sweep and into the next row, so that copies are in
-// flight while the consumers look up lists, reduce and write results: with
-// loads of their own into registers, 64 KB in flight per SM only while
-// streaming, the single launch took 643 us at 1021 x 256000 fp32, half of the
-// memory's rate.  Barriers of the consumers are named (1): the copying warp
-// takes no part.
-constexpr int kRowThreads = 512;
-constexpr int kRowWarps = kRowThreads / 32;
-constexpr int kStreamThreads = kRowThreads + 32;
-constexpr int kPerThread = 4;                              // vectors of a chunk per thread
-constexpr int kChunkVecs = kPerThread * kRowThreads;       // 32 KB
+// CTAs that stream rows have NT consumers and a warp that copies for them (TMA
+// bulk copies into a ring of shared memory).  That warp runs ahead, into a
+// row's second sweep and into the next row, so that copies are in flight while
+// the consumers look up lists, reduce and write results: with loads of their
+// own into registers, 64 KB in flight per SM only while streaming, the single
+// launch took 643 us at 1021 x 256000 fp32, half of the memory's rate.
+// Barriers of the consumers are named (1): the other warps take no part.
+constexpr int kPerThread = 4;  // vectors of a chunk per consumer
 constexpr int kMaxStages = 6;
 
-__device__ __forceinline__ void row_sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+template <int NT>
+__device__ __forceinline__ void row_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory");
+}
+template <int NT>
 __device__ __forceinline__ bool row_or(bool b) {
   int r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, 1, 512, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+      "bar.red.or.pred q, 1, %2, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(static_cast<int>(b))
+      : "r"(static_cast<int>(b)), "n"(NT)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ int row_count(bool b) {
-  int r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-      "bar.red.popc.u32 %0, 1, 512, p;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<int>(b))
-      : "memory");
-  return r;
-}
-static_assert(kRowThreads == 512, "the barriers above");
 
 // A vector of -inf.
 template <typename T>
@@ -208,9 +196,11 @@ struct RingBars {
   uint64_t full[kMaxStages], empty[kMaxStages];
   int abort;
 };
+template <int NT>
 struct Ring {
+  static constexpr int kChunk = kPerThread * NT;  // vectors
   RingBars* bars;
-  uint4* buf;  // stages x kChunkVecs, 16-byte aligned
+  uint4* buf;  // stages x kChunk, 16-byte aligned
   int stages;
   int slot = 0;
   uint32_t phase = 0;
@@ -219,7 +209,7 @@ struct Ring {
   __device__ __forceinline__ void init() {
     for (int s = 0; s < stages; ++s) {
       mbar_init(&bars->full[s], 1);
-      mbar_init(&bars->empty[s], kRowWarps);
+      mbar_init(&bars->empty[s], NT / 32);
     }
     bars->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -234,13 +224,13 @@ struct Ring {
   // wait ran out.
   template <typename T>
   __device__ __forceinline__ bool copy(const Row<T>& r, int v0, int v1, uint64_t pol) {
-    for (int c = v0; c < v1; c += kChunkVecs) {
+    for (int c = v0; c < v1; c += kChunk) {
       if (!mbar_wait(&bars->empty[slot], phase ^ 1u, &bars->abort)) return false;
-      const uint32_t bytes = static_cast<uint32_t>(min(kChunkVecs, v1 - c)) * 16u;
+      const uint32_t bytes = static_cast<uint32_t>(min(kChunk, v1 - c)) * 16u;
       mbar_arrive_expect_tx(&bars->full[slot], bytes);
       asm volatile(
           "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-          " [%0], [%1], %2, [%3], %4;" ::"r"(smem_addr(buf + slot * kChunkVecs)),
+          " [%0], [%1], %2, [%3], %4;" ::"r"(smem_addr(buf + slot * kChunk)),
           "l"(__cvta_generic_to_global(r.vec(c))), "r"(bytes), "r"(smem_addr(&bars->full[slot])),
           "l"(pol)
           : "memory");
@@ -258,7 +248,7 @@ struct Ring {
   // Consumers: the next chunk, and its release.
   __device__ __forceinline__ const uint4* wait() {
     mbar_wait(&bars->full[slot], phase, &bars->abort);
-    return buf + slot * kChunkVecs;
+    return buf + slot * kChunk;
   }
   __device__ __forceinline__ void release() {
     __syncwarp();
@@ -270,16 +260,16 @@ struct Ring {
   template <typename T, typename F>
   __device__ __forceinline__ void each_warp(int v0, int v1, F f) {
     const int tid = threadIdx.x;
-    for (int c = v0; c < v1; c += kChunkVecs) {
+    for (int c = v0; c < v1; c += kChunk) {
       const uint4* p = wait() + tid;
-      if (c + kChunkVecs <= v1) {
+      if (c + kChunk <= v1) {
 #pragma unroll
-        for (int u = 0; u < kPerThread; ++u) f(p[u * kRowThreads], c + u * kRowThreads + tid);
+        for (int u = 0; u < kPerThread; ++u) f(p[u * NT], c + u * NT + tid);
       } else {
 #pragma unroll
         for (int u = 0; u < kPerThread; ++u) {
-          const int i = c + u * kRowThreads + tid;
-          f(i < v1 ? p[u * kRowThreads] : nothing<T>(), i);
+          const int i = c + u * NT + tid;
+          f(i < v1 ? p[u * NT] : nothing<T>(), i);
         }
       }
       release();
@@ -289,23 +279,25 @@ struct Ring {
   template <typename F>
   __device__ __forceinline__ void each(int v0, int v1, F f) {
     const int tid = threadIdx.x;
-    for (int c = v0; c < v1; c += kChunkVecs) {
+    for (int c = v0; c < v1; c += kChunk) {
       const uint4* p = wait() + tid;
-      if (c + kChunkVecs <= v1) {
+      if (c + kChunk <= v1) {
 #pragma unroll
-        for (int u = 0; u < kPerThread; ++u) f(p[u * kRowThreads], c + u * kRowThreads + tid);
+        for (int u = 0; u < kPerThread; ++u) f(p[u * NT], c + u * NT + tid);
       } else {
 #pragma unroll
         for (int u = 0; u < kPerThread; ++u)
-          if (c + u * kRowThreads + tid < v1) f(p[u * kRowThreads], c + u * kRowThreads + tid);
+          if (c + u * NT + tid < v1) f(p[u * NT], c + u * NT + tid);
       }
       release();
     }
   }
 };
 // Chunks of a share.
+template <int NT>
 __device__ __forceinline__ uint32_t chunks_of(int v0, int v1) {
-  return v1 > v0 ? static_cast<uint32_t>((v1 - v0 + kChunkVecs - 1) / kChunkVecs) : 0u;
+  constexpr int n = Ring<NT>::kChunk;
+  return v1 > v0 ? static_cast<uint32_t>((v1 - v0 + n - 1) / n) : 0u;
 }
 
 // What CTAs of a cluster tell each other about a row: 16 bytes each, sent to

@@ -132,10 +132,12 @@ __host__ __device__ constexpr int64_t bit_words(int64_t vecs, int vec) {
 //
 // kGrad: the consumers wait for the row's sums, go over their share once more,
 // which L2 still holds, and write the gradient.
-constexpr int kFwdThreads = kRowThreads + 64;  // consumers, copying warp, finishing warp
+constexpr int kFwdConsumers = 512;
+constexpr int kFwdChunk = Ring<kFwdConsumers>::kChunk;
+constexpr int kFwdThreads = kFwdConsumers + 64;  // consumers, copying warp, finishing warp
 
 struct Turn {  // a row on its way from the consumers to the finishing warp
-  float2 warp_state[kRowWarps];
+  float2 warp_state[kFwdConsumers / 32];
   float tg_logit;
   int bad;
   Sums sums;
@@ -144,7 +146,7 @@ struct Turn {  // a row on its way from the consumers to the finishing warp
 template <typename T, bool kGrad>
 __global__ void __launch_bounds__(kFwdThreads, 2)
     top_forward_kernel(TopArgs a, int words, int stages) {
-  constexpr int VE = Elem<T>::kVec, NT = kRowThreads;
+  constexpr int VE = Elem<T>::kVec, NT = kFwdConsumers;
   extern __shared__ uint4 top_smem[];
   __shared__ __align__(8) RingBars bars;
   __shared__ __align__(16) Exchange exchange;
@@ -154,18 +156,18 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   __shared__ Turn turns[2];
   const int K = static_cast<int>(a.K), V = static_cast<int>(a.V), tid = threadIdx.x;
   const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
-  uint32_t* bits = reinterpret_cast<uint32_t*>(top_smem + stages * kChunkVecs);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(top_smem + stages * kFwdChunk);
   const uint8_t* bytes = reinterpret_cast<const uint8_t*>(bits);
   // the lists of two rows: student's and teacher's logits, words
   auto list = [&](uint32_t turn) {
     float* p = reinterpret_cast<float*>(bits + words) + (turn & 1u) * 3 * K;
     return Lists{p, p + K, reinterpret_cast<int*>(p + 2 * K)};
   };
-  Ring ring(&bars, top_smem, stages);
+  Ring<NT> ring(&bars, top_smem, stages);
   if (tid == 0) {
     exchange_init(exchange);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ready_bar[i], kRowWarps);
+      mbar_init(&ready_bar[i], kFwdConsumers / 32);
       mbar_init(&done_bar[i], 1);
     }
     ring.init();
@@ -199,7 +201,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       const float t_rest = a.rest ? a.rest[row] : -INFINITY;
       Turn& t = turns[turn & 1u];
       mbar_wait(&ready_bar[turn & 1u], (turn >> 1) & 1u, &bars.abort);
-      const float2 own = lane < kRowWarps ? t.warp_state[lane] : make_float2(-INFINITY, 0.f);
+      const float2 own = lane < kFwdConsumers / 32 ? t.warp_state[lane] : make_float2(-INFINITY, 0.f);
       Lse2 rest = merge_warp(Lse2{own.x, own.y});
       bool wrong = t.bad != 0;
       if (C > 1) {
@@ -245,10 +247,10 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         int v0, v1;
         share_of(r, &v0, &v1);
         if (!ring.copy(r, v0, v1, first)) break;
-        copied += chunks_of(v0, v1);
+        copied += chunks_of<NT>(v0, v1);
         if (kGrad && tg >= 0 && tg < V) {
           if (!ring.copy(r, v0, v1, once)) break;
-          copied += chunks_of(v0, v1);
+          copied += chunks_of<NT>(v0, v1);
         }
       }
       ring.drain(copied);
@@ -328,7 +330,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         };
         if (tid < K) enter(tid, e);
         for (int k = tid + NT; k < K; k += NT) enter(k, fetch(row, k, fetch_word(row, k)));
-        bad = row_or(bad);
+        bad = row_or<NT>(bad);
         // ---- the log-sum-exp of the words outside U
         Run st = run_empty();
         const uint8_t* own_bytes = bytes - v0 * VE / 8;
@@ -370,7 +372,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           e = fetch(next_row, tid, next_word);
           tg_logit = logit_of(next_row, next_tg);
         }
-        row_sync();  // the bits are read: back to 0 for the next row
+        row_sync<NT>();  // the bits are read: back to 0 for the next row
         for (int k = tid; k < K; k += NT) {
           const int pos = l.idx[k] - r.head + VE - v0 * VE;
           if (l.idx[k] >= 0 && pos >= 0 && pos < words * 32) bits[pos >> 5] = 0;
@@ -395,7 +397,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             // the words of U and the target over what was written there
             bool listed = false;
             for (int k = tid; k < K; k += NT) listed = listed || l.idx[k] == tg;
-            listed = row_or(listed);
+            listed = row_or<NT>(listed);
             for (int k = tid; k < K; k += NT) {
               const int v = l.idx[k];
               if (v >= 0 && mine(v - r.head + VE - v0 * VE))
@@ -406,7 +408,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
               Elem<T>::store1(grow + at, target_grad(c, this_logit));
           }
         }
-        row_sync();  // all bits are 0, and in the gradient's case the list is read
+        row_sync<NT>();  // all bits are 0, and in the gradient's case the list is read
         ++turn;
       }
       if (tg == a.ignore_index && next_live) {
@@ -514,10 +516,10 @@ cudaError_t run_forward(const TopArgs& a, int sms, int device, int l2, cudaStrea
   const size_t lists = size_t(words) * 4 + list_bytes(a.K);
   // two CTAs per SM share its shared memory; a long vocabulary's bits may leave room for one
   int resident = 2;
-  int stages = static_cast<int>((kStreamSmem / 2 - int64_t(lists)) / (kChunkVecs * 16));
+  int stages = static_cast<int>((kStreamSmem / 2 - int64_t(lists)) / (kFwdChunk * 16));
   if (stages < 2) {
     resident = 1;
-    stages = static_cast<int>((kStreamSmem - int64_t(lists)) / (kChunkVecs * 16));
+    stages = static_cast<int>((kStreamSmem - int64_t(lists)) / (kFwdChunk * 16));
   }
   if (stages > kMaxStages) stages = kMaxStages;
   auto kernel = top_forward_kernel<T, kGrad>;
@@ -535,7 +537,7 @@ cudaError_t run_forward(const TopArgs& a, int sms, int device, int l2, cudaStrea
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.blockDim = dim3(kFwdThreads);
-  cfg.dynamicSmemBytes = size_t(stages) * kChunkVecs * 16 + lists;
+  cfg.dynamicSmemBytes = size_t(stages) * kFwdChunk * 16 + lists;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = st;

@@ -41,22 +41,26 @@ namespace {
 
 using namespace top;
 
-constexpr int kThreads = kRowThreads;
-constexpr int kWarps = kRowWarps;
 constexpr int kBins = 1024;
-// Up to this K a thread's part has one maximum, above it one per vector of a
-// chunk: the maxima have to be several times K for the threshold to be near
-// the K-th logit.  A warp looks at 512 of them.
-constexpr int kFewMaxima = 96;
-constexpr int kPool = 512;
-constexpr int kPerLane = kPool / 32;
+static_assert(kBins * 4 >= kPerThread * 512 * 2, "the maxima are in the histogram's place");
+// Up to this K a row belongs to 256 threads, above it to 512, whose maxima are
+// more.  What a row costs beside its bytes takes a CTA 10 us, one thing after
+// the other: four small CTAs per SM hide more of it than two large ones.
+constexpr int kSmallK = 256;
+// Up to a quarter of the threads a thread's part has one maximum, above it one
+// per vector of a chunk: the maxima have to be several times K for the
+// threshold to be near the K-th logit.  A warp looks at a pool of them, one
+// per thread.
+template <int NT>
+constexpr int kFewMaxima = NT / 4;
 
 // A selection may keep this many more than K: it need not split a bin.
 __host__ __device__ constexpr int slack(int K) { return K / 4 + 64; }
-// Room for candidates: what a selection keeps and a round of vectors.
-constexpr int kRound = 256;  // vectors of a round
+// Room for candidates: twice what a selection keeps (so that a chunk that brings
+// K more finds room, and a sort its power of two), and a round of vectors.
+constexpr int kRound = 128;  // vectors of a round
 __host__ __device__ constexpr int capacity(int K, int vec) {
-  return K + slack(K) + kRound * vec;
+  return 2 * (K + slack(K)) + kRound * vec;
 }
 constexpr int kQueue = 32 + 32 * kPerThread;  // vectors that wait, per warp
 
@@ -92,7 +96,9 @@ __device__ __forceinline__ float element(uint4 w, int j, bf16_t) {
 
 struct Shared {
   uint64_t* entry;  // [cap] rank keys of the candidates
-  int* hist;        // [kBins]; at a row's end, the few entries that are ordered by counting
+  // [kBins]: a selection's bins; between selections the maxima that a threshold
+  // is found from; at a row's end the few entries that are ordered by counting
+  int* hist;
 };
 __device__ __forceinline__ float entry_value(uint64_t e) {
   return value_of(static_cast<uint32_t>(e >> 32));
@@ -101,21 +107,21 @@ __device__ __forceinline__ int entry_index(uint64_t e) {
   return static_cast<int>(~static_cast<uint32_t>(e));
 }
 
+template <int NT>
 struct Scratch {  // static shared memory of a CTA
   int pushed;     // candidates
   uint32_t lo, hi;
-  int warp_count[kWarps];
+  int warp_count[NT / 32];
   int bin, above, inside;
   int kept;
   uint32_t drop_key;
   unsigned long long drop_sum;
-  float2 warp_state[kWarps];
-  __align__(16) uint16_t maxima[kPerThread * kThreads];  // the top halves of the maxima's keys
-  uint32_t pool_key[2][kWarps];
-  int left[kWarps];
+  float2 warp_state[NT / 32];
+  uint32_t pool_key[2][kPerThread];
+  int left[NT / 32];
   uint64_t kth;   // the K-th entry, 0 if there are fewer
   uint64_t highest;
-  int queue[kWarps][kQueue];
+  int queue[NT / 32][kQueue];
 };
 
 // What has been dropped, as a base-2 state (all threads hold the same).
@@ -126,31 +132,31 @@ __device__ __forceinline__ void add_state(float2& a, float m2, float s) {
 
 // Adds those of entries [from, n) that is_dropped says to `out`: integers in
 // units of 2^-31 of the largest, so that their order does not matter.
-template <typename F>
-__device__ void drop(const Shared& sh, Scratch& sc, int from, int n, float2& out, F is_dropped) {
+template <int NT, typename F>
+__device__ void drop(const Shared& sh, Scratch<NT>& sc, int from, int n, float2& out, F is_dropped) {
   const int tid = threadIdx.x;
   if (tid == 0) {
     sc.drop_key = 0;
     sc.drop_sum = 0;
   }
-  row_sync();
+  row_sync<NT>();
   uint32_t m = 0;
-  for (int i = from + tid; i < n; i += kThreads)
+  for (int i = from + tid; i < n; i += NT)
     if (is_dropped(sh.entry[i])) m = max(m, static_cast<uint32_t>(sh.entry[i] >> 32));
   m = __reduce_max_sync(0xffffffffu, m);
   if ((tid & 31) == 0 && m) atomicMax(&sc.drop_key, m);
-  row_sync();
+  row_sync<NT>();
   const uint32_t top = sc.drop_key;
   if (top == 0) return;  // nothing dropped (a candidate's key is above that of -inf)
   const float m2 = value_of(top) * kLog2e;
   unsigned long long sum = 0;
-  for (int i = from + tid; i < n; i += kThreads)
+  for (int i = from + tid; i < n; i += NT)
     if (is_dropped(sh.entry[i]))
       sum += static_cast<uint32_t>(ex2(fmaf(entry_value(sh.entry[i]), kLog2e, -m2)) * 2147483648.f);
 #pragma unroll
   for (int k = 16; k >= 1; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
   if ((tid & 31) == 0 && sum) atomicAdd(&sc.drop_sum, sum);
-  row_sync();
+  row_sync<NT>();
   add_state(out, m2, static_cast<float>(sc.drop_sum) * (1.f / 2147483648.f));
 }
 
@@ -162,7 +168,8 @@ __device__ void drop(const Shared& sh, Scratch& sc, int from, int n, float2& out
 // entries, then the bin that holds the K-th, until the bins up to that one
 // hold few enough.  The K-th bin narrows by 1024 a level; single keys are
 // unique, so that it ends.
-__device__ __noinline__ int select(const Shared& sh, Scratch& sc, int n, int K, float2& dropped,
+template <int NT>
+__device__ __noinline__ int select(const Shared& sh, Scratch<NT>& sc, int n, int K, float2& dropped,
                                    uint32_t& least) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
@@ -170,9 +177,9 @@ __device__ __noinline__ int select(const Shared& sh, Scratch& sc, int n, int K, 
     sc.hi = 0;
     sc.kept = 0;
   }
-  row_sync();
+  row_sync<NT>();
   uint32_t lo = 0xffffffffu, hi = 0;
-  for (int i = tid; i < n; i += kThreads) {
+  for (int i = tid; i < n; i += NT) {
     const uint32_t k = static_cast<uint32_t>(sh.entry[i] >> 32);
     lo = min(lo, k);
     hi = max(hi, k);
@@ -183,54 +190,63 @@ __device__ __noinline__ int select(const Shared& sh, Scratch& sc, int n, int K, 
     atomicMin(&sc.lo, lo);
     atomicMax(&sc.hi, hi);
   }
-  row_sync();
+  row_sync<NT>();
   uint64_t from = uint64_t(sc.lo) << 32, to = (uint64_t(sc.hi) << 32) | 0xffffffffu;
   int above = 0;  // entries ranking above the range
   for (int level = 0; level < 8; ++level) {
     const uint64_t span = to - from;
     const int shift = max(0, 54 - __clzll(static_cast<long long>(span | 1)));
-    for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
-    row_sync();
-    for (int i = tid; i < n; i += kThreads) {
+    for (int i = tid; i < kBins; i += NT) sh.hist[i] = 0;
+    row_sync<NT>();
+    for (int i = tid; i < n; i += NT) {
       const uint64_t k = sh.entry[i];
       if (k >= from && k <= to) atomicAdd(&sh.hist[(k - from) >> shift], 1);
     }
-    row_sync();
-    // bins from the highest down, two per thread
-    const int b0 = kBins - 1 - 2 * tid, c0 = sh.hist[b0], c1 = sh.hist[b0 - 1];
-    int run = c0 + c1;
+    row_sync<NT>();
+    // bins from the highest down, a few per thread
+    constexpr int kOwn = kBins / NT;
+    const int b0 = kBins - 1 - kOwn * tid;
+    int own[kOwn], mine = 0;
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) mine += own[j] = sh.hist[b0 - j];
+    int run = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xffffffffu, run, d);
       if (lane >= d) run += o;
     }
     if (lane == 31) sc.warp_count[warp] = run;
-    row_sync();
-    const int sum = lane < warp ? sc.warp_count[lane] : 0;  // (16 warps)
-    const int ahead = above + static_cast<int>(__reduce_add_sync(0xffffffffu, sum)) + run - (c0 + c1);
-    if (ahead < K && ahead + c0 + c1 >= K) {
-      const bool second = ahead + c0 < K;
-      sc.bin = second ? b0 - 1 : b0;
-      sc.above = second ? ahead + c0 : ahead;
-      sc.inside = second ? c1 : c0;
+    row_sync<NT>();
+    const int sum = lane < warp ? sc.warp_count[lane] : 0;
+    int ahead = above + static_cast<int>(__reduce_add_sync(0xffffffffu, sum)) + run - mine;
+    if (ahead < K && ahead + mine >= K) {
+#pragma unroll
+      for (int j = 0; j < kOwn; ++j) {
+        if (ahead < K && ahead + own[j] >= K) {
+          sc.bin = b0 - j;
+          sc.above = ahead;
+          sc.inside = own[j];
+        }
+        ahead += own[j];
+      }
     }
-    row_sync();
+    row_sync<NT>();
     above = sc.above;
     const uint64_t start = from + (uint64_t(sc.bin) << shift);
     const uint64_t end = start + ((uint64_t(1) << shift) - 1);
     from = start;
     if (end < to) to = end;
     if (above + sc.inside <= K + slack(K)) break;
-    row_sync();  // the result is read before the next level writes it
+    row_sync<NT>();  // the result is read before the next level writes it
   }
   drop(sh, sc, 0, n, dropped, [&](uint64_t e) { return e < from; });
   // moved towards the front, a block of entries at a time: writes stay behind reads
-  for (int base = 0; base < n; base += kThreads) {
+  for (int base = 0; base < n; base += NT) {
     const int i = base + tid;
     const uint64_t e = i < n ? sh.entry[i] : 0;
-    row_sync();
+    row_sync<NT>();
     if (i < n && e >= from) sh.entry[atomicAdd(&sc.kept, 1)] = e;
-    row_sync();
+    row_sync<NT>();
   }
   least = static_cast<uint32_t>(from >> 32);
   return sc.kept;
@@ -242,10 +258,10 @@ static_assert(kCountMax * 8 <= kBins * 4, "they are in the histogram's place");
 
 // n <= kCountMax entries: f(place, entry) by one thread for each, its place the
 // number that rank before it, counted by as many threads per entry as there are.
-template <typename F>
+template <int NT, typename F>
 __device__ __forceinline__ void count_entries(const uint64_t* entry, int n, F f) {
   const int tid = threadIdx.x;
-  const int parts = n <= 32 ? 16 : n <= 64 ? 8 : n <= 128 ? 4 : 2;
+  const int parts = n <= NT / 16 ? 16 : n <= NT / 8 ? 8 : n <= NT / 4 ? 4 : n <= NT / 2 ? 2 : 1;
   const int i = tid / parts, part = tid % parts;
   if ((tid & ~31) / parts >= n) return;  // nothing for the whole warp
   const uint64_t own = i < n ? entry[i] : ~0ull;
@@ -259,15 +275,16 @@ __device__ __forceinline__ void count_entries(const uint64_t* entry, int n, F f)
 // Sorts n entries, highest rank first (bitonic, a power of two of them: the
 // room is there).  Steps within 32 entries are done in registers, by threads
 // that hold an entry each.
+template <int NT>
 __device__ __noinline__ void sort_entries(const Shared& sh, int n) {
   const int tid = threadIdx.x;
-  int P = kThreads;
+  int P = NT;
   while (P < n) P *= 2;
-  for (int i = n + tid; i < P; i += kThreads) sh.entry[i] = 0;
-  row_sync();
+  for (int i = n + tid; i < P; i += NT) sh.entry[i] = 0;
+  row_sync<NT>();
   for (int size = 2; size <= P; size *= 2) {
     for (int step = size / 2; step >= 32; step /= 2) {
-      for (int i = tid; i < P / 2; i += kThreads) {
+      for (int i = tid; i < P / 2; i += NT) {
         const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
         const uint64_t x = sh.entry[lo], y = sh.entry[hi];
         if ((x < y) == ((lo & size) == 0)) {
@@ -275,11 +292,11 @@ __device__ __noinline__ void sort_entries(const Shared& sh, int n) {
           sh.entry[hi] = x;
         }
       }
-      row_sync();
+      row_sync<NT>();
     }
     // (sizes up to 32 need no other entries in between)
     if (size < 32) continue;
-    for (int i = tid; i < P; i += kThreads) {
+    for (int i = tid; i < P; i += NT) {
       uint64_t x = sh.entry[i];
       for (int z = size == 32 ? 2 : size; z <= size; z *= 2) {
         const bool down = (i & z) == 0;  // highest first
@@ -291,12 +308,13 @@ __device__ __noinline__ void sort_entries(const Shared& sh, int n) {
       }
       sh.entry[i] = x;
     }
-    row_sync();
+    row_sync<NT>();
   }
 }
 
 // The largest t such that `want` of the warp's values reach it: a bit a round,
 // from the first that is not the same in all.
+template <int kPerLane>
 __device__ __forceinline__ uint32_t warp_threshold(const uint32_t (&key)[kPerLane], int want) {
   uint32_t lo = key[0], hi = key[0];
 #pragma unroll
@@ -319,29 +337,30 @@ __device__ __forceinline__ uint32_t warp_threshold(const uint32_t (&key)[kPerLan
 }
 
 // One CTA per row at a time.
-template <typename T>
-__global__ void __launch_bounds__(kStreamThreads, 2)
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT + 32, 1024 / NT)
     top_select_kernel(TopSelectArgs a, int cap, int stages) {
-  constexpr int VE = Elem<T>::kVec;
+  constexpr int VE = Elem<T>::kVec, kChunk = Ring<NT>::kChunk;
+  constexpr int kPerLane = NT / 32;
   extern __shared__ uint4 select_smem[];
-  __shared__ Scratch sc;
+  __shared__ Scratch<NT> sc;
   __shared__ __align__(8) RingBars bars;
-  const Shared sh{reinterpret_cast<uint64_t*>(select_smem + stages * kChunkVecs),
-                  reinterpret_cast<int*>(select_smem + stages * kChunkVecs) + 2 * cap};
+  const Shared sh{reinterpret_cast<uint64_t*>(select_smem + stages * kChunk),
+                  reinterpret_cast<int*>(select_smem + stages * kChunk) + 2 * cap};
   const int K = static_cast<int>(a.K), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int V = static_cast<int>(a.V);
-  Ring ring(&bars, select_smem, stages);
+  Ring<NT> ring(&bars, select_smem, stages);
   if (tid == 0) ring.init();
   __syncthreads();
 
-  if (tid >= kThreads) {
-    if (tid == kThreads) {  // ---- copies
+  if (tid >= NT) {
+    if (tid == NT) {  // ---- copies
       const uint64_t once = policy_evict_first();
       uint32_t copied = 0;
       for (int64_t row = blockIdx.x; row < a.BT; row += gridDim.x) {
         const Row<T> r(static_cast<const T*>(a.logits) + row * a.ld, V);
         if (!ring.copy(r, 0, r.nvec, once)) break;
-        copied += chunks_of(0, r.nvec);
+        copied += chunks_of<NT>(0, r.nvec);
       }
       ring.drain(copied);
     }
@@ -353,7 +372,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       float thr = -INFINITY;
       int waiting = 0;  // vectors in the warp's queue
       if (tid == 0) sc.pushed = 0;
-      row_sync();
+      row_sync<NT>();
 
       auto push = [&](float x, int v) {
         const int at = atomicAdd(&sc.pushed, 1);
@@ -405,22 +424,24 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       // Raises the threshold: each pool of maxima finds what its share of K
       // reach; the least of those holds for all.
       auto raise_threshold = [&]() {
-        const int pools = K <= kFewMaxima ? kThreads / kPool : kPerThread * kThreads / kPool;
-        if (K <= kFewMaxima) {
-          sc.maxima[tid] =
+        const int pools = K <= kFewMaxima<NT> ? 1 : kPerThread;
+        // the top halves of their keys
+        uint16_t* maxima = reinterpret_cast<uint16_t*>(sh.hist);
+        if (K <= kFewMaxima<NT>) {
+          maxima[tid] =
               static_cast<uint16_t>(key_of(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3])) >> 16);
         } else {
 #pragma unroll
           for (int u = 0; u < kPerThread; ++u)
-            sc.maxima[u * kThreads + tid] = static_cast<uint16_t>(key_of(mx[u]) >> 16);
+            maxima[u * NT + tid] = static_cast<uint16_t>(key_of(mx[u]) >> 16);
         }
-        row_sync();
+        row_sync<NT>();
         uint32_t* keys = sc.pool_key[found++ & 1u];
         if (warp < pools) {
-          const uint4* m = reinterpret_cast<const uint4*>(sc.maxima + warp * kPool) + lane;
+          const uint4* m = reinterpret_cast<const uint4*>(maxima + warp * NT) + lane;
           uint32_t key[kPerLane];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
+          for (int q = 0; q < kPerLane / 8; ++q) {
             const uint4 k8 = m[q * 32];
             const uint32_t two[4] = {k8.x, k8.y, k8.z, k8.w};
 #pragma unroll
@@ -432,7 +453,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
           const uint32_t t = warp_threshold(key, (K + pools - 1) / pools);
           if (lane == 0) keys[warp] = t << 16;
         }
-        row_sync();
+        row_sync<NT>();
         // (logits at it are candidates too)
         thr = fmaxf(thr, before(__reduce_min_sync(0xffffffffu, keys[lane % pools])));
       };
@@ -440,16 +461,16 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       // many already.  `rounds`: all that is still to come has a larger index
       // than all so far, so that what equals the K-th cannot rank.
       auto room = [&](int more, bool rounds) {
-        row_sync();
+        row_sync<NT>();
         int n = sc.pushed;
-        row_sync();
+        row_sync<NT>();
         if (n <= cap && n + more > cap) {
           uint32_t least;
           n = select(sh, sc, n, K, dropped, least);
           thr = fmaxf(thr, rounds ? value_of(least) : before(least));
-          row_sync();
+          row_sync<NT>();
           if (tid == 0) sc.pushed = n;
-          row_sync();
+          row_sync<NT>();
         }
         return n;
       };
@@ -457,11 +478,11 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       if (tid < r.head) take_loose(tid);
       int chunks = 0;
       bool full = false;  // more candidates came than there is room for
-      for (int c = 0; c < r.nvec; c += kChunkVecs) {
+      for (int c = 0; c < r.nvec; c += kChunk) {
         const uint4* p = ring.wait() + tid;
-        const bool whole = c + kChunkVecs <= r.nvec;
+        const bool whole = c + kChunk <= r.nvec;
         auto vec = [&](int u) {
-          return c + u * kThreads + tid < r.nvec ? p[u * kThreads] : nothing<T>();
+          return c + u * NT + tid < r.nvec ? p[u * NT] : nothing<T>();
         };
         if (c == 0) {
 #pragma unroll
@@ -484,7 +505,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
             if (!above) raise(st, vm);
             const uint32_t b = __ballot_sync(0xffffffffu, above);
             if (above)
-              sc.queue[warp][waiting + __popc(b & ((1u << lane) - 1u))] = c + u * kThreads + tid;
+              sc.queue[warp][waiting + __popc(b & ((1u << lane) - 1u))] = c + u * NT + tid;
             waiting += __popc(b);
             unusual = fminf(thr, st.limit);
           }
@@ -492,7 +513,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         };
         if (whole) {
 #pragma unroll
-          for (int u = 0; u < kPerThread; ++u) step(p[u * kThreads], u);
+          for (int u = 0; u < kPerThread; ++u) step(p[u * NT], u);
         } else {
 #pragma unroll
           for (int u = 0; u < kPerThread; ++u) step(vec(u), u);
@@ -502,9 +523,9 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         ++chunks;
         // (always the same decision in all warps)
         const bool doubled = (chunks & (chunks - 1)) == 0;
-        if (doubled || K > kFewMaxima) {
+        if (doubled || K > kFewMaxima<NT>) {
           // (not where little is left that a better one would spare)
-          if (doubled && chunks > 1 && r.nvec - c > (chunks / 2 + 1) * kChunkVecs) raise_threshold();
+          if (doubled && chunks > 1 && r.nvec - c > (chunks / 2 + 1) * kChunk) raise_threshold();
           if (!full) full = room(kRound * VE, false) > cap;
         }
       }
@@ -512,13 +533,13 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       if (lane == 0) sc.left[warp] = waiting;
       raise_threshold();
       {
-        const int count = lane < kWarps ? sc.left[lane] : 0;
+        const int count = lane < (NT / 32) ? sc.left[lane] : 0;
         const int ahead = static_cast<int>(
             __reduce_add_sync(0xffffffffu, lane < warp ? count : 0));
         const int total = static_cast<int>(__reduce_add_sync(0xffffffffu, count));
-        int* flat = reinterpret_cast<int*>(sc.maxima);  // (has been read)
+        int* flat = sh.hist;  // (the maxima have been read)
         if (lane < waiting) flat[ahead + lane] = sc.queue[warp][lane];
-        row_sync();
+        row_sync<NT>();
         if (tid < total) take(*r.vec(flat[tid]), flat[tid]);
         __syncwarp();
       }
@@ -528,7 +549,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         if (r.tail0 + tid < V) take_loose(r.tail0 + tid);
       } else {  // again, in rounds of rising index with room made before each
         if (tid == 0) sc.pushed = 0;
-        row_sync();
+        row_sync<NT>();
         st = run_empty();
         dropped = make_float2(-INFINITY, 0.f);
         thr = -INFINITY;
@@ -546,24 +567,24 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         sc.kept = 0;
         sc.kth = 0;
       }
-      row_sync();
+      row_sync<NT>();
       n = sc.pushed;
       // those above the threshold: K of them, or hardly more, or all there are
       uint64_t* few = reinterpret_cast<uint64_t*>(sh.hist);
       if (!full) {
-        for (int i = tid; i < n; i += kThreads) {
+        for (int i = tid; i < n; i += NT) {
           const uint64_t e = sh.entry[i];
           if (entry_value(e) > thr) {
             const int at = atomicAdd(&sc.kept, 1);
             if (at < kCountMax) few[at] = e;
           }
         }
-        row_sync();
+        row_sync<NT>();
       }
       const int kept = sc.kept;
       uint64_t highest = 0;
       if (!full && kept <= kCountMax) {
-        count_entries(few, kept, [&](int place, uint64_t e) {
+        count_entries<NT>(few, kept, [&](int place, uint64_t e) {
           if (place < K) {
             a.values[row * a.ld_v + place] = entry_value(e);
             a.index[row * a.ld_i + place] = entry_index(e);
@@ -571,22 +592,22 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
           if (place == K - 1) sc.kth = e;
           if (place == 0) sc.highest = e;
         });
-        for (int i = kept + tid; i < K; i += kThreads) {
+        for (int i = kept + tid; i < K; i += NT) {
           a.values[row * a.ld_v + i] = -INFINITY;
           a.index[row * a.ld_i + i] = -1;
         }
-        row_sync();
+        row_sync<NT>();
         const uint64_t kth = sc.kth;
         drop(sh, sc, 0, n, dropped, [&](uint64_t e) { return e < kth; });
         highest = kept > 0 ? sc.highest : 0;
       } else {
-        row_sync();  // sc.kept is read
+        row_sync<NT>();  // sc.kept is read
         if (n > K + slack(K)) {
           uint32_t least;
           n = select(sh, sc, n, K, dropped, least);
         }
-        sort_entries(sh, n);
-        for (int i = tid; i < K; i += kThreads) {
+        sort_entries<NT>(sh, n);
+        for (int i = tid; i < K; i += NT) {
           const uint64_t e = i < n ? sh.entry[i] : 0;
           a.values[row * a.ld_v + i] = i < n ? entry_value(e) : -INFINITY;
           a.index[row * a.ld_i + i] = i < n ? entry_index(e) : -1;
@@ -595,7 +616,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         highest = n > 0 ? sh.entry[0] : 0;
       }
       if (warp == 0) {
-        const float2 own = lane < kWarps ? sc.warp_state[lane] : make_float2(-INFINITY, 0.f);
+        const float2 own = lane < (NT / 32) ? sc.warp_state[lane] : make_float2(-INFINITY, 0.f);
         const Lse2 rest = merge(merge_warp(Lse2{own.x, own.y}), Lse2{dropped.x, dropped.y});
         if (lane == 0) {
           const bool inf = highest != 0 && entry_value(highest) == INFINITY;
@@ -605,40 +626,52 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
             atomicOr(a.dev_status, FCT_DEV_NO_DISTRIBUTION);
         }
       }
-      row_sync();
+      row_sync<NT>();
     }
   }
   __syncthreads();
   if (tid == 0 && bars.abort && a.dev_status) atomicOr(a.dev_status, FCT_DEV_WAIT_TIMEOUT);
 }
 
-constexpr int kSmem = kStreamSmem / 2 - 9 * 1024;  // dynamic, beside the static
-
-template <typename T>
+template <typename T, int NT>
 cudaError_t run(const TopSelectArgs& a, int sms, int device, cudaStream_t st) {
   const int K = static_cast<int>(a.K);
   const int cap = capacity(K, Elem<T>::kVec);
-  const size_t lists = size_t(cap) * 8 + kBins * 4;
-  auto kernel = top_select_kernel<T>;
+  constexpr int kChunkBytes = Ring<NT>::kChunk * 16, kStatic = sizeof(Scratch<NT>) + sizeof(RingBars);
+  const int lists = cap * 8 + kBins * 4;
+  auto kernel = top_select_kernel<T, NT>;
   static std::once_flag once[64];
   static cudaError_t set[64];
   std::call_once(once[device], [&] {
-    set[device] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    set[device] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kStreamSmem / 2 - kStatic);
   });
   if (set[device] != cudaSuccess) return set[device];
-  const int stages = static_cast<int>((kSmem - lists) / (kChunkVecs * 16));
-  int64_t grid = int64_t(sms) * 2;
+  // as many CTAs per SM as its registers allow, fewer where the lists are long
+  int resident = 1024 / NT;
+  int stages = 0;
+  for (; resident > 1; --resident) {
+    stages = (kStreamSmem / resident - kStatic - lists) / kChunkBytes;
+    if (stages >= 2) break;
+  }
+  if (stages > 4) stages = 4;
+  int64_t grid = int64_t(sms) * resident;
   if (grid > a.BT) grid = a.BT;
-  kernel<<<static_cast<unsigned>(grid), kStreamThreads, size_t(stages) * kChunkVecs * 16 + lists,
-           st>>>(a, cap, stages);
+  kernel<<<static_cast<unsigned>(grid), NT + 32, size_t(stages) * kChunkBytes + lists, st>>>(a, cap,
+                                                                                            stages);
   return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t run_sized(const TopSelectArgs& a, int sms, int device, cudaStream_t st) {
+  return a.K <= kSmallK ? run<T, 256>(a, sms, device, st) : run<T, 512>(a, sms, device, st);
 }
 
 }  // namespace
 
 cudaError_t launch_top_select(const TopSelectArgs& a, int sms, int device, cudaStream_t st) {
-  return a.dtype == FCT_BF16 ? run<bf16_t>(a, sms, device, st)
-                             : run<float>(a, sms, device, st);
+  return a.dtype == FCT_BF16 ? run_sized<bf16_t>(a, sms, device, st)
+                             : run_sized<float>(a, sms, device, st);
 }
 
 }  // namespace fct
