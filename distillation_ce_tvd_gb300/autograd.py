@@ -10,6 +10,7 @@ bits instead of the teacher, with the same gradient bit for bit.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding
 
@@ -128,3 +129,140 @@ def fused_linear_ce_tvd_mean_loss(h_student, w_student, h_teacher, w_teacher, ta
     bfloat16)."""
     return FusedLinearCETVDMeanLoss.apply(h_student, w_student, h_teacher, w_teacher, target,
                                           ignore_index, alpha, beta, chunk_rows, logits_dtype)
+
+
+# ------------------------------------------------------------------ a teacher's top logits
+
+class FusedCETVDTopFunction(torch.autograd.Function):
+    """(student, target, a teacher's top logits) -> per-row (ce, tvd); gradient w.r.t. student only.
+
+    The forward keeps four values per row besides its inputs (student_lse, student_rest,
+    teacher_lse, sigma).  With ``inplace=True`` the backward writes the gradient over the student
+    logits' storage; the student tensor must not be used again after the backward.
+    """
+
+    @staticmethod
+    def forward(ctx, student, target, top_values, top_index, rest_lse=None,
+                ignore_index=binding.IGNORE_INDEX, inplace=False):
+        ce, tvd, *saved = binding.fused_ce_tvd_top_forward(
+            student.detach(), target, top_values.detach(), top_index,
+            None if rest_lse is None else rest_lse.detach(), ignore_index)
+        ctx.save_for_backward(student, target, top_values, top_index, rest_lse, *saved)
+        ctx.ignore_index = ignore_index
+        ctx.inplace = inplace
+        return ce, tvd
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_ce, grad_tvd):
+        student, *rest = ctx.saved_tensors
+        grad = binding.fused_ce_tvd_top_backward(
+            student.detach(), *rest, grad_ce.float().contiguous(), grad_tvd.float().contiguous(),
+            ctx.ignore_index, inplace=ctx.inplace)
+        return grad, None, None, None, None, None, None
+
+
+def fused_ce_tvd_top_loss(student, target, top_values, top_index, rest_lse=None,
+                          ignore_index=binding.IGNORE_INDEX, inplace=False):
+    """Per-row (ce, tvd) against a teacher's top logits (as binding.fct_top_logits gives them), with
+    autograd support for the student's logits."""
+    return FusedCETVDTopFunction.apply(student, target, top_values, top_index, rest_lse,
+                                       ignore_index, inplace)
+
+
+class FusedCETVDTopMeanLoss(torch.autograd.Function):
+    """alpha * mean(ce) + beta * mean(tvd) against a teacher's top logits, over the rows not ignored.
+
+    As for FusedCETVDMeanLoss, the forward runs forward and backward in one launch and keeps the
+    student's gradient, which the backward scales by the incoming one.
+    """
+
+    @staticmethod
+    def forward(ctx, student, target, top_values, top_index, rest_lse=None,
+                ignore_index=binding.IGNORE_INDEX, alpha=1.0, beta=1.0, inplace=False):
+        gce, gtvd, _ = binding.fused_ce_tvd_mean_upstream(target, ignore_index, alpha, beta)
+        ce, tvd, *_, grad = binding.fused_ce_tvd_top_forward_backward(
+            student.detach(), target, top_values.detach(), top_index,
+            None if rest_lse is None else rest_lse.detach(), gce, gtvd, ignore_index,
+            inplace=inplace)
+        ctx.save_for_backward(grad)
+        loss = binding.fused_ce_tvd_mean_loss(ce, tvd, target, ignore_index, alpha, beta)
+        return loss.reshape(())
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_out):
+        (grad,) = ctx.saved_tensors
+        return (grad * grad_out.to(grad.dtype),) + (None,) * 8
+
+
+def fused_ce_tvd_top_mean_loss(student, target, top_values, top_index, rest_lse=None,
+                               ignore_index=binding.IGNORE_INDEX, alpha=1.0, beta=1.0,
+                               inplace=False):
+    """Scalar alpha * mean(ce) + beta * mean(tvd) against a teacher's top logits, with autograd
+    support for the student's logits."""
+    return FusedCETVDTopMeanLoss.apply(student, target, top_values, top_index, rest_lse,
+                                       ignore_index, alpha, beta, inplace)
+
+
+class FusedLinearCETVDTopFunction(torch.autograd.Function):
+    """(h, w, target, a teacher's top logits) -> per-row (ce, tvd) of the logits h @ w.T.
+
+    Neither direction holds the logits: the forward keeps four values per row, and the backward
+    computes the logits again, a piece of the vocabulary at a time.  Gradients for h and w (bf16).
+    """
+
+    @staticmethod
+    def forward(ctx, h, w, target, top_values, top_index, rest_lse=None,
+                ignore_index=binding.IGNORE_INDEX, piece_cols=0):
+        ce, tvd, *saved = binding.fused_linear_ce_tvd_top_forward(
+            h.detach(), w.detach(), target, top_values.detach(), top_index,
+            None if rest_lse is None else rest_lse.detach(), ignore_index)
+        ctx.save_for_backward(h, w, target, top_values, top_index, rest_lse, *saved)
+        ctx.ignore_index, ctx.piece_cols = ignore_index, piece_cols
+        return ce, tvd
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_ce, grad_tvd):
+        h, w, *rest = ctx.saved_tensors
+        grad_h, grad_w = binding.fused_linear_ce_tvd_top_backward(
+            h.detach(), w.detach(), *rest, grad_ce.float().contiguous(),
+            grad_tvd.float().contiguous(), ctx.ignore_index, piece_cols=ctx.piece_cols,
+            want_grad_h=ctx.needs_input_grad[0], want_grad_w=ctx.needs_input_grad[1])
+        return (grad_h, grad_w) + (None,) * 6
+
+
+def fused_linear_ce_tvd_top_loss(h, w, target, top_values, top_index, rest_lse=None,
+                                 ignore_index=binding.IGNORE_INDEX, piece_cols=0):
+    """Per-row (ce, tvd) of the lm_head logits h @ w.T against a teacher's top logits, with autograd
+    support for h (BT, d) and w (V, d), both bf16."""
+    return FusedLinearCETVDTopFunction.apply(h, w, target, top_values, top_index, rest_lse,
+                                             ignore_index, piece_cols)
+
+
+class FusedLinearCEFunction(torch.autograd.Function):
+    """(h, w, target) -> per-row cross-entropy of the logits h @ w.T, which are never held whole."""
+
+    @staticmethod
+    def forward(ctx, h, w, target, ignore_index=binding.IGNORE_INDEX, piece_cols=0):
+        ce, lse = binding.fused_linear_ce_forward(h.detach(), w.detach(), target, ignore_index)
+        ctx.save_for_backward(h, w, target, lse)
+        ctx.ignore_index, ctx.piece_cols = ignore_index, piece_cols
+        return ce
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_ce):
+        h, w, target, lse = ctx.saved_tensors
+        grad_h, grad_w = binding.fused_linear_ce_backward(
+            h.detach(), w.detach(), target, lse, grad_ce.float().contiguous(), ctx.ignore_index,
+            piece_cols=ctx.piece_cols, want_grad_h=ctx.needs_input_grad[0],
+            want_grad_w=ctx.needs_input_grad[1])
+        return grad_h, grad_w, None, None, None
+
+
+def fused_linear_ce_loss(h, w, target, ignore_index=binding.IGNORE_INDEX, piece_cols=0):
+    """Per-row cross-entropy of the lm_head logits h @ w.T, with autograd support for h (BT, d) and
+    w (V, d), both bf16."""
+    return FusedLinearCEFunction.apply(h, w, target, ignore_index, piece_cols)

@@ -1354,6 +1354,13 @@ def _rows_out(x, n, index, device, name):
     return x
 
 
+def _stats_out(given, BT, index, device):
+    """The loss's per-row outputs: as given, or rows of one allocation."""
+    if all(x is None for x in given):
+        return torch.empty((len(given), BT), device=device, dtype=torch.float32).unbind(0)
+    return tuple(_rows_out(x, BT, index, device, n) for x, n in zip(given, _TOP_STATS))
+
+
 def _top_list(values, index_of_words, rest_lse, BT, index):
     """The fct_top_list of a teacher's (BT, K) logits and int32 indices, and rest_lse (BT,) or None."""
     v, ld_v, K = _table(values, torch.float32, BT, index, "top_values")
@@ -1439,8 +1446,7 @@ def fused_ce_tvd_top_forward(student, target, top_values, top_index, rest_lse=No
     x, ld, code = _logits2(student, "student")
     BT, V = student.shape
     at, dev = student.get_device(), student.device
-    given = (ce, tvd, student_lse, student_rest, teacher_lse, sigma)
-    outs = tuple(_rows_out(o, BT, at, dev, n) for o, n in zip(given, _TOP_STATS))
+    outs = _stats_out((ce, tvd, student_lse, student_rest, teacher_lse, sigma), BT, at, dev)
     rc = _library().fused_ce_tvd_top_forward(
         x, ld, code, _vec(target, torch.int64, BT, at, "target"),
         _top_list(top_values, top_index, rest_lse, BT, at), BT, V, int(ignore_index),
@@ -1485,8 +1491,7 @@ def fused_ce_tvd_top_forward_backward(student, target, top_values, top_index, re
     BT, V = student.shape
     at, dev = student.get_device(), student.device
     gce, gtvd, stride = _upstream_pair(grad_ce, grad_tvd, BT, dev, at)
-    given = (ce, tvd, student_lse, student_rest, teacher_lse, sigma)
-    outs = tuple(_rows_out(o, BT, at, dev, n) for o, n in zip(given, _TOP_STATS))
+    outs = _stats_out((ce, tvd, student_lse, student_rest, teacher_lse, sigma), BT, at, dev)
     grad, g, ld_g = _gradient_out(student, grad_student, inplace, at)
     rc = _library().fused_ce_tvd_top_forward_backward(
         x, ld, code, _vec(target, torch.int64, BT, at, "target"),
@@ -1572,8 +1577,7 @@ def fused_linear_ce_tvd_top_forward(h, w, target, top_values, top_index, rest_ls
     hp, ld_h, wp, ld_w, BT, V, d, at = _hidden(h, w)
     dev = h.device
     lists = _top_list(top_values, top_index, rest_lse, BT, at)
-    given = (ce, tvd, student_lse, student_rest, teacher_lse, sigma)
-    outs = tuple(_rows_out(o, BT, at, dev, n) for o, n in zip(given, _TOP_STATS))
+    outs = _stats_out((ce, tvd, student_lse, student_rest, teacher_lse, sigma), BT, at, dev)
     space = _space(workspace, fused_linear_ce_tvd_top_forward_workspace_size(
         BT, V, top_index.shape[1]), dev, at)
     rc = _library().fused_linear_ce_tvd_top_forward(
