@@ -408,6 +408,15 @@ struct Sums {  // of one row's list, held by every lane of a warp
 // logits of K places (-inf where unused), and the student's state outside U.
 // The signs are those of p and q from their sums, before any log-sum-exp is
 // rounded.
+// (A sum of 1 and of terms that fp32 does not see beside 1 is 1: a student and a
+// teacher that are both that sure of a word tie.)  The rest is the list's last
+// place, and neighbours are added first: a small term meets other small ones
+// before it meets a large one.
+__device__ __forceinline__ float list_add(float a) {
+#pragma unroll
+  for (int m = 1; m <= 16; m <<= 1) a += __shfl_xor_sync(0xffffffffu, a, m);
+  return a;
+}
 static __device__ Sums list_sums(const float* s, const float* t, int K, float rest_m2, float rest_s,
                                  float t_rest) {
   const int lane = threadIdx.x & 31;
@@ -428,15 +437,19 @@ static __device__ Sums list_sums(const float* s, const float* t, int K, float re
     us += ex2(fmaf(s[k], kLog2e, ns));
     ut += ex2(fmaf(t[k], kLog2e, nt));
   }
-  us = warp_sum(us);
-  ut = warp_sum(ut);
-  const float rs = rest_s == 0.f ? 0.f : __fmul_rn(rest_s, ex2(rest_m2 + ns));
   const float rt = ex2(fmaf(t_rest, kLog2e, nt));
-  const float zs = us + rs, zt = ut + rt;
+  us = list_add(us);
+  const float zt = list_add(lane == (K & 31) ? ut + rt : ut);
+  ut = list_add(ut);
+  const float rs = rest_s == 0.f ? 0.f : __fmul_rn(rest_s, ex2(rest_m2 + ns));
+  const float zs = us + rs;
   Sums o;
-  o.lse = finish(ms2, zs);
-  o.rest = finish(rest_m2, rest_s);
-  o.t_lse = finish(mt2, zt);
+  // (a lane each: 64-bit arithmetic is slow)
+  const float f = finish(lane == 0 ? ms2 : lane == 1 ? rest_m2 : mt2,
+                         lane == 0 ? zs : lane == 1 ? rest_s : zt);
+  o.lse = __shfl_sync(0xffffffffu, f, 0);
+  o.rest = __shfl_sync(0xffffffffu, f, 1);
+  o.t_lse = __shfl_sync(0xffffffffu, f, 2);
   if (o.t_lse == -INFINITY) {  // no teacher: cross-entropy alone
     o.tvd = 0.f;
     o.sigma = 0.f;

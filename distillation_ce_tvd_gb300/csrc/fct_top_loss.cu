@@ -293,6 +293,12 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     }
     for (; row < a.BT; row += n_clusters) {
       T* grow = kGrad ? static_cast<T*>(a.grad) + row * a.ld_g : nullptr;
+      float up_ce = 0.f, up_tvd = 0.f, t_rest = 0.f;
+      if constexpr (kGrad) {
+        up_ce = a.grad_ce[row * a.grad_stride];
+        up_tvd = a.grad_tvd[row * a.grad_stride];
+        t_rest = a.rest ? a.rest[row] : -INFINITY;
+      }
       const int64_t next_row = row + n_clusters;
       const int64_t next_tg = fetch_target(next_row);
       const bool next_live = next_tg != a.ignore_index;
@@ -385,9 +391,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           } else {
             mbar_wait(&done_bar[turn & 1u], (turn >> 1) & 1u, &bars.abort);
             const Sums sums = t.sums;
-            const Coefs c = make_coefs(a.grad_ce[row * a.grad_stride],
-                                       a.grad_tvd[row * a.grad_stride], sums.lse, sums.rest,
-                                       sums.t_lse, a.rest ? a.rest[row] : -INFINITY, sums.sigma);
+            const Coefs c = make_coefs(up_ce, up_tvd, sums.lse, sums.rest, sums.t_lse, t_rest,
+                                       sums.sigma);
             const Outside o(c);
             const bool same = same_alignment(srow, grow);
             ring.each(v0, v1, [&](uint4 w, int iv) {
