@@ -300,45 +300,43 @@ __device__ __forceinline__ uint32_t chunks_of(int v0, int v1) {
   return v1 > v0 ? static_cast<uint32_t>((v1 - v0 + n - 1) / n) : 0u;
 }
 
-// What CTAs of a cluster tell each other about a row: 16 bytes each, sent to
-// every CTA's slots, counted on its barrier.  Two turns alternate: a CTA sends
-// for row i + 2 after it has all of row i + 1, which the others sent after
-// they had taken theirs of row i.
+// What CTAs of a cluster tell each other about a row: 16 bytes per share of it,
+// sent to every CTA's slots, counted on its barrier.  Two turns alternate: a
+// CTA sends for row i + 2 after it has all of row i + 1, which the others sent
+// after they had taken theirs of row i.
+constexpr int kMaxShares = 8;
 struct Exchange {
-  uint4 slot[2][8];
+  uint4 slot[2][kMaxShares];
   uint64_t bar[2];
 };
 __device__ __forceinline__ void exchange_init(Exchange& x) {
   mbar_init(&x.bar[0], 1);
   mbar_init(&x.bar[1], 1);
 }
-// By one warp of each CTA; `mine` counts from lane 0.
-__device__ __forceinline__ void exchange_send(Exchange& x, uint32_t turn, int C, int rank,
-                                              uint4 mine) {
+// By one warp of each of C CTAs: `mine` of lane i is share first + i's, n of them.
+__device__ __forceinline__ void exchange_send(Exchange& x, uint32_t turn, int C, int shares,
+                                              int first, int n, uint4 mine) {
   const int lane = threadIdx.x & 31;
-  mine.x = __shfl_sync(0xffffffffu, mine.x, 0);
-  mine.y = __shfl_sync(0xffffffffu, mine.y, 0);
-  mine.z = __shfl_sync(0xffffffffu, mine.z, 0);
-  mine.w = __shfl_sync(0xffffffffu, mine.w, 0);
-  if (lane == 0) mbar_arrive_expect_tx(&x.bar[turn & 1u], static_cast<uint32_t>(C) * 16u);
+  if (lane == 0) mbar_arrive_expect_tx(&x.bar[turn & 1u], static_cast<uint32_t>(shares) * 16u);
   __syncwarp();
-  if (lane < C) {
-    asm volatile(
-        "{\n\t.reg .b32 dst, bar;\n\t"
-        "mapa.shared::cluster.u32 dst, %0, %2;\n\t"
-        "mapa.shared::cluster.u32 bar, %1, %2;\n\t"
-        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [dst], {%3, %4, %5, %6}, "
-        "[bar];\n\t}" ::"r"(smem_addr(&x.slot[turn & 1u][rank])),
-        "r"(smem_addr(&x.bar[turn & 1u])), "r"(lane), "r"(mine.x), "r"(mine.y), "r"(mine.z),
-        "r"(mine.w)
-        : "memory");
+  if (lane < n) {
+    for (int to = 0; to < C; ++to)
+      asm volatile(
+          "{\n\t.reg .b32 dst, bar;\n\t"
+          "mapa.shared::cluster.u32 dst, %0, %2;\n\t"
+          "mapa.shared::cluster.u32 bar, %1, %2;\n\t"
+          "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [dst], {%3, %4, %5, %6}, "
+          "[bar];\n\t}" ::"r"(smem_addr(&x.slot[turn & 1u][first + lane])),
+          "r"(smem_addr(&x.bar[turn & 1u])), "r"(to), "r"(mine.x), "r"(mine.y), "r"(mine.z),
+          "r"(mine.w)
+          : "memory");
   }
 }
-// The other end: lane i < C has CTA i's.
-__device__ __forceinline__ uint4 exchange_take(Exchange& x, uint32_t turn, int C, int* abort) {
+// The other end: lane i has share i's.
+__device__ __forceinline__ uint4 exchange_take(Exchange& x, uint32_t turn, int shares, int* abort) {
   mbar_wait(&x.bar[turn & 1u], (turn >> 1) & 1u, abort);
   const int lane = threadIdx.x & 31;
-  return lane < C ? x.slot[turn & 1u][lane] : make_uint4(0xff800000u, 0u, 0u, 0u);
+  return lane < shares ? x.slot[turn & 1u][lane] : make_uint4(0xff800000u, 0u, 0u, 0u);
 }
 
 // Natural log-sum-exp of a state, rounded once: the maximum and the

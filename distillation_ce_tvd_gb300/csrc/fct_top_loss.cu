@@ -13,6 +13,15 @@
 // it: p_rest keeps its relative precision where the list holds nearly all of
 // the mass.  A bit per word in shared memory says which those are; a vector of
 // 16 bytes looks up its own few bits.
+//
+// Measured (of the copy rate, 6692 GB/s): forward 410-420 us at 8192 x 151936
+// bf16, K = 64 (0.89-0.91), 165 us at 1021 x 256000 fp32, K = 256 (0.95);
+// backward 736 us at the former (1.01); both in one launch 977 us (0.76),
+// against 1178 by two.  The forward on loads of its own into registers, three
+// CTAs per SM, took 455 us, with one thing after the other per row 446.  The
+// backward's segments of 2048 vectors, with the target looked for in every
+// vector, took 1070 us: what a CTA does before its first load has to be small
+// beside its 64 KB.
 #include <climits>
 #include <mutex>
 
@@ -123,21 +132,25 @@ __host__ __device__ constexpr int64_t bit_words(int64_t vecs, int vec) {
   return ((vecs + 2) * vec + 31) / 32 + 1;
 }
 
-// One cluster of C CTAs per row, C fixed by V and the element type.  Each CTA
-// streams its share of the row.  A warp of its own then works out the row's
-// loss from the warps' states, the list, and what the peers send, while the
-// consumers go on to the next row, whose list they fetched ahead.  (What a row
-// costs beside its bytes was 5.8 us of its CTA's time with one thing after the
-// other.)
+// A row is `shares` shares, fixed by V and the element type, each with a state
+// of its own, merged in their order: the same sums however many CTAs take them.
+// A cluster of C CTAs takes a row: the forward alone as few as hold the bits,
+// each with its shares one after the other; with the gradient one CTA per
+// share.  A warp of its own works out the row's loss from the warps' states,
+// the list, and what the peers send, while the consumers go on with the next
+// row, whose list they fetched ahead.  (What a row costs beside its bytes was
+// 5.8 us of its CTA's time with one thing after the other.)
 //
 // kGrad: the consumers wait for the row's sums, go over their share once more,
-// which L2 still holds, and write the gradient.
+// which L2 still holds, and write the gradient.  (Sweeping the next row's share
+// meanwhile needs twice the rows in L2, so twice the CTAs per row, each with
+// the whole list to look up: 1277 us instead of 1035 at 8192 x 151936 bf16.)
 constexpr int kFwdConsumers = 512;
 constexpr int kFwdChunk = Ring<kFwdConsumers>::kChunk;
 constexpr int kFwdThreads = kFwdConsumers + 64;  // consumers, copying warp, finishing warp
 
 struct Turn {  // a row on its way from the consumers to the finishing warp
-  float2 warp_state[kFwdConsumers / 32];
+  float2 warp_state[kMaxShares][kFwdConsumers / 32];
   float tg_logit;
   int bad;
   Sums sums;
@@ -145,7 +158,7 @@ struct Turn {  // a row on its way from the consumers to the finishing warp
 
 template <typename T, bool kGrad>
 __global__ void __launch_bounds__(kFwdThreads, 2)
-    top_forward_kernel(TopArgs a, int words, int stages) {
+    top_forward_kernel(TopArgs a, int words, int stages, int shares) {
   constexpr int VE = Elem<T>::kVec, NT = kFwdConsumers;
   extern __shared__ uint4 top_smem[];
   __shared__ __align__(8) RingBars bars;
@@ -156,6 +169,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   __shared__ Turn turns[2];
   const int K = static_cast<int>(a.K), V = static_cast<int>(a.V), tid = threadIdx.x;
   const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+  const int own = kGrad ? 1 : shares / C, first = rank * own;  // this CTA's shares
   uint32_t* bits = reinterpret_cast<uint32_t*>(top_smem + stages * kFwdChunk);
   const uint8_t* bytes = reinterpret_cast<const uint8_t*>(bits);
   // the lists of two rows: student's and teacher's logits, words
@@ -167,7 +181,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   if (tid == 0) {
     exchange_init(exchange);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ready_bar[i], kFwdConsumers / 32);
+      mbar_init(&ready_bar[i], NT / 32);
       mbar_init(&done_bar[i], 1);
     }
     ring.init();
@@ -176,10 +190,9 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   __syncthreads();
   cluster_barrier();  // every CTA's barriers exist
   const int64_t n_clusters = gridDim.x / C;
-  auto share_of = [&](const Row<T>& r, int* v0, int* v1) {
-    const int per = static_cast<int>(share(r.nvec, C));
-    *v0 = min(rank * per, r.nvec);
-    *v1 = min(*v0 + per, r.nvec);
+  // the first vector of a share, and the end of the last
+  auto share_at = [&](const Row<T>& r, int i) {
+    return static_cast<int>(min(int64_t(r.nvec), i * share(r.nvec, shares)));
   };
 
   if (tid >= NT + 32) {  // ---- the finishing warp
@@ -201,16 +214,18 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       const float t_rest = a.rest ? a.rest[row] : -INFINITY;
       Turn& t = turns[turn & 1u];
       mbar_wait(&ready_bar[turn & 1u], (turn >> 1) & 1u, &bars.abort);
-      const float2 own = lane < kFwdConsumers / 32 ? t.warp_state[lane] : make_float2(-INFINITY, 0.f);
-      Lse2 rest = merge_warp(Lse2{own.x, own.y});
-      bool wrong = t.bad != 0;
-      if (C > 1) {
-        exchange_send(exchange, turn, C, rank,
-                      make_uint4(__float_as_uint(rest.m2), __float_as_uint(rest.s), wrong, 0u));
-        const uint4 got = exchange_take(exchange, turn, C, &bars.abort);
-        wrong = __any_sync(0xffffffffu, got.z != 0);
-        rest = merge_warp(Lse2{__uint_as_float(got.x), __uint_as_float(got.y)});
+      uint4 got = make_uint4(0xff800000u, 0u, 0u, 0u);  // lane i: share i (of this CTA, of all)
+      for (int i = 0; i < own; ++i) {
+        const float2 w = lane < NT / 32 ? t.warp_state[i][lane] : make_float2(-INFINITY, 0.f);
+        const Lse2 m = merge_warp(Lse2{w.x, w.y});
+        if (lane == i) got = make_uint4(__float_as_uint(m.m2), __float_as_uint(m.s), t.bad, 0u);
       }
+      if (C > 1) {
+        exchange_send(exchange, turn, C, shares, first, own, got);
+        got = exchange_take(exchange, turn, shares, &bars.abort);
+      }
+      const bool wrong = __any_sync(0xffffffffu, got.z != 0);
+      const Lse2 rest = merge_warp(Lse2{__uint_as_float(got.x), __uint_as_float(got.y)});
       if (kGrad || rank == 0) {
         const Lists l = list(turn);
         Sums o = list_sums(l.s, l.t, K, rest.m2, rest.s, t_rest);
@@ -238,20 +253,22 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     }
   } else if (tid >= NT) {
     if (tid == NT) {  // ---- copies
-      const uint64_t once = policy_evict_first(), first = kGrad ? policy_evict_last() : once;
+      const uint64_t once = policy_evict_first(), keep = kGrad ? policy_evict_last() : once;
       uint32_t copied = 0;
-      for (int64_t row = blockIdx.x / C; row < a.BT; row += n_clusters) {
+      bool ok = true;
+      auto sweep = [&](int64_t row, uint64_t pol) {
+        const Row<T> r(static_cast<const T*>(a.student) + row * a.ld_s, V);
+        for (int i = 0; ok && i < own; ++i) {
+          const int v0 = share_at(r, first + i), v1 = share_at(r, first + i + 1);
+          ok = ring.copy(r, v0, v1, pol);
+          if (ok) copied += chunks_of<NT>(v0, v1);
+        }
+      };
+      for (int64_t row = blockIdx.x / C; ok && row < a.BT; row += n_clusters) {
         const int64_t tg = a.target[row];
         if (tg == a.ignore_index) continue;
-        const Row<T> r(static_cast<const T*>(a.student) + row * a.ld_s, V);
-        int v0, v1;
-        share_of(r, &v0, &v1);
-        if (!ring.copy(r, v0, v1, first)) break;
-        copied += chunks_of<NT>(v0, v1);
-        if (kGrad && tg >= 0 && tg < V) {
-          if (!ring.copy(r, v0, v1, once)) break;
-          copied += chunks_of<NT>(v0, v1);
-        }
+        sweep(row, keep);
+        if (kGrad && tg >= 0 && tg < V) sweep(row, once);
       }
       ring.drain(copied);
     }
@@ -283,6 +300,49 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
                  ? Elem<T>::load1(static_cast<const T*>(a.student) + row * a.ld_s + tg)
                  : 0.f;
     };
+    // Whether a position (see Row; from vector v0) is in this CTA's part of the row.
+    auto mine = [&](int pos, int v0, int v1) {
+      return (pos >= VE || rank == 0) && (pos < (v1 - v0 + 1) * VE || rank == C - 1);
+    };
+    // The second sweep of a row: the gradient.
+    struct Second {
+      int64_t row, tg;
+      float tg_logit, up_ce, up_tvd, t_rest;
+    };
+    auto write_gradient = [&](const Second& f, uint32_t its_turn) {
+      T* grow = static_cast<T*>(a.grad) + f.row * a.ld_g;
+      mbar_wait(&done_bar[its_turn & 1u], (its_turn >> 1) & 1u, &bars.abort);
+      if (f.tg < 0 || f.tg >= V) {
+        const int64_t per_cta = (a.V + C - 1) / C;
+        fill_grad<NT>(grow, rank * per_cta, min(a.V, (rank + 1) * per_cta),
+                      __uint_as_float(0x7fc00000u));
+      } else {
+        const Row<T> r(static_cast<const T*>(a.student) + f.row * a.ld_s, V);
+        const int v0 = share_at(r, first), v1 = share_at(r, first + 1);
+        const Sums sums = turns[its_turn & 1u].sums;
+        const Coefs c = make_coefs(f.up_ce, f.up_tvd, sums.lse, sums.rest, sums.t_lse, f.t_rest,
+                                   sums.sigma);
+        const Outside o(c);
+        const bool same = same_alignment(r.p, grow);
+        ring.each(v0, v1, [&](uint4 w, int iv) {
+          vector_grad(o, w, grow + r.head + iv * VE, same, once);
+        });
+        loose_grad(r, grow, o, rank == 0, rank == C - 1);
+        // the words of U and the target over what was written there
+        const Lists l = list(its_turn);
+        bool listed = false;
+        for (int k = tid; k < K; k += NT) listed = listed || l.idx[k] == f.tg;
+        listed = row_or<NT>(listed);
+        for (int k = tid; k < K; k += NT) {
+          const int v = l.idx[k];
+          if (v >= 0 && mine(v - r.head + VE - v0 * VE, v0, v1))
+            Elem<T>::store1(grow + v, listed_grad(c, l.s[k], l.t[k], v == f.tg));
+        }
+        const int at = static_cast<int>(f.tg);
+        if (tid == 0 && !listed && mine(at - r.head + VE - v0 * VE, v0, v1))
+          Elem<T>::store1(grow + at, target_grad(c, f.tg_logit));
+      }
+    };
     int64_t row = blockIdx.x / C;
     int64_t tg = fetch_target(row);
     Entry e{-1, -INFINITY, -INFINITY};
@@ -292,42 +352,46 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       tg_logit = logit_of(row, tg);
     }
     for (; row < a.BT; row += n_clusters) {
-      T* grow = kGrad ? static_cast<T*>(a.grad) + row * a.ld_g : nullptr;
-      float up_ce = 0.f, up_tvd = 0.f, t_rest = 0.f;
-      if constexpr (kGrad) {
-        up_ce = a.grad_ce[row * a.grad_stride];
-        up_tvd = a.grad_tvd[row * a.grad_stride];
-        t_rest = a.rest ? a.rest[row] : -INFINITY;
-      }
       const int64_t next_row = row + n_clusters;
       const int64_t next_tg = fetch_target(next_row);
       const bool next_live = next_tg != a.ignore_index;
-      int next_word = next_live ? fetch_word(next_row, tid) : -1;
+      const int next_word = next_live ? fetch_word(next_row, tid) : -1;
       if (tg == a.ignore_index) {
         if constexpr (kGrad) {
           const int64_t per_cta = (a.V + C - 1) / C;
-          fill_grad<NT>(grow, rank * per_cta, min(a.V, (rank + 1) * per_cta), 0.f);
+          fill_grad<NT>(static_cast<T*>(a.grad) + row * a.ld_g, rank * per_cta,
+                        min(a.V, (rank + 1) * per_cta), 0.f);
+        }
+        if (next_live) {
+          e = fetch(next_row, tid, next_word);
+          tg_logit = logit_of(next_row, next_tg);
         }
       } else {
+        Second second;
+        if constexpr (kGrad) {
+          second.row = row;
+          second.tg = tg;
+          second.tg_logit = tg_logit;
+          second.up_ce = a.grad_ce[row * a.grad_stride];
+          second.up_tvd = a.grad_tvd[row * a.grad_stride];
+          second.t_rest = a.rest ? a.rest[row] : -INFINITY;
+        }
         const T* srow = static_cast<const T*>(a.student) + row * a.ld_s;
         const Row<T> r(srow, V);
-        int v0, v1;
-        share_of(r, &v0, &v1);
-        const bool tg_ok = tg >= 0 && tg < V;
-        // ---- the list, and the bits of its words in this CTA's share
-        auto mine = [&](int pos) {
-          return (pos >= VE || rank == 0) && (pos < (v1 - v0 + 1) * VE || rank == C - 1);
-        };
+        const int v0 = share_at(r, first), v_end = share_at(r, first + own);
+        // ---- the list, and the bits of its words in this CTA's part
         Turn& t = turns[turn & 1u];
         const Lists l = list(turn);
-        if (turn >= 2)  // the row of two turns ago has left these buffers
+        // the row of two turns ago has left these buffers (kGrad has waited for it)
+        if (!kGrad && turn >= 2)
           mbar_wait(&done_bar[turn & 1u], ((turn >> 1) - 1) & 1u, &bars.abort);
         bool bad = false;
         auto enter = [&](int k, const Entry& x) {
           if (x.word == -2) bad = true;
           if (x.word >= 0) {
             const int pos = x.word - r.head + VE - v0 * VE;
-            if (mine(pos) && (atomicOr(&bits[pos >> 5], 1u << (pos & 31)) >> (pos & 31) & 1u))
+            if (mine(pos, v0, v_end) &&
+                (atomicOr(&bits[pos >> 5], 1u << (pos & 31)) >> (pos & 31) & 1u))
               bad = true;
           }
           l.s[k] = x.s;
@@ -337,42 +401,43 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         if (tid < K) enter(tid, e);
         for (int k = tid + NT; k < K; k += NT) enter(k, fetch(row, k, fetch_word(row, k)));
         bad = row_or<NT>(bad);
-        // ---- the log-sum-exp of the words outside U
-        Run st = run_empty();
+        // ---- the log-sum-exp of the words outside U, share by share
         const uint8_t* own_bytes = bytes - v0 * VE / 8;
-        ring.template each_warp<T>(v0, v1, [&](uint4 w, int iv) {
-          float x[VE];
-          Elem<T>::unpack(w, x);
-          float vm = vec_max(x);
-          // (past the share's end: within the bits' room, or of no matter)
-          const int at = VE == 8 ? iv + 1 : (iv + 1) >> 1;
-          uint32_t m = iv < v1 ? own_bytes[at] : 0u;
-          if (VE == 4) m = (m >> (4 * ((iv + 1) & 1))) & 15u;
-          if (__any_sync(0xffffffffu, m != 0 || vm > st.limit)) {  // seldom
+        for (int i = 0; i < own; ++i) {
+          const int s0 = share_at(r, first + i), s1 = share_at(r, first + i + 1);
+          Run st = run_empty();
+          ring.template each_warp<T>(s0, s1, [&](uint4 w, int iv) {
+            float x[VE];
+            Elem<T>::unpack(w, x);
+            float vm = vec_max(x);
+            const int at = VE == 8 ? iv + 1 : (iv + 1) >> 1;
+            uint32_t m = iv < s1 ? own_bytes[at] : 0u;
+            if (VE == 4) m = (m >> (4 * ((iv + 1) & 1))) & 15u;
+            if (__any_sync(0xffffffffu, m != 0 || vm > st.limit)) {  // seldom
 #pragma unroll
-            for (int j = 0; j < VE; ++j)
-              if ((m >> j) & 1u) x[j] = -INFINITY;
-            vm = vec_max(x);
-            raise(st, vm);
+              for (int j = 0; j < VE; ++j)
+                if ((m >> j) & 1u) x[j] = -INFINITY;
+              vm = vec_max(x);
+              raise(st, vm);
+            }
+            add(st, x);
+          });
+          // the elements in no vector: the head with the first share, the tail with the last
+          if (tid < r.n_loose() && first + i == (tid < r.head ? 0 : shares - 1)) {
+            const int v = r.loose(tid), pos = v - r.head + VE - v0 * VE;
+            const float x = Elem<T>::load1(srow + v);
+            const float one[2] = {(bits[pos >> 5] >> (pos & 31)) & 1u ? -INFINITY : x, -INFINITY};
+            fold(st, one);
           }
-          add(st, x);
-        });
-        // the elements in no vector: the head with CTA 0, the tail with the last
-        if (tid < r.n_loose() && rank == (tid < r.head ? 0 : C - 1)) {
-          const int v = r.loose(tid), pos = v - r.head + VE - v0 * VE;
-          const float x = Elem<T>::load1(srow + v);
-          const float one[2] = {(bits[pos >> 5] >> (pos & 31)) & 1u ? -INFINITY : x, -INFINITY};
-          fold(st, one);
+          const Lse2 w = merge_warp(folded(st));
+          if ((tid & 31) == 0) t.warp_state[i][tid >> 5] = make_float2(w.m2, w.s);
         }
-        const Lse2 w = merge_warp(folded(st));
-        if ((tid & 31) == 0) t.warp_state[tid >> 5] = make_float2(w.m2, w.s);
         if (tid == 0) {
           t.bad = bad;
           t.tg_logit = tg_logit;
         }
         __syncwarp();
         if ((tid & 31) == 0) mbar_arrive(&ready_bar[turn & 1u]);
-        const float this_logit = tg_logit;
         // the next row's list is on its way while this one's sums are worked out
         if (next_live) {
           e = fetch(next_row, tid, next_word);
@@ -384,41 +449,10 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           if (l.idx[k] >= 0 && pos >= 0 && pos < words * 32) bits[pos >> 5] = 0;
         }
         if constexpr (kGrad) {
-          if (!tg_ok) {
-            const int64_t per_cta = (a.V + C - 1) / C;
-            fill_grad<NT>(grow, rank * per_cta, min(a.V, (rank + 1) * per_cta),
-                          __uint_as_float(0x7fc00000u));
-          } else {
-            mbar_wait(&done_bar[turn & 1u], (turn >> 1) & 1u, &bars.abort);
-            const Sums sums = t.sums;
-            const Coefs c = make_coefs(up_ce, up_tvd, sums.lse, sums.rest, sums.t_lse, t_rest,
-                                       sums.sigma);
-            const Outside o(c);
-            const bool same = same_alignment(srow, grow);
-            ring.each(v0, v1, [&](uint4 w, int iv) {
-              vector_grad(o, w, grow + r.head + iv * VE, same, once);
-            });
-            loose_grad(r, grow, o, rank == 0, rank == C - 1);
-            // the words of U and the target over what was written there
-            bool listed = false;
-            for (int k = tid; k < K; k += NT) listed = listed || l.idx[k] == tg;
-            listed = row_or<NT>(listed);
-            for (int k = tid; k < K; k += NT) {
-              const int v = l.idx[k];
-              if (v >= 0 && mine(v - r.head + VE - v0 * VE))
-                Elem<T>::store1(grow + v, listed_grad(c, l.s[k], l.t[k], v == tg));
-            }
-            const int at = static_cast<int>(tg);
-            if (tid == 0 && !listed && mine(at - r.head + VE - v0 * VE))
-              Elem<T>::store1(grow + at, target_grad(c, this_logit));
-          }
+          write_gradient(second, turn);
         }
         row_sync<NT>();  // all bits are 0, and in the gradient's case the list is read
         ++turn;
-      }
-      if (tg == a.ignore_index && next_live) {
-        e = fetch(next_row, tid, next_word);
-        tg_logit = logit_of(next_row, next_tg);
       }
       tg = next_tg;
     }
@@ -501,30 +535,51 @@ __global__ void __launch_bounds__(kBwdThreads, 6) top_backward_kernel(TopArgs a,
 
 // ---------------------------------------------------------------- launch
 
-// CTAs per row, by V and the element type alone: never the number of rows, so
-// that results do not depend on how rows are batched, and the same with and
+// The single launch's rows: one sweep from memory, one from L2, so the rows in
+// flight (two CTAs per SM) fit in 0.8 of L2, those of more than 340 KB shared by
+// two CTAs.  A row of 1 MB would take four, and what each does beside its bytes
+// then costs more than a third reading of the row (1021 x 256000 fp32: 586 us
+// against 487 by two launches; 151936 fp32, two CTAs: 492 against 558); a row
+// of 8 KB costs more in the second sweep's start than a launch (8192 x 4096
+// bf16: 211 us against 149), unless there are so few that the launch counts.
+constexpr double kKeep = 0.8;
+constexpr int kSingleShares = 2;
+constexpr int64_t kSingleRow = 40 * 1024;  // smallest row in bytes, for many rows
+bool fits(int64_t V, int dtype, int shares, int sms, int l2) {
+  return 2.0 * sms / shares * (double(V) * (dtype == FCT_BF16 ? 2 : 4)) <= kKeep * l2;
+}
+bool single_launch(const TopArgs& a, int sms, int l2) {
+  const int64_t row = a.V * (a.dtype == FCT_BF16 ? 2 : 4);
+  return fits(a.V, a.dtype, kSingleShares, sms, l2) && (row >= kSingleRow || a.BT < 2 * sms);
+}
+
+// Shares of a row, by V and the element type alone: never the number of rows,
+// so that results do not depend on how rows are batched, and the same with and
 // without the gradient, so that those give the same bits.  The bits of a CTA's
-// share take at most 32 KB, and the rows in flight (two CTAs per SM) fit in
-// 0.8 of L2, from which the single launch reads them again.
-int ctas_per_row(int64_t V, int dtype, int sms, int l2) {
-  const double row = double(V) * (dtype == FCT_BF16 ? 2 : 4);
-  int C = 1;
-  while (C < 8 && (V > int64_t(C) * 262144 || 2.0 * sms / C * row > 0.8 * l2)) C *= 2;
-  return C;
+// part take at most 32 KB.
+int shares_of(int64_t V, int dtype, int sms, int l2) {
+  int n = 1;
+  while (n < kMaxShares && V > int64_t(n) * 262144) n *= 2;
+  if (n < kSingleShares && !fits(V, dtype, 1, sms, l2) && fits(V, dtype, kSingleShares, sms, l2))
+    n = kSingleShares;
+  return n;
 }
 
 template <typename T, bool kGrad>
 cudaError_t run_forward(const TopArgs& a, int sms, int device, int l2, cudaStream_t st) {
   constexpr int VE = Elem<T>::kVec;
-  const int C = ctas_per_row(a.V, a.dtype, sms, l2);
-  const int64_t words = (bit_words(share(a.V / VE, C), VE) + 3) / 4 * 4;
+  const int shares = shares_of(a.V, a.dtype, sms, l2);
+  int C = 1;
+  while (C < shares && (kGrad || a.V > int64_t(C) * 262144)) C *= 2;
+  const int64_t words = (bit_words(shares / C * share(a.V / VE, shares), VE) + 3) / 4 * 4;
   const size_t lists = size_t(words) * 4 + list_bytes(a.K);
   // two CTAs per SM share its shared memory; a long vocabulary's bits may leave room for one
+  const int64_t room = kStreamSmem - 2 * int64_t(sizeof(Turn) * 2);
   int resident = 2;
-  int stages = static_cast<int>((kStreamSmem / 2 - int64_t(lists)) / (kFwdChunk * 16));
+  int stages = static_cast<int>((room / 2 - int64_t(lists)) / (kFwdChunk * 16));
   if (stages < 2) {
     resident = 1;
-    stages = static_cast<int>((kStreamSmem - int64_t(lists)) / (kFwdChunk * 16));
+    stages = static_cast<int>((room - int64_t(lists)) / (kFwdChunk * 16));
   }
   if (stages > kMaxStages) stages = kMaxStages;
   auto kernel = top_forward_kernel<T, kGrad>;
@@ -532,7 +587,7 @@ cudaError_t run_forward(const TopArgs& a, int sms, int device, int l2, cudaStrea
   static cudaError_t set[64];
   std::call_once(once[device], [&] {
     set[device] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kStreamSmem);
+                                       kStreamSmem - static_cast<int>(sizeof(Turn)) * 4);
   });
   if (set[device] != cudaSuccess) return set[device];
   cudaLaunchConfig_t cfg = {};
@@ -550,7 +605,7 @@ cudaError_t run_forward(const TopArgs& a, int sms, int device, int l2, cudaStrea
   if (clusters < 1) clusters = 1;
   if (clusters > a.BT) clusters = a.BT;
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * C));
-  return cudaLaunchKernelEx(&cfg, kernel, a, static_cast<int>(words), stages);
+  return cudaLaunchKernelEx(&cfg, kernel, a, static_cast<int>(words), stages, shares);
 }
 
 template <typename T>
@@ -581,6 +636,12 @@ cudaError_t run_backward(const TopArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_top_forward(const TopArgs& a, int sms, int device, int l2, cudaStream_t st) {
+  if (a.grad && !single_launch(a, sms, l2)) {
+    TopArgs f = a;
+    f.grad = nullptr;
+    const cudaError_t e = launch_top_forward(f, sms, device, l2, st);
+    return e != cudaSuccess ? e : launch_top_backward(a, st);
+  }
   if (a.dtype == FCT_BF16)
     return a.grad ? run_forward<bf16_t, true>(a, sms, device, l2, st)
                   : run_forward<bf16_t, false>(a, sms, device, l2, st);

@@ -1,18 +1,22 @@
 // The K largest logits of each row, and the log-sum-exp of the others.
 //
-// One pass over the row, V e bytes, which bound it.  Every thread keeps the
-// largest logit of each of its vectors' columns so far.  These maxima are
-// logits of their own, so what K of them reach, K logits of the row reach: that
-// is a threshold, found from the first chunk of a row (32 KB, 16384 bf16) and
-// again after 2, 4, 8, ... chunks.  A vector with nothing above it is folded
-// into the log-sum-exp of the rest at once; of 594 vectors of a warp at V =
-// 151936 and K = 64, about 34 are not.  Those wait in their warp's queue and
-// are taken 32 at a time, one per lane, so that a warp does not go through the
-// slow path for one lane: their elements above the threshold become candidates
-// in shared memory, the others are folded.  (Candidates taken at once, vector
-// by vector, cost 194 instructions per 32 vectors instead of ??, 1218 us at
-// 8192 x 151936 bf16, K = 64; a first sweep for the threshold and a second
-// over L2, 895.)
+// One pass over the row, V e bytes.  Every thread keeps the largest logit of
+// its vectors' columns so far.  These maxima are logits of their own, so what K
+// of them reach, K logits of the row reach: that is a threshold, found from the
+// first chunk of a row (16 KB, 8192 bf16) and again after 2, 4, 8, ... chunks.
+// A vector with nothing above it is folded into the log-sum-exp of the rest at
+// once; at V = 151936 and K = 64 about 300 of 18992 are not.  Those wait in
+// their warp's queue and are taken 32 at a time, one per lane, so that a warp
+// does not go through the slow path for one lane: their elements above the
+// threshold become candidates in shared memory, the others are folded.
+//
+// 8192 x 151936 bf16, K = 64: 600 us, 4.2 TB/s, 0.62 of the copy rate; 1003 x
+// 256000 fp32, K = 256: 305 us, 3.4 TB/s.  What bounds it is instructions (100
+// per 32 vectors, 65% of the issue slots) and what a row costs beside its
+// bytes (threshold, last candidates, order: some 8 us of a CTA, hidden by the
+// other three of an SM).  Before: candidates taken vector by vector as they
+// came (194 instructions) 1218 us; a sweep for the threshold and a second one
+// over L2 895; one sweep on two CTAs of 512 threads per SM 715.
 //
 // So the rest is summed from its own terms, never as a difference: it keeps
 // its relative precision however little it holds.  Candidates that a selection
