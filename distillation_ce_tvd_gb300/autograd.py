@@ -173,27 +173,32 @@ def fused_ce_tvd_top_loss(student, target, top_values, top_index, rest_lse=None,
 class FusedCETVDTopMeanLoss(torch.autograd.Function):
     """alpha * mean(ce) + beta * mean(tvd) against a teacher's top logits, over the rows not ignored.
 
-    As for FusedCETVDMeanLoss, the forward runs forward and backward in one launch and keeps the
-    student's gradient, which the backward scales by the incoming one.
+    The backward takes the mean's weights times the incoming gradient as the rows' upstream
+    gradients, on the device: unlike FusedCETVDMeanLoss, no gradient is kept from the forward, and
+    none is scaled in a pass of its own.
     """
 
     @staticmethod
     def forward(ctx, student, target, top_values, top_index, rest_lse=None,
                 ignore_index=binding.IGNORE_INDEX, alpha=1.0, beta=1.0, inplace=False):
-        gce, gtvd, _ = binding.fused_ce_tvd_mean_upstream(target, ignore_index, alpha, beta)
-        ce, tvd, *_, grad = binding.fused_ce_tvd_top_forward_backward(
+        ce, tvd, *saved = binding.fused_ce_tvd_top_forward(
             student.detach(), target, top_values.detach(), top_index,
-            None if rest_lse is None else rest_lse.detach(), gce, gtvd, ignore_index,
-            inplace=inplace)
-        ctx.save_for_backward(grad)
+            None if rest_lse is None else rest_lse.detach(), ignore_index)
         loss = binding.fused_ce_tvd_mean_loss(ce, tvd, target, ignore_index, alpha, beta)
+        ctx.save_for_backward(student, target, top_values, top_index, rest_lse, *saved)
+        ctx.mean = (ignore_index, alpha, beta)
+        ctx.inplace = inplace
         return loss.reshape(())
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_out):
-        (grad,) = ctx.saved_tensors
-        return (grad * grad_out.to(grad.dtype),) + (None,) * 8
+        student, target, *rest = ctx.saved_tensors
+        gce, gtvd, _ = binding.fused_ce_tvd_mean_upstream(target, *ctx.mean)
+        scale = grad_out.float()
+        grad = binding.fused_ce_tvd_top_backward(student.detach(), target, *rest, gce * scale,
+                                                 gtvd * scale, ctx.mean[0], inplace=ctx.inplace)
+        return (grad,) + (None,) * 8
 
 
 def fused_ce_tvd_top_mean_loss(student, target, top_values, top_index, rest_lse=None,

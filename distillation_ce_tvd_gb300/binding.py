@@ -1484,7 +1484,7 @@ def fused_ce_tvd_top_forward_backward(student, target, top_values, top_index, re
                                       student_lse=None, student_rest=None, teacher_lse=None,
                                       sigma=None, grad_student=None, inplace=False,
                                       dev_status=None):
-    """Forward and backward against a teacher's top logits in one launch, given the upstream
+    """Forward and backward against a teacher's top logits in one call, given the upstream
     gradients: (ce, tvd, student_lse, student_rest, teacher_lse, sigma, grad_student), equal to
     fused_ce_tvd_top_forward followed by fused_ce_tvd_top_backward."""
     x, ld, code = _logits2(student, "student")

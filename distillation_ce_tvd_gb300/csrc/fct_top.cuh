@@ -344,7 +344,7 @@ __device__ __forceinline__ uint4 exchange_take(Exchange& x, uint32_t turn, int s
 // three roundings would be of numbers near 20, and the backward takes
 // exp(x - lse) of the result.)
 __device__ __forceinline__ float finish(float m2, float s) {
-  if (s == 0.f) return -INFINITY;
+  if (s == 0.f && m2 == -INFINITY) return -INFINITY;
   if (!(s > 0.f) || !(fabsf(m2) < INFINITY)) return __uint_as_float(0x7fc00000u);
   int e;
   const float f = frexpf(s, &e);

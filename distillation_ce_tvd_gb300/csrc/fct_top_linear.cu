@@ -587,6 +587,30 @@ __global__ void __launch_bounds__(kSortThreads) merge_kernel(MergeArgs a) {
   }
 }
 
+// The hidden states with zeros in ignored rows, for d weight: a padded batch's
+// rows may hold anything there, and 0 times NaN is NaN.
+__global__ void __launch_bounds__(256) live_rows_kernel(const uint16_t* h, int64_t ld_h,
+                                                        const int64_t* target, int64_t ignore_index,
+                                                        uint16_t* out, int64_t ld_out, int64_t rows,
+                                                        int64_t d) {
+  const int64_t per = (d + 7) / 8, total = rows * per;
+  for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
+    const int64_t r = i / per, c = (i - r * per) * 8;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (target[r] != ignore_index) {
+      if (c + 8 <= d) {
+        v = *reinterpret_cast<const uint4*>(h + r * ld_h + c);
+      } else {  // the last columns; the row's padding is no one's
+        uint16_t e[8] = {};
+        for (int j = 0; c + j < d; ++j) e[j] = h[r * ld_h + c + j];
+        v = make_uint4(e[0] | uint32_t(e[1]) << 16, e[2] | uint32_t(e[3]) << 16,
+                       e[4] | uint32_t(e[5]) << 16, e[6] | uint32_t(e[7]) << 16);
+      }
+    }
+    *reinterpret_cast<uint4*>(out + r * ld_out + c) = v;
+  }
+}
+
 // bf16 rows from the fp32 sum over the pieces.
 __global__ void __launch_bounds__(256) round_kernel(const float* src, int64_t ld_src, uint16_t* dst,
                                                     int64_t ld, int64_t rows, int64_t cols) {
@@ -697,6 +721,8 @@ struct BackwardSpace {
   float* listed;
   float* tg_logit;
   RowCoefs* rows;
+  uint16_t* live;  // the hidden states, zero in ignored rows
+  int64_t ld_live;
   uint16_t* G;
   float* sum;   // d hidden summed over pieces, or the partial sums of its one product
   size_t sum_bytes;
@@ -712,6 +738,8 @@ struct BackwardSpace {
     listed = c.take<float>(BT, K);
     tg_logit = c.take<float>(BT, 1);
     rows = c.take<RowCoefs>(BT, 1);
+    ld_live = (d + 7) / 8 * 8;
+    live = c.take<uint16_t>(BT, ld_live);
     G = c.take<uint16_t>(BT, ld_g);
     // one piece: room to split its K where d hidden has few tiles
     sum_bytes = 0;
@@ -767,6 +795,13 @@ cudaError_t launch_top_linear_backward(const TopLinearArgs& a, int sms, int devi
   list_kernel<true><<<static_cast<unsigned>(a.BT), kSortThreads, 0, st>>>(l);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  if (a.grad_w != nullptr) {
+    const int64_t blocks = (a.BT * (w.ld_live / 8) + 255) / 256, most = int64_t(sms) * 8;
+    live_rows_kernel<<<static_cast<unsigned>(blocks < most ? blocks : most), 256, 0, st>>>(
+        static_cast<const uint16_t*>(a.h), a.ld_h, a.target, a.ignore_index, w.live, w.ld_live,
+        a.BT, a.d);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
   const size_t ew = a.grad_w_kind == FCT_GEMM_BF16 ? 2 : 4;
   for (int64_t v0 = 0; v0 < a.V; v0 += w.piece) {
     const int64_t n = a.V - v0 < w.piece ? a.V - v0 : w.piece;
@@ -792,7 +827,7 @@ cudaError_t launch_top_linear_backward(const TopLinearArgs& a, int sms, int devi
     }
     // d weight of the piece (n x d) = G^T (n x BT) h (BT x d)
     if (a.grad_w != nullptr &&
-        (e = launch_gemm(GemmOperand{w.G, w.ld_g, true}, GemmOperand{a.h, a.ld_h, true},
+        (e = launch_gemm(GemmOperand{w.G, w.ld_g, true}, GemmOperand{w.live, w.ld_live, true},
                          static_cast<char*>(a.grad_w) + size_t(v0) * size_t(a.ld_gw) * ew, a.ld_gw,
                          a.grad_w_kind, n, a.d, a.BT, a.dev_status, sms, st)) != cudaSuccess)
       return e;

@@ -712,7 +712,7 @@ typedef struct {
 
 /*
  * The loss of (BT, V) student logits against top lists: forward, backward,
- * and both in one launch where the upstream gradients are known before.
+ * and both in one call where the upstream gradients are known before.
  *
  *   student, target, ignore_index, grad_ce, grad_tvd, grad_stride,
  *   grad_student : as for fused_ce_tvd_forward, _backward and
@@ -724,9 +724,10 @@ typedef struct {
  *                  words).  The backward reads the last four.  Rows with
  *                  target == ignore_index: zeros, and the list is not read.
  *   V            : at most 2^23, else FCT_ERR_UNSUPPORTED.
- * The forward reads the row once, the backward reads and writes it once, the
- * single launch reads and writes it once in memory (its second pass reads
- * from L2) and gives the bits of the two calls.  The forward takes sign(p - q)
+ * The forward reads the row once, the backward reads and writes it once.  Both
+ * together give the bits of the two calls; rows of 40 to 680 KB (and fewer, of
+ * few rows) go in one launch that reads a row from memory once and the second
+ * time from L2, others in two.  The forward takes sign(p - q)
  * from fp32 sums relative to the maxima, the backward from exp(s -
  * student_lse) and exp(t - teacher_lse); where both are within their roundings
  * of each other and p > 3/4, it takes the sign that sigma has (a student and a
@@ -793,9 +794,9 @@ int fused_ce_tvd_top_forward_backward(
  * Logits are sums in fp32 of partial sums of 1024 products (which the tensor
  * cores accumulate in fp32), the same in both directions.  The gradient of a
  * logit is rounded to bf16 for the two products.  An ignored row gets a zero
- * gradient; its hidden states enter d weight times zero, so they have to be
- * finite.  A row that is NaN (a wrong target or list, not-finite logits)
- * makes d weight NaN.  Repeated calls give the same bits.
+ * gradient and adds nothing to d weight, whatever its hidden states hold.  A
+ * row that is NaN (a wrong target or list, not-finite logits) makes d weight
+ * NaN.  Repeated calls give the same bits.
  */
 size_t fused_linear_ce_tvd_top_forward_workspace_size(int64_t BT, int64_t V,
                                                       int64_t K);

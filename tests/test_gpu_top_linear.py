@@ -203,6 +203,21 @@ def test_all_rows_ignored_and_no_teacher():
     check(c, *call(c))
 
 
+def test_a_padded_batch():
+    """Ignored rows whose hidden states and lists hold anything: no part of either gradient."""
+    c = make(40, 700, 72, 6, 21)
+    c["target"][25:] = tu.IGNORE
+    want = call(c)
+    c["h"][25:] = math.nan
+    c["h"][30] = math.inf
+    c["index"][25:], c["values"][25:] = 1 << 30, math.nan
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = call(c, dev_status=status)
+    for a, b in zip((*want[0], *want[1:]), (*got[0], *got[1:])):
+        assert torch.equal(a, b)
+    assert status.item() == 0 and (got[1][25:] == 0).all()
+
+
 def test_repeated_calls_streams_graphs_and_no_rows():
     c = make(150, 3000, 256, 20, 15)
     x = cuda(c)
