@@ -45,8 +45,7 @@ namespace {
 
 using namespace top;
 
-constexpr int kBins = 1024;
-static_assert(kBins * 4 >= kPerThread * 512 * 2, "the maxima are in the histogram's place");
+constexpr int kBins = 512;  // of a level of a selection
 // Up to this K a row belongs to 256 threads, above it to 512, whose maxima are
 // more.  What a row costs beside its bytes takes a CTA 10 us, one thing after
 // the other: four small CTAs per SM hide more of it than two large ones.
@@ -62,7 +61,7 @@ constexpr int kFewMaxima = NT / 4;
 __host__ __device__ constexpr int slack(int K) { return K / 4 + 64; }
 // Room for candidates: twice what a selection keeps (so that a chunk that brings
 // K more finds room, and a sort its power of two), and a round of vectors.
-constexpr int kRound = 128;  // vectors of a round
+constexpr int kRound = 64;  // vectors of a round
 __host__ __device__ constexpr int capacity(int K, int vec) {
   return 2 * (K + slack(K)) + kRound * vec;
 }
@@ -100,10 +99,14 @@ __device__ __forceinline__ float element(uint4 w, int j, bf16_t) {
 
 struct Shared {
   uint64_t* entry;  // [cap] rank keys of the candidates
-  // [kBins]: a selection's bins; between selections the maxima that a threshold
-  // is found from; at a row's end the few entries that are ordered by counting
+  // [hist_ints(threads)]: a selection's bins; between selections the maxima that
+  // a threshold is found from; at a row's end the few entries that are ordered
+  // by counting
   int* hist;
 };
+__host__ __device__ constexpr int hist_ints(int threads) {
+  return kBins > kPerThread * threads / 2 ? kBins : kPerThread * threads / 2;
+}
 __device__ __forceinline__ float entry_value(uint64_t e) {
   return value_of(static_cast<uint32_t>(e >> 32));
 }
@@ -170,7 +173,7 @@ __device__ void drop(const Shared& sh, Scratch<NT>& sc, int from, int n, float2&
 //
 // Levels of a histogram over a range of rank keys: the range first spans all
 // entries, then the bin that holds the K-th, until the bins up to that one
-// hold few enough.  The K-th bin narrows by 1024 a level; single keys are
+// hold few enough.  The K-th bin narrows by 512 a level; single keys are
 // unique, so that it ends.
 template <int NT>
 __device__ __noinline__ int select(const Shared& sh, Scratch<NT>& sc, int n, int K, float2& dropped,
@@ -197,9 +200,9 @@ __device__ __noinline__ int select(const Shared& sh, Scratch<NT>& sc, int n, int
   row_sync<NT>();
   uint64_t from = uint64_t(sc.lo) << 32, to = (uint64_t(sc.hi) << 32) | 0xffffffffu;
   int above = 0;  // entries ranking above the range
-  for (int level = 0; level < 8; ++level) {
+  for (int level = 0; level < 9; ++level) {
     const uint64_t span = to - from;
-    const int shift = max(0, 54 - __clzll(static_cast<long long>(span | 1)));
+    const int shift = max(0, 55 - __clzll(static_cast<long long>(span | 1)));
     for (int i = tid; i < kBins; i += NT) sh.hist[i] = 0;
     row_sync<NT>();
     for (int i = tid; i < n; i += NT) {
@@ -209,6 +212,7 @@ __device__ __noinline__ int select(const Shared& sh, Scratch<NT>& sc, int n, int
     row_sync<NT>();
     // bins from the highest down, a few per thread
     constexpr int kOwn = kBins / NT;
+    static_assert(kOwn * NT == kBins, "whole bins per thread");
     const int b0 = kBins - 1 - kOwn * tid;
     int own[kOwn], mine = 0;
 #pragma unroll
@@ -266,14 +270,16 @@ template <int NT, typename F>
 __device__ __forceinline__ void count_entries(const uint64_t* entry, int n, F f) {
   const int tid = threadIdx.x;
   const int parts = n <= NT / 16 ? 16 : n <= NT / 8 ? 8 : n <= NT / 4 ? 4 : n <= NT / 2 ? 2 : 1;
-  const int i = tid / parts, part = tid % parts;
-  if ((tid & ~31) / parts >= n) return;  // nothing for the whole warp
-  const uint64_t own = i < n ? entry[i] : ~0ull;
-  int place = 0;
+  const int part = tid % parts;
+  for (int base = (tid & ~31) / parts; base < n; base += NT / parts) {  // (the warp's first entry)
+    const int i = base + (tid & 31) / parts;
+    const uint64_t own = i < n ? entry[i] : ~0ull;
+    int place = 0;
 #pragma unroll 8
-  for (int j = part; j < n; j += parts) place += entry[j] > own;
-  for (int d = 1; d < parts; d *= 2) place += __shfl_xor_sync(0xffffffffu, place, d);
-  if (i < n && part == 0) f(place, own);
+    for (int j = part; j < n; j += parts) place += entry[j] > own;
+    for (int d = 1; d < parts; d *= 2) place += __shfl_xor_sync(0xffffffffu, place, d);
+    if (i < n && part == 0) f(place, own);
+  }
 }
 
 // Sorts n entries, highest rank first (bitonic, a power of two of them: the
@@ -442,17 +448,15 @@ __global__ void __launch_bounds__(NT + 32, 1024 / NT)
         row_sync<NT>();
         uint32_t* keys = sc.pool_key[found++ & 1u];
         if (warp < pools) {
-          const uint4* m = reinterpret_cast<const uint4*>(maxima + warp * NT) + lane;
+          const uint2* m = reinterpret_cast<const uint2*>(maxima + warp * NT) + lane;
           uint32_t key[kPerLane];
 #pragma unroll
-          for (int q = 0; q < kPerLane / 8; ++q) {
-            const uint4 k8 = m[q * 32];
-            const uint32_t two[4] = {k8.x, k8.y, k8.z, k8.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              key[q * 8 + 2 * j] = two[j] & 0xffffu;
-              key[q * 8 + 2 * j + 1] = two[j] >> 16;
-            }
+          for (int q = 0; q < kPerLane / 4; ++q) {
+            const uint2 k4 = m[q * 32];
+            key[q * 4] = k4.x & 0xffffu;
+            key[q * 4 + 1] = k4.x >> 16;
+            key[q * 4 + 2] = k4.y & 0xffffu;
+            key[q * 4 + 3] = k4.y >> 16;
           }
           const uint32_t t = warp_threshold(key, (K + pools - 1) / pools);
           if (lane == 0) keys[warp] = t << 16;
@@ -642,7 +646,7 @@ cudaError_t run(const TopSelectArgs& a, int sms, int device, cudaStream_t st) {
   const int K = static_cast<int>(a.K);
   const int cap = capacity(K, Elem<T>::kVec);
   constexpr int kChunkBytes = Ring<NT>::kChunk * 16, kStatic = sizeof(Scratch<NT>) + sizeof(RingBars);
-  const int lists = cap * 8 + kBins * 4;
+  const int lists = cap * 8 + hist_ints(NT) * 4;
   auto kernel = top_select_kernel<T, NT>;
   static std::once_flag once[64];
   static cudaError_t set[64];
