@@ -145,32 +145,35 @@ __host__ __device__ constexpr int64_t bit_words(int64_t vecs, int vec) {
 // which L2 still holds, and write the gradient.  (Sweeping the next row's share
 // meanwhile needs twice the rows in L2, so twice the CTAs per row, each with
 // the whole list to look up: 1277 us instead of 1035 at 8192 x 151936 bf16.)
-constexpr int kFwdConsumers = 512;
-constexpr int kFwdChunk = Ring<kFwdConsumers>::kChunk;
-constexpr int kFwdThreads = kFwdConsumers + 64;  // consumers, copying warp, finishing warp
+//
+// NT consumers per CTA, with a copying and a finishing warp: 512, two CTAs per
+// SM, or 256, four per SM, for short rows, of which more are then on their way
+// (forward, 8192 rows of bf16: 4096 words 108 -> 70 us, 32000 152 -> 134).
+constexpr int64_t kShortRow = 128 * 1024;  // bytes
 
+template <int NT>
 struct Turn {  // a row on its way from the consumers to the finishing warp
-  float2 warp_state[kMaxShares][kFwdConsumers / 32];
+  float2 warp_state[kMaxShares][NT / 32];
   float tg_logit;
   int bad;
   Sums sums;
 };
 
-template <typename T, bool kGrad>
-__global__ void __launch_bounds__(kFwdThreads, 2)
+template <typename T, bool kGrad, int NT>
+__global__ void __launch_bounds__(NT + 64, 1024 / NT)
     top_forward_kernel(TopArgs a, int words, int stages, int shares) {
-  constexpr int VE = Elem<T>::kVec, NT = kFwdConsumers;
+  constexpr int VE = Elem<T>::kVec;
   extern __shared__ uint4 top_smem[];
   __shared__ __align__(8) RingBars bars;
   __shared__ __align__(16) Exchange exchange;
   // the consumers are done with a row of turn t; its sums are there and its
   // buffers are free
   __shared__ __align__(8) uint64_t ready_bar[2], done_bar[2];
-  __shared__ Turn turns[2];
+  __shared__ Turn<NT> turns[2];
   const int K = static_cast<int>(a.K), V = static_cast<int>(a.V), tid = threadIdx.x;
   const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
   const int own = kGrad ? 1 : shares / C, first = rank * own;  // this CTA's shares
-  uint32_t* bits = reinterpret_cast<uint32_t*>(top_smem + stages * kFwdChunk);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(top_smem + stages * Ring<NT>::kChunk);
   const uint8_t* bytes = reinterpret_cast<const uint8_t*>(bits);
   // the lists of two rows: student's and teacher's logits, words
   auto list = [&](uint32_t turn) {
@@ -186,7 +189,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     }
     ring.init();
   }
-  for (int i = tid; i < words; i += kFwdThreads) bits[i] = 0;
+  for (int i = tid; i < words; i += NT + 64) bits[i] = 0;
   __syncthreads();
   cluster_barrier();  // every CTA's barriers exist
   const int64_t n_clusters = gridDim.x / C;
@@ -212,7 +215,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         continue;
       }
       const float t_rest = a.rest ? a.rest[row] : -INFINITY;
-      Turn& t = turns[turn & 1u];
+      Turn<NT>& t = turns[turn & 1u];
       mbar_wait(&ready_bar[turn & 1u], (turn >> 1) & 1u, &bars.abort);
       uint4 got = make_uint4(0xff800000u, 0u, 0u, 0u);  // lane i: share i (of this CTA, of all)
       for (int i = 0; i < own; ++i) {
@@ -380,7 +383,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         const Row<T> r(srow, V);
         const int v0 = share_at(r, first), v_end = share_at(r, first + own);
         // ---- the list, and the bits of its words in this CTA's part
-        Turn& t = turns[turn & 1u];
+        Turn<NT>& t = turns[turn & 1u];
         const Lists l = list(turn);
         // the row of two turns ago has left these buffers (kGrad has waited for it)
         if (!kGrad && turn >= 2)
@@ -539,12 +542,13 @@ __global__ void __launch_bounds__(kBwdThreads, 6) top_backward_kernel(TopArgs a,
 // flight (two CTAs per SM) fit in 0.8 of L2, those of more than 340 KB shared by
 // two CTAs.  A row of 1 MB would take four, and what each does beside its bytes
 // then costs more than a third reading of the row (1021 x 256000 fp32: 586 us
-// against 487 by two launches; 151936 fp32, two CTAs: 492 against 558); a row
+// against 487 by two launches; 151936 fp32, two CTAs: 482 against 566); a row
 // of 8 KB costs more in the second sweep's start than a launch (8192 x 4096
-// bf16: 211 us against 149), unless there are so few that the launch counts.
+// bf16: 125 us against 111; 8000: 139 against 142; 16000: 179 against 200),
+// unless there are so few that the launch counts.
 constexpr double kKeep = 0.8;
 constexpr int kSingleShares = 2;
-constexpr int64_t kSingleRow = 40 * 1024;  // smallest row in bytes, for many rows
+constexpr int64_t kSingleRow = 16 * 1024;  // smallest row in bytes, for many rows
 bool fits(int64_t V, int dtype, int shares, int sms, int l2) {
   return 2.0 * sms / shares * (double(V) * (dtype == FCT_BF16 ? 2 : 4)) <= kKeep * l2;
 }
@@ -565,29 +569,30 @@ int shares_of(int64_t V, int dtype, int sms, int l2) {
   return n;
 }
 
-template <typename T, bool kGrad>
+template <typename T, bool kGrad, int NT>
 cudaError_t run_forward(const TopArgs& a, int sms, int device, int l2, cudaStream_t st) {
   constexpr int VE = Elem<T>::kVec;
+  constexpr int kChunkBytes = Ring<NT>::kChunk * 16;
+  constexpr int kStatic = 2 * int(sizeof(Turn<NT>)) + 1024;  // and what the system takes
   const int shares = shares_of(a.V, a.dtype, sms, l2);
   int C = 1;
   while (C < shares && (kGrad || a.V > int64_t(C) * 262144)) C *= 2;
   const int64_t words = (bit_words(shares / C * share(a.V / VE, shares), VE) + 3) / 4 * 4;
-  const size_t lists = size_t(words) * 4 + list_bytes(a.K);
-  // two CTAs per SM share its shared memory; a long vocabulary's bits may leave room for one
-  const int64_t room = kStreamSmem - 2 * int64_t(sizeof(Turn) * 2);
-  int resident = 2;
-  int stages = static_cast<int>((room / 2 - int64_t(lists)) / (kFwdChunk * 16));
-  if (stages < 2) {
-    resident = 1;
-    stages = static_cast<int>((room - int64_t(lists)) / (kFwdChunk * 16));
+  const int lists = static_cast<int>(words * 4 + int64_t(list_bytes(a.K)));
+  // as many CTAs per SM as its registers allow; long lists, or a long
+  // vocabulary's bits, may leave room for fewer
+  int resident = 1024 / NT, stages = 0;
+  for (;; --resident) {
+    stages = (kStreamSmem / resident - kStatic - lists) / kChunkBytes;
+    if (stages >= 2 || resident == 1) break;
   }
   if (stages > kMaxStages) stages = kMaxStages;
-  auto kernel = top_forward_kernel<T, kGrad>;
+  auto kernel = top_forward_kernel<T, kGrad, NT>;
   static std::once_flag once[64];
   static cudaError_t set[64];
   std::call_once(once[device], [&] {
     set[device] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kStreamSmem - static_cast<int>(sizeof(Turn)) * 4);
+                                       kStreamSmem - kStatic);
   });
   if (set[device] != cudaSuccess) return set[device];
   cudaLaunchConfig_t cfg = {};
@@ -596,8 +601,8 @@ cudaError_t run_forward(const TopArgs& a, int sms, int device, int l2, cudaStrea
   attr[0].val.clusterDim.x = static_cast<unsigned>(C);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(kFwdThreads);
-  cfg.dynamicSmemBytes = size_t(stages) * kFwdChunk * 16 + lists;
+  cfg.blockDim = dim3(NT + 64);
+  cfg.dynamicSmemBytes = size_t(stages) * kChunkBytes + size_t(lists);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = st;
@@ -606,6 +611,15 @@ cudaError_t run_forward(const TopArgs& a, int sms, int device, int l2, cudaStrea
   if (clusters > a.BT) clusters = a.BT;
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * C));
   return cudaLaunchKernelEx(&cfg, kernel, a, static_cast<int>(words), stages, shares);
+}
+
+template <typename T>
+cudaError_t run_sized(const TopArgs& a, int sms, int device, int l2, cudaStream_t st) {
+  if (a.V * int64_t(sizeof(T)) <= kShortRow)
+    return a.grad ? run_forward<T, true, 256>(a, sms, device, l2, st)
+                  : run_forward<T, false, 256>(a, sms, device, l2, st);
+  return a.grad ? run_forward<T, true, 512>(a, sms, device, l2, st)
+                : run_forward<T, false, 512>(a, sms, device, l2, st);
 }
 
 template <typename T>
@@ -642,11 +656,8 @@ cudaError_t launch_top_forward(const TopArgs& a, int sms, int device, int l2, cu
     const cudaError_t e = launch_top_forward(f, sms, device, l2, st);
     return e != cudaSuccess ? e : launch_top_backward(a, st);
   }
-  if (a.dtype == FCT_BF16)
-    return a.grad ? run_forward<bf16_t, true>(a, sms, device, l2, st)
-                  : run_forward<bf16_t, false>(a, sms, device, l2, st);
-  return a.grad ? run_forward<float, true>(a, sms, device, l2, st)
-                : run_forward<float, false>(a, sms, device, l2, st);
+  return a.dtype == FCT_BF16 ? run_sized<bf16_t>(a, sms, device, l2, st)
+                             : run_sized<float>(a, sms, device, l2, st);
 }
 
 cudaError_t launch_top_backward(const TopArgs& a, cudaStream_t st) {
