@@ -14,10 +14,18 @@
 // Precision: the tensor cores' fp32 accumulators drop what lies below them
 // (4096 products: 1.5e-5 off, always towards 0, at logits near 3.5; products
 // and sums in fp32 registers: 2e-6).  A loss of nearly equal masses shows
-// that.  So a tile's sum runs in the accumulator over 1024 products at a time,
+// that.  So a tile's sum runs in the accumulator over 768 products at a time,
 // and these partial sums are added in fp32 registers: eight epilogue warps
-// hold 128 columns of a row per thread.  (1024 against all of 4096 costs
-// nothing that shows, 512 costs 9% at d = 2048 and 256 20%.)
+// hold 128 columns of a row per thread.  Against 64 bits the loss is then 0.5
+// to 0.9 as far off as with products and sums in fp32 (with 1024 products 1.0
+// to 1.4, with 512 0.4).  768 and 1024 cost nothing that shows against all of
+// 4096, 512 costs 3 to 9% at d = 2048, 256 20%.
+//
+// Measured: forward 8192 x 151936 x 4096 6.5-6.8 ms in a row of calls (1.5-1.57
+// PFLOP/s, under the power cap), 5.55 ms after a pause (1.84); backward 4096 x
+// 151936 x 2048 4.7 ms (1.63); the tensor cores are busy 85% of the cycles
+// where the plain GEMM's are 92%.  16 rows, 151936 x 4096: 212-220 us of 186 that
+// reading the weights takes.
 //
 // Roles per CTA of a pair, as in the plain GEMM: warp 0 issues the copies,
 // warp 1 (of CTA 0) the products, warps 4 to 11 are the epilogue, two per 32
@@ -43,7 +51,7 @@ constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kLeanRegs = 40, kEpiRegs = 232;
 static_assert(128 * kLeanRegs + 256 * kEpiRegs <= kThreads * 168, "the launch's registers");
 constexpr int kCols = 128;   // columns of a tile row that an epilogue thread holds
-constexpr int kChunk = 16;   // K blocks of 64 summed in the accumulator
+constexpr int kChunk = 12;   // K blocks of 64 summed in the accumulator
 constexpr size_t kSmem = size_t(kGStages) * kGStageBytes + kEpiWarps * kOutBufBytes + 1024;
 constexpr int kSortThreads = 128;
 

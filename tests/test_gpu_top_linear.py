@@ -2,8 +2,8 @@
 against the definition in 64 bits.
 
 Bounds: a logit is a sum of d products; the tensor cores add 16 products at a time to a partial sum
-of at most 1024, dropping bits below it (64 steps of at most 2^-23 of the sum of magnitudes: a step
-of the accumulator's last bit), and the partial sums are added in float32 (d / 1024 steps of 2^-24).  A logit's gradient is rounded to
+of at most 768, dropping bits below it (48 steps of at most 2^-23 of the sum of magnitudes: a step of
+the accumulator's last bit), and the partial sums are added in float32 (d / 768 steps of 2^-24).  A logit's gradient is rounded to
 bfloat16 (2^-8, half a step), and enters sums over the vocabulary (d hidden) or the rows (d weight)
 that the tensor cores accumulate the same way, at most n / 16 steps; the results are rounded once.
 """
@@ -24,7 +24,7 @@ def make(rows, V, d, K, seed, rest=True):
     h = torch.randn(rows, d, generator=g).bfloat16()
     w = (torch.randn(V, d, generator=g) * (2.5 / math.sqrt(d))).bfloat16()
     s = h.double() @ w.double().t()
-    err = (64 * 2.0 ** -23 + (d / 1024 + 1) * 2.0 ** -24) * (h.double().abs() @ w.double().abs().t())
+    err = (48 * 2.0 ** -23 + (d / 768 + 1) * 2.0 ** -24) * (h.double().abs() @ w.double().abs().t())
     if K:
         _, target, values, index, rests, gce, gtvd = tu.make(rows, V, K, torch.float32, seed, rest)
         t = 0.8 * s + torch.randn(rows, V, generator=g)
