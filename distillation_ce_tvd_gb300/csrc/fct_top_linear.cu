@@ -454,6 +454,12 @@ struct ListArgs {
   const float* grad_tvd;
   int64_t grad_stride;
   int32_t* dev_status;
+  // backward with d weight: the hidden states, copied with zeros in ignored rows
+  // (a padded batch's rows may hold anything there, and 0 times NaN is NaN)
+  const uint16_t* h = nullptr;
+  int64_t ld_h = 0, d = 0;
+  uint16_t* live = nullptr;
+  int64_t ld_live = 0;
 };
 
 // One CTA per row: the list sorted by word, so that a tile finds its part, and
@@ -501,6 +507,22 @@ __global__ void __launch_bounds__(kSortThreads) list_kernel(ListArgs a) {
       a.teacher[row * a.K + k] =
           used ? a.values[row * a.ld_v + static_cast<int64_t>(key[k] & 0xffffffffu)] : -INFINITY;
       if (used && k > 0 && static_cast<int>(key[k - 1] >> 32) == v) bad = true;
+    }
+  }
+  if (kGrad && a.live != nullptr) {
+    const uint16_t* src = a.h + row * a.ld_h;
+    uint16_t* dst = a.live + row * a.ld_live;
+    for (int64_t c = tid * 8; c < a.d; c += kSortThreads * 8) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (!ignored && c + 8 <= a.d) {
+        v = *reinterpret_cast<const uint4*>(src + c);
+      } else if (!ignored) {  // the last columns; the row's padding is no one's
+        uint16_t e[8] = {};
+        for (int j = 0; c + j < a.d; ++j) e[j] = src[c + j];
+        v = make_uint4(e[0] | uint32_t(e[1]) << 16, e[2] | uint32_t(e[3]) << 16,
+                       e[4] | uint32_t(e[5]) << 16, e[6] | uint32_t(e[7]) << 16);
+      }
+      *reinterpret_cast<uint4*>(dst + c) = v;
     }
   }
   const int wrong = __syncthreads_or(bad);
@@ -592,30 +614,6 @@ __global__ void __launch_bounds__(kSortThreads) merge_kernel(MergeArgs a) {
     a.rest_lse[row] = o.rest;
     a.t_lse[row] = o.t_lse;
     a.sigma[row] = o.sigma;
-  }
-}
-
-// The hidden states with zeros in ignored rows, for d weight: a padded batch's
-// rows may hold anything there, and 0 times NaN is NaN.
-__global__ void __launch_bounds__(256) live_rows_kernel(const uint16_t* h, int64_t ld_h,
-                                                        const int64_t* target, int64_t ignore_index,
-                                                        uint16_t* out, int64_t ld_out, int64_t rows,
-                                                        int64_t d) {
-  const int64_t per = (d + 7) / 8, total = rows * per;
-  for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
-    const int64_t r = i / per, c = (i - r * per) * 8;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (target[r] != ignore_index) {
-      if (c + 8 <= d) {
-        v = *reinterpret_cast<const uint4*>(h + r * ld_h + c);
-      } else {  // the last columns; the row's padding is no one's
-        uint16_t e[8] = {};
-        for (int j = 0; c + j < d; ++j) e[j] = h[r * ld_h + c + j];
-        v = make_uint4(e[0] | uint32_t(e[1]) << 16, e[2] | uint32_t(e[3]) << 16,
-                       e[4] | uint32_t(e[5]) << 16, e[6] | uint32_t(e[7]) << 16);
-      }
-    }
-    *reinterpret_cast<uint4*>(out + r * ld_out + c) = v;
   }
 }
 
@@ -800,16 +798,16 @@ cudaError_t launch_top_linear_backward(const TopLinearArgs& a, int sms, int devi
   ListArgs l{a.V, a.K, a.values, a.ld_v, a.index, a.ld_i, a.rest, a.target, a.ignore_index,
              w.words, w.teacher, nullptr, w.rows, a.lse, a.rest_lse, a.t_lse, a.sigma, a.grad_ce,
              a.grad_tvd, a.grad_stride, a.dev_status};
+  if (a.grad_w != nullptr) {
+    l.h = static_cast<const uint16_t*>(a.h);
+    l.ld_h = a.ld_h;
+    l.d = a.d;
+    l.live = w.live;
+    l.ld_live = w.ld_live;
+  }
   list_kernel<true><<<static_cast<unsigned>(a.BT), kSortThreads, 0, st>>>(l);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (a.grad_w != nullptr) {
-    const int64_t blocks = (a.BT * (w.ld_live / 8) + 255) / 256, most = int64_t(sms) * 8;
-    live_rows_kernel<<<static_cast<unsigned>(blocks < most ? blocks : most), 256, 0, st>>>(
-        static_cast<const uint16_t*>(a.h), a.ld_h, a.target, a.ignore_index, w.live, w.ld_live,
-        a.BT, a.d);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
   const size_t ew = a.grad_w_kind == FCT_GEMM_BF16 ? 2 : 4;
   for (int64_t v0 = 0; v0 < a.V; v0 += w.piece) {
     const int64_t n = a.V - v0 < w.piece ? a.V - v0 : w.piece;
