@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc_fence_after();
               const uint32_t sa = smem0 + stage * kGStageBytes;
               const uint64_t adesc = smem_desc<false>(sa), bdesc = smem_desc<false>(sa + kHalfBytes);
-  #pragma unroll
+#pragma unroll
               for (int kk = 0; kk < kBK / 16; ++kk)
                 umma_bf16<kId>(d, adesc + kk * desc_k_step<false>(), bdesc + kk * desc_k_step<false>(),
                                (kb > kb0 || kk > 0) ? 1u : 0u);

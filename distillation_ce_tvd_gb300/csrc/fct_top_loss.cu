@@ -22,7 +22,6 @@
 // backward's segments of 2048 vectors, with the target looked for in every
 // vector, took 1070 us: what a CTA does before its first load has to be small
 // beside its 64 KB.
-#include <climits>
 #include <mutex>
 
 #include "fct_internal.h"
@@ -112,10 +111,21 @@ __device__ __forceinline__ void loose_grad(const Row<T>& r, T* grow, const Outsi
   }
 }
 
-// A gradient row, or its part [v0, v1), set to one value.
+// A gradient row's part [v0, v1) set to 0 (rows that are ignored) or to NaN.
 template <int NT, typename T>
-__device__ __forceinline__ void fill_grad(T* grow, int64_t v0, int64_t v1, float value) {
-  for (int64_t v = v0 + threadIdx.x; v < v1; v += NT) Elem<T>::store1(grow + v, value);
+__device__ __forceinline__ void fill_grad(T* grow, int64_t v0, int64_t v1, bool zero) {
+  constexpr int VE = Elem<T>::kVec;
+  const int tid = threadIdx.x;
+  T* p = grow + v0;
+  const int64_t n = v1 > v0 ? v1 - v0 : 0;
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) % 16 / sizeof(T));
+  const int64_t head = off ? min(int64_t(VE - off), n) : 0, nvec = (n - head) / VE;
+  const float value = zero ? 0.f : __uint_as_float(0x7fc00000u);
+  const uint32_t word = zero ? 0u : Elem<T>::kNanBits | (VE == 8 ? Elem<T>::kNanBits << 16 : 0u);
+  uint4* vecs = reinterpret_cast<uint4*>(p + head);
+  for (int64_t i = tid; i < nvec; i += NT) vecs[i] = make_uint4(word, word, word, word);
+  const int64_t loose = n - nvec * VE;  // fewer than two vectors
+  if (tid < loose) Elem<T>::store1(p + (tid < head ? tid : nvec * VE + tid), value);
 }
 
 // ---------------------------------------------------------------- forward
@@ -317,8 +327,7 @@ __global__ void __launch_bounds__(NT + 64, 1024 / NT)
       mbar_wait(&done_bar[its_turn & 1u], (its_turn >> 1) & 1u, &bars.abort);
       if (f.tg < 0 || f.tg >= V) {
         const int64_t per_cta = (a.V + C - 1) / C;
-        fill_grad<NT>(grow, rank * per_cta, min(a.V, (rank + 1) * per_cta),
-                      __uint_as_float(0x7fc00000u));
+        fill_grad<NT>(grow, rank * per_cta, min(a.V, (rank + 1) * per_cta), false);
       } else {
         const Row<T> r(static_cast<const T*>(a.student) + f.row * a.ld_s, V);
         const int v0 = share_at(r, first), v1 = share_at(r, first + 1);
@@ -363,7 +372,7 @@ __global__ void __launch_bounds__(NT + 64, 1024 / NT)
         if constexpr (kGrad) {
           const int64_t per_cta = (a.V + C - 1) / C;
           fill_grad<NT>(static_cast<T*>(a.grad) + row * a.ld_g, rank * per_cta,
-                        min(a.V, (rank + 1) * per_cta), 0.f);
+                        min(a.V, (rank + 1) * per_cta), true);
         }
         if (next_live) {
           e = fetch(next_row, tid, next_word);
@@ -494,7 +503,7 @@ __global__ void __launch_bounds__(kBwdThreads, 6) top_backward_kernel(TopArgs a,
     const bool ignored = tg == a.ignore_index;
     if (!ignored && first && tid == 0 && a.dev_status)
       atomicOr(a.dev_status, FCT_DEV_TARGET_OUT_OF_RANGE);
-    fill_grad<NT>(grow, e0, e1, ignored ? 0.f : __uint_as_float(0x7fc00000u));
+    fill_grad<NT>(grow, e0, e1, ignored);
     return;
   }
   const Coefs c = make_coefs(a.grad_ce[row * a.grad_stride], a.grad_tvd[row * a.grad_stride],

@@ -10,8 +10,8 @@
 // does not go through the slow path for one lane: their elements above the
 // threshold become candidates in shared memory, the others are folded.
 //
-// 8192 x 151936 bf16, K = 64: 600 us, 4.2 TB/s, 0.62 of the copy rate; 1003 x
-// 256000 fp32, K = 256: 305 us, 3.4 TB/s.  What bounds it is instructions (100
+// 8192 x 151936 bf16, K = 64: 595 us, 4.2 TB/s, 0.63 of the copy rate; 1003 x
+// 256000 fp32, K = 256: 296-303 us, 3.4 TB/s.  What bounds it is instructions (100
 // per 32 vectors, 65% of the issue slots) and what a row costs beside its
 // bytes (threshold, last candidates, order: some 8 us of a CTA, hidden by the
 // other three of an SM).  Before: candidates taken vector by vector as they
@@ -30,11 +30,7 @@
 // taken again in rounds of rising index with a selection in between, whose
 // threshold only ever meets later rounds: there, an equal logit has a larger
 // index than K that rank before it.
-#include <climits>
-#include <cstring>
 #include <mutex>
-
-#include <cuda_bf16.h>
 
 #include "fct_internal.h"
 #include "fct_top.cuh"
@@ -656,12 +652,13 @@ cudaError_t run(const TopSelectArgs& a, int sms, int device, cudaStream_t st) {
   });
   if (set[device] != cudaSuccess) return set[device];
   // as many CTAs per SM as its registers allow, fewer where the lists are long
-  int resident = 1024 / NT;
-  int stages = 0;
-  for (; resident > 1; --resident) {
+  // (two of 512 threads always find room for two chunks each)
+  int resident = 1024 / NT, stages = 0;
+  for (; resident >= 2; --resident) {
     stages = (kStreamSmem / resident - kStatic - lists) / kChunkBytes;
     if (stages >= 2) break;
   }
+  if (stages < 2) return cudaErrorInvalidConfiguration;
   if (stages > 4) stages = 4;
   int64_t grid = int64_t(sms) * resident;
   if (grid > a.BT) grid = a.BT;

@@ -654,6 +654,8 @@ int fused_ce_tvd_vp_backward(const void* student, int64_t ld_student,
  * outside U taken together: at most that of the whole rows, and equal to it
  * where U holds all words, or where the teacher gives none outside U any
  * probability (rest_lse NULL).
+ * Logits of more than 2.3e38 in magnitude count as not finite (their product
+ * with log2 e is not).
  */
 
 /*
@@ -724,14 +726,15 @@ typedef struct {
  *                  words).  The backward reads the last four.  Rows with
  *                  target == ignore_index: zeros, and the list is not read.
  *   V            : at most 2^23, else FCT_ERR_UNSUPPORTED.
- * The forward reads the row once, the backward reads and writes it once.  Both
- * together give the bits of the two calls; rows of 16 to 680 KB (and less, where
- * there are few rows) go in one launch that reads a row from memory once and the second
- * time from L2, others in two.  The forward takes sign(p - q)
- * from fp32 sums relative to the maxima, the backward from exp(s -
- * student_lse) and exp(t - teacher_lse); where both are within their roundings
- * of each other and p > 3/4, it takes the sign that sigma has (a student and a
- * teacher sure of one word: the fp32 log-sum-exps do not hold 1 - p).
+ * The forward reads the row once, the backward reads and writes it once.
+ * Both together give the bits of the two calls; rows of 16 to 680 KB (and
+ * less, where there are few rows) go in one launch that reads a row from
+ * memory once and the second time from L2, others in two.  The forward takes
+ * sign(p - q) from fp32 sums relative to the maxima, the backward from exp(s
+ * - student_lse) and exp(t - teacher_lse); where both are within their
+ * roundings of each other and p > 3/4, it takes the sign that sigma has (a
+ * student and a teacher sure of one word: the fp32 log-sum-exps do not hold 1
+ * - p).
  */
 int fused_ce_tvd_top_forward(const void* student, int64_t ld_student,
                              fct_dtype dtype, const int64_t* target,
