@@ -125,3 +125,57 @@ def test_a_training_step_as_a_graph():
     step()
     for a, b in zip((*captured["stats"], *captured["grads"]), (*out["stats"], *out["grads"])):
         assert torch.equal(a, b)
+
+
+def test_a_captured_mean_loss_and_its_backward():
+    """Loss and gradient by torch.autograd, captured once and replayed on new logits; the scale of
+    the loss is read at the replay."""
+    _, _, s, target, lists = setup()
+    scale = torch.ones((), device="cuda")
+
+    def step(x):
+        loss = autograd.fused_ce_tvd_top_mean_loss(x, target, *lists, alpha=0.5, beta=2.0)
+        return loss.detach(), torch.autograd.grad(loss * scale, x)[0]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(s.clone().requires_grad_())
+    torch.cuda.current_stream().wait_stream(side)
+    x = s.clone().requires_grad_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss, grad = step(x)
+    with torch.no_grad():
+        x.copy_(s.roll(1, 1))
+    scale.fill_(-3.0)
+    graph.replay()
+    want_loss, want_grad = step(x.detach().clone().requires_grad_())
+    assert torch.equal(loss, want_loss) and torch.equal(grad, want_grad)
+
+
+def test_calls_on_two_streams_at_once():
+    """Lists, loss and both linear calls on two streams, with workspaces of their own: the same bits
+    as one after the other."""
+    h, w, s, target, lists = setup(rows=300, V=5000, d=128, K=40)
+
+    def work(x, hidden):
+        top = binding.fct_top_logits(x, 40)
+        both = binding.fused_ce_tvd_top_forward_backward(x, target, *lists, 1.0, 0.5)
+        stats = binding.fused_linear_ce_tvd_top_forward(hidden, w, target, *lists)
+        grads = binding.fused_linear_ce_tvd_top_backward(hidden, w, target, *lists, *stats[2:], 1.0,
+                                                         0.5, piece_cols=2048)
+        return (*top, *both, *stats, *grads)
+
+    inputs = [(s, h), (s.flip(0).contiguous(), h.flip(0).contiguous())]
+    want = [work(*x) for x in inputs]
+    streams = [torch.cuda.Stream() for _ in inputs]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = []
+        for stream, x in zip(streams, inputs):
+            with torch.cuda.stream(stream):
+                got.append(work(*x))
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))

@@ -234,6 +234,31 @@ def test_upstream_broadcast_split_and_repeated():
         assert torch.equal(one[i], torch.cat([c[i] for c in cut]))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V", [1, 5, 13, 2001, 131_080])
+def test_rows_without_a_gradient_at_every_offset(dtype, V):
+    """Rows that are ignored get 0, rows of a target outside the vocabulary NaN, and nothing else is
+    written, wherever a row starts and however it ends."""
+    rows = 8
+    s, target, values, index, rest, gce, gtvd = cuda(*tu.make(rows, V, 3, dtype, 5))
+    target[0::3], target[1::3] = -100, V
+    for ld in (V + 1, V + 2):                      # 16-byte phases differ from row to row
+        whole = torch.full((rows * ld + 8,), 5.0, dtype=dtype, device="cuda")
+        grad = whole.as_strided((rows, V), (ld, 1), 1)
+        used = torch.zeros_like(whole, dtype=torch.bool)
+        used.as_strided((rows, V), (ld, 1), 1)[:] = True
+        stats = binding.fused_ce_tvd_top_forward(s, target, values, index, rest)
+        for call in (
+                lambda: binding.fused_ce_tvd_top_backward(s, target, values, index, rest, *stats[2:],
+                                                          gce, gtvd, grad_student=grad),
+                lambda: binding.fused_ce_tvd_top_forward_backward(s, target, values, index, rest, gce,
+                                                                  gtvd, grad_student=grad)):
+            whole.fill_(5.0)
+            call()
+            assert (grad[0::3] == 0).all() and grad[1::3].isnan().all()
+            assert not grad[2::3].isnan().any() and (whole[~used] == 5).all()
+
+
 def test_streams_graphs_and_no_rows():
     s, target, values, index, rest, gce, gtvd = cuda(*tu.make(64, 4000, 16, torch.bfloat16, 16))
     want = binding.fused_ce_tvd_top_forward_backward(s, target, values, index, rest, gce, gtvd)
