@@ -548,22 +548,24 @@ __global__ void __launch_bounds__(kBwdThreads, 6) top_backward_kernel(TopArgs a,
 // ---------------------------------------------------------------- launch
 
 // The single launch's rows: one sweep from memory, one from L2, so the rows in
-// flight (two CTAs per SM) fit in 0.8 of L2, those of more than 340 KB shared by
-// two CTAs.  A row of 1 MB would take four, and what each does beside its bytes
-// then costs more than a third reading of the row (1021 x 256000 fp32: 586 us
-// against 487 by two launches; 151936 fp32, two CTAs: 482 against 566); a row
-// of 8 KB costs more in the second sweep's start than a launch (8192 x 4096
-// bf16: 125 us against 111; 8000: 139 against 142; 16000: 179 against 200),
-// unless there are so few that the launch counts.
+// flight fit in 0.8 of L2: with two CTAs per SM rows of up to 340 KB, or of up
+// to 680 KB shared by two CTAs; longer rows have 768 consumers, one CTA per SM,
+// and two CTAs per row: up to 1.3 MB (1021 x 256000 fp32, K = 256: 401 us; with
+// 512 consumers 441, and two such CTAs per SM 466, though they exceed L2; by
+// two launches 480-490).  Four CTAs per row cost more beside their bytes than a
+// third reading of the row (562 there).  A row of 8 KB costs more in the second
+// sweep's start than a launch (8192 x 4096 bf16: 125 us against 111; 8000: 139
+// against 142; 16000: 179 against 200), unless there are so few that the launch
+// counts.
 constexpr double kKeep = 0.8;
 constexpr int kSingleShares = 2;
 constexpr int64_t kSingleRow = 16 * 1024;  // smallest row in bytes, for many rows
-bool fits(int64_t V, int dtype, int shares, int sms, int l2) {
-  return 2.0 * sms / shares * (double(V) * (dtype == FCT_BF16 ? 2 : 4)) <= kKeep * l2;
+int64_t row_bytes(int64_t V, int dtype) { return V * (dtype == FCT_BF16 ? 2 : 4); }
+bool fits(int64_t V, int dtype, int shares, int per_sm, int sms, int l2) {
+  return double(per_sm) * sms / shares * double(row_bytes(V, dtype)) <= kKeep * l2;
 }
-bool single_launch(const TopArgs& a, int sms, int l2) {
-  const int64_t row = a.V * (a.dtype == FCT_BF16 ? 2 : 4);
-  return fits(a.V, a.dtype, kSingleShares, sms, l2) && (row >= kSingleRow || a.BT < 2 * sms);
+bool long_row(int64_t V, int dtype, int sms, int l2) {
+  return !fits(V, dtype, kSingleShares, 2, sms, l2);
 }
 
 // Shares of a row, by V and the element type alone: never the number of rows,
@@ -573,9 +575,14 @@ bool single_launch(const TopArgs& a, int sms, int l2) {
 int shares_of(int64_t V, int dtype, int sms, int l2) {
   int n = 1;
   while (n < kMaxShares && V > int64_t(n) * 262144) n *= 2;
-  if (n < kSingleShares && !fits(V, dtype, 1, sms, l2) && fits(V, dtype, kSingleShares, sms, l2))
-    n = kSingleShares;
+  if (n < kSingleShares && !fits(V, dtype, 1, 2, sms, l2)) n = kSingleShares;
   return n;
+}
+bool single_launch(const TopArgs& a, int sms, int l2) {
+  const int per_sm = long_row(a.V, a.dtype, sms, l2) ? 1 : 2;
+  return shares_of(a.V, a.dtype, sms, l2) <= kSingleShares &&
+         fits(a.V, a.dtype, kSingleShares, per_sm, sms, l2) &&
+         (row_bytes(a.V, a.dtype) >= kSingleRow || a.BT < 2 * sms);
 }
 
 template <typename T, bool kGrad, int NT>
@@ -624,9 +631,12 @@ cudaError_t run_forward(const TopArgs& a, int sms, int device, int l2, cudaStrea
 
 template <typename T>
 cudaError_t run_sized(const TopArgs& a, int sms, int device, int l2, cudaStream_t st) {
-  if (a.V * int64_t(sizeof(T)) <= kShortRow)
+  if (row_bytes(a.V, a.dtype) <= kShortRow)
     return a.grad ? run_forward<T, true, 256>(a, sms, device, l2, st)
                   : run_forward<T, false, 256>(a, sms, device, l2, st);
+  if (long_row(a.V, a.dtype, sms, l2))
+    return a.grad ? run_forward<T, true, 768>(a, sms, device, l2, st)
+                  : run_forward<T, false, 768>(a, sms, device, l2, st);
   return a.grad ? run_forward<T, true, 512>(a, sms, device, l2, st)
                 : run_forward<T, false, 512>(a, sms, device, l2, st);
 }
