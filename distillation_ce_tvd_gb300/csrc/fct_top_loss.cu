@@ -16,12 +16,13 @@
 //
 // Measured (of the copy rate, 6692 GB/s): forward 410-420 us at 8192 x 151936
 // bf16, K = 64 (0.89-0.91), 165 us at 1021 x 256000 fp32, K = 256 (0.95);
-// backward 736 us at the former (1.01); both in one launch 977 us (0.76),
-// against 1178 by two.  The forward on loads of its own into registers, three
+// backward 736 us at the former (1.01); both in one launch 972 us (0.77),
+// against 1178 by two; at the latter 400 us (0.78) against 480.  The forward on loads of its own into registers, three
 // CTAs per SM, took 455 us, with one thing after the other per row 446.  The
 // backward's segments of 2048 vectors, with the target looked for in every
 // vector, took 1070 us: what a CTA does before its first load has to be small
 // beside its 64 KB.
+#include <atomic>
 #include <mutex>
 
 #include "fct_internal.h"
@@ -158,7 +159,9 @@ __host__ __device__ constexpr int64_t bit_words(int64_t vecs, int vec) {
 //
 // NT consumers per CTA, with a copying and a finishing warp: 512, two CTAs per
 // SM, or 256, four per SM, for short rows, of which more are then on their way
-// (forward, 8192 rows of bf16: 4096 words 108 -> 70 us, 32000 152 -> 134).
+// (forward, 8192 rows of bf16: 4096 words 108 -> 70 us, 32000 152 -> 134), or
+// 768, one per SM, for long ones (single_launch says why; forward of 64 x 256000
+// fp32 34 -> 23 us).  Of rows of 304 KB 768 would take 506 us instead of 420.
 constexpr int64_t kShortRow = 128 * 1024;  // bytes
 
 template <int NT>
@@ -550,23 +553,22 @@ __global__ void __launch_bounds__(kBwdThreads, 6) top_backward_kernel(TopArgs a,
 // The single launch's rows: one sweep from memory, one from L2, so the rows in
 // flight fit in 0.8 of L2: with two CTAs per SM rows of up to 340 KB, or of up
 // to 680 KB shared by two CTAs; longer rows have 768 consumers, one CTA per SM,
-// and two CTAs per row: up to 1.3 MB (1021 x 256000 fp32, K = 256: 401 us; with
-// 512 consumers 441, and two such CTAs per SM 466, though they exceed L2; by
-// two launches 480-490).  Four CTAs per row cost more beside their bytes than a
-// third reading of the row (562 there).  A row of 8 KB costs more in the second
-// sweep's start than a launch (8192 x 4096 bf16: 125 us against 111; 8000: 139
-// against 142; 16000: 179 against 200), unless there are so few that the launch
-// counts.
+// and two CTAs per row, up to 1.3 MB, or four, up to 2.7 MB (1021 x 256000
+// fp32, K = 256: 400 us; with 512 consumers 441, and two such CTAs per SM 466,
+// though they exceed L2; four CTAs per row 464; by two launches 480-490.  500 x
+// 400000 fp32: two launches 373 us, two CTAs do not fit, four 302.)  A row of
+// 8 KB costs more in the second sweep's start than a launch (8192 x 4096 bf16:
+// 125 us against 111; 8000: 139 against 142; 16000: 179 against 200), unless
+// there are so few that the launch counts.
 constexpr double kKeep = 0.8;
-constexpr int kSingleShares = 2;
+constexpr int kSingleShares = 4;           // at most; two for rows of 512 consumers
 constexpr int64_t kSingleRow = 16 * 1024;  // smallest row in bytes, for many rows
+constexpr int kLongThreads = 768;
 int64_t row_bytes(int64_t V, int dtype) { return V * (dtype == FCT_BF16 ? 2 : 4); }
 bool fits(int64_t V, int dtype, int shares, int per_sm, int sms, int l2) {
   return double(per_sm) * sms / shares * double(row_bytes(V, dtype)) <= kKeep * l2;
 }
-bool long_row(int64_t V, int dtype, int sms, int l2) {
-  return !fits(V, dtype, kSingleShares, 2, sms, l2);
-}
+bool long_row(int64_t V, int dtype, int sms, int l2) { return !fits(V, dtype, 2, 2, sms, l2); }
 
 // Shares of a row, by V and the element type alone: never the number of rows,
 // so that results do not depend on how rows are batched, and the same with and
@@ -575,13 +577,14 @@ bool long_row(int64_t V, int dtype, int sms, int l2) {
 int shares_of(int64_t V, int dtype, int sms, int l2) {
   int n = 1;
   while (n < kMaxShares && V > int64_t(n) * 262144) n *= 2;
-  if (n < kSingleShares && !fits(V, dtype, 1, 2, sms, l2)) n = kSingleShares;
+  const int per_sm = long_row(V, dtype, sms, l2) ? 1 : 2;
+  while (n < kSingleShares && !fits(V, dtype, n, per_sm, sms, l2)) n *= 2;
   return n;
 }
 bool single_launch(const TopArgs& a, int sms, int l2) {
+  const int n = shares_of(a.V, a.dtype, sms, l2);
   const int per_sm = long_row(a.V, a.dtype, sms, l2) ? 1 : 2;
-  return shares_of(a.V, a.dtype, sms, l2) <= kSingleShares &&
-         fits(a.V, a.dtype, kSingleShares, per_sm, sms, l2) &&
+  return n <= kSingleShares && fits(a.V, a.dtype, n, per_sm, sms, l2) &&
          (row_bytes(a.V, a.dtype) >= kSingleRow || a.BT < 2 * sms);
 }
 
@@ -604,13 +607,6 @@ cudaError_t run_forward(const TopArgs& a, int sms, int device, int l2, cudaStrea
   }
   if (stages > kMaxStages) stages = kMaxStages;
   auto kernel = top_forward_kernel<T, kGrad, NT>;
-  static std::once_flag once[64];
-  static cudaError_t set[64];
-  std::call_once(once[device], [&] {
-    set[device] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kStreamSmem - kStatic);
-  });
-  if (set[device] != cudaSuccess) return set[device];
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -621,10 +617,32 @@ cudaError_t run_forward(const TopArgs& a, int sms, int device, int l2, cudaStrea
   cfg.dynamicSmemBytes = size_t(stages) * kChunkBytes + size_t(lists);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.stream = st;
+  static std::once_flag once[64];
+  static cudaError_t set[64];
+  static std::atomic<int> most[64][kMaxShares + 1];
+  std::call_once(once[device], [&] {
+    set[device] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kStreamSmem - kStatic);
+  });
+  if (set[device] != cudaSuccess) return set[device];
   int64_t clusters = int64_t(sms) * resident / C;
+  if (C > 2) {
+    // (one CTA per SM, as V is large: 36 clusters of four and 15 of eight are
+    // there at once, not 38 and 19, and with those the rest waits for a whole
+    // second round; forward of 500 x 600000 bf16 229 us, so 131)
+    int n = most[device][C];
+    if (n == 0) {
+      cfg.gridDim = dim3(static_cast<unsigned>(C));
+      const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      if (n < 1) return cudaErrorInvalidConfiguration;
+      most[device][C] = n;
+    }
+    if (clusters > n) clusters = n;
+  }
   if (clusters < 1) clusters = 1;
   if (clusters > a.BT) clusters = a.BT;
+  cfg.stream = st;
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * C));
   return cudaLaunchKernelEx(&cfg, kernel, a, static_cast<int>(words), stages, shares);
 }
@@ -635,8 +653,8 @@ cudaError_t run_sized(const TopArgs& a, int sms, int device, int l2, cudaStream_
     return a.grad ? run_forward<T, true, 256>(a, sms, device, l2, st)
                   : run_forward<T, false, 256>(a, sms, device, l2, st);
   if (long_row(a.V, a.dtype, sms, l2))
-    return a.grad ? run_forward<T, true, 768>(a, sms, device, l2, st)
-                  : run_forward<T, false, 768>(a, sms, device, l2, st);
+    return a.grad ? run_forward<T, true, kLongThreads>(a, sms, device, l2, st)
+                  : run_forward<T, false, kLongThreads>(a, sms, device, l2, st);
   return a.grad ? run_forward<T, true, 512>(a, sms, device, l2, st)
                 : run_forward<T, false, 512>(a, sms, device, l2, st);
 }

@@ -56,6 +56,35 @@ def test_large_vocabularies(dtype):
     check(*tu.make(2, 300007, 33, dtype, 4, rest=False))       # rows shared by several CTAs
 
 
+@pytest.mark.parametrize("dtype,V", [(torch.float32, 170_007), (torch.float32, 262_144),
+                                     (torch.float32, 400_003), (torch.float32, 700_001),
+                                     (torch.bfloat16, 524_289), (torch.bfloat16, 1_048_583)])
+def test_rows_of_a_megabyte_and_more(dtype, V):
+    """Rows shared by two, four and eight CTAs, in one launch and in two."""
+    check(*tu.make(3, V, 70, dtype, V))
+
+
+@pytest.mark.parametrize("dtype,V", [(torch.float32, 180_001), (torch.float32, 400_003),
+                                     (torch.bfloat16, 530_003)])
+def test_many_long_rows(dtype, V):
+    """More rows than are in flight: the bits of calls on a few rows each, and of two launches."""
+    rows, K = 170, 40
+    g = torch.Generator(device="cuda").manual_seed(V)
+    s = torch.randn(rows, V, generator=g, device="cuda").to(dtype)
+    target = torch.randint(V, (rows,), generator=g, device="cuda")
+    target[::7] = -100
+    lists = binding.fct_top_logits(s.flip(0), K)
+    up = torch.rand(rows, generator=g, device="cuda") / rows
+    whole = binding.fused_ce_tvd_top_forward_backward(s, target, *lists, up, up)
+    for a in range(0, rows, 17):
+        part = [x[a:a + 17] for x in (s, target, *lists)]
+        stats = binding.fused_ce_tvd_top_forward(*part)
+        grad = binding.fused_ce_tvd_top_backward(*part, *stats[2:], up[a:a + 17], up[a:a + 17])
+        for x, y in zip(whole, (*stats, grad)):
+            assert torch.equal(x[a:a + 17], y)
+    assert not any(x.isnan().any() for x in whole)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_peaked_students(dtype):
     """Nearly all mass inside the list, and nearly all outside."""
