@@ -55,11 +55,14 @@ constexpr int kFewMaxima = NT / 4;
 
 // A selection may keep this many more than K: it need not split a bin.
 __host__ __device__ constexpr int slack(int K) { return K / 4 + 64; }
-// Room for candidates: twice what a selection keeps (so that a chunk that brings
-// K more finds room, and a sort its power of two), and a round of vectors.
+// Room for candidates: twice what a selection keeps (a sort needs its power of
+// two), and a round of vectors or 3/4 K.  A chunk that comes after a selection
+// then finds room for 2 K + 64: the first chunks bring up to 1.4 K (the threshold
+// is K of their vectors' maxima, of which there are 2 K at least) and 10 to 20%
+// more, as it is the least of four, and what waited in the queues.
 constexpr int kRound = 64;  // vectors of a round
 __host__ __device__ constexpr int capacity(int K, int vec) {
-  return 2 * (K + slack(K)) + kRound * vec;
+  return 2 * (K + slack(K)) + (kRound * vec > 3 * K / 4 ? kRound * vec : 3 * K / 4);
 }
 constexpr int kQueue = 32 + 32 * kPerThread;  // vectors that wait, per warp
 
@@ -464,11 +467,16 @@ __global__ void __launch_bounds__(NT + 32, 1024 / NT)
       // The candidates so far, with room made for `more` unless there are too
       // many already.  `rounds`: all that is still to come has a larger index
       // than all so far, so that what equals the K-th cannot rank.
-      auto room = [&](int more, bool rounds) {
+      // `chunk`: the next chunk may bring what this one did, and half of that (a row
+      // that runs out of room is taken again: 1003 x 256000 fp32 at K = 1024 took
+      // 3800 us with only a round's room made after each chunk).
+      int so_far = 0;
+      auto room = [&](int more, bool rounds, bool chunk) {
         row_sync<NT>();
         int n = sc.pushed;
         row_sync<NT>();
-        if (n <= cap && n + more > cap) {
+        if (chunk) more += max(0, n - so_far) * 3 / 2;
+        if (n <= cap && n + more > cap && n > K + slack(K)) {
           uint32_t least;
           n = select(sh, sc, n, K, dropped, least);
           thr = fmaxf(thr, rounds ? value_of(least) : before(least));
@@ -476,6 +484,7 @@ __global__ void __launch_bounds__(NT + 32, 1024 / NT)
           if (tid == 0) sc.pushed = n;
           row_sync<NT>();
         }
+        so_far = n;
         return n;
       };
 
@@ -530,7 +539,7 @@ __global__ void __launch_bounds__(NT + 32, 1024 / NT)
         if (doubled || K > kFewMaxima<NT>) {
           // (not where little is left that a better one would spare)
           if (doubled && chunks > 1 && r.nvec - c > (chunks / 2 + 1) * kChunk) raise_threshold();
-          if (!full) full = room(kRound * VE, false) > cap;
+          if (!full) full = room(kRound * VE, false, true) > cap;
         }
       }
       // what still waits, of all warps together, against the row's threshold
@@ -547,7 +556,7 @@ __global__ void __launch_bounds__(NT + 32, 1024 / NT)
         if (tid < total) take(*r.vec(flat[tid]), flat[tid]);
         __syncwarp();
       }
-      int n = room(VE, false);
+      int n = room(VE, false, false);
       full = full || n > cap;
       if (!full) {
         if (r.tail0 + tid < V) take_loose(r.tail0 + tid);
@@ -559,10 +568,10 @@ __global__ void __launch_bounds__(NT + 32, 1024 / NT)
         thr = -INFINITY;
         if (tid < r.head) take_loose(tid);
         for (int c = 0; c < r.nvec; c += kRound) {
-          room(kRound * VE, true);
+          room(kRound * VE, true, false);
           if (tid < kRound && c + tid < r.nvec) take(*r.vec(c + tid), c + tid);
         }
-        room(VE, true);
+        room(VE, true, false);
         if (r.tail0 + tid < V) take_loose(r.tail0 + tid);
       }
       const Lse2 w = merge_warp(folded(st));
