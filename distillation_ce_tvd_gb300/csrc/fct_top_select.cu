@@ -493,6 +493,10 @@ __global__ void __launch_bounds__(NT + 32, 1024 / NT)
       bool full = false;  // more candidates came than there is room for
       for (int c = 0; c < r.nvec; c += kChunk) {
         const uint4* p = ring.wait() + tid;
+        if (full) {  // (in all warps alike: the row is taken again)
+          ring.release();
+          continue;
+        }
         const bool whole = c + kChunk <= r.nvec;
         auto vec = [&](int u) {
           return c + u * NT + tid < r.nvec ? p[u * NT] : nothing<T>();
@@ -567,9 +571,35 @@ __global__ void __launch_bounds__(NT + 32, 1024 / NT)
         dropped = make_float2(-INFINITY, 0.f);
         thr = -INFINITY;
         if (tid < r.head) take_loose(tid);
-        for (int c = 0; c < r.nvec; c += kRound) {
-          room(kRound * VE, true, false);
-          if (tid < kRound && c + tid < r.nvec) take(*r.vec(c + tid), c + tid);
+        for (int c = 0; c < r.nvec; c += kChunk) {
+          // a chunk with nothing above the threshold (most, where a row's highest
+          // logits are many equal ones) is folded at once
+          uint4 raw[kPerThread];
+          bool above = false;
+#pragma unroll
+          for (int u = 0; u < kPerThread; ++u) {
+            const int i = c + u * NT + tid;
+            raw[u] = i < r.nvec ? *r.vec(i) : nothing<T>();
+          }
+#pragma unroll
+          for (int u = 0; u < kPerThread; ++u) {
+            float x[VE];
+            Elem<T>::unpack(raw[u], x);
+            above = above || vec_max(x) > thr;
+          }
+          if (!row_or<NT>(above)) {
+#pragma unroll
+            for (int u = 0; u < kPerThread; ++u) {
+              float x[VE];
+              Elem<T>::unpack(raw[u], x);
+              fold(st, x);
+            }
+            continue;
+          }
+          for (int i = c; i < min(c + kChunk, r.nvec); i += kRound) {
+            room(kRound * VE, true, false);
+            if (tid < kRound && i + tid < r.nvec) take(*r.vec(i + tid), i + tid);
+          }
         }
         room(VE, true, false);
         if (r.tail0 + tid < V) take_loose(r.tail0 + tid);
