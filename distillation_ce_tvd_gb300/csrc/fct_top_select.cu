@@ -43,23 +43,23 @@ using namespace top;
 
 constexpr int kBins = 512;  // of a level of a selection
 // Up to this K a row belongs to 256 threads, above it to 512, whose maxima are
-// more.  What a row costs beside its bytes takes a CTA 10 us, one thing after
-// the other: four small CTAs per SM hide more of it than two large ones.
-constexpr int kSmallK = 256;
-// Up to a quarter of the threads a thread's part has one maximum, above it one
-// per vector of a chunk: the maxima have to be several times K for the
-// threshold to be near the K-th logit.  A warp looks at a pool of them, one
-// per thread.
+// more: they have to be twice K at least.  What a row costs beside its bytes
+// takes a CTA 10 us, one thing after the other: four small CTAs per SM hide more
+// of it than two large ones (4096 x 151936 bf16, K = 400: 640 us, by 512 threads
+// 783; 512, where three fit: 767 and 889, but 123 and 115 at 1003 x 32000).
+constexpr int kSmallK = 512;
+// Up to half of the threads a thread's part has one maximum, above it one per
+// vector of a chunk.  A warp looks at a pool of them, one per thread.
 template <int NT>
-constexpr int kFewMaxima = NT / 4;
+constexpr int kFewMaxima = NT / 2;
 
 // A selection may keep this many more than K: it need not split a bin.
 __host__ __device__ constexpr int slack(int K) { return K / 4 + 64; }
 // Room for candidates: twice what a selection keeps (a sort needs its power of
-// two), and a round of vectors or 3/4 K.  A chunk that comes after a selection
-// then finds room for 2 K + 64: the first chunks bring up to 1.4 K (the threshold
-// is K of their vectors' maxima, of which there are 2 K at least) and 10 to 20%
-// more, as it is the least of four, and what waited in the queues.
+// two), and a round of vectors or 3/4 K.  The chunks up to the next threshold
+// then find room for 2 K + 64 after a selection: they bring up to 1.4 K (the
+// threshold is K of the maxima, of which there are 2 K at least) and 10 to 20%
+// more, where it is the least of four, and what waited in the queues.
 constexpr int kRound = 64;  // vectors of a round
 __host__ __device__ constexpr int capacity(int K, int vec) {
   return 2 * (K + slack(K)) + (kRound * vec > 3 * K / 4 ? kRound * vec : 3 * K / 4);
@@ -467,15 +467,15 @@ __global__ void __launch_bounds__(NT + 32, 1024 / NT)
       // The candidates so far, with room made for `more` unless there are too
       // many already.  `rounds`: all that is still to come has a larger index
       // than all so far, so that what equals the K-th cannot rank.
-      // `chunk`: the next chunk may bring what this one did, and half of that (a row
-      // that runs out of room is taken again: 1003 x 256000 fp32 at K = 1024 took
-      // 3800 us with only a round's room made after each chunk).
+      // `chunks`: those up to the next threshold, as many as there were, may bring
+      // what those did, and half of that (a row that runs out of room is taken again:
+      // 1003 x 256000 fp32 at K = 1024 took 3800 us with only a round's room made).
       int so_far = 0;
-      auto room = [&](int more, bool rounds, bool chunk) {
+      auto room = [&](int more, bool rounds, bool chunks) {
         row_sync<NT>();
         int n = sc.pushed;
         row_sync<NT>();
-        if (chunk) more += max(0, n - so_far) * 3 / 2;
+        if (chunks) more += max(0, n - so_far) * 3 / 2;
         if (n <= cap && n + more > cap && n > K + slack(K)) {
           uint32_t least;
           n = select(sh, sc, n, K, dropped, least);
@@ -538,11 +538,11 @@ __global__ void __launch_bounds__(NT + 32, 1024 / NT)
         while (waiting >= 32) digest();
         ring.release();
         ++chunks;
-        // (always the same decision in all warps)
-        const bool doubled = (chunks & (chunks - 1)) == 0;
-        if (doubled || K > kFewMaxima<NT>) {
+        // when the chunks have doubled (making room after each cost 10 to 18% at K =
+        // 256): the same decision in all warps
+        if ((chunks & (chunks - 1)) == 0) {
           // (not where little is left that a better one would spare)
-          if (doubled && chunks > 1 && r.nvec - c > (chunks / 2 + 1) * kChunk) raise_threshold();
+          if (chunks > 1 && r.nvec - c > (chunks / 2 + 1) * kChunk) raise_threshold();
           if (!full) full = room(kRound * VE, false, true) > cap;
         }
       }
@@ -679,9 +679,9 @@ __global__ void __launch_bounds__(NT + 32, 1024 / NT)
 template <typename T, int NT>
 cudaError_t run(const TopSelectArgs& a, int sms, int device, cudaStream_t st) {
   const int K = static_cast<int>(a.K);
-  const int cap = capacity(K, Elem<T>::kVec);
+  int cap = capacity(K, Elem<T>::kVec);
   constexpr int kChunkBytes = Ring<NT>::kChunk * 16, kStatic = sizeof(Scratch<NT>) + sizeof(RingBars);
-  const int lists = cap * 8 + hist_ints(NT) * 4;
+  int lists = cap * 8 + hist_ints(NT) * 4;
   auto kernel = top_select_kernel<T, NT>;
   static std::once_flag once[64];
   static cudaError_t set[64];
@@ -699,6 +699,11 @@ cudaError_t run(const TopSelectArgs& a, int sms, int device, cudaStream_t st) {
   }
   if (stages < 2) return cudaErrorInvalidConfiguration;
   if (stages > 4) stages = 4;
+  // what shared memory is left holds candidates: fewer selections (8192 x 151936
+  // bf16, K = 256: 7% less time)
+  const int unused = (kStreamSmem / resident - kStatic - lists - stages * kChunkBytes) / 8;
+  cap += unused < 4 * K ? unused : 4 * K;
+  lists = cap * 8 + hist_ints(NT) * 4;
   int64_t grid = int64_t(sms) * resident;
   if (grid > a.BT) grid = a.BT;
   kernel<<<static_cast<unsigned>(grid), NT + 32, size_t(stages) * kChunkBytes + lists, st>>>(a, cap,
