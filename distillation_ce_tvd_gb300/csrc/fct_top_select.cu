@@ -568,8 +568,7 @@ __global__ void __launch_bounds__(NT + 32, 1024 / NT)
         if (tid == 0) sc.pushed = 0;
         row_sync<NT>();
         st = run_empty();
-        dropped = make_float2(-INFINITY, 0.f);
-        thr = -INFINITY;
+        dropped = make_float2(-INFINITY, 0.f);  // (the threshold stays: K logits reach it)
         if (tid < r.head) take_loose(tid);
         for (int c = 0; c < r.nvec; c += kChunk) {
           // a chunk with nothing above the threshold (most, where a row's highest

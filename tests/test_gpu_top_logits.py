@@ -50,6 +50,19 @@ def test_orders(order, K, dtype):
     check(x.to(dtype).repeat(2, 1).cuda(), K)
 
 
+@pytest.mark.parametrize("K", [64, 128, 129, 512, 513, 1024])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_equal_logits(dtype, K):
+    """Rows of a few values: all or hundreds of times K reach the K-th, in every part of the row."""
+    V = 50_021
+    g = torch.Generator().manual_seed(K)
+    x = torch.stack([torch.zeros(V), torch.randint(8, (V,), generator=g).float(),
+                     torch.round(2 * (100 + torch.randn(V, generator=g))) / 2,
+                     torch.where(torch.rand(V, generator=g) < 0.3, 1.0, torch.randn(V, generator=g))])
+    x[0, 40_000:40_010] = 1.0
+    check(x.to(dtype).cuda(), K)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_little_is_left_outside(dtype):
     """The rest keeps its relative precision where the list holds nearly all of the mass."""
