@@ -11,12 +11,14 @@
 // threshold become candidates in shared memory, the others are folded.
 //
 // 8192 x 151936 bf16, K = 64: 595 us, 4.2 TB/s, 0.63 of the copy rate; 1003 x
-// 256000 fp32, K = 256: 296-303 us, 3.4 TB/s.  What bounds it is instructions (100
-// per 32 vectors, 65% of the issue slots) and what a row costs beside its
+// 256000 fp32, K = 256: 271 us, 3.8 TB/s.  What bounds it is instructions (100 per
+// 32 vectors, 65% of the issue slots: 65 of a vector, the others of a row's end) and what a row costs beside its
 // bytes (threshold, last candidates, order: some 8 us of a CTA, hidden by the
 // other three of an SM).  Before: candidates taken vector by vector as they
 // came (194 instructions) 1218 us; a sweep for the threshold and a second one
-// over L2 895; one sweep on two CTAs of 512 threads per SM 715.
+// over L2 895; one sweep on two CTAs of 512 threads per SM 715.  Rows of few
+// values, which are taken again (see below): 608 x 151936 bf16 zeros, K = 64, 83
+// us, eight values 113, random ones 53; rising from word to word 1560.
 //
 // So the rest is summed from its own terms, never as a difference: it keeps
 // its relative precision however little it holds.  Candidates that a selection
